@@ -1,0 +1,643 @@
+// Block-scaled products of quantised rows with the experts' FP4 weights
+// (csf_expert_matmul).
+//
+// Per expert the weight rows are the M side (128 a tile), its slots the N
+// side: experts have few slots each, and N can be any multiple of 16.  The
+// 5th-generation tensor cores multiply codes and block scales as stored
+// (E2M1 x E2M1 with UE4M3 scales per 16, or E2M1 x E4M3 with UE8M0 scales per
+// 32) and accumulate in 32 bits, so nothing is dequantised on the way.  The
+// weight scales are read in the 128 x 4 tile layout that csf_decode writes:
+// a tile copies straight to tensor memory.
+//
+// One persistent block per SM walks tiles (expert, slot tile, row tile):
+//   warp 0   weights (TMA, 128-byte swizzle) and their scale tiles
+//   warp 1   x rows gathered through the slot index (TMA gather of four rows
+//            a request) and their scale bytes (4-byte asynchronous copies into
+//            the same tile layout)
+//   warp 2   scale copies to tensor memory and the matrix instructions
+//   warp 3   tensor-memory allocation
+//   warps 4-7 epilogue: one weight row a lane, slots along the columns
+// A ring of shared-memory stages of 128 code bytes per row joins them; two
+// accumulator sets let the epilogue of a tile overlap the next tile's
+// products.  A gated product holds two accumulators: row tile t of the gate
+// half and of the up half, from the same x rows.
+#include <algorithm>
+#include <cstring>
+#include <mutex>
+
+#include <cuda.h>
+
+#include "csf_internal.cuh"
+#include "csf_quant.cuh"
+#include "csf_tc.cuh"
+
+namespace csfk {
+namespace {
+
+constexpr int kMmThreads = 256;
+constexpr int kMmMaxExperts = 8192;
+constexpr uint32_t kTmemCols = 512;
+constexpr int kSmemLimit = 227 * 1024;
+constexpr int kMaxStages = 12;
+
+struct MmParams {
+    const uint8_t *x_scales;
+    int64_t x_scale_stride;
+    const uint8_t *w_scales;
+    int64_t w_scale_expert;      // bytes between experts' scale stacks
+    const int32_t *rows;
+    const void *start;
+    const float *alpha;
+    const void *bias;
+    const float *row_scale;
+    const void *residual;
+    int64_t residual_stride;
+    void *out;
+    int64_t out_stride;          // elements, or code bytes of a quantised output
+    uint8_t *out_scales;
+    int64_t out_scale_stride;
+    const float *out_tensor_scale;
+    uint32_t *err;
+    int64_t slots;
+    int32_t x_rows;
+    int32_t es64;
+    int32_t E, N, K, F;          // F: output columns (N, or N / 2 gated)
+    int32_t ncb;                 // scale tiles per 128-row block of a weight stack
+    int32_t row_tiles;           // row tiles per expert
+    int32_t second;              // weight rows from a tile's first 128 rows to its second
+    int32_t nt;                  // most slots per tile (a multiple of 16)
+    int32_t stages;
+    uint32_t stage_bytes;
+    int32_t act, bias_dtype, residual_dtype;
+};
+
+enum Out { kOutBf16 = 0, kOutF16 = 1, kOutF32 = 2, kOutNv = 3, kOutMx = 4 };
+
+__device__ __forceinline__ float activate(float v, int act) {
+    if (act == CSF_ACT_RELU) return fmaxf(v, 0.f);
+    if (act == CSF_ACT_SILU) return __fdividef(v, 1.f + __expf(-v));
+    if (act == CSF_ACT_GELU_TANH)   // v * sigmoid(2 * sqrt(2 / pi) * (v + 0.044715 v^3))
+        return __fdividef(v, 1.f + __expf(-1.5957691216057308f * (v + 0.044715f * v * v * v)));
+    return v;
+}
+
+__device__ __forceinline__ int64_t start_at(const MmParams &p, int e) {
+    if (!p.start) return e == 0 ? 0 : p.slots;
+    const int64_t v = p.es64 ? static_cast<const long long *>(p.start)[e] : static_cast<const int *>(p.start)[e];
+    return v < 0 ? 0 : v > p.slots ? p.slots : v;
+}
+
+struct Tile {
+    int e, n, rt;     // expert, slots, row tile
+    int64_t slot;     // first slot
+};
+
+// The tile with this number: the last expert whose first tile is not past
+// it, found 32 candidates at a time; then its slot tile and row tile (row
+// tiles of one slot tile are neighbours, so their x rows are shared in L2).
+__device__ __forceinline__ Tile find_tile(const MmParams &p, const uint32_t *first, uint32_t tile, int lane) {
+    int lo = 0, len = p.E;
+    while (len > 1) {
+        const int step = (len + 31) >> 5;
+        const int i = lo + lane * step;
+        const uint32_t m = __ballot_sync(0xFFFFFFFFu, i < lo + len && first[i] <= tile);
+        const int last = 31 - __clz(m);
+        const int at = lo + last * step;
+        len = min(step, lo + len - at);
+        lo = at;
+    }
+    Tile t;
+    t.e = lo;
+    const uint32_t local = tile - first[lo];
+    const uint32_t rt = (uint32_t)p.row_tiles, parts = (first[lo + 1] - first[lo]) / rt;
+    const uint32_t part = local / rt;
+    t.rt = (int)(local - part * rt);
+    const int64_t s = start_at(p, lo);
+    const int64_t cnt = start_at(p, lo + 1) - s;
+    const int64_t per = ((cnt + parts - 1) / parts + 15) & ~15ll;   // an expert's slot tiles are alike
+    t.slot = s + part * per;
+    t.n = (int)min(per, cnt - part * per);
+    return t;
+}
+
+template <int OUT>
+__device__ __forceinline__ void emit(const MmParams &p, const float (&v)[16], int f, int64_t slot, int n, int lane,
+                                     float tensor_scale, float inv6) {
+    if constexpr (OUT == kOutBf16 || OUT == kOutF16 || OUT == kOutF32) {
+        if (f >= p.F) return;
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+            if (j >= n) break;
+            const int64_t at = (slot + j) * p.out_stride + f;
+            if constexpr (OUT == kOutBf16) static_cast<__nv_bfloat16 *>(p.out)[at] = __float2bfloat16_rn(v[j]);
+            if constexpr (OUT == kOutF16) static_cast<__half *>(p.out)[at] = __float2half_rn(v[j]);
+            if constexpr (OUT == kOutF32) static_cast<float *>(p.out)[at] = v[j];
+        }
+    } else {
+        // A warp's 32 rows are one MXFP8 block or two NVFP4 blocks of each slot.
+        const int fp = (p.F + 31) & ~31;
+        const bool inside = f < fp;
+        uint8_t *codes = static_cast<uint8_t *>(p.out);
+        const int blocks = OUT == kOutMx ? fp >> 5 : fp >> 4;
+        const int pad = ((blocks + 15) & ~15) - blocks;
+        const bool last_warp = (f | 31) == fp - 1;       // writes the scale row's padding
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+            if (j >= n) break;
+            const float u = f < p.F ? v[j] : 0.f;
+            const uint32_t mag = __float_as_uint(u) & 0x7FFFFFFFu;
+            uint8_t *srow = p.out_scales + (slot + j) * p.out_scale_stride;
+            uint8_t *crow = codes + (slot + j) * p.out_stride;
+            if constexpr (OUT == kOutMx) {
+                const uint32_t s = quant::mx_scale(__reduce_max_sync(0xFFFFFFFFu, mag));
+                const uint32_t q = quant::e4m3(u * quant::mx_inverse(s));
+                if (inside) crow[f] = (uint8_t)q;
+                if (inside && lane == 0) srow[f >> 5] = (uint8_t)s;
+            } else {
+                uint32_t m = mag;
+#pragma unroll
+                for (int d = 1; d < 16; d <<= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
+                const uint32_t s = quant::nv_scale(m, inv6);
+                const float w = u * quant::nv_inverse(s, tensor_scale);
+                const float w1 = __shfl_down_sync(0xFFFFFFFFu, w, 1);
+                if (inside && (lane & 1) == 0) crow[f >> 1] = (uint8_t)quant::e2m1x2(w, w1);
+                if (inside && (lane & 15) == 0) srow[f >> 4] = (uint8_t)s;
+            }
+            if (last_warp && lane < pad) srow[blocks + lane] = 0;
+        }
+    }
+}
+
+struct Shared {
+    uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2];
+    uint32_t tmem, abort, total, warp_sum[kMmThreads / 32];
+};
+
+// KIND: csf_rows_kind of x.  AT: 128-row weight tiles per tile.  GATED: the
+// second one is the up half.
+template <int KIND, int AT, bool GATED, int OUT>
+__global__ void __launch_bounds__(kMmThreads, 1)
+expert_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
+                     const __grid_constant__ MmParams p) {
+    extern __shared__ __align__(1024) uint8_t dyn[];
+    __shared__ Shared sh;
+    constexpr bool kNv = KIND == CSF_ROWS_NVFP4;
+    constexpr int kStepK = kNv ? 256 : 128;               // elements per stage: 128 bytes of codes a row
+    constexpr int kTilesPerStage = kNv ? 4 : 1;           // 128 x 4 scale tiles per stage and 128 rows
+    constexpr uint32_t kABytes = 128 * 128;
+    constexpr uint32_t kACopied = kNv ? kABytes : kABytes / 2;   // E2M1 codes unpack on the way: counted as stored
+    constexpr int kAccCols = AT == 1 ? 128 : 96;          // accumulator columns (most slots per tile)
+    constexpr uint32_t kSfCols = 4 * kTilesPerStage;      // tensor-memory columns of one operand's scales
+    constexpr uint32_t kSfSet = (AT + 1) * kSfCols;
+    constexpr uint32_t kSfBase = 2 * AT * kAccCols;
+    static_assert(kSfBase + 2 * kSfSet <= kTmemCols, "tensor memory");
+
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const uint32_t ring = (tc::smem_u32(dyn) + 1023u) & ~1023u;
+    uint32_t *first = reinterpret_cast<uint32_t *>(dyn + (ring - tc::smem_u32(dyn)) + (size_t)p.stages * p.stage_bytes);
+
+    const uint32_t b_off = AT * kABytes, sfa_off = b_off + (uint32_t)p.nt * 128u,
+                   sfb_off = sfa_off + AT * kTilesPerStage * 512u;
+    const uint32_t full0 = tc::smem_u32(sh.full), empty0 = tc::smem_u32(sh.empty);
+    const uint32_t accf0 = tc::smem_u32(sh.acc_full), acce0 = tc::smem_u32(sh.acc_empty);
+
+    if (tid == 0) {
+        for (int i = 0; i < p.stages; ++i) {
+            tc::bar_init(full0 + 8 * i, 2 + 32);    // two expects and the scale-copying lanes
+            tc::bar_init(empty0 + 8 * i, 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            tc::bar_init(accf0 + 8 * i, 1);
+            tc::bar_init(acce0 + 8 * i, 128);
+        }
+        sh.abort = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 3) tc::tmem_alloc(tc::smem_u32(&sh.tmem), kTmemCols);
+
+    // first[e]: number of the first tile of expert e.
+    uint32_t running = 0;
+    bool bad = false;
+    for (int e0 = 0; e0 < p.E; e0 += kMmThreads) {
+        const int e = e0 + tid;
+        uint32_t tiles = 0;
+        if (e < p.E) {
+            const int64_t a = start_at(p, e), b = start_at(p, e + 1);
+            if (b > a) tiles = (uint32_t)((b - a + p.nt - 1) / p.nt) * (uint32_t)p.row_tiles;
+            if (p.start) {
+                const long long raw = p.es64 ? static_cast<const long long *>(p.start)[e + 1] : static_cast<const int *>(p.start)[e + 1];
+                bad |= raw != b || b < a;
+            }
+        }
+        uint32_t sum = tiles;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const uint32_t o = __shfl_up_sync(0xFFFFFFFFu, sum, d);
+            if (lane >= d) sum += o;
+        }
+        if (lane == 31) sh.warp_sum[warp] = sum;
+        __syncthreads();
+        uint32_t before = running;
+        for (int w = 0; w < kMmThreads / 32; ++w) {
+            const uint32_t s = sh.warp_sum[w];
+            if (w < warp) before += s;
+            running += s;
+        }
+        if (e < p.E) first[e] = before + sum - tiles;
+        __syncthreads();
+    }
+    if (tid == 0) first[p.E] = running;
+    if (bad && p.err && blockIdx.x == 0) atomicOr(p.err, CSF_DEV_ERR_CORRUPT);
+    tc::fence_before();
+    __syncthreads();
+    tc::fence_after();
+    const uint32_t total = first[p.E];
+    const uint32_t tmem = sh.tmem;
+    volatile uint32_t *abort = &sh.abort;
+    const int ksteps = (p.K + kStepK - 1) / kStepK;
+
+    if (warp == 0) {
+        // ---- weights and their scales ----
+        if (lane == 0) {
+            asm volatile("prefetch.tensormap [%0];" ::"l"(&wmap) : "memory");
+        }
+        uint32_t it = 0;
+        bool ok = true;
+        for (uint32_t tile = blockIdx.x; ok && tile < total; tile += gridDim.x) {
+            const Tile t = find_tile(p, first, tile, lane);
+            const int row = t.rt * (GATED ? 128 : 128 * AT);
+            const uint8_t *sf = p.w_scales + (int64_t)t.e * p.w_scale_expert;
+            if (lane == 0) {
+                for (int k = 0; k < ksteps; ++k, ++it) {
+                    const uint32_t s = it % (uint32_t)p.stages, ph = (it / (uint32_t)p.stages) & 1u;
+                    if (!tc::bar_wait(empty0 + 8 * s, ph ^ 1u, abort)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t base = ring + s * p.stage_bytes, bar = full0 + 8 * s;
+                    const int tiles = min(kTilesPerStage, p.ncb - k * kTilesPerStage);
+                    int subs = AT;     // the last tile of an odd count of 128-row blocks has one
+                    if (AT == 2 && row + p.second >= p.N) subs = 1;
+                    tc::bar_expect(bar, (uint32_t)subs * (kACopied + (uint32_t)tiles * 512u));
+                    for (int a = 0; a < subs; ++a) {
+                        const int r = row + a * p.second;
+                        tc::tma_load_3d(base + a * kABytes, &wmap, kNv ? k * 128 : k * kStepK, r, t.e, bar);
+                        tc::bulk_load(base + sfa_off + a * kTilesPerStage * 512u,
+                                      sf + ((int64_t)(r >> 7) * p.ncb + k * kTilesPerStage) * 512, (uint32_t)tiles * 512u, bar);
+                    }
+                }
+            }
+            ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
+        }
+    } else if (warp == 1) {
+        // ---- x rows and their scales ----
+        if (lane == 0) {
+            asm volatile("prefetch.tensormap [%0];" ::"l"(&xmap) : "memory");
+        }
+        uint32_t it = 0;
+        bool ok = true, bad_row = false;
+        for (uint32_t tile = blockIdx.x; ok && tile < total; tile += gridDim.x) {
+            const Tile t = find_tile(p, first, tile, lane);
+            const int n16 = (t.n + 15) & ~15;
+            // lane l gathers rows 4l .. 4l+3; columns past the tile's slots repeat its last row
+            int32_t r[4], q[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int64_t s = t.slot + min(4 * lane + j, t.n - 1);
+                const int64_t v = p.rows ? (int64_t)p.rows[s] : s;
+                r[j] = v < 0 || v >= p.x_rows ? 0 : (int32_t)v;
+                bad_row |= r[j] != v;
+            }
+            // and copies the scales of rows l, l + 32, ...
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int c = 32 * j + lane;
+                const int32_t o0 = __shfl_sync(0xFFFFFFFFu, r[0], c >> 2), o1 = __shfl_sync(0xFFFFFFFFu, r[1], c >> 2);
+                const int32_t o2 = __shfl_sync(0xFFFFFFFFu, r[2], c >> 2), o3 = __shfl_sync(0xFFFFFFFFu, r[3], c >> 2);
+                q[j] = (c & 2) ? ((c & 1) ? o3 : o2) : ((c & 1) ? o1 : o0);
+            }
+            for (int k = 0; ok && k < ksteps; ++k, ++it) {
+                const uint32_t s = it % (uint32_t)p.stages, ph = (it / (uint32_t)p.stages) & 1u;
+                ok = tc::bar_wait(empty0 + 8 * s, ph ^ 1u, abort);
+                ok = __all_sync(0xFFFFFFFFu, ok);
+                if (!ok) break;
+                const uint32_t base = ring + s * p.stage_bytes, bar = full0 + 8 * s;
+                if (lane == 0) tc::bar_expect(bar, (uint32_t)n16 * 128u);
+                __syncwarp();
+                if (4 * lane < n16) tc::tma_gather4(base + b_off + lane * 512u, &xmap, k * 128, r[0], r[1], r[2], r[3], bar);
+                const int tiles = min(kTilesPerStage, p.ncb - k * kTilesPerStage);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    if (32 * j + lane < n16) {
+                        const uint8_t *src = p.x_scales + (int64_t)q[j] * p.x_scale_stride + k * (4 * kTilesPerStage);
+                        const uint32_t dst = base + sfb_off + lane * 16u + j * 4u;
+#pragma unroll
+                        for (int i = 0; i < kTilesPerStage; ++i)
+                            if (i < tiles) tc::cp_async4(dst + i * 512u, src + 4 * i);
+                    }
+                }
+                tc::cp_async_arrive(bar);
+            }
+        }
+        if (bad_row && p.err) atomicOr(p.err, CSF_DEV_ERR_CORRUPT);
+    } else if (warp == 2) {
+        // ---- matrix instructions ----
+        // Instruction descriptor: operand types, scale type, N / 8, M / 128.
+        const uint32_t idesc0 = kNv ? (1u << 7) | (1u << 10) | (1u << 27) : (5u << 7) | (0u << 10) | (1u << 23) | (1u << 27);
+        uint32_t it = 0, nth = 0;
+        bool ok = true;
+        for (uint32_t tile = blockIdx.x; ok && tile < total; tile += gridDim.x, ++nth) {
+            const Tile t = find_tile(p, first, tile, lane);
+            const uint32_t set = nth & 1u, aph = (nth >> 1) & 1u;
+            if (lane == 0) {
+                const uint32_t idesc = idesc0 | ((uint32_t)((t.n + 15) >> 4) << 18);
+                int subs = AT;
+                if (AT == 2 && t.rt * (GATED ? 128 : 128 * AT) + p.second >= p.N) subs = 1;
+                ok = tc::bar_wait(acce0 + 8 * set, aph ^ 1u, abort);
+                tc::fence_after();
+                const uint32_t d0 = tmem + set * (AT * kAccCols);
+                for (int k = 0; ok && k < ksteps; ++k, ++it) {
+                    const uint32_t s = it % (uint32_t)p.stages, ph = (it / (uint32_t)p.stages) & 1u;
+                    if (!tc::bar_wait(full0 + 8 * s, ph, abort)) {
+                        ok = false;
+                        break;
+                    }
+                    tc::fence_async_proxy();     // the scale bytes of x came by ordinary copies
+                    tc::fence_after();
+                    const uint32_t base = ring + s * p.stage_bytes;
+                    const uint32_t sf = tmem + kSfBase + (it & 1u) * kSfSet;
+                    const int tiles = min(kTilesPerStage, p.ncb - k * kTilesPerStage);
+                    for (int i = 0; i < tiles; ++i) {
+                        tc::copy_scales(sf + 4 * i, tc::desc_plain(base + sfb_off + i * 512u));
+                        for (int a = 0; a < subs; ++a)
+                            tc::copy_scales(sf + (a + 1) * kSfCols + 4 * i,
+                                            tc::desc_plain(base + sfa_off + (a * kTilesPerStage + i) * 512u));
+                    }
+                    const uint64_t bd = tc::desc_sw128(base + b_off);
+                    for (int a = 0; a < subs; ++a) {
+                        const uint64_t ad = tc::desc_sw128(base + a * kABytes);
+                        const uint32_t d = d0 + a * kAccCols, sfa = sf + (a + 1) * kSfCols;
+                        if constexpr (kNv) {
+                            for (int i = 0; i < tiles; ++i)
+                                tc::mma_nvfp4(d, ad + 2 * i, bd + 2 * i, idesc, sfa + 4 * i, sf + 4 * i, (k | i) != 0);
+                        } else {
+                            for (int i = 0; i < 4; ++i)
+                                tc::mma_mxf8(d, ad + 2 * i, bd + 2 * i, idesc | ((uint32_t)i << 29) | ((uint32_t)i << 4), sfa, sf,
+                                             (k | i) != 0);
+                        }
+                    }
+                    tc::commit(empty0 + 8 * s);
+                }
+                if (ok) tc::commit(accf0 + 8 * set);
+            }
+            ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
+        }
+    } else if (warp >= 4) {
+        // ---- epilogue ----
+        const int w = warp - 4;
+        uint32_t nth = 0;
+        float tensor_scale = 1.f, inv6 = 1.f;
+        if constexpr (OUT == kOutNv) {
+            if (p.out_tensor_scale) tensor_scale = *p.out_tensor_scale;
+            inv6 = 1.f / (6.f * tensor_scale);
+        }
+        for (uint32_t tile = blockIdx.x; tile < total; tile += gridDim.x, ++nth) {
+            const Tile t = find_tile(p, first, tile, lane);
+            const uint32_t set = nth & 1u, aph = (nth >> 1) & 1u;
+            const int row = t.rt * (GATED ? 128 : 128 * AT) + 32 * w + lane;
+            const float alpha = p.alpha ? p.alpha[t.e] : 1.f;
+            float bias[AT];
+#pragma unroll
+            for (int a = 0; a < AT; ++a) {
+                const int r = row + a * p.second;
+                bias[a] = p.bias && r < p.N ? quant::load_as_float(p.bias, (int64_t)t.e * p.N + r, p.bias_dtype) : 0.f;
+            }
+            bool ok = tc::bar_wait(accf0 + 8 * set, aph, abort);
+            if (!__all_sync(0xFFFFFFFFu, ok)) break;
+            tc::fence_after();
+            const uint32_t d0 = tmem + set * (AT * kAccCols) + ((uint32_t)(32 * w) << 16);
+            for (int c = 0; c < t.n; c += 16) {
+                const int n = min(16, t.n - c);
+                float acc[AT][16];
+#pragma unroll
+                for (int a = 0; a < AT; ++a) tc::tmem_load16(d0 + a * kAccCols + c, acc[a]);
+                tc::wait_ld();
+                if (c + 16 >= t.n) {
+                    tc::fence_before();
+                    tc::bar_arrive(acce0 + 8 * set);
+                }
+                const int64_t slot = t.slot + c;
+#pragma unroll
+                for (int a = 0; a < (GATED ? 1 : AT); ++a) {
+                    const int f = row + a * 128;
+                    float y[16];
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        y[j] = activate(fmaf(acc[a][j], alpha, bias[a]), p.act);
+                        if constexpr (GATED) y[j] *= fmaf(acc[AT - 1][j], alpha, bias[AT - 1]);
+                    }
+                    if (p.row_scale) {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            if (j < n) y[j] *= p.row_scale[slot + j];
+                    }
+                    if (p.residual && f < p.F) {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            if (j < n) y[j] += quant::load_as_float(p.residual, (slot + j) * p.residual_stride + f, p.residual_dtype);
+                    }
+                    emit<OUT>(p, y, f, slot, n, lane, tensor_scale, inv6);
+                }
+            }
+        }
+    }
+
+    // A wait that gave up: let copies and products in flight land before the
+    // block's memory goes.
+    __syncthreads();
+    if (sh.abort) {
+        if (tid == 0 && p.err) atomicOr(p.err, CSF_DEV_ERR_TIMEOUT);
+        const uint64_t t0 = tc::timer_ns();
+        while (tc::timer_ns() - t0 < 5000000ull) __nanosleep(1000);
+        __syncthreads();
+    }
+    if (warp == 3) tc::tmem_free(tmem, kTmemCols);
+}
+
+// ---- host side ------------------------------------------------------------------------------------------------------
+
+using EncodeFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *, const cuuint64_t *,
+                              const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeFn encode_fn() {
+    static EncodeFn fn = [] {
+        void *f = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12080, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess) {
+            cudaGetLastError();
+            f = nullptr;
+        }
+        return reinterpret_cast<EncodeFn>(f);
+    }();
+    return fn;
+}
+
+using Kernel = void (*)(CUtensorMap, CUtensorMap, MmParams);
+
+template <int KIND, int OUT>
+Kernel pick(int at, bool gated) {
+    if (gated) return expert_matmul_kernel<KIND, 2, true, OUT>;
+    (void)at;
+    return expert_matmul_kernel<KIND, 1, false, OUT>;
+}
+
+template <int KIND>
+Kernel pick_out(int out, int at, bool gated) {
+    switch (out) {
+        case kOutBf16: return pick<KIND, kOutBf16>(at, gated);
+        case kOutF16: return pick<KIND, kOutF16>(at, gated);
+        case kOutF32: return pick<KIND, kOutF32>(at, gated);
+        case kOutNv: return pick<KIND, kOutNv>(at, gated);
+        default: return pick<KIND, kOutMx>(at, gated);
+    }
+}
+
+int sm_count() {
+    static int counts[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) {
+        cudaGetLastError();
+        return 0;
+    }
+    if (counts[dev] == 0) {
+        int n = 0;
+        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+            cudaGetLastError();
+            return 0;
+        }
+        counts[dev] = n;
+    }
+    return counts[dev];
+}
+
+csf_status check(const csf_expert_matmul_args *a) {
+    if (!a) return CSF_ERR_ARG;
+    if (!rows_valid(a->x) || a->experts < 1 || a->n < 1 || a->slots < 0) return CSF_ERR_ARG;
+    if (a->act < CSF_ACT_NONE || a->act > CSF_ACT_GELU_TANH) return CSF_ERR_ARG;
+    if (a->experts > kMmMaxExperts || a->slots >= (1ll << 31) || a->x.rows >= (1ll << 31)) return CSF_ERR_UNSUPPORTED;
+    if (a->x.cols % (a->x.kind == CSF_ROWS_NVFP4 ? 32 : 128) || (a->gated && a->n % 256)) return CSF_ERR_UNSUPPORTED;
+    if (!a->expert_start && a->experts != 1) return CSF_ERR_ARG;
+    if (!a->rows && a->slots > a->x.rows) return CSF_ERR_ARG;
+    if (a->slots == 0) return CSF_OK;
+    if (a->x.rows == 0) return CSF_ERR_ARG;
+    if (!a->w || !a->w_scales || !aligned_to(a->w, 32) || !aligned_to(a->w_scales, 16)) return CSF_ERR_ARG;
+    const int32_t F = a->gated ? a->n / 2 : a->n;
+    if (a->bias && !dtype_known(a->bias_dtype)) return CSF_ERR_ARG;
+    if (a->residual && (!dtype_known(a->residual_dtype) || a->residual_stride < F)) return CSF_ERR_ARG;
+    if (a->out) {
+        if (!dtype_known(a->out_dtype) || a->out_stride < F) return CSF_ERR_ARG;
+    } else if (!rows_valid(a->out_rows) || a->out_rows.cols != F || a->out_rows.rows != a->slots) {
+        return CSF_ERR_ARG;
+    }
+    return CSF_OK;
+}
+
+}  // namespace
+}  // namespace csfk
+
+using namespace csfk;
+
+extern "C" csf_status csf_expert_matmul(const csf_expert_matmul_args *a, void *stream) {
+    csf_status st = check(a);
+    if (st != CSF_OK || a->slots == 0) return st;
+    const bool nv = a->x.kind == CSF_ROWS_NVFP4;
+    const int32_t K = a->x.cols, N = a->n, E = a->experts;
+    const int at = a->gated ? 2 : 1;
+
+    MmParams p;
+    std::memset(&p, 0, sizeof(p));
+    p.x_scales = a->x.scales;
+    p.x_scale_stride = a->x.scale_stride;
+    const int32_t C = K / (nv ? 16 : 32);
+    p.ncb = (C + 3) / 4;
+    p.w_scales = a->w_scales;
+    p.w_scale_expert = round_up(N, 128) * 4 * p.ncb;
+    p.rows = a->rows;
+    p.start = a->expert_start;
+    p.es64 = a->expert_start_is_int64;
+    p.alpha = a->alpha;
+    p.bias = a->bias;
+    p.bias_dtype = a->bias_dtype;
+    p.row_scale = a->row_scale;
+    p.residual = a->residual;
+    p.residual_stride = a->residual_stride;
+    p.residual_dtype = a->residual_dtype;
+    p.err = a->error_word;
+    p.slots = a->slots;
+    p.x_rows = (int32_t)a->x.rows;
+    p.E = E;
+    p.N = N;
+    p.K = K;
+    p.F = a->gated ? N / 2 : N;
+    p.act = a->act;
+    int out;
+    if (a->out) {
+        out = a->out_dtype;
+        p.out = a->out;
+        p.out_stride = a->out_stride;
+    } else {
+        out = a->out_rows.kind == CSF_ROWS_NVFP4 ? kOutNv : kOutMx;
+        p.out = a->out_rows.codes;
+        p.out_stride = a->out_rows.code_stride;
+        p.out_scales = a->out_rows.scales;
+        p.out_scale_stride = a->out_rows.scale_stride;
+        p.out_tensor_scale = a->out_rows.tensor_scale;
+    }
+    p.second = a->gated ? N / 2 : 128;
+    p.row_tiles = a->gated ? N / 256 : (N + 128 * at - 1) / (128 * at);
+    const int most = at == 1 ? 128 : 96;
+    p.nt = (int)std::min<int64_t>(most, round_up(a->slots, 16));
+    const uint32_t sf = nv ? 2048u : 512u;
+    p.stage_bytes = (uint32_t)round_up(at * 16384 + p.nt * 128 + (at + 1) * sf, 1024);
+    const int fixed = 1024 + 4 * (E + 1) + 16;
+    const int room = kSmemLimit - (int)round_up(sizeof(Shared), 1024) - fixed;
+    p.stages = std::min<int>(kMaxStages, room / (int)p.stage_bytes);
+    // never two blocks on an SM: each holds the whole tensor memory
+    const int smem = std::max(fixed + p.stages * (int)p.stage_bytes, 120 * 1024);
+
+    const int64_t most_tiles = (int64_t)p.row_tiles * (std::min<int64_t>(E, a->slots) + a->slots / p.nt);
+    if (most_tiles >= (1ll << 31)) return CSF_ERR_UNSUPPORTED;
+    const int sms = sm_count();
+    EncodeFn encode = encode_fn();
+    if (sms < 1 || !encode) return CSF_ERR_CUDA;
+
+    CUtensorMap wmap, xmap;
+    {
+        const cuuint64_t dims[3] = {(cuuint64_t)(nv ? K / 2 : K), (cuuint64_t)N, (cuuint64_t)E};
+        const cuuint64_t strides[2] = {(cuuint64_t)K / 2, (cuuint64_t)K / 2 * (cuuint64_t)N};
+        const cuuint32_t box[3] = {128, 128, 1}, ones[3] = {1, 1, 1};
+        if (encode(&wmap, nv ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B, 3,
+                   const_cast<uint8_t *>(a->w), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+            return CSF_ERR_CUDA;
+    }
+    {
+        const cuuint64_t dims[2] = {(cuuint64_t)(nv ? K / 2 : K), (cuuint64_t)a->x.rows};
+        const cuuint64_t strides[1] = {(cuuint64_t)a->x.code_stride};
+        const cuuint32_t box[2] = {128, 1}, ones[2] = {1, 1};
+        if (encode(&xmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, a->x.codes, dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+            return CSF_ERR_CUDA;
+    }
+    Kernel k = nv ? pick_out<CSF_ROWS_NVFP4>(out, at, a->gated) : pick_out<CSF_ROWS_MXFP8>(out, at, a->gated);
+    if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) {
+        cudaGetLastError();
+        return CSF_ERR_CUDA;
+    }
+    const int grid = (int)std::min<int64_t>(sms, most_tiles);
+    k<<<grid, kMmThreads, smem, static_cast<cudaStream_t>(stream)>>>(wmap, xmap, p);
+    if (cudaGetLastError() != cudaSuccess) return CSF_ERR_CUDA;
+    return CSF_OK;
+}

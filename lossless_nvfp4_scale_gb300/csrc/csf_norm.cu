@@ -1,0 +1,247 @@
+// Residual addition, root-mean-square norm and quantisation in one pass
+// (csf_rms_norm): y = h * rsqrt(mean(h^2) + eps) * weight, h = x + residual.
+//
+// Bound by memory: a row is read once and stays in registers, in chunks of 8
+// columns a thread, while its sum of squares is formed; then the chunks are
+// scaled, the block maxima come from shuffles between the 4 (32 columns,
+// MXFP8) or 2 (16 columns, NVFP4) threads of a block, and codes and scales
+// leave.  Rows too wide for the registers are read twice.
+#include "csf_internal.cuh"
+#include "csf_quant.cuh"
+
+namespace csfk {
+namespace {
+
+constexpr int kNormMaxThreads = 1024;
+
+struct NormParams {
+    const void *x, *residual, *weight;
+    void *sum;
+    int64_t x_stride, residual_stride, sum_stride;   // elements
+    uint8_t *codes, *scales;
+    int64_t code_stride, scale_stride;
+    const float *tensor_scale;
+    int64_t rows;
+    int32_t cols, chunks;        // chunks: 8-column pieces of the padded row
+    float eps, inv_cols;
+    int32_t wide_x, wide_residual, wide_sum, wide_weight;   // 16-byte accesses allowed
+};
+
+template <typename T> struct Elem;
+template <> struct Elem<__nv_bfloat16> {
+    static __device__ float to(__nv_bfloat16 v) { return __bfloat162float(v); }
+    static __device__ __nv_bfloat16 from(float v) { return __float2bfloat16_rn(v); }
+};
+template <> struct Elem<__half> {
+    static __device__ float to(__half v) { return __half2float(v); }
+    static __device__ __half from(float v) { return __float2half_rn(v); }
+};
+template <> struct Elem<float> {
+    static __device__ float to(float v) { return v; }
+    static __device__ float from(float v) { return v; }
+};
+
+// Columns c .. c+7 of a row, 0 past its end.
+template <typename T>
+__device__ __forceinline__ void load8(float (&v)[8], const T *row, int c, int cols, bool wide) {
+    if (wide && c + 8 <= cols) {
+        union { uint4 q[sizeof(T) / 2]; T e[8]; } u;
+#pragma unroll
+        for (int i = 0; i < (int)(sizeof(T) / 2); ++i) u.q[i] = reinterpret_cast<const uint4 *>(row + c)[i];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = Elem<T>::to(u.e[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = c + i < cols ? Elem<T>::to(row[c + i]) : 0.f;
+    }
+}
+
+template <typename T>
+__device__ __forceinline__ void store8(const float (&v)[8], T *row, int c, int cols, bool wide) {
+    if (wide && c + 8 <= cols) {
+        union { uint4 q[sizeof(T) / 2]; T e[8]; } u;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) u.e[i] = Elem<T>::from(v[i]);
+#pragma unroll
+        for (int i = 0; i < (int)(sizeof(T) / 2); ++i) reinterpret_cast<uint4 *>(row + c)[i] = u.q[i];
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (c + i < cols) row[c + i] = Elem<T>::from(v[i]);
+    }
+}
+
+// h of one chunk: x + residual.
+template <typename T>
+__device__ __forceinline__ void load_h(float (&h)[8], const NormParams &p, int64_t row, int c) {
+    load8(h, static_cast<const T *>(p.x) + row * p.x_stride, c, p.cols, p.wide_x);
+    if (p.residual) {
+        float r[8];
+        load8(r, static_cast<const T *>(p.residual) + row * p.residual_stride, c, p.cols, p.wide_residual);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) h[i] += r[i];
+    }
+}
+
+// Quantise one chunk of y; every thread of a scale block calls it together.
+template <int KIND>
+__device__ __forceinline__ void quantize8(const float (&y)[8], const NormParams &p, int64_t row, int chunk, float g, float inv6) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(y[i]) & 0x7FFFFFFFu);
+    m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+    if constexpr (KIND == CSF_ROWS_MXFP8) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+    if (chunk >= p.chunks) return;
+    if constexpr (KIND == CSF_ROWS_MXFP8) {
+        const uint32_t s = quant::mx_scale(m);
+        const float inv = quant::mx_inverse(s);
+        uint2 q;
+        q.x = quant::e4m3x2(y[0] * inv, y[1] * inv) | quant::e4m3x2(y[2] * inv, y[3] * inv) << 16;
+        q.y = quant::e4m3x2(y[4] * inv, y[5] * inv) | quant::e4m3x2(y[6] * inv, y[7] * inv) << 16;
+        *reinterpret_cast<uint2 *>(p.codes + row * p.code_stride + chunk * 8) = q;
+        if ((chunk & 3) == 0) p.scales[row * p.scale_stride + (chunk >> 2)] = (uint8_t)s;
+    } else {
+        const uint32_t s = quant::nv_scale(m, inv6);
+        const float inv = quant::nv_inverse(s, g);
+        const uint32_t q = quant::e2m1x2(y[0] * inv, y[1] * inv) | quant::e2m1x2(y[2] * inv, y[3] * inv) << 8 |
+                           quant::e2m1x2(y[4] * inv, y[5] * inv) << 16 | quant::e2m1x2(y[6] * inv, y[7] * inv) << 24;
+        *reinterpret_cast<uint32_t *>(p.codes + row * p.code_stride + chunk * 4) = q;
+        if ((chunk & 1) == 0) p.scales[row * p.scale_stride + (chunk >> 1)] = (uint8_t)s;
+    }
+}
+
+// One row per block of blockDim.x threads (WARP: per warp).  CHUNKS > 0: that
+// many chunks a thread stay in registers; 0: the row is read twice.
+template <typename T, int KIND, int CHUNKS, bool WARP>
+__global__ void __launch_bounds__(WARP ? 256 : kNormMaxThreads)
+rms_norm_kernel(const __grid_constant__ NormParams p) {
+    __shared__ float part[32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int tid = WARP ? lane : threadIdx.x, threads = WARP ? 32 : blockDim.x;
+    const int64_t row = WARP ? (int64_t)blockIdx.x * (blockDim.x >> 5) + warp : (int64_t)blockIdx.x;
+    if (row >= p.rows) return;
+    float h[CHUNKS > 0 ? CHUNKS : 1][8];
+    float sum = 0.f;
+    if constexpr (CHUNKS > 0) {
+#pragma unroll
+        for (int j = 0; j < CHUNKS; ++j) load_h<T>(h[j], p, row, (tid + j * threads) * 8);
+#pragma unroll
+        for (int j = 0; j < CHUNKS; ++j) {
+            if (p.sum) store8(h[j], static_cast<T *>(p.sum) + row * p.sum_stride, (tid + j * threads) * 8, p.cols, p.wide_sum);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sum = fmaf(h[j][i], h[j][i], sum);
+        }
+    } else {
+        for (int c = tid; c < p.chunks; c += threads) {
+            load_h<T>(h[0], p, row, c * 8);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sum = fmaf(h[0][i], h[0][i], sum);
+        }
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
+    if constexpr (!WARP) {
+        if (lane == 0) part[warp] = sum;
+        __syncthreads();
+        sum = lane < (threads >> 5) ? part[lane] : 0.f;
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
+    }
+    const float r = rsqrtf(sum * p.inv_cols + p.eps);
+    const float g = KIND == CSF_ROWS_NVFP4 && p.tensor_scale ? *p.tensor_scale : 1.f;
+    const float inv6 = 1.f / (6.f * g);
+    const T *weight = static_cast<const T *>(p.weight);
+    if constexpr (CHUNKS > 0) {
+#pragma unroll
+        for (int j = 0; j < CHUNKS; ++j) {
+            const int c = tid + j * threads;
+            float w[8];
+            load8(w, weight, c * 8, p.cols, p.wide_weight);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) h[j][i] = h[j][i] * r * w[i];
+            quantize8<KIND>(h[j], p, row, c, g, inv6);
+        }
+    } else {
+        for (int c0 = 0; c0 < p.chunks; c0 += threads) {
+            const int c = c0 + tid;
+            load_h<T>(h[0], p, row, c * 8);
+            if (p.sum) store8(h[0], static_cast<T *>(p.sum) + row * p.sum_stride, c * 8, p.cols, p.wide_sum);
+            float w[8];
+            load8(w, weight, c * 8, p.cols, p.wide_weight);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) h[0][i] = h[0][i] * r * w[i];
+            quantize8<KIND>(h[0], p, row, c, g, inv6);
+        }
+    }
+    const int blocks = KIND == CSF_ROWS_MXFP8 ? p.chunks >> 2 : p.chunks >> 1;
+    if (tid < ((blocks + 15) & ~15) - blocks) p.scales[row * p.scale_stride + blocks + tid] = 0;
+}
+
+template <typename T, int KIND>
+cudaError_t launch_norm(const NormParams &p, cudaStream_t s) {
+    if (p.chunks <= 32) {
+        rms_norm_kernel<T, KIND, 1, true><<<(unsigned)((p.rows + 7) / 8), 256, 0, s>>>(p);
+    } else {
+        const int per1 = (p.chunks + 31) & ~31;
+        const unsigned grid = (unsigned)p.rows;
+        if (per1 <= 256)
+            rms_norm_kernel<T, KIND, 1, false><<<grid, per1, 0, s>>>(p);
+        else if ((p.chunks + 1) / 2 <= kNormMaxThreads)
+            rms_norm_kernel<T, KIND, 2, false><<<grid, ((p.chunks + 1) / 2 + 31) & ~31, 0, s>>>(p);
+        else
+            rms_norm_kernel<T, KIND, 0, false><<<grid, kNormMaxThreads, 0, s>>>(p);
+    }
+    return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t launch_norm_kind(int kind, const NormParams &p, cudaStream_t s) {
+    return kind == CSF_ROWS_NVFP4 ? launch_norm<T, CSF_ROWS_NVFP4>(p, s) : launch_norm<T, CSF_ROWS_MXFP8>(p, s);
+}
+
+bool wide(const void *p, int64_t stride, int dtype) {
+    return aligned_to(p, 16) && (stride * (int64_t)dtype_bytes(dtype)) % 16 == 0;
+}
+
+}  // namespace
+}  // namespace csfk
+
+using namespace csfk;
+
+extern "C" csf_status csf_rms_norm(const csf_rms_norm_args *a, void *stream) {
+    if (!a || !dtype_known(a->dtype) || !rows_valid(a->out)) return CSF_ERR_ARG;
+    if (a->out.rows == 0) return CSF_OK;
+    const int64_t cols = a->out.cols;
+    if (!a->x || !a->weight || a->x_stride < cols) return CSF_ERR_ARG;
+    if ((a->residual && a->residual_stride < cols) || (a->sum_out && a->sum_stride < cols)) return CSF_ERR_ARG;
+    const uintptr_t e = dtype_bytes(a->dtype);
+    if (!aligned_to(a->x, e) || !aligned_to(a->weight, e) || !aligned_to(a->residual, e) || !aligned_to(a->sum_out, e)) return CSF_ERR_ARG;
+    if (a->out.rows >= (1ll << 31) || cols > (1 << 24)) return CSF_ERR_UNSUPPORTED;
+    NormParams p;
+    p.x = a->x;
+    p.residual = a->residual;
+    p.weight = a->weight;
+    p.sum = a->sum_out;
+    p.x_stride = a->x_stride;
+    p.residual_stride = a->residual_stride;
+    p.sum_stride = a->sum_stride;
+    p.codes = a->out.codes;
+    p.scales = a->out.scales;
+    p.code_stride = a->out.code_stride;
+    p.scale_stride = a->out.scale_stride;
+    p.tensor_scale = a->out.tensor_scale;
+    p.rows = a->out.rows;
+    p.cols = (int32_t)cols;
+    p.chunks = (int32_t)(round_up(cols, 32) / 8);
+    p.eps = a->eps;
+    p.inv_cols = 1.f / (float)cols;
+    p.wide_x = wide(a->x, a->x_stride, a->dtype);
+    p.wide_residual = wide(a->residual, a->residual_stride, a->dtype);
+    p.wide_sum = wide(a->sum_out, a->sum_stride, a->dtype);
+    p.wide_weight = aligned_to(a->weight, 16);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const cudaError_t err = a->dtype == CSF_BF16  ? launch_norm_kind<__nv_bfloat16>(a->out.kind, p, s)
+                            : a->dtype == CSF_F16 ? launch_norm_kind<__half>(a->out.kind, p, s)
+                                                  : launch_norm_kind<float>(a->out.kind, p, s);
+    return err == cudaSuccess ? CSF_OK : CSF_ERR_CUDA;
+}

@@ -1,0 +1,79 @@
+// Quantised rows (csf_rows in csf_ops.h): block scales, code conversions and
+// element types shared by the operator kernels.  Internal to the library.
+#pragma once
+
+#include <cstdint>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp4.h>
+#include <cuda_fp8.h>
+
+#include "csf_ops.h"
+
+namespace csfk {
+namespace quant {
+
+// Smallest power of two s with amax <= 448 s, as its UE8M0 byte: 448 =
+// 1.75 * 2^8, so the exponent of amax less 8, and one more when its fraction
+// is above .75.  amax_bits: the bits of a non-negative float.
+__device__ __forceinline__ uint32_t mx_scale(uint32_t amax_bits) {
+    const int x = (int)(amax_bits >> 23);
+    if (x == 255) return 255;
+    const int b = x - 8 + ((amax_bits & 0x7FFFFFu) > 0x600000u ? 1 : 0);
+    return b < 0 ? 0 : (uint32_t)b;
+}
+
+// 1 / scale, exact (a NaN scale's codes mean nothing: 1).
+__device__ __forceinline__ float mx_inverse(uint32_t byte) {
+    return __uint_as_float(byte == 255 ? 127u << 23 : (254u - byte) << 23);
+}
+
+// UE4M3 byte of amax / (6 * tensor scale); inv6 = 1 / (6 * tensor scale).
+__device__ __forceinline__ uint32_t nv_scale(uint32_t amax_bits, float inv6) {
+    if ((amax_bits >> 23) == 255) return 0x7F;
+    return __nv_cvt_float_to_fp8(__uint_as_float(amax_bits) * inv6, __NV_SATFINITE, __NV_E4M3);
+}
+
+// 1 / (scale * tensor scale), 0 for a zero scale.
+__device__ __forceinline__ float nv_inverse(uint32_t byte, float tensor_scale) {
+    const float s = __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)byte, __NV_E4M3)));
+    return s > 0.f ? 1.f / (s * tensor_scale) : 0.f;
+}
+
+__device__ __forceinline__ uint32_t e4m3(float v) { return __nv_cvt_float_to_fp8(v, __NV_SATFINITE, __NV_E4M3); }
+
+// Two values -> two E4M3 bytes, the first in the low byte.
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
+    return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
+}
+
+// Two values -> two E2M1 codes, the first in the low nibble.
+__device__ __forceinline__ uint32_t e2m1x2(float lo, float hi) {
+    return __nv_cvt_float2_to_fp4x2(make_float2(lo, hi), __NV_E2M1, cudaRoundNearest);
+}
+
+__device__ __forceinline__ float load_as_float(const void *p, int64_t i, int dtype) {
+    if (dtype == CSF_BF16) return __bfloat162float(static_cast<const __nv_bfloat16 *>(p)[i]);
+    if (dtype == CSF_F16) return __half2float(static_cast<const __half *>(p)[i]);
+    return static_cast<const float *>(p)[i];
+}
+
+}  // namespace quant
+
+inline int64_t round_up(int64_t n, int64_t m) { return (n + m - 1) / m * m; }
+inline size_t dtype_bytes(int dtype) { return dtype == CSF_F32 ? 4 : 2; }
+inline bool dtype_known(int dtype) { return dtype == CSF_BF16 || dtype == CSF_F16 || dtype == CSF_F32; }
+inline bool aligned_to(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+// A csf_rows that a call reads or writes; `rows` of 0 need no buffers.
+inline bool rows_valid(const csf_rows &r) {
+    if ((r.kind != CSF_ROWS_NVFP4 && r.kind != CSF_ROWS_MXFP8) || r.cols < 1 || r.rows < 0) return false;
+    if (r.rows == 0) return true;
+    const int64_t cols = round_up(r.cols, 32);
+    const int64_t code_bytes = r.kind == CSF_ROWS_NVFP4 ? cols / 2 : cols;
+    const int64_t blocks = r.kind == CSF_ROWS_NVFP4 ? cols / 16 : cols / 32;
+    return r.codes && r.scales && aligned_to(r.codes, 16) && aligned_to(r.scales, 16) && r.code_stride % 16 == 0 &&
+           r.scale_stride % 16 == 0 && r.code_stride >= code_bytes && r.scale_stride >= round_up(blocks, 16);
+}
+
+}  // namespace csfk

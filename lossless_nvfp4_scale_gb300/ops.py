@@ -1,0 +1,272 @@
+"""Python binding of the expert-layer operators (include/csf_ops.h): what a
+caller of csf.decode runs on either side of the decoded scales.
+
+Argument marshalling only, as in csf.py: the kernels of libcsf.so do the work,
+PyTorch supplies device memory and streams, and there is no CPU fallback.
+
+Typical use (one layer of experts)::
+
+    q, h = ops.rms_norm(x, norm_weight, ops.NVFP4, residual=h, tensor_scale=g)
+    r = ops.route(logits, k=8)
+    csf.decode(stack, ws, expert_start=r.expert_start, layout=csf.LAYOUT_BLOCKED)
+    a = ops.expert_matmul(q, w_gate_up, ws, expert_start=r.expert_start, rows=r.rows, alpha=alpha,
+                          activation="silu", gated=True, out=ops.NVFP4, out_tensor_scale=g2)
+    y = ops.expert_matmul(a, w_down, down_ws, expert_start=r.expert_start, alpha=alpha2)
+"""
+from __future__ import annotations
+
+import ctypes
+from dataclasses import dataclass
+
+import torch
+
+from . import csf
+from .csf import CsfError, _check, _es, _stream, lib
+
+NVFP4 = 0     # rows of E2M1 codes, a UE4M3 scale per 16; goes with NVFP4 weights
+MXFP8 = 1     # rows of E4M3 codes, a UE8M0 scale per 32; goes with MXFP4 weights
+_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+_ACTS = {None: 0, "none": 0, "relu": 1, "silu": 2, "gelu": 3}
+
+_i32, _i64, _vp, _f32 = ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p, ctypes.c_float
+
+
+class CRows(ctypes.Structure):
+    """csf_rows: quantised rows."""
+    _fields_ = [("kind", _i32), ("cols", _i32), ("rows", _i64), ("codes", _vp), ("code_stride", _i64),
+                ("scales", _vp), ("scale_stride", _i64), ("tensor_scale", _vp)]
+
+
+class CRmsNorm(ctypes.Structure):
+    """csf_rms_norm_args."""
+    _fields_ = [("x", _vp), ("x_stride", _i64), ("residual", _vp), ("residual_stride", _i64), ("sum_out", _vp),
+                ("sum_stride", _i64), ("weight", _vp), ("dtype", _i32), ("eps", _f32), ("out", CRows)]
+
+
+class CRoute(ctypes.Structure):
+    """csf_route_args."""
+    _fields_ = [("logits", _vp), ("logits_stride", _i64), ("dtype", _i32), ("tokens", _i32), ("experts", _i32),
+                ("k", _i32), ("renormalize", _i32), ("ids", _vp), ("weights", _vp), ("expert_start", _vp),
+                ("rows", _vp), ("slots", _vp), ("scratch", _vp), ("scratch_bytes", ctypes.c_size_t)]
+
+
+class CExpertMatmul(ctypes.Structure):
+    """csf_expert_matmul_args."""
+    _fields_ = [("x", CRows), ("rows", _vp), ("slots", _i64), ("experts", _i32), ("n", _i32), ("w", _vp),
+                ("w_scales", _vp), ("expert_start", _vp), ("expert_start_is_int64", _i32), ("alpha", _vp),
+                ("bias", _vp), ("bias_dtype", _i32), ("act", _i32), ("gated", _i32), ("row_scale", _vp),
+                ("residual", _vp), ("residual_stride", _i64), ("residual_dtype", _i32), ("out_dtype", _i32),
+                ("out", _vp), ("out_stride", _i64), ("out_rows", CRows), ("error_word", _vp)]
+
+
+lib.csf_rms_norm.argtypes = [ctypes.POINTER(CRmsNorm), _vp]
+lib.csf_rms_norm.restype = ctypes.c_int
+lib.csf_route.argtypes = [ctypes.POINTER(CRoute), _vp]
+lib.csf_route.restype = ctypes.c_int
+lib.csf_route_scratch_bytes.argtypes = [_i32, _i32]
+lib.csf_route_scratch_bytes.restype = ctypes.c_size_t
+lib.csf_expert_matmul.argtypes = [ctypes.POINTER(CExpertMatmul), _vp]
+lib.csf_expert_matmul.restype = ctypes.c_int
+
+
+def _up(n: int, m: int) -> int:
+    return (n + m - 1) // m * m
+
+
+def _code_bytes(kind: int, cols: int) -> int:
+    return _up(cols, 32) // (2 if kind == NVFP4 else 1)
+
+
+def _scale_bytes(kind: int, cols: int) -> int:
+    return _up(_up(cols, 32) // (16 if kind == NVFP4 else 32), 16)
+
+
+@dataclass
+class Quantized:
+    """Quantised rows (csf_rows): uint8 codes [rows, code bytes] and scales
+    [rows, scale bytes], rows 16-byte aligned.  `tensor_scale` is the NVFP4
+    tensor scale they were made with (float32 [1]) or None; a product takes it
+    through its alpha."""
+    kind: int
+    codes: torch.Tensor
+    scales: torch.Tensor
+    cols: int
+    tensor_scale: torch.Tensor | None = None
+
+    @property
+    def rows(self) -> int:
+        return self.codes.shape[0]
+
+    def cstruct(self) -> CRows:
+        c, s, t = self.codes, self.scales, self.tensor_scale
+        return CRows(self.kind, self.cols, c.shape[0], c.data_ptr(), c.stride(0), s.data_ptr(), s.stride(0),
+                     None if t is None else t.data_ptr())
+
+
+def empty_quantized(kind: int, rows: int, cols: int, device=None, tensor_scale: torch.Tensor | None = None) -> Quantized:
+    """Quantised rows with undefined contents."""
+    if kind not in (NVFP4, MXFP8):
+        raise CsfError("quantised rows are NVFP4 or MXFP8")
+    device = device if device is not None else "cuda"
+    return Quantized(kind, torch.empty((rows, _code_bytes(kind, cols)), dtype=torch.uint8, device=device),
+                     torch.empty((rows, _scale_bytes(kind, cols)), dtype=torch.uint8, device=device), cols, tensor_scale)
+
+
+def _check_quantized(q: Quantized, what: str):
+    c, s = q.codes, q.scales
+    if q.kind not in (NVFP4, MXFP8):
+        raise CsfError(f"{what}: quantised rows are NVFP4 or MXFP8")
+    if c.dtype != torch.uint8 or s.dtype != torch.uint8 or not c.is_cuda or not s.is_cuda:
+        raise CsfError(f"{what}: codes and scales must be uint8 CUDA tensors")
+    if c.dim() != 2 or s.dim() != 2 or c.shape[0] != s.shape[0] or c.stride(1) != 1 or s.stride(1) != 1:
+        raise CsfError(f"{what}: codes and scales must be [rows, bytes] with contiguous rows")
+    if q.cols < 1 or c.shape[1] < _code_bytes(q.kind, q.cols) or s.shape[1] < _scale_bytes(q.kind, q.cols):
+        raise CsfError(f"{what}: codes or scales are too narrow for {q.cols} columns")
+
+
+def _matrix(t, name: str, rows: int, cols: int, dtype=None):
+    if not t.is_cuda or t.dtype not in _DTYPES or (dtype is not None and t.dtype != dtype):
+        raise CsfError(f"{name} must be a CUDA tensor of {dtype or 'bfloat16, float16 or float32'}")
+    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols or (t.stride(1) != 1 and cols > 1):
+        raise CsfError(f"{name} must be [{rows}, {cols}] with contiguous rows")
+    return t.data_ptr(), (t.stride(0) if rows > 1 else max(t.stride(0), cols))
+
+
+def _vector(t, name: str, n: int, dtype):
+    if t is None:
+        return None
+    if not t.is_cuda or t.dtype != dtype or t.numel() != n or not t.is_contiguous():
+        raise CsfError(f"{name} must be a contiguous CUDA tensor of {n} {dtype}")
+    return t.data_ptr()
+
+
+def rms_norm(x: torch.Tensor, weight: torch.Tensor, kind: int, residual: torch.Tensor | None = None, eps: float = 1e-6,
+             tensor_scale: torch.Tensor | None = None, out: Quantized | None = None,
+             sum_out: torch.Tensor | None = None, stream=None):
+    """Residual addition, root-mean-square norm and quantisation of the rows
+    of `x` [rows, cols] in one launch (csf_rms_norm).  Returns the quantised
+    rows and the sum x + residual (in `sum_out`, which may be `residual`
+    itself, or a new tensor; None without a residual and a `sum_out`)."""
+    if x.dim() != 2 or x.dtype not in _DTYPES:
+        raise CsfError("rms_norm: x must be [rows, cols] of bfloat16, float16 or float32")
+    rows, cols = x.shape
+    xp, xs = _matrix(x, "rms_norm: x", rows, cols)
+    rp, rs = (None, 0) if residual is None else _matrix(residual, "rms_norm: residual", rows, cols, x.dtype)
+    if sum_out is None and residual is not None:
+        sum_out = torch.empty((rows, cols), dtype=x.dtype, device=x.device)
+    sp, ss = (None, 0) if sum_out is None else _matrix(sum_out, "rms_norm: sum_out", rows, cols, x.dtype)
+    wp = _vector(weight, "rms_norm: weight", cols, x.dtype)
+    if out is None:
+        out = empty_quantized(kind, rows, cols, x.device, tensor_scale)
+    else:
+        _check_quantized(out, "rms_norm: out")
+        if out.kind != kind or out.rows != rows or out.cols != cols:
+            raise CsfError("rms_norm: out does not match x and kind")
+        out.tensor_scale = tensor_scale
+    _vector(tensor_scale, "rms_norm: tensor_scale", 1, torch.float32)
+    if tensor_scale is not None and kind != NVFP4:
+        raise CsfError("rms_norm: only NVFP4 rows have a tensor scale")
+    a = CRmsNorm(xp, xs, rp, rs, sp, ss, wp, _DTYPES[x.dtype], eps, out.cstruct())
+    _check(lib.csf_rms_norm(ctypes.byref(a), _stream(stream)), "csf_rms_norm")
+    return out, sum_out
+
+
+@dataclass
+class Routing:
+    """The router's choice (csf_route).  Slots are numbered by expert, then by
+    token; rows[slot] is a slot's token, slots[token, j] a choice's slot."""
+    ids: torch.Tensor            # int32 [tokens, k], -1 where no expert was left
+    weights: torch.Tensor        # float32 [tokens, k]
+    expert_start: torch.Tensor   # int32 [experts + 1], as csf.decode takes it
+    rows: torch.Tensor           # int32 [tokens * k]
+    slots: torch.Tensor          # int32 [tokens, k]
+
+
+def route(logits: torch.Tensor, k: int, renormalize: bool = True, stream=None) -> Routing:
+    """Choose each token's k experts from `logits` [tokens, experts] and group
+    the choices by expert (csf_route)."""
+    if logits.dim() != 2:
+        raise CsfError("route: logits must be [tokens, experts]")
+    T, E = logits.shape
+    lp, ls = _matrix(logits, "route: logits", T, E)
+    dev = logits.device
+    i32 = dict(dtype=torch.int32, device=dev)
+    n = T * max(k, 0)
+    r = Routing(torch.empty((T, max(k, 0)), **i32), torch.empty((T, max(k, 0)), dtype=torch.float32, device=dev),
+                torch.empty(E + 1, **i32), torch.empty(n, **i32), torch.empty((T, max(k, 0)), **i32))
+    need = lib.csf_route_scratch_bytes(T, E)
+    scratch = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+    a = CRoute(lp, ls, _DTYPES[logits.dtype], T, E, k, int(renormalize), r.ids.data_ptr(), r.weights.data_ptr(),
+               r.expert_start.data_ptr(), r.rows.data_ptr(), r.slots.data_ptr(),
+               scratch.data_ptr() if need else None, need)
+    s = stream if stream is not None else torch.cuda.current_stream()
+    if need:
+        scratch.record_stream(s)
+    _check(lib.csf_route(ctypes.byref(a), s.cuda_stream), "csf_route")
+    return r
+
+
+def expert_matmul(x: Quantized, w: torch.Tensor, w_scales: torch.Tensor, expert_start: torch.Tensor | None = None,
+                  rows: torch.Tensor | None = None, alpha: torch.Tensor | None = None, bias: torch.Tensor | None = None,
+                  activation: str | None = None, gated: bool = False, row_scale: torch.Tensor | None = None,
+                  residual: torch.Tensor | None = None, out=torch.bfloat16, out_tensor_scale: torch.Tensor | None = None,
+                  error_word: torch.Tensor | None = None, stream=None):
+    """Block-scaled product of quantised rows with the experts' FP4 weights
+    (csf_expert_matmul).
+
+    `w` is uint8 [E, N, K/2] (NVFP4 weights for NVFP4 rows, MXFP4 for MXFP8),
+    `w_scales` their scales as csf.decode(..., layout=LAYOUT_BLOCKED) writes
+    them.  Slots [expert_start[e], expert_start[e+1]) belong to expert e; slot s
+    reads row rows[s] of x (row s without `rows`).  Without `expert_start` the
+    one expert owns every slot.  p = alpha[e] * (x . w) + bias[e]; y = act(p),
+    or act(p[:N/2]) * p[N/2:] when `gated`; out = y * row_scale[s] + residual.
+    `out` is a dtype, a tensor, NVFP4 or MXFP8 (a new Quantized), or a
+    Quantized.  Activations: None, "relu", "silu", "gelu" (tanh form)."""
+    _check_quantized(x, "expert_matmul: x")
+    if w.dtype != torch.uint8 or not w.is_cuda or w.dim() != 3 or not w.is_contiguous() or w.shape[2] * 2 != x.cols:
+        raise CsfError(f"expert_matmul: w must be a contiguous uint8 CUDA tensor [E, N, {x.cols // 2}]")
+    E, N = w.shape[0], w.shape[1]
+    C = x.cols // (16 if x.kind == NVFP4 else 32)
+    if w_scales.dtype != torch.uint8 or not w_scales.is_cuda or not w_scales.is_contiguous() or \
+            w_scales.numel() < E * _up(N, 128) * _up(C, 4):
+        raise CsfError("expert_matmul: w_scales must be a contiguous uint8 CUDA tensor in the blocked layout")
+    if activation not in _ACTS:
+        raise CsfError(f"expert_matmul: unknown activation {activation!r}")
+    if rows is not None and (not rows.is_cuda or rows.dtype != torch.int32 or not rows.is_contiguous() or rows.dim() != 1):
+        raise CsfError("expert_matmul: rows must be a contiguous int32 CUDA vector")
+    es, es64 = _es(expert_start)
+    if expert_start is not None and expert_start.numel() != E + 1:
+        raise CsfError("expert_start must have E+1 entries")
+    S = x.rows if rows is None else rows.shape[0]
+    F = N // 2 if gated else N
+    bias_dtype = 0
+    if bias is not None:
+        if bias.dtype not in _DTYPES:
+            raise CsfError("expert_matmul: bias must be bfloat16, float16 or float32")
+        bias_dtype = _DTYPES[bias.dtype]
+    rp, rs = (None, 0) if residual is None else _matrix(residual, "expert_matmul: residual", S, F)
+    if isinstance(out, torch.dtype):
+        if out not in _DTYPES:
+            raise CsfError("expert_matmul: out must be bfloat16, float16 or float32")
+        out = torch.empty((S, F), dtype=out, device=x.codes.device)
+    elif isinstance(out, int):
+        out = empty_quantized(out, S, F, x.codes.device, out_tensor_scale)
+    if isinstance(out, Quantized):
+        _check_quantized(out, "expert_matmul: out")
+        if out.rows != S or out.cols != F:
+            raise CsfError("expert_matmul: out does not match the product")
+        out.tensor_scale = out_tensor_scale
+        _vector(out_tensor_scale, "expert_matmul: out_tensor_scale", 1, torch.float32)
+        op, os_, odt, orows = None, 0, 0, out.cstruct()
+    else:
+        op, os_ = _matrix(out, "expert_matmul: out", S, F)
+        odt, orows = _DTYPES[out.dtype], CRows()
+    a = CExpertMatmul(
+        x.cstruct(), None if rows is None else rows.data_ptr(), S, E, N, w.data_ptr(), w_scales.data_ptr(), es, es64,
+        _vector(alpha, "expert_matmul: alpha", E, torch.float32),
+        None if bias is None else _vector(bias, "expert_matmul: bias", E * N, bias.dtype), bias_dtype, _ACTS[activation],
+        int(gated), _vector(row_scale, "expert_matmul: row_scale", S, torch.float32), rp, rs,
+        0 if residual is None else _DTYPES[residual.dtype], odt, op, os_, orows,
+        _vector(error_word, "expert_matmul: error_word", 1, torch.int32))
+    _check(lib.csf_expert_matmul(ctypes.byref(a), _stream(stream)), "csf_expert_matmul")
+    return out
