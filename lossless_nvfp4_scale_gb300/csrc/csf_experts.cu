@@ -16,14 +16,20 @@
 //            the same tile layout)
 //   warp 2   scale copies to tensor memory and the matrix instructions
 //   warp 3   tensor-memory allocation
-//   warps 4-7 epilogue: one weight row a lane, slots along the columns
+//   warps 4-11 epilogue
 // A ring of shared-memory stages of 128 code bytes per row joins them; two
 // accumulator sets let the epilogue of a tile overlap the next tile's
 // products.  A gated product holds two accumulators: row tile t of the gate
 // half and of the up half, from the same x rows.
+//
+// The epilogue reads an accumulator a weight row a lane, 16 slots at a time,
+// applies what belongs to the row (alpha, bias, activation), and turns the
+// 16 x 32 piece around in shared memory, so that a lane then holds 8 columns
+// of one slot: residual and output move 16 bytes a lane, and the lanes of a
+// scale block are neighbours.
 #include <algorithm>
 #include <cstring>
-#include <mutex>
+#include <type_traits>
 
 #include <cuda.h>
 
@@ -34,7 +40,9 @@
 namespace csfk {
 namespace {
 
-constexpr int kMmThreads = 256;
+constexpr int kMmThreads = 384;
+constexpr int kEpiWarps = 8;
+constexpr int kTurnStride = 36;      // floats between slots of a warp's 16 x 32 piece: reads and writes without bank conflicts
 constexpr int kMmMaxExperts = 8192;
 constexpr uint32_t kTmemCols = 512;
 constexpr int kSmemLimit = 227 * 1024;
@@ -69,14 +77,16 @@ struct MmParams {
     int32_t stages;
     uint32_t stage_bytes;
     int32_t act, bias_dtype, residual_dtype;
+    int32_t out_wide, residual_wide;   // 16-byte accesses allowed
 };
 
 enum Out { kOutBf16 = 0, kOutF16 = 1, kOutF32 = 2, kOutNv = 3, kOutMx = 4 };
 
-__device__ __forceinline__ float activate(float v, int act) {
-    if (act == CSF_ACT_RELU) return fmaxf(v, 0.f);
-    if (act == CSF_ACT_SILU) return __fdividef(v, 1.f + __expf(-v));
-    if (act == CSF_ACT_GELU_TANH)   // v * sigmoid(2 * sqrt(2 / pi) * (v + 0.044715 v^3))
+template <int ACT>
+__device__ __forceinline__ float activate(float v) {
+    if constexpr (ACT == CSF_ACT_RELU) return fmaxf(v, 0.f);
+    if constexpr (ACT == CSF_ACT_SILU) return __fdividef(v, 1.f + __expf(-v));
+    if constexpr (ACT == CSF_ACT_GELU_TANH)   // v * sigmoid(2 * sqrt(2 / pi) * (v + 0.044715 v^3))
         return __fdividef(v, 1.f + __expf(-1.5957691216057308f * (v + 0.044715f * v * v * v)));
     return v;
 }
@@ -120,50 +130,113 @@ __device__ __forceinline__ Tile find_tile(const MmParams &p, const uint32_t *fir
     return t;
 }
 
-template <int OUT>
-__device__ __forceinline__ void emit(const MmParams &p, const float (&v)[16], int f, int64_t slot, int n, int lane,
-                                     float tensor_scale, float inv6) {
-    if constexpr (OUT == kOutBf16 || OUT == kOutF16 || OUT == kOutF32) {
-        if (f >= p.F) return;
+// 8 values of a row of type `dtype`, columns f .. f+7, 0 past the row's end.
+struct Raw8 {
+    uint4 a, b;
+};
+
+__device__ __forceinline__ Raw8 load_raw8(const void *base, int64_t at, int dtype, int cols, bool wide) {
+    Raw8 r = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+    if (cols <= 0) return r;
+    if (dtype == CSF_F32) {
+        const float *p = static_cast<const float *>(base) + at;
+        if (wide && cols >= 8) {
+            r.a = reinterpret_cast<const uint4 *>(p)[0];
+            r.b = reinterpret_cast<const uint4 *>(p)[1];
+        } else {
+            uint32_t v[8];
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-            if (j >= n) break;
-            const int64_t at = (slot + j) * p.out_stride + f;
-            if constexpr (OUT == kOutBf16) static_cast<__nv_bfloat16 *>(p.out)[at] = __float2bfloat16_rn(v[j]);
-            if constexpr (OUT == kOutF16) static_cast<__half *>(p.out)[at] = __float2half_rn(v[j]);
-            if constexpr (OUT == kOutF32) static_cast<float *>(p.out)[at] = v[j];
+            for (int i = 0; i < 8; ++i) v[i] = i < cols ? __float_as_uint(p[i]) : 0;
+            r.a = make_uint4(v[0], v[1], v[2], v[3]);
+            r.b = make_uint4(v[4], v[5], v[6], v[7]);
         }
     } else {
-        // A warp's 32 rows are one MXFP8 block or two NVFP4 blocks of each slot.
+        const uint16_t *p = static_cast<const uint16_t *>(base) + at;
+        if (wide && cols >= 8) {
+            r.a = *reinterpret_cast<const uint4 *>(p);
+        } else {
+            uint32_t v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = i < cols ? p[i] : 0;
+            r.a = make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
+        }
+    }
+    return r;
+}
+
+__device__ __forceinline__ void add_raw8(float (&y)[8], const Raw8 &r, int dtype) {
+    const uint32_t u[8] = {r.a.x, r.a.y, r.a.z, r.a.w, r.b.x, r.b.y, r.b.z, r.b.w};
+    if (dtype == CSF_F32) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[i] += __uint_as_float(u[i]);
+    } else if (dtype == CSF_BF16) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            y[2 * i] += __uint_as_float(u[i] << 16);
+            y[2 * i + 1] += __uint_as_float(u[i] & 0xFFFF0000u);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            __half2 h;
+            memcpy(&h, &u[i], 4);
+            const float2 f = __half22float2(h);
+            y[2 * i] += f.x;
+            y[2 * i + 1] += f.y;
+        }
+    }
+}
+
+// Columns f .. f+7 of one slot's output.  Every lane calls it (a scale block
+// is 2 or 4 lanes wide); `live` lanes write.
+template <int OUT>
+__device__ __forceinline__ void emit8(const MmParams &p, float (&y)[8], int f, int64_t slot, bool live, float tensor_scale) {
+    const int cols = p.F - f;
+    if constexpr (OUT == kOutNv || OUT == kOutMx) {
         const int fp = (p.F + 31) & ~31;
-        const bool inside = f < fp;
-        uint8_t *codes = static_cast<uint8_t *>(p.out);
-        const int blocks = OUT == kOutMx ? fp >> 5 : fp >> 4;
-        const int pad = ((blocks + 15) & ~15) - blocks;
-        const bool last_warp = (f | 31) == fp - 1;       // writes the scale row's padding
+        if (cols < 8) {
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-            if (j >= n) break;
-            const float u = f < p.F ? v[j] : 0.f;
-            const uint32_t mag = __float_as_uint(u) & 0x7FFFFFFFu;
-            uint8_t *srow = p.out_scales + (slot + j) * p.out_scale_stride;
-            uint8_t *crow = codes + (slot + j) * p.out_stride;
-            if constexpr (OUT == kOutMx) {
-                const uint32_t s = quant::mx_scale(__reduce_max_sync(0xFFFFFFFFu, mag));
-                const uint32_t q = quant::e4m3(u * quant::mx_inverse(s));
-                if (inside) crow[f] = (uint8_t)q;
-                if (inside && lane == 0) srow[f >> 5] = (uint8_t)s;
+            for (int i = 0; i < 8; ++i) y[i] = i < cols ? y[i] : 0.f;
+        }
+        uint8_t *srow = p.out_scales + slot * p.out_scale_stride;
+        quant::quantize8<OUT == kOutNv ? CSF_ROWS_NVFP4 : CSF_ROWS_MXFP8>(
+            y, static_cast<uint8_t *>(p.out) + slot * p.out_stride, srow, f >> 3, live && f < fp, tensor_scale);
+        if (live && f + 8 == fp) {     // the row's last columns: clear the scale row's padding
+            const int blocks = OUT == kOutNv ? fp >> 4 : fp >> 5;
+            for (int i = blocks; i < ((blocks + 15) & ~15); ++i) srow[i] = 0;
+        }
+    } else {
+        if (!live || cols <= 0) return;
+        if constexpr (OUT == kOutF32) {
+            float *o = static_cast<float *>(p.out) + slot * p.out_stride + f;
+            if (p.out_wide && cols >= 8) {
+                reinterpret_cast<float4 *>(o)[0] = make_float4(y[0], y[1], y[2], y[3]);
+                reinterpret_cast<float4 *>(o)[1] = make_float4(y[4], y[5], y[6], y[7]);
             } else {
-                uint32_t m = mag;
 #pragma unroll
-                for (int d = 1; d < 16; d <<= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
-                const uint32_t s = quant::nv_scale(m, inv6);
-                const float w = u * quant::nv_inverse(s, tensor_scale);
-                const float w1 = __shfl_down_sync(0xFFFFFFFFu, w, 1);
-                if (inside && (lane & 1) == 0) crow[f >> 1] = (uint8_t)quant::e2m1x2(w, w1);
-                if (inside && (lane & 15) == 0) srow[f >> 4] = (uint8_t)s;
+                for (int i = 0; i < 8; ++i)
+                    if (i < cols) o[i] = y[i];
             }
-            if (last_warp && lane < pad) srow[blocks + lane] = 0;
+        } else {
+            uint16_t *o = static_cast<uint16_t *>(p.out) + slot * p.out_stride + f;
+            uint32_t u[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if constexpr (OUT == kOutBf16) {
+                    const __nv_bfloat162 h = __floats2bfloat162_rn(y[2 * i], y[2 * i + 1]);
+                    memcpy(&u[i], &h, 4);
+                } else {
+                    const __half2 h = __floats2half2_rn(y[2 * i], y[2 * i + 1]);
+                    memcpy(&u[i], &h, 4);
+                }
+            }
+            if (p.out_wide && cols >= 8) {
+                *reinterpret_cast<uint4 *>(o) = make_uint4(u[0], u[1], u[2], u[3]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (i < cols) o[i] = (uint16_t)(u[i >> 1] >> (16 * (i & 1)));
+            }
         }
     }
 }
@@ -173,14 +246,15 @@ struct Shared {
     uint32_t tmem, abort, total, warp_sum[kMmThreads / 32];
 };
 
-// KIND: csf_rows_kind of x.  AT: 128-row weight tiles per tile.  GATED: the
-// second one is the up half.
-template <int KIND, int AT, bool GATED, int OUT>
+// KIND: csf_rows_kind of x.  GATED: a tile has 128 gate rows and their up rows.
+template <int KIND, bool GATED, int OUT>
 __global__ void __launch_bounds__(kMmThreads, 1)
 expert_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
                      const __grid_constant__ MmParams p) {
     extern __shared__ __align__(1024) uint8_t dyn[];
     __shared__ Shared sh;
+    __shared__ __align__(16) float turn[kEpiWarps][16 * kTurnStride];
+    constexpr int AT = GATED ? 2 : 1;                     // 128-row weight tiles per tile
     constexpr bool kNv = KIND == CSF_ROWS_NVFP4;
     constexpr int kStepK = kNv ? 256 : 128;               // elements per stage: 128 bytes of codes a row
     constexpr int kTilesPerStage = kNv ? 4 : 1;           // 128 x 4 scale tiles per stage and 128 rows
@@ -208,7 +282,7 @@ expert_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_cons
         }
         for (int i = 0; i < 2; ++i) {
             tc::bar_init(accf0 + 8 * i, 1);
-            tc::bar_init(acce0 + 8 * i, 128);
+            tc::bar_init(acce0 + 8 * i, 32 * kEpiWarps);
         }
         sh.abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -265,7 +339,7 @@ expert_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_cons
         bool ok = true;
         for (uint32_t tile = blockIdx.x; ok && tile < total; tile += gridDim.x) {
             const Tile t = find_tile(p, first, tile, lane);
-            const int row = t.rt * (GATED ? 128 : 128 * AT);
+            const int row = t.rt * 128;
             const uint8_t *sf = p.w_scales + (int64_t)t.e * p.w_scale_expert;
             if (lane == 0) {
                 for (int k = 0; k < ksteps; ++k, ++it) {
@@ -276,10 +350,9 @@ expert_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_cons
                     }
                     const uint32_t base = ring + s * p.stage_bytes, bar = full0 + 8 * s;
                     const int tiles = min(kTilesPerStage, p.ncb - k * kTilesPerStage);
-                    int subs = AT;     // the last tile of an odd count of 128-row blocks has one
-                    if (AT == 2 && row + p.second >= p.N) subs = 1;
-                    tc::bar_expect(bar, (uint32_t)subs * (kACopied + (uint32_t)tiles * 512u));
-                    for (int a = 0; a < subs; ++a) {
+                    tc::bar_expect(bar, (uint32_t)AT * (kACopied + (uint32_t)tiles * 512u));
+#pragma unroll
+                    for (int a = 0; a < AT; ++a) {
                         const int r = row + a * p.second;
                         tc::tma_load_3d(base + a * kABytes, &wmap, kNv ? k * 128 : k * kStepK, r, t.e, bar);
                         tc::bulk_load(base + sfa_off + a * kTilesPerStage * 512u,
@@ -351,8 +424,6 @@ expert_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_cons
             const uint32_t set = nth & 1u, aph = (nth >> 1) & 1u;
             if (lane == 0) {
                 const uint32_t idesc = idesc0 | ((uint32_t)((t.n + 15) >> 4) << 18);
-                int subs = AT;
-                if (AT == 2 && t.rt * (GATED ? 128 : 128 * AT) + p.second >= p.N) subs = 1;
                 ok = tc::bar_wait(acce0 + 8 * set, aph ^ 1u, abort);
                 tc::fence_after();
                 const uint32_t d0 = tmem + set * (AT * kAccCols);
@@ -369,12 +440,12 @@ expert_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_cons
                     const int tiles = min(kTilesPerStage, p.ncb - k * kTilesPerStage);
                     for (int i = 0; i < tiles; ++i) {
                         tc::copy_scales(sf + 4 * i, tc::desc_plain(base + sfb_off + i * 512u));
-                        for (int a = 0; a < subs; ++a)
+                        for (int a = 0; a < AT; ++a)
                             tc::copy_scales(sf + (a + 1) * kSfCols + 4 * i,
                                             tc::desc_plain(base + sfa_off + (a * kTilesPerStage + i) * 512u));
                     }
                     const uint64_t bd = tc::desc_sw128(base + b_off);
-                    for (int a = 0; a < subs; ++a) {
+                    for (int a = 0; a < AT; ++a) {
                         const uint64_t ad = tc::desc_sw128(base + a * kABytes);
                         const uint32_t d = d0 + a * kAccCols, sfa = sf + (a + 1) * kSfCols;
                         if constexpr (kNv) {
@@ -394,60 +465,86 @@ expert_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_cons
         }
     } else if (warp >= 4) {
         // ---- epilogue ----
-        const int w = warp - 4;
+        // Warps w and w + 4 read the same 32 rows and take every other 16 slots.
+        const int w = (warp - 4) & 3, half = (warp - 4) >> 2;
+        const int part = lane & 3, sub = lane >> 2;           // after the turn: 8 columns of a slot
+        float *buf = turn[warp - 4];
         uint32_t nth = 0;
-        float tensor_scale = 1.f, inv6 = 1.f;
+        float tensor_scale = 1.f;
         if constexpr (OUT == kOutNv) {
             if (p.out_tensor_scale) tensor_scale = *p.out_tensor_scale;
-            inv6 = 1.f / (6.f * tensor_scale);
         }
         for (uint32_t tile = blockIdx.x; tile < total; tile += gridDim.x, ++nth) {
             const Tile t = find_tile(p, first, tile, lane);
             const uint32_t set = nth & 1u, aph = (nth >> 1) & 1u;
-            const int row = t.rt * (GATED ? 128 : 128 * AT) + 32 * w + lane;
+            const int row = t.rt * 128 + 32 * w;
+            const int f = row + 8 * part;
             const float alpha = p.alpha ? p.alpha[t.e] : 1.f;
             float bias[AT];
 #pragma unroll
             for (int a = 0; a < AT; ++a) {
-                const int r = row + a * p.second;
+                const int r = row + lane + a * p.second;
                 bias[a] = p.bias && r < p.N ? quant::load_as_float(p.bias, (int64_t)t.e * p.N + r, p.bias_dtype) : 0.f;
             }
-            bool ok = tc::bar_wait(accf0 + 8 * set, aph, abort);
+            // residual and row weight of this lane's slots of a 16-slot piece
+            Raw8 res[2];
+            float rs[2];
+            auto fetch = [&](int c) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int j = c + 8 * i + sub;
+                    const bool live = j < t.n;
+                    rs[i] = p.row_scale && live ? p.row_scale[t.slot + j] : 1.f;
+                    if (p.residual)
+                        res[i] = load_raw8(p.residual, (t.slot + j) * p.residual_stride + f, p.residual_dtype, live ? p.F - f : 0,
+                                           p.residual_wide);
+                }
+            };
+            fetch(16 * half);
+            const bool ok = tc::bar_wait(accf0 + 8 * set, aph, abort);
             if (!__all_sync(0xFFFFFFFFu, ok)) break;
             tc::fence_after();
             const uint32_t d0 = tmem + set * (AT * kAccCols) + ((uint32_t)(32 * w) << 16);
-            for (int c = 0; c < t.n; c += 16) {
-                const int n = min(16, t.n - c);
+            if (16 * half >= t.n) tc::bar_arrive(acce0 + 8 * set);
+            for (int c = 16 * half; c < t.n; c += 32) {
                 float acc[AT][16];
 #pragma unroll
                 for (int a = 0; a < AT; ++a) tc::tmem_load16(d0 + a * kAccCols + c, acc[a]);
                 tc::wait_ld();
-                if (c + 16 >= t.n) {
+                if (c + 32 >= t.n) {
                     tc::fence_before();
                     tc::bar_arrive(acce0 + 8 * set);
                 }
-                const int64_t slot = t.slot + c;
-#pragma unroll
-                for (int a = 0; a < (GATED ? 1 : AT); ++a) {
-                    const int f = row + a * 128;
-                    float y[16];
+                auto turn_in = [&](auto act) {
 #pragma unroll
                     for (int j = 0; j < 16; ++j) {
-                        y[j] = activate(fmaf(acc[a][j], alpha, bias[a]), p.act);
-                        if constexpr (GATED) y[j] *= fmaf(acc[AT - 1][j], alpha, bias[AT - 1]);
+                        float y = activate<decltype(act)::value>(fmaf(acc[0][j], alpha, bias[0]));
+                        if constexpr (GATED) y *= fmaf(acc[AT - 1][j], alpha, bias[AT - 1]);
+                        buf[j * kTurnStride + lane] = y;
                     }
-                    if (p.row_scale) {
-#pragma unroll
-                        for (int j = 0; j < 16; ++j)
-                            if (j < n) y[j] *= p.row_scale[slot + j];
-                    }
-                    if (p.residual && f < p.F) {
-#pragma unroll
-                        for (int j = 0; j < 16; ++j)
-                            if (j < n) y[j] += quant::load_as_float(p.residual, (slot + j) * p.residual_stride + f, p.residual_dtype);
-                    }
-                    emit<OUT>(p, y, f, slot, n, lane, tensor_scale, inv6);
+                };
+                switch (p.act) {
+                    case CSF_ACT_RELU: turn_in(std::integral_constant<int, CSF_ACT_RELU>{}); break;
+                    case CSF_ACT_SILU: turn_in(std::integral_constant<int, CSF_ACT_SILU>{}); break;
+                    case CSF_ACT_GELU_TANH: turn_in(std::integral_constant<int, CSF_ACT_GELU_TANH>{}); break;
+                    default: turn_in(std::integral_constant<int, CSF_ACT_NONE>{}); break;
                 }
+                __syncwarp();
+                const Raw8 r0[2] = {res[0], res[1]};
+                const float s0[2] = {rs[0], rs[1]};
+                if (c + 32 < t.n) fetch(c + 32);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int j = 8 * i + sub;
+                    const float4 lo = *reinterpret_cast<const float4 *>(buf + j * kTurnStride + 8 * part);
+                    const float4 hi = *reinterpret_cast<const float4 *>(buf + j * kTurnStride + 8 * part + 4);
+                    float y[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) y[q] *= s0[i];
+                    if (p.residual) add_raw8(y, r0[i], p.residual_dtype);
+                    emit8<OUT>(p, y, f, t.slot + c + j, c + j < t.n, tensor_scale);
+                }
+                __syncwarp();
             }
         }
     }
@@ -487,20 +584,18 @@ EncodeFn encode_fn() {
 using Kernel = void (*)(CUtensorMap, CUtensorMap, MmParams);
 
 template <int KIND, int OUT>
-Kernel pick(int at, bool gated) {
-    if (gated) return expert_matmul_kernel<KIND, 2, true, OUT>;
-    (void)at;
-    return expert_matmul_kernel<KIND, 1, false, OUT>;
+Kernel pick(bool gated) {
+    return gated ? expert_matmul_kernel<KIND, true, OUT> : expert_matmul_kernel<KIND, false, OUT>;
 }
 
 template <int KIND>
-Kernel pick_out(int out, int at, bool gated) {
+Kernel pick_out(int out, bool gated) {
     switch (out) {
-        case kOutBf16: return pick<KIND, kOutBf16>(at, gated);
-        case kOutF16: return pick<KIND, kOutF16>(at, gated);
-        case kOutF32: return pick<KIND, kOutF32>(at, gated);
-        case kOutNv: return pick<KIND, kOutNv>(at, gated);
-        default: return pick<KIND, kOutMx>(at, gated);
+        case kOutBf16: return pick<KIND, kOutBf16>(gated);
+        case kOutF16: return pick<KIND, kOutF16>(gated);
+        case kOutF32: return pick<KIND, kOutF32>(gated);
+        case kOutNv: return pick<KIND, kOutNv>(gated);
+        default: return pick<KIND, kOutMx>(gated);
     }
 }
 
@@ -574,6 +669,8 @@ extern "C" csf_status csf_expert_matmul(const csf_expert_matmul_args *a, void *s
     p.residual = a->residual;
     p.residual_stride = a->residual_stride;
     p.residual_dtype = a->residual_dtype;
+    p.residual_wide = a->residual && aligned_to(a->residual, 16) &&
+                      (a->residual_stride * (int64_t)dtype_bytes(a->residual_dtype)) % 16 == 0;
     p.err = a->error_word;
     p.slots = a->slots;
     p.x_rows = (int32_t)a->x.rows;
@@ -585,6 +682,7 @@ extern "C" csf_status csf_expert_matmul(const csf_expert_matmul_args *a, void *s
     int out;
     if (a->out) {
         out = a->out_dtype;
+        p.out_wide = aligned_to(a->out, 16) && (a->out_stride * (int64_t)dtype_bytes(out)) % 16 == 0;
         p.out = a->out;
         p.out_stride = a->out_stride;
     } else {
@@ -596,13 +694,13 @@ extern "C" csf_status csf_expert_matmul(const csf_expert_matmul_args *a, void *s
         p.out_tensor_scale = a->out_rows.tensor_scale;
     }
     p.second = a->gated ? N / 2 : 128;
-    p.row_tiles = a->gated ? N / 256 : (N + 128 * at - 1) / (128 * at);
+    p.row_tiles = a->gated ? N / 256 : (N + 127) / 128;
     const int most = at == 1 ? 128 : 96;
     p.nt = (int)std::min<int64_t>(most, round_up(a->slots, 16));
     const uint32_t sf = nv ? 2048u : 512u;
     p.stage_bytes = (uint32_t)round_up(at * 16384 + p.nt * 128 + (at + 1) * sf, 1024);
     const int fixed = 1024 + 4 * (E + 1) + 16;
-    const int room = kSmemLimit - (int)round_up(sizeof(Shared), 1024) - fixed;
+    const int room = kSmemLimit - (int)round_up(sizeof(Shared) + sizeof(float) * kEpiWarps * 16 * kTurnStride, 1024) - fixed;
     p.stages = std::min<int>(kMaxStages, room / (int)p.stage_bytes);
     // never two blocks on an SM: each holds the whole tensor memory
     const int smem = std::max(fixed + p.stages * (int)p.stage_bytes, 120 * 1024);
@@ -631,7 +729,7 @@ extern "C" csf_status csf_expert_matmul(const csf_expert_matmul_args *a, void *s
                    CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
             return CSF_ERR_CUDA;
     }
-    Kernel k = nv ? pick_out<CSF_ROWS_NVFP4>(out, at, a->gated) : pick_out<CSF_ROWS_MXFP8>(out, at, a->gated);
+    Kernel k = nv ? pick_out<CSF_ROWS_NVFP4>(out, a->gated) : pick_out<CSF_ROWS_MXFP8>(out, a->gated);
     if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) {
         cudaGetLastError();
         return CSF_ERR_CUDA;

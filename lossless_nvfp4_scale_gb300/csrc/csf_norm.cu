@@ -83,33 +83,6 @@ __device__ __forceinline__ void load_h(float (&h)[8], const NormParams &p, int64
     }
 }
 
-// Quantise one chunk of y; every thread of a scale block calls it together.
-template <int KIND>
-__device__ __forceinline__ void quantize8(const float (&y)[8], const NormParams &p, int64_t row, int chunk, float g, float inv6) {
-    uint32_t m = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(y[i]) & 0x7FFFFFFFu);
-    m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
-    if constexpr (KIND == CSF_ROWS_MXFP8) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
-    if (chunk >= p.chunks) return;
-    if constexpr (KIND == CSF_ROWS_MXFP8) {
-        const uint32_t s = quant::mx_scale(m);
-        const float inv = quant::mx_inverse(s);
-        uint2 q;
-        q.x = quant::e4m3x2(y[0] * inv, y[1] * inv) | quant::e4m3x2(y[2] * inv, y[3] * inv) << 16;
-        q.y = quant::e4m3x2(y[4] * inv, y[5] * inv) | quant::e4m3x2(y[6] * inv, y[7] * inv) << 16;
-        *reinterpret_cast<uint2 *>(p.codes + row * p.code_stride + chunk * 8) = q;
-        if ((chunk & 3) == 0) p.scales[row * p.scale_stride + (chunk >> 2)] = (uint8_t)s;
-    } else {
-        const uint32_t s = quant::nv_scale(m, inv6);
-        const float inv = quant::nv_inverse(s, g);
-        const uint32_t q = quant::e2m1x2(y[0] * inv, y[1] * inv) | quant::e2m1x2(y[2] * inv, y[3] * inv) << 8 |
-                           quant::e2m1x2(y[4] * inv, y[5] * inv) << 16 | quant::e2m1x2(y[6] * inv, y[7] * inv) << 24;
-        *reinterpret_cast<uint32_t *>(p.codes + row * p.code_stride + chunk * 4) = q;
-        if ((chunk & 1) == 0) p.scales[row * p.scale_stride + (chunk >> 1)] = (uint8_t)s;
-    }
-}
-
 // One row per block of blockDim.x threads (WARP: per warp).  CHUNKS > 0: that
 // many chunks a thread stay in registers; 0: the row is read twice.
 template <typename T, int KIND, int CHUNKS, bool WARP>
@@ -149,7 +122,7 @@ rms_norm_kernel(const __grid_constant__ NormParams p) {
     }
     const float r = rsqrtf(sum * p.inv_cols + p.eps);
     const float g = KIND == CSF_ROWS_NVFP4 && p.tensor_scale ? *p.tensor_scale : 1.f;
-    const float inv6 = 1.f / (6.f * g);
+    uint8_t *codes = p.codes + row * p.code_stride, *scales = p.scales + row * p.scale_stride;
     const T *weight = static_cast<const T *>(p.weight);
     if constexpr (CHUNKS > 0) {
 #pragma unroll
@@ -159,7 +132,7 @@ rms_norm_kernel(const __grid_constant__ NormParams p) {
             load8(w, weight, c * 8, p.cols, p.wide_weight);
 #pragma unroll
             for (int i = 0; i < 8; ++i) h[j][i] = h[j][i] * r * w[i];
-            quantize8<KIND>(h[j], p, row, c, g, inv6);
+            quant::quantize8<KIND>(h[j], codes, scales, c, c < p.chunks, g);
         }
     } else {
         for (int c0 = 0; c0 < p.chunks; c0 += threads) {
@@ -170,11 +143,11 @@ rms_norm_kernel(const __grid_constant__ NormParams p) {
             load8(w, weight, c * 8, p.cols, p.wide_weight);
 #pragma unroll
             for (int i = 0; i < 8; ++i) h[0][i] = h[0][i] * r * w[i];
-            quantize8<KIND>(h[0], p, row, c, g, inv6);
+            quant::quantize8<KIND>(h[0], codes, scales, c, c < p.chunks, g);
         }
     }
     const int blocks = KIND == CSF_ROWS_MXFP8 ? p.chunks >> 2 : p.chunks >> 1;
-    if (tid < ((blocks + 15) & ~15) - blocks) p.scales[row * p.scale_stride + blocks + tid] = 0;
+    if (tid < ((blocks + 15) & ~15) - blocks) scales[blocks + tid] = 0;
 }
 
 template <typename T, int KIND>

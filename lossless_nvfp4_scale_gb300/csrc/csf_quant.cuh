@@ -28,10 +28,10 @@ __device__ __forceinline__ float mx_inverse(uint32_t byte) {
     return __uint_as_float(byte == 255 ? 127u << 23 : (254u - byte) << 23);
 }
 
-// UE4M3 byte of amax / (6 * tensor scale); inv6 = 1 / (6 * tensor scale).
-__device__ __forceinline__ uint32_t nv_scale(uint32_t amax_bits, float inv6) {
+// UE4M3 byte of amax / (6 * tensor scale).
+__device__ __forceinline__ uint32_t nv_scale(uint32_t amax_bits, float six_tensor_scales) {
     if ((amax_bits >> 23) == 255) return 0x7F;
-    return __nv_cvt_float_to_fp8(__uint_as_float(amax_bits) * inv6, __NV_SATFINITE, __NV_E4M3);
+    return __nv_cvt_float_to_fp8(__fdiv_rn(__uint_as_float(amax_bits), six_tensor_scales), __NV_SATFINITE, __NV_E4M3);
 }
 
 // 1 / (scale * tensor scale), 0 for a zero scale.
@@ -50,6 +50,35 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
 // Two values -> two E2M1 codes, the first in the low nibble.
 __device__ __forceinline__ uint32_t e2m1x2(float lo, float hi) {
     return __nv_cvt_float2_to_fp4x2(make_float2(lo, hi), __NV_E2M1, cudaRoundNearest);
+}
+
+// Quantise columns 8 * chunk .. +7 of a row.  Every lane of a block's 4 (32
+// columns, MXFP8) or 2 (16 columns, NVFP4) calls it together, `write` or not.
+template <int KIND>
+__device__ __forceinline__ void quantize8(const float (&y)[8], uint8_t *codes, uint8_t *scales, int chunk, bool write,
+                                          float tensor_scale) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(y[i]) & 0x7FFFFFFFu);
+    m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+    if constexpr (KIND == CSF_ROWS_MXFP8) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+    if (!write) return;
+    if constexpr (KIND == CSF_ROWS_MXFP8) {
+        const uint32_t s = mx_scale(m);
+        const float inv = mx_inverse(s);
+        uint2 q;
+        q.x = e4m3x2(y[0] * inv, y[1] * inv) | e4m3x2(y[2] * inv, y[3] * inv) << 16;
+        q.y = e4m3x2(y[4] * inv, y[5] * inv) | e4m3x2(y[6] * inv, y[7] * inv) << 16;
+        *reinterpret_cast<uint2 *>(codes + chunk * 8) = q;
+        if ((chunk & 3) == 0) scales[chunk >> 2] = (uint8_t)s;
+    } else {
+        const uint32_t s = nv_scale(m, 6.f * tensor_scale);
+        const float inv = nv_inverse(s, tensor_scale);
+        *reinterpret_cast<uint32_t *>(codes + chunk * 4) =
+            e2m1x2(y[0] * inv, y[1] * inv) | e2m1x2(y[2] * inv, y[3] * inv) << 8 |
+            e2m1x2(y[4] * inv, y[5] * inv) << 16 | e2m1x2(y[6] * inv, y[7] * inv) << 24;
+        if ((chunk & 1) == 0) scales[chunk >> 1] = (uint8_t)s;
+    }
 }
 
 __device__ __forceinline__ float load_as_float(const void *p, int64_t i, int dtype) {
