@@ -11,11 +11,12 @@
 //
 // One persistent block per SM walks tiles (expert, slot tile, row tile):
 //   warp 0   weights (TMA, 128-byte swizzle) and their scale tiles
-//   warp 1   x rows gathered through the slot index (TMA gather of four rows
-//            a request) and their scale bytes (4-byte asynchronous copies into
-//            the same tile layout)
+//   warps 1, 3  x rows gathered through the slot index: 16-byte asynchronous
+//            copies, swizzled as TMA would, and 4-byte ones of the scale bytes
+//            into the tile layout.  (TMA's gather of four rows measured 64
+//            cycles a request from one warp, 2000 a stage of 128 rows; the
+//            copies take a tenth of that.)
 //   warp 2   scale copies to tensor memory and the matrix instructions
-//   warp 3   tensor-memory allocation
 //   warps 4-11 epilogue
 // A ring of shared-memory stages of 128 code bytes per row joins them; two
 // accumulator sets let the epilogue of a tile overlap the next tile's
@@ -49,8 +50,8 @@ constexpr int kSmemLimit = 227 * 1024;
 constexpr int kMaxStages = 12;
 
 struct MmParams {
-    const uint8_t *x_scales;
-    int64_t x_scale_stride;
+    const uint8_t *x_codes, *x_scales;
+    int64_t x_code_stride, x_scale_stride;
     const uint8_t *w_scales;
     int64_t w_scale_expert;      // bytes between experts' scale stacks
     const int32_t *rows;
@@ -249,8 +250,7 @@ struct Shared {
 // KIND: csf_rows_kind of x.  GATED: a tile has 128 gate rows and their up rows.
 template <int KIND, bool GATED, int OUT>
 __global__ void __launch_bounds__(kMmThreads, 1)
-expert_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
-                     const __grid_constant__ MmParams p) {
+expert_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ MmParams p) {
     extern __shared__ __align__(1024) uint8_t dyn[];
     __shared__ Shared sh;
     __shared__ __align__(16) float turn[kEpiWarps][16 * kTurnStride];
@@ -277,7 +277,7 @@ expert_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_cons
 
     if (tid == 0) {
         for (int i = 0; i < p.stages; ++i) {
-            tc::bar_init(full0 + 8 * i, 2 + 32);    // two expects and the scale-copying lanes
+            tc::bar_init(full0 + 8 * i, 1 + 64);    // the weights' expect and the copying lanes
             tc::bar_init(empty0 + 8 * i, 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -287,7 +287,7 @@ expert_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_cons
         sh.abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == 3) tc::tmem_alloc(tc::smem_u32(&sh.tmem), kTmemCols);
+    if (warp == 2) tc::tmem_alloc(tc::smem_u32(&sh.tmem), kTmemCols);
 
     // first[e]: number of the first tile of expert e.
     uint32_t running = 0;
@@ -332,22 +332,17 @@ expert_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_cons
 
     if (warp == 0) {
         // ---- weights and their scales ----
-        if (lane == 0) {
-            asm volatile("prefetch.tensormap [%0];" ::"l"(&wmap) : "memory");
-        }
         uint32_t it = 0;
         bool ok = true;
         for (uint32_t tile = blockIdx.x; ok && tile < total; tile += gridDim.x) {
             const Tile t = find_tile(p, first, tile, lane);
             const int row = t.rt * 128;
             const uint8_t *sf = p.w_scales + (int64_t)t.e * p.w_scale_expert;
-            if (lane == 0) {
-                for (int k = 0; k < ksteps; ++k, ++it) {
-                    const uint32_t s = it % (uint32_t)p.stages, ph = (it / (uint32_t)p.stages) & 1u;
-                    if (!tc::bar_wait(empty0 + 8 * s, ph ^ 1u, abort)) {
-                        ok = false;
-                        break;
-                    }
+            for (int k = 0; k < ksteps; ++k, ++it) {
+                const uint32_t s = it % (uint32_t)p.stages, ph = (it / (uint32_t)p.stages) & 1u;
+                ok = __all_sync(0xFFFFFFFFu, tc::bar_wait(empty0 + 8 * s, ph ^ 1u, abort));
+                if (!ok) break;
+                if (tc::elect_one()) {
                     const uint32_t base = ring + s * p.stage_bytes, bar = full0 + 8 * s;
                     const int tiles = min(kTilesPerStage, p.ncb - k * kTilesPerStage);
                     tc::bar_expect(bar, (uint32_t)AT * (kACopied + (uint32_t)tiles * 512u));
@@ -359,57 +354,61 @@ expert_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_cons
                                       sf + ((int64_t)(r >> 7) * p.ncb + k * kTilesPerStage) * 512, (uint32_t)tiles * 512u, bar);
                     }
                 }
+                __syncwarp();
             }
-            ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
         }
-    } else if (warp == 1) {
+    } else if (warp == 1 || warp == 3) {
         // ---- x rows and their scales ----
-        if (lane == 0) {
-            asm volatile("prefetch.tensormap [%0];" ::"l"(&xmap) : "memory");
-        }
+        const int half = warp >> 1;
+        const int piece = lane & 7, sub = lane >> 3;      // 8 lanes a row, 4 rows a copy
+        const int code_bytes = kNv ? p.K / 2 : p.K;
         uint32_t it = 0;
         bool ok = true, bad_row = false;
         for (uint32_t tile = blockIdx.x; ok && tile < total; tile += gridDim.x) {
             const Tile t = find_tile(p, first, tile, lane);
             const int n16 = (t.n + 15) & ~15;
-            // lane l gathers rows 4l .. 4l+3; columns past the tile's slots repeat its last row
-            int32_t r[4], q[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int64_t s = t.slot + min(4 * lane + j, t.n - 1);
+            // columns past the tile's slots repeat its last row; every other group of 4 rows is this warp's
+            auto x_row = [&](int c) {
+                const int64_t s = t.slot + min(c, t.n - 1);
                 const int64_t v = p.rows ? (int64_t)p.rows[s] : s;
-                r[j] = v < 0 || v >= p.x_rows ? 0 : (int32_t)v;
-                bad_row |= r[j] != v;
-            }
-            // and copies the scales of rows l, l + 32, ...
+                const int32_t r = v < 0 || v >= p.x_rows ? 0 : (int32_t)v;
+                bad_row |= r != v;
+                return r;
+            };
+            int32_t code_row[kAccCols / 8], scale_row[kAccCols / 32];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int c = 32 * j + lane;
-                const int32_t o0 = __shfl_sync(0xFFFFFFFFu, r[0], c >> 2), o1 = __shfl_sync(0xFFFFFFFFu, r[1], c >> 2);
-                const int32_t o2 = __shfl_sync(0xFFFFFFFFu, r[2], c >> 2), o3 = __shfl_sync(0xFFFFFFFFu, r[3], c >> 2);
-                q[j] = (c & 2) ? ((c & 1) ? o3 : o2) : ((c & 1) ? o1 : o0);
-            }
-            for (int k = 0; ok && k < ksteps; ++k, ++it) {
+            for (int j = 0; j < kAccCols / 8; ++j) code_row[j] = 8 * j < n16 ? x_row(8 * j + 4 * half + sub) : 0;
+#pragma unroll
+            for (int j = 0; j < kAccCols / 32; ++j) scale_row[j] = 32 * j < n16 ? x_row(32 * j + lane) : 0;
+            for (int k = 0; k < ksteps; ++k, ++it) {
                 const uint32_t s = it % (uint32_t)p.stages, ph = (it / (uint32_t)p.stages) & 1u;
-                ok = tc::bar_wait(empty0 + 8 * s, ph ^ 1u, abort);
-                ok = __all_sync(0xFFFFFFFFu, ok);
+                ok = __all_sync(0xFFFFFFFFu, tc::bar_wait(empty0 + 8 * s, ph ^ 1u, abort));
                 if (!ok) break;
-                const uint32_t base = ring + s * p.stage_bytes, bar = full0 + 8 * s;
-                if (lane == 0) tc::bar_expect(bar, (uint32_t)n16 * 128u);
-                __syncwarp();
-                if (4 * lane < n16) tc::tma_gather4(base + b_off + lane * 512u, &xmap, k * 128, r[0], r[1], r[2], r[3], bar);
+                const uint32_t base = ring + s * p.stage_bytes;
+                const int at = k * 128 + 16 * piece;
+                const bool live = at < code_bytes;
+                const uint8_t *src = p.x_codes + (live ? at : 0);
+                // row r's 16-byte piece q lies at piece q ^ (r % 8) of its 128 bytes
+                const uint32_t dst = base + b_off + (uint32_t)(4 * half + sub) * 128u + (uint32_t)((piece ^ (4 * half + sub)) << 4);
+#pragma unroll
+                for (int j = 0; j < kAccCols / 8; ++j)
+                    if (8 * j < n16) tc::cp_async16(dst + j * 1024u, src + (int64_t)code_row[j] * p.x_code_stride, live);
                 const int tiles = min(kTilesPerStage, p.ncb - k * kTilesPerStage);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
+                for (int j = 0; j < kAccCols / 32; ++j) {
                     if (32 * j + lane < n16) {
-                        const uint8_t *src = p.x_scales + (int64_t)q[j] * p.x_scale_stride + k * (4 * kTilesPerStage);
-                        const uint32_t dst = base + sfb_off + lane * 16u + j * 4u;
+                        const uint8_t *sf = p.x_scales + (int64_t)scale_row[j] * p.x_scale_stride + k * (4 * kTilesPerStage);
+                        const uint32_t to = base + sfb_off + lane * 16u + j * 4u;
+                        if constexpr (kNv) {      // two of the stage's four scale tiles each
 #pragma unroll
-                        for (int i = 0; i < kTilesPerStage; ++i)
-                            if (i < tiles) tc::cp_async4(dst + i * 512u, src + 4 * i);
+                            for (int i = 0; i < 2; ++i)
+                                if (2 * half + i < tiles) tc::cp_async4(to + (2 * half + i) * 512u, sf + 4 * (2 * half + i));
+                        } else if ((j & 1) == half) {
+                            tc::cp_async4(to, sf);
+                        }
                     }
                 }
-                tc::cp_async_arrive(bar);
+                tc::cp_async_arrive(full0 + 8 * s);
             }
         }
         if (bad_row && p.err) atomicOr(p.err, CSF_DEV_ERR_CORRUPT);
@@ -422,46 +421,51 @@ expert_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_cons
         for (uint32_t tile = blockIdx.x; ok && tile < total; tile += gridDim.x, ++nth) {
             const Tile t = find_tile(p, first, tile, lane);
             const uint32_t set = nth & 1u, aph = (nth >> 1) & 1u;
-            if (lane == 0) {
-                const uint32_t idesc = idesc0 | ((uint32_t)((t.n + 15) >> 4) << 18);
-                ok = tc::bar_wait(acce0 + 8 * set, aph ^ 1u, abort);
+            const uint32_t idesc = idesc0 | ((uint32_t)((t.n + 15) >> 4) << 18);
+            ok = __all_sync(0xFFFFFFFFu, tc::bar_wait(acce0 + 8 * set, aph ^ 1u, abort));
+            tc::fence_after();
+            const uint32_t d0 = tmem + set * (AT * kAccCols);
+            for (int k = 0; ok && k < ksteps; ++k, ++it) {
+                const uint32_t s = it % (uint32_t)p.stages, ph = (it / (uint32_t)p.stages) & 1u;
+                ok = __all_sync(0xFFFFFFFFu, tc::bar_wait(full0 + 8 * s, ph, abort));
+                if (!ok) break;
+                tc::fence_async_proxy();     // x came by ordinary copies
                 tc::fence_after();
-                const uint32_t d0 = tmem + set * (AT * kAccCols);
-                for (int k = 0; ok && k < ksteps; ++k, ++it) {
-                    const uint32_t s = it % (uint32_t)p.stages, ph = (it / (uint32_t)p.stages) & 1u;
-                    if (!tc::bar_wait(full0 + 8 * s, ph, abort)) {
-                        ok = false;
-                        break;
+                const uint32_t base = ring + s * p.stage_bytes;
+                const uint32_t sf = tmem + kSfBase + (it & 1u) * kSfSet;
+                const int tiles = min(kTilesPerStage, p.ncb - k * kTilesPerStage);
+                if (tc::elect_one()) {
+                    const uint64_t sb = tc::desc_plain(base + sfb_off), sa = tc::desc_plain(base + sfa_off);
+                    const uint64_t bd = tc::desc_sw128(base + b_off), ad = tc::desc_sw128(base);
+#pragma unroll
+                    for (int i = 0; i < kTilesPerStage; ++i) {
+                        if (i < tiles) {
+                            tc::copy_scales(sf + 4 * i, sb + i * 32);
+#pragma unroll
+                            for (int a = 0; a < AT; ++a)
+                                tc::copy_scales(sf + (a + 1) * kSfCols + 4 * i, sa + (a * kTilesPerStage + i) * 32);
+                        }
                     }
-                    tc::fence_async_proxy();     // the scale bytes of x came by ordinary copies
-                    tc::fence_after();
-                    const uint32_t base = ring + s * p.stage_bytes;
-                    const uint32_t sf = tmem + kSfBase + (it & 1u) * kSfSet;
-                    const int tiles = min(kTilesPerStage, p.ncb - k * kTilesPerStage);
-                    for (int i = 0; i < tiles; ++i) {
-                        tc::copy_scales(sf + 4 * i, tc::desc_plain(base + sfb_off + i * 512u));
-                        for (int a = 0; a < AT; ++a)
-                            tc::copy_scales(sf + (a + 1) * kSfCols + 4 * i,
-                                            tc::desc_plain(base + sfa_off + (a * kTilesPerStage + i) * 512u));
-                    }
-                    const uint64_t bd = tc::desc_sw128(base + b_off);
+#pragma unroll
                     for (int a = 0; a < AT; ++a) {
-                        const uint64_t ad = tc::desc_sw128(base + a * kABytes);
                         const uint32_t d = d0 + a * kAccCols, sfa = sf + (a + 1) * kSfCols;
-                        if constexpr (kNv) {
-                            for (int i = 0; i < tiles; ++i)
-                                tc::mma_nvfp4(d, ad + 2 * i, bd + 2 * i, idesc, sfa + 4 * i, sf + 4 * i, (k | i) != 0);
-                        } else {
-                            for (int i = 0; i < 4; ++i)
-                                tc::mma_mxf8(d, ad + 2 * i, bd + 2 * i, idesc | ((uint32_t)i << 29) | ((uint32_t)i << 4), sfa, sf,
-                                             (k | i) != 0);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            if constexpr (kNv) {
+                                if (i < tiles)
+                                    tc::mma_nvfp4(d, ad + a * (kABytes >> 4) + 2 * i, bd + 2 * i, idesc, sfa + 4 * i, sf + 4 * i,
+                                                  (k | i) != 0);
+                            } else {
+                                tc::mma_mxf8(d, ad + a * (kABytes >> 4) + 2 * i, bd + 2 * i,
+                                             idesc | ((uint32_t)i << 29) | ((uint32_t)i << 4), sfa, sf, (k | i) != 0);
+                            }
                         }
                     }
                     tc::commit(empty0 + 8 * s);
+                    if (k + 1 == ksteps) tc::commit(accf0 + 8 * set);
                 }
-                if (ok) tc::commit(accf0 + 8 * set);
+                __syncwarp();
             }
-            ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
         }
     } else if (warp >= 4) {
         // ---- epilogue ----
@@ -558,7 +562,7 @@ expert_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_cons
         while (tc::timer_ns() - t0 < 5000000ull) __nanosleep(1000);
         __syncthreads();
     }
-    if (warp == 3) tc::tmem_free(tmem, kTmemCols);
+    if (warp == 2) tc::tmem_free(tmem, kTmemCols);
 }
 
 // ---- host side ------------------------------------------------------------------------------------------------------
@@ -581,7 +585,7 @@ EncodeFn encode_fn() {
     return fn;
 }
 
-using Kernel = void (*)(CUtensorMap, CUtensorMap, MmParams);
+using Kernel = void (*)(CUtensorMap, MmParams);
 
 template <int KIND, int OUT>
 Kernel pick(bool gated) {
@@ -653,6 +657,8 @@ extern "C" csf_status csf_expert_matmul(const csf_expert_matmul_args *a, void *s
 
     MmParams p;
     std::memset(&p, 0, sizeof(p));
+    p.x_codes = a->x.codes;
+    p.x_code_stride = a->x.code_stride;
     p.x_scales = a->x.scales;
     p.x_scale_stride = a->x.scale_stride;
     const int32_t C = K / (nv ? 16 : 32);
@@ -711,7 +717,7 @@ extern "C" csf_status csf_expert_matmul(const csf_expert_matmul_args *a, void *s
     EncodeFn encode = encode_fn();
     if (sms < 1 || !encode) return CSF_ERR_CUDA;
 
-    CUtensorMap wmap, xmap;
+    CUtensorMap wmap;
     {
         const cuuint64_t dims[3] = {(cuuint64_t)(nv ? K / 2 : K), (cuuint64_t)N, (cuuint64_t)E};
         const cuuint64_t strides[2] = {(cuuint64_t)K / 2, (cuuint64_t)K / 2 * (cuuint64_t)N};
@@ -721,21 +727,13 @@ extern "C" csf_status csf_expert_matmul(const csf_expert_matmul_args *a, void *s
                    CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
             return CSF_ERR_CUDA;
     }
-    {
-        const cuuint64_t dims[2] = {(cuuint64_t)(nv ? K / 2 : K), (cuuint64_t)a->x.rows};
-        const cuuint64_t strides[1] = {(cuuint64_t)a->x.code_stride};
-        const cuuint32_t box[2] = {128, 1}, ones[2] = {1, 1};
-        if (encode(&xmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, a->x.codes, dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-            return CSF_ERR_CUDA;
-    }
     Kernel k = nv ? pick_out<CSF_ROWS_NVFP4>(out, a->gated) : pick_out<CSF_ROWS_MXFP8>(out, a->gated);
     if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) {
         cudaGetLastError();
         return CSF_ERR_CUDA;
     }
     const int grid = (int)std::min<int64_t>(sms, most_tiles);
-    k<<<grid, kMmThreads, smem, static_cast<cudaStream_t>(stream)>>>(wmap, xmap, p);
+    k<<<grid, kMmThreads, smem, static_cast<cudaStream_t>(stream)>>>(wmap, p);
     if (cudaGetLastError() != cudaSuccess) return CSF_ERR_CUDA;
     return CSF_OK;
 }

@@ -16,6 +16,16 @@ __device__ __forceinline__ uint64_t timer_ns() {
     return t;
 }
 
+// One thread of the warp, known to the compiler as one: what it issues needs
+// no loop over lanes.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t is;
+    asm volatile(
+        "{\n .reg .pred p;\n elect.sync _|p, 0xFFFFFFFF;\n selp.u32 %0, 1, 0, p;\n}"
+        : "=r"(is));
+    return is != 0;
+}
+
 // ---- mbarriers ----------------------------------------------------------------------------------------------------
 
 __device__ __forceinline__ void bar_init(uint32_t bar, uint32_t count) {
@@ -79,18 +89,13 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void *map, int x
         : "memory");
 }
 
-// Four rows of a 2-d tensor, one box row each, to consecutive rows at dst.
-__device__ __forceinline__ void tma_gather4(uint32_t dst, const void *map, int x, int r0, int r1, int r2, int r3,
-                                            uint32_t bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes [%0], [%1, {%2, "
-        "%3, %4, %5, %6}], [%7];" ::"r"(dst),
-        "l"(map), "r"(x), "r"(r0), "r"(r1), "r"(r2), "r"(r3), "r"(bar)
-        : "memory");
-}
-
 __device__ __forceinline__ void cp_async4(uint32_t dst, const void *src) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+
+// 16 bytes, past L1; zeros where `live` is false.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool live) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
 }
 
 // One arrival on bar (already counted in it) once this thread's copies so far have landed.
