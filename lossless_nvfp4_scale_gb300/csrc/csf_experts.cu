@@ -11,13 +11,15 @@
 //
 // One persistent block per SM walks tiles (expert, slot tile, row tile):
 //   warp 0   weights (TMA, 128-byte swizzle) and their scale tiles
-//   warps 1, 3  x rows gathered through the slot index: 16-byte asynchronous
+//   warps 2, 3, 12, 13  x rows gathered through the slot index: 16-byte asynchronous
 //            copies, swizzled as TMA would, and 4-byte ones of the scale bytes
 //            into the tile layout.  (TMA's gather of four rows measured 64
 //            cycles a request from one warp, 2000 a stage of 128 rows; the
 //            copies take a tenth of that.)
-//   warp 2   scale copies to tensor memory and the matrix instructions
-//   warps 4-11 epilogue
+//   warp 1   scale copies to tensor memory and the matrix instructions
+//   warps 4-11  epilogue
+// Their inner loops run alone on a scheduler, a few cycles an instruction, so
+// pointers advance and the ring's position is counted rather than computed.
 // A ring of shared-memory stages of 128 code bytes per row joins them; two
 // accumulator sets let the epilogue of a tile overlap the next tile's
 // products.  A gated product holds two accumulators: row tile t of the gate
@@ -41,8 +43,9 @@
 namespace csfk {
 namespace {
 
-constexpr int kMmThreads = 384;
+constexpr int kMmThreads = 448;
 constexpr int kEpiWarps = 8;
+constexpr int kXWarps = 4;
 constexpr int kTurnStride = 36;      // floats between slots of a warp's 16 x 32 piece: reads and writes without bank conflicts
 constexpr int kMmMaxExperts = 8192;
 constexpr uint32_t kTmemCols = 512;
@@ -242,6 +245,14 @@ __device__ __forceinline__ void emit8(const MmParams &p, float (&y)[8], int f, i
     }
 }
 
+// Position in the ring of stages, and the parity of its round.
+struct Ring {
+    uint32_t s = 0, parity = 0;
+    __device__ __forceinline__ void next(int stages) {
+        if (++s == (uint32_t)stages) s = 0, parity ^= 1u;
+    }
+};
+
 struct Shared {
     uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2];
     uint32_t tmem, abort, total, warp_sum[kMmThreads / 32];
@@ -267,8 +278,8 @@ expert_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_cons
     static_assert(kSfBase + 2 * kSfSet <= kTmemCols, "tensor memory");
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const uint32_t ring = (tc::smem_u32(dyn) + 1023u) & ~1023u;
-    uint32_t *first = reinterpret_cast<uint32_t *>(dyn + (ring - tc::smem_u32(dyn)) + (size_t)p.stages * p.stage_bytes);
+    const uint32_t ring0 = (tc::smem_u32(dyn) + 1023u) & ~1023u;
+    uint32_t *first = reinterpret_cast<uint32_t *>(dyn + (ring0 - tc::smem_u32(dyn)) + (size_t)p.stages * p.stage_bytes);
 
     const uint32_t b_off = AT * kABytes, sfa_off = b_off + (uint32_t)p.nt * 128u,
                    sfb_off = sfa_off + AT * kTilesPerStage * 512u;
@@ -277,7 +288,7 @@ expert_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_cons
 
     if (tid == 0) {
         for (int i = 0; i < p.stages; ++i) {
-            tc::bar_init(full0 + 8 * i, 1 + 64);    // the weights' expect and the copying lanes
+            tc::bar_init(full0 + 8 * i, 1 + 32 * kXWarps);    // the weights' expect and the copying lanes
             tc::bar_init(empty0 + 8 * i, 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -287,7 +298,7 @@ expert_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_cons
         sh.abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == 2) tc::tmem_alloc(tc::smem_u32(&sh.tmem), kTmemCols);
+    if (warp == 1) tc::tmem_alloc(tc::smem_u32(&sh.tmem), kTmemCols);
 
     // first[e]: number of the first tile of expert e.
     uint32_t running = 0;
@@ -332,91 +343,96 @@ expert_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_cons
 
     if (warp == 0) {
         // ---- weights and their scales ----
-        uint32_t it = 0;
+        Ring ring;
         bool ok = true;
         for (uint32_t tile = blockIdx.x; ok && tile < total; tile += gridDim.x) {
             const Tile t = find_tile(p, first, tile, lane);
             const int row = t.rt * 128;
-            const uint8_t *sf = p.w_scales + (int64_t)t.e * p.w_scale_expert;
-            for (int k = 0; k < ksteps; ++k, ++it) {
-                const uint32_t s = it % (uint32_t)p.stages, ph = (it / (uint32_t)p.stages) & 1u;
-                ok = __all_sync(0xFFFFFFFFu, tc::bar_wait(empty0 + 8 * s, ph ^ 1u, abort));
+            const uint8_t *sf = p.w_scales + (int64_t)t.e * p.w_scale_expert + (int64_t)t.rt * p.ncb * 512;
+            int left = p.ncb;
+            for (int k = 0; k < ksteps; ++k, left -= kTilesPerStage, sf += kTilesPerStage * 512, ring.next(p.stages)) {
+                ok = __all_sync(0xFFFFFFFFu, tc::bar_wait(empty0 + 8 * ring.s, ring.parity ^ 1u, abort));
                 if (!ok) break;
                 if (tc::elect_one()) {
-                    const uint32_t base = ring + s * p.stage_bytes, bar = full0 + 8 * s;
-                    const int tiles = min(kTilesPerStage, p.ncb - k * kTilesPerStage);
-                    tc::bar_expect(bar, (uint32_t)AT * (kACopied + (uint32_t)tiles * 512u));
+                    const uint32_t base = ring0 + ring.s * p.stage_bytes, bar = full0 + 8 * ring.s;
+                    const uint32_t bytes = (uint32_t)min(kTilesPerStage, left) * 512u;
+                    tc::bar_expect(bar, (uint32_t)AT * (kACopied + bytes));
 #pragma unroll
                     for (int a = 0; a < AT; ++a) {
-                        const int r = row + a * p.second;
-                        tc::tma_load_3d(base + a * kABytes, &wmap, kNv ? k * 128 : k * kStepK, r, t.e, bar);
-                        tc::bulk_load(base + sfa_off + a * kTilesPerStage * 512u,
-                                      sf + ((int64_t)(r >> 7) * p.ncb + k * kTilesPerStage) * 512, (uint32_t)tiles * 512u, bar);
+                        tc::tma_load_3d(base + a * kABytes, &wmap, kNv ? k * 128 : k * kStepK, row + a * p.second, t.e, bar);
+                        tc::bulk_load(base + sfa_off + a * kTilesPerStage * 512u, sf + (int64_t)a * (p.second >> 7) * p.ncb * 512, bytes, bar);
                     }
                 }
                 __syncwarp();
             }
         }
-    } else if (warp == 1 || warp == 3) {
+    } else if (warp == 2 || warp == 3 || warp >= 4 + kEpiWarps) {
         // ---- x rows and their scales ----
-        const int half = warp >> 1;
-        const int piece = lane & 7, sub = lane >> 3;      // 8 lanes a row, 4 rows a copy
+        const int xw = warp < 4 ? warp - 2 : warp - (2 + kEpiWarps);
+        const int piece = lane & 7, sub = lane >> 3;      // 8 lanes a row, 4 rows a copy; every fourth group of 4 rows
         const int code_bytes = kNv ? p.K / 2 : p.K;
-        uint32_t it = 0;
+        const uint32_t r8 = (uint32_t)(4 * (xw & 1) + sub);   // row mod 8
+        // row r's 16-byte piece q lies at piece q ^ (r % 8) of its 128 bytes
+        const uint32_t b_dst = b_off + (uint32_t)(4 * xw + sub) * 128u + (((uint32_t)piece ^ r8) << 4);
+        const uint32_t sf_dst = sfb_off + (kNv ? xw * 512u : xw * 4u) + lane * 16u;
+        constexpr int kCopies = kAccCols / 16, kScaleCopies = kNv ? kAccCols / 32 : 1;
+        Ring ring;
         bool ok = true, bad_row = false;
         for (uint32_t tile = blockIdx.x; ok && tile < total; tile += gridDim.x) {
             const Tile t = find_tile(p, first, tile, lane);
             const int n16 = (t.n + 15) & ~15;
-            // columns past the tile's slots repeat its last row; every other group of 4 rows is this warp's
+            // columns past the tile's slots repeat its last row
             auto x_row = [&](int c) {
                 const int64_t s = t.slot + min(c, t.n - 1);
                 const int64_t v = p.rows ? (int64_t)p.rows[s] : s;
-                const int32_t r = v < 0 || v >= p.x_rows ? 0 : (int32_t)v;
+                const int64_t r = v < 0 || v >= p.x_rows ? 0 : v;
                 bad_row |= r != v;
                 return r;
             };
-            int32_t code_row[kAccCols / 8], scale_row[kAccCols / 32];
+            const uint8_t *src[kCopies], *sf[kScaleCopies];
 #pragma unroll
-            for (int j = 0; j < kAccCols / 8; ++j) code_row[j] = 8 * j < n16 ? x_row(8 * j + 4 * half + sub) : 0;
+            for (int j = 0; j < kCopies; ++j)
+                src[j] = p.x_codes + (16 * j < n16 ? x_row(16 * j + 4 * xw + sub) * p.x_code_stride : 0) + 16 * piece;
 #pragma unroll
-            for (int j = 0; j < kAccCols / 32; ++j) scale_row[j] = 32 * j < n16 ? x_row(32 * j + lane) : 0;
-            for (int k = 0; k < ksteps; ++k, ++it) {
-                const uint32_t s = it % (uint32_t)p.stages, ph = (it / (uint32_t)p.stages) & 1u;
-                ok = __all_sync(0xFFFFFFFFu, tc::bar_wait(empty0 + 8 * s, ph ^ 1u, abort));
+            for (int j = 0; j < kScaleCopies; ++j) {
+                const int c = 32 * (kNv ? j : xw) + lane;
+                sf[j] = p.x_scales + (c < n16 ? x_row(c) * p.x_scale_stride : 0) + (kNv ? 4 * xw : 0);
+            }
+            const int copies = n16 >> 4;
+            int at = 16 * piece, left = p.ncb;
+            for (int k = 0; k < ksteps; ++k, at += 128, left -= kTilesPerStage, ring.next(p.stages)) {
+                ok = __all_sync(0xFFFFFFFFu, tc::bar_wait(empty0 + 8 * ring.s, ring.parity ^ 1u, abort));
                 if (!ok) break;
-                const uint32_t base = ring + s * p.stage_bytes;
-                const int at = k * 128 + 16 * piece;
+                const uint32_t base = ring0 + ring.s * p.stage_bytes;
+                const uint32_t dst = base + b_dst, sdst = base + sf_dst;
                 const bool live = at < code_bytes;
-                const uint8_t *src = p.x_codes + (live ? at : 0);
-                // row r's 16-byte piece q lies at piece q ^ (r % 8) of its 128 bytes
-                const uint32_t dst = base + b_off + (uint32_t)(4 * half + sub) * 128u + (uint32_t)((piece ^ (4 * half + sub)) << 4);
+                if constexpr (kNv) {          // this warp's one of the stage's four scale tiles
+                    if (xw < left) {
 #pragma unroll
-                for (int j = 0; j < kAccCols / 8; ++j)
-                    if (8 * j < n16) tc::cp_async16(dst + j * 1024u, src + (int64_t)code_row[j] * p.x_code_stride, live);
-                const int tiles = min(kTilesPerStage, p.ncb - k * kTilesPerStage);
-#pragma unroll
-                for (int j = 0; j < kAccCols / 32; ++j) {
-                    if (32 * j + lane < n16) {
-                        const uint8_t *sf = p.x_scales + (int64_t)scale_row[j] * p.x_scale_stride + k * (4 * kTilesPerStage);
-                        const uint32_t to = base + sfb_off + lane * 16u + j * 4u;
-                        if constexpr (kNv) {      // two of the stage's four scale tiles each
-#pragma unroll
-                            for (int i = 0; i < 2; ++i)
-                                if (2 * half + i < tiles) tc::cp_async4(to + (2 * half + i) * 512u, sf + 4 * (2 * half + i));
-                        } else if ((j & 1) == half) {
-                            tc::cp_async4(to, sf);
+                        for (int j = 0; j < kScaleCopies; ++j) {
+                            if (32 * j + lane < n16) tc::cp_async4(sdst + j * 4u, sf[j]);
+                            sf[j] += 16;
                         }
                     }
+                } else {
+                    if (32 * xw + lane < n16) tc::cp_async4(sdst, sf[0]);
+                    sf[0] += 4;
                 }
-                tc::cp_async_arrive(full0 + 8 * s);
+#pragma unroll
+                for (int j = 0; j < kCopies; ++j) {
+                    if (j < copies) tc::cp_async16(dst + j * 2048u, src[j], live);
+                    src[j] += 128;
+                }
+                tc::cp_async_arrive(full0 + 8 * ring.s);
             }
         }
         if (bad_row && p.err) atomicOr(p.err, CSF_DEV_ERR_CORRUPT);
-    } else if (warp == 2) {
+    } else if (warp == 1) {
         // ---- matrix instructions ----
         // Instruction descriptor: operand types, scale type, N / 8, M / 128.
         const uint32_t idesc0 = kNv ? (1u << 7) | (1u << 10) | (1u << 27) : (5u << 7) | (0u << 10) | (1u << 23) | (1u << 27);
-        uint32_t it = 0, nth = 0;
+        Ring ring;
+        uint32_t nth = 0, sf_set = 0;
         bool ok = true;
         for (uint32_t tile = blockIdx.x; ok && tile < total; tile += gridDim.x, ++nth) {
             const Tile t = find_tile(p, first, tile, lane);
@@ -425,105 +441,129 @@ expert_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_cons
             ok = __all_sync(0xFFFFFFFFu, tc::bar_wait(acce0 + 8 * set, aph ^ 1u, abort));
             tc::fence_after();
             const uint32_t d0 = tmem + set * (AT * kAccCols);
-            for (int k = 0; ok && k < ksteps; ++k, ++it) {
-                const uint32_t s = it % (uint32_t)p.stages, ph = (it / (uint32_t)p.stages) & 1u;
-                ok = __all_sync(0xFFFFFFFFu, tc::bar_wait(full0 + 8 * s, ph, abort));
+            int left = p.ncb;
+            for (int k = 0; ok && k < ksteps; ++k, left -= kTilesPerStage, sf_set ^= 1u, ring.next(p.stages)) {
+                ok = __all_sync(0xFFFFFFFFu, tc::bar_wait(full0 + 8 * ring.s, ring.parity, abort));
                 if (!ok) break;
                 tc::fence_async_proxy();     // x came by ordinary copies
                 tc::fence_after();
-                const uint32_t base = ring + s * p.stage_bytes;
-                const uint32_t sf = tmem + kSfBase + (it & 1u) * kSfSet;
-                const int tiles = min(kTilesPerStage, p.ncb - k * kTilesPerStage);
                 if (tc::elect_one()) {
+                    const uint32_t base = ring0 + ring.s * p.stage_bytes;
+                    const uint32_t sf = tmem + kSfBase + sf_set * kSfSet;
                     const uint64_t sb = tc::desc_plain(base + sfb_off), sa = tc::desc_plain(base + sfa_off);
                     const uint64_t bd = tc::desc_sw128(base + b_off), ad = tc::desc_sw128(base);
+                    auto issue = [&](int tiles) {
 #pragma unroll
-                    for (int i = 0; i < kTilesPerStage; ++i) {
-                        if (i < tiles) {
-                            tc::copy_scales(sf + 4 * i, sb + i * 32);
+                        for (int i = 0; i < kTilesPerStage; ++i) {
+                            if (i < tiles) {
+                                tc::copy_scales(sf + 4 * i, sb + i * 32);
 #pragma unroll
-                            for (int a = 0; a < AT; ++a)
-                                tc::copy_scales(sf + (a + 1) * kSfCols + 4 * i, sa + (a * kTilesPerStage + i) * 32);
-                        }
-                    }
-#pragma unroll
-                    for (int a = 0; a < AT; ++a) {
-                        const uint32_t d = d0 + a * kAccCols, sfa = sf + (a + 1) * kSfCols;
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            if constexpr (kNv) {
-                                if (i < tiles)
-                                    tc::mma_nvfp4(d, ad + a * (kABytes >> 4) + 2 * i, bd + 2 * i, idesc, sfa + 4 * i, sf + 4 * i,
-                                                  (k | i) != 0);
-                            } else {
-                                tc::mma_mxf8(d, ad + a * (kABytes >> 4) + 2 * i, bd + 2 * i,
-                                             idesc | ((uint32_t)i << 29) | ((uint32_t)i << 4), sfa, sf, (k | i) != 0);
+                                for (int a = 0; a < AT; ++a)
+                                    tc::copy_scales(sf + (a + 1) * kSfCols + 4 * i, sa + (a * kTilesPerStage + i) * 32);
                             }
                         }
-                    }
-                    tc::commit(empty0 + 8 * s);
+#pragma unroll
+                        for (int a = 0; a < AT; ++a) {
+                            const uint32_t d = d0 + a * kAccCols, sfa = sf + (a + 1) * kSfCols;
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                if constexpr (kNv) {
+                                    if (i < tiles)
+                                        tc::mma_nvfp4(d, ad + a * (kABytes >> 4) + 2 * i, bd + 2 * i, idesc, sfa + 4 * i, sf + 4 * i,
+                                                      (k | i) != 0);
+                                } else {
+                                    tc::mma_mxf8(d, ad + a * (kABytes >> 4) + 2 * i, bd + 2 * i,
+                                                 idesc | ((uint32_t)i << 29) | ((uint32_t)i << 4), sfa, sf, (k | i) != 0);
+                                }
+                            }
+                        }
+                    };
+                    if (left >= kTilesPerStage) issue(kTilesPerStage);
+                    else issue(left);
+                    tc::commit(empty0 + 8 * ring.s);
                     if (k + 1 == ksteps) tc::commit(accf0 + 8 * set);
                 }
                 __syncwarp();
             }
         }
-    } else if (warp >= 4) {
+    } else {
         // ---- epilogue ----
-        // Warps w and w + 4 read the same 32 rows and take every other 16 slots.
+        // Warps w and w + 4 read the same 32 rows and take every other 16
+        // slots.  What a piece reads from memory is fetched one piece ahead,
+        // across tiles.
         const int w = (warp - 4) & 3, half = (warp - 4) >> 2;
         const int part = lane & 3, sub = lane >> 2;           // after the turn: 8 columns of a slot
         float *buf = turn[warp - 4];
-        uint32_t nth = 0;
         float tensor_scale = 1.f;
         if constexpr (OUT == kOutNv) {
             if (p.out_tensor_scale) tensor_scale = *p.out_tensor_scale;
         }
-        for (uint32_t tile = blockIdx.x; tile < total; tile += gridDim.x, ++nth) {
+        struct Piece {
+            int64_t slot;
+            int n, c, f;          // slots of the tile, first slot of the piece, this lane's first column
+            float alpha, bias[AT], rs[2];
+            Raw8 res[2];
+        };
+        auto fetch = [&](Piece &q) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int j = q.c + 8 * i + sub;
+                const bool live = j < q.n;
+                q.rs[i] = p.row_scale && live ? p.row_scale[q.slot + j] : 1.f;
+                if (p.residual)
+                    q.res[i] = load_raw8(p.residual, (q.slot + j) * p.residual_stride + q.f, p.residual_dtype, live ? p.F - q.f : 0,
+                                         p.residual_wide);
+            }
+        };
+        auto open = [&](Piece &q, uint32_t tile) {
             const Tile t = find_tile(p, first, tile, lane);
-            const uint32_t set = nth & 1u, aph = (nth >> 1) & 1u;
             const int row = t.rt * 128 + 32 * w;
-            const int f = row + 8 * part;
-            const float alpha = p.alpha ? p.alpha[t.e] : 1.f;
-            float bias[AT];
+            q.slot = t.slot;
+            q.n = t.n;
+            q.c = 16 * half;
+            q.f = row + 8 * part;
+            q.alpha = p.alpha ? p.alpha[t.e] : 1.f;
 #pragma unroll
             for (int a = 0; a < AT; ++a) {
                 const int r = row + lane + a * p.second;
-                bias[a] = p.bias && r < p.N ? quant::load_as_float(p.bias, (int64_t)t.e * p.N + r, p.bias_dtype) : 0.f;
+                q.bias[a] = p.bias && r < p.N ? quant::load_as_float(p.bias, (int64_t)t.e * p.N + r, p.bias_dtype) : 0.f;
             }
-            // residual and row weight of this lane's slots of a 16-slot piece
-            Raw8 res[2];
-            float rs[2];
-            auto fetch = [&](int c) {
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int j = c + 8 * i + sub;
-                    const bool live = j < t.n;
-                    rs[i] = p.row_scale && live ? p.row_scale[t.slot + j] : 1.f;
-                    if (p.residual)
-                        res[i] = load_raw8(p.residual, (t.slot + j) * p.residual_stride + f, p.residual_dtype, live ? p.F - f : 0,
-                                           p.residual_wide);
-                }
-            };
-            fetch(16 * half);
-            const bool ok = tc::bar_wait(accf0 + 8 * set, aph, abort);
-            if (!__all_sync(0xFFFFFFFFu, ok)) break;
-            tc::fence_after();
-            const uint32_t d0 = tmem + set * (AT * kAccCols) + ((uint32_t)(32 * w) << 16);
-            if (16 * half >= t.n) tc::bar_arrive(acce0 + 8 * set);
-            for (int c = 16 * half; c < t.n; c += 32) {
+            fetch(q);
+        };
+        uint32_t tile = blockIdx.x, nth = 0;
+        Piece cur;
+        if (tile < total) open(cur, tile);
+        while (tile < total) {
+            const uint32_t set = nth & 1u, aph = (nth >> 1) & 1u;
+            const bool opening = cur.c == 16 * half, closing = cur.c + 32 >= cur.n;
+            Piece next = cur;
+            const uint32_t next_tile = closing ? tile + gridDim.x : tile;
+            if (!closing) {
+                next.c += 32;
+                fetch(next);
+            } else if (next_tile < total) {
+                open(next, next_tile);
+            }
+            if (opening) {
+                const bool ok = tc::bar_wait(accf0 + 8 * set, aph, abort);
+                if (!__all_sync(0xFFFFFFFFu, ok)) break;
+                tc::fence_after();
+            }
+            if (cur.c < cur.n) {
+                const uint32_t d = tmem + set * (AT * kAccCols) + ((uint32_t)(32 * w) << 16) + cur.c;
                 float acc[AT][16];
 #pragma unroll
-                for (int a = 0; a < AT; ++a) tc::tmem_load16(d0 + a * kAccCols + c, acc[a]);
+                for (int a = 0; a < AT; ++a) tc::tmem_load16(d + a * kAccCols, acc[a]);
                 tc::wait_ld();
-                if (c + 32 >= t.n) {
+                if (closing) {
                     tc::fence_before();
                     tc::bar_arrive(acce0 + 8 * set);
                 }
                 auto turn_in = [&](auto act) {
 #pragma unroll
                     for (int j = 0; j < 16; ++j) {
-                        float y = activate<decltype(act)::value>(fmaf(acc[0][j], alpha, bias[0]));
-                        if constexpr (GATED) y *= fmaf(acc[AT - 1][j], alpha, bias[AT - 1]);
+                        float y = activate<decltype(act)::value>(fmaf(acc[0][j], cur.alpha, cur.bias[0]));
+                        if constexpr (GATED) y *= fmaf(acc[AT - 1][j], cur.alpha, cur.bias[AT - 1]);
                         buf[j * kTurnStride + lane] = y;
                     }
                 };
@@ -534,9 +574,6 @@ expert_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_cons
                     default: turn_in(std::integral_constant<int, CSF_ACT_NONE>{}); break;
                 }
                 __syncwarp();
-                const Raw8 r0[2] = {res[0], res[1]};
-                const float s0[2] = {rs[0], rs[1]};
-                if (c + 32 < t.n) fetch(c + 32);
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     const int j = 8 * i + sub;
@@ -544,12 +581,17 @@ expert_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_cons
                     const float4 hi = *reinterpret_cast<const float4 *>(buf + j * kTurnStride + 8 * part + 4);
                     float y[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
 #pragma unroll
-                    for (int q = 0; q < 8; ++q) y[q] *= s0[i];
-                    if (p.residual) add_raw8(y, r0[i], p.residual_dtype);
-                    emit8<OUT>(p, y, f, t.slot + c + j, c + j < t.n, tensor_scale);
+                    for (int q = 0; q < 8; ++q) y[q] *= cur.rs[i];
+                    if (p.residual) add_raw8(y, cur.res[i], p.residual_dtype);
+                    emit8<OUT>(p, y, cur.f, cur.slot + cur.c + j, cur.c + j < cur.n, tensor_scale);
                 }
                 __syncwarp();
+            } else {
+                tc::bar_arrive(acce0 + 8 * set);     // no piece of this tile is this warp's
             }
+            cur = next;
+            tile = next_tile;
+            nth += closing;
         }
     }
 
@@ -562,7 +604,7 @@ expert_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_cons
         while (tc::timer_ns() - t0 < 5000000ull) __nanosleep(1000);
         __syncthreads();
     }
-    if (warp == 2) tc::tmem_free(tmem, kTmemCols);
+    if (warp == 1) tc::tmem_free(tmem, kTmemCols);
 }
 
 // ---- host side ------------------------------------------------------------------------------------------------------
