@@ -11,11 +11,10 @@
 //
 // One persistent block per SM walks tiles (expert, slot tile, row tile):
 //   warp 0   weights (TMA, 128-byte swizzle) and their scale tiles
-//   warps 2, 3, 12, 13  x rows gathered through the slot index: 16-byte asynchronous
-//            copies, swizzled as TMA would, and 4-byte ones of the scale bytes
-//            into the tile layout.  (TMA's gather of four rows measured 64
-//            cycles a request from one warp, 2000 a stage of 128 rows; the
-//            copies take a tenth of that.)
+//   warps 2, 3, 12, 13  x rows gathered through the slot index: 16-byte
+//            asynchronous copies, swizzled as TMA would
+//   warp 14  the scale bytes of those rows, through registers into the tile
+//            layout, 32 bytes of a row at a time
 //   warp 1   scale copies to tensor memory and the matrix instructions
 //   warps 4-11  epilogue
 // Their inner loops run alone on a scheduler, a few cycles an instruction, so
@@ -43,7 +42,7 @@
 namespace csfk {
 namespace {
 
-constexpr int kMmThreads = 448;
+constexpr int kMmThreads = 480;
 constexpr int kEpiWarps = 8;
 constexpr int kXWarps = 4;
 constexpr int kTurnStride = 36;      // floats between slots of a warp's 16 x 32 piece: reads and writes without bank conflicts
@@ -109,7 +108,7 @@ struct Tile {
 // The tile with this number: the last expert whose first tile is not past
 // it, found 32 candidates at a time; then its slot tile and row tile (row
 // tiles of one slot tile are neighbours, so their x rows are shared in L2).
-__device__ __forceinline__ Tile find_tile(const MmParams &p, const uint32_t *first, uint32_t tile, int lane) {
+__device__ __forceinline__ Tile find_tile(const MmParams &p, const uint32_t *first, const uint32_t *slot0, uint32_t tile, int lane) {
     int lo = 0, len = p.E;
     while (len > 1) {
         const int step = (len + 31) >> 5;
@@ -126,9 +125,8 @@ __device__ __forceinline__ Tile find_tile(const MmParams &p, const uint32_t *fir
     const uint32_t rt = (uint32_t)p.row_tiles, parts = (first[lo + 1] - first[lo]) / rt;
     const uint32_t part = local / rt;
     t.rt = (int)(local - part * rt);
-    const int64_t s = start_at(p, lo);
-    const int64_t cnt = start_at(p, lo + 1) - s;
-    const int64_t per = ((cnt + parts - 1) / parts + 15) & ~15ll;   // an expert's slot tiles are alike
+    const uint32_t s = slot0[lo], cnt = slot0[lo + 1] - s;
+    const uint32_t per = ((cnt + parts - 1) / parts + 15u) & ~15u;   // an expert's slot tiles are alike
     t.slot = s + part * per;
     t.n = (int)min(per, cnt - part * per);
     return t;
@@ -138,6 +136,16 @@ __device__ __forceinline__ Tile find_tile(const MmParams &p, const uint32_t *fir
 struct Raw8 {
     uint4 a, b;
 };
+
+__device__ __forceinline__ uint32_t load_raw(const void *base, int64_t at, int dtype) {
+    return dtype == CSF_F32 ? static_cast<const uint32_t *>(base)[at] : static_cast<const uint16_t *>(base)[at];
+}
+
+__device__ __forceinline__ float raw_as_float(uint32_t v, int dtype) {
+    if (dtype == CSF_F32) return __uint_as_float(v);
+    if (dtype == CSF_BF16) return __uint_as_float(v << 16);
+    return __half2float(__ushort_as_half((unsigned short)v));
+}
 
 __device__ __forceinline__ Raw8 load_raw8(const void *base, int64_t at, int dtype, int cols, bool wide) {
     Raw8 r = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
@@ -193,6 +201,15 @@ __device__ __forceinline__ void add_raw8(float (&y)[8], const Raw8 &r, int dtype
 
 // Columns f .. f+7 of one slot's output.  Every lane calls it (a scale block
 // is 2 or 4 lanes wide); `live` lanes write.
+// The x row of a tile's column c; columns past its slots repeat the last one.
+__device__ __forceinline__ int64_t x_row(const MmParams &p, const Tile &t, int c, bool &bad) {
+    const int64_t s = t.slot + min(c, t.n - 1);
+    const int64_t v = p.rows ? (int64_t)p.rows[s] : s;
+    const int64_t r = v < 0 || v >= p.x_rows ? 0 : v;
+    bad |= r != v;
+    return r;
+}
+
 template <int OUT>
 __device__ __forceinline__ void emit8(const MmParams &p, float (&y)[8], int f, int64_t slot, bool live, float tensor_scale) {
     const int cols = p.F - f;
@@ -281,6 +298,8 @@ expert_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_cons
     const uint32_t ring0 = (tc::smem_u32(dyn) + 1023u) & ~1023u;
     uint32_t *first = reinterpret_cast<uint32_t *>(dyn + (ring0 - tc::smem_u32(dyn)) + (size_t)p.stages * p.stage_bytes);
 
+    uint32_t *slot0 = first + p.E + 1;          // an expert's first slot
+
     const uint32_t b_off = AT * kABytes, sfa_off = b_off + (uint32_t)p.nt * 128u,
                    sfb_off = sfa_off + AT * kTilesPerStage * 512u;
     const uint32_t full0 = tc::smem_u32(sh.full), empty0 = tc::smem_u32(sh.empty);
@@ -288,7 +307,7 @@ expert_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_cons
 
     if (tid == 0) {
         for (int i = 0; i < p.stages; ++i) {
-            tc::bar_init(full0 + 8 * i, 1 + 32 * kXWarps);    // the weights' expect and the copying lanes
+            tc::bar_init(full0 + 8 * i, 2 + 32 * kXWarps);    // the weights' expect, the scales, the copying lanes
             tc::bar_init(empty0 + 8 * i, 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -308,6 +327,7 @@ expert_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_cons
         uint32_t tiles = 0;
         if (e < p.E) {
             const int64_t a = start_at(p, e), b = start_at(p, e + 1);
+            slot0[e] = (uint32_t)a;
             if (b > a) tiles = (uint32_t)((b - a + p.nt - 1) / p.nt) * (uint32_t)p.row_tiles;
             if (p.start) {
                 const long long raw = p.es64 ? static_cast<const long long *>(p.start)[e + 1] : static_cast<const int *>(p.start)[e + 1];
@@ -331,7 +351,7 @@ expert_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_cons
         if (e < p.E) first[e] = before + sum - tiles;
         __syncthreads();
     }
-    if (tid == 0) first[p.E] = running;
+    if (tid == 0) first[p.E] = running, slot0[p.E] = (uint32_t)start_at(p, p.E);
     if (bad && p.err && blockIdx.x == 0) atomicOr(p.err, CSF_DEV_ERR_CORRUPT);
     tc::fence_before();
     __syncthreads();
@@ -346,7 +366,7 @@ expert_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_cons
         Ring ring;
         bool ok = true;
         for (uint32_t tile = blockIdx.x; ok && tile < total; tile += gridDim.x) {
-            const Tile t = find_tile(p, first, tile, lane);
+            const Tile t = find_tile(p, first, slot0, tile, lane);
             const int row = t.rt * 128;
             const uint8_t *sf = p.w_scales + (int64_t)t.e * p.w_scale_expert + (int64_t)t.rt * p.ncb * 512;
             int left = p.ncb;
@@ -366,64 +386,97 @@ expert_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_cons
                 __syncwarp();
             }
         }
-    } else if (warp == 2 || warp == 3 || warp >= 4 + kEpiWarps) {
-        // ---- x rows and their scales ----
+    } else if (warp == 2 || warp == 3 || (warp >= 4 + kEpiWarps && warp < 4 + kEpiWarps + kXWarps - 2)) {
+        // ---- x rows ----
         const int xw = warp < 4 ? warp - 2 : warp - (2 + kEpiWarps);
         const int piece = lane & 7, sub = lane >> 3;      // 8 lanes a row, 4 rows a copy; every fourth group of 4 rows
         const int code_bytes = kNv ? p.K / 2 : p.K;
         const uint32_t r8 = (uint32_t)(4 * (xw & 1) + sub);   // row mod 8
         // row r's 16-byte piece q lies at piece q ^ (r % 8) of its 128 bytes
         const uint32_t b_dst = b_off + (uint32_t)(4 * xw + sub) * 128u + (((uint32_t)piece ^ r8) << 4);
-        const uint32_t sf_dst = sfb_off + (kNv ? xw * 512u : xw * 4u) + lane * 16u;
-        constexpr int kCopies = kAccCols / 16, kScaleCopies = kNv ? kAccCols / 32 : 1;
+        constexpr int kCopies = kAccCols / 16;
         Ring ring;
         bool ok = true, bad_row = false;
         for (uint32_t tile = blockIdx.x; ok && tile < total; tile += gridDim.x) {
-            const Tile t = find_tile(p, first, tile, lane);
-            const int n16 = (t.n + 15) & ~15;
-            // columns past the tile's slots repeat its last row
-            auto x_row = [&](int c) {
-                const int64_t s = t.slot + min(c, t.n - 1);
-                const int64_t v = p.rows ? (int64_t)p.rows[s] : s;
-                const int64_t r = v < 0 || v >= p.x_rows ? 0 : v;
-                bad_row |= r != v;
-                return r;
-            };
-            const uint8_t *src[kCopies], *sf[kScaleCopies];
+            const Tile t = find_tile(p, first, slot0, tile, lane);
+            const uint8_t *src[kCopies];
 #pragma unroll
             for (int j = 0; j < kCopies; ++j)
-                src[j] = p.x_codes + (16 * j < n16 ? x_row(16 * j + 4 * xw + sub) * p.x_code_stride : 0) + 16 * piece;
-#pragma unroll
-            for (int j = 0; j < kScaleCopies; ++j) {
-                const int c = 32 * (kNv ? j : xw) + lane;
-                sf[j] = p.x_scales + (c < n16 ? x_row(c) * p.x_scale_stride : 0) + (kNv ? 4 * xw : 0);
-            }
-            const int copies = n16 >> 4;
-            int at = 16 * piece, left = p.ncb;
-            for (int k = 0; k < ksteps; ++k, at += 128, left -= kTilesPerStage, ring.next(p.stages)) {
+                src[j] = p.x_codes + (16 * j < t.n ? x_row(p, t, 16 * j + 4 * xw + sub, bad_row) * p.x_code_stride : 0) + 16 * piece;
+            const int copies = (t.n + 15) >> 4;
+            int at = 16 * piece;
+            for (int k = 0; k < ksteps; ++k, at += 128, ring.next(p.stages)) {
                 ok = __all_sync(0xFFFFFFFFu, tc::bar_wait(empty0 + 8 * ring.s, ring.parity ^ 1u, abort));
                 if (!ok) break;
-                const uint32_t base = ring0 + ring.s * p.stage_bytes;
-                const uint32_t dst = base + b_dst, sdst = base + sf_dst;
+                const uint32_t dst = ring0 + ring.s * p.stage_bytes + b_dst;
                 const bool live = at < code_bytes;
-                if constexpr (kNv) {          // this warp's one of the stage's four scale tiles
-                    if (xw < left) {
-#pragma unroll
-                        for (int j = 0; j < kScaleCopies; ++j) {
-                            if (32 * j + lane < n16) tc::cp_async4(sdst + j * 4u, sf[j]);
-                            sf[j] += 16;
-                        }
-                    }
-                } else {
-                    if (32 * xw + lane < n16) tc::cp_async4(sdst, sf[0]);
-                    sf[0] += 4;
-                }
 #pragma unroll
                 for (int j = 0; j < kCopies; ++j) {
                     if (j < copies) tc::cp_async16(dst + j * 2048u, src[j], live);
                     src[j] += 128;
                 }
                 tc::cp_async_arrive(full0 + 8 * ring.s);
+            }
+        }
+        if (bad_row && p.err) atomicOr(p.err, CSF_DEV_ERR_CORRUPT);
+    } else if (warp == 4 + kEpiWarps + kXWarps - 2) {
+        // ---- scales of the x rows ----
+        // Row lane + 32 j; 16 bytes are four scale tiles: a stage (NVFP4) or
+        // four (MXFP8).  The next 32 bytes are under way while these leave.
+        constexpr int kRows = kAccCols / 32, kStagesPer16 = 4 / kTilesPerStage;
+        const int units = (p.ncb + 3) / 4;
+        Ring ring;
+        bool ok = true, bad_row = false;
+        for (uint32_t tile = blockIdx.x; ok && tile < total; tile += gridDim.x) {
+            const Tile t = find_tile(p, first, slot0, tile, lane);
+            const uint4 *src[kRows];
+            uint4 next[kRows][2];
+#pragma unroll
+            for (int j = 0; j < kRows; ++j)
+                src[j] = reinterpret_cast<const uint4 *>(p.x_scales + (32 * j < t.n ? x_row(p, t, 32 * j + lane, bad_row) * p.x_scale_stride : 0));
+            auto load = [&](int u) {
+#pragma unroll
+                for (int j = 0; j < kRows; ++j)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        if (32 * j < t.n && u + h < units) next[j][h] = __ldg(src[j] + u + h);
+            };
+            load(0);
+            int k = 0;
+            for (int u = 0; ok && u < units; u += 2) {
+                uint4 now[kRows][2];
+#pragma unroll
+                for (int j = 0; j < kRows; ++j) now[j][0] = next[j][0], now[j][1] = next[j][1];
+                load(u + 2);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                    for (int q = 0; q < kStagesPer16; ++q) {
+                        if (!ok || k >= ksteps) break;
+                        ok = __all_sync(0xFFFFFFFFu, tc::bar_wait(empty0 + 8 * ring.s, ring.parity ^ 1u, abort));
+                        if (!ok) break;
+                        const uint32_t dst = ring0 + ring.s * p.stage_bytes + sfb_off + lane * 16u;
+#pragma unroll
+                        for (int j = 0; j < kRows; ++j) {
+                            if (32 * j < t.n) {
+                                const uint4 v = now[j][h];
+                                if constexpr (kNv) {
+                                    tc::store_shared(dst + j * 4u, v.x);
+                                    tc::store_shared(dst + j * 4u + 512u, v.y);
+                                    tc::store_shared(dst + j * 4u + 1024u, v.z);
+                                    tc::store_shared(dst + j * 4u + 1536u, v.w);
+                                } else {
+                                    tc::store_shared(dst + j * 4u, q == 0 ? v.x : q == 1 ? v.y : q == 2 ? v.z : v.w);
+                                }
+                            }
+                        }
+                        tc::fence_async_proxy();
+                        __syncwarp();
+                        if (lane == 0) tc::bar_arrive(full0 + 8 * ring.s);
+                        ring.next(p.stages);
+                        ++k;
+                    }
+                }
             }
         }
         if (bad_row && p.err) atomicOr(p.err, CSF_DEV_ERR_CORRUPT);
@@ -435,7 +488,7 @@ expert_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_cons
         uint32_t nth = 0, sf_set = 0;
         bool ok = true;
         for (uint32_t tile = blockIdx.x; ok && tile < total; tile += gridDim.x, ++nth) {
-            const Tile t = find_tile(p, first, tile, lane);
+            const Tile t = find_tile(p, first, slot0, tile, lane);
             const uint32_t set = nth & 1u, aph = (nth >> 1) & 1u;
             const uint32_t idesc = idesc0 | ((uint32_t)((t.n + 15) >> 4) << 18);
             ok = __all_sync(0xFFFFFFFFu, tc::bar_wait(acce0 + 8 * set, aph ^ 1u, abort));
@@ -486,7 +539,7 @@ expert_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_cons
                 __syncwarp();
             }
         }
-    } else {
+    } else if (warp < 4 + kEpiWarps) {
         // ---- epilogue ----
         // Warps w and w + 4 read the same 32 rows and take every other 16
         // slots.  What a piece reads from memory is fetched one piece ahead,
@@ -501,7 +554,8 @@ expert_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_cons
         struct Piece {
             int64_t slot;
             int n, c, f;          // slots of the tile, first slot of the piece, this lane's first column
-            float alpha, bias[AT], rs[2];
+            float alpha, rs[2];
+            uint32_t bias[AT];    // as stored
             Raw8 res[2];
         };
         auto fetch = [&](Piece &q) {
@@ -516,7 +570,7 @@ expert_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_cons
             }
         };
         auto open = [&](Piece &q, uint32_t tile) {
-            const Tile t = find_tile(p, first, tile, lane);
+            const Tile t = find_tile(p, first, slot0, tile, lane);
             const int row = t.rt * 128 + 32 * w;
             q.slot = t.slot;
             q.n = t.n;
@@ -526,7 +580,7 @@ expert_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_cons
 #pragma unroll
             for (int a = 0; a < AT; ++a) {
                 const int r = row + lane + a * p.second;
-                q.bias[a] = p.bias && r < p.N ? quant::load_as_float(p.bias, (int64_t)t.e * p.N + r, p.bias_dtype) : 0.f;
+                q.bias[a] = p.bias && r < p.N ? load_raw(p.bias, (int64_t)t.e * p.N + r, p.bias_dtype) : 0u;
             }
             fetch(q);
         };
@@ -559,11 +613,14 @@ expert_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_cons
                     tc::fence_before();
                     tc::bar_arrive(acce0 + 8 * set);
                 }
+                float bias[AT];
+#pragma unroll
+                for (int a = 0; a < AT; ++a) bias[a] = raw_as_float(cur.bias[a], p.bias_dtype);
                 auto turn_in = [&](auto act) {
 #pragma unroll
                     for (int j = 0; j < 16; ++j) {
-                        float y = activate<decltype(act)::value>(fmaf(acc[0][j], cur.alpha, cur.bias[0]));
-                        if constexpr (GATED) y *= fmaf(acc[AT - 1][j], cur.alpha, cur.bias[AT - 1]);
+                        float y = activate<decltype(act)::value>(fmaf(acc[0][j], cur.alpha, bias[0]));
+                        if constexpr (GATED) y *= fmaf(acc[AT - 1][j], cur.alpha, bias[AT - 1]);
                         buf[j * kTurnStride + lane] = y;
                     }
                 };
@@ -747,7 +804,7 @@ extern "C" csf_status csf_expert_matmul(const csf_expert_matmul_args *a, void *s
     p.nt = (int)std::min<int64_t>(most, round_up(a->slots, 16));
     const uint32_t sf = nv ? 2048u : 512u;
     p.stage_bytes = (uint32_t)round_up(at * 16384 + p.nt * 128 + (at + 1) * sf, 1024);
-    const int fixed = 1024 + 4 * (E + 1) + 16;
+    const int fixed = 1024 + 8 * (E + 1) + 16;
     const int room = kSmemLimit - (int)round_up(sizeof(Shared) + sizeof(float) * kEpiWarps * 16 * kTurnStride, 1024) - fixed;
     p.stages = std::min<int>(kMaxStages, room / (int)p.stage_bytes);
     // never two blocks on an SM: each holds the whole tensor memory

@@ -89,8 +89,8 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void *map, int x
         : "memory");
 }
 
-__device__ __forceinline__ void cp_async4(uint32_t dst, const void *src) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+__device__ __forceinline__ void store_shared(uint32_t dst, uint32_t v) {
+    asm volatile("st.shared.u32 [%0], %1;" ::"r"(dst), "r"(v) : "memory");
 }
 
 // 16 bytes, past L1; zeros where `live` is false.
