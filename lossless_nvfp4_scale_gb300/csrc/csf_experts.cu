@@ -24,9 +24,9 @@
 // products.  A gated product holds two accumulators: row tile t of the gate
 // half and of the up half, from the same x rows.
 //
-// The epilogue reads an accumulator a weight row a lane, 16 slots at a time,
+// The epilogue reads an accumulator a weight row a lane, 8 slots at a time,
 // applies what belongs to the row (alpha, bias, activation), and turns the
-// 16 x 32 piece around in shared memory, so that a lane then holds 8 columns
+// 8 x 32 piece around in shared memory, so that a lane then holds 8 columns
 // of one slot: residual and output move 16 bytes a lane, and the lanes of a
 // scale block are neighbours.
 #include <algorithm>
@@ -45,7 +45,7 @@ namespace {
 constexpr int kMmThreads = 480;
 constexpr int kEpiWarps = 8;
 constexpr int kXWarps = 4;
-constexpr int kTurnStride = 36;      // floats between slots of a warp's 16 x 32 piece: reads and writes without bank conflicts
+constexpr int kTurnStride = 36;      // floats between slots of a warp's 8 x 32 piece: reads and writes without bank conflicts
 constexpr int kMmMaxExperts = 8192;
 constexpr uint32_t kTmemCols = 512;
 constexpr int kSmemLimit = 227 * 1024;
@@ -132,11 +132,6 @@ __device__ __forceinline__ Tile find_tile(const MmParams &p, const uint32_t *fir
     return t;
 }
 
-// 8 values of a row of type `dtype`, columns f .. f+7, 0 past the row's end.
-struct Raw8 {
-    uint4 a, b;
-};
-
 __device__ __forceinline__ uint32_t load_raw(const void *base, int64_t at, int dtype) {
     return dtype == CSF_F32 ? static_cast<const uint32_t *>(base)[at] : static_cast<const uint16_t *>(base)[at];
 }
@@ -147,46 +142,44 @@ __device__ __forceinline__ float raw_as_float(uint32_t v, int dtype) {
     return __half2float(__ushort_as_half((unsigned short)v));
 }
 
-__device__ __forceinline__ Raw8 load_raw8(const void *base, int64_t at, int dtype, int cols, bool wide) {
+// 8 values of a row of type `dtype`, as stored.
+struct Raw8 {
+    uint4 a, b;
+};
+
+// The first `cols` of 8 values, one at a time: ragged or unaligned rows.
+__device__ __noinline__ Raw8 load_few(const char *p, int dtype, int cols) {
+    uint32_t v[8];
+    for (int i = 0; i < 8; ++i) v[i] = i < cols ? load_raw(p, i, dtype) : 0;
+    Raw8 r;
+    r.a = dtype == CSF_F32 ? make_uint4(v[0], v[1], v[2], v[3])
+                           : make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
+    r.b = make_uint4(v[4], v[5], v[6], v[7]);
+    return r;
+}
+
+__device__ __forceinline__ Raw8 load_raw8(const char *p, int dtype, int cols, bool wide) {
     Raw8 r = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
-    if (cols <= 0) return r;
-    if (dtype == CSF_F32) {
-        const float *p = static_cast<const float *>(base) + at;
-        if (wide && cols >= 8) {
-            r.a = reinterpret_cast<const uint4 *>(p)[0];
-            r.b = reinterpret_cast<const uint4 *>(p)[1];
-        } else {
-            uint32_t v[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = i < cols ? __float_as_uint(p[i]) : 0;
-            r.a = make_uint4(v[0], v[1], v[2], v[3]);
-            r.b = make_uint4(v[4], v[5], v[6], v[7]);
-        }
-    } else {
-        const uint16_t *p = static_cast<const uint16_t *>(base) + at;
-        if (wide && cols >= 8) {
-            r.a = *reinterpret_cast<const uint4 *>(p);
-        } else {
-            uint32_t v[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = i < cols ? p[i] : 0;
-            r.a = make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
-        }
+    if (wide && cols >= 8) {
+        r.a = reinterpret_cast<const uint4 *>(p)[0];
+        if (dtype == CSF_F32) r.b = reinterpret_cast<const uint4 *>(p)[1];
+    } else if (cols > 0) {
+        r = load_few(p, dtype, cols);
     }
     return r;
 }
 
 __device__ __forceinline__ void add_raw8(float (&y)[8], const Raw8 &r, int dtype) {
     const uint32_t u[8] = {r.a.x, r.a.y, r.a.z, r.a.w, r.b.x, r.b.y, r.b.z, r.b.w};
-    if (dtype == CSF_F32) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] += __uint_as_float(u[i]);
-    } else if (dtype == CSF_BF16) {
+    if (dtype == CSF_BF16) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             y[2 * i] += __uint_as_float(u[i] << 16);
             y[2 * i + 1] += __uint_as_float(u[i] & 0xFFFF0000u);
         }
+    } else if (dtype == CSF_F32) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[i] += __uint_as_float(u[i]);
     } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -199,8 +192,65 @@ __device__ __forceinline__ void add_raw8(float (&y)[8], const Raw8 &r, int dtype
     }
 }
 
-// Columns f .. f+7 of one slot's output.  Every lane calls it (a scale block
-// is 2 or 4 lanes wide); `live` lanes write.
+// The first `cols` of 8 elements of 2 bytes (in u) or 4 (y), one at a time.
+template <bool F32>
+__device__ __noinline__ void store_few(char *o, uint4 u, float4 lo, float4 hi, int cols) {
+    const uint32_t h[4] = {u.x, u.y, u.z, u.w};
+    const float y[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+    for (int i = 0; i < 8; ++i) {
+        if (i >= cols) break;
+        if (F32) reinterpret_cast<float *>(o)[i] = y[i];
+        else reinterpret_cast<uint16_t *>(o)[i] = (uint16_t)(h[i >> 1] >> (16 * (i & 1)));
+    }
+}
+
+// Columns f .. f+7 of one slot's output, at o (and the slot's scales at
+// srow).  Every lane calls it (a scale block is 2 or 4 lanes wide); `live`
+// lanes write.
+template <int OUT>
+__device__ __forceinline__ void emit8(const MmParams &p, float (&y)[8], int f, char *o, uint8_t *srow, bool live,
+                                      float tensor_scale) {
+    const int cols = p.F - f;
+    if constexpr (OUT == kOutNv || OUT == kOutMx) {
+        constexpr int kKind = OUT == kOutNv ? CSF_ROWS_NVFP4 : CSF_ROWS_MXFP8;
+        const int fp = (p.F + 31) & ~31;
+        if (cols < 8) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) y[i] = i < cols ? y[i] : 0.f;
+        }
+        quant::quantize8<kKind>(y, reinterpret_cast<uint8_t *>(o), srow, f >> 3, live && f < fp, tensor_scale);
+        if (live && f + 8 == fp) {     // the row's last columns: clear the scale row's padding
+            const int blocks = OUT == kOutNv ? fp >> 4 : fp >> 5;
+            for (int i = blocks; i < ((blocks + 15) & ~15); ++i) srow[i] = 0;
+        }
+    } else if constexpr (OUT == kOutF32) {
+        if (!live || cols <= 0) return;
+        const float4 lo = make_float4(y[0], y[1], y[2], y[3]), hi = make_float4(y[4], y[5], y[6], y[7]);
+        if (p.out_wide && cols >= 8) {
+            reinterpret_cast<float4 *>(o)[0] = lo;
+            reinterpret_cast<float4 *>(o)[1] = hi;
+        } else {
+            store_few<true>(o, make_uint4(0, 0, 0, 0), lo, hi, cols);
+        }
+    } else {
+        if (!live || cols <= 0) return;
+        uint32_t u[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (OUT == kOutBf16) {
+                const __nv_bfloat162 h = __floats2bfloat162_rn(y[2 * i], y[2 * i + 1]);
+                memcpy(&u[i], &h, 4);
+            } else {
+                const __half2 h = __floats2half2_rn(y[2 * i], y[2 * i + 1]);
+                memcpy(&u[i], &h, 4);
+            }
+        }
+        const uint4 q = make_uint4(u[0], u[1], u[2], u[3]);
+        if (p.out_wide && cols >= 8) *reinterpret_cast<uint4 *>(o) = q;
+        else store_few<false>(o, q, make_float4(0, 0, 0, 0), make_float4(0, 0, 0, 0), cols);
+    }
+}
+
 // The x row of a tile's column c; columns past its slots repeat the last one.
 __device__ __forceinline__ int64_t x_row(const MmParams &p, const Tile &t, int c, bool &bad) {
     const int64_t s = t.slot + min(c, t.n - 1);
@@ -208,58 +258,6 @@ __device__ __forceinline__ int64_t x_row(const MmParams &p, const Tile &t, int c
     const int64_t r = v < 0 || v >= p.x_rows ? 0 : v;
     bad |= r != v;
     return r;
-}
-
-template <int OUT>
-__device__ __forceinline__ void emit8(const MmParams &p, float (&y)[8], int f, int64_t slot, bool live, float tensor_scale) {
-    const int cols = p.F - f;
-    if constexpr (OUT == kOutNv || OUT == kOutMx) {
-        const int fp = (p.F + 31) & ~31;
-        if (cols < 8) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) y[i] = i < cols ? y[i] : 0.f;
-        }
-        uint8_t *srow = p.out_scales + slot * p.out_scale_stride;
-        quant::quantize8<OUT == kOutNv ? CSF_ROWS_NVFP4 : CSF_ROWS_MXFP8>(
-            y, static_cast<uint8_t *>(p.out) + slot * p.out_stride, srow, f >> 3, live && f < fp, tensor_scale);
-        if (live && f + 8 == fp) {     // the row's last columns: clear the scale row's padding
-            const int blocks = OUT == kOutNv ? fp >> 4 : fp >> 5;
-            for (int i = blocks; i < ((blocks + 15) & ~15); ++i) srow[i] = 0;
-        }
-    } else {
-        if (!live || cols <= 0) return;
-        if constexpr (OUT == kOutF32) {
-            float *o = static_cast<float *>(p.out) + slot * p.out_stride + f;
-            if (p.out_wide && cols >= 8) {
-                reinterpret_cast<float4 *>(o)[0] = make_float4(y[0], y[1], y[2], y[3]);
-                reinterpret_cast<float4 *>(o)[1] = make_float4(y[4], y[5], y[6], y[7]);
-            } else {
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    if (i < cols) o[i] = y[i];
-            }
-        } else {
-            uint16_t *o = static_cast<uint16_t *>(p.out) + slot * p.out_stride + f;
-            uint32_t u[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if constexpr (OUT == kOutBf16) {
-                    const __nv_bfloat162 h = __floats2bfloat162_rn(y[2 * i], y[2 * i + 1]);
-                    memcpy(&u[i], &h, 4);
-                } else {
-                    const __half2 h = __floats2half2_rn(y[2 * i], y[2 * i + 1]);
-                    memcpy(&u[i], &h, 4);
-                }
-            }
-            if (p.out_wide && cols >= 8) {
-                *reinterpret_cast<uint4 *>(o) = make_uint4(u[0], u[1], u[2], u[3]);
-            } else {
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    if (i < cols) o[i] = (uint16_t)(u[i >> 1] >> (16 * (i & 1)));
-            }
-        }
-    }
 }
 
 // Position in the ring of stages, and the parity of its round.
@@ -281,7 +279,7 @@ __global__ void __launch_bounds__(kMmThreads, 1)
 expert_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ MmParams p) {
     extern __shared__ __align__(1024) uint8_t dyn[];
     __shared__ Shared sh;
-    __shared__ __align__(16) float turn[kEpiWarps][16 * kTurnStride];
+    __shared__ __align__(16) float turn[kEpiWarps][2 * 8 * kTurnStride];
     constexpr int AT = GATED ? 2 : 1;                     // 128-row weight tiles per tile
     constexpr bool kNv = KIND == CSF_ROWS_NVFP4;
     constexpr int kStepK = kNv ? 256 : 128;               // elements per stage: 128 bytes of codes a row
@@ -541,9 +539,9 @@ expert_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_cons
         }
     } else if (warp < 4 + kEpiWarps) {
         // ---- epilogue ----
-        // Warps w and w + 4 read the same 32 rows and take every other 16
-        // slots.  What a piece reads from memory is fetched one piece ahead,
-        // across tiles.
+        // Warps w and w + 4 read the same 32 weight rows and take every other
+        // 8 slots.  One rolled loop: longer code ran out of the instruction
+        // cache.
         const int w = (warp - 4) & 3, half = (warp - 4) >> 2;
         const int part = lane & 3, sub = lane >> 2;           // after the turn: 8 columns of a slot
         float *buf = turn[warp - 4];
@@ -551,77 +549,56 @@ expert_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_cons
         if constexpr (OUT == kOutNv) {
             if (p.out_tensor_scale) tensor_scale = *p.out_tensor_scale;
         }
-        struct Piece {
-            int64_t slot;
-            int n, c, f;          // slots of the tile, first slot of the piece, this lane's first column
-            float alpha, rs[2];
-            uint32_t bias[AT];    // as stored
-            Raw8 res[2];
-        };
-        auto fetch = [&](Piece &q) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int j = q.c + 8 * i + sub;
-                const bool live = j < q.n;
-                q.rs[i] = p.row_scale && live ? p.row_scale[q.slot + j] : 1.f;
-                if (p.residual)
-                    q.res[i] = load_raw8(p.residual, (q.slot + j) * p.residual_stride + q.f, p.residual_dtype, live ? p.F - q.f : 0,
-                                         p.residual_wide);
-            }
-        };
-        auto open = [&](Piece &q, uint32_t tile) {
+        constexpr int kOutBytes = OUT == kOutF32 ? 4 : OUT == kOutBf16 || OUT == kOutF16 ? 2 : 1;
+        const int res_bytes = p.residual_dtype == CSF_F32 ? 4 : 2;
+        const int64_t out_step = 16 * p.out_stride * kOutBytes, res_step = 16 * p.residual_stride * res_bytes;
+        uint32_t nth = 0, buf_set = 0;
+        for (uint32_t tile = blockIdx.x; tile < total; tile += gridDim.x, ++nth) {
             const Tile t = find_tile(p, first, slot0, tile, lane);
-            const int row = t.rt * 128 + 32 * w;
-            q.slot = t.slot;
-            q.n = t.n;
-            q.c = 16 * half;
-            q.f = row + 8 * part;
-            q.alpha = p.alpha ? p.alpha[t.e] : 1.f;
+            const uint32_t set = nth & 1u, aph = (nth >> 1) & 1u;
+            const int row = t.rt * 128 + 32 * w, f = row + 8 * part;
+            const int64_t slot = t.slot + 8 * half + sub;     // this lane's next slot
+            const char *res_at = static_cast<const char *>(p.residual) + (slot * p.residual_stride + f) * res_bytes;
+            const float *scale_at = p.row_scale + slot;
+            char *out_at = static_cast<char *>(p.out) + slot * p.out_stride * kOutBytes + (OUT == kOutNv || OUT == kOutMx ? 0 : f * kOutBytes);
+            uint8_t *srow = p.out_scales + slot * p.out_scale_stride;
+            int c = 8 * half;
+            Raw8 res = {};
+            float rs = 1.f;
+            if (p.residual && c + sub < t.n) res = load_raw8(res_at, p.residual_dtype, p.F - f, p.residual_wide);
+            if (p.row_scale && c + sub < t.n) rs = *scale_at;
+            const float alpha = p.alpha ? p.alpha[t.e] : 1.f;
+            uint32_t raw_bias[AT];
 #pragma unroll
             for (int a = 0; a < AT; ++a) {
                 const int r = row + lane + a * p.second;
-                q.bias[a] = p.bias && r < p.N ? load_raw(p.bias, (int64_t)t.e * p.N + r, p.bias_dtype) : 0u;
+                raw_bias[a] = p.bias && r < p.N ? load_raw(p.bias, (int64_t)t.e * p.N + r, p.bias_dtype) : 0u;
             }
-            fetch(q);
-        };
-        uint32_t tile = blockIdx.x, nth = 0;
-        Piece cur;
-        if (tile < total) open(cur, tile);
-        while (tile < total) {
-            const uint32_t set = nth & 1u, aph = (nth >> 1) & 1u;
-            const bool opening = cur.c == 16 * half, closing = cur.c + 32 >= cur.n;
-            Piece next = cur;
-            const uint32_t next_tile = closing ? tile + gridDim.x : tile;
-            if (!closing) {
-                next.c += 32;
-                fetch(next);
-            } else if (next_tile < total) {
-                open(next, next_tile);
-            }
-            if (opening) {
-                const bool ok = tc::bar_wait(accf0 + 8 * set, aph, abort);
-                if (!__all_sync(0xFFFFFFFFu, ok)) break;
-                tc::fence_after();
-            }
-            if (cur.c < cur.n) {
-                const uint32_t d = tmem + set * (AT * kAccCols) + ((uint32_t)(32 * w) << 16) + cur.c;
-                float acc[AT][16];
+            const bool ok = tc::bar_wait(accf0 + 8 * set, aph, abort);
+            if (!__all_sync(0xFFFFFFFFu, ok)) break;
+            tc::fence_after();
+            float bias[AT];
 #pragma unroll
-                for (int a = 0; a < AT; ++a) tc::tmem_load16(d + a * kAccCols, acc[a]);
+            for (int a = 0; a < AT; ++a) bias[a] = raw_as_float(raw_bias[a], p.bias_dtype);
+            uint32_t d = tmem + set * (AT * kAccCols) + ((uint32_t)(32 * w) << 16) + c;
+            if (c >= t.n) tc::bar_arrive(acce0 + 8 * set);     // no slots of this tile are this warp's
+#pragma unroll 1
+            for (; c < t.n; c += 16, d += 16, buf_set ^= 8 * kTurnStride) {
+                float acc[AT][8];
+#pragma unroll
+                for (int a = 0; a < AT; ++a) tc::tmem_load8(d + a * kAccCols, acc[a]);
                 tc::wait_ld();
-                if (closing) {
+                if (c + 16 >= t.n) {
                     tc::fence_before();
                     tc::bar_arrive(acce0 + 8 * set);
                 }
-                float bias[AT];
-#pragma unroll
-                for (int a = 0; a < AT; ++a) bias[a] = raw_as_float(cur.bias[a], p.bias_dtype);
+                float *to = buf + buf_set;      // two buffers: one barrier a round
                 auto turn_in = [&](auto act) {
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        float y = activate<decltype(act)::value>(fmaf(acc[0][j], cur.alpha, bias[0]));
-                        if constexpr (GATED) y *= fmaf(acc[AT - 1][j], cur.alpha, bias[AT - 1]);
-                        buf[j * kTurnStride + lane] = y;
+                    for (int j = 0; j < 8; ++j) {
+                        float y = activate<decltype(act)::value>(fmaf(acc[0][j], alpha, bias[0]));
+                        if constexpr (GATED) y *= fmaf(acc[AT - 1][j], alpha, bias[AT - 1]);
+                        to[j * kTurnStride + lane] = y;
                     }
                 };
                 switch (p.act) {
@@ -631,24 +608,25 @@ expert_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_cons
                     default: turn_in(std::integral_constant<int, CSF_ACT_NONE>{}); break;
                 }
                 __syncwarp();
+                const float4 lo = *reinterpret_cast<const float4 *>(to + sub * kTurnStride + 8 * part);
+                const float4 hi = *reinterpret_cast<const float4 *>(to + sub * kTurnStride + 8 * part + 4);
+                float y[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+                const bool live = c + sub < t.n, more = c + 16 + sub < t.n;
+                if (p.row_scale) {
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int j = 8 * i + sub;
-                    const float4 lo = *reinterpret_cast<const float4 *>(buf + j * kTurnStride + 8 * part);
-                    const float4 hi = *reinterpret_cast<const float4 *>(buf + j * kTurnStride + 8 * part + 4);
-                    float y[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-#pragma unroll
-                    for (int q = 0; q < 8; ++q) y[q] *= cur.rs[i];
-                    if (p.residual) add_raw8(y, cur.res[i], p.residual_dtype);
-                    emit8<OUT>(p, y, cur.f, cur.slot + cur.c + j, cur.c + j < cur.n, tensor_scale);
+                    for (int q = 0; q < 8; ++q) y[q] *= rs;
+                    scale_at += 16;
+                    if (more) rs = *scale_at;
                 }
-                __syncwarp();
-            } else {
-                tc::bar_arrive(acce0 + 8 * set);     // no piece of this tile is this warp's
+                if (p.residual) {
+                    add_raw8(y, res, p.residual_dtype);
+                    res_at += res_step;
+                    if (more) res = load_raw8(res_at, p.residual_dtype, p.F - f, p.residual_wide);
+                }
+                emit8<OUT>(p, y, f, out_at, srow, live, tensor_scale);
+                out_at += out_step;
+                srow += 16 * p.out_scale_stride;
             }
-            cur = next;
-            tile = next_tile;
-            nth += closing;
         }
     }
 
