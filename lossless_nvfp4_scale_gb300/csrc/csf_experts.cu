@@ -440,6 +440,14 @@ expert_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_cons
                         if (32 * j < t.n && u + h < units) next[j][h] = __ldg(src[j] + u + h);
             };
             load(0);
+            if (p.residual) {      // what the epilogue will add, into L2: 32 bytes a lane
+                const int bytes = p.residual_dtype == CSF_F32 ? 4 : 2;
+                const int sectors = 128 * bytes / 32, per = 32 / sectors, sec = lane % sectors;
+                const int f = t.rt * 128 + sec * (32 / bytes);
+                const char *at = static_cast<const char *>(p.residual) + ((t.slot + lane / sectors) * p.residual_stride + f) * bytes;
+                for (int r = lane / sectors; r < t.n; r += per, at += per * p.residual_stride * bytes)
+                    if (f < p.F) tc::prefetch_l2(at);
+            }
             int k = 0;
             for (int u = 0; ok && u < units; u += 2) {
                 uint4 now[kRows][2];

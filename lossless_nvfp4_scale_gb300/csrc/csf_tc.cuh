@@ -89,6 +89,8 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void *map, int x
         : "memory");
 }
 
+__device__ __forceinline__ void prefetch_l2(const void *p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+
 __device__ __forceinline__ void store_shared(uint32_t dst, uint32_t v) {
     asm volatile("st.shared.u32 [%0], %1;" ::"r"(dst), "r"(v) : "memory");
 }
