@@ -75,6 +75,7 @@ struct MmParams {
     int32_t E, N, K, F;          // F: output columns (N, or N / 2 gated)
     int32_t ncb;                 // scale tiles per 128-row block of a weight stack
     int32_t row_tiles;           // row tiles per expert
+    uint32_t row_tiles_magic;    // 2^32 / row_tiles, rounded up
     int32_t second;              // weight rows from a tile's first 128 rows to its second
     int32_t nt;                  // most slots per tile (a multiple of 16)
     int32_t stages;
@@ -105,28 +106,30 @@ struct Tile {
     int64_t slot;     // first slot
 };
 
-// The tile with this number: the last expert whose first tile is not past
-// it, found 32 candidates at a time; then its slot tile and row tile (row
-// tiles of one slot tile are neighbours, so their x rows are shared in L2).
+// The tile with this number.  Row tiles of one slot tile are neighbours, so
+// their x rows are shared in L2.  Its expert is the last whose first slot tile
+// is not past the tile's, found 32 candidates at a time.
 __device__ __forceinline__ Tile find_tile(const MmParams &p, const uint32_t *first, const uint32_t *slot0, uint32_t tile, int lane) {
+    const uint32_t rt = (uint32_t)p.row_tiles;
+    uint32_t st = rt == 1 ? tile : __umulhi(tile, p.row_tiles_magic);      // tile / row tiles, or one more
+    int row_tile = (int)(tile - st * rt);
+    if (row_tile < 0) --st, row_tile += (int)rt;
     int lo = 0, len = p.E;
     while (len > 1) {
         const int step = (len + 31) >> 5;
         const int i = lo + lane * step;
-        const uint32_t m = __ballot_sync(0xFFFFFFFFu, i < lo + len && first[i] <= tile);
-        const int last = 31 - __clz(m);
-        const int at = lo + last * step;
+        const uint32_t m = __ballot_sync(0xFFFFFFFFu, i < lo + len && first[i] <= st);
+        const int at = lo + (31 - __clz(m)) * step;
         len = min(step, lo + len - at);
         lo = at;
     }
     Tile t;
     t.e = lo;
-    const uint32_t local = tile - first[lo];
-    const uint32_t rt = (uint32_t)p.row_tiles, parts = (first[lo + 1] - first[lo]) / rt;
-    const uint32_t part = local / rt;
-    t.rt = (int)(local - part * rt);
+    t.rt = row_tile;
+    const uint32_t part = st - first[lo], parts = first[lo + 1] - first[lo];
     const uint32_t s = slot0[lo], cnt = slot0[lo + 1] - s;
-    const uint32_t per = ((cnt + parts - 1) / parts + 15u) & ~15u;   // an expert's slot tiles are alike
+    // an expert's slot tiles are alike
+    const uint32_t per = parts == 1 ? cnt : ((cnt + parts - 1) / parts + 15u) & ~15u;
     t.slot = s + part * per;
     t.n = (int)min(per, cnt - part * per);
     return t;
@@ -317,7 +320,7 @@ expert_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_cons
     }
     if (warp == 1) tc::tmem_alloc(tc::smem_u32(&sh.tmem), kTmemCols);
 
-    // first[e]: number of the first tile of expert e.
+    // first[e]: number of the first slot tile of expert e.
     uint32_t running = 0;
     bool bad = false;
     for (int e0 = 0; e0 < p.E; e0 += kMmThreads) {
@@ -326,7 +329,7 @@ expert_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_cons
         if (e < p.E) {
             const int64_t a = start_at(p, e), b = start_at(p, e + 1);
             slot0[e] = (uint32_t)a;
-            if (b > a) tiles = (uint32_t)((b - a + p.nt - 1) / p.nt) * (uint32_t)p.row_tiles;
+            if (b > a) tiles = (uint32_t)((b - a + p.nt - 1) / p.nt);
             if (p.start) {
                 const long long raw = p.es64 ? static_cast<const long long *>(p.start)[e + 1] : static_cast<const int *>(p.start)[e + 1];
                 bad |= raw != b || b < a;
@@ -354,7 +357,7 @@ expert_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_cons
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
-    const uint32_t total = first[p.E];
+    const uint32_t total = first[p.E] * (uint32_t)p.row_tiles;
     const uint32_t tmem = sh.tmem;
     volatile uint32_t *abort = &sh.abort;
     const int ksteps = (p.K + kStepK - 1) / kStepK;
@@ -560,34 +563,52 @@ expert_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_cons
         constexpr int kOutBytes = OUT == kOutF32 ? 4 : OUT == kOutBf16 || OUT == kOutF16 ? 2 : 1;
         const int res_bytes = p.residual_dtype == CSF_F32 ? 4 : 2;
         const int64_t out_step = 16 * p.out_stride * kOutBytes, res_step = 16 * p.residual_stride * res_bytes;
+        // What a tile needs before its first round, fetched a tile ahead.
+        struct Head {
+            Tile t;
+            Raw8 res;
+            float alpha, rs;
+            uint32_t bias[AT];      // as stored
+        };
+        auto open = [&](Head &h, uint32_t tile) {
+            h.t = find_tile(p, first, slot0, tile, lane);
+            const int row = h.t.rt * 128 + 32 * w, f = row + 8 * part, c = 8 * half + sub;
+            if (p.residual && c < h.t.n)
+                h.res = load_raw8(static_cast<const char *>(p.residual) + ((h.t.slot + c) * p.residual_stride + f) * res_bytes,
+                                  p.residual_dtype, p.F - f, p.residual_wide);
+            if (p.row_scale && c < h.t.n) h.rs = p.row_scale[h.t.slot + c];
+            if (p.alpha) h.alpha = p.alpha[h.t.e];
+#pragma unroll
+            for (int a = 0; a < AT; ++a) {
+                const int r = row + lane + a * p.second;
+                if (p.bias && r < p.N) h.bias[a] = load_raw(p.bias, (int64_t)h.t.e * p.N + r, p.bias_dtype);
+            }
+        };
         uint32_t nth = 0, buf_set = 0;
+        Head next = {};
+        next.alpha = 1.f;
+        next.rs = 1.f;
+        if (blockIdx.x < total) open(next, blockIdx.x);
         for (uint32_t tile = blockIdx.x; tile < total; tile += gridDim.x, ++nth) {
-            const Tile t = find_tile(p, first, slot0, tile, lane);
+            const Tile t = next.t;
             const uint32_t set = nth & 1u, aph = (nth >> 1) & 1u;
-            const int row = t.rt * 128 + 32 * w, f = row + 8 * part;
+            const int f = t.rt * 128 + 32 * w + 8 * part;
             const int64_t slot = t.slot + 8 * half + sub;     // this lane's next slot
             const char *res_at = static_cast<const char *>(p.residual) + (slot * p.residual_stride + f) * res_bytes;
             const float *scale_at = p.row_scale + slot;
             char *out_at = static_cast<char *>(p.out) + slot * p.out_stride * kOutBytes + (OUT == kOutNv || OUT == kOutMx ? 0 : f * kOutBytes);
             uint8_t *srow = p.out_scales + slot * p.out_scale_stride;
             int c = 8 * half;
-            Raw8 res = {};
-            float rs = 1.f;
-            if (p.residual && c + sub < t.n) res = load_raw8(res_at, p.residual_dtype, p.F - f, p.residual_wide);
-            if (p.row_scale && c + sub < t.n) rs = *scale_at;
-            const float alpha = p.alpha ? p.alpha[t.e] : 1.f;
-            uint32_t raw_bias[AT];
+            Raw8 res = next.res;
+            float rs = next.rs;
+            const float alpha = next.alpha;
+            float bias[AT];
 #pragma unroll
-            for (int a = 0; a < AT; ++a) {
-                const int r = row + lane + a * p.second;
-                raw_bias[a] = p.bias && r < p.N ? load_raw(p.bias, (int64_t)t.e * p.N + r, p.bias_dtype) : 0u;
-            }
+            for (int a = 0; a < AT; ++a) bias[a] = raw_as_float(next.bias[a], p.bias_dtype);
+            if (tile + gridDim.x < total) open(next, tile + gridDim.x);
             const bool ok = tc::bar_wait(accf0 + 8 * set, aph, abort);
             if (!__all_sync(0xFFFFFFFFu, ok)) break;
             tc::fence_after();
-            float bias[AT];
-#pragma unroll
-            for (int a = 0; a < AT; ++a) bias[a] = raw_as_float(raw_bias[a], p.bias_dtype);
             uint32_t d = tmem + set * (AT * kAccCols) + ((uint32_t)(32 * w) << 16) + c;
             if (c >= t.n) tc::bar_arrive(acce0 + 8 * set);     // no slots of this tile are this warp's
 #pragma unroll 1
@@ -786,6 +807,7 @@ extern "C" csf_status csf_expert_matmul(const csf_expert_matmul_args *a, void *s
     }
     p.second = a->gated ? N / 2 : 128;
     p.row_tiles = a->gated ? N / 256 : (N + 127) / 128;
+    p.row_tiles_magic = (uint32_t)((1ull << 32) / (uint32_t)p.row_tiles + 1);
     const int most = at == 1 ? 128 : 96;
     p.nt = (int)std::min<int64_t>(most, round_up(a->slots, 16));
     const uint32_t sf = nv ? 2048u : 512u;
