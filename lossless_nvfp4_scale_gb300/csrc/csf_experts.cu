@@ -14,7 +14,8 @@
 //   warps 2, 3, 12, 13  x rows gathered through the slot index: 16-byte
 //            asynchronous copies, swizzled as TMA would
 //   warp 14  the scale bytes of those rows, through registers into the tile
-//            layout, 32 bytes of a row at a time
+//            layout
+//   warp 15  which tile comes next and which x rows it takes, a few tiles ahead
 //   warp 1   scale copies to tensor memory and the matrix instructions
 //   warps 4-11  epilogue
 // Their inner loops run alone on a scheduler, a few cycles an instruction, so
@@ -42,7 +43,7 @@
 namespace csfk {
 namespace {
 
-constexpr int kMmThreads = 480;
+constexpr int kMmThreads = 512;
 constexpr int kEpiWarps = 8;
 constexpr int kXWarps = 4;
 constexpr int kTurnStride = 36;      // floats between slots of a warp's 8 x 32 piece: reads and writes without bank conflicts
@@ -103,7 +104,7 @@ __device__ __forceinline__ int64_t start_at(const MmParams &p, int e) {
 
 struct Tile {
     int e, n, rt;     // expert, slots, row tile
-    int64_t slot;     // first slot
+    uint32_t slot;    // first slot
 };
 
 // The tile with this number.  Row tiles of one slot tile are neighbours, so
@@ -254,15 +255,6 @@ __device__ __forceinline__ void emit8(const MmParams &p, float (&y)[8], int f, c
     }
 }
 
-// The x row of a tile's column c; columns past its slots repeat the last one.
-__device__ __forceinline__ int64_t x_row(const MmParams &p, const Tile &t, int c, bool &bad) {
-    const int64_t s = t.slot + min(c, t.n - 1);
-    const int64_t v = p.rows ? (int64_t)p.rows[s] : s;
-    const int64_t r = v < 0 || v >= p.x_rows ? 0 : v;
-    bad |= r != v;
-    return r;
-}
-
 // Position in the ring of stages, and the parity of its round.
 struct Ring {
     uint32_t s = 0, parity = 0;
@@ -271,9 +263,15 @@ struct Ring {
     }
 };
 
+constexpr int kTileRing = 4;         // tiles that the roles may be apart
+constexpr int kMaxTileSlots = 224;
+constexpr int kTileUsers = 3 + kXWarps + kEpiWarps;
+
 struct Shared {
-    uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2];
-    uint32_t tmem, abort, total, warp_sum[kMmThreads / 32];
+    uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2], tile_full[kTileRing], tile_empty[kTileRing];
+    Tile tile[kTileRing];                        // n = 0: no more
+    int32_t x_row[kTileRing][kMaxTileSlots];
+    uint32_t tmem, abort, warp_sum[kMmThreads / 32];
 };
 
 // KIND: csf_rows_kind of x.  GATED: a tile has 128 gate rows and their up rows.
@@ -289,11 +287,12 @@ expert_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_cons
     constexpr int kTilesPerStage = kNv ? 4 : 1;           // 128 x 4 scale tiles per stage and 128 rows
     constexpr uint32_t kABytes = 128 * 128;
     constexpr uint32_t kACopied = kNv ? kABytes : kABytes / 2;   // E2M1 codes unpack on the way: counted as stored
-    constexpr int kAccCols = AT == 1 ? 128 : 96;          // accumulator columns (most slots per tile)
+    constexpr int kAccCols = AT == 1 ? kMaxTileSlots : 96;   // accumulator columns (most slots per tile)
+    constexpr int kRowBlocks = (kAccCols + 127) / 128;    // 128-row blocks of x scales
     constexpr uint32_t kSfCols = 4 * kTilesPerStage;      // tensor-memory columns of one operand's scales
-    constexpr uint32_t kSfSet = (AT + 1) * kSfCols;
     constexpr uint32_t kSfBase = 2 * AT * kAccCols;
-    static_assert(kSfBase + 2 * kSfSet <= kTmemCols, "tensor memory");
+    constexpr uint32_t kSfA = kSfBase + kRowBlocks * kSfCols;
+    static_assert(kSfA + AT * kSfCols <= kTmemCols, "tensor memory");
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t ring0 = (tc::smem_u32(dyn) + 1023u) & ~1023u;
@@ -305,6 +304,7 @@ expert_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_cons
                    sfb_off = sfa_off + AT * kTilesPerStage * 512u;
     const uint32_t full0 = tc::smem_u32(sh.full), empty0 = tc::smem_u32(sh.empty);
     const uint32_t accf0 = tc::smem_u32(sh.acc_full), acce0 = tc::smem_u32(sh.acc_empty);
+    const uint32_t tilef0 = tc::smem_u32(sh.tile_full), tilee0 = tc::smem_u32(sh.tile_empty);
 
     if (tid == 0) {
         for (int i = 0; i < p.stages; ++i) {
@@ -314,6 +314,10 @@ expert_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_cons
         for (int i = 0; i < 2; ++i) {
             tc::bar_init(accf0 + 8 * i, 1);
             tc::bar_init(acce0 + 8 * i, 32 * kEpiWarps);
+        }
+        for (int i = 0; i < kTileRing; ++i) {
+            tc::bar_init(tilef0 + 8 * i, 1);
+            tc::bar_init(tilee0 + 8 * i, kTileUsers);
         }
         sh.abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -362,19 +366,55 @@ expert_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_cons
     volatile uint32_t *abort = &sh.abort;
     const int ksteps = (p.K + kStepK - 1) / kStepK;
 
-    if (warp == 0) {
+    // Roles that take tiles: wait for the next one's description; done with
+    // it, one lane of each says so.
+    auto take = [&](const Ring &r, Tile &t) {
+        if (!tc::bar_wait(tilef0 + 8 * r.s, r.parity, abort)) return false;
+        t = sh.tile[r.s];
+        return t.n > 0;
+    };
+    auto done_with = [&](Ring &r) {
+        tc::bar_arrive(tilee0 + 8 * r.s);
+        r.next(kTileRing);
+    };
+
+    if (warp == 15) {
+        // ---- tiles and their x rows ----
+        Ring tr;
+        bool bad_row = false;
+        for (uint32_t tile = blockIdx.x;; tile += gridDim.x) {
+            Tile t = {};
+            if (tile < total) t = find_tile(p, first, slot0, tile, lane);
+            if (!__all_sync(0xFFFFFFFFu, tc::bar_wait(tilee0 + 8 * tr.s, tr.parity ^ 1u, abort))) break;
+            // columns past the tile's slots repeat its last row
+            for (int c = lane; c < ((t.n + 15) & ~15); c += 32) {
+                const int64_t s = (int64_t)t.slot + min(c, t.n - 1);
+                const int64_t v = p.rows ? (int64_t)p.rows[s] : s;
+                const int32_t r = v < 0 || v >= p.x_rows ? 0 : (int32_t)v;
+                bad_row |= r != v;
+                sh.x_row[tr.s][c] = r;
+            }
+            if (lane == 0) sh.tile[tr.s] = t;
+            __syncwarp();
+            if (lane == 0) tc::bar_arrive(tilef0 + 8 * tr.s);
+            tr.next(kTileRing);
+            if (tile >= total) break;
+        }
+        if (bad_row && p.err) atomicOr(p.err, CSF_DEV_ERR_CORRUPT);
+    } else if (warp == 0) {
         // ---- weights and their scales ----
-        Ring ring;
-        bool ok = true;
-        for (uint32_t tile = blockIdx.x; ok && tile < total; tile += gridDim.x) {
-            const Tile t = find_tile(p, first, slot0, tile, lane);
-            const int row = t.rt * 128;
-            const uint8_t *sf = p.w_scales + (int64_t)t.e * p.w_scale_expert + (int64_t)t.rt * p.ncb * 512;
-            int left = p.ncb;
-            for (int k = 0; k < ksteps; ++k, left -= kTilesPerStage, sf += kTilesPerStage * 512, ring.next(p.stages)) {
-                ok = __all_sync(0xFFFFFFFFu, tc::bar_wait(empty0 + 8 * ring.s, ring.parity ^ 1u, abort));
-                if (!ok) break;
-                if (tc::elect_one()) {
+        if (tc::elect_one()) {
+            Ring ring, tr;
+            Tile t;
+            bool ok = true;
+            while (ok && take(tr, t)) {
+                done_with(tr);
+                const int row = t.rt * 128;
+                const uint8_t *sf = p.w_scales + (int64_t)t.e * p.w_scale_expert + (int64_t)t.rt * p.ncb * 512;
+                int left = p.ncb;
+                for (int k = 0; k < ksteps; ++k, left -= kTilesPerStage, sf += kTilesPerStage * 512, ring.next(p.stages)) {
+                    ok = tc::bar_wait(empty0 + 8 * ring.s, ring.parity ^ 1u, abort);
+                    if (!ok) break;
                     const uint32_t base = ring0 + ring.s * p.stage_bytes, bar = full0 + 8 * ring.s;
                     const uint32_t bytes = (uint32_t)min(kTilesPerStage, left) * 512u;
                     tc::bar_expect(bar, (uint32_t)AT * (kACopied + bytes));
@@ -384,26 +424,29 @@ expert_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_cons
                         tc::bulk_load(base + sfa_off + a * kTilesPerStage * 512u, sf + (int64_t)a * (p.second >> 7) * p.ncb * 512, bytes, bar);
                     }
                 }
-                __syncwarp();
             }
         }
-    } else if (warp == 2 || warp == 3 || (warp >= 4 + kEpiWarps && warp < 4 + kEpiWarps + kXWarps - 2)) {
+        __syncwarp();
+    } else if (warp == 2 || warp == 3 || warp == 12 || warp == 13) {
         // ---- x rows ----
-        const int xw = warp < 4 ? warp - 2 : warp - (2 + kEpiWarps);
+        const int xw = warp < 4 ? warp - 2 : warp - 10;
         const int piece = lane & 7, sub = lane >> 3;      // 8 lanes a row, 4 rows a copy; every fourth group of 4 rows
         const int code_bytes = kNv ? p.K / 2 : p.K;
         const uint32_t r8 = (uint32_t)(4 * (xw & 1) + sub);   // row mod 8
         // row r's 16-byte piece q lies at piece q ^ (r % 8) of its 128 bytes
         const uint32_t b_dst = b_off + (uint32_t)(4 * xw + sub) * 128u + (((uint32_t)piece ^ r8) << 4);
         constexpr int kCopies = kAccCols / 16;
-        Ring ring;
-        bool ok = true, bad_row = false;
-        for (uint32_t tile = blockIdx.x; ok && tile < total; tile += gridDim.x) {
-            const Tile t = find_tile(p, first, slot0, tile, lane);
+        Ring ring, tr;
+        Tile t;
+        bool ok = true;
+        while (ok && __all_sync(0xFFFFFFFFu, take(tr, t))) {
             const uint8_t *src[kCopies];
 #pragma unroll
             for (int j = 0; j < kCopies; ++j)
-                src[j] = p.x_codes + (16 * j < t.n ? x_row(p, t, 16 * j + 4 * xw + sub, bad_row) * p.x_code_stride : 0) + 16 * piece;
+                src[j] = p.x_codes + (16 * j < t.n ? sh.x_row[tr.s][16 * j + 4 * xw + sub] * p.x_code_stride : 0) + 16 * piece;
+            __syncwarp();
+            if (lane == 0) tc::bar_arrive(tilee0 + 8 * tr.s);
+            tr.next(kTileRing);
             const int copies = (t.n + 15) >> 4;
             int at = 16 * piece;
             for (int k = 0; k < ksteps; ++k, at += 128, ring.next(p.stages)) {
@@ -419,123 +462,135 @@ expert_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_cons
                 tc::cp_async_arrive(full0 + 8 * ring.s);
             }
         }
-        if (bad_row && p.err) atomicOr(p.err, CSF_DEV_ERR_CORRUPT);
-    } else if (warp == 4 + kEpiWarps + kXWarps - 2) {
+    } else if (warp == 14) {
         // ---- scales of the x rows ----
         // Row lane + 32 j; 16 bytes are four scale tiles: a stage (NVFP4) or
-        // four (MXFP8).  The next 32 bytes are under way while these leave.
-        constexpr int kRows = kAccCols / 32, kStagesPer16 = 4 / kTilesPerStage;
+        // four (MXFP8).  The next 16, of the next tile where this one ends,
+        // are under way while these leave.
+        constexpr int kRows = (kAccCols + 31) / 32, kStagesPer16 = 4 / kTilesPerStage;
         const int units = (p.ncb + 3) / 4;
-        Ring ring;
-        bool ok = true, bad_row = false;
-        for (uint32_t tile = blockIdx.x; ok && tile < total; tile += gridDim.x) {
-            const Tile t = find_tile(p, first, slot0, tile, lane);
-            const uint4 *src[kRows];
-            uint4 next[kRows][2];
+        Ring ring, tr;
+        Tile t;
+        const uint4 *src[kRows];
+        uint4 next[kRows];
+        auto load = [&](int u) {
 #pragma unroll
             for (int j = 0; j < kRows; ++j)
-                src[j] = reinterpret_cast<const uint4 *>(p.x_scales + (32 * j < t.n ? x_row(p, t, 32 * j + lane, bad_row) * p.x_scale_stride : 0));
-            auto load = [&](int u) {
+                if (32 * j < t.n) next[j] = __ldg(src[j] + u);
+        };
+        auto open = [&]() {
+            if (!__all_sync(0xFFFFFFFFu, take(tr, t))) return false;
 #pragma unroll
-                for (int j = 0; j < kRows; ++j)
-#pragma unroll
-                    for (int h = 0; h < 2; ++h)
-                        if (32 * j < t.n && u + h < units) next[j][h] = __ldg(src[j] + u + h);
-            };
+            for (int j = 0; j < kRows; ++j) {
+                const int c = 32 * j + lane;
+                src[j] = reinterpret_cast<const uint4 *>(p.x_scales + (c < t.n ? sh.x_row[tr.s][c] * p.x_scale_stride : 0));
+            }
+            __syncwarp();
+            if (lane == 0) tc::bar_arrive(tilee0 + 8 * tr.s);
+            tr.next(kTileRing);
             load(0);
             if (p.residual) {      // what the epilogue will add, into L2: 32 bytes a lane
                 const int bytes = p.residual_dtype == CSF_F32 ? 4 : 2;
                 const int sectors = 128 * bytes / 32, per = 32 / sectors, sec = lane % sectors;
                 const int f = t.rt * 128 + sec * (32 / bytes);
-                const char *at = static_cast<const char *>(p.residual) + ((t.slot + lane / sectors) * p.residual_stride + f) * bytes;
+                const char *at = static_cast<const char *>(p.residual) + ((t.slot + (int64_t)(lane / sectors)) * p.residual_stride + f) * bytes;
                 for (int r = lane / sectors; r < t.n; r += per, at += per * p.residual_stride * bytes)
                     if (f < p.F) tc::prefetch_l2(at);
             }
+            return true;
+        };
+        bool more = open();
+        while (more) {
+            const int n = t.n;
+            bool ok = true;
             int k = 0;
-            for (int u = 0; ok && u < units; u += 2) {
-                uint4 now[kRows][2];
+            for (int u = 0; ok && u < units; ++u) {
+                uint4 now[kRows];
 #pragma unroll
-                for (int j = 0; j < kRows; ++j) now[j][0] = next[j][0], now[j][1] = next[j][1];
-                load(u + 2);
+                for (int j = 0; j < kRows; ++j) now[j] = next[j];
+                if (u + 1 < units) load(u + 1);
+                else more = open();
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
+                for (int q = 0; q < kStagesPer16; ++q) {
+                    if (k >= ksteps) break;
+                    ok = __all_sync(0xFFFFFFFFu, tc::bar_wait(empty0 + 8 * ring.s, ring.parity ^ 1u, abort));
+                    if (!ok) break;
+                    const uint32_t dst = ring0 + ring.s * p.stage_bytes + sfb_off + lane * 16u;
 #pragma unroll
-                    for (int q = 0; q < kStagesPer16; ++q) {
-                        if (!ok || k >= ksteps) break;
-                        ok = __all_sync(0xFFFFFFFFu, tc::bar_wait(empty0 + 8 * ring.s, ring.parity ^ 1u, abort));
-                        if (!ok) break;
-                        const uint32_t dst = ring0 + ring.s * p.stage_bytes + sfb_off + lane * 16u;
-#pragma unroll
-                        for (int j = 0; j < kRows; ++j) {
-                            if (32 * j < t.n) {
-                                const uint4 v = now[j][h];
-                                if constexpr (kNv) {
-                                    tc::store_shared(dst + j * 4u, v.x);
-                                    tc::store_shared(dst + j * 4u + 512u, v.y);
-                                    tc::store_shared(dst + j * 4u + 1024u, v.z);
-                                    tc::store_shared(dst + j * 4u + 1536u, v.w);
-                                } else {
-                                    tc::store_shared(dst + j * 4u, q == 0 ? v.x : q == 1 ? v.y : q == 2 ? v.z : v.w);
-                                }
+                    for (int j = 0; j < kRows; ++j) {
+                        if (32 * j < n) {
+                            const uint4 v = now[j];
+                            const uint32_t to = dst + (j >> 2) * (kTilesPerStage * 512u) + (j & 3) * 4u;
+                            if constexpr (kNv) {
+                                tc::store_shared(to, v.x);
+                                tc::store_shared(to + 512u, v.y);
+                                tc::store_shared(to + 1024u, v.z);
+                                tc::store_shared(to + 1536u, v.w);
+                            } else {
+                                tc::store_shared(to, q == 0 ? v.x : q == 1 ? v.y : q == 2 ? v.z : v.w);
                             }
                         }
-                        tc::fence_async_proxy();
-                        __syncwarp();
-                        if (lane == 0) tc::bar_arrive(full0 + 8 * ring.s);
-                        ring.next(p.stages);
-                        ++k;
                     }
+                    tc::fence_async_proxy();
+                    __syncwarp();
+                    if (lane == 0) tc::bar_arrive(full0 + 8 * ring.s);
+                    ring.next(p.stages);
+                    ++k;
                 }
             }
+            more = more && ok;
         }
-        if (bad_row && p.err) atomicOr(p.err, CSF_DEV_ERR_CORRUPT);
     } else if (warp == 1) {
         // ---- matrix instructions ----
-        // Instruction descriptor: operand types, scale type, N / 8, M / 128.
-        const uint32_t idesc0 = kNv ? (1u << 7) | (1u << 10) | (1u << 27) : (5u << 7) | (0u << 10) | (1u << 23) | (1u << 27);
-        Ring ring;
-        uint32_t nth = 0, sf_set = 0;
-        bool ok = true;
-        for (uint32_t tile = blockIdx.x; ok && tile < total; tile += gridDim.x, ++nth) {
-            const Tile t = find_tile(p, first, slot0, tile, lane);
-            const uint32_t set = nth & 1u, aph = (nth >> 1) & 1u;
-            const uint32_t idesc = idesc0 | ((uint32_t)((t.n + 15) >> 4) << 18);
-            ok = __all_sync(0xFFFFFFFFu, tc::bar_wait(acce0 + 8 * set, aph ^ 1u, abort));
-            tc::fence_after();
-            const uint32_t d0 = tmem + set * (AT * kAccCols);
-            int left = p.ncb;
-            for (int k = 0; ok && k < ksteps; ++k, left -= kTilesPerStage, sf_set ^= 1u, ring.next(p.stages)) {
-                ok = __all_sync(0xFFFFFFFFu, tc::bar_wait(full0 + 8 * ring.s, ring.parity, abort));
-                if (!ok) break;
-                tc::fence_async_proxy();     // x came by ordinary copies
+        if (tc::elect_one()) {
+            // Instruction descriptor: operand types, scale type, N / 8, M / 128.
+            const uint32_t idesc0 = kNv ? (1u << 7) | (1u << 10) | (1u << 27) : (5u << 7) | (0u << 10) | (1u << 23) | (1u << 27);
+            Ring ring, tr;
+            Tile t;
+            uint32_t nth = 0;
+            bool ok = true;
+            const uint32_t sfb = tmem + kSfBase, sfa = tmem + kSfA;
+            while (ok && take(tr, t)) {
+                done_with(tr);
+                const uint32_t set = nth & 1u, aph = (nth >> 1) & 1u;
+                ++nth;
+                const uint32_t idesc = idesc0 | ((uint32_t)((t.n + 15) >> 4) << 18);
+                const bool wide = t.n > 128;
+                ok = tc::bar_wait(acce0 + 8 * set, aph ^ 1u, abort);
                 tc::fence_after();
-                if (tc::elect_one()) {
+                const uint32_t d0 = tmem + set * (AT * kAccCols);
+                int left = p.ncb;
+                for (int k = 0; ok && k < ksteps; ++k, left -= kTilesPerStage, ring.next(p.stages)) {
+                    ok = tc::bar_wait(full0 + 8 * ring.s, ring.parity, abort);
+                    if (!ok) break;
+                    tc::fence_async_proxy();     // x came by ordinary copies
                     const uint32_t base = ring0 + ring.s * p.stage_bytes;
-                    const uint32_t sf = tmem + kSfBase + sf_set * kSfSet;
                     const uint64_t sb = tc::desc_plain(base + sfb_off), sa = tc::desc_plain(base + sfa_off);
                     const uint64_t bd = tc::desc_sw128(base + b_off), ad = tc::desc_sw128(base);
                     auto issue = [&](int tiles) {
 #pragma unroll
                         for (int i = 0; i < kTilesPerStage; ++i) {
                             if (i < tiles) {
-                                tc::copy_scales(sf + 4 * i, sb + i * 32);
+                                // tensor-memory columns of an operand's scales: a k tile's 128-row blocks side by side
+                                tc::copy_scales(sfb + 4 * kRowBlocks * i, sb + i * 32);
+                                if (kRowBlocks > 1 && wide) tc::copy_scales(sfb + 4 * kRowBlocks * i + 4, sb + (kTilesPerStage + i) * 32);
 #pragma unroll
                                 for (int a = 0; a < AT; ++a)
-                                    tc::copy_scales(sf + (a + 1) * kSfCols + 4 * i, sa + (a * kTilesPerStage + i) * 32);
+                                    tc::copy_scales(sfa + a * kSfCols + 4 * i, sa + (a * kTilesPerStage + i) * 32);
                             }
                         }
 #pragma unroll
                         for (int a = 0; a < AT; ++a) {
-                            const uint32_t d = d0 + a * kAccCols, sfa = sf + (a + 1) * kSfCols;
+                            const uint32_t d = d0 + a * kAccCols;
 #pragma unroll
                             for (int i = 0; i < 4; ++i) {
                                 if constexpr (kNv) {
                                     if (i < tiles)
-                                        tc::mma_nvfp4(d, ad + a * (kABytes >> 4) + 2 * i, bd + 2 * i, idesc, sfa + 4 * i, sf + 4 * i,
-                                                      (k | i) != 0);
+                                        tc::mma_nvfp4(d, ad + a * (kABytes >> 4) + 2 * i, bd + 2 * i, idesc, sfa + a * kSfCols + 4 * i,
+                                                      sfb + 4 * kRowBlocks * i, (k | i) != 0);
                                 } else {
                                     tc::mma_mxf8(d, ad + a * (kABytes >> 4) + 2 * i, bd + 2 * i,
-                                                 idesc | ((uint32_t)i << 29) | ((uint32_t)i << 4), sfa, sf, (k | i) != 0);
+                                                 idesc | ((uint32_t)i << 29) | ((uint32_t)i << 4), sfa + a * kSfCols, sfb, (k | i) != 0);
                                 }
                             }
                         }
@@ -545,10 +600,10 @@ expert_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_cons
                     tc::commit(empty0 + 8 * ring.s);
                     if (k + 1 == ksteps) tc::commit(accf0 + 8 * set);
                 }
-                __syncwarp();
             }
         }
-    } else if (warp < 4 + kEpiWarps) {
+        __syncwarp();
+    } else {
         // ---- epilogue ----
         // Warps w and w + 4 read the same 32 weight rows and take every other
         // 8 slots.  One rolled loop: longer code ran out of the instruction
@@ -570,13 +625,20 @@ expert_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_cons
             float alpha, rs;
             uint32_t bias[AT];      // as stored
         };
-        auto open = [&](Head &h, uint32_t tile) {
-            h.t = find_tile(p, first, slot0, tile, lane);
+        Ring tr;
+        auto open = [&](Head &h) {
+            if (!__all_sync(0xFFFFFFFFu, take(tr, h.t))) {
+                h.t.n = 0;
+                return;
+            }
+            __syncwarp();
+            if (lane == 0) tc::bar_arrive(tilee0 + 8 * tr.s);
+            tr.next(kTileRing);
             const int row = h.t.rt * 128 + 32 * w, f = row + 8 * part, c = 8 * half + sub;
             if (p.residual && c < h.t.n)
-                h.res = load_raw8(static_cast<const char *>(p.residual) + ((h.t.slot + c) * p.residual_stride + f) * res_bytes,
+                h.res = load_raw8(static_cast<const char *>(p.residual) + (((int64_t)h.t.slot + c) * p.residual_stride + f) * res_bytes,
                                   p.residual_dtype, p.F - f, p.residual_wide);
-            if (p.row_scale && c < h.t.n) h.rs = p.row_scale[h.t.slot + c];
+            if (p.row_scale && c < h.t.n) h.rs = p.row_scale[(int64_t)h.t.slot + c];
             if (p.alpha) h.alpha = p.alpha[h.t.e];
 #pragma unroll
             for (int a = 0; a < AT; ++a) {
@@ -588,12 +650,12 @@ expert_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_cons
         Head next = {};
         next.alpha = 1.f;
         next.rs = 1.f;
-        if (blockIdx.x < total) open(next, blockIdx.x);
-        for (uint32_t tile = blockIdx.x; tile < total; tile += gridDim.x, ++nth) {
+        open(next);
+        for (; next.t.n > 0; ++nth) {
             const Tile t = next.t;
             const uint32_t set = nth & 1u, aph = (nth >> 1) & 1u;
             const int f = t.rt * 128 + 32 * w + 8 * part;
-            const int64_t slot = t.slot + 8 * half + sub;     // this lane's next slot
+            const int64_t slot = (int64_t)t.slot + 8 * half + sub;     // this lane's next slot
             const char *res_at = static_cast<const char *>(p.residual) + (slot * p.residual_stride + f) * res_bytes;
             const float *scale_at = p.row_scale + slot;
             char *out_at = static_cast<char *>(p.out) + slot * p.out_stride * kOutBytes + (OUT == kOutNv || OUT == kOutMx ? 0 : f * kOutBytes);
@@ -605,7 +667,7 @@ expert_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_cons
             float bias[AT];
 #pragma unroll
             for (int a = 0; a < AT; ++a) bias[a] = raw_as_float(next.bias[a], p.bias_dtype);
-            if (tile + gridDim.x < total) open(next, tile + gridDim.x);
+            open(next);
             const bool ok = tc::bar_wait(accf0 + 8 * set, aph, abort);
             if (!__all_sync(0xFFFFFFFFu, ok)) break;
             tc::fence_after();
@@ -808,10 +870,11 @@ extern "C" csf_status csf_expert_matmul(const csf_expert_matmul_args *a, void *s
     p.second = a->gated ? N / 2 : 128;
     p.row_tiles = a->gated ? N / 256 : (N + 127) / 128;
     p.row_tiles_magic = (uint32_t)((1ull << 32) / (uint32_t)p.row_tiles + 1);
-    const int most = at == 1 ? 128 : 96;
+    const int64_t mean = a->slots / std::min<int64_t>(E, a->slots);
+    const int most = a->gated ? 96 : mean > 96 ? kMaxTileSlots : 128;
     p.nt = (int)std::min<int64_t>(most, round_up(a->slots, 16));
     const uint32_t sf = nv ? 2048u : 512u;
-    p.stage_bytes = (uint32_t)round_up(at * 16384 + p.nt * 128 + (at + 1) * sf, 1024);
+    p.stage_bytes = (uint32_t)round_up(at * 16384 + p.nt * 128 + (at + (p.nt + 127) / 128) * sf, 1024);
     const int fixed = 1024 + 8 * (E + 1) + 16;
     const int room = kSmemLimit - (int)round_up(sizeof(Shared) + sizeof(float) * kEpiWarps * 16 * kTurnStride, 1024) - fixed;
     p.stages = std::min<int>(kMaxStages, room / (int)p.stage_bytes);
