@@ -11,8 +11,10 @@
 //
 // One persistent block per SM walks tiles (expert, slot tile, row tile):
 //   warp 0   weights (TMA, 128-byte swizzle) and their scale tiles
-//   warps 2, 3, 12, 13  x rows gathered through the slot index: 16-byte
-//            asynchronous copies, swizzled as TMA would
+//   warps 2, 3, 12, 13  x rows: through TMA, 32 rows a request, where slots are
+//            rows; gathered through the index by 16-byte asynchronous copies,
+//            swizzled as TMA would, where they are not (TMA's gather of four
+//            rows took 64 cycles a request)
 //   warp 14  the scale bytes of those rows, through registers into the tile
 //            layout
 //   warp 15  which tile comes next and which x rows it takes, a few tiles ahead
@@ -46,6 +48,7 @@ namespace {
 constexpr int kMmThreads = 512;
 constexpr int kEpiWarps = 8;
 constexpr int kXWarps = 4;
+constexpr int kXBox = 32;             // x rows per TMA request
 constexpr int kTurnStride = 36;      // floats between slots of a warp's 8 x 32 piece: reads and writes without bank conflicts
 constexpr int kMmMaxExperts = 8192;
 constexpr uint32_t kTmemCols = 512;
@@ -82,6 +85,7 @@ struct MmParams {
     int32_t stages;
     uint32_t stage_bytes;
     int32_t act, bias_dtype, residual_dtype;
+    int32_t x_tma;               // x rows through TMA
     int32_t out_wide, residual_wide;   // 16-byte accesses allowed
 };
 
@@ -264,7 +268,7 @@ struct Ring {
 };
 
 constexpr int kTileRing = 4;         // tiles that the roles may be apart
-constexpr int kMaxTileSlots = 224;
+constexpr int kMaxTileSlots = 192;
 constexpr int kTileUsers = 3 + kXWarps + kEpiWarps;
 
 struct Shared {
@@ -277,7 +281,8 @@ struct Shared {
 // KIND: csf_rows_kind of x.  GATED: a tile has 128 gate rows and their up rows.
 template <int KIND, bool GATED, int OUT>
 __global__ void __launch_bounds__(kMmThreads, 1)
-expert_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ MmParams p) {
+expert_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
+                     const __grid_constant__ MmParams p) {
     extern __shared__ __align__(1024) uint8_t dyn[];
     __shared__ Shared sh;
     __shared__ __align__(16) float turn[kEpiWarps][2 * 8 * kTurnStride];
@@ -308,7 +313,7 @@ expert_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_cons
 
     if (tid == 0) {
         for (int i = 0; i < p.stages; ++i) {
-            tc::bar_init(full0 + 8 * i, 2 + 32 * kXWarps);    // the weights' expect, the scales, the copying lanes
+            tc::bar_init(full0 + 8 * i, p.x_tma ? 3 : 2 + 32 * kXWarps);    // weights, x scales, x (its copying lanes)
             tc::bar_init(empty0 + 8 * i, 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -317,7 +322,7 @@ expert_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_cons
         }
         for (int i = 0; i < kTileRing; ++i) {
             tc::bar_init(tilef0 + 8 * i, 1);
-            tc::bar_init(tilee0 + 8 * i, kTileUsers);
+            tc::bar_init(tilee0 + 8 * i, p.x_tma ? kTileUsers - (kXWarps - 1) : kTileUsers);
         }
         sh.abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -429,6 +434,24 @@ expert_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_cons
         __syncwarp();
     } else if (warp == 2 || warp == 3 || warp == 12 || warp == 13) {
         // ---- x rows ----
+        if (p.x_tma) {
+            if (warp == 2 && tc::elect_one()) {
+                Ring ring, tr;
+                Tile t;
+                bool ok = true;
+                while (ok && take(tr, t)) {
+                    done_with(tr);
+                    for (int k = 0; k < ksteps; ++k, ring.next(p.stages)) {
+                        ok = tc::bar_wait(empty0 + 8 * ring.s, ring.parity ^ 1u, abort);
+                        if (!ok) break;
+                        const uint32_t base = ring0 + ring.s * p.stage_bytes + b_off, bar = full0 + 8 * ring.s;
+                        tc::bar_expect(bar, (uint32_t)((t.n + kXBox - 1) / kXBox) * (kXBox * 128u));
+                        for (int c = 0; c < t.n; c += kXBox) tc::tma_load_2d(base + c * 128u, &xmap, k * 128, (int)t.slot + c, bar);
+                    }
+                }
+            }
+            __syncwarp();
+        } else {
         const int xw = warp < 4 ? warp - 2 : warp - 10;
         const int piece = lane & 7, sub = lane >> 3;      // 8 lanes a row, 4 rows a copy; every fourth group of 4 rows
         const int code_bytes = kNv ? p.K / 2 : p.K;
@@ -462,22 +485,22 @@ expert_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_cons
                 tc::cp_async_arrive(full0 + 8 * ring.s);
             }
         }
+        }
     } else if (warp == 14) {
         // ---- scales of the x rows ----
-        // Row lane + 32 j; 16 bytes are four scale tiles: a stage (NVFP4) or
-        // four (MXFP8).  The next 16, of the next tile where this one ends,
-        // are under way while these leave.
+        // Row lane + 32 j; 16 bytes are four scale tiles: a unit of one stage
+        // (NVFP4) or four (MXFP8).  Two units, across tiles, are under way.
         constexpr int kRows = (kAccCols + 31) / 32, kStagesPer16 = 4 / kTilesPerStage;
         const int units = (p.ncb + 3) / 4;
+        struct Unit {
+            uint4 v[kRows];
+            int n, stages;      // slots (0: no more tiles), stages it serves
+        };
         Ring ring, tr;
         Tile t;
         const uint4 *src[kRows];
-        uint4 next[kRows];
-        auto load = [&](int u) {
-#pragma unroll
-            for (int j = 0; j < kRows; ++j)
-                if (32 * j < t.n) next[j] = __ldg(src[j] + u);
-        };
+        int u = units;
+        bool more = true;
         auto open = [&]() {
             if (!__all_sync(0xFFFFFFFFu, take(tr, t))) return false;
 #pragma unroll
@@ -488,7 +511,6 @@ expert_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_cons
             __syncwarp();
             if (lane == 0) tc::bar_arrive(tilee0 + 8 * tr.s);
             tr.next(kTileRing);
-            load(0);
             if (p.residual) {      // what the epilogue will add, into L2: 32 bytes a lane
                 const int bytes = p.residual_dtype == CSF_F32 ? 4 : 2;
                 const int sectors = 128 * bytes / 32, per = 32 / sectors, sec = lane % sectors;
@@ -499,46 +521,50 @@ expert_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_cons
             }
             return true;
         };
-        bool more = open();
-        while (more) {
-            const int n = t.n;
-            bool ok = true;
-            int k = 0;
-            for (int u = 0; ok && u < units; ++u) {
-                uint4 now[kRows];
+        auto load = [&](Unit &w) {
+            if (more && u == units) more = open(), u = 0;
+            w.n = more ? t.n : 0;
+            if (!more) return;
+            w.stages = min(kStagesPer16, ksteps - u * kStagesPer16);
 #pragma unroll
-                for (int j = 0; j < kRows; ++j) now[j] = next[j];
-                if (u + 1 < units) load(u + 1);
-                else more = open();
+            for (int j = 0; j < kRows; ++j)
+                if (32 * j < t.n) w.v[j] = __ldg(src[j] + u);
+            ++u;
+        };
+        // What a unit holds goes to its stages; then it takes the one after the next.
+        auto store = [&](Unit &w) {
+            if (w.n == 0) return false;
 #pragma unroll
-                for (int q = 0; q < kStagesPer16; ++q) {
-                    if (k >= ksteps) break;
-                    ok = __all_sync(0xFFFFFFFFu, tc::bar_wait(empty0 + 8 * ring.s, ring.parity ^ 1u, abort));
-                    if (!ok) break;
-                    const uint32_t dst = ring0 + ring.s * p.stage_bytes + sfb_off + lane * 16u;
+            for (int q = 0; q < kStagesPer16; ++q) {
+                if (q >= w.stages) break;
+                if (!__all_sync(0xFFFFFFFFu, tc::bar_wait(empty0 + 8 * ring.s, ring.parity ^ 1u, abort))) return false;
+                const uint32_t dst = ring0 + ring.s * p.stage_bytes + sfb_off + lane * 16u;
 #pragma unroll
-                    for (int j = 0; j < kRows; ++j) {
-                        if (32 * j < n) {
-                            const uint4 v = now[j];
-                            const uint32_t to = dst + (j >> 2) * (kTilesPerStage * 512u) + (j & 3) * 4u;
-                            if constexpr (kNv) {
-                                tc::store_shared(to, v.x);
-                                tc::store_shared(to + 512u, v.y);
-                                tc::store_shared(to + 1024u, v.z);
-                                tc::store_shared(to + 1536u, v.w);
-                            } else {
-                                tc::store_shared(to, q == 0 ? v.x : q == 1 ? v.y : q == 2 ? v.z : v.w);
-                            }
+                for (int j = 0; j < kRows; ++j) {
+                    if (32 * j < w.n) {
+                        const uint4 v = w.v[j];
+                        const uint32_t to = dst + (j >> 2) * (kTilesPerStage * 512u) + (j & 3) * 4u;
+                        if constexpr (kNv) {
+                            tc::store_shared(to, v.x);
+                            tc::store_shared(to + 512u, v.y);
+                            tc::store_shared(to + 1024u, v.z);
+                            tc::store_shared(to + 1536u, v.w);
+                        } else {
+                            tc::store_shared(to, q == 0 ? v.x : q == 1 ? v.y : q == 2 ? v.z : v.w);
                         }
                     }
-                    tc::fence_async_proxy();
-                    __syncwarp();
-                    if (lane == 0) tc::bar_arrive(full0 + 8 * ring.s);
-                    ring.next(p.stages);
-                    ++k;
                 }
+                __syncwarp();
+                if (lane == 0) tc::bar_arrive(full0 + 8 * ring.s);
+                ring.next(p.stages);
             }
-            more = more && ok;
+            load(w);
+            return true;
+        };
+        Unit even, odd;
+        load(even);
+        load(odd);
+        while (store(even) && store(odd)) {
         }
     } else if (warp == 1) {
         // ---- matrix instructions ----
@@ -563,7 +589,7 @@ expert_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_cons
                 for (int k = 0; ok && k < ksteps; ++k, left -= kTilesPerStage, ring.next(p.stages)) {
                     ok = tc::bar_wait(full0 + 8 * ring.s, ring.parity, abort);
                     if (!ok) break;
-                    tc::fence_async_proxy();     // x came by ordinary copies
+                    tc::fence_async_proxy();     // x and its scales came by ordinary stores and copies
                     const uint32_t base = ring0 + ring.s * p.stage_bytes;
                     const uint64_t sb = tc::desc_plain(base + sfb_off), sa = tc::desc_plain(base + sfa_off);
                     const uint64_t bd = tc::desc_sw128(base + b_off), ad = tc::desc_sw128(base);
@@ -753,7 +779,7 @@ EncodeFn encode_fn() {
     return fn;
 }
 
-using Kernel = void (*)(CUtensorMap, MmParams);
+using Kernel = void (*)(CUtensorMap, CUtensorMap, MmParams);
 
 template <int KIND, int OUT>
 Kernel pick(bool gated) {
@@ -872,11 +898,12 @@ extern "C" csf_status csf_expert_matmul(const csf_expert_matmul_args *a, void *s
     p.row_tiles_magic = (uint32_t)((1ull << 32) / (uint32_t)p.row_tiles + 1);
     const int64_t mean = a->slots / std::min<int64_t>(E, a->slots);
     const int most = a->gated ? 96 : mean > 96 ? kMaxTileSlots : 128;
-    p.nt = (int)std::min<int64_t>(most, round_up(a->slots, 16));
+    p.nt = (int)std::min<int64_t>(most, round_up(a->slots, kXBox));
     const uint32_t sf = nv ? 2048u : 512u;
     p.stage_bytes = (uint32_t)round_up(at * 16384 + p.nt * 128 + (at + (p.nt + 127) / 128) * sf, 1024);
     const int fixed = 1024 + 8 * (E + 1) + 16;
-    const int room = kSmemLimit - (int)round_up(sizeof(Shared) + sizeof(float) * kEpiWarps * 16 * kTurnStride, 1024) - fixed;
+    const int fixed_static = sizeof(Shared) + sizeof(float) * kEpiWarps * 16 * kTurnStride;
+    const int room = kSmemLimit - (int)round_up(fixed_static, 1024) - fixed;
     p.stages = std::min<int>(kMaxStages, room / (int)p.stage_bytes);
     // never two blocks on an SM: each holds the whole tensor memory
     const int smem = std::max(fixed + p.stages * (int)p.stage_bytes, 120 * 1024);
@@ -887,7 +914,7 @@ extern "C" csf_status csf_expert_matmul(const csf_expert_matmul_args *a, void *s
     EncodeFn encode = encode_fn();
     if (sms < 1 || !encode) return CSF_ERR_CUDA;
 
-    CUtensorMap wmap;
+    CUtensorMap wmap, xmap;
     {
         const cuuint64_t dims[3] = {(cuuint64_t)(nv ? K / 2 : K), (cuuint64_t)N, (cuuint64_t)E};
         const cuuint64_t strides[2] = {(cuuint64_t)K / 2, (cuuint64_t)K / 2 * (cuuint64_t)N};
@@ -897,13 +924,24 @@ extern "C" csf_status csf_expert_matmul(const csf_expert_matmul_args *a, void *s
                    CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
             return CSF_ERR_CUDA;
     }
+    p.x_tma = !a->rows;
+    if (p.x_tma) {
+        const cuuint64_t dims[2] = {(cuuint64_t)(nv ? K / 2 : K), (cuuint64_t)a->x.rows};
+        const cuuint64_t strides[1] = {(cuuint64_t)a->x.code_stride};
+        const cuuint32_t box[2] = {128, kXBox}, ones[2] = {1, 1};
+        if (encode(&xmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, a->x.codes, dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+            return CSF_ERR_CUDA;
+    } else {
+        xmap = wmap;      // not read
+    }
     Kernel k = nv ? pick_out<CSF_ROWS_NVFP4>(out, a->gated) : pick_out<CSF_ROWS_MXFP8>(out, a->gated);
     if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) {
         cudaGetLastError();
         return CSF_ERR_CUDA;
     }
     const int grid = (int)std::min<int64_t>(sms, most_tiles);
-    k<<<grid, kMmThreads, smem, static_cast<cudaStream_t>(stream)>>>(wmap, p);
+    k<<<grid, kMmThreads, smem, static_cast<cudaStream_t>(stream)>>>(wmap, xmap, p);
     if (cudaGetLastError() != cudaSuccess) return CSF_ERR_CUDA;
     return CSF_OK;
 }
