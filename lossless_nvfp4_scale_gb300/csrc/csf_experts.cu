@@ -34,6 +34,8 @@
 // scale block are neighbours.
 #include <algorithm>
 #include <cstring>
+#include <mutex>
+#include <set>
 #include <type_traits>
 
 #include <cuda.h>
@@ -268,7 +270,7 @@ struct Ring {
 };
 
 constexpr int kTileRing = 4;         // tiles that the roles may be apart
-constexpr int kMaxTileSlots = 192;
+constexpr int kMaxTileSlots = 224;
 constexpr int kTileUsers = 3 + kXWarps + kEpiWarps;
 
 struct Shared {
@@ -341,7 +343,8 @@ expert_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_cons
             if (b > a) tiles = (uint32_t)((b - a + p.nt - 1) / p.nt);
             if (p.start) {
                 const long long raw = p.es64 ? static_cast<const long long *>(p.start)[e + 1] : static_cast<const int *>(p.start)[e + 1];
-                bad |= raw != b || b < a;
+                const long long raw0 = p.es64 ? static_cast<const long long *>(p.start)[e] : static_cast<const int *>(p.start)[e];
+                bad |= raw != b || raw0 != a || b < a;
             }
         }
         uint32_t sum = tiles;
@@ -815,6 +818,28 @@ int sm_count() {
     return counts[dev];
 }
 
+// Raises a kernel's shared-memory limit once a device.
+bool allow_smem(const void *kernel) {
+    static std::mutex mu;
+    static std::set<std::pair<const void *, int>> done;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) {
+        cudaGetLastError();
+        return false;
+    }
+    std::lock_guard<std::mutex> lock(mu);
+    if (done.count({kernel, dev})) return true;
+    cudaFuncAttributes attr;
+    if (cudaFuncGetAttributes(&attr, kernel) != cudaSuccess ||
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit - (int)round_up(attr.sharedSizeBytes, 1024)) !=
+            cudaSuccess) {
+        cudaGetLastError();
+        return false;
+    }
+    done.insert({kernel, dev});
+    return true;
+}
+
 csf_status check(const csf_expert_matmul_args *a) {
     if (!a) return CSF_ERR_ARG;
     if (!rows_valid(a->x) || a->experts < 1 || a->n < 1 || a->slots < 0) return CSF_ERR_ARG;
@@ -936,10 +961,7 @@ extern "C" csf_status csf_expert_matmul(const csf_expert_matmul_args *a, void *s
         xmap = wmap;      // not read
     }
     Kernel k = nv ? pick_out<CSF_ROWS_NVFP4>(out, a->gated) : pick_out<CSF_ROWS_MXFP8>(out, a->gated);
-    if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) {
-        cudaGetLastError();
-        return CSF_ERR_CUDA;
-    }
+    if (!allow_smem(reinterpret_cast<const void *>(k))) return CSF_ERR_CUDA;
     const int grid = (int)std::min<int64_t>(sms, most_tiles);
     k<<<grid, kMmThreads, smem, static_cast<cudaStream_t>(stream)>>>(wmap, xmap, p);
     if (cudaGetLastError() != cudaSuccess) return CSF_ERR_CUDA;

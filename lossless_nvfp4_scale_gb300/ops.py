@@ -16,57 +16,46 @@ Typical use (one layer of experts)::
 from __future__ import annotations
 
 import ctypes
+import struct
 from dataclasses import dataclass
 
 import torch
 
-from . import csf
-from .csf import CsfError, _check, _es, _stream, lib
+from .csf import CsfError, _check, _es, lib
 
 NVFP4 = 0     # rows of E2M1 codes, a UE4M3 scale per 16; goes with NVFP4 weights
 MXFP8 = 1     # rows of E4M3 codes, a UE8M0 scale per 32; goes with MXFP4 weights
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 _ACTS = {None: 0, "none": 0, "relu": 1, "silu": 2, "gelu": 3}
 
-_i32, _i64, _vp, _f32 = ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p, ctypes.c_float
+_vp = ctypes.c_void_p
 
 
-class CRows(ctypes.Structure):
-    """csf_rows: quantised rows."""
-    _fields_ = [("kind", _i32), ("cols", _i32), ("rows", _i64), ("codes", _vp), ("code_stride", _i64),
-                ("scales", _vp), ("scale_stride", _i64), ("tensor_scale", _vp)]
+# The argument structs of csf_ops.h, packed as bytes: a fifth of the time that
+# ctypes structures take to fill, which is what a one-token call waits for.
+_ROWS = "iiqPqPqP"                                    # csf_rows
+_RMS_NORM = struct.Struct("@PqPqPqPif" + _ROWS)       # csf_rms_norm_args
+_ROUTE = struct.Struct("@PqiiiiiPPPPPPN")             # csf_route_args
+_EXPERT_MATMUL = struct.Struct("@" + _ROWS + "PqiiPPPiPPiiiPPqiiPq" + _ROWS + "P")   # csf_expert_matmul_args
+_NO_ROWS = (0, 0, 0, 0, 0, 0, 0, 0)
 
-
-class CRmsNorm(ctypes.Structure):
-    """csf_rms_norm_args."""
-    _fields_ = [("x", _vp), ("x_stride", _i64), ("residual", _vp), ("residual_stride", _i64), ("sum_out", _vp),
-                ("sum_stride", _i64), ("weight", _vp), ("dtype", _i32), ("eps", _f32), ("out", CRows)]
-
-
-class CRoute(ctypes.Structure):
-    """csf_route_args."""
-    _fields_ = [("logits", _vp), ("logits_stride", _i64), ("dtype", _i32), ("tokens", _i32), ("experts", _i32),
-                ("k", _i32), ("renormalize", _i32), ("ids", _vp), ("weights", _vp), ("expert_start", _vp),
-                ("rows", _vp), ("slots", _vp), ("scratch", _vp), ("scratch_bytes", ctypes.c_size_t)]
-
-
-class CExpertMatmul(ctypes.Structure):
-    """csf_expert_matmul_args."""
-    _fields_ = [("x", CRows), ("rows", _vp), ("slots", _i64), ("experts", _i32), ("n", _i32), ("w", _vp),
-                ("w_scales", _vp), ("expert_start", _vp), ("expert_start_is_int64", _i32), ("alpha", _vp),
-                ("bias", _vp), ("bias_dtype", _i32), ("act", _i32), ("gated", _i32), ("row_scale", _vp),
-                ("residual", _vp), ("residual_stride", _i64), ("residual_dtype", _i32), ("out_dtype", _i32),
-                ("out", _vp), ("out_stride", _i64), ("out_rows", CRows), ("error_word", _vp)]
-
-
-lib.csf_rms_norm.argtypes = [ctypes.POINTER(CRmsNorm), _vp]
+lib.csf_rms_norm.argtypes = [ctypes.c_char_p, _vp]
 lib.csf_rms_norm.restype = ctypes.c_int
-lib.csf_route.argtypes = [ctypes.POINTER(CRoute), _vp]
+lib.csf_route.argtypes = [ctypes.c_char_p, _vp]
 lib.csf_route.restype = ctypes.c_int
-lib.csf_route_scratch_bytes.argtypes = [_i32, _i32]
+lib.csf_route_scratch_bytes.argtypes = [ctypes.c_int32, ctypes.c_int32]
 lib.csf_route_scratch_bytes.restype = ctypes.c_size_t
-lib.csf_expert_matmul.argtypes = [ctypes.POINTER(CExpertMatmul), _vp]
+lib.csf_expert_matmul.argtypes = [ctypes.c_char_p, _vp]
 lib.csf_expert_matmul.restype = ctypes.c_int
+
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _on(stream, call, *args, **kwargs):
+    """The call with `stream` current, so that what it allocates is the
+    stream's own."""
+    with torch.cuda.stream(stream):
+        return call(*args, **kwargs)
 
 
 def _up(n: int, m: int) -> int:
@@ -97,10 +86,11 @@ class Quantized:
     def rows(self) -> int:
         return self.codes.shape[0]
 
-    def cstruct(self) -> CRows:
+    def fields(self) -> tuple:
+        """The fields of csf_rows."""
         c, s, t = self.codes, self.scales, self.tensor_scale
-        return CRows(self.kind, self.cols, c.shape[0], c.data_ptr(), c.stride(0), s.data_ptr(), s.stride(0),
-                     None if t is None else t.data_ptr())
+        return (self.kind, self.cols, c.shape[0], c.data_ptr(), c.stride(0), s.data_ptr(), s.stride(0),
+                0 if t is None else t.data_ptr())
 
 
 def empty_quantized(kind: int, rows: int, cols: int, device=None, tensor_scale: torch.Tensor | None = None) -> Quantized:
@@ -108,6 +98,8 @@ def empty_quantized(kind: int, rows: int, cols: int, device=None, tensor_scale: 
     if kind not in (NVFP4, MXFP8):
         raise CsfError("quantised rows are NVFP4 or MXFP8")
     device = device if device is not None else "cuda"
+    if cols < 1:
+        raise CsfError("quantised rows have at least one column")
     return Quantized(kind, torch.empty((rows, _code_bytes(kind, cols)), dtype=torch.uint8, device=device),
                      torch.empty((rows, _scale_bytes(kind, cols)), dtype=torch.uint8, device=device), cols, tensor_scale)
 
@@ -134,7 +126,7 @@ def _matrix(t, name: str, rows: int, cols: int, dtype=None):
 
 def _vector(t, name: str, n: int, dtype):
     if t is None:
-        return None
+        return 0
     if not t.is_cuda or t.dtype != dtype or t.numel() != n or not t.is_contiguous():
         raise CsfError(f"{name} must be a contiguous CUDA tensor of {n} {dtype}")
     return t.data_ptr()
@@ -147,14 +139,16 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, kind: int, residual: torch.T
     of `x` [rows, cols] in one launch (csf_rms_norm).  Returns the quantised
     rows and the sum x + residual (in `sum_out`, which may be `residual`
     itself, or a new tensor; None without a residual and a `sum_out`)."""
+    if stream is not None:
+        return _on(stream, rms_norm, x, weight, kind, residual, eps, tensor_scale, out, sum_out)
     if x.dim() != 2 or x.dtype not in _DTYPES:
         raise CsfError("rms_norm: x must be [rows, cols] of bfloat16, float16 or float32")
     rows, cols = x.shape
     xp, xs = _matrix(x, "rms_norm: x", rows, cols)
-    rp, rs = (None, 0) if residual is None else _matrix(residual, "rms_norm: residual", rows, cols, x.dtype)
+    rp, rs = (0, 0) if residual is None else _matrix(residual, "rms_norm: residual", rows, cols, x.dtype)
     if sum_out is None and residual is not None:
         sum_out = torch.empty((rows, cols), dtype=x.dtype, device=x.device)
-    sp, ss = (None, 0) if sum_out is None else _matrix(sum_out, "rms_norm: sum_out", rows, cols, x.dtype)
+    sp, ss = (0, 0) if sum_out is None else _matrix(sum_out, "rms_norm: sum_out", rows, cols, x.dtype)
     wp = _vector(weight, "rms_norm: weight", cols, x.dtype)
     if out is None:
         out = empty_quantized(kind, rows, cols, x.device, tensor_scale)
@@ -166,8 +160,10 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, kind: int, residual: torch.T
     _vector(tensor_scale, "rms_norm: tensor_scale", 1, torch.float32)
     if tensor_scale is not None and kind != NVFP4:
         raise CsfError("rms_norm: only NVFP4 rows have a tensor scale")
-    a = CRmsNorm(xp, xs, rp, rs, sp, ss, wp, _DTYPES[x.dtype], eps, out.cstruct())
-    _check(lib.csf_rms_norm(ctypes.byref(a), _stream(stream)), "csf_rms_norm")
+    a = _RMS_NORM.pack(xp, xs, rp, rs, sp, ss, wp, _DTYPES[x.dtype], eps, *out.fields())
+    status = lib.csf_rms_norm(a, _raw_stream(x.device.index))
+    if status:
+        _check(status, "csf_rms_norm")
     return out, sum_out
 
 
@@ -185,24 +181,27 @@ class Routing:
 def route(logits: torch.Tensor, k: int, renormalize: bool = True, stream=None) -> Routing:
     """Choose each token's k experts from `logits` [tokens, experts] and group
     the choices by expert (csf_route)."""
+    if stream is not None:
+        return _on(stream, route, logits, k, renormalize)
     if logits.dim() != 2:
         raise CsfError("route: logits must be [tokens, experts]")
     T, E = logits.shape
+    if not 1 <= k <= min(32, E):
+        raise CsfError(f"route: k must be 1 to {min(32, E)}")
     lp, ls = _matrix(logits, "route: logits", T, E)
     dev = logits.device
     i32 = dict(dtype=torch.int32, device=dev)
-    n = T * max(k, 0)
-    r = Routing(torch.empty((T, max(k, 0)), **i32), torch.empty((T, max(k, 0)), dtype=torch.float32, device=dev),
-                torch.empty(E + 1, **i32), torch.empty(n, **i32), torch.empty((T, max(k, 0)), **i32))
+    n = T * k
+    r = Routing(torch.empty((T, k), **i32), torch.empty((T, k), dtype=torch.float32, device=dev),
+                torch.empty(E + 1, **i32), torch.empty(n, **i32), torch.empty((T, k), **i32))
     need = lib.csf_route_scratch_bytes(T, E)
     scratch = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
-    a = CRoute(lp, ls, _DTYPES[logits.dtype], T, E, k, int(renormalize), r.ids.data_ptr(), r.weights.data_ptr(),
-               r.expert_start.data_ptr(), r.rows.data_ptr(), r.slots.data_ptr(),
-               scratch.data_ptr() if need else None, need)
-    s = stream if stream is not None else torch.cuda.current_stream()
-    if need:
-        scratch.record_stream(s)
-    _check(lib.csf_route(ctypes.byref(a), s.cuda_stream), "csf_route")
+    a = _ROUTE.pack(lp, ls, _DTYPES[logits.dtype], T, E, k, renormalize, r.ids.data_ptr(), r.weights.data_ptr(),
+                    r.expert_start.data_ptr(), r.rows.data_ptr(), r.slots.data_ptr(),
+                    scratch.data_ptr() if need else 0, need)
+    status = lib.csf_route(a, _raw_stream(dev.index))
+    if status:
+        _check(status, "csf_route")
     return r
 
 
@@ -222,6 +221,9 @@ def expert_matmul(x: Quantized, w: torch.Tensor, w_scales: torch.Tensor, expert_
     or act(p[:N/2]) * p[N/2:] when `gated`; out = y * row_scale[s] + residual.
     `out` is a dtype, a tensor, NVFP4 or MXFP8 (a new Quantized), or a
     Quantized.  Activations: None, "relu", "silu", "gelu" (tanh form)."""
+    if stream is not None:
+        return _on(stream, expert_matmul, x, w, w_scales, expert_start, rows, alpha, bias, activation, gated, row_scale,
+                   residual, out, out_tensor_scale, error_word)
     _check_quantized(x, "expert_matmul: x")
     if w.dtype != torch.uint8 or not w.is_cuda or w.dim() != 3 or not w.is_contiguous() or w.shape[2] * 2 != x.cols:
         raise CsfError(f"expert_matmul: w must be a contiguous uint8 CUDA tensor [E, N, {x.cols // 2}]")
@@ -244,7 +246,7 @@ def expert_matmul(x: Quantized, w: torch.Tensor, w_scales: torch.Tensor, expert_
         if bias.dtype not in _DTYPES:
             raise CsfError("expert_matmul: bias must be bfloat16, float16 or float32")
         bias_dtype = _DTYPES[bias.dtype]
-    rp, rs = (None, 0) if residual is None else _matrix(residual, "expert_matmul: residual", S, F)
+    rp, rs = (0, 0) if residual is None else _matrix(residual, "expert_matmul: residual", S, F)
     if isinstance(out, torch.dtype):
         if out not in _DTYPES:
             raise CsfError("expert_matmul: out must be bfloat16, float16 or float32")
@@ -257,16 +259,18 @@ def expert_matmul(x: Quantized, w: torch.Tensor, w_scales: torch.Tensor, expert_
             raise CsfError("expert_matmul: out does not match the product")
         out.tensor_scale = out_tensor_scale
         _vector(out_tensor_scale, "expert_matmul: out_tensor_scale", 1, torch.float32)
-        op, os_, odt, orows = None, 0, 0, out.cstruct()
+        op, os_, odt, orows = 0, 0, 0, out.fields()
     else:
         op, os_ = _matrix(out, "expert_matmul: out", S, F)
-        odt, orows = _DTYPES[out.dtype], CRows()
-    a = CExpertMatmul(
-        x.cstruct(), None if rows is None else rows.data_ptr(), S, E, N, w.data_ptr(), w_scales.data_ptr(), es, es64,
+        odt, orows = _DTYPES[out.dtype], _NO_ROWS
+    a = _EXPERT_MATMUL.pack(
+        *x.fields(), 0 if rows is None else rows.data_ptr(), S, E, N, w.data_ptr(), w_scales.data_ptr(), es or 0, es64,
         _vector(alpha, "expert_matmul: alpha", E, torch.float32),
-        None if bias is None else _vector(bias, "expert_matmul: bias", E * N, bias.dtype), bias_dtype, _ACTS[activation],
-        int(gated), _vector(row_scale, "expert_matmul: row_scale", S, torch.float32), rp, rs,
-        0 if residual is None else _DTYPES[residual.dtype], odt, op, os_, orows,
+        0 if bias is None else _vector(bias, "expert_matmul: bias", E * N, bias.dtype), bias_dtype, _ACTS[activation],
+        gated, _vector(row_scale, "expert_matmul: row_scale", S, torch.float32), rp, rs,
+        0 if residual is None else _DTYPES[residual.dtype], odt, op, os_, *orows,
         _vector(error_word, "expert_matmul: error_word", 1, torch.int32))
-    _check(lib.csf_expert_matmul(ctypes.byref(a), _stream(stream)), "csf_expert_matmul")
+    status = lib.csf_expert_matmul(a, _raw_stream(w.device.index))
+    if status:
+        _check(status, "csf_expert_matmul")
     return out
