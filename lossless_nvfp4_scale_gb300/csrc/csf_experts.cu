@@ -27,9 +27,9 @@
 // products.  A gated product holds two accumulators: row tile t of the gate
 // half and of the up half, from the same x rows.
 //
-// The epilogue reads an accumulator a weight row a lane, 8 slots at a time,
+// The epilogue reads an accumulator a weight row a lane, 8 or 16 slots at a time,
 // applies what belongs to the row (alpha, bias, activation), and turns the
-// 8 x 32 piece around in shared memory, so that a lane then holds 8 columns
+// piece around in shared memory, so that a lane then holds 8 columns
 // of one slot: residual and output move 16 bytes a lane, and the lanes of a
 // scale block are neighbours.
 #include <algorithm>
@@ -51,7 +51,7 @@ constexpr int kMmThreads = 512;
 constexpr int kEpiWarps = 8;
 constexpr int kXWarps = 4;
 constexpr int kXBox = 32;             // x rows per TMA request
-constexpr int kTurnStride = 36;      // floats between slots of a warp's 8 x 32 piece: reads and writes without bank conflicts
+constexpr int kTurnStride = 36;      // floats between slots of a warp's 16 x 32 piece: reads and writes without bank conflicts
 constexpr int kMmMaxExperts = 8192;
 constexpr uint32_t kTmemCols = 512;
 constexpr int kSmemLimit = 227 * 1024;
@@ -281,13 +281,14 @@ struct Shared {
 };
 
 // KIND: csf_rows_kind of x.  GATED: a tile has 128 gate rows and their up rows.
-template <int KIND, bool GATED, int OUT>
+// RES: there is a residual or a row weight.
+template <int KIND, bool GATED, bool RES, int OUT>
 __global__ void __launch_bounds__(kMmThreads, 1)
 expert_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
                      const __grid_constant__ MmParams p) {
     extern __shared__ __align__(1024) uint8_t dyn[];
     __shared__ Shared sh;
-    __shared__ __align__(16) float turn[kEpiWarps][2 * 8 * kTurnStride];
+    __shared__ __align__(16) float turn[kEpiWarps][16 * kTurnStride];
     constexpr int AT = GATED ? 2 : 1;                     // 128-row weight tiles per tile
     constexpr bool kNv = KIND == CSF_ROWS_NVFP4;
     constexpr int kStepK = kNv ? 256 : 128;               // elements per stage: 128 bytes of codes a row
@@ -295,6 +296,7 @@ expert_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_cons
     constexpr uint32_t kABytes = 128 * 128;
     constexpr uint32_t kACopied = kNv ? kABytes : kABytes / 2;   // E2M1 codes unpack on the way: counted as stored
     constexpr int kAccCols = AT == 1 ? kMaxTileSlots : 96;   // accumulator columns (most slots per tile)
+    constexpr int kGroups = RES && !GATED ? 2 : 1;        // 8-slot groups an epilogue warp takes a round
     constexpr int kRowBlocks = (kAccCols + 127) / 128;    // 128-row blocks of x scales
     constexpr uint32_t kSfCols = 4 * kTilesPerStage;      // tensor-memory columns of one operand's scales
     constexpr uint32_t kSfBase = 2 * AT * kAccCols;
@@ -492,7 +494,8 @@ expert_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_cons
     } else if (warp == 14) {
         // ---- scales of the x rows ----
         // Row lane + 32 j; 16 bytes are four scale tiles: a unit of one stage
-        // (NVFP4) or four (MXFP8).  Two units, across tiles, are under way.
+        // (NVFP4) or four (MXFP8).  Units are loaded ahead, across tiles: two of
+        // up to 224 slots, four of up to 96 (they stay in registers).
         constexpr int kRows = (kAccCols + 31) / 32, kStagesPer16 = 4 / kTilesPerStage;
         const int units = (p.ncb + 3) / 4;
         struct Unit {
@@ -514,7 +517,7 @@ expert_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_cons
             __syncwarp();
             if (lane == 0) tc::bar_arrive(tilee0 + 8 * tr.s);
             tr.next(kTileRing);
-            if (p.residual) {      // what the epilogue will add, into L2: 32 bytes a lane
+            if (RES && p.residual) {      // what the epilogue will add, into L2: 32 bytes a lane
                 const int bytes = p.residual_dtype == CSF_F32 ? 4 : 2;
                 const int sectors = 128 * bytes / 32, per = 32 / sectors, sec = lane % sectors;
                 const int f = t.rt * 128 + sec * (32 / bytes);
@@ -534,7 +537,7 @@ expert_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_cons
                 if (32 * j < t.n) w.v[j] = __ldg(src[j] + u);
             ++u;
         };
-        // What a unit holds goes to its stages; then it takes the one after the next.
+        // What a unit holds goes to its stages; then it takes a later one.
         auto store = [&](Unit &w) {
             if (w.n == 0) return false;
 #pragma unroll
@@ -564,10 +567,20 @@ expert_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_cons
             load(w);
             return true;
         };
-        Unit even, odd;
-        load(even);
-        load(odd);
-        while (store(even) && store(odd)) {
+        if constexpr (GATED) {
+            Unit a, b, c, d;
+            load(a);
+            load(b);
+            load(c);
+            load(d);
+            while (store(a) && store(b) && store(c) && store(d)) {
+            }
+        } else {
+            Unit a, b;
+            load(a);
+            load(b);
+            while (store(a) && store(b)) {
+            }
         }
     } else if (warp == 1) {
         // ---- matrix instructions ----
@@ -635,8 +648,9 @@ expert_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_cons
     } else {
         // ---- epilogue ----
         // Warps w and w + 4 read the same 32 weight rows and take every other
-        // 8 slots.  One rolled loop: longer code ran out of the instruction
+        // 8 G slots.  One rolled loop: longer code ran out of the instruction
         // cache.
+        constexpr int G = kGroups;
         const int w = (warp - 4) & 3, half = (warp - 4) >> 2;
         const int part = lane & 3, sub = lane >> 2;           // after the turn: 8 columns of a slot
         float *buf = turn[warp - 4];
@@ -646,12 +660,12 @@ expert_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_cons
         }
         constexpr int kOutBytes = OUT == kOutF32 ? 4 : OUT == kOutBf16 || OUT == kOutF16 ? 2 : 1;
         const int res_bytes = p.residual_dtype == CSF_F32 ? 4 : 2;
-        const int64_t out_step = 16 * p.out_stride * kOutBytes, res_step = 16 * p.residual_stride * res_bytes;
+        const int64_t out_8 = 8 * p.out_stride * kOutBytes, res_8 = 8 * p.residual_stride * res_bytes, srow_8 = 8 * p.out_scale_stride;
         // What a tile needs before its first round, fetched a tile ahead.
         struct Head {
             Tile t;
-            Raw8 res;
-            float alpha, rs;
+            Raw8 res[G];
+            float alpha, rs[G];
             uint32_t bias[AT];      // as stored
         };
         Ring tr;
@@ -663,11 +677,15 @@ expert_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_cons
             __syncwarp();
             if (lane == 0) tc::bar_arrive(tilee0 + 8 * tr.s);
             tr.next(kTileRing);
-            const int row = h.t.rt * 128 + 32 * w, f = row + 8 * part, c = 8 * half + sub;
-            if (p.residual && c < h.t.n)
-                h.res = load_raw8(static_cast<const char *>(p.residual) + (((int64_t)h.t.slot + c) * p.residual_stride + f) * res_bytes,
-                                  p.residual_dtype, p.F - f, p.residual_wide);
-            if (p.row_scale && c < h.t.n) h.rs = p.row_scale[(int64_t)h.t.slot + c];
+            const int row = h.t.rt * 128 + 32 * w, f = row + 8 * part;
+#pragma unroll
+            for (int i = 0; i < G; ++i) {
+                const int c = 8 * G * half + 8 * i + sub;
+                if (RES && p.residual && c < h.t.n)
+                    h.res[i] = load_raw8(static_cast<const char *>(p.residual) + (((int64_t)h.t.slot + c) * p.residual_stride + f) * res_bytes,
+                                         p.residual_dtype, p.F - f, p.residual_wide);
+                if (RES && p.row_scale && c < h.t.n) h.rs[i] = p.row_scale[(int64_t)h.t.slot + c];
+            }
             if (p.alpha) h.alpha = p.alpha[h.t.e];
 #pragma unroll
             for (int a = 0; a < AT; ++a) {
@@ -675,23 +693,26 @@ expert_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_cons
                 if (p.bias && r < p.N) h.bias[a] = load_raw(p.bias, (int64_t)h.t.e * p.N + r, p.bias_dtype);
             }
         };
-        uint32_t nth = 0, buf_set = 0;
+        uint32_t nth = 0;
         Head next = {};
         next.alpha = 1.f;
-        next.rs = 1.f;
+#pragma unroll
+        for (int i = 0; i < G; ++i) next.rs[i] = 1.f;
         open(next);
         for (; next.t.n > 0; ++nth) {
             const Tile t = next.t;
             const uint32_t set = nth & 1u, aph = (nth >> 1) & 1u;
             const int f = t.rt * 128 + 32 * w + 8 * part;
-            const int64_t slot = (int64_t)t.slot + 8 * half + sub;     // this lane's next slot
+            const int64_t slot = (int64_t)t.slot + 8 * G * half + sub;     // the first of this lane's slots
             const char *res_at = static_cast<const char *>(p.residual) + (slot * p.residual_stride + f) * res_bytes;
             const float *scale_at = p.row_scale + slot;
             char *out_at = static_cast<char *>(p.out) + slot * p.out_stride * kOutBytes + (OUT == kOutNv || OUT == kOutMx ? 0 : f * kOutBytes);
             uint8_t *srow = p.out_scales + slot * p.out_scale_stride;
-            int c = 8 * half;
-            Raw8 res = next.res;
-            float rs = next.rs;
+            int c = 8 * G * half;
+            Raw8 res[G];
+            float rs[G];
+#pragma unroll
+            for (int i = 0; i < G; ++i) res[i] = next.res[i], rs[i] = next.rs[i];
             const float alpha = next.alpha;
             float bias[AT];
 #pragma unroll
@@ -703,22 +724,22 @@ expert_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_cons
             uint32_t d = tmem + set * (AT * kAccCols) + ((uint32_t)(32 * w) << 16) + c;
             if (c >= t.n) tc::bar_arrive(acce0 + 8 * set);     // no slots of this tile are this warp's
 #pragma unroll 1
-            for (; c < t.n; c += 16, d += 16, buf_set ^= 8 * kTurnStride) {
-                float acc[AT][8];
+            for (; c < t.n; c += 16 * G, d += 16 * G) {
+                float acc[AT][8 * G];
 #pragma unroll
-                for (int a = 0; a < AT; ++a) tc::tmem_load8(d + a * kAccCols, acc[a]);
+                for (int a = 0; a < AT; ++a) tc::tmem_load(d + a * kAccCols, acc[a]);
                 tc::wait_ld();
-                if (c + 16 >= t.n) {
+                if (c + 16 * G >= t.n) {
                     tc::fence_before();
                     tc::bar_arrive(acce0 + 8 * set);
                 }
-                float *to = buf + buf_set;      // two buffers: one barrier a round
+                __syncwarp();      // the last round's reads
                 auto turn_in = [&](auto act) {
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
+                    for (int j = 0; j < 8 * G; ++j) {
                         float y = activate<decltype(act)::value>(fmaf(acc[0][j], alpha, bias[0]));
                         if constexpr (GATED) y *= fmaf(acc[AT - 1][j], alpha, bias[AT - 1]);
-                        to[j * kTurnStride + lane] = y;
+                        buf[j * kTurnStride + lane] = y;
                     }
                 };
                 switch (p.act) {
@@ -728,24 +749,28 @@ expert_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_cons
                     default: turn_in(std::integral_constant<int, CSF_ACT_NONE>{}); break;
                 }
                 __syncwarp();
-                const float4 lo = *reinterpret_cast<const float4 *>(to + sub * kTurnStride + 8 * part);
-                const float4 hi = *reinterpret_cast<const float4 *>(to + sub * kTurnStride + 8 * part + 4);
-                float y[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-                const bool live = c + sub < t.n, more = c + 16 + sub < t.n;
-                if (p.row_scale) {
 #pragma unroll
-                    for (int q = 0; q < 8; ++q) y[q] *= rs;
-                    scale_at += 16;
-                    if (more) rs = *scale_at;
+                for (int i = 0; i < G; ++i) {
+                    const float4 *from = reinterpret_cast<const float4 *>(buf + (8 * i + sub) * kTurnStride + 8 * part);
+                    const float4 lo = from[0], hi = from[1];
+                    float y[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+                    const int j = c + 8 * i + sub;
+                    const bool more = j + 16 * G < t.n;
+                    if (RES && p.row_scale) {
+#pragma unroll
+                        for (int q = 0; q < 8; ++q) y[q] *= rs[i];
+                        if (more) rs[i] = scale_at[8 * i + 16 * G];
+                    }
+                    if (RES && p.residual) {
+                        add_raw8(y, res[i], p.residual_dtype);
+                        if (more) res[i] = load_raw8(res_at + (i + 2 * G) * res_8, p.residual_dtype, p.F - f, p.residual_wide);
+                    }
+                    emit8<OUT>(p, y, f, out_at + i * out_8, srow + i * srow_8, j < t.n, tensor_scale);
                 }
-                if (p.residual) {
-                    add_raw8(y, res, p.residual_dtype);
-                    res_at += res_step;
-                    if (more) res = load_raw8(res_at, p.residual_dtype, p.F - f, p.residual_wide);
-                }
-                emit8<OUT>(p, y, f, out_at, srow, live, tensor_scale);
-                out_at += out_step;
-                srow += 16 * p.out_scale_stride;
+                scale_at += 16 * G;
+                res_at += 2 * G * res_8;
+                out_at += 2 * G * out_8;
+                srow += 2 * G * srow_8;
             }
         }
     }
@@ -785,18 +810,19 @@ EncodeFn encode_fn() {
 using Kernel = void (*)(CUtensorMap, CUtensorMap, MmParams);
 
 template <int KIND, int OUT>
-Kernel pick(bool gated) {
-    return gated ? expert_matmul_kernel<KIND, true, OUT> : expert_matmul_kernel<KIND, false, OUT>;
+Kernel pick(bool gated, bool res) {
+    if (gated) return res ? expert_matmul_kernel<KIND, true, true, OUT> : expert_matmul_kernel<KIND, true, false, OUT>;
+    return res ? expert_matmul_kernel<KIND, false, true, OUT> : expert_matmul_kernel<KIND, false, false, OUT>;
 }
 
 template <int KIND>
-Kernel pick_out(int out, bool gated) {
+Kernel pick_out(int out, bool gated, bool res) {
     switch (out) {
-        case kOutBf16: return pick<KIND, kOutBf16>(gated);
-        case kOutF16: return pick<KIND, kOutF16>(gated);
-        case kOutF32: return pick<KIND, kOutF32>(gated);
-        case kOutNv: return pick<KIND, kOutNv>(gated);
-        default: return pick<KIND, kOutMx>(gated);
+        case kOutBf16: return pick<KIND, kOutBf16>(gated, res);
+        case kOutF16: return pick<KIND, kOutF16>(gated, res);
+        case kOutF32: return pick<KIND, kOutF32>(gated, res);
+        case kOutNv: return pick<KIND, kOutNv>(gated, res);
+        default: return pick<KIND, kOutMx>(gated, res);
     }
 }
 
@@ -960,7 +986,7 @@ extern "C" csf_status csf_expert_matmul(const csf_expert_matmul_args *a, void *s
     } else {
         xmap = wmap;      // not read
     }
-    Kernel k = nv ? pick_out<CSF_ROWS_NVFP4>(out, a->gated) : pick_out<CSF_ROWS_MXFP8>(out, a->gated);
+    Kernel k = nv ? pick_out<CSF_ROWS_NVFP4>(out, a->gated, a->residual || a->row_scale) : pick_out<CSF_ROWS_MXFP8>(out, a->gated, a->residual || a->row_scale);
     if (!allow_smem(reinterpret_cast<const void *>(k))) return CSF_ERR_CUDA;
     const int grid = (int)std::min<int64_t>(sms, most_tiles);
     k<<<grid, kMmThreads, smem, static_cast<cudaStream_t>(stream)>>>(wmap, xmap, p);
