@@ -19,7 +19,8 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libcsf.so")
 SOURCES = ["csf_api.cu", "csf_decode.cu", "csf_tiles.cu", "csf_tiled.cu", "csf_prepare.cu",
-           "csf_prepare_static.cu", "csf_norm.cu", "csf_route.cu", "csf_experts.cu"]
+           "csf_prepare_static.cu", "csf_norm.cu", "csf_route.cu", "csf_experts.cu",
+           "csf_experts_nv.cu", "csf_experts_mx.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -34,7 +35,8 @@ def _inputs():
     files = [os.path.join(CSRC, s) for s in SOURCES]
     files += [os.path.join(CSRC, "csf_internal.cuh"), os.path.join(CSRC, "csf_device.cuh"),
               os.path.join(INCLUDE, "csf.h"), os.path.join(INCLUDE, "csf_tile.cuh"),
-              os.path.join(CSRC, "csf_quant.cuh"), os.path.join(CSRC, "csf_tc.cuh"), os.path.join(INCLUDE, "csf_ops.h")]
+              os.path.join(CSRC, "csf_quant.cuh"), os.path.join(CSRC, "csf_tc.cuh"),
+              os.path.join(CSRC, "csf_experts.cuh"), os.path.join(INCLUDE, "csf_ops.h")]
     return files
 
 
