@@ -29,24 +29,6 @@ EncodeFn encode_fn() {
     return fn;
 }
 
-int sm_count() {
-    static int counts[64];
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) {
-        cudaGetLastError();
-        return 0;
-    }
-    if (counts[dev] == 0) {
-        int n = 0;
-        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
-            cudaGetLastError();
-            return 0;
-        }
-        counts[dev] = n;
-    }
-    return counts[dev];
-}
-
 // Raises a kernel's shared-memory limit once a device.
 bool allow_smem(const void *kernel) {
     static std::mutex mu;
@@ -93,6 +75,25 @@ csf_status check(const csf_expert_matmul_args *a) {
 
 }  // namespace
 }  // namespace mm
+
+int sm_count() {
+    static int counts[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) {
+        cudaGetLastError();
+        return 0;
+    }
+    if (counts[dev] == 0) {
+        int n = 0;
+        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+            cudaGetLastError();
+            return 0;
+        }
+        counts[dev] = n;
+    }
+    return counts[dev];
+}
+
 }  // namespace csfk
 
 using namespace csfk;

@@ -2,10 +2,13 @@
 // (csf_rms_norm): y = h * rsqrt(mean(h^2) + eps) * weight, h = x + residual.
 //
 // Bound by memory: a row is read once and stays in registers, in chunks of 8
-// columns a thread, while its sum of squares is formed; then the chunks are
-// scaled, the block maxima come from shuffles between the 4 (32 columns,
+// columns a thread, while its sum of squares is formed and the next row is
+// under way; then the chunks are scaled, the block maxima come from shuffles between the 4 (32 columns,
 // MXFP8) or 2 (16 columns, NVFP4) threads of a block, and codes and scales
 // leave.  Rows too wide for the registers are read twice.
+#include <algorithm>
+#include <atomic>
+
 #include "csf_internal.cuh"
 #include "csf_quant.cuh"
 
@@ -83,88 +86,171 @@ __device__ __forceinline__ void load_h(float (&h)[8], const NormParams &p, int64
     }
 }
 
-// One row per block of blockDim.x threads (WARP: per warp).  CHUNKS > 0: that
-// many chunks a thread stay in registers; 0: the row is read twice.
-template <typename T, int KIND, int CHUNKS, bool WARP>
-__global__ void __launch_bounds__(WARP ? 256 : kNormMaxThreads)
+// 8 elements as stored.
+template <typename T>
+struct Raw {
+    union { uint4 q[sizeof(T) / 2]; T e[8]; };
+};
+
+template <typename T>
+__device__ __forceinline__ void load_raw(Raw<T> &r, const T *at) {
+#pragma unroll
+    for (int i = 0; i < (int)(sizeof(T) / 2); ++i) r.q[i] = reinterpret_cast<const uint4 *>(at)[i];
+}
+
+// Threads of a block that loads ahead: what it holds of 32-bit rows takes
+// more than the 64 registers that 1024 threads leave.
+template <typename T>
+__host__ __device__ constexpr int max_ahead() {
+    return sizeof(T) == 4 ? 512 : kNormMaxThreads;
+}
+
+// One row at a time per block of blockDim.x threads (WARP: per warp), rows a
+// grid apart.
+//   CHUNKS > 0  a row stays in registers, that many chunks a thread; 0: it is
+//               read twice.
+//   AHEAD       the next row is loaded before this one's sum is formed, and
+//               16-bit weights stay in registers (16-byte loads, whole chunks)
+template <typename T, int KIND, int CHUNKS, bool WARP, bool AHEAD>
+__global__ void __launch_bounds__(WARP ? 256 : AHEAD ? max_ahead<T>() : kNormMaxThreads)
 rms_norm_kernel(const __grid_constant__ NormParams p) {
-    __shared__ float part[32];
+    __shared__ float part[2][32];
+    constexpr int kHeld = CHUNKS > 0 ? CHUNKS : 1;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int tid = WARP ? lane : threadIdx.x, threads = WARP ? 32 : blockDim.x;
-    const int64_t row = WARP ? (int64_t)blockIdx.x * (blockDim.x >> 5) + warp : (int64_t)blockIdx.x;
-    if (row >= p.rows) return;
-    float h[CHUNKS > 0 ? CHUNKS : 1][8];
-    float sum = 0.f;
-    if constexpr (CHUNKS > 0) {
+    const int per_block = WARP ? blockDim.x >> 5 : 1;
+    const int64_t step = (int64_t)gridDim.x * per_block;
+    const T *weight = static_cast<const T *>(p.weight);
+    const float g = KIND == CSF_ROWS_NVFP4 && p.tensor_scale ? *p.tensor_scale : 1.f;
+    const int blocks = KIND == CSF_ROWS_MXFP8 ? p.chunks >> 2 : p.chunks >> 1;
+    constexpr bool kHoldWeight = AHEAD && sizeof(T) == 2;      // 32-bit ones would not fit the registers
+    Raw<T> xr[kHeld], rr[kHeld], wr[kHeld];
+    auto load_ahead = [&](int64_t row) {
 #pragma unroll
-        for (int j = 0; j < CHUNKS; ++j) load_h<T>(h[j], p, row, (tid + j * threads) * 8);
-#pragma unroll
-        for (int j = 0; j < CHUNKS; ++j) {
-            if (p.sum) store8(h[j], static_cast<T *>(p.sum) + row * p.sum_stride, (tid + j * threads) * 8, p.cols, p.wide_sum);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) sum = fmaf(h[j][i], h[j][i], sum);
+        for (int j = 0; j < kHeld; ++j) {
+            const int c = (tid + j * threads) * 8;
+            if (c >= p.cols) continue;
+            load_raw(xr[j], static_cast<const T *>(p.x) + row * p.x_stride + c);
+            if (p.residual) load_raw(rr[j], static_cast<const T *>(p.residual) + row * p.residual_stride + c);
         }
-    } else {
-        for (int c = tid; c < p.chunks; c += threads) {
-            load_h<T>(h[0], p, row, c * 8);
+    };
+    int64_t row = (int64_t)blockIdx.x * per_block + (WARP ? warp : 0);
+    if constexpr (AHEAD) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) sum = fmaf(h[0][i], h[0][i], sum);
+        for (int j = 0; j < kHeld; ++j) {
+#pragma unroll
+            for (int i = 0; i < (int)(sizeof(T) / 2); ++i) xr[j].q[i] = rr[j].q[i] = wr[j].q[i] = make_uint4(0, 0, 0, 0);
+            const int c = (tid + j * threads) * 8;
+            if (kHoldWeight && c < p.cols) load_raw(wr[j], weight + c);
         }
+        if (row < p.rows) load_ahead(row);
     }
+    for (int set = 0; row < p.rows; row += step, set ^= 1) {
+        float h[kHeld][8];
+        float sum = 0.f;
+        if constexpr (AHEAD) {
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
-    if constexpr (!WARP) {
-        if (lane == 0) part[warp] = sum;
-        __syncthreads();
-        sum = lane < (threads >> 5) ? part[lane] : 0.f;
+            for (int j = 0; j < kHeld; ++j) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    h[j][i] = Elem<T>::to(xr[j].e[i]);
+                    if (p.residual) h[j][i] += Elem<T>::to(rr[j].e[i]);
+                }
+            }
+            if (row + step < p.rows) load_ahead(row + step);
+        } else if constexpr (CHUNKS > 0) {
+#pragma unroll
+            for (int j = 0; j < CHUNKS; ++j) load_h<T>(h[j], p, row, (tid + j * threads) * 8);
+        }
+        if constexpr (CHUNKS > 0) {
+#pragma unroll
+            for (int j = 0; j < CHUNKS; ++j) {
+                if (p.sum) store8(h[j], static_cast<T *>(p.sum) + row * p.sum_stride, (tid + j * threads) * 8, p.cols, p.wide_sum);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) sum = fmaf(h[j][i], h[j][i], sum);
+            }
+        } else {
+            for (int c = tid; c < p.chunks; c += threads) {
+                load_h<T>(h[0], p, row, c * 8);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) sum = fmaf(h[0][i], h[0][i], sum);
+            }
+        }
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
+        if constexpr (!WARP) {
+            if (lane == 0) part[set][warp] = sum;
+            __syncthreads();
+            sum = lane < (threads >> 5) ? part[set][lane] : 0.f;
+#pragma unroll
+            for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
+        }
+        const float r = rsqrtf(sum * p.inv_cols + p.eps);
+        uint8_t *codes = p.codes + row * p.code_stride, *scales = p.scales + row * p.scale_stride;
+        if constexpr (CHUNKS > 0) {
+#pragma unroll
+            for (int j = 0; j < CHUNKS; ++j) {
+                const int c = tid + j * threads;
+                float w[8];
+                if constexpr (kHoldWeight) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) w[i] = Elem<T>::to(wr[j].e[i]);
+                } else {
+                    load8(w, weight, c * 8, p.cols, p.wide_weight);
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) h[j][i] = h[j][i] * r * w[i];
+                quant::quantize8<KIND>(h[j], codes, scales, c, c < p.chunks, g);
+            }
+        } else {
+            for (int c0 = 0; c0 < p.chunks; c0 += threads) {
+                const int c = c0 + tid;
+                load_h<T>(h[0], p, row, c * 8);
+                if (p.sum) store8(h[0], static_cast<T *>(p.sum) + row * p.sum_stride, c * 8, p.cols, p.wide_sum);
+                float w[8];
+                load8(w, weight, c * 8, p.cols, p.wide_weight);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) h[0][i] = h[0][i] * r * w[i];
+                quant::quantize8<KIND>(h[0], codes, scales, c, c < p.chunks, g);
+            }
+        }
+        if (tid < ((blocks + 15) & ~15) - blocks) scales[blocks + tid] = 0;
     }
-    const float r = rsqrtf(sum * p.inv_cols + p.eps);
-    const float g = KIND == CSF_ROWS_NVFP4 && p.tensor_scale ? *p.tensor_scale : 1.f;
-    uint8_t *codes = p.codes + row * p.code_stride, *scales = p.scales + row * p.scale_stride;
-    const T *weight = static_cast<const T *>(p.weight);
+}
+
+template <typename T, int KIND, int CHUNKS, bool WARP>
+cudaError_t launch_shape(const NormParams &p, int threads, bool ahead, cudaStream_t s) {
+    const int64_t units = WARP ? (p.rows + threads / 32 - 1) / (threads / 32) : p.rows;
     if constexpr (CHUNKS > 0) {
-#pragma unroll
-        for (int j = 0; j < CHUNKS; ++j) {
-            const int c = tid + j * threads;
-            float w[8];
-            load8(w, weight, c * 8, p.cols, p.wide_weight);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) h[j][i] = h[j][i] * r * w[i];
-            quant::quantize8<KIND>(h[j], codes, scales, c, c < p.chunks, g);
-        }
-    } else {
-        for (int c0 = 0; c0 < p.chunks; c0 += threads) {
-            const int c = c0 + tid;
-            load_h<T>(h[0], p, row, c * 8);
-            if (p.sum) store8(h[0], static_cast<T *>(p.sum) + row * p.sum_stride, c * 8, p.cols, p.wide_sum);
-            float w[8];
-            load8(w, weight, c * 8, p.cols, p.wide_weight);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) h[0][i] = h[0][i] * r * w[i];
-            quant::quantize8<KIND>(h[0], codes, scales, c, c < p.chunks, g);
+        if (ahead && threads <= max_ahead<T>()) {
+            // enough blocks to fill the SMs; each then takes rows in turn
+            auto k = rms_norm_kernel<T, KIND, CHUNKS, WARP, true>;
+            static std::atomic<int> per_sm[kNormMaxThreads / 32 + 1];      // by warps; alike on every device of this architecture
+            int n = per_sm[threads / 32];
+            if (n == 0) {
+                int got = 0;
+                const cudaError_t err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&got, k, threads, 0);
+                if (err != cudaSuccess) return err;
+                per_sm[threads / 32] = n = got > 0 ? got : 1;
+            }
+            const int64_t grid = std::min<int64_t>(units, (int64_t)n * sm_count());
+            if (grid < 1) return cudaErrorUnknown;
+            k<<<(unsigned)grid, threads, 0, s>>>(p);
+            return cudaGetLastError();
         }
     }
-    const int blocks = KIND == CSF_ROWS_MXFP8 ? p.chunks >> 2 : p.chunks >> 1;
-    if (tid < ((blocks + 15) & ~15) - blocks) scales[blocks + tid] = 0;
+    rms_norm_kernel<T, KIND, CHUNKS, WARP, false><<<(unsigned)units, threads, 0, s>>>(p);
+    return cudaGetLastError();
 }
 
 template <typename T, int KIND>
 cudaError_t launch_norm(const NormParams &p, cudaStream_t s) {
-    if (p.chunks <= 32) {
-        rms_norm_kernel<T, KIND, 1, true><<<(unsigned)((p.rows + 7) / 8), 256, 0, s>>>(p);
-    } else {
-        const int per1 = (p.chunks + 31) & ~31;
-        const unsigned grid = (unsigned)p.rows;
-        if (per1 <= 256)
-            rms_norm_kernel<T, KIND, 1, false><<<grid, per1, 0, s>>>(p);
-        else if ((p.chunks + 1) / 2 <= kNormMaxThreads)
-            rms_norm_kernel<T, KIND, 2, false><<<grid, ((p.chunks + 1) / 2 + 31) & ~31, 0, s>>>(p);
-        else
-            rms_norm_kernel<T, KIND, 0, false><<<grid, kNormMaxThreads, 0, s>>>(p);
-    }
-    return cudaGetLastError();
+    const bool ahead = p.wide_x && p.wide_residual && p.wide_weight && p.cols % 8 == 0;
+    if (p.chunks <= 32) return launch_shape<T, KIND, 1, true>(p, 256, ahead, s);
+    const int one = (p.chunks + 31) & ~31, two = ((p.chunks + 1) / 2 + 31) & ~31;
+    if (one <= 256) return launch_shape<T, KIND, 1, false>(p, one, ahead, s);
+    if (two <= kNormMaxThreads) return launch_shape<T, KIND, 2, false>(p, two, ahead, s);
+    return launch_shape<T, KIND, 0, false>(p, kNormMaxThreads, false, s);
 }
 
 template <typename T>

@@ -89,6 +89,9 @@ __device__ __forceinline__ float load_as_float(const void *p, int64_t i, int dty
 
 }  // namespace quant
 
+// SMs of the current device (0: no device).
+int sm_count();
+
 inline int64_t round_up(int64_t n, int64_t m) { return (n + m - 1) / m * m; }
 inline size_t dtype_bytes(int dtype) { return dtype == CSF_F32 ? 4 : 2; }
 inline bool dtype_known(int dtype) { return dtype == CSF_BF16 || dtype == CSF_F16 || dtype == CSF_F32; }

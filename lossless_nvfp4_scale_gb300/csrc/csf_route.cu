@@ -23,7 +23,7 @@ constexpr int kRouteMaxK = 32;
 struct RouteParams {
     const void *logits;
     int64_t stride;
-    int32_t dtype, T, E, k, renormalize;
+    int32_t T, E, k, renormalize;
     int32_t *ids, *start, *rows, *slots;
     float *weights;
     uint32_t *counts;    // [blocks][E]: counts, then their prefixes over the blocks
@@ -80,7 +80,7 @@ __device__ __forceinline__ void scan_experts(const uint32_t *cnt, uint32_t *out,
 
 // VPL: logits per lane (E <= 32 * VPL).  ONE: the only block, which also
 // places the slots.
-template <int VPL, bool ONE>
+template <typename T, int VPL, bool ONE>
 __global__ void __launch_bounds__(kRouteThreads)
 route_choose_kernel(const __grid_constant__ RouteParams p) {
     __shared__ uint32_t mask[2][kRouteMaxExperts];
@@ -94,17 +94,30 @@ route_choose_kernel(const __grid_constant__ RouteParams p) {
     __syncthreads();
     for (int i = warp; i < nt; i += kRouteThreads / 32) {
         const int64_t t = t0 + i;
+        const T *row = static_cast<const T *>(p.logits) + t * p.stride;
+        T raw[VPL];
         uint32_t key[VPL];
-        uint32_t best = 0;
-        int at = 0;
 #pragma unroll
         for (int j = 0; j < VPL; ++j) {
             const int e = lane + 32 * j;
-            key[j] = e < p.E ? key_of(quant::load_as_float(p.logits, t * p.stride + e, p.dtype)) : 0;
+            raw[j] = e < p.E ? row[e] : T(0.f);
         }
 #pragma unroll
-        for (int j = 0; j < VPL; ++j)
-            if (key[j] > best) best = key[j], at = j;
+        for (int j = 0; j < VPL; ++j) key[j] = lane + 32 * j < p.E ? key_of((float)raw[j]) : 0;
+        // The lane's two best, ties to the lower expert.  Eight choices seldom
+        // take a lane's third: only then are its logits gone through again.
+        uint32_t best, second;
+        int best_at, second_at;
+        auto look = [&]() {
+            best = second = 0;
+            best_at = second_at = 0;
+#pragma unroll
+            for (int j = 0; j < VPL; ++j) {
+                if (key[j] > best) second = best, second_at = best_at, best = key[j], best_at = j;
+                else if (key[j] > second) second = key[j], second_at = j;
+            }
+        };
+        look();
         const float vmax = value_of(__reduce_max_sync(0xFFFFFFFFu, best));
         float total = 0.f;
         if (!p.renormalize) {
@@ -114,23 +127,28 @@ route_choose_kernel(const __grid_constant__ RouteParams p) {
             total = warp_sum(total);
         }
         int id = -1;
-        float w = 0.f;
+        uint32_t mine = 0, taken = 0;      // this lane's choice; which of its logits are gone
+        int spare = 1;
         for (int c = 0; c < p.k; ++c) {
             const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, best);
             if (top == 0) break;                       // no expert left
-            const uint32_t e = __reduce_min_sync(0xFFFFFFFFu, best == top ? (uint32_t)(lane + 32 * at) : 0xFFFFFFFFu);
-            if (lane == c) id = (int)e, w = expf(value_of(top) - vmax);
+            const uint32_t e = __reduce_min_sync(0xFFFFFFFFu, best == top ? (uint32_t)(lane + 32 * best_at) : 0xFFFFFFFFu);
+            if (lane == c) id = (int)e, mine = top;
             if ((e & 31) == (uint32_t)lane) {
-                best = 0;
+                taken |= 1u << (e >> 5);
+                if (spare) {
+                    best = second, best_at = second_at;
+                    spare = 0;
+                } else {
 #pragma unroll
-                for (int j = 0; j < VPL; ++j) {
-                    if (j == (int)(e >> 5)) key[j] = 0;
+                    for (int j = 0; j < VPL; ++j)
+                        if (taken >> j & 1) key[j] = 0;
+                    look();
+                    spare = 1;
                 }
-#pragma unroll
-                for (int j = 0; j < VPL; ++j)
-                    if (key[j] > best) best = key[j], at = j;
             }
         }
+        const float w = id < 0 ? 0.f : expf(value_of(mine) - vmax);
         if (p.renormalize) total = warp_sum(w);
         if (lane < p.k) {
             p.ids[t * p.k + lane] = id;
@@ -228,12 +246,19 @@ __global__ void route_none_kernel(int32_t *start, int E) {
     for (int e = threadIdx.x; e <= E; e += blockDim.x) start[e] = 0;
 }
 
+template <typename T, bool ONE>
+void choose_type(const RouteParams &p, int blocks, cudaStream_t s) {
+    if (p.E <= 128) route_choose_kernel<T, 4, ONE><<<blocks, kRouteThreads, 0, s>>>(p);
+    else if (p.E <= 256) route_choose_kernel<T, 8, ONE><<<blocks, kRouteThreads, 0, s>>>(p);
+    else if (p.E <= 512) route_choose_kernel<T, 16, ONE><<<blocks, kRouteThreads, 0, s>>>(p);
+    else route_choose_kernel<T, 32, ONE><<<blocks, kRouteThreads, 0, s>>>(p);
+}
+
 template <bool ONE>
-void choose(const RouteParams &p, int blocks, cudaStream_t s) {
-    if (p.E <= 128) route_choose_kernel<4, ONE><<<blocks, kRouteThreads, 0, s>>>(p);
-    else if (p.E <= 256) route_choose_kernel<8, ONE><<<blocks, kRouteThreads, 0, s>>>(p);
-    else if (p.E <= 512) route_choose_kernel<16, ONE><<<blocks, kRouteThreads, 0, s>>>(p);
-    else route_choose_kernel<32, ONE><<<blocks, kRouteThreads, 0, s>>>(p);
+void choose(const RouteParams &p, int dtype, int blocks, cudaStream_t s) {
+    if (dtype == CSF_BF16) choose_type<__nv_bfloat16, ONE>(p, blocks, s);
+    else if (dtype == CSF_F16) choose_type<__half, ONE>(p, blocks, s);
+    else choose_type<float, ONE>(p, blocks, s);
 }
 
 }  // namespace
@@ -265,7 +290,6 @@ extern "C" csf_status csf_route(const csf_route_args *a, void *stream) {
     RouteParams p;
     p.logits = a->logits;
     p.stride = a->logits_stride;
-    p.dtype = a->dtype;
     p.T = a->tokens;
     p.E = a->experts;
     p.k = a->k;
@@ -281,9 +305,9 @@ extern "C" csf_status csf_route(const csf_route_args *a, void *stream) {
     if (p.T == 0) {
         route_none_kernel<<<1, 256, 0, s>>>(p.start, p.E);
     } else if (blocks == 1) {
-        choose<true>(p, 1, s);
+        choose<true>(p, a->dtype, 1, s);
     } else {
-        choose<false>(p, blocks, s);
+        choose<false>(p, a->dtype, blocks, s);
         route_scan_kernel<<<(p.E + 31) / 32, 1024, 0, s>>>(p, blocks);
         route_place_kernel<<<blocks, kRouteThreads, 0, s>>>(p);
     }
