@@ -157,20 +157,37 @@ extern "C" csf_status csf_expert_matmul(const csf_expert_matmul_args *a, void *s
     // average: a dense 8191-slot product takes 79 us in wide tiles and 94 in
     // narrow ones, 512 experts of 64 slots 138 and 119.
     const int64_t mean = a->slots / std::min<int64_t>(E, a->slots);
-    const int shape = a->gated ? kGated : mean > tile_slots(kNarrow) ? kWide : kNarrow;
+    int shape = a->gated ? kGated : mean > tile_slots(kNarrow) ? kWide : kNarrow;
     p.nt = (int)std::min<int64_t>(tile_slots(shape), round_up(a->slots, kXBox));
+    const int64_t busy = std::min<int64_t>(E, a->slots);      // experts with slots, at most
+    int64_t most_tiles = (int64_t)p.row_tiles * (busy + a->slots / p.nt);
+    const int sms = sm_count();
+    // Few tiles of a long K: clusters share them.  That costs 1.3 us and a
+    // stage takes 0.2, so K has 16 stages at least and a part 5; and clusters
+    // of half the SMs' blocks are placed at once, of more in turns.  One slot
+    // of a 5120-deep MXFP4 product, 1 / 2 / 4 / 8 blocks a tile: 14.1 / 11.0 /
+    // 9.2 / 15.9 us with 2048 rows (8: 128 blocks), 14.2 / 11.0 / 9.1 / 8.5
+    // with 256; of a 1280-deep one 7.3 / 7.9.
+    p.split = 1;
+    const int64_t small_tiles = (int64_t)p.row_tiles * (busy + a->slots / kSplitSlots);
+    const int units = (p.ncb + 3) / 4, steps = nv ? units : p.ncb;
+    while (p.split < kMaxSplit && steps >= 16 && small_tiles * p.split * 2 <= sms / 2 && steps >= 5 * p.split * 2 && units >= p.split * 2)
+        p.split *= 2;
+    if (p.split > 1) {
+        shape = a->gated ? kGatedShared : kNarrowShared;
+        p.nt = kSplitSlots;
+        most_tiles = small_tiles;
+    }
+    p.b_rows = std::max(p.nt, kXBox);
     const uint32_t sf = nv ? 2048u : 512u;
-    p.stage_bytes = (uint32_t)round_up(at * 16384 + p.nt * 128 + (at + (p.nt + 127) / 128) * sf, 1024);
-    const int fixed = 1024 + 8 * (E + 1) + 16;
-    const int fixed_static = sizeof(Shared) + sizeof(float) * kEpiWarps * 16 * kTurnStride;
-    const int room = kSmemLimit - (int)round_up(fixed_static, 1024) - fixed;
+    p.stage_bytes = (uint32_t)round_up(at * 16384 + p.b_rows * 128 + (at + (p.nt + 127) / 128) * sf, 1024);
+    const int fixed = 1024 + 8 * (E + 1) + 32 + (p.split - 1) * at * kSplitSlots * 128 * 4;
+    const int room = kSmemLimit - (int)round_up(sizeof(Shared) + sizeof(float) * kEpiWarps * 16 * kTurnStride, 1024) - fixed;
     p.stages = std::min<int>(kMaxStages, room / (int)p.stage_bytes);
     // never two blocks on an SM: each holds the whole tensor memory
     const int smem = std::max(fixed + p.stages * (int)p.stage_bytes, 120 * 1024);
 
-    const int64_t most_tiles = (int64_t)p.row_tiles * (std::min<int64_t>(E, a->slots) + a->slots / p.nt);
     if (most_tiles >= (1ll << 31)) return CSF_ERR_UNSUPPORTED;
-    const int sms = sm_count();
     EncodeFn encode = encode_fn();
     if (sms < 1 || !encode) return CSF_ERR_CUDA;
 
@@ -198,8 +215,22 @@ extern "C" csf_status csf_expert_matmul(const csf_expert_matmul_args *a, void *s
     const bool res = a->residual || a->row_scale;
     Kernel k = nv ? nvfp4_kernel(out, shape, res) : mxfp8_kernel(out, shape, res);
     if (!allow_smem(reinterpret_cast<const void *>(k))) return CSF_ERR_CUDA;
-    const int grid = (int)std::min<int64_t>(sms, most_tiles);
-    k<<<grid, kMmThreads, smem, static_cast<cudaStream_t>(stream)>>>(wmap, xmap, p);
-    if (cudaGetLastError() != cudaSuccess) return CSF_ERR_CUDA;
+    cudaLaunchConfig_t config = {};
+    config.gridDim = dim3((unsigned)(p.split > 1 ? most_tiles * p.split : std::min<int64_t>(sms, most_tiles)));
+    config.blockDim = dim3(kMmThreads);
+    config.dynamicSmemBytes = (size_t)smem;
+    config.stream = static_cast<cudaStream_t>(stream);
+    cudaLaunchAttribute cluster;
+    if (p.split > 1) {
+        cluster.id = cudaLaunchAttributeClusterDimension;
+        cluster.val.clusterDim.x = (unsigned)p.split;
+        cluster.val.clusterDim.y = cluster.val.clusterDim.z = 1;
+        config.attrs = &cluster;
+        config.numAttrs = 1;
+    }
+    if (cudaLaunchKernelEx(&config, k, wmap, xmap, p) != cudaSuccess) {
+        cudaGetLastError();
+        return CSF_ERR_CUDA;
+    }
     return CSF_OK;
 }

@@ -27,6 +27,10 @@
 // products.  A gated product holds two accumulators: row tile t of the gate
 // half and of the up half, from the same x rows.
 //
+// Where few slots make few tiles, a cluster of 2 to 8 blocks shares a tile:
+// each sums its part of K, the others send their sums to the first block's
+// shared memory, which adds them in order and runs the epilogue.
+//
 // The epilogue reads an accumulator a weight row a lane, 8 or 16 slots at a time,
 // applies what belongs to the row (alpha, bias, activation), and turns the
 // piece around in shared memory, so that a lane then holds 8 columns
@@ -85,6 +89,8 @@ struct MmParams {
     int32_t stages;
     uint32_t stage_bytes;
     int32_t act, bias_dtype, residual_dtype;
+    int32_t split;               // blocks of a cluster that share a tile's K
+    int32_t b_rows;              // x rows of a stage
     int32_t x_tma;               // x rows through TMA
     int32_t out_wide, residual_wide;   // 16-byte accesses allowed
 };
@@ -268,12 +274,16 @@ struct Ring {
 };
 
 constexpr int kMaxTileSlots = 224;
-__host__ __device__ constexpr int tile_slots(int shape) { return shape == 0 ? 128 : shape == 1 ? kMaxTileSlots : 96; }
+__host__ __device__ constexpr int tile_slots(int shape) {
+    return shape == 1 ? kMaxTileSlots : shape == 0 || shape == 3 ? 128 : 96;
+}
+constexpr int kSplitSlots = 16;      // slots of a tile that a cluster shares
+constexpr int kMaxSplit = 8;
 constexpr int kTileRing = 4;         // tiles that the roles may be apart
 constexpr int kTileUsers = 3 + kXWarps + kEpiWarps;
 
 struct Shared {
-    uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2], tile_full[kTileRing], tile_empty[kTileRing];
+    uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2], tile_full[kTileRing], tile_empty[kTileRing], sums_full;
     Tile tile[kTileRing];                        // n = 0: no more
     int32_t x_row[kTileRing][kMaxTileSlots];
     uint32_t tmem, abort, warp_sum[kMmThreads / 32];
@@ -281,8 +291,9 @@ struct Shared {
 
 // What a tile spans: 128 weight rows and up to 128 or 224 slots, or 128 gate
 // rows, their 128 up rows and up to 96 slots.  (Tensor memory holds two sets
-// of accumulators and the scales.)
-enum Shape { kNarrow = 0, kWide = 1, kGated = 2 };
+// of accumulators and the scales.)  The shared ones are the narrow and the
+// gated tile with K spread over a cluster.
+enum Shape { kNarrow = 0, kWide = 1, kGated = 2, kNarrowShared = 3, kGatedShared = 4 };
 
 // KIND: csf_rows_kind of x.  RES: there is a residual or a row weight.
 template <int KIND, int SHAPE, bool RES, int OUT>
@@ -292,7 +303,7 @@ expert_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_cons
     extern __shared__ __align__(1024) uint8_t dyn[];
     __shared__ Shared sh;
     __shared__ __align__(16) float turn[kEpiWarps][16 * kTurnStride];
-    constexpr bool GATED = SHAPE == kGated;
+    constexpr bool GATED = SHAPE == kGated || SHAPE == kGatedShared, SHARED = SHAPE >= kNarrowShared;
     constexpr int AT = GATED ? 2 : 1;                     // 128-row weight tiles per tile
     constexpr bool kNv = KIND == CSF_ROWS_NVFP4;
     constexpr int kStepK = kNv ? 256 : 128;               // elements per stage: 128 bytes of codes a row
@@ -312,8 +323,11 @@ expert_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_cons
     uint32_t *first = reinterpret_cast<uint32_t *>(dyn + (ring0 - tc::smem_u32(dyn)) + (size_t)p.stages * p.stage_bytes);
 
     uint32_t *slot0 = first + p.E + 1;          // an expert's first slot
+    // the other blocks' sums of a shared tile: [block][weight tile][slot][row]
+    float *sums = reinterpret_cast<float *>(first + ((2 * p.E + 2 + 3) & ~3));
+    const uint32_t rank = SHARED ? tc::cluster_rank() : 0, split = SHARED ? (uint32_t)p.split : 1;
 
-    const uint32_t b_off = AT * kABytes, sfa_off = b_off + (uint32_t)p.nt * 128u,
+    const uint32_t b_off = AT * kABytes, sfa_off = b_off + (uint32_t)p.b_rows * 128u,
                    sfb_off = sfa_off + AT * kTilesPerStage * 512u;
     const uint32_t full0 = tc::smem_u32(sh.full), empty0 = tc::smem_u32(sh.empty);
     const uint32_t accf0 = tc::smem_u32(sh.acc_full), acce0 = tc::smem_u32(sh.acc_empty);
@@ -332,6 +346,7 @@ expert_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_cons
             tc::bar_init(tilef0 + 8 * i, 1);
             tc::bar_init(tilee0 + 8 * i, p.x_tma ? kTileUsers - (kXWarps - 1) : kTileUsers);
         }
+        tc::bar_init(tc::smem_u32(&sh.sums_full), SHARED ? (split - 1) * 32u * kEpiWarps : 1);
         sh.abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -375,10 +390,19 @@ expert_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_cons
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
-    const uint32_t total = first[p.E] * (uint32_t)p.row_tiles;
+    uint32_t total = first[p.E] * (uint32_t)p.row_tiles;
+    // one tile a cluster at most (a corrupt expert_start may ask for more)
+    if constexpr (SHARED) total = min(total, gridDim.x / split);
     const uint32_t tmem = sh.tmem;
     volatile uint32_t *abort = &sh.abort;
-    const int ksteps = (p.K + kStepK - 1) / kStepK;
+    // this block's part of K, in whole 16-byte units of x scales
+    constexpr int kStagesPer16 = 4 / kTilesPerStage;
+    const int all_units = (p.ncb + 3) / 4, all_steps = (p.K + kStepK - 1) / kStepK;
+    const int unit0 = (int)(rank * (uint32_t)all_units / split), unit1 = (int)((rank + 1) * (uint32_t)all_units / split);
+    const int k0 = unit0 * kStagesPer16, ksteps = min(all_steps, unit1 * kStagesPer16) - k0;
+    const int left0 = p.ncb - k0 * kTilesPerStage;      // scale tiles from there on
+    const uint32_t tile0 = blockIdx.x / split, tile_step = gridDim.x / split;
+    if constexpr (SHARED) tc::cluster_sync();           // the barriers of the first block are set up
 
     // Roles that take tiles: wait for the next one's description; done with
     // it, one lane of each says so.
@@ -396,7 +420,7 @@ expert_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_cons
         // ---- tiles and their x rows ----
         Ring tr;
         bool bad_row = false;
-        for (uint32_t tile = blockIdx.x;; tile += gridDim.x) {
+        for (uint32_t tile = tile0;; tile += tile_step) {
             Tile t = {};
             if (tile < total) t = find_tile(p, first, slot0, tile, lane);
             if (!__all_sync(0xFFFFFFFFu, tc::bar_wait(tilee0 + 8 * tr.s, tr.parity ^ 1u, abort))) break;
@@ -424,8 +448,8 @@ expert_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_cons
             while (ok && take(tr, t)) {
                 done_with(tr);
                 const int row = t.rt * 128;
-                const uint8_t *sf = p.w_scales + (int64_t)t.e * p.w_scale_expert + (int64_t)t.rt * p.ncb * 512;
-                int left = p.ncb;
+                const uint8_t *sf = p.w_scales + (int64_t)t.e * p.w_scale_expert + ((int64_t)t.rt * p.ncb + k0 * kTilesPerStage) * 512;
+                int left = left0;
                 for (int k = 0; k < ksteps; ++k, left -= kTilesPerStage, sf += kTilesPerStage * 512, ring.next(p.stages)) {
                     ok = tc::bar_wait(empty0 + 8 * ring.s, ring.parity ^ 1u, abort);
                     if (!ok) break;
@@ -434,7 +458,7 @@ expert_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_cons
                     tc::bar_expect(bar, (uint32_t)AT * (kACopied + bytes));
 #pragma unroll
                     for (int a = 0; a < AT; ++a) {
-                        tc::tma_load_3d(base + a * kABytes, &wmap, kNv ? k * 128 : k * kStepK, row + a * p.second, t.e, bar);
+                        tc::tma_load_3d(base + a * kABytes, &wmap, (k0 + k) * (kNv ? 128 : kStepK), row + a * p.second, t.e, bar);
                         tc::bulk_load(base + sfa_off + a * kTilesPerStage * 512u, sf + (int64_t)a * (p.second >> 7) * p.ncb * 512, bytes, bar);
                     }
                 }
@@ -455,7 +479,7 @@ expert_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_cons
                         if (!ok) break;
                         const uint32_t base = ring0 + ring.s * p.stage_bytes + b_off, bar = full0 + 8 * ring.s;
                         tc::bar_expect(bar, (uint32_t)((t.n + kXBox - 1) / kXBox) * (kXBox * 128u));
-                        for (int c = 0; c < t.n; c += kXBox) tc::tma_load_2d(base + c * 128u, &xmap, k * 128, (int)t.slot + c, bar);
+                        for (int c = 0; c < t.n; c += kXBox) tc::tma_load_2d(base + c * 128u, &xmap, (k0 + k) * 128, (int)t.slot + c, bar);
                     }
                 }
             }
@@ -468,6 +492,7 @@ expert_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_cons
         // row r's 16-byte piece q lies at piece q ^ (r % 8) of its 128 bytes
         const uint32_t b_dst = b_off + (uint32_t)(4 * xw + sub) * 128u + (((uint32_t)piece ^ r8) << 4);
         constexpr int kCopies = kAccCols / 16;
+        const int at0 = k0 * 128 + 16 * piece;
         Ring ring, tr;
         Tile t;
         bool ok = true;
@@ -475,12 +500,12 @@ expert_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_cons
             const uint8_t *src[kCopies];
 #pragma unroll
             for (int j = 0; j < kCopies; ++j)
-                src[j] = p.x_codes + (16 * j < t.n ? sh.x_row[tr.s][16 * j + 4 * xw + sub] * p.x_code_stride : 0) + 16 * piece;
+                src[j] = p.x_codes + (16 * j < t.n ? sh.x_row[tr.s][16 * j + 4 * xw + sub] * p.x_code_stride : 0) + at0;
             __syncwarp();
             if (lane == 0) tc::bar_arrive(tilee0 + 8 * tr.s);
             tr.next(kTileRing);
             const int copies = (t.n + 15) >> 4;
-            int at = 16 * piece;
+            int at = at0;
             for (int k = 0; k < ksteps; ++k, at += 128, ring.next(p.stages)) {
                 ok = __all_sync(0xFFFFFFFFu, tc::bar_wait(empty0 + 8 * ring.s, ring.parity ^ 1u, abort));
                 if (!ok) break;
@@ -499,8 +524,8 @@ expert_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_cons
         // ---- scales of the x rows ----
         // Row lane + 32 j; 16 bytes are four scale tiles: a unit of one stage
         // (NVFP4) or four (MXFP8).  Two units, across tiles, are under way.
-        constexpr int kRows = (kAccCols + 31) / 32, kStagesPer16 = 4 / kTilesPerStage;
-        const int units = (p.ncb + 3) / 4;
+        constexpr int kRows = (kAccCols + 31) / 32;
+        const int units = unit1 - unit0;
         struct Unit {
             uint4 v[kRows];
             int n, stages;      // slots (0: no more tiles), stages it serves
@@ -515,7 +540,7 @@ expert_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_cons
 #pragma unroll
             for (int j = 0; j < kRows; ++j) {
                 const int c = 32 * j + lane;
-                src[j] = reinterpret_cast<const uint4 *>(p.x_scales + (c < t.n ? sh.x_row[tr.s][c] * p.x_scale_stride : 0));
+                src[j] = reinterpret_cast<const uint4 *>(p.x_scales + (c < t.n ? sh.x_row[tr.s][c] * p.x_scale_stride : 0)) + unit0;
             }
             __syncwarp();
             if (lane == 0) tc::bar_arrive(tilee0 + 8 * tr.s);
@@ -604,7 +629,7 @@ expert_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_cons
                 ok = tc::bar_wait(acce0 + 8 * set, aph ^ 1u, abort);
                 tc::fence_after();
                 const uint32_t d0 = tmem + set * (AT * kAccCols);
-                int left = p.ncb;
+                int left = left0;
                 for (int k = 0; ok && k < ksteps; ++k, left -= kTilesPerStage, ring.next(p.stages)) {
                     ok = tc::bar_wait(full0 + 8 * ring.s, ring.parity, abort);
                     if (!ok) break;
@@ -672,8 +697,28 @@ expert_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_cons
             uint32_t bias[AT];      // as stored
         };
         Ring tr;
+        if (SHARED && rank > 0) {
+            // Not the tile's first block: its sums go there.  (Each cluster
+            // has one tile at most.)
+            Tile t;
+            if (__all_sync(0xFFFFFFFFu, take(tr, t)) && __all_sync(0xFFFFFFFFu, tc::bar_wait(accf0, 0, abort))) {
+                tc::fence_after();
+                const uint32_t d = tmem + ((uint32_t)(32 * w) << 16) + 8 * half;
+#pragma unroll
+                for (int a = 0; a < AT; ++a) {
+                    float acc[8];
+                    tc::tmem_load(d + a * kAccCols, acc);
+                    tc::wait_ld();
+                    float *at = sums + (((rank - 1) * AT + a) * kSplitSlots + 8 * half) * 128 + 32 * w + lane;
+                    const uint32_t to = tc::in_block(tc::smem_u32(at), 0);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) tc::store_cluster(to + j * 512u, acc[j]);
+                }
+                tc::bar_arrive_cluster(tc::in_block(tc::smem_u32(&sh.sums_full), 0));
+            }
+        }
         auto open = [&](Head &h) {
-            if (!__all_sync(0xFFFFFFFFu, take(tr, h.t))) {
+            if ((SHARED && rank > 0) || !__all_sync(0xFFFFFFFFu, take(tr, h.t))) {
                 h.t.n = 0;
                 return;
             }
@@ -732,6 +777,16 @@ expert_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_cons
 #pragma unroll
                 for (int a = 0; a < AT; ++a) tc::tmem_load(d + a * kAccCols, acc[a]);
                 tc::wait_ld();
+                if constexpr (SHARED) {
+                    if (!__all_sync(0xFFFFFFFFu, tc::bar_wait<true>(tc::smem_u32(&sh.sums_full), 0, abort))) break;
+                    for (uint32_t r = 0; r + 1 < split; ++r) {
+#pragma unroll
+                        for (int a = 0; a < AT; ++a)
+#pragma unroll
+                            for (int j = 0; j < 8 * G; ++j)
+                                acc[a][j] += sums[((r * AT + a) * kSplitSlots + c + j) * 128 + 32 * w + lane];
+                    }
+                }
                 if (c + 16 * G >= t.n) {
                     tc::fence_before();
                     tc::bar_arrive(acce0 + 8 * set);
@@ -787,6 +842,7 @@ expert_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_cons
         while (tc::timer_ns() - t0 < 5000000ull) __nanosleep(1000);
         __syncthreads();
     }
+    if constexpr (SHARED) tc::cluster_sync();      // nothing is under way to a block that leaves
     if (warp == 1) tc::tmem_free(tmem, kTmemCols);
 }
 
@@ -797,7 +853,10 @@ Kernel pick(int shape, bool res) {
     switch (shape) {
         case kNarrow: return res ? expert_matmul_kernel<KIND, kNarrow, true, OUT> : expert_matmul_kernel<KIND, kNarrow, false, OUT>;
         case kWide: return res ? expert_matmul_kernel<KIND, kWide, true, OUT> : expert_matmul_kernel<KIND, kWide, false, OUT>;
-        default: return res ? expert_matmul_kernel<KIND, kGated, true, OUT> : expert_matmul_kernel<KIND, kGated, false, OUT>;
+        case kGated: return res ? expert_matmul_kernel<KIND, kGated, true, OUT> : expert_matmul_kernel<KIND, kGated, false, OUT>;
+        // for these the residual is asked for at run time: their epilogues are short
+        case kNarrowShared: return expert_matmul_kernel<KIND, kNarrowShared, true, OUT>;
+        default: return expert_matmul_kernel<KIND, kGatedShared, true, OUT>;
     }
 }
 

@@ -52,16 +52,30 @@ __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
     return done != 0;
 }
 
+// The same for a barrier that other blocks of the cluster arrive on: what they
+// wrote before is visible after.
+__device__ __forceinline__ bool bar_try_cluster(uint32_t bar, uint32_t parity) {
+    uint32_t done;
+    asm volatile(
+        "{\n .reg .pred p;\n"
+        " mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+        " selp.u32 %0, 1, 0, p;\n}"
+        : "=r"(done)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return done != 0;
+}
+
 constexpr uint64_t kWaitLimitNs = 2000000000ull;   // a wait that lasts this long gives up
 
 // Wait for a phase, or give up: after the limit, or once another thread of
 // the block gave up (*abort).  A false return means the caller stops.
+template <bool CLUSTER = false>
 __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile uint32_t *abort) {
-    if (bar_try(bar, parity)) return true;
     uint64_t t0 = 0;
-    for (uint32_t i = 1;; ++i) {
-        if (bar_try(bar, parity)) return true;
-        if ((i & 63u) == 0) {
+    for (uint32_t i = 0;; ++i) {
+        if (CLUSTER ? bar_try_cluster(bar, parity) : bar_try(bar, parity)) return true;
+        if ((i & 63u) == 63u) {
             if (*abort) return false;
             const uint64_t t = timer_ns();
             if (t0 == 0) t0 = t;
@@ -71,6 +85,34 @@ __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile
             }
         }
     }
+}
+
+// ---- clusters -----------------------------------------------------------------------------------------------------
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+
+// Every thread of every block of the cluster.
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// A shared-memory address of this block, in the block of that rank.
+__device__ __forceinline__ uint32_t in_block(uint32_t addr, uint32_t rank) {
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+
+__device__ __forceinline__ void store_cluster(uint32_t dst, float v) {
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(dst), "f"(v) : "memory");
+}
+
+__device__ __forceinline__ void bar_arrive_cluster(uint32_t bar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
 // ---- copies -------------------------------------------------------------------------------------------------------

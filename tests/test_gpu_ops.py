@@ -382,6 +382,22 @@ def test_matmul_epilogue(ops, act, gated, out, kind):
 
 
 @pytest.mark.parametrize("kind", [0, 1])
+@pytest.mark.parametrize("counts,N,K,gather", [([1], 256, 5120, 0), ([1], 2048, 5120, 0), ([16], 256, 1664, 3), ([17], 512, 2048, 0),
+                                               ([2, 0, 9], 256, 2176, 4), ([1] * 8, 256, 1664, 1), ([100], 256, 4096, 0)])
+def test_matmul_of_few_slots_with_k_shared_by_clusters(ops, counts, N, K, gather, kind):
+    q = Problem(ops, kind, counts, N, K, seed=15, gather=gather)
+    bias, residual = torch.randn(q.E, N, **q.dev), torch.randn(q.S, N, **q.dev)
+    q.check(q.run(out=F32, alpha=q.alpha, bias=bias), alpha=q.alpha, bias=bias)
+    q.check(q.run(out=BF16, alpha=q.alpha, residual=residual), alpha=q.alpha, residual=residual)
+    q.check(q.run(out=F32, alpha=q.alpha, activation="silu", gated=True), act="silu", gated=True, alpha=q.alpha)
+    first = q.run(out=ops.MXFP8)
+    q.check(first)
+    for _ in range(3):
+        again = q.run(out=ops.MXFP8)
+        assert torch.equal(first.codes, again.codes) and torch.equal(first.scales, again.scales)
+
+
+@pytest.mark.parametrize("kind", [0, 1])
 @pytest.mark.parametrize("N", [33, 64, 250])
 def test_matmul_ragged_quantized_outputs(ops, N, kind):
     q = Problem(ops, kind, [5, 70], N, 256, seed=4)
