@@ -3,8 +3,7 @@
 //
 // Tokens are taken 64 at a time by a block, one token a warp: the row's
 // logits sit in registers as order-preserving integers and each of the k
-// choices is one warp maximum and one warp minimum over the experts that hold
-// it.  A token picks an expert at most once, so a 64-bit mask per expert holds
+// choices is one or two warp reductions.  A token picks an expert at most once, so a 64-bit mask per expert holds
 // a block's choices: its population is the block's count and the bits below a
 // token its rank, whatever the order of the updates -- the slots depend on the
 // logits alone.  Up to 64 tokens one block does everything; else a scan over
@@ -30,19 +29,39 @@ struct RouteParams {
     uint32_t *totals;    // [E]
 };
 
-// Larger logit, larger key; -inf (an expert switched off) has key 0, NaN the largest.
-__device__ __forceinline__ uint32_t key_of(float v) {
-    const uint32_t b = __float_as_uint(v + 0.f);      // -0 becomes 0
-    if ((b & 0x7FFFFFFFu) > 0x7F800000u) return 0xFFFFFFFFu;
-    if (b == 0xFF800000u) return 0;
-    return b ^ ((b >> 31) ? 0xFFFFFFFFu : 0x80000000u);
-}
-
-__device__ __forceinline__ float value_of(uint32_t key) {
-    if (key == 0xFFFFFFFFu) return __uint_as_float(0x7FC00000u);
-    if (key == 0) return __uint_as_float(0xFF800000u);
-    return __uint_as_float(key ^ ((key >> 31) ? 0x80000000u : 0xFFFFFFFFu));
-}
+// Order-preserving integers of logits: larger logit, larger rank; -0 as 0; NaN
+// above every number; ranks up to `off` are -inf, an expert switched off.
+template <typename T> struct Rank;
+template <> struct Rank<float> {
+    static constexpr uint32_t off = 0;
+    static __device__ __forceinline__ uint32_t of(float v) {
+        const uint32_t b = __float_as_uint(v + 0.f);
+        if ((b & 0x7FFFFFFFu) > 0x7F800000u) return 0xFFFFFFFFu;
+        if (b == 0xFF800000u) return 0;
+        return b ^ ((b >> 31) ? 0xFFFFFFFFu : 0x80000000u);
+    }
+    static __device__ __forceinline__ float value(uint32_t r) {
+        if (r == 0xFFFFFFFFu) return __uint_as_float(0x7FC00000u);
+        return __uint_as_float(r ^ ((r >> 31) ? 0x80000000u : 0xFFFFFFFFu));
+    }
+};
+// 16-bit types: a rank in 16 bits, INF the bits of infinity.
+template <uint32_t INF>
+struct Rank16 {
+    static constexpr uint32_t off = 0xFFFFu ^ (INF | 0x8000u);
+    static __device__ __forceinline__ uint32_t of(uint32_t b) {
+        if ((b & 0x7FFFu) > INF) return 0xFFFFu;
+        if (b == 0x8000u) b = 0;
+        return b & 0x8000u ? b ^ 0xFFFFu : b | 0x8000u;
+    }
+    static __device__ __forceinline__ uint32_t bits(uint32_t r) { return r & 0x8000u ? r ^ 0x8000u : r ^ 0xFFFFu; }
+};
+template <> struct Rank<__nv_bfloat16> : Rank16<0x7F80u> {
+    static __device__ __forceinline__ float value(uint32_t r) { return __uint_as_float(bits(r) << 16); }
+};
+template <> struct Rank<__half> : Rank16<0x7C00u> {
+    static __device__ __forceinline__ float value(uint32_t r) { return __half2float(__ushort_as_half((unsigned short)bits(r))); }
+};
 
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
@@ -78,8 +97,83 @@ __device__ __forceinline__ void scan_experts(const uint32_t *cnt, uint32_t *out,
     __syncthreads();
 }
 
-// VPL: logits per lane (E <= 32 * VPL).  ONE: the only block, which also
-// places the slots.
+// A warp's choice among E logits, VPL a lane (E <= 32 * VPL): lane c gets the
+// c-th best's expert and rank.  Each lane keeps the two best of its own (eight
+// choices of hundreds seldom take a lane's third; only then are its logits
+// gone through again).  16-bit ranks carry the expert in their low half, ties
+// to the lower one, so that a choice is one warp maximum; 32-bit ones take a
+// second reduction for the expert.
+template <typename T, int VPL>
+struct Choice {
+    static constexpr bool kPacked = sizeof(T) == 2;
+    uint32_t key[VPL];
+    uint32_t best, second;
+    int best_at, second_at;
+
+    __device__ __forceinline__ static uint32_t rank(uint32_t k) { return kPacked ? k >> 16 : k; }
+
+    __device__ __forceinline__ void set(const T (&raw)[VPL], int E, int lane) {
+#pragma unroll
+        for (int j = 0; j < VPL; ++j) {
+            const int e = lane + 32 * j;
+            if constexpr (kPacked) {
+                uint16_t b;
+                memcpy(&b, &raw[j], 2);
+                key[j] = e < E ? Rank<T>::of(b) << 16 | (0xFFFFu - (uint32_t)e) : 0;
+            } else {
+                key[j] = e < E ? Rank<T>::of(raw[j]) : 0;
+            }
+        }
+    }
+
+    // The two best of the lane below `limit` (packed) or of those left (not).
+    __device__ __forceinline__ void look(uint32_t limit) {
+        best = second = 0;
+        best_at = second_at = 0;
+#pragma unroll
+        for (int j = 0; j < VPL; ++j) {
+            if constexpr (kPacked) {
+                const uint32_t k = key[j] < limit ? key[j] : 0;
+                second = max(second, min(best, k));
+                best = max(best, k);
+            } else {
+                if (key[j] > best) second = best, second_at = best_at, best = key[j], best_at = j;
+                else if (key[j] > second) second = key[j], second_at = j;
+            }
+        }
+    }
+
+    __device__ __forceinline__ void choose(int k, int lane, int &id, uint32_t &mine) {
+        uint32_t taken = 0;
+        bool spare = true;
+        id = -1;
+        mine = 0;
+        for (int c = 0; c < k; ++c) {
+            const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, best);
+            if (rank(top) <= Rank<T>::off) break;      // no expert left
+            uint32_t e;
+            if constexpr (kPacked) e = 0xFFFFu - (top & 0xFFFFu);
+            else e = __reduce_min_sync(0xFFFFFFFFu, best == top ? (uint32_t)(lane + 32 * best_at) : 0xFFFFFFFFu);
+            if (lane == c) id = (int)e, mine = rank(top);
+            if ((e & 31) == (uint32_t)lane) {
+                if constexpr (!kPacked) taken |= 1u << (e >> 5);
+                if (spare) {
+                    best = second, best_at = second_at;
+                } else {
+                    if constexpr (!kPacked) {
+#pragma unroll
+                        for (int j = 0; j < VPL; ++j)
+                            if (taken >> j & 1) key[j] = 0;
+                    }
+                    look(top);
+                }
+                spare = !spare;
+            }
+        }
+    }
+};
+
+// ONE: the only block, which also places the slots.
 template <typename T, int VPL, bool ONE>
 __global__ void __launch_bounds__(kRouteThreads)
 route_choose_kernel(const __grid_constant__ RouteParams p) {
@@ -96,59 +190,25 @@ route_choose_kernel(const __grid_constant__ RouteParams p) {
         const int64_t t = t0 + i;
         const T *row = static_cast<const T *>(p.logits) + t * p.stride;
         T raw[VPL];
-        uint32_t key[VPL];
 #pragma unroll
-        for (int j = 0; j < VPL; ++j) {
-            const int e = lane + 32 * j;
-            raw[j] = e < p.E ? row[e] : T(0.f);
-        }
-#pragma unroll
-        for (int j = 0; j < VPL; ++j) key[j] = lane + 32 * j < p.E ? key_of((float)raw[j]) : 0;
-        // The lane's two best, ties to the lower expert.  Eight choices seldom
-        // take a lane's third: only then are its logits gone through again.
-        uint32_t best, second;
-        int best_at, second_at;
-        auto look = [&]() {
-            best = second = 0;
-            best_at = second_at = 0;
-#pragma unroll
-            for (int j = 0; j < VPL; ++j) {
-                if (key[j] > best) second = best, second_at = best_at, best = key[j], best_at = j;
-                else if (key[j] > second) second = key[j], second_at = j;
-            }
-        };
-        look();
-        const float vmax = value_of(__reduce_max_sync(0xFFFFFFFFu, best));
+        for (int j = 0; j < VPL; ++j) raw[j] = lane + 32 * j < p.E ? row[lane + 32 * j] : T(0.f);
+        Choice<T, VPL> choice;
+        choice.set(raw, p.E, lane);
+        choice.look(0xFFFFFFFFu);
+        const uint32_t top = choice.rank(__reduce_max_sync(0xFFFFFFFFu, choice.best));
+        const bool any = top > Rank<T>::off;
+        const float vmax = Rank<T>::value(top);
         float total = 0.f;
-        if (!p.renormalize) {
+        if (!p.renormalize && any) {
 #pragma unroll
             for (int j = 0; j < VPL; ++j)
-                if (key[j]) total += expf(value_of(key[j]) - vmax);
+                if (choice.rank(choice.key[j]) > Rank<T>::off) total += expf((float)raw[j] - vmax);
             total = warp_sum(total);
         }
-        int id = -1;
-        uint32_t mine = 0, taken = 0;      // this lane's choice; which of its logits are gone
-        int spare = 1;
-        for (int c = 0; c < p.k; ++c) {
-            const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, best);
-            if (top == 0) break;                       // no expert left
-            const uint32_t e = __reduce_min_sync(0xFFFFFFFFu, best == top ? (uint32_t)(lane + 32 * best_at) : 0xFFFFFFFFu);
-            if (lane == c) id = (int)e, mine = top;
-            if ((e & 31) == (uint32_t)lane) {
-                taken |= 1u << (e >> 5);
-                if (spare) {
-                    best = second, best_at = second_at;
-                    spare = 0;
-                } else {
-#pragma unroll
-                    for (int j = 0; j < VPL; ++j)
-                        if (taken >> j & 1) key[j] = 0;
-                    look();
-                    spare = 1;
-                }
-            }
-        }
-        const float w = id < 0 ? 0.f : expf(value_of(mine) - vmax);
+        int id;
+        uint32_t mine;
+        choice.choose(p.k, lane, id, mine);
+        const float w = id < 0 ? 0.f : expf(Rank<T>::value(mine) - vmax);
         if (p.renormalize) total = warp_sum(w);
         if (lane < p.k) {
             p.ids[t * p.k + lane] = id;
@@ -186,35 +246,34 @@ route_choose_kernel(const __grid_constant__ RouteParams p) {
     }
 }
 
-// Exclusive prefix of the blocks' counts per expert, 32 experts a block and
-// one segment of the blocks a warp.
+// Exclusive prefix of the blocks' counts per expert: 8 experts a block (32
+// bytes of a row of counts), 128 segments of the blocks.
 __global__ void __launch_bounds__(1024)
 route_scan_kernel(const __grid_constant__ RouteParams p, int blocks) {
-    __shared__ uint32_t part[32][33];
-    const int lane = threadIdx.x & 31, seg = threadIdx.x >> 5;
-    const int e = blockIdx.x * 32 + lane;
-    const int per = (blocks + 31) / 32, b0 = min(blocks, seg * per), b1 = min(blocks, b0 + per);
+    __shared__ uint32_t part[32][8];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int e = blockIdx.x * 8 + (lane & 7), seg = warp * 4 + (lane >> 3);
+    const int per = (blocks + 127) / 128, b0 = min(blocks, seg * per), b1 = e < p.E ? min(blocks, b0 + per) : b0;
     uint32_t sum = 0;
-    if (e < p.E) {
 #pragma unroll 8
-        for (int b = b0; b < b1; ++b) sum += p.counts[(int64_t)b * p.E + e];
-    }
-    part[seg][lane] = sum;
-    __syncthreads();
-    uint32_t before = 0, total = 0;
+    for (int b = b0; b < b1; ++b) sum += p.counts[(int64_t)b * p.E + e];
+    uint32_t upto = sum;
 #pragma unroll
-    for (int s = 0; s < 32; ++s) {
-        const uint32_t v = part[s][lane];
-        before += s < seg ? v : 0;
-        total += v;
+    for (int d = 8; d < 32; d <<= 1) {
+        const uint32_t o = __shfl_up_sync(0xFFFFFFFFu, upto, d);
+        if (lane >= d) upto += o;
     }
-    if (e < p.E) {
-        if (seg == 0) p.totals[e] = total;
-        for (int b = b0; b < b1; ++b) {
-            const uint32_t c = p.counts[(int64_t)b * p.E + e];
-            p.counts[(int64_t)b * p.E + e] = before;
-            before += c;
-        }
+    if (lane >= 24) part[warp][lane & 7] = upto;
+    __syncthreads();
+    uint32_t before = upto - sum;
+    for (int w = 0; w < warp; ++w) before += part[w][lane & 7];
+    if (seg == 127 && e < p.E) p.totals[e] = before + sum;
+#pragma unroll 4
+    for (int b = b0; b < b1; ++b) {
+        uint32_t *at = p.counts + (int64_t)b * p.E + e;
+        const uint32_t c = *at;
+        *at = before;
+        before += c;
     }
 }
 
@@ -250,6 +309,7 @@ template <typename T, bool ONE>
 void choose_type(const RouteParams &p, int blocks, cudaStream_t s) {
     if (p.E <= 128) route_choose_kernel<T, 4, ONE><<<blocks, kRouteThreads, 0, s>>>(p);
     else if (p.E <= 256) route_choose_kernel<T, 8, ONE><<<blocks, kRouteThreads, 0, s>>>(p);
+    else if (p.E <= 384) route_choose_kernel<T, 12, ONE><<<blocks, kRouteThreads, 0, s>>>(p);
     else if (p.E <= 512) route_choose_kernel<T, 16, ONE><<<blocks, kRouteThreads, 0, s>>>(p);
     else route_choose_kernel<T, 32, ONE><<<blocks, kRouteThreads, 0, s>>>(p);
 }
@@ -308,7 +368,7 @@ extern "C" csf_status csf_route(const csf_route_args *a, void *stream) {
         choose<true>(p, a->dtype, 1, s);
     } else {
         choose<false>(p, a->dtype, blocks, s);
-        route_scan_kernel<<<(p.E + 31) / 32, 1024, 0, s>>>(p, blocks);
+        route_scan_kernel<<<(p.E + 7) / 8, 1024, 0, s>>>(p, blocks);
         route_place_kernel<<<blocks, kRouteThreads, 0, s>>>(p);
     }
     return cudaGetLastError() == cudaSuccess ? CSF_OK : CSF_ERR_CUDA;
