@@ -34,10 +34,24 @@ __device__ __forceinline__ uint32_t nv_scale(uint32_t amax_bits, float six_tenso
     return __nv_cvt_float_to_fp8(__fdiv_rn(__uint_as_float(amax_bits), six_tensor_scales), __NV_SATFINITE, __NV_E4M3);
 }
 
-// 1 / (scale * tensor scale), 0 for a zero scale.
-__device__ __forceinline__ float nv_inverse(uint32_t byte, float tensor_scale) {
+// scale * tensor scale, and its inverse (0 for a zero scale).
+struct Whole {
+    float value, inverse;
+};
+
+__device__ __forceinline__ Whole nv_whole(uint32_t byte, float tensor_scale) {
     const float s = __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)byte, __NV_E4M3)));
-    return s > 0.f ? 1.f / (s * tensor_scale) : 0.f;
+    Whole w;
+    w.value = s * tensor_scale;
+    w.inverse = s > 0.f ? 1.f / w.value : 0.f;
+    return w;
+}
+
+// v / whole: the product with the inverse, corrected by its remainder, so that
+// values next to the middle of two codes round as the quotient does.
+__device__ __forceinline__ float over(float v, const Whole &w) {
+    const float q = v * w.inverse;
+    return fmaf(fmaf(-q, w.value, v), w.inverse, q);
 }
 
 __device__ __forceinline__ uint32_t e4m3(float v) { return __nv_cvt_float_to_fp8(v, __NV_SATFINITE, __NV_E4M3); }
@@ -73,10 +87,10 @@ __device__ __forceinline__ void quantize8(const float (&y)[8], uint8_t *codes, u
         if ((chunk & 3) == 0) scales[chunk >> 2] = (uint8_t)s;
     } else {
         const uint32_t s = nv_scale(m, 6.f * tensor_scale);
-        const float inv = nv_inverse(s, tensor_scale);
+        const Whole w = nv_whole(s, tensor_scale);
         *reinterpret_cast<uint32_t *>(codes + chunk * 4) =
-            e2m1x2(y[0] * inv, y[1] * inv) | e2m1x2(y[2] * inv, y[3] * inv) << 8 |
-            e2m1x2(y[4] * inv, y[5] * inv) << 16 | e2m1x2(y[6] * inv, y[7] * inv) << 24;
+            e2m1x2(over(y[0], w), over(y[1], w)) | e2m1x2(over(y[2], w), over(y[3], w)) << 8 |
+            e2m1x2(over(y[4], w), over(y[5], w)) << 16 | e2m1x2(over(y[6], w), over(y[7], w)) << 24;
         if ((chunk & 1) == 0) scales[chunk >> 1] = (uint8_t)s;
     }
 }
