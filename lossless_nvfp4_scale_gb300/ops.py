@@ -51,6 +51,33 @@ lib.csf_expert_matmul.restype = ctypes.c_int
 _raw_stream = torch._C._cuda_getCurrentRawStream
 
 
+_error_words: dict[int, torch.Tensor] = {}
+
+
+def _error_word(device: int) -> int:
+    """The device's own error word, for calls that bring none."""
+    word = _error_words.get(device)
+    if word is None:
+        if torch.cuda.is_current_stream_capturing():
+            return 0                    # nothing to allocate in a graph
+        word = _error_words[device] = torch.zeros(1, dtype=torch.int32, device=torch.device("cuda", device))
+        torch.cuda.synchronize(device)  # once: any stream may set it from here on
+    return word.data_ptr()
+
+
+def errors(device: int | None = None) -> int:
+    """CSF_DEV_ERR_* bits of the expert_matmul calls on a device that were given
+    no error_word, and clears them.  Synchronises."""
+    device = torch.cuda.current_device() if device is None else device
+    torch.cuda.synchronize(device)
+    word = _error_words.get(device)
+    if word is None:
+        return 0
+    bits = int(word.item())
+    word.zero_()
+    return bits
+
+
 def _on(stream, call, *args, **kwargs):
     """The call with `stream` current, so that what it allocates is the
     stream's own."""
@@ -220,7 +247,8 @@ def expert_matmul(x: Quantized, w: torch.Tensor, w_scales: torch.Tensor, expert_
     one expert owns every slot.  p = alpha[e] * (x . w) + bias[e]; y = act(p),
     or act(p[:N/2]) * p[N/2:] when `gated`; out = y * row_scale[s] + residual.
     `out` is a dtype, a tensor, NVFP4 or MXFP8 (a new Quantized), or a
-    Quantized.  Activations: None, "relu", "silu", "gelu" (tanh form)."""
+    Quantized.  Activations: None, "relu", "silu", "gelu" (tanh form).
+    Data errors reach `error_word` (int32 [1]) or, without one, errors()."""
     if stream is not None:
         return _on(stream, expert_matmul, x, w, w_scales, expert_start, rows, alpha, bias, activation, gated, row_scale,
                    residual, out, out_tensor_scale, error_word)
@@ -263,14 +291,15 @@ def expert_matmul(x: Quantized, w: torch.Tensor, w_scales: torch.Tensor, expert_
     else:
         op, os_ = _matrix(out, "expert_matmul: out", S, F)
         odt, orows = _DTYPES[out.dtype], _NO_ROWS
+    device = w.device.index
     a = _EXPERT_MATMUL.pack(
         *x.fields(), 0 if rows is None else rows.data_ptr(), S, E, N, w.data_ptr(), w_scales.data_ptr(), es or 0, es64,
         _vector(alpha, "expert_matmul: alpha", E, torch.float32),
         0 if bias is None else _vector(bias, "expert_matmul: bias", E * N, bias.dtype), bias_dtype, _ACTS[activation],
         gated, _vector(row_scale, "expert_matmul: row_scale", S, torch.float32), rp, rs,
         0 if residual is None else _DTYPES[residual.dtype], odt, op, os_, *orows,
-        _vector(error_word, "expert_matmul: error_word", 1, torch.int32))
-    status = lib.csf_expert_matmul(a, _raw_stream(w.device.index))
+        _error_word(device) if error_word is None else _vector(error_word, "expert_matmul: error_word", 1, torch.int32))
+    status = lib.csf_expert_matmul(a, _raw_stream(device))
     if status:
         _check(status, "csf_expert_matmul")
     return out

@@ -458,6 +458,17 @@ def test_matmul_reports_bad_indices_and_starts(ops):
         assert out.shape == (13, 64)
 
 
+def test_errors_of_calls_without_an_error_word(ops):
+    from lossless_nvfp4_scale_gb300 import csf
+    q = Problem(ops, ops.NVFP4, [6, 7], 64, 64, seed=8, gather=5)
+    ops.errors()
+    q.run()
+    assert ops.errors() == 0
+    q.rows[2] = 99
+    q.run()
+    assert ops.errors() == csf.DEV_ERR_CORRUPT and ops.errors() == 0
+
+
 def test_matmul_no_slots(ops):
     q = Problem(ops, ops.NVFP4, [0, 0], 64, 64)
     assert q.run().shape == (0, 64)
@@ -550,3 +561,50 @@ def test_binding_refusals(ops):
     with pytest.raises(ops.CsfError, match="tensor scale"):
         ops.rms_norm(torch.zeros(1, 32, device="cuda"), torch.ones(32, device="cuda"), ops.MXFP8,
                      tensor_scale=torch.ones(1, device="cuda"))
+
+
+# ---- offsets past 32 bits --------------------------------------------------------------------------------------------
+
+def test_norm_past_32_bits(ops):
+    rows, cols = 560_000, 4096                                    # 2.29e9 elements
+    x = torch.empty(rows, cols, dtype=BF16, device="cuda")
+    x.normal_(generator=gen(1))
+    w = torch.ones(cols, device="cuda", dtype=BF16)
+    q, _ = ops.rms_norm(x, w, ops.MXFP8)
+    at = torch.tensor([0, 1, 262_143, 524_287, 524_288, rows - 1], device="cuda")
+    part = ops.Quantized(ops.MXFP8, q.codes[at], q.scales[at], cols)
+    check_norm(part, None, x[at], w, None, 1e-6, ops)
+
+
+def test_route_past_32_bits(ops):
+    T, E, k = 2_200_000, 1000, 2                                  # 2.2e9 logits
+    v = torch.empty(T, E, dtype=BF16, device="cuda")
+    v.normal_(generator=gen(2))
+    r = ops.route(v, k)
+    at = torch.tensor([0, 63, 64, 2_147_483, 2_147_484, T - 1], device="cuda")
+    part = torch.sort(v[at].double(), dim=1, descending=True, stable=True).indices[:, :k]
+    assert torch.equal(r.ids[at].long(), part)
+    # every choice has a slot of its expert, and slots are in token order
+    assert int(r.expert_start[-1]) == T * k
+    slots = r.slots.long().view(-1)
+    assert torch.equal(r.rows[slots].long(), torch.arange(T, device="cuda").repeat_interleave(k))
+    assert torch.equal(torch.searchsorted(r.expert_start[1:].long(), slots, right=True), r.ids.long().view(-1))
+    step = r.rows[1:] > r.rows[:-1]
+    first = torch.zeros(T * k, dtype=torch.bool, device="cuda")
+    first[r.expert_start[:-1].long().clamp(max=T * k - 1)] = True
+    assert (step | first[1:]).all()
+
+
+def test_matmul_past_32_bits(ops):
+    S, N, K = 70_000, 40_000, 64                                  # 2.8e9 outputs
+    q = Problem(ops, ops.NVFP4, [4], N, K, seed=20)
+    g = gen(21)
+    codes = torch.randint(0, 256, (S, K // 2), dtype=torch.uint8, device="cuda", generator=g)
+    scales = torch.zeros(S, 16, dtype=torch.uint8, device="cuda")
+    scales[:, :4] = torch.randint(0x20, 0x40, (S, 4), dtype=torch.uint8, device="cuda", generator=g)
+    at = torch.tensor([0, 53_687, 53_688, S - 1], device="cuda")   # 53687.09 rows reach 2^31 outputs
+    codes[at], scales[at] = q.x.codes, q.x.scales
+    residual = torch.empty(S, N, dtype=BF16, device="cuda")
+    residual.normal_(generator=g)
+    out = ops.expert_matmul(ops.Quantized(ops.NVFP4, codes, scales, K), q.w, q.ws, residual=residual)
+    q.check(out[at], residual=residual[at])
