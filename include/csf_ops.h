@@ -116,10 +116,10 @@ typedef struct {
     size_t scratch_bytes;
 } csf_route_args;
 
-/* Scratch bytes of csf_route (0 for up to 64 tokens).  Host only. */
+/* Scratch bytes of csf_route (0 for up to 512 tokens).  Host only. */
 size_t csf_route_scratch_bytes(int32_t tokens, int32_t experts);
 
-/* One launch for up to 64 tokens, else three.  Errors: CSF_ERR_ARG,
+/* One launch for up to 512 tokens, else three.  Errors: CSF_ERR_ARG,
  * CSF_ERR_SIZE (scratch), CSF_ERR_UNSUPPORTED (experts or k beyond the
  * limits), CSF_ERR_CUDA. */
 csf_status csf_route(const csf_route_args *a, void *stream);

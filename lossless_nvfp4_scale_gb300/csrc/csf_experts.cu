@@ -155,7 +155,7 @@ extern "C" csf_status csf_expert_matmul(const csf_expert_matmul_args *a, void *s
     p.row_tiles_magic = (uint32_t)((1ull << 32) / (uint32_t)p.row_tiles + 1);
     // Wide tiles where the experts' slots fill more than a narrow one on
     // average: a dense 8191-slot product takes 79 us in wide tiles and 94 in
-    // narrow ones, 512 experts of 64 slots 138 and 119.
+    // narrow ones, 512 experts of 64 slots (2048 x 800 NVFP4) 138 and 119.
     const int64_t mean = a->slots / std::min<int64_t>(E, a->slots);
     int shape = a->gated ? kGated : mean > tile_slots(kNarrow) ? kWide : kNarrow;
     p.nt = (int)std::min<int64_t>(tile_slots(shape), round_up(a->slots, kXBox));

@@ -111,6 +111,12 @@ __device__ __forceinline__ void store_cluster(uint32_t dst, float v) {
     asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(dst), "f"(v) : "memory");
 }
 
+__device__ __forceinline__ uint32_t load_cluster(uint32_t src) {
+    uint32_t v;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(src) : "memory");
+    return v;
+}
+
 __device__ __forceinline__ void bar_arrive_cluster(uint32_t bar) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }

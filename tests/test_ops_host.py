@@ -103,9 +103,9 @@ def test_route_refusals(ops):
     assert call(logits=258) == ARG                               # float32 off its alignment
     assert call(E=1025, ls=1025) == UNSUPPORTED and call(E=64, ls=64, k=33) == UNSUPPORTED
     assert call(T=1 << 30, k=2) == UNSUPPORTED
-    need = ops.lib.csf_route_scratch_bytes(65, 8)
-    assert ops.lib.csf_route_scratch_bytes(64, 8) == 0 and need >= 3 * 8 * 4
-    assert call(T=65, scratch=0, nbytes=need) == ARG and call(T=65, scratch=256, nbytes=need - 1) == SIZE
+    need = ops.lib.csf_route_scratch_bytes(513, 8)
+    assert ops.lib.csf_route_scratch_bytes(512, 8) == 0 and need >= 10 * 8 * 4
+    assert call(T=513, scratch=0, nbytes=need) == ARG and call(T=513, scratch=256, nbytes=need - 1) == SIZE
 
 
 def test_expert_matmul_refusals(ops):
