@@ -108,12 +108,32 @@ struct MmParams {
 
 enum Out { kOutBf16 = 0, kOutF16 = 1, kOutF32 = 2, kOutNv = 3, kOutMx = 4 };
 
+// v / (1 + exp(-z)), to a few units in the last place: the exponent's product
+// with log2(e) carries its rounding error along, and the quotient its
+// remainder.  (expf and the division cost the dense product 52 us of 130; the
+// approximate forms alone are off by 1e-6 of the value, which shows where the
+// result is rounded to 8 bits.)
+__device__ __forceinline__ float times_sigmoid(float v, float z) {
+    constexpr float kLog2e = 1.4426950408889634f, kRest = (float)(1.4426950408889634 - (double)kLog2e), kLn2 = 0.6931471805599453f;
+    z = fminf(fmaxf(z, -86.f), 86.f);        // past that the quotient is 0 or v
+    const float t = -z * kLog2e;
+    const float rest = fmaf(-z, kLog2e, -t) - z * kRest;
+    float e;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(t));
+    const float d = 1.f + fmaf(e, rest * kLn2, e);
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d));
+    const float q = v * r;
+    // an infinite v has no remainder: itself, or (negative) NaN as inf / inf
+    return fabsf(v) < __int_as_float(0x7F800000) ? fmaf(fmaf(-q, d, v), r, q) : v > 0.f ? v : __int_as_float(0x7FC00000);
+}
+
 template <int ACT>
 __device__ __forceinline__ float activate(float v) {
     if constexpr (ACT == CSF_ACT_RELU) return fmaxf(v, 0.f);
-    if constexpr (ACT == CSF_ACT_SILU) return __fdividef(v, 1.f + __expf(-v));
+    if constexpr (ACT == CSF_ACT_SILU) return times_sigmoid(v, v);
     if constexpr (ACT == CSF_ACT_GELU_TANH)   // v * sigmoid(2 * sqrt(2 / pi) * (v + 0.044715 v^3))
-        return __fdividef(v, 1.f + __expf(-1.5957691216057308f * (v + 0.044715f * v * v * v)));
+        return times_sigmoid(v, 1.5957691216057308f * (v + 0.044715f * v * v * v));
     return v;
 }
 

@@ -220,14 +220,15 @@ def test_route(ops, T, E, k, dtype, renormalize):
     check_route(ops.route(logits, k, renormalize=renormalize), logits, k, renormalize)
 
 
-@pytest.mark.parametrize("T", [40, 200])
-def test_route_ties_masks_and_empty_rows(ops, T):
-    E, k = 40, 6
-    v = torch.randint(-2, 3, (T, E), device="cuda", generator=gen(T)).float()     # many ties
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+@pytest.mark.parametrize("T,E", [(40, 40), (200, 40), (70, 501), (600, 501), (1000, 130)])
+def test_route_ties_masks_and_empty_rows(ops, T, E, dtype):
+    k = 6
+    v = torch.randint(-2, 3, (T, E), device="cuda", generator=gen(T)).to(dtype)   # many ties
     v[::3, 5:] = -math.inf                                                        # fewer experts than k
     v[::7] = -math.inf                                                            # none left
     v[1, 3], v[1, 9] = 0.0, -0.0                                                  # equal zeros
-    v[2, 4] = torch.finfo(F32).min                                                # the lowest number is no mask
+    v[2, 4] = torch.finfo(dtype).min                                               # the lowest number is no mask
     v[2, 5:] = -math.inf
     check_route(ops.route(v, k, renormalize=True), v, k, True)
     r = ops.route(v, k, renormalize=False)
@@ -235,8 +236,11 @@ def test_route_ties_masks_and_empty_rows(ops, T):
     assert (r.weights[::7] == 0).all() and (r.ids[::7] == -1).all() and (r.slots[::7] == -1).all()
 
 
-def test_route_non_finite(ops):
-    v = torch.randn(70, 30, device="cuda", generator=gen(3))
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+def test_route_non_finite(ops, dtype):
+    v = torch.randn(70, 30, device="cuda", generator=gen(3)).to(dtype)
+    v[5, 3], v[6, 3] = -math.nan, math.nan
+    v[5:7].view(torch.int16 if dtype is not F32 else torch.int32)[0, 3] |= -0x8000 if dtype is not F32 else -0x80000000
     v[0, 7] = math.nan
     v[1, 7] = math.inf
     v[66, 2] = math.nan
@@ -245,13 +249,16 @@ def test_route_non_finite(ops):
     assert r.ids[0, 0] == 7 and r.ids[1, 0] == 7 and r.ids[66, :2].tolist() == [2, 9]
     assert torch.isnan(r.weights[0]).all() and torch.isnan(r.weights[66]).all()
     clean = torch.ones(70, dtype=torch.bool, device="cuda")
-    clean[[0, 1, 66]] = False
+    assert r.ids[5, 0] == 3 and r.ids[6, 0] == 3                  # a NaN of either sign
+    clean[[0, 1, 5, 6, 66]] = False
     assert torch.isfinite(r.weights[clean]).all()
 
 
-def test_route_strided_logits_no_tokens_and_repeats(ops):
-    big = torch.randn(300, 150, device="cuda", generator=gen(9))
-    v = big[:, 11:111]
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("width,off", [(150, 11), (151, 10), (152, 16)])
+def test_route_strided_logits_no_tokens_and_repeats(ops, width, off, dtype):
+    big = torch.randn(600, width, device="cuda", generator=gen(9)).to(dtype)
+    v = big[:, off:off + 101]
     a, b = ops.route(v, 5), ops.route(v, 5)
     check_route(a, v, 5, True)
     for f in ("ids", "weights", "expert_start", "rows", "slots"):
@@ -608,3 +615,19 @@ def test_matmul_past_32_bits(ops):
     residual.normal_(generator=g)
     out = ops.expert_matmul(ops.Quantized(ops.NVFP4, codes, scales, K), q.w, q.ws, residual=residual)
     q.check(out[at], residual=residual[at])
+
+
+@pytest.mark.parametrize("act,plus,minus", [(None, math.inf, -math.inf), ("relu", math.inf, 0.0), ("silu", math.inf, math.nan),
+                                            ("gelu", math.inf, math.nan)])
+def test_matmul_infinite_sums(ops, act, plus, minus):
+    """An infinite bias makes its own column what the formula makes of it, large ones saturate the sigmoid."""
+    q = Problem(ops, ops.NVFP4, [5], 64, 64, seed=16)
+    bias = torch.zeros(1, 64, device="cuda")
+    bias[0, 3], bias[0, 4], bias[0, 5], bias[0, 6] = math.inf, -math.inf, 1e30, -1e30
+    out = q.run(out=F32, bias=bias, activation=act)
+    assert (out[:, 3] == plus).all()
+    assert (torch.isnan(out[:, 4]) if math.isnan(minus) else out[:, 4] == minus).all()
+    keep = [i for i in range(64) if i not in (3, 4, 5, 6)]
+    assert torch.isfinite(out[:, keep]).all()
+    assert ((out[:, 5] - 1e30).abs() <= 1e24).all()
+    assert (out[:, 6] == -1e30).all() if act is None else (out[:, 6].abs() <= 1e-5).all()
