@@ -20,7 +20,7 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libcsf.so")
 SOURCES = ["csf_api.cu", "csf_decode.cu", "csf_tiles.cu", "csf_tiled.cu", "csf_prepare.cu",
            "csf_prepare_static.cu", "csf_norm.cu", "csf_route.cu", "csf_experts.cu",
-           "csf_experts_nv.cu", "csf_experts_mx.cu"]
+           "csf_experts_nv.cu", "csf_experts_nv_rows.cu", "csf_experts_mx.cu", "csf_experts_mx_rows.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

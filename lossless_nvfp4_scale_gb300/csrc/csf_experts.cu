@@ -201,8 +201,7 @@ extern "C" csf_status csf_expert_matmul(const csf_expert_matmul_args *a, void *s
                    CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
             return CSF_ERR_CUDA;
     }
-    p.x_tma = !a->rows;
-    if (p.x_tma) {
+    if (!a->rows) {
         const cuuint64_t dims[2] = {(cuuint64_t)(nv ? K / 2 : K), (cuuint64_t)a->x.rows};
         const cuuint64_t strides[1] = {(cuuint64_t)a->x.code_stride};
         const cuuint32_t box[2] = {128, kXBox}, ones[2] = {1, 1};
@@ -213,7 +212,8 @@ extern "C" csf_status csf_expert_matmul(const csf_expert_matmul_args *a, void *s
         xmap = wmap;      // not read
     }
     const bool res = a->residual || a->row_scale;
-    Kernel k = nv ? nvfp4_kernel(out, shape, res) : mxfp8_kernel(out, shape, res);
+    Kernel k = a->rows ? (nv ? nvfp4_rows_kernel(out, shape, res) : mxfp8_rows_kernel(out, shape, res))
+                       : (nv ? nvfp4_kernel(out, shape, res) : mxfp8_kernel(out, shape, res));
     if (!allow_smem(reinterpret_cast<const void *>(k))) return CSF_ERR_CUDA;
     cudaLaunchConfig_t config = {};
     config.gridDim = dim3((unsigned)(p.split > 1 ? most_tiles * p.split : std::min<int64_t>(sms, most_tiles)));

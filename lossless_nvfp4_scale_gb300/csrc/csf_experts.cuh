@@ -16,7 +16,7 @@
 //            swizzled as TMA would, where they are not (TMA's gather of four
 //            rows took 64 cycles a request)
 //   warp 14  the scale bytes of those rows, through registers into the tile
-//            layout
+//            layout (with the copying warps that TMA leaves free)
 //   warp 15  which tile comes next and which x rows it takes, a few tiles ahead
 //   warp 1   scale copies to tensor memory and the matrix instructions
 //   warps 4-11  epilogue
@@ -41,8 +41,8 @@
 // bfloat16 products 1.94 PFLOP/s):
 //   512 experts of 64 slots, 1024 x 1600 NVFP4, gated   88 us, 5.86 TB/s: memory
 //   384 experts of 5, 2048 x 5120 MXFP4, gated         351 us, 6.12 TB/s: memory
-//   512 of 64, 2048 x 800 NVFP4, bias and residual     156 us, 4.85 TB/s: the
-//     epilogue (118 us without a residual) and short K: a tile is 4 stages
+//   512 of 64, 2048 x 800 NVFP4, bias and residual     151 us, 5.02 TB/s: the
+//     epilogue (108 us without a residual) and short K: a tile is 4 stages
 //   8191 slots of one 2048 x 5120 MXFP4                 78 us, 2.2 PFLOP/s:
 //     shared-memory bandwidth (operands in, operands to the tensor cores)
 //   64 slots on 8 of 512, gated                        8.3 us: latency
@@ -102,7 +102,6 @@ struct MmParams {
     int32_t act, bias_dtype, residual_dtype;
     int32_t split;               // blocks of a cluster that share a tile's K
     int32_t b_rows;              // x rows of a stage
-    int32_t x_tma;               // x rows through TMA
     int32_t out_wide, residual_wide;   // 16-byte accesses allowed
 };
 
@@ -128,13 +127,9 @@ __device__ __forceinline__ float times_sigmoid(float v, float z) {
     return fabsf(v) < __int_as_float(0x7F800000) ? fmaf(fmaf(-q, d, v), r, q) : v > 0.f ? v : __int_as_float(0x7FC00000);
 }
 
-template <int ACT>
-__device__ __forceinline__ float activate(float v) {
-    if constexpr (ACT == CSF_ACT_RELU) return fmaxf(v, 0.f);
-    if constexpr (ACT == CSF_ACT_SILU) return times_sigmoid(v, v);
-    if constexpr (ACT == CSF_ACT_GELU_TANH)   // v * sigmoid(2 * sqrt(2 / pi) * (v + 0.044715 v^3))
-        return times_sigmoid(v, 1.5957691216057308f * (v + 0.044715f * v * v * v));
-    return v;
+// v * sigmoid(2 * sqrt(2 / pi) * (v + 0.044715 v^3)) is the tanh form of GELU.
+__device__ __forceinline__ float smooth(float v, bool gelu) {
+    return times_sigmoid(v, gelu ? 1.5957691216057308f * (v + 0.044715f * v * v * v) : v);
 }
 
 __device__ __forceinline__ int64_t start_at(const MmParams &p, int e) {
@@ -311,7 +306,6 @@ __host__ __device__ constexpr int tile_slots(int shape) {
 constexpr int kSplitSlots = 16;      // slots of a tile that a cluster shares
 constexpr int kMaxSplit = 8;
 constexpr int kTileRing = 4;         // tiles that the roles may be apart
-constexpr int kTileUsers = 3 + kXWarps + kEpiWarps;
 
 struct Shared {
     uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2], tile_full[kTileRing], tile_empty[kTileRing], sums_full;
@@ -326,8 +320,11 @@ struct Shared {
 // gated tile with K spread over a cluster.
 enum Shape { kNarrow = 0, kWide = 1, kGated = 2, kNarrowShared = 3, kGatedShared = 4 };
 
-// KIND: csf_rows_kind of x.  RES: there is a residual or a row weight.
-template <int KIND, int SHAPE, bool RES, int OUT>
+// KIND: csf_rows_kind of x.  ROWS: slot s reads row rows[s] of x, else row s.
+// RES: there is a residual or a row weight.  (Each is a kernel of its own
+// because the roles' loops share an instruction cache: what is not run should
+// not lie between them.)
+template <int KIND, bool ROWS, int SHAPE, bool RES, int OUT>
 __global__ void __launch_bounds__(kMmThreads, 1)
 expert_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
                      const __grid_constant__ MmParams p) {
@@ -337,6 +334,9 @@ expert_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_cons
     constexpr bool GATED = SHAPE == kGated || SHAPE == kGatedShared, SHARED = SHAPE >= kNarrowShared;
     constexpr int AT = GATED ? 2 : 1;                     // 128-row weight tiles per tile
     constexpr bool kNv = KIND == CSF_ROWS_NVFP4;
+    constexpr int kScaleWarps = ROWS || RES ? 1 : kXWarps;   // warps that bring the x scales
+    // warps that take tiles: weights, products, x, x scales, epilogue
+    constexpr int kTileUsers = 2 + (ROWS ? kXWarps : 1) + kScaleWarps + kEpiWarps;
     constexpr int kStepK = kNv ? 256 : 128;               // elements per stage: 128 bytes of codes a row
     constexpr int kTilesPerStage = kNv ? 4 : 1;           // 128 x 4 scale tiles per stage and 128 rows
     constexpr uint32_t kABytes = 128 * 128;
@@ -366,7 +366,7 @@ expert_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_cons
 
     if (tid == 0) {
         for (int i = 0; i < p.stages; ++i) {
-            tc::bar_init(full0 + 8 * i, p.x_tma ? 3 : 2 + 32 * kXWarps);    // weights, x scales, x (its copying lanes)
+            tc::bar_init(full0 + 8 * i, ROWS ? 2 + 32 * kXWarps : 2 + kScaleWarps);    // weights; x and x scales (by warps and their lanes)
             tc::bar_init(empty0 + 8 * i, 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -375,7 +375,7 @@ expert_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_cons
         }
         for (int i = 0; i < kTileRing; ++i) {
             tc::bar_init(tilef0 + 8 * i, 1);
-            tc::bar_init(tilee0 + 8 * i, p.x_tma ? kTileUsers - (kXWarps - 1) : kTileUsers);
+            tc::bar_init(tilee0 + 8 * i, kTileUsers);
         }
         tc::bar_init(tc::smem_u32(&sh.sums_full), SHARED ? (split - 1) * 32u * kEpiWarps : 1);
         sh.abort = 0;
@@ -447,6 +447,98 @@ expert_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_cons
         r.next(kTileRing);
     };
 
+    // What the epilogue will add to a tile, into L2: 32 bytes a lane.  (Asked
+    // for by the scale warp as it opens a tile: the product above with bias
+    // and residual takes 151 us; 164 where the epilogue asks a tile ahead, 189
+    // where a warp of its own asks as early as it can, 200 unasked.)
+    auto prefetch_residual = [&](const Tile &t) {
+        const int bytes = p.residual_dtype == CSF_F32 ? 4 : 2;
+        const int sectors = 128 * bytes / 32, per = 32 / sectors, sec = lane % sectors;
+        const int f = t.rt * 128 + sec * (32 / bytes);
+        const char *at = static_cast<const char *>(p.residual) + ((t.slot + (int64_t)(lane / sectors)) * p.residual_stride + f) * bytes;
+        for (int r = lane / sectors; r < t.n; r += per, at += per * p.residual_stride * bytes)
+            if (f < p.F) tc::prefetch_l2(at);
+    };
+
+    // Scales of the x rows, by one warp or by several (32 rows in turn each).
+    // 16 bytes of a row are four scale tiles: one stage (NVFP4) or four
+    // (MXFP8).  A unit is 32 bytes of each row where registers and stages
+    // allow, else 16.  The next one, of the next tile where this one ends, is
+    // under way before this one waits for its stages (gate/up experts of 64
+    // slots: 88 us, 99 with the load after the wait).
+    auto x_scale_role = [&](auto warps, const int which) {
+        constexpr int kWarps = decltype(warps)::value, kRows = ((kAccCols + 31) / 32 + kWarps - 1) / kWarps;
+        constexpr int kParts = kNv && kRows <= 4 ? 2 : 1;
+        const int units = unit1 - unit0;              // of 16 bytes
+        uint4 next[kRows][kParts];
+        int next_n = -1, next_stages = 0;             // its slots (-1: nothing yet, 0: no more tiles) and stages
+        Ring ring, tr;
+        Tile t;
+        const uint4 *src[kRows];
+        int u = units;
+        bool more = true;
+        auto open = [&]() {
+            if (!__all_sync(0xFFFFFFFFu, take(tr, t))) return false;
+#pragma unroll
+            for (int j = 0; j < kRows; ++j) {
+                const int c = 32 * (j * kWarps + which) + lane;
+                src[j] = reinterpret_cast<const uint4 *>(p.x_scales + (c < t.n ? sh.x_row[tr.s][c] * p.x_scale_stride : 0)) + unit0;
+            }
+            __syncwarp();
+            if (lane == 0) tc::bar_arrive(tilee0 + 8 * tr.s);
+            tr.next(kTileRing);
+            if (RES && p.residual) prefetch_residual(t);
+            return true;
+        };
+        while (next_n != 0) {
+            const int n = next_n, stages = next_stages;
+            uint4 now[kRows][kParts];
+#pragma unroll
+            for (int j = 0; j < kRows; ++j)
+#pragma unroll
+                for (int h = 0; h < kParts; ++h) now[j][h] = next[j][h];
+            if (more && u >= units) more = open(), u = 0;
+            next_n = more ? t.n : 0;
+            if (more) {
+                next_stages = min(kParts * kStagesPer16, ksteps - u * kStagesPer16);
+#pragma unroll
+                for (int j = 0; j < kRows; ++j)
+#pragma unroll
+                    for (int h = 0; h < kParts; ++h)
+                        if (32 * (j * kWarps + which) < t.n && u + h < units) next[j][h] = __ldg(src[j] + u + h);
+                u += kParts;
+            }
+            bool ok = true;
+#pragma unroll
+            for (int q = 0; q < kParts * kStagesPer16; ++q) {
+                if (n < 0 || q >= stages) break;
+                ok = __all_sync(0xFFFFFFFFu, tc::bar_wait(empty0 + 8 * ring.s, ring.parity ^ 1u, abort));
+                if (!ok) break;
+                const uint32_t dst = ring0 + ring.s * p.stage_bytes + sfb_off + lane * 16u;
+#pragma unroll
+                for (int j = 0; j < kRows; ++j) {
+                    const int block = j * kWarps + which;      // of 32 rows
+                    if (32 * block < n) {
+                        const uint4 v = now[j][q / kStagesPer16];
+                        const uint32_t to = dst + (block >> 2) * (kTilesPerStage * 512u) + (block & 3) * 4u;
+                        if constexpr (kNv) {
+                            tc::store_shared(to, v.x);
+                            tc::store_shared(to + 512u, v.y);
+                            tc::store_shared(to + 1024u, v.z);
+                            tc::store_shared(to + 1536u, v.w);
+                        } else {
+                            tc::store_shared(to, q % 4 == 0 ? v.x : q % 4 == 1 ? v.y : q % 4 == 2 ? v.z : v.w);
+                        }
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) tc::bar_arrive(full0 + 8 * ring.s);
+                ring.next(p.stages);
+            }
+            if (!ok) break;
+        }
+    };
+
     if (warp == 15) {
         // ---- tiles and their x rows ----
         Ring tr;
@@ -458,7 +550,7 @@ expert_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_cons
             // columns past the tile's slots repeat its last row
             for (int c = lane; c < ((t.n + 15) & ~15); c += 32) {
                 const int64_t s = (int64_t)t.slot + min(c, t.n - 1);
-                const int64_t v = p.rows ? (int64_t)p.rows[s] : s;
+                const int64_t v = ROWS ? (int64_t)p.rows[s] : s;
                 const int32_t r = v < 0 || v >= p.x_rows ? 0 : (int32_t)v;
                 bad_row |= r != v;
                 sh.x_row[tr.s][c] = r;
@@ -498,7 +590,7 @@ expert_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_cons
         __syncwarp();
     } else if (warp == 2 || warp == 3 || warp == 12 || warp == 13) {
         // ---- x rows ----
-        if (p.x_tma) {
+        if constexpr (!ROWS) {
             if (warp == 2 && tc::elect_one()) {
                 Ring ring, tr;
                 Tile t;
@@ -515,6 +607,13 @@ expert_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_cons
                 }
             }
             __syncwarp();
+            // The other copying warps share the scales: one alone was late for
+            // short stages (512 experts of 64 slots, 2048 x 800: 108 us, 116
+            // alone).  Not with a residual: there the epilogue is the bound,
+            // and warps that share its schedulers slow it (164 us, 173).
+            if constexpr (kScaleWarps > 1) {
+                if (warp != 2) x_scale_role(std::integral_constant<int, kScaleWarps>{}, warp == 3 ? 0 : warp - 11);
+            }
         } else {
         const int xw = warp < 4 ? warp - 2 : warp - 10;
         const int piece = lane & 7, sub = lane >> 3;      // 8 lanes a row, 4 rows a copy; every fourth group of 4 rows
@@ -552,95 +651,7 @@ expert_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_cons
         }
         }
     } else if (warp == 14) {
-        // ---- scales of the x rows ----
-        // Row lane + 32 j; 16 bytes are four scale tiles: a unit of one stage
-        // (NVFP4) or four (MXFP8).  Two units, across tiles, are under way.
-        constexpr int kRows = (kAccCols + 31) / 32;
-        const int units = unit1 - unit0;
-        struct Unit {
-            uint4 v[kRows];
-            int n, stages;      // slots (0: no more tiles), stages it serves
-        };
-        Ring ring, tr;
-        Tile t;
-        const uint4 *src[kRows];
-        int u = units;
-        bool more = true;
-        auto open = [&]() {
-            if (!__all_sync(0xFFFFFFFFu, take(tr, t))) return false;
-#pragma unroll
-            for (int j = 0; j < kRows; ++j) {
-                const int c = 32 * j + lane;
-                src[j] = reinterpret_cast<const uint4 *>(p.x_scales + (c < t.n ? sh.x_row[tr.s][c] * p.x_scale_stride : 0)) + unit0;
-            }
-            __syncwarp();
-            if (lane == 0) tc::bar_arrive(tilee0 + 8 * tr.s);
-            tr.next(kTileRing);
-            if (RES && p.residual) {      // what the epilogue will add, into L2: 32 bytes a lane
-                const int bytes = p.residual_dtype == CSF_F32 ? 4 : 2;
-                const int sectors = 128 * bytes / 32, per = 32 / sectors, sec = lane % sectors;
-                const int f = t.rt * 128 + sec * (32 / bytes);
-                const char *at = static_cast<const char *>(p.residual) + ((t.slot + (int64_t)(lane / sectors)) * p.residual_stride + f) * bytes;
-                for (int r = lane / sectors; r < t.n; r += per, at += per * p.residual_stride * bytes)
-                    if (f < p.F) tc::prefetch_l2(at);
-            }
-            return true;
-        };
-        auto load = [&](Unit &w) {
-            if (more && u == units) more = open(), u = 0;
-            w.n = more ? t.n : 0;
-            if (!more) return;
-            w.stages = min(kStagesPer16, ksteps - u * kStagesPer16);
-#pragma unroll
-            for (int j = 0; j < kRows; ++j)
-                if (32 * j < t.n) w.v[j] = __ldg(src[j] + u);
-            ++u;
-        };
-        // What a unit holds goes to its stages, and it takes a later one:
-        // before it waits for them, where the registers allow (gate/up experts
-        // of 64 slots 88 against 99 us; 224 slots a tile would spill).
-        constexpr bool kLoadFirst = kRows <= 4;
-        auto store = [&](Unit &w) {
-            const int n = w.n, stages = w.stages;
-            if (n == 0) return false;
-            uint4 now[kLoadFirst ? kRows : 1];
-            if constexpr (kLoadFirst) {
-#pragma unroll
-                for (int j = 0; j < kRows; ++j) now[j] = w.v[j];
-                load(w);
-            }
-#pragma unroll
-            for (int q = 0; q < kStagesPer16; ++q) {
-                if (q >= stages) break;
-                if (!__all_sync(0xFFFFFFFFu, tc::bar_wait(empty0 + 8 * ring.s, ring.parity ^ 1u, abort))) return false;
-                const uint32_t dst = ring0 + ring.s * p.stage_bytes + sfb_off + lane * 16u;
-#pragma unroll
-                for (int j = 0; j < kRows; ++j) {
-                    if (32 * j < n) {
-                        const uint4 v = kLoadFirst ? now[kLoadFirst ? j : 0] : w.v[j];
-                        const uint32_t to = dst + (j >> 2) * (kTilesPerStage * 512u) + (j & 3) * 4u;
-                        if constexpr (kNv) {
-                            tc::store_shared(to, v.x);
-                            tc::store_shared(to + 512u, v.y);
-                            tc::store_shared(to + 1024u, v.z);
-                            tc::store_shared(to + 1536u, v.w);
-                        } else {
-                            tc::store_shared(to, q == 0 ? v.x : q == 1 ? v.y : q == 2 ? v.z : v.w);
-                        }
-                    }
-                }
-                __syncwarp();
-                if (lane == 0) tc::bar_arrive(full0 + 8 * ring.s);
-                ring.next(p.stages);
-            }
-            if constexpr (!kLoadFirst) load(w);
-            return true;
-        };
-        Unit even, odd;
-        load(even);
-        load(odd);
-        while (store(even) && store(odd)) {
-        }
+        x_scale_role(std::integral_constant<int, kScaleWarps>{}, kScaleWarps - 1);
     } else if (warp == 1) {
         // ---- matrix instructions ----
         if (tc::elect_one()) {
@@ -826,16 +837,17 @@ expert_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_cons
                 auto turn_in = [&](auto act) {
 #pragma unroll
                     for (int j = 0; j < 8 * G; ++j) {
-                        float y = activate<decltype(act)::value>(fmaf(acc[0][j], alpha, bias[0]));
+                        float y = act(fmaf(acc[0][j], alpha, bias[0]));
                         if constexpr (GATED) y *= fmaf(acc[AT - 1][j], alpha, bias[AT - 1]);
                         buf[j * kTurnStride + lane] = y;
                     }
                 };
-                switch (p.act) {
-                    case CSF_ACT_RELU: turn_in(std::integral_constant<int, CSF_ACT_RELU>{}); break;
-                    case CSF_ACT_SILU: turn_in(std::integral_constant<int, CSF_ACT_SILU>{}); break;
-                    case CSF_ACT_GELU_TANH: turn_in(std::integral_constant<int, CSF_ACT_GELU_TANH>{}); break;
-                    default: turn_in(std::integral_constant<int, CSF_ACT_NONE>{}); break;
+                if (p.act == CSF_ACT_SILU || p.act == CSF_ACT_GELU_TANH) {
+                    const bool gelu = p.act == CSF_ACT_GELU_TANH;
+                    turn_in([&](float v) { return smooth(v, gelu); });
+                } else {
+                    const float least = p.act == CSF_ACT_RELU ? 0.f : __int_as_float(0xFF800000);
+                    turn_in([&](float v) { return v < least ? least : v; });
                 }
                 __syncwarp();
 #pragma unroll
@@ -879,33 +891,35 @@ expert_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_cons
 
 using Kernel = void (*)(CUtensorMap, CUtensorMap, MmParams);
 
-template <int KIND, int OUT>
+template <int KIND, bool ROWS, int OUT>
 Kernel pick(int shape, bool res) {
     switch (shape) {
-        case kNarrow: return res ? expert_matmul_kernel<KIND, kNarrow, true, OUT> : expert_matmul_kernel<KIND, kNarrow, false, OUT>;
-        case kWide: return res ? expert_matmul_kernel<KIND, kWide, true, OUT> : expert_matmul_kernel<KIND, kWide, false, OUT>;
-        case kGated: return res ? expert_matmul_kernel<KIND, kGated, true, OUT> : expert_matmul_kernel<KIND, kGated, false, OUT>;
+        case kNarrow: return res ? expert_matmul_kernel<KIND, ROWS, kNarrow, true, OUT> : expert_matmul_kernel<KIND, ROWS, kNarrow, false, OUT>;
+        case kWide: return res ? expert_matmul_kernel<KIND, ROWS, kWide, true, OUT> : expert_matmul_kernel<KIND, ROWS, kWide, false, OUT>;
+        case kGated: return res ? expert_matmul_kernel<KIND, ROWS, kGated, true, OUT> : expert_matmul_kernel<KIND, ROWS, kGated, false, OUT>;
         // for these the residual is asked for at run time: their epilogues are short
-        case kNarrowShared: return expert_matmul_kernel<KIND, kNarrowShared, true, OUT>;
-        default: return expert_matmul_kernel<KIND, kGatedShared, true, OUT>;
+        case kNarrowShared: return expert_matmul_kernel<KIND, ROWS, kNarrowShared, true, OUT>;
+        default: return expert_matmul_kernel<KIND, ROWS, kGatedShared, true, OUT>;
     }
 }
 
-template <int KIND>
+template <int KIND, bool ROWS>
 Kernel pick_kernel(int out, int shape, bool res) {
     switch (out) {
-        case kOutBf16: return pick<KIND, kOutBf16>(shape, res);
-        case kOutF16: return pick<KIND, kOutF16>(shape, res);
-        case kOutF32: return pick<KIND, kOutF32>(shape, res);
-        case kOutNv: return pick<KIND, kOutNv>(shape, res);
-        default: return pick<KIND, kOutMx>(shape, res);
+        case kOutBf16: return pick<KIND, ROWS, kOutBf16>(shape, res);
+        case kOutF16: return pick<KIND, ROWS, kOutF16>(shape, res);
+        case kOutF32: return pick<KIND, ROWS, kOutF32>(shape, res);
+        case kOutNv: return pick<KIND, ROWS, kOutNv>(shape, res);
+        default: return pick<KIND, ROWS, kOutMx>(shape, res);
     }
 }
 
 // The kernel for a kind of x, an output, a shape and a residual's presence
-// (one translation unit a kind).
+// (one translation unit a kind and an indexing of x).
 Kernel nvfp4_kernel(int out, int shape, bool res);
+Kernel nvfp4_rows_kernel(int out, int shape, bool res);
 Kernel mxfp8_kernel(int out, int shape, bool res);
+Kernel mxfp8_rows_kernel(int out, int shape, bool res);
 
 }  // namespace mm
 }  // namespace csfk

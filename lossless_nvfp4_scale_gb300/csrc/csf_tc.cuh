@@ -68,23 +68,30 @@ __device__ __forceinline__ bool bar_try_cluster(uint32_t bar, uint32_t parity) {
 
 constexpr uint64_t kWaitLimitNs = 2000000000ull;   // a wait that lasts this long gives up
 
-// Wait for a phase, or give up: after the limit, or once another thread of
-// the block gave up (*abort).  A false return means the caller stops.
+// Whether a wait that began at t0 (0: now) goes on: its start, or 0 to give up,
+// after the limit or because another thread of the block did (*abort).  Apart
+// from the waits: inlined in each it made the products' kernel a tenth
+// longer, which its instruction fetches feel.
+static __device__ __noinline__ uint64_t keep_waiting(uint64_t t0, volatile uint32_t *abort) {
+    if (*abort) return 0;
+    const uint64_t t = timer_ns();
+    if (t0 == 0) return t;
+    if (t - t0 <= kWaitLimitNs) return t0;
+    *abort = 1;
+    return 0;
+}
+
+// Wait for a phase, or give up.  A false return means the caller stops.
 template <bool CLUSTER = false>
 __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile uint32_t *abort) {
     uint64_t t0 = 0;
-    for (uint32_t i = 0;; ++i) {
-        if (CLUSTER ? bar_try_cluster(bar, parity) : bar_try(bar, parity)) return true;
-        if ((i & 63u) == 63u) {
-            if (*abort) return false;
-            const uint64_t t = timer_ns();
-            if (t0 == 0) t0 = t;
-            if (t - t0 > kWaitLimitNs) {
-                *abort = 1;
-                return false;
-            }
-        }
-    }
+    do {
+#pragma unroll 1
+        for (int i = 0; i < 64; ++i)
+            if (CLUSTER ? bar_try_cluster(bar, parity) : bar_try(bar, parity)) return true;
+        t0 = keep_waiting(t0, abort);
+    } while (t0 != 0);
+    return false;
 }
 
 // ---- clusters -----------------------------------------------------------------------------------------------------
