@@ -168,22 +168,31 @@ extern "C" csf_status csf_expert_matmul(const csf_expert_matmul_args *a, void *s
     // of a 5120-deep MXFP4 product, 1 / 2 / 4 / 8 blocks a tile: 14.1 / 11.0 /
     // 9.2 / 15.9 us with 2048 rows (8: 128 blocks), 14.2 / 11.0 / 9.1 / 8.5
     // with 256; of a 1280-deep one 7.3 / 7.9.
-    p.split = 1;
     const int64_t small_tiles = (int64_t)p.row_tiles * (busy + a->slots / kSplitSlots);
     const int units = (p.ncb + 3) / 4, steps = nv ? units : p.ncb;
+    const uint32_t sf = nv ? 2048u : 512u;
+    const int held = (int)round_up(sizeof(Shared) + sizeof(float) * kEpiWarps * 16 * kTurnStride, 1024);
+    // Shared memory of a launch whose clusters have `split` blocks: what is
+    // not stages, a stage, and how many stages that leaves.
+    int fixed = 0;
+    auto fit = [&](int split) {
+        const int slots = split > 1 ? kSplitSlots : p.nt;
+        p.b_rows = std::max(slots, kXBox);
+        p.stage_bytes = (uint32_t)round_up(at * 16384 + p.b_rows * 128 + (at + (slots + 127) / 128) * sf, 1024);
+        fixed = 1024 + 8 * (E + 1) + 32 + (split - 1) * at * kSplitSlots * 128 * 4;
+        p.stages = std::min<int>(kMaxStages, (kSmemLimit - held - fixed) / (int)p.stage_bytes);
+    };
+    p.split = 1;
     while (p.split < kMaxSplit && steps >= 16 && small_tiles * p.split * 2 <= sms / 2 && steps >= 5 * p.split * 2 && units >= p.split * 2)
         p.split *= 2;
+    // many experts' prefixes leave less for the exchanged sums
+    for (fit(p.split); p.split > 1 && p.stages < 3; fit(p.split)) p.split /= 2;
     if (p.split > 1) {
         shape = a->gated ? kGatedShared : kNarrowShared;
         p.nt = kSplitSlots;
         most_tiles = small_tiles;
     }
-    p.b_rows = std::max(p.nt, kXBox);
-    const uint32_t sf = nv ? 2048u : 512u;
-    p.stage_bytes = (uint32_t)round_up(at * 16384 + p.b_rows * 128 + (at + (p.nt + 127) / 128) * sf, 1024);
-    const int fixed = 1024 + 8 * (E + 1) + 32 + (p.split - 1) * at * kSplitSlots * 128 * 4;
-    const int room = kSmemLimit - (int)round_up(sizeof(Shared) + sizeof(float) * kEpiWarps * 16 * kTurnStride, 1024) - fixed;
-    p.stages = std::min<int>(kMaxStages, room / (int)p.stage_bytes);
+    if (p.stages < 2) return CSF_ERR_UNSUPPORTED;
     // never two blocks on an SM: each holds the whole tensor memory
     const int smem = std::max(fixed + p.stages * (int)p.stage_bytes, 120 * 1024);
 

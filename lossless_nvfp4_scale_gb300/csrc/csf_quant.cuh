@@ -54,8 +54,6 @@ __device__ __forceinline__ float over(float v, const Whole &w) {
     return fmaf(fmaf(-q, w.value, v), w.inverse, q);
 }
 
-__device__ __forceinline__ uint32_t e4m3(float v) { return __nv_cvt_float_to_fp8(v, __NV_SATFINITE, __NV_E4M3); }
-
 // Two values -> two E4M3 bytes, the first in the low byte.
 __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
     return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
@@ -93,12 +91,6 @@ __device__ __forceinline__ void quantize8(const float (&y)[8], uint8_t *codes, u
             e2m1x2(over(y[4], w), over(y[5], w)) << 16 | e2m1x2(over(y[6], w), over(y[7], w)) << 24;
         if ((chunk & 1) == 0) scales[chunk >> 1] = (uint8_t)s;
     }
-}
-
-__device__ __forceinline__ float load_as_float(const void *p, int64_t i, int dtype) {
-    if (dtype == CSF_BF16) return __bfloat162float(static_cast<const __nv_bfloat16 *>(p)[i]);
-    if (dtype == CSF_F16) return __half2float(static_cast<const __half *>(p)[i]);
-    return static_cast<const float *>(p)[i];
 }
 
 }  // namespace quant

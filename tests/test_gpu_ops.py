@@ -631,3 +631,41 @@ def test_matmul_infinite_sums(ops, act, plus, minus):
     assert torch.isfinite(out[:, keep]).all()
     assert ((out[:, 5] - 1e30).abs() <= 1e24).all()
     assert (out[:, 6] == -1e30).all() if act is None else (out[:, 6].abs() <= 1e-5).all()
+
+
+@pytest.mark.parametrize("kind,K", [(0, 4096), (1, 2048)])
+def test_matmul_one_slot_of_8192_experts(ops, kind, K):
+    """The most experts, one of them with a slot: their prefixes leave little shared memory for a cluster's sums."""
+    E, N, e = 8192, 256, 8190
+    q = Problem(ops, kind, [1], N, K, seed=17)
+    w = torch.zeros(E, N, K // 2, dtype=torch.uint8, device="cuda")
+    ws = torch.zeros(E, q.ws.numel(), dtype=torch.uint8, device="cuda")
+    w[e], ws[e] = q.w[0], q.ws
+    start = torch.zeros(E + 1, dtype=torch.int64, device="cuda")
+    start[e + 1:] = 1
+    for kw in (dict(out=F32), dict(out=F32, gated=True, activation="silu")):
+        out = ops.expert_matmul(q.x, w, ws.view(-1), expert_start=start, **kw)
+        q.check(out, act=kw.get("activation"), gated=kw.get("gated", False))
+    assert ops.errors() == 0
+    many = torch.zeros(E + 1, dtype=torch.int32, device="cuda")      # as many slots as x rows, all on one expert
+    x = ops.Quantized(kind, q.x.codes.expand(300, -1).contiguous(), q.x.scales.expand(300, -1).contiguous(), K)
+    many[e + 1:] = 300
+    out = ops.expert_matmul(x, w, ws.view(-1), expert_start=many, out=F32)
+    assert (out == out[0]).all()
+    q.check(out[:1])
+
+
+def test_products_on_two_streams_at_once(ops):
+    """Each block takes a whole SM's tensor memory; two products that overlap share the SMs in turn."""
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    p = Problem(ops, ops.NVFP4, [70] * 30, 512, 640, seed=18)
+    q = Problem(ops, ops.MXFP8, [1], 2048, 5120, seed=19)          # a cluster a tile
+    want_p, want_q = p.run(out=F32), q.run(out=F32)
+    torch.cuda.synchronize()
+    outs = []
+    for _ in range(10):
+        outs.append((p.run(out=F32, stream=a), q.run(out=F32, stream=b)))
+    torch.cuda.synchronize()
+    for x, y in outs:
+        assert torch.equal(x, want_p) and torch.equal(y, want_q)
+    assert ops.errors() == 0
