@@ -136,7 +136,7 @@ typedef enum { CSF_ACT_NONE = 0, CSF_ACT_RELU = 1, CSF_ACT_SILU = 2, CSF_ACT_GEL
  * with x and w as the values they stand for without their tensor scales
  * (alpha carries the product of those).  x NVFP4 goes with w NVFP4, x MXFP8
  * with w MXFP4.  Sums in 32 bits.  Slots at or past expert_start[E] are not
- * written.
+ * written; with an expert_start that is out of order or range, none is.
  */
 typedef struct {
     csf_rows x;              /* rows x cols (= K); K a multiple of 32 (NVFP4) or 128 (MXFP8) */

@@ -417,13 +417,14 @@ expert_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_cons
         __syncthreads();
     }
     if (tid == 0) first[p.E] = running, slot0[p.E] = (uint32_t)start_at(p, p.E);
-    if (bad && p.err && blockIdx.x == 0) atomicOr(p.err, CSF_DEV_ERR_CORRUPT);
     tc::fence_before();
-    __syncthreads();
+    bad = __syncthreads_or(bad);
     tc::fence_after();
-    uint32_t total = first[p.E] * (uint32_t)p.row_tiles;
-    // one tile a cluster at most (a corrupt expert_start may ask for more)
-    if constexpr (SHARED) total = min(total, gridDim.x / split);
+    if (bad && p.err && blockIdx.x == 0 && tid == 0) atomicOr(p.err, CSF_DEV_ERR_CORRUPT);
+    // An expert_start out of order or range makes no tiles: its experts could
+    // overlap, and their tiles be more than 32 bits count.
+    uint32_t total = bad ? 0 : first[p.E] * (uint32_t)p.row_tiles;
+    if constexpr (SHARED) total = min(total, gridDim.x / split);      // one tile a cluster
     const uint32_t tmem = sh.tmem;
     volatile uint32_t *abort = &sh.abort;
     // this block's part of K, in whole 16-byte units of x scales

@@ -465,6 +465,19 @@ def test_matmul_reports_bad_indices_and_starts(ops):
         assert out.shape == (13, 64)
 
 
+@pytest.mark.parametrize("bad", [[0, 6, 14], [0, 7, 5], [-1, 6, 13], [0, 14, 13], [9, 3, 13]])
+@pytest.mark.parametrize("K", [64, 5120])
+def test_matmul_writes_nothing_for_a_bad_start(ops, bad, K):
+    from lossless_nvfp4_scale_gb300 import csf
+    for int64 in (False, True):
+        q = Problem(ops, ops.NVFP4, [6, 7], 64, K, seed=8)
+        err = torch.zeros(1, dtype=torch.int32, device="cuda")
+        out = torch.full((13, 64), 5.0, device="cuda")
+        start = torch.tensor(bad, dtype=torch.int64 if int64 else torch.int32, device="cuda")
+        q.run(out=out, expert_start=start, error_word=err)
+        assert int(err) == csf.DEV_ERR_CORRUPT and (out == 5.0).all()
+
+
 def test_errors_of_calls_without_an_error_word(ops):
     from lossless_nvfp4_scale_gb300 import csf
     q = Problem(ops, ops.NVFP4, [6, 7], 64, 64, seed=8, gather=5)
