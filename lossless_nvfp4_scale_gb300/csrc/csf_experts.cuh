@@ -107,27 +107,34 @@ struct MmParams {
 
 enum Out { kOutBf16 = 0, kOutF16 = 1, kOutF32 = 2, kOutNv = 3, kOutMx = 4 };
 
-// v / (1 + exp(-z)), to a few units in the last place: the exponent's product
-// with log2(e) carries its rounding error along, and the quotient its
-// remainder.  (expf and the division cost the dense product 52 us of 130; the
-// approximate forms alone are off by 1e-6 of the value, which shows where the
-// result is rounded to 8 bits.)
+// v / (1 + exp(-z)), within 2^-20 of itself: with h = exp(-|z| / 2) the divisor
+// is 1 + h^2, and the dividend v or, for a negative z, v h^2, one factor at a
+// time so that neither a large v nor a small h^2 is lost.  The exponent's
+// product with log2(e) carries its rounding error along (the error of a
+// product by fma), and the quotient its remainder (Markstein's last step of a
+// division, 1990).  (expf and the division cost the dense product 52 us of
+// 130; the approximate forms alone are off by 1e-6 of the value, which shows
+// where the result is rounded to 8 bits.)
 __device__ __forceinline__ float times_sigmoid(float v, float z) {
-    constexpr float kLog2e = 1.4426950408889634f, kRest = (float)(1.4426950408889634 - (double)kLog2e), kLn2 = 0.6931471805599453f;
-    z = fminf(fmaxf(z, -86.f), 86.f);        // past that the quotient is 0 or v
-    const float t = -z * kLog2e;
-    const float rest = fmaf(-z, kLog2e, -t) - z * kRest;
-    float e;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(t));
-    const float d = 1.f + fmaf(e, rest * kLn2, e);
+    constexpr double kHalfLog2e = 0.72134752044448170;
+    constexpr float kScale = (float)kHalfLog2e, kRest = (float)(kHalfLog2e - (double)kScale), kLn2 = 0.6931471805599453f;
+    const float m = fminf(fabsf(z), 180.f);           // h of more is 0
+    const float t = -m * kScale;
+    const float rest = fmaf(-m, kScale, -t) - m * kRest;
+    float h;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(h) : "f"(t));
+    h = fmaf(h, rest * kLn2, h);
+    const float d = fmaf(h, h, 1.f);
     float r;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d));
-    const float q = v * r;
-    // an infinite v has no remainder: itself, or (negative) NaN as inf / inf
-    return fabsf(v) < __int_as_float(0x7F800000) ? fmaf(fmaf(-q, d, v), r, q) : v > 0.f ? v : __int_as_float(0x7FC00000);
+    const float s = z < 0.f ? h : 1.f;
+    const float n = v * s * s;                        // -inf * 0: NaN, as inf / inf
+    const float q = n * r;
+    return fabsf(n) < __int_as_float(0x7F800000) ? fmaf(fmaf(-q, d, n), r, q) : n;     // an infinity has no remainder
 }
 
-// v * sigmoid(2 * sqrt(2 / pi) * (v + 0.044715 v^3)) is the tanh form of GELU.
+// v * sigmoid(z), z = 2 * sqrt(2 / pi) * (v + 0.044715 v^3), is the tanh form of
+// GELU.  z's roundings (2^-22 of it at most) add |z| 2^-21 to the 2^-20 above.
 __device__ __forceinline__ float smooth(float v, bool gelu) {
     return times_sigmoid(v, gelu ? 1.5957691216057308f * (v + 0.044715f * v * v * v) : v);
 }

@@ -682,3 +682,52 @@ def test_products_on_two_streams_at_once(ops):
     for x, y in outs:
         assert torch.equal(x, want_p) and torch.equal(y, want_q)
     assert ops.errors() == 0
+
+
+# ---- activations over the range of float32 ---------------------------------------------------------------------------
+# x codes of 0 make p = bias exactly, so the bias chooses the activation's argument.
+
+def through_bias(ops, v, act, up_half=None, out=F32, **kw):
+    """act(v), or act(v) * up_half gated, as the product's epilogue computes it for a 1-D v (a multiple of 128)."""
+    N = v.numel() * (1 if up_half is None else 2)
+    bias = v if up_half is None else torch.cat([v, up_half])
+    x = ops.Quantized(ops.NVFP4, torch.zeros(1, 16, dtype=torch.uint8, device="cuda"),
+                      torch.zeros(1, 16, dtype=torch.uint8, device="cuda"), 32)
+    w = torch.zeros(1, N, 16, dtype=torch.uint8, device="cuda")
+    ws = torch.zeros(up(N, 128) * 4, dtype=torch.uint8, device="cuda")
+    return ops.expert_matmul(x, w, ws, bias=bias.view(1, N), activation=act, gated=up_half is not None, out=out, **kw)
+
+
+def activation(v, act):
+    """The definition in 64 bits, and the argument of its sigmoid."""
+    z = v if act == "silu" else 2 * math.sqrt(2 / math.pi) * (v + 0.044715 * v ** 3)
+    return v / (1 + torch.exp(-z)), z
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+def test_activation_of_large_negative_sums_is_zero(ops, act):
+    low = torch.finfo(BF16).min
+    v = torch.tensor([-torch.finfo(F32).max, low, -1e38, -1e37, -1e35, -1e30, -1e20, -1e10, -1e5, -300.0] + [0.0] * 118, device="cuda")
+    assert (through_bias(ops, v, act)[0] == 0).all()
+    half = through_bias(ops, v.to(BF16), act, out=BF16)[0]                # the first is an infinity in bfloat16
+    assert torch.isnan(half[0]) and (half[1:] == 0).all()
+    big = torch.full_like(v, 1e30)
+    assert (through_bias(ops, v, act, up_half=big)[0] == 0).all()
+    # and large positive ones are themselves
+    assert torch.equal(through_bias(ops, -v, act)[0], -v)
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+def test_activation_relative_error(ops, act):
+    """The exponential is within 2^-22, its sum with 1 and the quotient within 2^-23 each: 2^-20 in all.  GELU's
+    argument z takes seven roundings of 2^-24 first, which the exponential turns into |z| 2^-21.  Below z = -86 two
+    exponentials multiply, the second's argument of up to 150 rounded once: 2^-16, and the spacing of the smallest
+    numbers."""
+    g = gen(31)
+    at = torch.cat([torch.linspace(-110, 30, 6000, device="cuda"), 4 * torch.randn(2048, device="cuda", generator=g),
+                    torch.randn(144, device="cuda", generator=g) * 1e-3])
+    got = through_bias(ops, at, act)[0].double()
+    want, z = activation(at.double(), act)
+    rel = 2.0 ** -20 + (z.abs() * 2.0 ** -21 if act == "gelu" else 0)
+    rel = torch.where(z < -86, rel + 2.0 ** -16, rel)
+    assert ((got - want).abs() <= rel * want.abs() + 2.0 ** -148).all()
