@@ -57,7 +57,8 @@ typedef struct {
     int64_t code_stride;       /* bytes between rows, a multiple of 16 */
     uint8_t *scales;           /* 16-byte aligned */
     int64_t scale_stride;      /* bytes between rows, a multiple of 16 */
-    const float *tensor_scale; /* NVFP4 output: device scalar > 0, NULL = 1; not read elsewhere */
+    const float *tensor_scale; /* NVFP4 output: device scalar, 2^-117 .. 2^125 (its products with scales
+                                  are normal numbers), NULL = 1; not read elsewhere */
 } csf_rows;
 
 /*

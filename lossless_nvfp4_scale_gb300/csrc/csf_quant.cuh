@@ -47,8 +47,9 @@ __device__ __forceinline__ Whole nv_whole(uint32_t byte, float tensor_scale) {
     return w;
 }
 
-// v / whole: the product with the inverse, corrected by its remainder, so that
-// values next to the middle of two codes round as the quotient does.
+// v / whole: the product with the inverse, corrected by its remainder
+// (Markstein's last step of a division, 1990), so that values next to the
+// middle of two codes round as the quotient does.
 __device__ __forceinline__ float over(float v, const Whole &w) {
     const float q = v * w.inverse;
     return fmaf(fmaf(-q, w.value, v), w.inverse, q);
@@ -86,9 +87,20 @@ __device__ __forceinline__ void quantize8(const float (&y)[8], uint8_t *codes, u
     } else {
         const uint32_t s = nv_scale(m, 6.f * tensor_scale);
         const Whole w = nv_whole(s, tensor_scale);
+        float v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = y[i];
+        if (s == 0x7E) {
+            // The largest scale: values may be far past 6 of it, and a quotient
+            // that overflows has no remainder to correct it by.  What is past
+            // 5 of it is coded 6.
+            const float most = 6.5f * w.value;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = fminf(fmaxf(v[i], -most), most);
+        }
         *reinterpret_cast<uint32_t *>(codes + chunk * 4) =
-            e2m1x2(over(y[0], w), over(y[1], w)) | e2m1x2(over(y[2], w), over(y[3], w)) << 8 |
-            e2m1x2(over(y[4], w), over(y[5], w)) << 16 | e2m1x2(over(y[6], w), over(y[7], w)) << 24;
+            e2m1x2(over(v[0], w), over(v[1], w)) | e2m1x2(over(v[2], w), over(v[3], w)) << 8 |
+            e2m1x2(over(v[4], w), over(v[5], w)) << 16 | e2m1x2(over(v[6], w), over(v[7], w)) << 24;
         if ((chunk & 1) == 0) scales[chunk >> 1] = (uint8_t)s;
     }
 }

@@ -731,3 +731,25 @@ def test_activation_relative_error(ops, act):
     rel = 2.0 ** -20 + (z.abs() * 2.0 ** -21 if act == "gelu" else 0)
     rel = torch.where(z < -86, rel + 2.0 ** -16, rel)
     assert ((got - want).abs() <= rel * want.abs() + 2.0 ** -148).all()
+
+
+# ---- codes of values far past what they can hold -----------------------------------------------------------------------
+
+@pytest.mark.parametrize("g", [1e-3, 1e-10, 1e-30, 1.0])
+def test_nvfp4_codes_saturate_with_their_sign(ops, g):
+    """The quotient of a huge value and a small tensor scale passes float32's range: still 6 with the value's sign, and
+    the block's other codes are the nearest ones."""
+    top = torch.finfo(F32).max
+    ts = torch.tensor([g], device="cuda")
+    v = torch.zeros(128, device="cuda")
+    v[0], v[1], v[17], v[18], v[33], v[50] = top, -top, -top, 4.8 * 448 * g, 1e35, torch.finfo(BF16).min
+    v[34:40] = torch.tensor([0.3, -0.8, 1.3, -1.7, 2.6, -4.9], device="cuda") * 448 * g
+    q = through_bias(ops, v, None, out=ops.NVFP4, out_tensor_scale=ts)
+    c = code_values(q, ops)[0]
+    s = scale_values(q.scales[:, :8], ops.NVFP4, ops)[0].repeat_interleave(16) * ts.double()
+    want = torch.where(s > 0, v.double() / s, torch.zeros_like(s)).clamp(-6, 6)
+    grid = torch.tensor(sorted(set(E2M1 + tuple(-e for e in E2M1))), dtype=torch.float64, device="cuda")
+    assert torch.equal(c, grid[(want[:, None] - grid).abs().argmin(1)])
+    # the norm's codes too: 128 equal values have norm 1, the weight makes them anything
+    qn, _ = ops.rms_norm(torch.ones(1, 128, device="cuda"), v, ops.NVFP4, eps=0.0, tensor_scale=ts)
+    assert torch.equal(code_values(qn, ops), code_values(q, ops)) and torch.equal(qn.scales[:, :8], q.scales[:, :8])
