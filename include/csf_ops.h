@@ -16,7 +16,8 @@
  * asynchronous on `stream`, no allocation, no host synchronisation, argument
  * and launch errors as a csf_status, data errors as CSF_DEV_ERR_* bits OR-ed
  * into the optional device word `error_word`.  Arguments are checked on the
- * host before any CUDA call.
+ * host before any CUDA call; a pointer off the alignment of its element is
+ * CSF_ERR_ARG.
  */
 #ifndef CSF_OPS_H
 #define CSF_OPS_H

@@ -63,11 +63,16 @@ csf_status check(const csf_expert_matmul_args *a) {
     if (a->x.rows == 0) return CSF_ERR_ARG;
     if (!a->w || !a->w_scales || !aligned_to(a->w, 32) || !aligned_to(a->w_scales, 16)) return CSF_ERR_ARG;
     const int32_t F = a->gated ? a->n / 2 : a->n;
-    if (a->bias && !dtype_known(a->bias_dtype)) return CSF_ERR_ARG;
-    if (a->residual && (!dtype_known(a->residual_dtype) || a->residual_stride < F)) return CSF_ERR_ARG;
+    if (!aligned_to(a->rows, 4) || !aligned_to(a->expert_start, a->expert_start_is_int64 ? 8 : 4)) return CSF_ERR_ARG;
+    if (!aligned_to(a->alpha, 4) || !aligned_to(a->row_scale, 4) || !aligned_to(a->error_word, 4)) return CSF_ERR_ARG;
+    if (a->bias && (!dtype_known(a->bias_dtype) || !aligned_to(a->bias, dtype_bytes(a->bias_dtype)))) return CSF_ERR_ARG;
+    if (a->residual && (!dtype_known(a->residual_dtype) || a->residual_stride < F ||
+                        !aligned_to(a->residual, dtype_bytes(a->residual_dtype))))
+        return CSF_ERR_ARG;
     if (a->out) {
-        if (!dtype_known(a->out_dtype) || a->out_stride < F) return CSF_ERR_ARG;
-    } else if (!rows_valid(a->out_rows) || a->out_rows.cols != F || a->out_rows.rows != a->slots) {
+        if (!dtype_known(a->out_dtype) || a->out_stride < F || !aligned_to(a->out, dtype_bytes(a->out_dtype))) return CSF_ERR_ARG;
+    } else if (!rows_valid(a->out_rows) || a->out_rows.cols != F || a->out_rows.rows != a->slots ||
+               !aligned_to(a->out_rows.tensor_scale, 4)) {
         return CSF_ERR_ARG;
     }
     return CSF_OK;

@@ -278,6 +278,7 @@ extern "C" csf_status csf_rms_norm(const csf_rms_norm_args *a, void *stream) {
     if ((a->residual && a->residual_stride < cols) || (a->sum_out && a->sum_stride < cols)) return CSF_ERR_ARG;
     const uintptr_t e = dtype_bytes(a->dtype);
     if (!aligned_to(a->x, e) || !aligned_to(a->weight, e) || !aligned_to(a->residual, e) || !aligned_to(a->sum_out, e)) return CSF_ERR_ARG;
+    if (!aligned_to(a->out.tensor_scale, 4)) return CSF_ERR_ARG;
     if (a->out.rows >= (1ll << 31) || cols > (1 << 24)) return CSF_ERR_UNSUPPORTED;
     NormParams p;
     p.x = a->x;

@@ -373,11 +373,12 @@ extern "C" csf_status csf_route(const csf_route_args *a, void *stream) {
     if (!a || !dtype_known(a->dtype) || a->tokens < 0 || a->experts < 1 || a->k < 1 || a->k > a->experts) return CSF_ERR_ARG;
     if (a->experts > kRouteMaxExperts || a->k > kRouteMaxK) return CSF_ERR_UNSUPPORTED;
     if ((int64_t)a->tokens * a->k >= (1ll << 31)) return CSF_ERR_UNSUPPORTED;
-    if (!a->expert_start) return CSF_ERR_ARG;
+    if (!a->expert_start || !aligned_to(a->expert_start, 4)) return CSF_ERR_ARG;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (a->tokens > 0) {
         if (!a->logits || !a->ids || !a->weights || !a->rows || !a->slots || a->logits_stride < a->experts) return CSF_ERR_ARG;
         if (!aligned_to(a->logits, dtype_bytes(a->dtype))) return CSF_ERR_ARG;
+        if (!aligned_to(a->ids, 4) || !aligned_to(a->weights, 4) || !aligned_to(a->rows, 4) || !aligned_to(a->slots, 4)) return CSF_ERR_ARG;
     }
     const size_t need = csf_route_scratch_bytes(a->tokens, a->experts);
     if (need > 0) {

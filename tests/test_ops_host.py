@@ -150,3 +150,37 @@ def test_binding_refusals_without_a_gpu(ops):
     assert q.codes.shape == (4, 128) and q.scales.shape == (4, 16)
     with pytest.raises(ops.CsfError, match="CUDA"):
         ops.expert_matmul(q, torch.zeros(1, 8, 128, dtype=torch.uint8), torch.zeros(1))
+
+
+def test_pointers_off_their_elements_are_refused(ops):
+    """Every pointer that a kernel reads or writes by elements, one byte or one half element off."""
+    def norm(**kw):
+        a = dict(x=256, xs=256, res=0, rs=0, out_sum=0, ss=0, w=256, dtype=0, eps=1e-6, ts=0)
+        a.update(kw)
+        return ops.lib.csf_rms_norm(ops._RMS_NORM.pack(*list(a.values())[:9], *rows(ts=a["ts"])), None)
+
+    assert norm(ts=258) == ARG and norm(res=257, rs=256) == ARG and norm(out_sum=257, ss=256) == ARG
+
+    def route(**kw):
+        a = dict(logits=256, ls=8, dtype=2, T=4, E=8, k=2, renormalize=1, ids=256, w=256, es=256, r=256, s=256, scratch=0, n=0)
+        a.update(kw)
+        return ops.lib.csf_route(ops._ROUTE.pack(*a.values()), None)
+
+    for name in ("ids", "w", "es", "r", "s"):
+        assert route(**{name: 258}) == ARG, name
+
+    def product(**kw):
+        a = dict(ri=0, S=4, E=2, N=256, w=256, ws=256, es=256, es64=0, alpha=0, bias=0, bdt=0, act=0, gated=0, rscale=0,
+                 res=0, rstr=256, rdt=0, odt=0, out=256, ostr=256)
+        err, orows = kw.pop("err", 0), kw.pop("orows", (0,) * 8)
+        a.update(kw)
+        return ops.lib.csf_expert_matmul(ops._EXPERT_MATMUL.pack(*rows(), *a.values(), *orows, err), None)
+
+    for name in ("ri", "es", "alpha", "rscale", "err"):
+        assert product(**{name: 258}) == ARG, name
+    assert product(es=260, es64=1) == ARG
+    for dtype, off in ((0, 257), (1, 257), (2, 258)):
+        assert product(bias=off, bdt=dtype) == ARG
+        assert product(res=off, rdt=dtype) == ARG
+        assert product(out=off, odt=dtype) == ARG
+    assert product(out=0, orows=rows(ts=258)) == ARG
