@@ -168,7 +168,7 @@ typedef struct {
 } csf_expert_matmul_args;
 
 /* One launch.  Errors: CSF_ERR_ARG, CSF_ERR_UNSUPPORTED (K or N off the
- * multiples above, E > 8192), CSF_ERR_CUDA. */
+ * multiples above or within 512 of 2^31, E > 8192), CSF_ERR_CUDA. */
 csf_status csf_expert_matmul(const csf_expert_matmul_args *a, void *stream);
 
 #ifdef __cplusplus

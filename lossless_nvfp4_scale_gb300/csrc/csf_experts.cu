@@ -56,6 +56,7 @@ csf_status check(const csf_expert_matmul_args *a) {
     if (!rows_valid(a->x) || a->experts < 1 || a->n < 1 || a->slots < 0) return CSF_ERR_ARG;
     if (a->act < CSF_ACT_NONE || a->act > CSF_ACT_GELU_TANH) return CSF_ERR_ARG;
     if (a->experts > kMmMaxExperts || a->slots >= (1ll << 31) || a->x.rows >= (1ll << 31)) return CSF_ERR_UNSUPPORTED;
+    if (a->n > INT32_MAX - 255 || a->x.cols > INT32_MAX - 511) return CSF_ERR_UNSUPPORTED;      // whole tiles of them count in 32 bits
     if (a->x.cols % (a->x.kind == CSF_ROWS_NVFP4 ? 32 : 128) || (a->gated && a->n % 256)) return CSF_ERR_UNSUPPORTED;
     if (!a->expert_start && a->experts != 1) return CSF_ERR_ARG;
     if (!a->rows && a->slots > a->x.rows) return CSF_ERR_ARG;

@@ -804,7 +804,7 @@ expert_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_cons
             const int64_t slot = (int64_t)t.slot + 8 * G * half + sub;     // the first of this lane's slots
             const char *res_at = static_cast<const char *>(p.residual) + (slot * p.residual_stride + f) * res_bytes;
             const float *scale_at = p.row_scale + slot;
-            char *out_at = static_cast<char *>(p.out) + slot * p.out_stride * kOutBytes + (OUT == kOutNv || OUT == kOutMx ? 0 : f * kOutBytes);
+            char *out_at = static_cast<char *>(p.out) + slot * p.out_stride * kOutBytes + (OUT == kOutNv || OUT == kOutMx ? 0 : (int64_t)f * kOutBytes);
             uint8_t *srow = p.out_scales + slot * p.out_scale_stride;
             int c = 8 * G * half;
             Raw8 res[G];

@@ -753,3 +753,19 @@ def test_nvfp4_codes_saturate_with_their_sign(ops, g):
     # the norm's codes too: 128 equal values have norm 1, the weight makes them anything
     qn, _ = ops.rms_norm(torch.ones(1, 128, device="cuda"), v, ops.NVFP4, eps=0.0, tensor_scale=ts)
     assert torch.equal(code_values(qn, ops), code_values(q, ops)) and torch.equal(qn.scales[:, :8], q.scales[:, :8])
+
+
+# ---- more columns than 31 bits of bytes ----------------------------------------------------------------------------------
+
+def test_matmul_of_rows_past_2_31_bytes(ops):
+    """Two float32 rows of 2^29 + 128 columns: the last block of columns starts 2^31 bytes into its row."""
+    far, S = 1 << 29, 2
+    q = Problem(ops, ops.NVFP4, [S], 256, 32, seed=24)
+    w = torch.zeros(1, far + 128, 16, dtype=torch.uint8, device="cuda")
+    ws = torch.zeros((far + 128) * 4, dtype=torch.uint8, device="cuda")       # a 128-row block is 512 bytes
+    w[0, :128], w[0, far:] = q.w[0, :128], q.w[0, 128:]
+    ws[:512], ws[-512:] = q.ws[:512], q.ws[512:]
+    out = torch.full((S, far + 128), 5.0, device="cuda")
+    ops.expert_matmul(q.x, w, ws, out=out)
+    q.check(torch.cat([out[:, :128], out[:, far:]], 1))
+    assert not out[:, 128:far].any()

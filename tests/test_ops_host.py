@@ -184,3 +184,14 @@ def test_pointers_off_their_elements_are_refused(ops):
         assert product(res=off, rdt=dtype) == ARG
         assert product(out=off, odt=dtype) == ARG
     assert product(out=0, orows=rows(ts=258)) == ARG
+
+
+def test_widths_next_to_32_bits_are_refused(ops):
+    """Columns and rows of whole tiles are counted in 32 bits."""
+    def product(x, N):
+        return ops.lib.csf_expert_matmul(ops._EXPERT_MATMUL.pack(
+            *x, 0, 4, 1, N, 256, 256, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 256, 1 << 31, *(0,) * 8, 0), None)
+
+    assert product(rows(), 2 ** 31 - 1) == UNSUPPORTED
+    k = 2 ** 31 - 128
+    assert product(rows(cols=k, cs=k // 2, ss=k // 16 + 16), 128) == UNSUPPORTED
