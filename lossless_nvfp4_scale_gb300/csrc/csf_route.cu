@@ -397,7 +397,7 @@ extern "C" csf_status csf_route(const csf_route_args *a, void *stream) {
     p.rows = a->rows;
     p.slots = a->slots;
     p.weights = a->weights;
-    const int blocks = (p.T + kRouteTokens - 1) / kRouteTokens;
+    const int blocks = (int)(((int64_t)p.T + kRouteTokens - 1) / kRouteTokens);
     p.totals = static_cast<uint32_t *>(a->scratch);
     p.counts = p.totals + p.E;
     if (p.T == 0) {

@@ -769,3 +769,24 @@ def test_matmul_of_rows_past_2_31_bytes(ops):
     ops.expert_matmul(q.x, w, ws, out=out)
     q.check(torch.cat([out[:, :128], out[:, far:]], 1))
     assert not out[:, 128:far].any()
+
+
+# ---- the most tokens that a router call takes ---------------------------------------------------------------------------
+
+def test_route_of_2_31_minus_1_tokens(ops):
+    """One expert, k = 1: choice and slot of token t are 0 and t, except where the expert is off."""
+    T = 2 ** 31 - 1
+    v = torch.zeros(T, 1, dtype=BF16, device="cuda")
+    v[5], v[T - 2] = -math.inf, -math.inf
+    r = ops.route(v, 1)
+    assert r.expert_start.tolist() == [0, T - 2]
+    for lo in range(0, T, 1 << 28):
+        hi = min(T, lo + (1 << 28))
+        t = torch.arange(lo, hi, dtype=torch.int32, device="cuda")
+        on = (t != 5) & (t != T - 2)
+        assert torch.equal(r.ids[lo:hi, 0], on.int() - 1)
+        assert torch.equal(r.weights[lo:hi, 0], on.float())
+        slot = t - (t > 5).int() - (t > T - 2).int()
+        assert torch.equal(r.slots[lo:hi, 0], torch.where(on, slot, torch.full_like(slot, -1)))
+        row = t + (t >= 5).int() + (t >= T - 3).int()
+        assert torch.equal(r.rows[lo:hi], torch.where(t < T - 2, row, torch.full_like(row, -1)))
