@@ -65,7 +65,9 @@ typedef struct {
 /*
  * h = x + residual (in 32 bits); sum_out = h rounded to the type of x;
  * y = h / sqrt(mean(h^2) + eps) * weight, quantised to `out`.  The norm is of
- * the unrounded h.
+ * the unrounded h, over the whole range of finite h: squares past float32's
+ * range are summed scaled.  An infinite h makes its own y NaN and the row's
+ * others 0, a NaN all of them NaN.
  */
 typedef struct {
     const void *x;          /* [rows][cols] of dtype, row stride x_stride elements */

@@ -20,6 +20,22 @@ namespace {
 
 constexpr int kNormMaxThreads = 1024;
 
+// Mean squares from kLeastMean up to infinity are taken as they are: what
+// underflows below them does not count.  Smaller rows are taken 2^96 times
+// larger (their values are below 2^-38, rows having 2^24 at most), others
+// 2^80 times smaller (values below 2^48), so that their squares and sums stay
+// in range.  (What loses bits by the latter is below 2^-46 in a row whose mean
+// square is above 2^104: below 2^-98 in the result.)
+constexpr float kLeastMean = 0x1p-100f, kUp = 0x1p96f, kDown = 0x1p-80f;
+
+// Where the registers are full (rows loaded ahead by a whole block) such rows
+// are marked and done when the block's others are: 16384 rows of 5120 to NVFP4
+// take 86 us, as without, and 97 with a branch for them in the loop.  Else
+// they are done at once.  The mark is an NVFP4 row's first scale (UE4M3, a
+// byte below 0x80) or an MXFP8 row's first code (the conversion's NaN is
+// 0x7F).
+constexpr uint8_t kAgain = 0xFF;
+
 struct NormParams {
     const void *x, *residual, *weight;
     void *sum;
@@ -108,6 +124,71 @@ __host__ __device__ constexpr int max_ahead() {
     return sizeof(T) == 4 ? 512 : kNormMaxThreads;
 }
 
+// A row's sum over its block or warp; `part` holds the warps' sums.
+template <bool WARP>
+__device__ __forceinline__ float add_up(float sum, float (&part)[32]) {
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
+    if constexpr (!WARP) {
+        const int lane = threadIdx.x & 31;
+        if (lane == 0) part[threadIdx.x >> 5] = sum;
+        __syncthreads();
+        sum = lane < (int)(blockDim.x >> 5) ? part[lane] : 0.f;
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
+    }
+    return sum;
+}
+
+// Whether a mean square can be taken as it is.
+__device__ __forceinline__ bool in_range(float mean) { return mean >= kLeastMean && mean < __int_as_float(0x7F800000); }
+
+// Mean square (plus eps) of a row that is read twice, of h times k.
+template <typename T, bool WARP>
+__device__ __forceinline__ float mean_of_row(const NormParams &p, int64_t row, float k, int tid, int threads, float (&part)[32]) {
+    float sum = 0.f;
+    for (int c = tid; c < p.chunks; c += threads) {
+        float h[8];
+        load_h<T>(h, p, row, c * 8);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum = fmaf(h[i] * k, h[i] * k, sum);
+    }
+    return add_up<WARP>(sum, part) * p.inv_cols + p.eps * k * k;
+}
+
+// A row that is read twice, its values any finite numbers.  (Rows of 20000
+// take 1 to 4% longer with the factor k.)
+template <typename T, int KIND, bool WARP>
+__device__ __forceinline__ void whole_row(const NormParams &p, int64_t row, int tid, int threads, float g, float (&part)[3][32]) {
+    float k = 1.f, mean = mean_of_row<T, WARP>(p, row, k, tid, threads, part[0]);
+    if (!in_range(mean)) {
+        k = mean < 1.f ? kUp : kDown;
+        mean = mean_of_row<T, WARP>(p, row, k, tid, threads, part[1]);
+    }
+    const float r = rsqrtf(mean);
+    uint8_t *codes = p.codes + row * p.code_stride, *scales = p.scales + row * p.scale_stride;
+    for (int c0 = 0; c0 < p.chunks; c0 += threads) {
+        const int c = c0 + tid;
+        float h[8], w[8];
+        load_h<T>(h, p, row, c * 8);
+        if (p.sum) store8(h, static_cast<T *>(p.sum) + row * p.sum_stride, c * 8, p.cols, p.wide_sum);
+        load8(w, static_cast<const T *>(p.weight), c * 8, p.cols, p.wide_weight);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) h[i] = h[i] * k * r * w[i];
+        quant::quantize8<KIND>(h, codes, scales, c, c < p.chunks, g);
+    }
+    const int blocks = KIND == CSF_ROWS_MXFP8 ? p.chunks >> 2 : p.chunks >> 1;
+    if (tid < ((blocks + 15) & ~15) - blocks) scales[blocks + tid] = 0;
+    if constexpr (!WARP) __syncthreads();      // part[0] is read
+}
+
+// The same as a function of its own: inlined, it cost two-chunk kernels spilled
+// registers (91 us for the NVFP4 rows above).
+template <typename T, int KIND, bool WARP>
+__device__ __noinline__ void whole_row_apart(const NormParams &p, int64_t row, int tid, int threads, float g, float (&part)[3][32]) {
+    whole_row<T, KIND, WARP>(p, row, tid, threads, g, part);
+}
+
 // One row at a time per block of blockDim.x threads (WARP: per warp), rows a
 // grid apart.
 //   CHUNKS > 0  a row stays in registers, that many chunks a thread; 0: it is
@@ -117,83 +198,90 @@ __host__ __device__ constexpr int max_ahead() {
 template <typename T, int KIND, int CHUNKS, bool WARP, bool AHEAD>
 __global__ void __launch_bounds__(WARP ? 256 : AHEAD ? max_ahead<T>() : kNormMaxThreads)
 rms_norm_kernel(const __grid_constant__ NormParams p) {
-    __shared__ float part[2][32];
-    constexpr int kHeld = CHUNKS > 0 ? CHUNKS : 1;
+    __shared__ float part[3][32];      // two rows' in turn: one's are read while the next one's are written; a row done again
+    __shared__ uint32_t again;         // a row is marked
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int tid = WARP ? lane : threadIdx.x, threads = WARP ? 32 : blockDim.x;
     const int per_block = WARP ? blockDim.x >> 5 : 1;
     const int64_t step = (int64_t)gridDim.x * per_block;
-    const T *weight = static_cast<const T *>(p.weight);
     const float g = KIND == CSF_ROWS_NVFP4 && p.tensor_scale ? *p.tensor_scale : 1.f;
-    const int blocks = KIND == CSF_ROWS_MXFP8 ? p.chunks >> 2 : p.chunks >> 1;
-    constexpr bool kHoldWeight = AHEAD && sizeof(T) == 2;      // 32-bit ones would not fit the registers
-    Raw<T> xr[kHeld], rr[kHeld], wr[kHeld];
-    auto load_ahead = [&](int64_t row) {
-#pragma unroll
-        for (int j = 0; j < kHeld; ++j) {
-            const int c = (tid + j * threads) * 8;
-            if (c >= p.cols) continue;
-            load_raw(xr[j], static_cast<const T *>(p.x) + row * p.x_stride + c);
-            if (p.residual) load_raw(rr[j], static_cast<const T *>(p.residual) + row * p.residual_stride + c);
-        }
-    };
     int64_t row = (int64_t)blockIdx.x * per_block + (WARP ? warp : 0);
-    if constexpr (AHEAD) {
-#pragma unroll
-        for (int j = 0; j < kHeld; ++j) {
-#pragma unroll
-            for (int i = 0; i < (int)(sizeof(T) / 2); ++i) xr[j].q[i] = rr[j].q[i] = wr[j].q[i] = make_uint4(0, 0, 0, 0);
-            const int c = (tid + j * threads) * 8;
-            if (kHoldWeight && c < p.cols) load_raw(wr[j], weight + c);
-        }
-        if (row < p.rows) load_ahead(row);
-    }
-    for (int set = 0; row < p.rows; row += step, set ^= 1) {
-        float h[kHeld][8];
-        float sum = 0.f;
-        if constexpr (AHEAD) {
-#pragma unroll
-            for (int j = 0; j < kHeld; ++j) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    h[j][i] = Elem<T>::to(xr[j].e[i]);
-                    if (p.residual) h[j][i] += Elem<T>::to(rr[j].e[i]);
-                }
-            }
-            if (row + step < p.rows) load_ahead(row + step);
-        } else if constexpr (CHUNKS > 0) {
-#pragma unroll
-            for (int j = 0; j < CHUNKS; ++j) load_h<T>(h[j], p, row, (tid + j * threads) * 8);
-        }
-        if constexpr (CHUNKS > 0) {
+    if constexpr (CHUNKS == 0) {
+        for (; row < p.rows; row += step) whole_row<T, KIND, WARP>(p, row, tid, threads, g, part);
+    } else {
+        constexpr bool kMark = AHEAD && !WARP && (CHUNKS == 2 || sizeof(T) == 2);
+        const T *weight = static_cast<const T *>(p.weight);
+        const int blocks = KIND == CSF_ROWS_MXFP8 ? p.chunks >> 2 : p.chunks >> 1;
+        constexpr bool kHoldWeight = AHEAD && sizeof(T) == 2;      // 32-bit ones would not fit the registers
+        Raw<T> xr[CHUNKS], rr[CHUNKS], wr[CHUNKS];
+        auto load_ahead = [&](int64_t row) {
 #pragma unroll
             for (int j = 0; j < CHUNKS; ++j) {
-                if (p.sum) store8(h[j], static_cast<T *>(p.sum) + row * p.sum_stride, (tid + j * threads) * 8, p.cols, p.wide_sum);
+                const int c = (tid + j * threads) * 8;
+                if (c >= p.cols) continue;
+                load_raw(xr[j], static_cast<const T *>(p.x) + row * p.x_stride + c);
+                if (p.residual) load_raw(rr[j], static_cast<const T *>(p.residual) + row * p.residual_stride + c);
+            }
+        };
+        if constexpr (AHEAD) {
+#pragma unroll
+            for (int j = 0; j < CHUNKS; ++j) {
+#pragma unroll
+                for (int i = 0; i < (int)(sizeof(T) / 2); ++i) xr[j].q[i] = rr[j].q[i] = wr[j].q[i] = make_uint4(0, 0, 0, 0);
+                const int c = (tid + j * threads) * 8;
+                if (kHoldWeight && c < p.cols) load_raw(wr[j], weight + c);
+            }
+            if (row < p.rows) load_ahead(row);
+        }
+        if (kMark && threadIdx.x == 0) again = 0;      // that thread sets it, too
+        for (int set = 0; row < p.rows; row += step, set ^= 1) {
+            float h[CHUNKS][8];
+            float sum = 0.f;
+            if constexpr (AHEAD) {
+#pragma unroll
+                for (int j = 0; j < CHUNKS; ++j) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        h[j][i] = Elem<T>::to(xr[j].e[i]);
+                        if (p.residual) h[j][i] += Elem<T>::to(rr[j].e[i]);
+                    }
+                }
+                if (row + step < p.rows) load_ahead(row + step);
+            } else {
+#pragma unroll
+                for (int j = 0; j < CHUNKS; ++j) load_h<T>(h[j], p, row, (tid + j * threads) * 8);
+            }
+#pragma unroll
+            for (int j = 0; j < CHUNKS; ++j) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) sum = fmaf(h[j][i], h[j][i], sum);
             }
-        } else {
-            for (int c = tid; c < p.chunks; c += threads) {
-                load_h<T>(h[0], p, row, c * 8);
+            auto store_sum = [&](int j) {
+                store8(h[j], static_cast<T *>(p.sum) + row * p.sum_stride, (tid + j * threads) * 8, p.cols, p.wide_sum);
+            };
+            if (!kMark && p.sum) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) sum = fmaf(h[0][i], h[0][i], sum);
+                for (int j = 0; j < CHUNKS; ++j) store_sum(j);
             }
-        }
+            float mean = add_up<WARP>(sum, part[set]) * p.inv_cols + p.eps;
+            const bool keep = in_range(mean);
+            if (!kMark && !keep) {      // alike in every thread of the row
+                const float k = mean < 1.f ? kUp : kDown;
+                sum = 0.f;
 #pragma unroll
-        for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
-        if constexpr (!WARP) {
-            if (lane == 0) part[set][warp] = sum;
-            __syncthreads();
-            sum = lane < (threads >> 5) ? part[set][lane] : 0.f;
+                for (int j = 0; j < CHUNKS; ++j) {
 #pragma unroll
-            for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
-        }
-        const float r = rsqrtf(sum * p.inv_cols + p.eps);
-        uint8_t *codes = p.codes + row * p.code_stride, *scales = p.scales + row * p.scale_stride;
-        if constexpr (CHUNKS > 0) {
+                    for (int i = 0; i < 8; ++i) h[j][i] *= k, sum = fmaf(h[j][i], h[j][i], sum);
+                }
+                mean = add_up<WARP>(sum, part[2]) * p.inv_cols + p.eps * k * k;
+            }
+            const float r = rsqrtf(mean);
+            uint8_t *codes = p.codes + row * p.code_stride, *scales = p.scales + row * p.scale_stride;
 #pragma unroll
             for (int j = 0; j < CHUNKS; ++j) {
                 const int c = tid + j * threads;
+                // only now: a row that is not kept is read again, and the sum may go where it lies
+                if (kMark && p.sum && keep) store_sum(j);
                 float w[8];
                 if constexpr (kHoldWeight) {
 #pragma unroll
@@ -205,19 +293,25 @@ rms_norm_kernel(const __grid_constant__ NormParams p) {
                 for (int i = 0; i < 8; ++i) h[j][i] = h[j][i] * r * w[i];
                 quant::quantize8<KIND>(h[j], codes, scales, c, c < p.chunks, g);
             }
-        } else {
-            for (int c0 = 0; c0 < p.chunks; c0 += threads) {
-                const int c = c0 + tid;
-                load_h<T>(h[0], p, row, c * 8);
-                if (p.sum) store8(h[0], static_cast<T *>(p.sum) + row * p.sum_stride, c * 8, p.cols, p.wide_sum);
-                float w[8];
-                load8(w, weight, c * 8, p.cols, p.wide_weight);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) h[0][i] = h[0][i] * r * w[i];
-                quant::quantize8<KIND>(h[0], codes, scales, c, c < p.chunks, g);
+            if (kMark && !keep && tid == 0) {
+                *(KIND == CSF_ROWS_NVFP4 ? scales : codes) = kAgain;
+                again = 1;
             }
+            if (tid < ((blocks + 15) & ~15) - blocks) scales[blocks + tid] = 0;
         }
-        if (tid < ((blocks + 15) & ~15) - blocks) scales[blocks + tid] = 0;
+        if constexpr (!kMark) return;
+        __syncthreads();      // the marks are written
+        if (!again) return;
+        // opaque copies: nothing of this is to be held in registers before
+        int tid1 = tid, threads1 = threads;
+        float g1 = g;
+        asm volatile("" : "+r"(tid1), "+r"(threads1), "+f"(g1)::"memory");
+        for (row = blockIdx.x; row < p.rows; row += step) {
+            const uint8_t *mark = KIND == CSF_ROWS_NVFP4 ? p.scales + row * p.scale_stride : p.codes + row * p.code_stride;
+            if (*const_cast<const volatile uint8_t *>(mark) != kAgain) continue;
+            if constexpr (CHUNKS == 1) whole_row<T, KIND, WARP>(p, row, tid1, threads1, g1, part);
+            else whole_row_apart<T, KIND, WARP>(p, row, tid1, threads1, g1, part);
+        }
     }
 }
 

@@ -34,7 +34,8 @@ __device__ __forceinline__ uint32_t nv_scale(uint32_t amax_bits, float six_tenso
     return __nv_cvt_float_to_fp8(__fdiv_rn(__uint_as_float(amax_bits), six_tensor_scales), __NV_SATFINITE, __NV_E4M3);
 }
 
-// scale * tensor scale, and its inverse (0 for a zero scale).
+// scale * tensor scale, and its inverse to a unit in the last place (0 for a
+// zero scale; whole ones are normal numbers up to 2^126).
 struct Whole {
     float value, inverse;
 };
@@ -43,7 +44,9 @@ __device__ __forceinline__ Whole nv_whole(uint32_t byte, float tensor_scale) {
     const float s = __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)byte, __NV_E4M3)));
     Whole w;
     w.value = s * tensor_scale;
-    w.inverse = s > 0.f ? 1.f / w.value : 0.f;
+    float inverse;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inverse) : "f"(w.value));
+    w.inverse = s > 0.f ? inverse : 0.f;
     return w;
 }
 

@@ -790,3 +790,62 @@ def test_route_of_2_31_minus_1_tokens(ops):
         assert torch.equal(r.slots[lo:hi, 0], torch.where(on, slot, torch.full_like(slot, -1)))
         row = t + (t >= 5).int() + (t >= T - 3).int()
         assert torch.equal(r.rows[lo:hi], torch.where(t < T - 2, row, torch.full_like(row, -1)))
+
+
+# ---- rows whose squares leave float32's range ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("kind", [0, 1])
+@pytest.mark.parametrize("cols", [40, 64, 257, 1600, 5120, 5121, 20000])
+def test_norm_of_rows_whose_squares_overflow_or_underflow(ops, cols, kind, dtype):
+    g = gen(cols)
+    x = torch.randn(6, cols, device="cuda", generator=g)
+    size = torch.tensor([1e37, 1e25, 3e19, 1.0, 1e-25, 1e-37], device="cuda")[:, None]
+    x = (x * size).to(dtype)
+    x[0, 0] = torch.finfo(dtype).max
+    w = (1 + 0.3 * torch.randn(cols, device="cuda", generator=g)).to(dtype)
+    ts = torch.tensor([0.02], device="cuda") if kind == ops.NVFP4 else None
+    q, _ = ops.rms_norm(x, w, kind, eps=0.0, tensor_scale=ts)
+    check_norm(q, None, x, w, None, 0.0, ops)
+    r = torch.zeros_like(x)
+    q2, total = ops.rms_norm(x, w, kind, residual=r, eps=1e-6, tensor_scale=ts)
+    check_norm(q2, total, x, w, r, 1e-6, ops)
+
+
+@pytest.mark.parametrize("kind", [0, 1])
+def test_norm_of_one_huge_value(ops, kind):
+    """The row that test_norm_zero_huge_and_non_finite_rows makes: one value of 3e37 among 63 zeros has norm 8."""
+    x = torch.zeros(2, 64, device="cuda")
+    x[0, 5], x[1, 3] = 3e37, 1e-30
+    w = torch.ones(64, device="cuda")
+    q, _ = ops.rms_norm(x, w, kind, eps=1e-6)
+    check_norm(q, None, x, w, None, 1e-6, ops)
+    assert (values(q, ops)[0, 5] - 8).abs() <= 0.5 and (values(q, ops)[0].abs().sum() - 8).abs() <= 0.5
+
+
+@pytest.mark.parametrize("kind", [0, 1])
+@pytest.mark.parametrize("cols,off", [(64, 0), (64, 1), (640, 0), (4096, 0), (16400, 0)])
+def test_norm_of_many_rows_some_out_of_range(ops, cols, off, kind):
+    """Blocks that take several rows, the residual stream updated in place; a NaN weight of either sign marks nothing."""
+    rows = 3000
+    g = gen(cols + off)
+    x = torch.randn(rows, cols, device="cuda", generator=g)
+    r = torch.randn(rows, cols + off, device="cuda", generator=g)
+    size = torch.ones(rows, 1, device="cuda")
+    size[::5], size[3::7], size[2::11] = 1e30, 1e-30, 1e19
+    x = (x * size).to(BF16)
+    r = (r * size).to(BF16)[:, off:]
+    w = (1 + 0.3 * torch.randn(cols, device="cuda", generator=g)).to(BF16)
+    ts = torch.tensor([0.02], device="cuda") if kind == ops.NVFP4 else None
+    r0, r1 = r.clone(), r.clone()
+    q, total = ops.rms_norm(x, w, kind, residual=r, sum_out=r, eps=0.0, tensor_scale=ts)
+    check_norm(q, total, x, w, r0, 0.0, ops)
+    for sign in (-32768, 0):
+        w2 = w.clone()
+        w2.view(torch.int16)[0] = 0x7FC0 + sign
+        r2 = r1.clone()
+        q2, total2 = ops.rms_norm(x, w2, kind, residual=r2, sum_out=r2, eps=0.0, tensor_scale=ts)
+        assert torch.equal(total2, total) and torch.equal(q2.scales[:, 1:], q.scales[:, 1:])
+        block = 16 if kind == ops.NVFP4 else 32
+        assert torch.isnan(scale_values(q2.scales[:, 0], kind, ops)).all()
+        assert torch.equal(code_values(q2, ops)[:, block:], code_values(q, ops)[:, block:])
