@@ -102,7 +102,7 @@ class Quantized:
     """Quantised rows (csf_rows): uint8 codes [rows, code bytes] and scales
     [rows, scale bytes], rows 16-byte aligned.  `tensor_scale` is the NVFP4
     tensor scale they were made with (float32 [1]) or None; a product takes it
-    through its alpha."""
+    through its alpha.  As an output they keep theirs where a call gives none."""
     kind: int
     codes: torch.Tensor
     scales: torch.Tensor
@@ -141,6 +141,16 @@ def _check_quantized(q: Quantized, what: str):
         raise CsfError(f"{what}: codes and scales must be [rows, bytes] with contiguous rows")
     if q.cols < 1 or c.shape[1] < _code_bytes(q.kind, q.cols) or s.shape[1] < _scale_bytes(q.kind, q.cols):
         raise CsfError(f"{what}: codes or scales are too narrow for {q.cols} columns")
+
+
+def _tensor_scale(out: Quantized, given: torch.Tensor | None, what: str) -> torch.Tensor | None:
+    """The tensor scale of a quantised output: the argument, or the one it has."""
+    scale = out.tensor_scale if given is None else given
+    if scale is not None:
+        if out.kind != NVFP4:
+            raise CsfError(f"{what}: only NVFP4 rows have a tensor scale")
+        _vector(scale, f"{what}: the tensor scale", 1, torch.float32)
+    return scale
 
 
 def _matrix(t, name: str, rows: int, cols: int, dtype=None):
@@ -183,10 +193,7 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, kind: int, residual: torch.T
         _check_quantized(out, "rms_norm: out")
         if out.kind != kind or out.rows != rows or out.cols != cols:
             raise CsfError("rms_norm: out does not match x and kind")
-        out.tensor_scale = tensor_scale
-    _vector(tensor_scale, "rms_norm: tensor_scale", 1, torch.float32)
-    if tensor_scale is not None and kind != NVFP4:
-        raise CsfError("rms_norm: only NVFP4 rows have a tensor scale")
+    out.tensor_scale = _tensor_scale(out, tensor_scale, "rms_norm")
     a = _RMS_NORM.pack(xp, xs, rp, rs, sp, ss, wp, _DTYPES[x.dtype], eps, *out.fields())
     status = lib.csf_rms_norm(a, _raw_stream(x.device.index))
     if status:
@@ -285,8 +292,7 @@ def expert_matmul(x: Quantized, w: torch.Tensor, w_scales: torch.Tensor, expert_
         _check_quantized(out, "expert_matmul: out")
         if out.rows != S or out.cols != F:
             raise CsfError("expert_matmul: out does not match the product")
-        out.tensor_scale = out_tensor_scale
-        _vector(out_tensor_scale, "expert_matmul: out_tensor_scale", 1, torch.float32)
+        out.tensor_scale = _tensor_scale(out, out_tensor_scale, "expert_matmul")
         op, os_, odt, orows = 0, 0, 0, out.fields()
     else:
         op, os_ = _matrix(out, "expert_matmul: out", S, F)

@@ -849,3 +849,25 @@ def test_norm_of_many_rows_some_out_of_range(ops, cols, off, kind):
         block = 16 if kind == ops.NVFP4 else 32
         assert torch.isnan(scale_values(q2.scales[:, 0], kind, ops)).all()
         assert torch.equal(code_values(q2, ops)[:, block:], code_values(q, ops)[:, block:])
+
+
+# ---- tensor scales of quantised outputs ---------------------------------------------------------------------------------
+
+def test_a_quantized_output_brings_its_tensor_scale(ops):
+    ts = torch.tensor([0.25], device="cuda")
+    q = Problem(ops, ops.NVFP4, [9], 64, 64, seed=22)
+    want = q.run(out=ops.NVFP4, out_tensor_scale=ts)
+    mine = q.run(out=ops.empty_quantized(ops.NVFP4, 9, 64, tensor_scale=ts))
+    assert mine.tensor_scale is ts
+    assert torch.equal(mine.codes, want.codes) and torch.equal(mine.scales, want.scales)
+    x, w = torch.randn(5, 64, **q.dev), torch.ones(64, device="cuda")
+    want, _ = ops.rms_norm(x, w, ops.NVFP4, tensor_scale=ts)
+    mine, _ = ops.rms_norm(x, w, ops.NVFP4, out=ops.empty_quantized(ops.NVFP4, 5, 64, tensor_scale=ts))
+    assert mine.tensor_scale is ts
+    assert torch.equal(mine.codes, want.codes) and torch.equal(mine.scales, want.scales)
+    with pytest.raises(ops.CsfError, match="tensor scale"):
+        q.run(out=ops.MXFP8, out_tensor_scale=ts)
+    out = ops.empty_quantized(ops.MXFP8, 9, 64)
+    with pytest.raises(ops.CsfError, match="tensor scale"):
+        q.run(out=out, out_tensor_scale=ts)
+    assert out.tensor_scale is None                       # a refused call changes nothing
