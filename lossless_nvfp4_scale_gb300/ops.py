@@ -12,6 +12,9 @@ Typical use (one layer of experts)::
     a = ops.expert_matmul(q, w_gate_up, ws, expert_start=r.expert_start, rows=r.rows, alpha=alpha,
                           activation="silu", gated=True, out=ops.NVFP4, out_tensor_scale=g2)
     y = ops.expert_matmul(a, w_down, down_ws, expert_start=r.expert_start, alpha=alpha2)
+
+A call runs on the current stream, or on `stream`, where new results are then
+that stream's.  Ordering the streams (wait_stream) is the caller's.
 """
 from __future__ import annotations
 
@@ -78,11 +81,17 @@ def errors(device: int | None = None) -> int:
     return bits
 
 
-def _on(stream, call, *args, **kwargs):
+def _on(stream, call, *args):
     """The call with `stream` current, so that what it allocates is the
-    stream's own."""
+    stream's own; what it reads or writes of other streams' is kept until it
+    has run, also where the caller lets go of it before."""
     with torch.cuda.stream(stream):
-        return call(*args, **kwargs)
+        result = call(*args)
+    for a in args:
+        for t in (a.codes, a.scales, a.tensor_scale) if isinstance(a, Quantized) else (a,):
+            if isinstance(t, torch.Tensor):
+                t.record_stream(stream)
+    return result
 
 
 def _up(n: int, m: int) -> int:

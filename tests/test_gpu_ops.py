@@ -871,3 +871,30 @@ def test_a_quantized_output_brings_its_tensor_scale(ops):
     with pytest.raises(ops.CsfError, match="tensor scale"):
         q.run(out=out, out_tensor_scale=ts)
     assert out.tensor_scale is None                       # a refused call changes nothing
+
+
+# ---- streams and error words --------------------------------------------------------------------------------------------
+
+def test_inputs_freed_while_another_stream_still_reads_them(ops):
+    """A call on a side stream keeps what it reads until it has run, also where the caller lets go of it at once."""
+    side = torch.cuda.Stream()
+    q = Problem(ops, ops.NVFP4, [300], 256, 320, seed=23)
+    w = torch.ones(1600, device="cuda")
+    x, logits = torch.randn(3000, 1600, **q.dev), torch.randn(3000, 256, **q.dev)
+    want_x, _ = ops.rms_norm(x, w, ops.MXFP8)
+    want_r, want_p = ops.route(logits, 4), q.run(out=F32)
+    torch.cuda.synchronize()
+    x2, l2, p2 = x.clone(), logits.clone(), ops.Quantized(q.kind, q.x.codes.clone(), q.x.scales.clone(), q.K)
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)                     # some milliseconds
+    got_x, _ = ops.rms_norm(x2, w, ops.MXFP8, stream=side)
+    got_r = ops.route(l2, 4, stream=side)
+    got_p = ops.expert_matmul(p2, q.w, q.ws, expert_start=q.start, out=F32, stream=side)
+    shapes = [(t.shape, t.dtype) for t in (x2, l2, p2.codes, p2.scales)]
+    del x2, l2, p2
+    again = [torch.zeros(s, dtype=d, device="cuda") for s, d in shapes]      # would take the freed memory
+    torch.cuda.synchronize()
+    assert torch.equal(got_x.codes, want_x.codes) and torch.equal(got_p, want_p)
+    assert torch.equal(got_r.ids, want_r.ids) and torch.equal(got_r.weights, want_r.weights)
+    del again
