@@ -20,6 +20,7 @@ from __future__ import annotations
 
 import ctypes
 import struct
+import threading
 from dataclasses import dataclass
 
 import torch
@@ -55,29 +56,34 @@ _raw_stream = torch._C._cuda_getCurrentRawStream
 
 
 _error_words: dict[int, torch.Tensor] = {}
+_error_lock = threading.RLock()     # held from choosing a device's word to the launch, and while it is read and cleared
 
 
-def _error_word(device: int) -> int:
+def _error_word(device: int) -> torch.Tensor:
     """The device's own error word, for calls that bring none."""
     word = _error_words.get(device)
     if word is None:
         if torch.cuda.is_current_stream_capturing():
-            return 0                    # nothing to allocate in a graph
+            raise CsfError("no memory for the device's error word within a capture: call errors() before it, or give error_word")
         word = _error_words[device] = torch.zeros(1, dtype=torch.int32, device=torch.device("cuda", device))
         torch.cuda.synchronize(device)  # once: any stream may set it from here on
-    return word.data_ptr()
+    return word
 
 
 def errors(device: int | None = None) -> int:
     """CSF_DEV_ERR_* bits of the expert_matmul calls on a device that were given
-    no error_word, and clears them.  Synchronises."""
+    no error_word, and clears them.  Synchronises; calls of other threads wait
+    meanwhile.  (Not so replays of captured calls: what one sets between the
+    reading and the clearing is lost.)  Before a capture of such calls it makes
+    the word that they report to."""
     device = torch.cuda.current_device() if device is None else device
-    torch.cuda.synchronize(device)
-    word = _error_words.get(device)
-    if word is None:
-        return 0
-    bits = int(word.item())
-    word.zero_()
+    with _error_lock:
+        word = _error_word(device)
+        torch.cuda.synchronize(device)
+        bits = int(word.item())
+        if bits:
+            word.zero_()
+            torch.cuda.synchronize(device)      # before any stream's next call
     return bits
 
 
@@ -307,14 +313,17 @@ def expert_matmul(x: Quantized, w: torch.Tensor, w_scales: torch.Tensor, expert_
         op, os_ = _matrix(out, "expert_matmul: out", S, F)
         odt, orows = _DTYPES[out.dtype], _NO_ROWS
     device = w.device.index
-    a = _EXPERT_MATMUL.pack(
-        *x.fields(), 0 if rows is None else rows.data_ptr(), S, E, N, w.data_ptr(), w_scales.data_ptr(), es or 0, es64,
-        _vector(alpha, "expert_matmul: alpha", E, torch.float32),
-        0 if bias is None else _vector(bias, "expert_matmul: bias", E * N, bias.dtype), bias_dtype, _ACTS[activation],
-        gated, _vector(row_scale, "expert_matmul: row_scale", S, torch.float32), rp, rs,
-        0 if residual is None else _DTYPES[residual.dtype], odt, op, os_, *orows,
-        _error_word(device) if error_word is None else _vector(error_word, "expert_matmul: error_word", 1, torch.int32))
-    status = lib.csf_expert_matmul(a, _raw_stream(device))
+    fields = (*x.fields(), 0 if rows is None else rows.data_ptr(), S, E, N, w.data_ptr(), w_scales.data_ptr(), es or 0, es64,
+              _vector(alpha, "expert_matmul: alpha", E, torch.float32),
+              0 if bias is None else _vector(bias, "expert_matmul: bias", E * N, bias.dtype), bias_dtype, _ACTS[activation],
+              gated, _vector(row_scale, "expert_matmul: row_scale", S, torch.float32), rp, rs,
+              0 if residual is None else _DTYPES[residual.dtype], odt, op, os_, *orows)
+    if error_word is None:
+        with _error_lock:
+            status = lib.csf_expert_matmul(_EXPERT_MATMUL.pack(*fields, _error_word(device).data_ptr()), _raw_stream(device))
+    else:
+        word = _vector(error_word, "expert_matmul: error_word", 1, torch.int32)
+        status = lib.csf_expert_matmul(_EXPERT_MATMUL.pack(*fields, word), _raw_stream(device))
     if status:
         _check(status, "csf_expert_matmul")
     return out

@@ -898,3 +898,66 @@ def test_inputs_freed_while_another_stream_still_reads_them(ops):
     assert torch.equal(got_x.codes, want_x.codes) and torch.equal(got_p, want_p)
     assert torch.equal(got_r.ids, want_r.ids) and torch.equal(got_r.weights, want_r.weights)
     del again
+
+
+def test_errors_of_a_captured_call_without_an_error_word(ops):
+    """A call is captured with the device's own word or refused; replays report there."""
+    from lossless_nvfp4_scale_gb300 import csf
+    q = Problem(ops, ops.NVFP4, [6, 7], 64, 64, seed=8, gather=5)
+    side = torch.cuda.Stream()
+    out = torch.empty(13, 64, device="cuda")
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        q.run(out=out, error_word=torch.zeros(1, dtype=torch.int32, device="cuda"))       # no word of its own needed
+    side.synchronize()
+    kept = dict(ops._error_words)
+    ops._error_words.clear()
+    try:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            with pytest.raises(ops.CsfError, match="capture"):
+                q.run(out=out)
+            q.run(out=out, error_word=torch.zeros(1, dtype=torch.int32, device="cuda"))
+    finally:
+        ops._error_words.clear()
+        ops._error_words.update(kept)
+    assert ops.errors() == 0                               # makes the word where there is none
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        q.run(out=out)
+    graph.replay()
+    assert ops.errors() == 0
+    q.rows[2] = 99
+    graph.replay()
+    assert ops.errors() == csf.DEV_ERR_CORRUPT and ops.errors() == 0
+
+
+def test_errors_of_two_threads_are_not_lost(ops):
+    """One thread makes bad calls, another reads and clears: each bad call is seen by one that ends after it."""
+    import threading
+    from lossless_nvfp4_scale_gb300 import csf
+    q = Problem(ops, ops.NVFP4, [6, 7], 64, 64, seed=8, gather=5)
+    q.rows[2] = 99
+    ops.errors()
+    stop, seen, side = threading.Event(), [], torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+
+    def reader():
+        while not stop.is_set():
+            seen.append(ops.errors())
+    t = threading.Thread(target=reader)
+    t.start()
+    lost = 0
+    try:
+        for _ in range(300):
+            before = len(seen)
+            q.run(stream=side)
+            side.synchronize()
+            ended = len(seen)
+            while len(seen) < ended + 2:                   # the second of these began after the call had ended
+                pass
+            lost += csf.DEV_ERR_CORRUPT not in seen[before:]
+    finally:
+        stop.set()
+        t.join()
+    assert lost == 0
