@@ -53,6 +53,20 @@ lib.csf_expert_matmul.argtypes = [ctypes.c_char_p, _vp]
 lib.csf_expert_matmul.restype = ctypes.c_int
 
 _raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
+
+
+def _launch(call, args: bytes, device: int, what: str):
+    """The library call on the tensors' device (a stream's handle, 0 of the
+    default one above all, means what it does on the current device) and that
+    device's current stream."""
+    if _current_device() == device:
+        status = call(args, _raw_stream(device))
+    else:
+        with torch.cuda.device(device):
+            status = call(args, _raw_stream(device))
+    if status:
+        _check(status, what)
 
 
 _error_words: dict[int, torch.Tensor] = {}
@@ -63,7 +77,9 @@ def _error_word(device: int) -> torch.Tensor:
     """The device's own error word, for calls that bring none."""
     word = _error_words.get(device)
     if word is None:
-        if torch.cuda.is_current_stream_capturing():
+        with torch.cuda.device(device):
+            capturing = torch.cuda.is_current_stream_capturing()
+        if capturing:
             raise CsfError("no memory for the device's error word within a capture: call errors() before it, or give error_word")
         word = _error_words[device] = torch.zeros(1, dtype=torch.int32, device=torch.device("cuda", device))
         torch.cuda.synchronize(device)  # once: any stream may set it from here on
@@ -91,6 +107,10 @@ def _on(stream, call, *args):
     """The call with `stream` current, so that what it allocates is the
     stream's own; what it reads or writes of other streams' is kept until it
     has run, also where the caller lets go of it before."""
+    device = (args[0].codes if isinstance(args[0], Quantized) else args[0]).get_device()
+    if stream.device.index != device:
+        raise CsfError(f"the stream is on cuda:{stream.device.index}, the tensors " +
+                       (f"on cuda:{device}" if device >= 0 else "are not CUDA tensors"))
     with torch.cuda.stream(stream):
         result = call(*args)
     for a in args:
@@ -146,41 +166,45 @@ def empty_quantized(kind: int, rows: int, cols: int, device=None, tensor_scale: 
                      torch.empty((rows, _scale_bytes(kind, cols)), dtype=torch.uint8, device=device), cols, tensor_scale)
 
 
-def _check_quantized(q: Quantized, what: str):
+def _where(device: int) -> str:
+    return f" on cuda:{device}" if device >= 0 else ""
+
+
+def _check_quantized(q: Quantized, what: str, device: int):
     c, s = q.codes, q.scales
     if q.kind not in (NVFP4, MXFP8):
         raise CsfError(f"{what}: quantised rows are NVFP4 or MXFP8")
-    if c.dtype != torch.uint8 or s.dtype != torch.uint8 or not c.is_cuda or not s.is_cuda:
-        raise CsfError(f"{what}: codes and scales must be uint8 CUDA tensors")
+    if c.dtype != torch.uint8 or s.dtype != torch.uint8 or device < 0 or c.get_device() != device or s.get_device() != device:
+        raise CsfError(f"{what}: codes and scales must be uint8 CUDA tensors{_where(device)}")
     if c.dim() != 2 or s.dim() != 2 or c.shape[0] != s.shape[0] or c.stride(1) != 1 or s.stride(1) != 1:
         raise CsfError(f"{what}: codes and scales must be [rows, bytes] with contiguous rows")
     if q.cols < 1 or c.shape[1] < _code_bytes(q.kind, q.cols) or s.shape[1] < _scale_bytes(q.kind, q.cols):
         raise CsfError(f"{what}: codes or scales are too narrow for {q.cols} columns")
 
 
-def _tensor_scale(out: Quantized, given: torch.Tensor | None, what: str) -> torch.Tensor | None:
+def _tensor_scale(out: Quantized, given: torch.Tensor | None, what: str, device: int) -> torch.Tensor | None:
     """The tensor scale of a quantised output: the argument, or the one it has."""
     scale = out.tensor_scale if given is None else given
     if scale is not None:
         if out.kind != NVFP4:
             raise CsfError(f"{what}: only NVFP4 rows have a tensor scale")
-        _vector(scale, f"{what}: the tensor scale", 1, torch.float32)
+        _vector(scale, f"{what}: the tensor scale", 1, torch.float32, device)
     return scale
 
 
-def _matrix(t, name: str, rows: int, cols: int, dtype=None):
-    if not t.is_cuda or t.dtype not in _DTYPES or (dtype is not None and t.dtype != dtype):
-        raise CsfError(f"{name} must be a CUDA tensor of {dtype or 'bfloat16, float16 or float32'}")
+def _matrix(t, name: str, rows: int, cols: int, device: int, dtype=None):
+    if device < 0 or t.get_device() != device or t.dtype not in _DTYPES or (dtype is not None and t.dtype != dtype):
+        raise CsfError(f"{name} must be a CUDA tensor of {dtype or 'bfloat16, float16 or float32'}{_where(device)}")
     if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols or (t.stride(1) != 1 and cols > 1):
         raise CsfError(f"{name} must be [{rows}, {cols}] with contiguous rows")
     return t.data_ptr(), (t.stride(0) if rows > 1 else max(t.stride(0), cols))
 
 
-def _vector(t, name: str, n: int, dtype):
+def _vector(t, name: str, n: int, dtype, device: int):
     if t is None:
         return 0
-    if not t.is_cuda or t.dtype != dtype or t.numel() != n or not t.is_contiguous():
-        raise CsfError(f"{name} must be a contiguous CUDA tensor of {n} {dtype}")
+    if t.get_device() != device or t.dtype != dtype or t.numel() != n or not t.is_contiguous():
+        raise CsfError(f"{name} must be a contiguous CUDA tensor of {n} {dtype}{_where(device)}")
     return t.data_ptr()
 
 
@@ -196,23 +220,22 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, kind: int, residual: torch.T
     if x.dim() != 2 or x.dtype not in _DTYPES:
         raise CsfError("rms_norm: x must be [rows, cols] of bfloat16, float16 or float32")
     rows, cols = x.shape
-    xp, xs = _matrix(x, "rms_norm: x", rows, cols)
-    rp, rs = (0, 0) if residual is None else _matrix(residual, "rms_norm: residual", rows, cols, x.dtype)
+    device = x.get_device()
+    xp, xs = _matrix(x, "rms_norm: x", rows, cols, device)
+    rp, rs = (0, 0) if residual is None else _matrix(residual, "rms_norm: residual", rows, cols, device, x.dtype)
     if sum_out is None and residual is not None:
         sum_out = torch.empty((rows, cols), dtype=x.dtype, device=x.device)
-    sp, ss = (0, 0) if sum_out is None else _matrix(sum_out, "rms_norm: sum_out", rows, cols, x.dtype)
-    wp = _vector(weight, "rms_norm: weight", cols, x.dtype)
+    sp, ss = (0, 0) if sum_out is None else _matrix(sum_out, "rms_norm: sum_out", rows, cols, device, x.dtype)
+    wp = _vector(weight, "rms_norm: weight", cols, x.dtype, device)
     if out is None:
         out = empty_quantized(kind, rows, cols, x.device, tensor_scale)
     else:
-        _check_quantized(out, "rms_norm: out")
+        _check_quantized(out, "rms_norm: out", device)
         if out.kind != kind or out.rows != rows or out.cols != cols:
             raise CsfError("rms_norm: out does not match x and kind")
-    out.tensor_scale = _tensor_scale(out, tensor_scale, "rms_norm")
+    out.tensor_scale = _tensor_scale(out, tensor_scale, "rms_norm", device)
     a = _RMS_NORM.pack(xp, xs, rp, rs, sp, ss, wp, _DTYPES[x.dtype], eps, *out.fields())
-    status = lib.csf_rms_norm(a, _raw_stream(x.device.index))
-    if status:
-        _check(status, "csf_rms_norm")
+    _launch(lib.csf_rms_norm, a, device, "csf_rms_norm")
     return out, sum_out
 
 
@@ -237,7 +260,8 @@ def route(logits: torch.Tensor, k: int, renormalize: bool = True, stream=None) -
     T, E = logits.shape
     if not 1 <= k <= min(32, E):
         raise CsfError(f"route: k must be 1 to {min(32, E)}")
-    lp, ls = _matrix(logits, "route: logits", T, E)
+    device = logits.get_device()
+    lp, ls = _matrix(logits, "route: logits", T, E, device)
     dev = logits.device
     i32 = dict(dtype=torch.int32, device=dev)
     n = T * k
@@ -248,9 +272,7 @@ def route(logits: torch.Tensor, k: int, renormalize: bool = True, stream=None) -
     a = _ROUTE.pack(lp, ls, _DTYPES[logits.dtype], T, E, k, renormalize, r.ids.data_ptr(), r.weights.data_ptr(),
                     r.expert_start.data_ptr(), r.rows.data_ptr(), r.slots.data_ptr(),
                     scratch.data_ptr() if need else 0, need)
-    status = lib.csf_route(a, _raw_stream(dev.index))
-    if status:
-        _check(status, "csf_route")
+    _launch(lib.csf_route, a, device, "csf_route")
     return r
 
 
@@ -274,21 +296,25 @@ def expert_matmul(x: Quantized, w: torch.Tensor, w_scales: torch.Tensor, expert_
     if stream is not None:
         return _on(stream, expert_matmul, x, w, w_scales, expert_start, rows, alpha, bias, activation, gated, row_scale,
                    residual, out, out_tensor_scale, error_word)
-    _check_quantized(x, "expert_matmul: x")
-    if w.dtype != torch.uint8 or not w.is_cuda or w.dim() != 3 or not w.is_contiguous() or w.shape[2] * 2 != x.cols:
-        raise CsfError(f"expert_matmul: w must be a contiguous uint8 CUDA tensor [E, N, {x.cols // 2}]")
+    device = x.codes.get_device()
+    _check_quantized(x, "expert_matmul: x", device)
+    if w.dtype != torch.uint8 or w.get_device() != device or w.dim() != 3 or not w.is_contiguous() or w.shape[2] * 2 != x.cols:
+        raise CsfError(f"expert_matmul: w must be a contiguous uint8 CUDA tensor [E, N, {x.cols // 2}]{_where(device)}")
     E, N = w.shape[0], w.shape[1]
     C = x.cols // (16 if x.kind == NVFP4 else 32)
-    if w_scales.dtype != torch.uint8 or not w_scales.is_cuda or not w_scales.is_contiguous() or \
+    if w_scales.dtype != torch.uint8 or w_scales.get_device() != device or not w_scales.is_contiguous() or \
             w_scales.numel() < E * _up(N, 128) * _up(C, 4):
-        raise CsfError("expert_matmul: w_scales must be a contiguous uint8 CUDA tensor in the blocked layout")
+        raise CsfError(f"expert_matmul: w_scales must be a contiguous uint8 CUDA tensor in the blocked layout{_where(device)}")
     if activation not in _ACTS:
         raise CsfError(f"expert_matmul: unknown activation {activation!r}")
-    if rows is not None and (not rows.is_cuda or rows.dtype != torch.int32 or not rows.is_contiguous() or rows.dim() != 1):
-        raise CsfError("expert_matmul: rows must be a contiguous int32 CUDA vector")
+    if rows is not None and (rows.get_device() != device or rows.dtype != torch.int32 or not rows.is_contiguous() or rows.dim() != 1):
+        raise CsfError(f"expert_matmul: rows must be a contiguous int32 CUDA vector{_where(device)}")
     es, es64 = _es(expert_start)
-    if expert_start is not None and expert_start.numel() != E + 1:
-        raise CsfError("expert_start must have E+1 entries")
+    if expert_start is not None:
+        if expert_start.get_device() != device:
+            raise CsfError(f"expert_start must be a CUDA tensor{_where(device)}")
+        if expert_start.numel() != E + 1:
+            raise CsfError("expert_start must have E+1 entries")
     S = x.rows if rows is None else rows.shape[0]
     F = N // 2 if gated else N
     bias_dtype = 0
@@ -296,7 +322,7 @@ def expert_matmul(x: Quantized, w: torch.Tensor, w_scales: torch.Tensor, expert_
         if bias.dtype not in _DTYPES:
             raise CsfError("expert_matmul: bias must be bfloat16, float16 or float32")
         bias_dtype = _DTYPES[bias.dtype]
-    rp, rs = (0, 0) if residual is None else _matrix(residual, "expert_matmul: residual", S, F)
+    rp, rs = (0, 0) if residual is None else _matrix(residual, "expert_matmul: residual", S, F, device)
     if isinstance(out, torch.dtype):
         if out not in _DTYPES:
             raise CsfError("expert_matmul: out must be bfloat16, float16 or float32")
@@ -304,26 +330,24 @@ def expert_matmul(x: Quantized, w: torch.Tensor, w_scales: torch.Tensor, expert_
     elif isinstance(out, int):
         out = empty_quantized(out, S, F, x.codes.device, out_tensor_scale)
     if isinstance(out, Quantized):
-        _check_quantized(out, "expert_matmul: out")
+        _check_quantized(out, "expert_matmul: out", device)
         if out.rows != S or out.cols != F:
             raise CsfError("expert_matmul: out does not match the product")
-        out.tensor_scale = _tensor_scale(out, out_tensor_scale, "expert_matmul")
+        out.tensor_scale = _tensor_scale(out, out_tensor_scale, "expert_matmul", device)
         op, os_, odt, orows = 0, 0, 0, out.fields()
     else:
-        op, os_ = _matrix(out, "expert_matmul: out", S, F)
+        op, os_ = _matrix(out, "expert_matmul: out", S, F, device)
         odt, orows = _DTYPES[out.dtype], _NO_ROWS
-    device = w.device.index
     fields = (*x.fields(), 0 if rows is None else rows.data_ptr(), S, E, N, w.data_ptr(), w_scales.data_ptr(), es or 0, es64,
-              _vector(alpha, "expert_matmul: alpha", E, torch.float32),
-              0 if bias is None else _vector(bias, "expert_matmul: bias", E * N, bias.dtype), bias_dtype, _ACTS[activation],
-              gated, _vector(row_scale, "expert_matmul: row_scale", S, torch.float32), rp, rs,
+              _vector(alpha, "expert_matmul: alpha", E, torch.float32, device),
+              0 if bias is None else _vector(bias, "expert_matmul: bias", E * N, bias.dtype, device), bias_dtype, _ACTS[activation],
+              gated, _vector(row_scale, "expert_matmul: row_scale", S, torch.float32, device), rp, rs,
               0 if residual is None else _DTYPES[residual.dtype], odt, op, os_, *orows)
     if error_word is None:
         with _error_lock:
-            status = lib.csf_expert_matmul(_EXPERT_MATMUL.pack(*fields, _error_word(device).data_ptr()), _raw_stream(device))
+            word = _error_word(device).data_ptr()
+            _launch(lib.csf_expert_matmul, _EXPERT_MATMUL.pack(*fields, word), device, "csf_expert_matmul")
     else:
-        word = _vector(error_word, "expert_matmul: error_word", 1, torch.int32)
-        status = lib.csf_expert_matmul(_EXPERT_MATMUL.pack(*fields, word), _raw_stream(device))
-    if status:
-        _check(status, "csf_expert_matmul")
+        word = _vector(error_word, "expert_matmul: error_word", 1, torch.int32, device)
+        _launch(lib.csf_expert_matmul, _EXPERT_MATMUL.pack(*fields, word), device, "csf_expert_matmul")
     return out

@@ -195,3 +195,70 @@ def test_widths_next_to_32_bits_are_refused(ops):
     assert product(rows(), 2 ** 31 - 1) == UNSUPPORTED
     k = 2 ** 31 - 128
     assert product(rows(cols=k, cs=k // 2, ss=k // 16 + 8), 128) == UNSUPPORTED       # strides are multiples of 16
+
+
+class On:
+    """A tensor that says it lies on a CUDA device."""
+    def __init__(self, t, device):
+        import torch
+        self.t, self.device = t, torch.device("cuda", device)
+
+    def __getattr__(self, name):
+        return getattr(self.t, name)
+
+    def get_device(self):
+        return self.device.index
+
+    is_cuda = True
+
+
+def test_tensors_of_another_device_are_refused(ops):
+    import types
+    import torch
+    x, w = torch.zeros(4, 64), torch.zeros(64)
+    with pytest.raises(ops.CsfError, match="residual.*on cuda:0"):
+        ops.rms_norm(On(x, 0), On(w, 0), ops.NVFP4, residual=On(x, 1))
+    with pytest.raises(ops.CsfError, match="weight.*on cuda:1"):
+        ops.rms_norm(On(x, 1), On(w, 0), ops.NVFP4)
+    with pytest.raises(ops.CsfError, match="out.*on cuda:0"):
+        ops.rms_norm(On(x, 0), On(w, 0), ops.NVFP4, out=ops.empty_quantized(ops.NVFP4, 4, 64, device="cpu"))
+
+    def product(at, **kw):
+        codes, scales = torch.zeros(4, 32, dtype=torch.uint8), torch.zeros(4, 16, dtype=torch.uint8)
+        weights, sf = torch.zeros(2, 8, 32, dtype=torch.uint8), torch.zeros(2 * 512, dtype=torch.uint8)
+        start = torch.zeros(3, dtype=torch.int32)
+        q = ops.Quantized(ops.NVFP4, On(codes, 0), On(scales, at.get("scales", 0)), 64)
+        ops.expert_matmul(q, On(weights, at.get("w", 0)), On(sf, at.get("sf", 0)), On(start, at.get("start", 0)), **kw)
+
+    for at, match in ((dict(scales=1), "x: codes and scales"), (dict(w=1), "w must"), (dict(sf=1), "w_scales"), (dict(start=1), "expert_start")):
+        with pytest.raises(ops.CsfError, match=match + ".*on cuda:0"):
+            product(at)
+    for name, t in (("rows", torch.zeros(4, dtype=torch.int32)), ("residual", torch.zeros(4, 8)), ("out", torch.zeros(4, 8)),
+                    ("alpha", torch.zeros(2)), ("bias", torch.zeros(2, 8)), ("row_scale", torch.zeros(4))):
+        with pytest.raises(ops.CsfError, match=name + ".*on cuda:0"):
+            product({}, **{"out": On(torch.zeros(4, 8), 0), name: On(t, 1)})
+    with pytest.raises(ops.CsfError, match="the stream is on cuda:1, the tensors on cuda:0"):
+        ops.route(On(x, 0), 2, stream=types.SimpleNamespace(device=torch.device("cuda", 1)))
+
+
+def test_a_call_runs_on_its_tensors_device(ops, monkeypatch):
+    """The device is made current around the library call where it is not; the stream is that device's."""
+    import contextlib
+    import torch
+    current, log = [0], []
+
+    @contextlib.contextmanager
+    def device(i):
+        was, current[0] = current[0], i
+        yield
+        current[0] = was
+
+    monkeypatch.setattr(ops, "_current_device", lambda: current[0])
+    monkeypatch.setattr(ops, "_raw_stream", lambda i: 100 + i)
+    monkeypatch.setattr(torch.cuda, "device", device)
+    for d in (0, 1):
+        ops._launch(lambda args, stream: log.append((args, stream, current[0])) or 0, b"x", d, "call")
+    assert log == [(b"x", 100, 0), (b"x", 101, 1)] and current == [0]
+    with pytest.raises(ops.CsfError, match="call"):
+        ops._launch(lambda args, stream: ARG, b"", 1, "call")
+    assert current == [0]
