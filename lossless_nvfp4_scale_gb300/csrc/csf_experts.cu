@@ -1,6 +1,7 @@
 // Host side of csf_expert_matmul: argument checks, tensor maps, the choice of
 // a kernel and its launch.
 #include <algorithm>
+#include <atomic>
 #include <cstring>
 #include <mutex>
 #include <set>
@@ -29,8 +30,9 @@ EncodeFn encode_fn() {
     return fn;
 }
 
-// Raises a kernel's shared-memory limit once a device.
-bool allow_smem(const void *kernel) {
+// Raises a kernel's shared-memory limit once a device.  (The standard library
+// may throw; the C entry must not.)
+bool allow_smem(const void *kernel) noexcept {
     static std::mutex mu;
     static std::set<std::pair<const void *, int>> done;
     int dev = 0;
@@ -38,16 +40,20 @@ bool allow_smem(const void *kernel) {
         cudaGetLastError();
         return false;
     }
-    std::lock_guard<std::mutex> lock(mu);
-    if (done.count({kernel, dev})) return true;
-    cudaFuncAttributes attr;
-    if (cudaFuncGetAttributes(&attr, kernel) != cudaSuccess ||
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit - (int)round_up(attr.sharedSizeBytes, 1024)) !=
-            cudaSuccess) {
-        cudaGetLastError();
+    try {
+        std::lock_guard<std::mutex> lock(mu);
+        if (done.count({kernel, dev})) return true;
+        cudaFuncAttributes attr;
+        if (cudaFuncGetAttributes(&attr, kernel) != cudaSuccess ||
+            cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 kSmemLimit - (int)round_up(attr.sharedSizeBytes, 1024)) != cudaSuccess) {
+            cudaGetLastError();
+            return false;
+        }
+        done.insert({kernel, dev});
+    } catch (...) {
         return false;
     }
-    done.insert({kernel, dev});
     return true;
 }
 
@@ -83,7 +89,7 @@ csf_status check(const csf_expert_matmul_args *a) {
 }  // namespace mm
 
 int sm_count() {
-    static int counts[64];
+    static std::atomic<int> counts[64];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) {
         cudaGetLastError();

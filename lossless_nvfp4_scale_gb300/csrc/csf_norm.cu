@@ -400,5 +400,7 @@ extern "C" csf_status csf_rms_norm(const csf_rms_norm_args *a, void *stream) {
     const cudaError_t err = a->dtype == CSF_BF16  ? launch_norm_kind<__nv_bfloat16>(a->out.kind, p, s)
                             : a->dtype == CSF_F16 ? launch_norm_kind<__half>(a->out.kind, p, s)
                                                   : launch_norm_kind<float>(a->out.kind, p, s);
-    return err == cudaSuccess ? CSF_OK : CSF_ERR_CUDA;
+    if (err == cudaSuccess) return CSF_OK;
+    cudaGetLastError();      // not left to the caller's next check
+    return CSF_ERR_CUDA;
 }
