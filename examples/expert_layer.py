@@ -35,21 +35,26 @@ class ExpertLayer:
     act_scale: torch.Tensor      # float32 [1]: the quantised activation's
     workspace: tuple[torch.Tensor, torch.Tensor]   # decoded scales, shared by layers of this shape
 
-    def __call__(self, x: torch.Tensor, residual: torch.Tensor, k: int):
-        """The experts' output for x [tokens, hidden], and the residual stream with x added."""
+    def __call__(self, x: torch.Tensor, residual: torch.Tensor, k: int, off: torch.Tensor | None = None):
+        """The experts' output for x [tokens, hidden], and the residual stream with x added.  `off` (bool, of the
+        logits' shape or one that broadcasts to it) switches experts off; a token may have fewer than k left, or none."""
         q, residual = ops.rms_norm(x, self.norm_weight, ops.NVFP4, residual=residual, tensor_scale=self.x_scale)
-        r = ops.route(residual @ self.router.T, k)
+        logits = residual @ self.router.T
+        r = ops.route(logits if off is None else logits.masked_fill(off, -float("inf")), k)
         csf.decode_pair(self.gate_up_scales, self.down_scales, *self.workspace, expert_start=r.expert_start,
                         layout=csf.LAYOUT_BLOCKED)
         act = ops.expert_matmul(q, self.gate_up, self.workspace[0], expert_start=r.expert_start, rows=r.rows,
                                 alpha=self.alpha[0], activation="silu", gated=True, out=ops.NVFP4,
                                 out_tensor_scale=self.act_scale)
-        # the router's weight of each slot (every token has k experts here)
-        weight = torch.empty_like(r.weights).view(-1)
+        # the router's weight of each slot; a choice that fell away has slot -1, the last of one slot more than there are
+        weight = r.weights.new_empty(r.weights.numel() + 1)
         weight[r.slots.view(-1).long()] = r.weights.view(-1)
         y = ops.expert_matmul(act, self.down, self.workspace[1], expert_start=r.expert_start, alpha=self.alpha[1],
-                              row_scale=weight, out=torch.float32)
-        return y[r.slots.long()].sum(1).to(x.dtype), residual
+                              row_scale=weight[:-1], out=torch.float32)
+        y = y[r.slots.long()]
+        if off is not None:          # rows of choices that fell away hold nothing
+            y = torch.where((r.slots >= 0).unsqueeze(-1), y, 0.0)
+        return y.sum(1).to(x.dtype), residual
 
 
 def random_layer(experts: int, hidden: int, inner: int, seed: int = 0) -> ExpertLayer:

@@ -77,3 +77,45 @@ def test_layer(example, tokens, k):
     got = (av * layer.act_scale.double())[r.slots.long()].view(tokens, k, -1, 16)
     exact = exact.view(tokens, k, -1, 16).clamp(-most, most)
     assert ((got - exact).abs() <= exact.abs().amax(-1, keepdim=True) * (1 / 6 + 1 / 16) + 6 * 2.0 ** -10 * 0.005).all()
+
+
+@pytest.mark.parametrize("tokens,k", [(1, 4), (33, 8), (200, 2)])
+def test_layer_with_experts_switched_off(example, tokens, k):
+    """Masked routing: tokens with all experts, fewer than k or none.  A token with none gets 0; what is left of the
+    others is what the router's choices and the slots' outputs add up to in 64 bits."""
+    csf, ops = example.csf, example.ops
+    E, H, I = 16, 320, 256
+    layer = example.random_layer(E, H, I, seed=tokens)
+    g = torch.Generator(device="cuda").manual_seed(tokens + 1)
+    x = torch.randn(tokens, H, device="cuda", generator=g).to(torch.bfloat16)
+    residual = torch.randn(tokens, H, device="cuda", generator=g).to(torch.bfloat16)
+    off = torch.rand(tokens, E, device="cuda", generator=g) < 0.5
+    off[::3, 1:] = True                                  # one expert left, fewer than k
+    off[::4] = True                                      # none
+    off[2::5] = False
+    junk = [torch.full((tokens * k, H), float("nan"), device="cuda") for _ in range(4)]      # what unwritten rows may hold
+    del junk
+    y, total = layer(x, residual, k, off=off)
+    none = off.all(1)
+    assert torch.isfinite(y).all() and (y[none] == 0).all()
+
+    q, _ = ops.rms_norm(x, layer.norm_weight, ops.NVFP4, residual=residual, tensor_scale=layer.x_scale)
+    r = ops.route((total @ layer.router.T).masked_fill(off, -float("inf")), k)
+    assert ((r.slots >= 0).sum(1) == (~off).sum(1).clamp(max=k)).all()
+    act = ops.expert_matmul(q, layer.gate_up, layer.workspace[0], expert_start=r.expert_start, rows=r.rows,
+                            alpha=layer.alpha[0], activation="silu", gated=True, out=ops.NVFP4,
+                            out_tensor_scale=layer.act_scale)
+    down = values(layer.down, csf.decode(layer.down_scales))
+    av = values(act.codes, act.scales[:, :I // 16])
+    want = torch.zeros(tokens, H, dtype=torch.float64, device="cuda")
+    size = torch.zeros_like(want)
+    for t in range(tokens):
+        for j in range(k):
+            e, s = int(r.ids[t, j]), int(r.slots[t, j])
+            if s < 0:
+                continue
+            scale = layer.alpha[1, e].double() * r.weights[t, j].double()
+            want[t] += (down[e] @ av[s]) * scale
+            size[t] += (down[e].abs() @ av[s].abs()) * scale.abs()
+    # as above: 32-bit sums of 256 terms, bfloat16 output
+    assert ((y.double() - want).abs() <= 2.0 ** -8 * want.abs() + 2.0 ** -18 * size).all()
