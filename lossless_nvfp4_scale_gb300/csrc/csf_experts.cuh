@@ -886,7 +886,9 @@ expert_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_cons
 
     // A wait that gave up: let copies and products in flight land before the
     // block's memory goes.
+    tc::fence_before();      // the last tensor-memory reads, before they are freed
     __syncthreads();
+    tc::fence_after();
     if (sh.abort) {
         if (tid == 0 && p.err) atomicOr(p.err, CSF_DEV_ERR_TIMEOUT);
         const uint64_t t0 = tc::timer_ns();
