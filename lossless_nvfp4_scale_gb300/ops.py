@@ -338,16 +338,19 @@ def expert_matmul(x: Quantized, w: torch.Tensor, w_scales: torch.Tensor, expert_
     else:
         op, os_ = _matrix(out, "expert_matmul: out", S, F, device)
         odt, orows = _DTYPES[out.dtype], _NO_ROWS
-    fields = (*x.fields(), 0 if rows is None else rows.data_ptr(), S, E, N, w.data_ptr(), w_scales.data_ptr(), es or 0, es64,
-              _vector(alpha, "expert_matmul: alpha", E, torch.float32, device),
-              0 if bias is None else _vector(bias, "expert_matmul: bias", E * N, bias.dtype, device), bias_dtype, _ACTS[activation],
-              gated, _vector(row_scale, "expert_matmul: row_scale", S, torch.float32, device), rp, rs,
-              0 if residual is None else _DTYPES[residual.dtype], odt, op, os_, *orows)
-    if error_word is None:
-        with _error_lock:
-            word = _error_word(device).data_ptr()
-            _launch(lib.csf_expert_matmul, _EXPERT_MATMUL.pack(*fields, word), device, "csf_expert_matmul")
-    else:
-        word = _vector(error_word, "expert_matmul: error_word", 1, torch.int32, device)
-        _launch(lib.csf_expert_matmul, _EXPERT_MATMUL.pack(*fields, word), device, "csf_expert_matmul")
+    own_word = error_word is None
+    if own_word:
+        _error_lock.acquire()
+    try:
+        a = _EXPERT_MATMUL.pack(
+            *x.fields(), 0 if rows is None else rows.data_ptr(), S, E, N, w.data_ptr(), w_scales.data_ptr(), es or 0, es64,
+            _vector(alpha, "expert_matmul: alpha", E, torch.float32, device),
+            0 if bias is None else _vector(bias, "expert_matmul: bias", E * N, bias.dtype, device), bias_dtype, _ACTS[activation],
+            gated, _vector(row_scale, "expert_matmul: row_scale", S, torch.float32, device), rp, rs,
+            0 if residual is None else _DTYPES[residual.dtype], odt, op, os_, *orows,
+            _error_word(device).data_ptr() if own_word else _vector(error_word, "expert_matmul: error_word", 1, torch.int32, device))
+        _launch(lib.csf_expert_matmul, a, device, "csf_expert_matmul")
+    finally:
+        if own_word:
+            _error_lock.release()
     return out
