@@ -139,8 +139,13 @@ typedef enum { CSF_ACT_NONE = 0, CSF_ACT_RELU = 1, CSF_ACT_SILU = 2, CSF_ACT_GEL
  *   out[s][n] = y[n] * row_scale[s] + residual[s][n]
  * with x and w as the values they stand for without their tensor scales
  * (alpha carries the product of those).  x NVFP4 goes with w NVFP4, x MXFP8
- * with w MXFP4.  Sums in 32 bits.  Slots at or past expert_start[E] are not
- * written; with an expert_start that is out of order or range, none is.
+ * with w MXFP4.  Sums in 32 bits, a matrix step (64 columns NVFP4, 32 MXFP8)
+ * at a time, each of which may be off by a unit in the last place of what it
+ * holds: a sum is within (K / 32 + 4) 2^-23 of sum_k |x w|.  SiLU and GELU are
+ * within 2^-20 of their value, GELU with 2^-21 |z| more, z the argument of its
+ * exponential.  Slots at or past expert_start[E] are not written; with an
+ * expert_start that is out of order or range, none is.  A row index out of
+ * range stands for row 0.
  */
 typedef struct {
     csf_rows x;              /* rows x cols (= K); K a multiple of 32 (NVFP4) or 128 (MXFP8) */

@@ -41,12 +41,12 @@
 // bfloat16 products 1.94 PFLOP/s):
 //   512 experts of 64 slots, 1024 x 1600 NVFP4, gated   88 us, 5.86 TB/s: memory
 //   384 experts of 5, 2048 x 5120 MXFP4, gated         351 us, 6.12 TB/s: memory
-//   512 of 64, 2048 x 800 NVFP4, bias and residual     151 us, 5.02 TB/s: the
+//   512 of 64, 2048 x 800 NVFP4, bias and residual     150 us, 5.05 TB/s: the
 //     epilogue (108 us without a residual) and short K: a tile is 4 stages
-//   8191 slots of one 2048 x 5120 MXFP4                 78 us, 2.2 PFLOP/s:
+//   8191 slots of one 2048 x 5120 MXFP4                 79 us, 2.2 PFLOP/s:
 //     shared-memory bandwidth (operands in, operands to the tensor cores)
-//   64 slots on 8 of 512, gated                        8.3 us: latency
-//   one slot of 2048 x 5120 MXFP4                      9.6 us: latency
+//   64 slots on 8 of 512, gated                        8.2 us: latency
+//   one slot of 2048 x 5120 MXFP4                      9.4 us: latency
 #pragma once
 
 #include <type_traits>
@@ -457,7 +457,7 @@ expert_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_cons
 
     // What the epilogue will add to a tile, into L2: 32 bytes a lane.  (Asked
     // for by the scale warp as it opens a tile: the product above with bias
-    // and residual takes 151 us; 164 where the epilogue asks a tile ahead, 189
+    // and residual takes 150 us; 164 where the epilogue asks a tile ahead, 189
     // where a warp of its own asks as early as it can, 200 unasked.)
     auto prefetch_residual = [&](const Tile &t) {
         const int bytes = p.residual_dtype == CSF_F32 ? 4 : 2;

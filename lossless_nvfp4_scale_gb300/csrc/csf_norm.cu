@@ -30,7 +30,7 @@ constexpr float kLeastMean = 0x1p-100f, kUp = 0x1p96f, kDown = 0x1p-80f;
 
 // Where the registers are full (rows loaded ahead by a whole block) such rows
 // are marked and done when the block's others are: 16384 rows of 5120 to NVFP4
-// take 86 us, as without, and 97 with a branch for them in the loop.  Else
+// take 86 us so, 85 without and 97 with a branch for them in the loop.  Else
 // they are done at once.  The mark is an NVFP4 row's first scale (UE4M3, a
 // byte below 0x80) or an MXFP8 row's first code (the conversion's NaN is
 // 0x7F).
