@@ -31,14 +31,17 @@ extern "C" {
 /* Element types of plain tensors. */
 typedef enum { CSF_BF16 = 0, CSF_F16 = 1, CSF_F32 = 2 } csf_dtype;
 
-/* Quantised rows.  A row of `cols` values is held as codes and one scale byte
- * per block of values; columns past `cols` up to the next multiple of 32 are
+/* Quantised rows.  A row of `cols` values is held as codes and one scale per
+ * block of values; columns past `cols` up to the next multiple of 32 are
  * coded 0.
  *   CSF_ROWS_NVFP4  E2M1 codes, two a byte (even column in the low nibble);
  *                   a UE4M3 scale per 16 columns; value = code * scale *
  *                   tensor scale.
  *   CSF_ROWS_MXFP8  E4M3 codes, one a byte; a UE8M0 scale (2^(byte - 127),
  *                   255 = NaN) per 32 columns; value = code * scale.
+ *   CSF_ROWS_FP8    E4M3 codes, one a byte; a float32 scale per 128 columns;
+ *                   value = code * scale.  Of csf_rms_norm and the operators
+ *                   of csf_layer.h.
  * Scale rows are row-major, `scale_stride` bytes apart (a multiple of 16);
  * bytes past the row's blocks are 0 up to the next multiple of 16.
  * How a block of values v with largest magnitude m becomes codes:
@@ -47,11 +50,14 @@ typedef enum { CSF_BF16 = 0, CSF_F16 = 1, CSF_F32 = 2 } csf_dtype;
  *          (ties to even, saturating); 0 where the scale rounds to 0.
  *   MXFP8: scale = the smallest power of two with m <= 448 * scale (2^-127 at
  *          least); code = v / scale rounded to E4M3 (ties to even).
- * A block that holds an infinity or a NaN gets a NaN scale (0x7F, 255). */
-typedef enum { CSF_ROWS_NVFP4 = 0, CSF_ROWS_MXFP8 = 1 } csf_rows_kind;
+ *   FP8:   scale = m / 448 (2^-126 at least); code = v / scale rounded to E4M3
+ *          (ties to even, saturating).
+ * A block that holds an infinity or a NaN gets a NaN scale (0x7F, 255, a
+ * float's NaN). */
+typedef enum { CSF_ROWS_NVFP4 = 0, CSF_ROWS_MXFP8 = 1, CSF_ROWS_FP8 = 3 } csf_rows_kind;
 
 typedef struct {
-    int32_t kind;              /* csf_rows_kind */
+    int32_t kind;              /* csf_rows_kind; csf_expert_matmul takes NVFP4 and MXFP8 */
     int32_t cols;              /* values per row, >= 1 */
     int64_t rows;              /* >= 0 */
     uint8_t *codes;            /* 16-byte aligned */

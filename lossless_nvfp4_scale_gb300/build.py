@@ -20,7 +20,8 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libcsf.so")
 SOURCES = ["csf_api.cu", "csf_decode.cu", "csf_tiles.cu", "csf_tiled.cu", "csf_prepare.cu",
            "csf_prepare_static.cu", "csf_norm.cu", "csf_route.cu", "csf_experts.cu",
-           "csf_experts_nv.cu", "csf_experts_nv_rows.cu", "csf_experts_mx.cu", "csf_experts_mx_rows.cu"]
+           "csf_experts_nv.cu", "csf_experts_nv_rows.cu", "csf_experts_mx.cu", "csf_experts_mx_rows.cu",
+           "csf_rows.cu", "csf_route_grad.cu", "csf_fp8.cu", "csf_fp8_order.cu", "csf_fp8_index.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -36,7 +37,9 @@ def _inputs():
     files += [os.path.join(CSRC, "csf_internal.cuh"), os.path.join(CSRC, "csf_device.cuh"),
               os.path.join(INCLUDE, "csf.h"), os.path.join(INCLUDE, "csf_tile.cuh"),
               os.path.join(CSRC, "csf_quant.cuh"), os.path.join(CSRC, "csf_tc.cuh"),
-              os.path.join(CSRC, "csf_experts.cuh"), os.path.join(INCLUDE, "csf_ops.h")]
+              os.path.join(CSRC, "csf_experts.cuh"), os.path.join(INCLUDE, "csf_ops.h"),
+              os.path.join(CSRC, "csf_elem.cuh"), os.path.join(CSRC, "csf_fp8.cuh"),
+              os.path.join(CSRC, "csf_grouped.cuh"), os.path.join(CSRC, "csf_host.cuh"), os.path.join(INCLUDE, "csf_layer.h")]
     return files
 
 

@@ -7,55 +7,11 @@
 #include <set>
 
 #include "csf_experts.cuh"
+#include "csf_host.cuh"
 
 namespace csfk {
 namespace mm {
 namespace {
-
-using EncodeFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *, const cuuint64_t *,
-                              const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
-                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeFn encode_fn() {
-    static EncodeFn fn = [] {
-        void *f = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12080, cudaEnableDefault, &q) != cudaSuccess ||
-            q != cudaDriverEntryPointSuccess) {
-            cudaGetLastError();
-            f = nullptr;
-        }
-        return reinterpret_cast<EncodeFn>(f);
-    }();
-    return fn;
-}
-
-// Raises a kernel's shared-memory limit once a device.  (The standard library
-// may throw; the C entry must not.)
-bool allow_smem(const void *kernel) noexcept {
-    static std::mutex mu;
-    static std::set<std::pair<const void *, int>> done;
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) {
-        cudaGetLastError();
-        return false;
-    }
-    try {
-        std::lock_guard<std::mutex> lock(mu);
-        if (done.count({kernel, dev})) return true;
-        cudaFuncAttributes attr;
-        if (cudaFuncGetAttributes(&attr, kernel) != cudaSuccess ||
-            cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 kSmemLimit - (int)round_up(attr.sharedSizeBytes, 1024)) != cudaSuccess) {
-            cudaGetLastError();
-            return false;
-        }
-        done.insert({kernel, dev});
-    } catch (...) {
-        return false;
-    }
-    return true;
-}
 
 csf_status check(const csf_expert_matmul_args *a) {
     if (!a) return CSF_ERR_ARG;
@@ -87,6 +43,46 @@ csf_status check(const csf_expert_matmul_args *a) {
 
 }  // namespace
 }  // namespace mm
+
+EncodeFn encode_fn() {
+    static EncodeFn fn = [] {
+        void *f = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12080, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess) {
+            cudaGetLastError();
+            f = nullptr;
+        }
+        return reinterpret_cast<EncodeFn>(f);
+    }();
+    return fn;
+}
+
+// (The standard library may throw; the C entry must not.)
+bool allow_smem(const void *kernel, int limit, int least_regs) noexcept {
+    static std::mutex mu;
+    static std::set<std::pair<const void *, int>> done;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) {
+        cudaGetLastError();
+        return false;
+    }
+    try {
+        std::lock_guard<std::mutex> lock(mu);
+        if (done.count({kernel, dev})) return true;
+        cudaFuncAttributes attr;
+        if (cudaFuncGetAttributes(&attr, kernel) != cudaSuccess || attr.numRegs < least_regs ||
+            cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 limit - (int)round_up(attr.sharedSizeBytes, 1024)) != cudaSuccess) {
+            cudaGetLastError();
+            return false;
+        }
+        done.insert({kernel, dev});
+    } catch (...) {
+        return false;
+    }
+    return true;
+}
 
 int sm_count() {
     static std::atomic<int> counts[64];
@@ -235,7 +231,7 @@ extern "C" csf_status csf_expert_matmul(const csf_expert_matmul_args *a, void *s
     const bool res = a->residual || a->row_scale;
     Kernel k = a->rows ? (nv ? nvfp4_rows_kernel(out, shape, res) : mxfp8_rows_kernel(out, shape, res))
                        : (nv ? nvfp4_kernel(out, shape, res) : mxfp8_kernel(out, shape, res));
-    if (!allow_smem(reinterpret_cast<const void *>(k))) return CSF_ERR_CUDA;
+    if (!allow_smem(reinterpret_cast<const void *>(k), kSmemLimit)) return CSF_ERR_CUDA;
     cudaLaunchConfig_t config = {};
     config.gridDim = dim3((unsigned)(p.split > 1 ? most_tiles * p.split : std::min<int64_t>(sms, most_tiles)));
     config.blockDim = dim3(kMmThreads);

@@ -4,8 +4,8 @@
 // Bound by memory: a row is read once and stays in registers, in chunks of 8
 // columns a thread, while its sum of squares is formed and the next row is
 // under way; then the chunks are scaled, the block maxima come from shuffles
-// between the 4 (32 columns, MXFP8) or 2 (16 columns, NVFP4) threads of a
-// block, and codes and scales leave.  Rows too wide for the registers are
+// between the 16 (128 columns, FP8), 4 (32, MXFP8) or 2 (16, NVFP4) threads of
+// a block, and codes and scales leave.  Rows too wide for the registers are
 // read twice.  16384 bfloat16 rows of 5120 with a residual to MXFP8: 99 us,
 // 5.96 TB/s (0.88 of the measured copy); 127 us with a block a row, whose
 // loads wait for its reduction.
@@ -32,8 +32,8 @@ constexpr float kLeastMean = 0x1p-100f, kUp = 0x1p96f, kDown = 0x1p-80f;
 // are marked and done when the block's others are: 16384 rows of 5120 to NVFP4
 // take 86 us so, 85 without and 97 with a branch for them in the loop.  Else
 // they are done at once.  The mark is an NVFP4 row's first scale (UE4M3, a
-// byte below 0x80) or an MXFP8 row's first code (the conversion's NaN is
-// 0x7F).
+// byte below 0x80) or an MXFP8 or FP8 row's first code (the conversion's NaN
+// is 0x7F).
 constexpr uint8_t kAgain = 0xFF;
 
 struct NormParams {
@@ -177,7 +177,7 @@ __device__ __forceinline__ void whole_row(const NormParams &p, int64_t row, int 
         for (int i = 0; i < 8; ++i) h[i] = h[i] * k * r * w[i];
         quant::quantize8<KIND>(h, codes, scales, c, c < p.chunks, g);
     }
-    const int blocks = KIND == CSF_ROWS_MXFP8 ? p.chunks >> 2 : p.chunks >> 1;
+    const int blocks = quant::scale_bytes<KIND>(p.chunks);
     if (tid < ((blocks + 15) & ~15) - blocks) scales[blocks + tid] = 0;
     if constexpr (!WARP) __syncthreads();      // part[0] is read
 }
@@ -211,7 +211,7 @@ rms_norm_kernel(const __grid_constant__ NormParams p) {
     } else {
         constexpr bool kMark = AHEAD && !WARP && (CHUNKS == 2 || sizeof(T) == 2);
         const T *weight = static_cast<const T *>(p.weight);
-        const int blocks = KIND == CSF_ROWS_MXFP8 ? p.chunks >> 2 : p.chunks >> 1;
+        const int blocks = quant::scale_bytes<KIND>(p.chunks);
         constexpr bool kHoldWeight = AHEAD && sizeof(T) == 2;      // 32-bit ones would not fit the registers
         Raw<T> xr[CHUNKS], rr[CHUNKS], wr[CHUNKS];
         auto load_ahead = [&](int64_t row) {
@@ -352,7 +352,9 @@ cudaError_t launch_norm(const NormParams &p, cudaStream_t s) {
 
 template <typename T>
 cudaError_t launch_norm_kind(int kind, const NormParams &p, cudaStream_t s) {
-    return kind == CSF_ROWS_NVFP4 ? launch_norm<T, CSF_ROWS_NVFP4>(p, s) : launch_norm<T, CSF_ROWS_MXFP8>(p, s);
+    return kind == CSF_ROWS_NVFP4  ? launch_norm<T, CSF_ROWS_NVFP4>(p, s)
+           : kind == CSF_ROWS_FP8 ? launch_norm<T, CSF_ROWS_FP8>(p, s)
+                                  : launch_norm<T, CSF_ROWS_MXFP8>(p, s);
 }
 
 bool wide(const void *p, int64_t stride, int dtype) {
@@ -365,7 +367,7 @@ bool wide(const void *p, int64_t stride, int dtype) {
 using namespace csfk;
 
 extern "C" csf_status csf_rms_norm(const csf_rms_norm_args *a, void *stream) {
-    if (!a || !dtype_known(a->dtype) || !rows_valid(a->out)) return CSF_ERR_ARG;
+    if (!a || !dtype_known(a->dtype) || !rows_valid(a->out, true)) return CSF_ERR_ARG;
     if (a->out.rows == 0) return CSF_OK;
     const int64_t cols = a->out.cols;
     if (!a->x || !a->weight || a->x_stride < cols) return CSF_ERR_ARG;

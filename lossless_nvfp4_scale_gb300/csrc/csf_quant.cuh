@@ -68,32 +68,73 @@ __device__ __forceinline__ uint32_t e2m1x2(float lo, float hi) {
     return __nv_cvt_float2_to_fp4x2(make_float2(lo, hi), __NV_E2M1, cudaRoundNearest);
 }
 
-// Quantise columns 8 * chunk .. +7 of a row.  Every lane of a block's 4 (32
-// columns, MXFP8) or 2 (16 columns, NVFP4) calls it together, `write` or not.
+// FP8 scale of a block whose largest magnitude is amax: a normal number, or
+// NaN.
+__device__ __forceinline__ float fp8_scale(uint32_t amax_bits) {
+    if ((amax_bits >> 23) == 255) return __int_as_float(0x7FFFFFFF);
+    return fmaxf(__fdiv_rn(__uint_as_float(amax_bits), 448.f), 0x1p-126f);
+}
+
+// What FP8 values and their scale are multiplied by before over(), so that its
+// remainders stay normal numbers.
+__device__ __forceinline__ float fp8_up(float scale) { return scale < 0x1p-60f ? 0x1p60f : 1.f; }
+
+// A scale (times fp8_up) and its inverse, for over().
+__device__ __forceinline__ Whole fp8_whole(float scale) {
+    Whole w;
+    w.value = scale;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(w.inverse) : "f"(scale));
+    return w;
+}
+
+// The largest magnitude (as bits) of the block that 8 of this lane's columns
+// are of, over the block's lanes: 16 of 8 columns (FP8), 4 (MXFP8) or 2
+// (NVFP4), which call it together.
 template <int KIND>
-__device__ __forceinline__ void quantize8(const float (&y)[8], uint8_t *codes, uint8_t *scales, int chunk, bool write,
-                                          float tensor_scale) {
+__device__ __forceinline__ uint32_t block_amax(const float (&y)[8]) {
     uint32_t m = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(y[i]) & 0x7FFFFFFFu);
     m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
-    if constexpr (KIND == CSF_ROWS_MXFP8) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
-    if (!write) return;
-    if constexpr (KIND == CSF_ROWS_MXFP8) {
-        const uint32_t s = mx_scale(m);
-        const float inv = mx_inverse(s);
-        uint2 q;
-        q.x = e4m3x2(y[0] * inv, y[1] * inv) | e4m3x2(y[2] * inv, y[3] * inv) << 16;
-        q.y = e4m3x2(y[4] * inv, y[5] * inv) | e4m3x2(y[6] * inv, y[7] * inv) << 16;
-        *reinterpret_cast<uint2 *>(codes + chunk * 8) = q;
-        if ((chunk & 3) == 0) scales[chunk >> 2] = (uint8_t)s;
+    if constexpr (KIND == CSF_ROWS_MXFP8 || KIND == CSF_ROWS_FP8) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+    if constexpr (KIND == CSF_ROWS_FP8) {
+        m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 4));
+        m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 8));
+    }
+    return m;
+}
+
+// 8 columns' codes (NVFP4: 4 bytes, in x) and their block's scale.
+struct Coded {
+    uint2 codes;
+    uint32_t scale;
+};
+
+// Codes of 8 columns whose block has largest magnitude m.
+template <int KIND>
+__device__ __forceinline__ Coded encode8(const float (&y)[8], uint32_t m, float tensor_scale) {
+    Coded q;
+    if constexpr (KIND == CSF_ROWS_FP8) {
+        const float scale = fp8_scale(m), up = fp8_up(scale);
+        const Whole w = fp8_whole(scale * up);
+        float v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = over(y[i] * up, w);
+        q.codes.x = e4m3x2(v[0], v[1]) | e4m3x2(v[2], v[3]) << 16;
+        q.codes.y = e4m3x2(v[4], v[5]) | e4m3x2(v[6], v[7]) << 16;
+        q.scale = __float_as_uint(scale);
+    } else if constexpr (KIND == CSF_ROWS_MXFP8) {
+        q.scale = mx_scale(m);
+        const float inv = mx_inverse(q.scale);
+        q.codes.x = e4m3x2(y[0] * inv, y[1] * inv) | e4m3x2(y[2] * inv, y[3] * inv) << 16;
+        q.codes.y = e4m3x2(y[4] * inv, y[5] * inv) | e4m3x2(y[6] * inv, y[7] * inv) << 16;
     } else {
-        const uint32_t s = nv_scale(m, 6.f * tensor_scale);
-        const Whole w = nv_whole(s, tensor_scale);
+        q.scale = nv_scale(m, 6.f * tensor_scale);
+        const Whole w = nv_whole(q.scale, tensor_scale);
         float v[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = y[i];
-        if (s == 0x7E) {
+        if (q.scale == 0x7E) {
             // The largest scale: values may be far past 6 of it, and a quotient
             // that overflows has no remainder to correct it by.  What is past
             // 5 of it is coded 6.
@@ -101,11 +142,38 @@ __device__ __forceinline__ void quantize8(const float (&y)[8], uint8_t *codes, u
 #pragma unroll
             for (int i = 0; i < 8; ++i) v[i] = fminf(fmaxf(v[i], -most), most);
         }
-        *reinterpret_cast<uint32_t *>(codes + chunk * 4) =
-            e2m1x2(over(v[0], w), over(v[1], w)) | e2m1x2(over(v[2], w), over(v[3], w)) << 8 |
-            e2m1x2(over(v[4], w), over(v[5], w)) << 16 | e2m1x2(over(v[6], w), over(v[7], w)) << 24;
-        if ((chunk & 1) == 0) scales[chunk >> 1] = (uint8_t)s;
+        q.codes.x = e2m1x2(over(v[0], w), over(v[1], w)) | e2m1x2(over(v[2], w), over(v[3], w)) << 8 |
+                    e2m1x2(over(v[4], w), over(v[5], w)) << 16 | e2m1x2(over(v[6], w), over(v[7], w)) << 24;
+        q.codes.y = 0;
     }
+    return q;
+}
+
+// Columns 8 * chunk .. +7 of a row; the scale by its block's first lane.
+template <int KIND>
+__device__ __forceinline__ void put8(const Coded &q, uint8_t *codes, uint8_t *scales, int chunk) {
+    if constexpr (KIND == CSF_ROWS_NVFP4) *reinterpret_cast<uint32_t *>(codes + chunk * 4) = q.codes.x;
+    else *reinterpret_cast<uint2 *>(codes + chunk * 8) = q.codes;
+    constexpr int kLanes = KIND == CSF_ROWS_FP8 ? 16 : KIND == CSF_ROWS_MXFP8 ? 4 : 2;
+    if (chunk % kLanes == 0) {
+        if constexpr (KIND == CSF_ROWS_FP8) *reinterpret_cast<uint32_t *>(scales + (chunk >> 2)) = q.scale;
+        else scales[chunk / kLanes] = (uint8_t)q.scale;
+    }
+}
+
+// Quantise columns 8 * chunk .. +7 of a row.  Every lane of a block calls it
+// together (block_amax), `write` or not.
+template <int KIND>
+__device__ __forceinline__ void quantize8(const float (&y)[8], uint8_t *codes, uint8_t *scales, int chunk, bool write,
+                                          float tensor_scale) {
+    const uint32_t m = block_amax<KIND>(y);
+    if (write) put8<KIND>(encode8<KIND>(y, m, tensor_scale), codes, scales, chunk);
+}
+
+// Bytes of scales of a row of `chunks` 8-column pieces.
+template <int KIND>
+__device__ __forceinline__ int scale_bytes(int chunks) {
+    return KIND == CSF_ROWS_FP8 ? (chunks + 15) / 16 * 4 : KIND == CSF_ROWS_MXFP8 ? chunks >> 2 : chunks >> 1;
 }
 
 }  // namespace quant
@@ -118,13 +186,15 @@ inline size_t dtype_bytes(int dtype) { return dtype == CSF_F32 ? 4 : 2; }
 inline bool dtype_known(int dtype) { return dtype == CSF_BF16 || dtype == CSF_F16 || dtype == CSF_F32; }
 inline bool aligned_to(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
-// A csf_rows that a call reads or writes; `rows` of 0 need no buffers.
-inline bool rows_valid(const csf_rows &r) {
-    if ((r.kind != CSF_ROWS_NVFP4 && r.kind != CSF_ROWS_MXFP8) || r.cols < 1 || r.rows < 0) return false;
+// A csf_rows that a call reads or writes; `rows` of 0 need no buffers.  `fp8`:
+// the call takes FP8 rows.
+inline bool rows_valid(const csf_rows &r, bool fp8 = false) {
+    if ((r.kind != CSF_ROWS_NVFP4 && r.kind != CSF_ROWS_MXFP8 && !(fp8 && r.kind == CSF_ROWS_FP8)) || r.cols < 1 || r.rows < 0)
+        return false;
     if (r.rows == 0) return true;
     const int64_t cols = round_up(r.cols, 32);
     const int64_t code_bytes = r.kind == CSF_ROWS_NVFP4 ? cols / 2 : cols;
-    const int64_t blocks = r.kind == CSF_ROWS_NVFP4 ? cols / 16 : cols / 32;
+    const int64_t blocks = r.kind == CSF_ROWS_NVFP4 ? cols / 16 : r.kind == CSF_ROWS_FP8 ? (cols + 127) / 128 * 4 : cols / 32;
     return r.codes && r.scales && aligned_to(r.codes, 16) && aligned_to(r.scales, 16) && r.code_stride % 16 == 0 &&
            r.scale_stride % 16 == 0 && r.code_stride >= code_bytes && r.scale_stride >= round_up(blocks, 16);
 }

@@ -1,0 +1,443 @@
+// Rows to their experts' slots and back (csf_dispatch, csf_combine) and the
+// gradient of the way back (csf_combine_grad).
+//
+// All three are bound by memory, so each goes by tokens: a token's row is read
+// once, whether it is written to k slots (and quantised once for them), added
+// up from k slots, or both multiplied with k slots' rows and written to k
+// others.  A thread has 8 columns at a time, 16 bytes of 16-bit rows; a warp's
+// lanes are neighbours, so that a row's pieces are whole lines wherever the
+// row lies.
+#include <algorithm>
+
+#include "csf_elem.cuh"
+#include "csf_internal.cuh"
+#include "csf_layer.h"
+
+namespace csfk {
+namespace {
+
+constexpr int kPlain = -1;           // a kernel's output: plain rows, or a csf_rows_kind
+constexpr int kMaxSlots = 1024, kMaxCols = 1 << 24;
+constexpr int kRowThreads = 256;
+
+// How a block's threads lie over rows: `lanes` a row (a multiple of 16, the
+// lanes of the widest scale block, or of 32), `per_block` rows.
+struct Span {
+    int32_t tokens, cols, chunks;    // chunks: 8-column pieces of the row padded to 32
+    int32_t lanes, per_block;
+};
+
+// The fewest rounds of up to 256 threads, evenly; short rows share a block.
+Span span_of(int32_t tokens, int32_t cols, int least_lanes) {
+    Span s;
+    s.tokens = tokens;
+    s.cols = cols;
+    s.chunks = (int32_t)(round_up(cols, 32) / 8);
+    const int rounds = (s.chunks + kRowThreads - 1) / kRowThreads;
+    const int each = (s.chunks + rounds - 1) / rounds;
+    s.lanes = (int32_t)round_up(each, each <= least_lanes ? least_lanes : 32);
+    s.per_block = kRowThreads / s.lanes;
+    return s;
+}
+
+unsigned blocks_of(const Span &s) { return (unsigned)(((int64_t)s.tokens + s.per_block - 1) / s.per_block); }
+
+struct DispatchParams {
+    Span span;
+    const void *x;
+    int64_t x_stride;            // elements
+    int32_t wide_x, wide_out;
+    const int32_t *slots;        // null: row t goes to row t
+    int32_t k, out_dtype;
+    int64_t out_count;
+    char *out;
+    int64_t out_stride;          // bytes
+    uint8_t *scales;
+    int64_t scale_stride;
+    const float *tensor_scale;
+    uint32_t *err;
+};
+
+__device__ __forceinline__ int64_t row_bytes(int64_t row, int64_t stride, int dtype) {
+    return row * stride * (dtype == CSF_F32 ? 4 : 2);
+}
+
+// DTYPE: csf_dtype of x; KIND: what comes out.
+template <int DTYPE, int KIND>
+__global__ void __launch_bounds__(kRowThreads) dispatch_kernel(const __grid_constant__ DispatchParams p) {
+    const int nth = threadIdx.x / p.span.lanes, tid = threadIdx.x - nth * p.span.lanes;
+    const int64_t t = (int64_t)blockIdx.x * p.span.per_block + nth;
+    const bool live = t < p.span.tokens;
+    const char *x = static_cast<const char *>(p.x) + row_bytes(live ? t : 0, p.x_stride, DTYPE);
+    const int32_t *slots = p.slots ? p.slots + t * p.k : nullptr;
+    const int k = p.slots ? p.k : 1;
+    const float g = KIND == CSF_ROWS_NVFP4 && p.tensor_scale ? *p.tensor_scale : 1.f;
+    bool bad = false;
+    for (int c0 = 0; c0 < p.span.chunks; c0 += p.span.lanes) {
+        const int c = c0 + tid;
+        elem::Raw r = elem::load(x, c * 8, live ? p.span.cols : 0, DTYPE, p.wide_x);
+        quant::Coded q;
+        if constexpr (KIND == kPlain) {
+            if (p.out_dtype != DTYPE) {
+                float y[8];
+                elem::to_floats(y, r, DTYPE);
+                r = elem::from_floats(y, p.out_dtype);
+            }
+        } else {
+            float y[8];
+            elem::to_floats(y, r, DTYPE);
+            q = quant::encode8<KIND>(y, quant::block_amax<KIND>(y), g);
+        }
+        if (!live || (KIND == kPlain && c * 8 >= p.span.cols)) continue;
+#pragma unroll 8
+        for (int j = 0; j < k; ++j) {
+            const int64_t s = slots ? __ldg(slots + j) : t;
+            if (s < 0 || s >= p.out_count) {
+                bad |= s != -1;
+                continue;
+            }
+            char *out = p.out + s * p.out_stride;
+            if constexpr (KIND == kPlain) {
+                elem::store(out, c * 8, p.span.cols, r, p.out_dtype, p.wide_out);
+            } else {
+                uint8_t *scales = p.scales + s * p.scale_stride;
+                if (c < p.span.chunks) quant::put8<KIND>(q, reinterpret_cast<uint8_t *>(out), scales, c);
+                const int blocks = quant::scale_bytes<KIND>(p.span.chunks);
+                if (c < ((blocks + 15) & ~15) - blocks) scales[blocks + c] = 0;
+            }
+        }
+    }
+    if (bad && p.err) atomicOr(p.err, CSF_DEV_ERR_CORRUPT);
+}
+
+struct CombineParams {
+    Span span;
+    const void *y, *residual;
+    void *out;
+    int64_t y_stride, y_rows, residual_stride, out_stride;   // elements
+    const int32_t *slots;
+    const float *weights;
+    int32_t k, residual_dtype, out_dtype;
+    int32_t wide_y, wide_residual, wide_out;
+    uint32_t *err;
+};
+
+// DTYPE: csf_dtype of y.
+template <int DTYPE>
+__global__ void __launch_bounds__(kRowThreads) combine_kernel(const __grid_constant__ CombineParams p) {
+    constexpr int kBatch = DTYPE == CSF_F32 ? 4 : 8;      // rows under way at once
+    const int nth = threadIdx.x / p.span.lanes, tid = threadIdx.x - nth * p.span.lanes;
+    const int64_t t = (int64_t)blockIdx.x * p.span.per_block + nth;
+    if (t >= p.span.tokens) return;
+    const int32_t *slots = p.slots + t * p.k;
+    const float *weights = p.weights ? p.weights + t * p.k : nullptr;
+    bool bad = false;
+    for (int c = tid; c * 8 < p.span.cols; c += p.span.lanes) {
+        elem::Raw res;
+        if (p.residual)
+            res = elem::load(static_cast<const char *>(p.residual) + row_bytes(t, p.residual_stride, p.residual_dtype), c * 8,
+                             p.span.cols, p.residual_dtype, p.wide_residual);
+        float sum[8] = {};
+        for (int j0 = 0; j0 < p.k; j0 += kBatch) {
+            elem::Raw r[kBatch];
+            float w[kBatch];
+            bool on[kBatch];
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j) {
+                const int64_t s = j0 + j < p.k ? __ldg(slots + j0 + j) : -1;
+                on[j] = s >= 0 && s < p.y_rows;
+                bad |= !on[j] && s != -1;
+                w[j] = on[j] && weights ? __ldg(weights + j0 + j) : 1.f;
+                if (on[j]) r[j] = elem::load(static_cast<const char *>(p.y) + row_bytes(s, p.y_stride, DTYPE), c * 8, p.span.cols, DTYPE, p.wide_y);
+            }
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j) {
+                if (!on[j]) continue;
+                float y[8];
+                elem::to_floats(y, r[j], DTYPE);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) sum[i] = fmaf(w[j], y[i], sum[i]);
+            }
+        }
+        if (p.residual) {
+            float y[8];
+            elem::to_floats(y, res, p.residual_dtype);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sum[i] += y[i];
+        }
+        elem::store(static_cast<char *>(p.out) + row_bytes(t, p.out_stride, p.out_dtype), c * 8, p.span.cols,
+                    elem::from_floats(sum, p.out_dtype), p.out_dtype, p.wide_out);
+    }
+    if (bad && p.err) atomicOr(p.err, CSF_DEV_ERR_CORRUPT);
+}
+
+struct CombineGradParams {
+    Span span;
+    const void *g, *y;
+    int64_t g_stride, y_stride;      // elements
+    int64_t slot_rows;
+    const int32_t *slots;
+    const float *weights;
+    float *dweights;
+    char *dy;                        // null: none
+    int64_t dy_stride;               // bytes
+    uint8_t *scales;
+    int64_t scale_stride;
+    const float *tensor_scale;
+    int32_t k, g_dtype, dy_dtype;
+    int32_t wide_g, wide_y, wide_dy;
+    uint32_t *err;
+};
+
+// The products of g with the slots' rows are summed by thread over its
+// columns, then over a warp's lanes, then over the row's warps in order.
+// DTYPE: csf_dtype of y; KIND: what dy is.
+template <int DTYPE, int KIND>
+__global__ void __launch_bounds__(kRowThreads) combine_grad_kernel(const __grid_constant__ CombineGradParams p) {
+    constexpr int kBatch = DTYPE == CSF_F32 ? 4 : 8;      // choices at a time
+    __shared__ float part[kRowThreads / 32][kBatch];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int nth = threadIdx.x / p.span.lanes, tid = threadIdx.x - nth * p.span.lanes;
+    const int warps = p.span.lanes >> 5;                  // of a row
+    const int64_t t = (int64_t)blockIdx.x * p.span.per_block + nth;
+    const bool live = t < p.span.tokens;
+    const char *g_row = static_cast<const char *>(p.g) + row_bytes(live ? t : 0, p.g_stride, p.g_dtype);
+    const float ts = KIND == CSF_ROWS_NVFP4 && p.tensor_scale ? *p.tensor_scale : 1.f;
+    const bool products = p.dweights != nullptr;
+    bool bad = false;
+    for (int j0 = 0; j0 < p.k; j0 += kBatch) {
+        int64_t slot[kBatch];
+        float w[kBatch], sum[kBatch];
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+            const int64_t s = live && j0 + j < p.k ? __ldg(p.slots + t * p.k + j0 + j) : -1;
+            const bool on = s >= 0 && s < p.slot_rows;
+            bad |= !on && s != -1;
+            slot[j] = on ? s : -1;
+            w[j] = on && p.weights ? __ldg(p.weights + t * p.k + j0 + j) : 1.f;
+            sum[j] = 0.f;
+        }
+        for (int c0 = 0; c0 < p.span.chunks; c0 += p.span.lanes) {
+            const int c = c0 + tid;
+            const elem::Raw gr = elem::load(g_row, c * 8, live ? p.span.cols : 0, p.g_dtype, p.wide_g);
+            elem::Raw yr[kBatch];
+            if (products) {
+#pragma unroll
+                for (int j = 0; j < kBatch; ++j) {
+                    yr[j].a = yr[j].b = make_uint4(0, 0, 0, 0);
+                    if (slot[j] >= 0)
+                        yr[j] = elem::load(static_cast<const char *>(p.y) + row_bytes(slot[j], p.y_stride, DTYPE), c * 8, p.span.cols, DTYPE, p.wide_y);
+                }
+            }
+            float g[8];
+            elem::to_floats(g, gr, p.g_dtype);
+            uint32_t amax = 0;
+            if constexpr (KIND != kPlain) amax = quant::block_amax<KIND>(g);
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j) {
+                if (slot[j] < 0) continue;
+                float y[8];
+                if (products && c * 8 < p.span.cols) {
+                    elem::to_floats(y, yr[j], DTYPE);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) sum[j] = fmaf(g[i], y[i], sum[j]);
+                }
+                if (!p.dy) continue;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) y[i] = w[j] * g[i];
+                char *out = p.dy + slot[j] * p.dy_stride;
+                if constexpr (KIND == kPlain) {
+                    if (c * 8 < p.span.cols) elem::store(out, c * 8, p.span.cols, elem::from_floats(y, p.dy_dtype), p.dy_dtype, p.wide_dy);
+                } else {
+                    // the largest of the rounded products is the rounded product of the largest
+                    const uint32_t m = __float_as_uint(w[j] * __uint_as_float(amax)) & 0x7FFFFFFFu;
+                    uint8_t *scales = p.scales + slot[j] * p.scale_stride;
+                    if (c < p.span.chunks) quant::put8<KIND>(quant::encode8<KIND>(y, m, ts), reinterpret_cast<uint8_t *>(out), scales, c);
+                    const int blocks = quant::scale_bytes<KIND>(p.span.chunks);
+                    if (c < ((blocks + 15) & ~15) - blocks) scales[blocks + c] = 0;
+                }
+            }
+        }
+        if (!products) continue;
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+#pragma unroll
+            for (int d = 16; d > 0; d >>= 1) sum[j] += __shfl_xor_sync(0xFFFFFFFFu, sum[j], d);
+            if (lane == j) part[warp][j] = sum[j];
+        }
+        __syncthreads();
+        if (live && tid < kBatch && j0 + tid < p.k) {
+            float total = 0.f;
+            for (int i = 0; i < warps; ++i) total += part[nth * warps + i][tid];
+            p.dweights[t * p.k + j0 + tid] = total;
+        }
+        __syncthreads();
+    }
+    if (bad && p.err) atomicOr(p.err, CSF_DEV_ERR_CORRUPT);
+}
+
+template <int DTYPE>
+void launch_dispatch(const DispatchParams &p, int kind, cudaStream_t s) {
+    const unsigned grid = blocks_of(p.span), threads = (unsigned)(p.span.lanes * p.span.per_block);
+    switch (kind) {
+        case kPlain: dispatch_kernel<DTYPE, kPlain><<<grid, threads, 0, s>>>(p); break;
+        case CSF_ROWS_NVFP4: dispatch_kernel<DTYPE, CSF_ROWS_NVFP4><<<grid, threads, 0, s>>>(p); break;
+        case CSF_ROWS_MXFP8: dispatch_kernel<DTYPE, CSF_ROWS_MXFP8><<<grid, threads, 0, s>>>(p); break;
+        default: dispatch_kernel<DTYPE, CSF_ROWS_FP8><<<grid, threads, 0, s>>>(p); break;
+    }
+}
+
+template <int DTYPE>
+void launch_combine_grad(const CombineGradParams &p, int kind, cudaStream_t s) {
+    const unsigned grid = blocks_of(p.span), threads = (unsigned)(p.span.lanes * p.span.per_block);
+    switch (kind) {
+        case kPlain: combine_grad_kernel<DTYPE, kPlain><<<grid, threads, 0, s>>>(p); break;
+        case CSF_ROWS_NVFP4: combine_grad_kernel<DTYPE, CSF_ROWS_NVFP4><<<grid, threads, 0, s>>>(p); break;
+        case CSF_ROWS_MXFP8: combine_grad_kernel<DTYPE, CSF_ROWS_MXFP8><<<grid, threads, 0, s>>>(p); break;
+        default: combine_grad_kernel<DTYPE, CSF_ROWS_FP8><<<grid, threads, 0, s>>>(p); break;
+    }
+}
+
+// A plain matrix that a call needs.
+bool matrix_ok(const void *p, int64_t stride, int32_t dtype, int32_t cols) {
+    return p && dtype_known(dtype) && stride >= cols && aligned_to(p, dtype_bytes(dtype));
+}
+
+csf_status launched() {
+    if (cudaGetLastError() == cudaSuccess) return CSF_OK;
+    return CSF_ERR_CUDA;
+}
+
+}  // namespace
+}  // namespace csfk
+
+using namespace csfk;
+
+extern "C" csf_status csf_dispatch(const csf_dispatch_args *a, void *stream) {
+    if (!a || a->tokens < 0 || a->cols < 1 || a->out_count < 0 || !dtype_known(a->dtype)) return CSF_ERR_ARG;
+    if (a->slots && a->k < 1) return CSF_ERR_ARG;
+    if (!a->slots && a->out_count != a->tokens) return CSF_ERR_ARG;
+    if (a->cols > kMaxCols || (a->slots && a->k > kMaxSlots)) return CSF_ERR_UNSUPPORTED;
+    if (!a->out && (!rows_valid(a->out_rows, true) || a->out_rows.cols != a->cols || a->out_rows.rows != a->out_count ||
+                    !aligned_to(a->out_rows.tensor_scale, 4)))
+        return CSF_ERR_ARG;
+    if (a->tokens == 0) return CSF_OK;
+    if (!matrix_ok(a->x, a->x_stride, a->dtype, a->cols) || !aligned_to(a->slots, 4) || !aligned_to(a->error_word, 4)) return CSF_ERR_ARG;
+    if (a->out && !matrix_ok(a->out, a->out_stride, a->out_dtype, a->cols)) return CSF_ERR_ARG;
+    DispatchParams p = {};
+    p.span = span_of(a->tokens, a->cols, 16);
+    p.x = a->x;
+    p.x_stride = a->x_stride;
+    p.wide_x = wide_rows(a->x, a->x_stride, a->dtype);
+    p.slots = a->slots;
+    p.k = a->k;
+    p.out_count = a->out_count;
+    p.err = a->error_word;
+    int kind = kPlain;
+    if (a->out) {
+        p.out = static_cast<char *>(a->out);
+        p.out_dtype = a->out_dtype;
+        p.out_stride = a->out_stride * (int64_t)dtype_bytes(a->out_dtype);
+        p.wide_out = wide_rows(a->out, a->out_stride, a->out_dtype);
+    } else {
+        kind = a->out_rows.kind;
+        p.out = reinterpret_cast<char *>(a->out_rows.codes);
+        p.out_stride = a->out_rows.code_stride;
+        p.scales = a->out_rows.scales;
+        p.scale_stride = a->out_rows.scale_stride;
+        p.tensor_scale = a->out_rows.tensor_scale;
+    }
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (a->dtype == CSF_BF16) launch_dispatch<CSF_BF16>(p, kind, s);
+    else if (a->dtype == CSF_F16) launch_dispatch<CSF_F16>(p, kind, s);
+    else launch_dispatch<CSF_F32>(p, kind, s);
+    return launched();
+}
+
+extern "C" csf_status csf_combine(const csf_combine_args *a, void *stream) {
+    if (!a || a->tokens < 0 || a->cols < 1 || a->k < 1 || a->y_rows < 0 || !dtype_known(a->y_dtype) || !dtype_known(a->out_dtype)) return CSF_ERR_ARG;
+    if (a->cols > kMaxCols || a->k > kMaxSlots) return CSF_ERR_UNSUPPORTED;
+    if (a->tokens == 0) return CSF_OK;
+    if (a->y_rows > 0 && !matrix_ok(a->y, a->y_stride, a->y_dtype, a->cols)) return CSF_ERR_ARG;
+    if (!matrix_ok(a->out, a->out_stride, a->out_dtype, a->cols)) return CSF_ERR_ARG;
+    if (a->residual && !matrix_ok(a->residual, a->residual_stride, a->residual_dtype, a->cols)) return CSF_ERR_ARG;
+    if (!a->slots || !aligned_to(a->slots, 4) || !aligned_to(a->weights, 4) || !aligned_to(a->error_word, 4)) return CSF_ERR_ARG;
+    CombineParams p = {};
+    p.span = span_of(a->tokens, a->cols, 16);
+    p.y = a->y;
+    p.y_stride = a->y_stride;
+    p.y_rows = a->y_rows;
+    p.wide_y = wide_rows(a->y, a->y_stride, a->y_dtype);
+    p.residual = a->residual;
+    p.residual_stride = a->residual_stride;
+    p.residual_dtype = a->residual_dtype;
+    p.wide_residual = wide_rows(a->residual, a->residual_stride, a->residual_dtype);
+    p.out = a->out;
+    p.out_stride = a->out_stride;
+    p.out_dtype = a->out_dtype;
+    p.wide_out = wide_rows(a->out, a->out_stride, a->out_dtype);
+    p.slots = a->slots;
+    p.weights = a->weights;
+    p.k = a->k;
+    p.err = a->error_word;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const unsigned grid = blocks_of(p.span), threads = (unsigned)(p.span.lanes * p.span.per_block);
+    if (a->y_dtype == CSF_BF16) combine_kernel<CSF_BF16><<<grid, threads, 0, s>>>(p);
+    else if (a->y_dtype == CSF_F16) combine_kernel<CSF_F16><<<grid, threads, 0, s>>>(p);
+    else combine_kernel<CSF_F32><<<grid, threads, 0, s>>>(p);
+    return launched();
+}
+
+extern "C" csf_status csf_combine_grad(const csf_combine_grad_args *a, void *stream) {
+    if (!a || a->tokens < 0 || a->cols < 1 || a->k < 1 || a->slot_rows < 0 || !dtype_known(a->g_dtype)) return CSF_ERR_ARG;
+    if (a->cols > kMaxCols || a->k > kMaxSlots) return CSF_ERR_UNSUPPORTED;
+    const bool quantised = !a->dy && a->dy_rows.codes;
+    if (quantised && (!rows_valid(a->dy_rows, true) || a->dy_rows.cols != a->cols || a->dy_rows.rows != a->slot_rows ||
+                      !aligned_to(a->dy_rows.tensor_scale, 4)))
+        return CSF_ERR_ARG;
+    if (a->tokens == 0) return CSF_OK;
+    if (!matrix_ok(a->g, a->g_stride, a->g_dtype, a->cols)) return CSF_ERR_ARG;
+    if (a->dy && !matrix_ok(a->dy, a->dy_stride, a->dy_dtype, a->cols)) return CSF_ERR_ARG;
+    if (a->dweights && (!dtype_known(a->y_dtype) || (a->slot_rows > 0 && !matrix_ok(a->y, a->y_stride, a->y_dtype, a->cols)))) return CSF_ERR_ARG;
+    if (!a->slots || !aligned_to(a->slots, 4) || !aligned_to(a->weights, 4) || !aligned_to(a->dweights, 4) || !aligned_to(a->error_word, 4))
+        return CSF_ERR_ARG;
+    if (!a->dy && !quantised && !a->dweights) return CSF_OK;
+    CombineGradParams p = {};
+    p.span = span_of(a->tokens, a->cols, 32);
+    p.g = a->g;
+    p.g_stride = a->g_stride;
+    p.g_dtype = a->g_dtype;
+    p.wide_g = wide_rows(a->g, a->g_stride, a->g_dtype);
+    p.dweights = a->dweights;
+    int y_dtype = a->g_dtype;        // not read
+    if (a->dweights) {
+        y_dtype = a->y_dtype;
+        p.y = a->y;
+        p.y_stride = a->y_stride;
+        p.wide_y = wide_rows(a->y, a->y_stride, a->y_dtype);
+    }
+    p.slot_rows = a->slot_rows;
+    p.slots = a->slots;
+    p.weights = a->weights;
+    p.k = a->k;
+    p.err = a->error_word;
+    int kind = kPlain;
+    if (a->dy) {
+        p.dy = static_cast<char *>(a->dy);
+        p.dy_dtype = a->dy_dtype;
+        p.dy_stride = a->dy_stride * (int64_t)dtype_bytes(a->dy_dtype);
+        p.wide_dy = wide_rows(a->dy, a->dy_stride, a->dy_dtype);
+    } else if (quantised) {
+        kind = a->dy_rows.kind;
+        p.dy = reinterpret_cast<char *>(a->dy_rows.codes);
+        p.dy_stride = a->dy_rows.code_stride;
+        p.scales = a->dy_rows.scales;
+        p.scale_stride = a->dy_rows.scale_stride;
+        p.tensor_scale = a->dy_rows.tensor_scale;
+    }
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (y_dtype == CSF_BF16) launch_combine_grad<CSF_BF16>(p, kind, s);
+    else if (y_dtype == CSF_F16) launch_combine_grad<CSF_F16>(p, kind, s);
+    else launch_combine_grad<CSF_F32>(p, kind, s);
+    return launched();
+}

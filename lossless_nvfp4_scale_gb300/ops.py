@@ -29,6 +29,8 @@ from .csf import CsfError, _check, _es, lib
 
 NVFP4 = 0     # rows of E2M1 codes, a UE4M3 scale per 16; goes with NVFP4 weights
 MXFP8 = 1     # rows of E4M3 codes, a UE8M0 scale per 32; goes with MXFP4 weights
+FP8 = 3       # rows of E4M3 codes, a float32 scale per 128; goes with E4M3 weights that have one per 128 x 128
+_KINDS = (NVFP4, MXFP8, FP8)
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 _ACTS = {None: 0, "none": 0, "relu": 1, "silu": 2, "gelu": 3}
 
@@ -51,6 +53,16 @@ lib.csf_route_scratch_bytes.argtypes = [ctypes.c_int32, ctypes.c_int32]
 lib.csf_route_scratch_bytes.restype = ctypes.c_size_t
 lib.csf_expert_matmul.argtypes = [ctypes.c_char_p, _vp]
 lib.csf_expert_matmul.restype = ctypes.c_int
+
+# Those of csf_layer.h.
+_FP8_MATMUL = struct.Struct("@" + _ROWS + "PqiiiiPPPiiPiiPPqiiPq" + _ROWS + "P")     # csf_fp8_matmul_args
+_DISPATCH = struct.Struct("@PqiiiiPqPqi4x" + _ROWS + "P")                # csf_dispatch_args
+_COMBINE = struct.Struct("@PqqiiiiPPPqiiPqP")                            # csf_combine_args
+_COMBINE_GRAD = struct.Struct("@PqPqqiiiiiiPPPq" + _ROWS + "PP")         # csf_combine_grad_args
+_ROUTE_GRAD = struct.Struct("@PqPqiiiiPPPi4x")                           # csf_route_grad_args
+for _call in (lib.csf_fp8_matmul, lib.csf_dispatch, lib.csf_combine, lib.csf_combine_grad, lib.csf_route_grad):
+    _call.argtypes = [ctypes.c_char_p, _vp]
+    _call.restype = ctypes.c_int
 
 _raw_stream = torch._C._cuda_getCurrentRawStream
 _current_device = torch._C._cuda_getDevice
@@ -129,13 +141,15 @@ def _code_bytes(kind: int, cols: int) -> int:
 
 
 def _scale_bytes(kind: int, cols: int) -> int:
+    if kind == FP8:
+        return _up((cols + 127) // 128 * 4, 16)
     return _up(_up(cols, 32) // (16 if kind == NVFP4 else 32), 16)
 
 
 @dataclass
 class Quantized:
     """Quantised rows (csf_rows): uint8 codes [rows, code bytes] and scales
-    [rows, scale bytes], rows 16-byte aligned.  `tensor_scale` is the NVFP4
+    [rows, scale bytes] (FP8's are float32 underneath), rows 16-byte aligned.  `tensor_scale` is the NVFP4
     tensor scale they were made with (float32 [1]) or None; a product takes it
     through its alpha.  As an output they keep theirs where a call gives none."""
     kind: int
@@ -157,8 +171,8 @@ class Quantized:
 
 def empty_quantized(kind: int, rows: int, cols: int, device=None, tensor_scale: torch.Tensor | None = None) -> Quantized:
     """Quantised rows with undefined contents."""
-    if kind not in (NVFP4, MXFP8):
-        raise CsfError("quantised rows are NVFP4 or MXFP8")
+    if kind not in _KINDS:
+        raise CsfError("quantised rows are NVFP4 or MXFP8 or FP8")
     device = device if device is not None else "cuda"
     if cols < 1:
         raise CsfError("quantised rows have at least one column")
@@ -170,10 +184,10 @@ def _where(device: int) -> str:
     return f" on cuda:{device}" if device >= 0 else ""
 
 
-def _check_quantized(q: Quantized, what: str, device: int):
+def _check_quantized(q: Quantized, what: str, device: int, kinds=_KINDS):
     c, s = q.codes, q.scales
-    if q.kind not in (NVFP4, MXFP8):
-        raise CsfError(f"{what}: quantised rows are NVFP4 or MXFP8")
+    if q.kind not in kinds:
+        raise CsfError(f"{what}: quantised rows are {' or '.join(('NVFP4', 'MXFP8', '', 'FP8')[k] for k in kinds)}")
     if c.dtype != torch.uint8 or s.dtype != torch.uint8 or device < 0 or c.get_device() != device or s.get_device() != device:
         raise CsfError(f"{what}: codes and scales must be uint8 CUDA tensors{_where(device)}")
     if c.dim() != 2 or s.dim() != 2 or c.shape[0] != s.shape[0] or c.stride(1) != 1 or s.stride(1) != 1:
@@ -297,7 +311,7 @@ def expert_matmul(x: Quantized, w: torch.Tensor, w_scales: torch.Tensor, expert_
         return _on(stream, expert_matmul, x, w, w_scales, expert_start, rows, alpha, bias, activation, gated, row_scale,
                    residual, out, out_tensor_scale, error_word)
     device = x.codes.get_device()
-    _check_quantized(x, "expert_matmul: x", device)
+    _check_quantized(x, "expert_matmul: x", device, (NVFP4, MXFP8))
     if w.dtype != torch.uint8 or w.get_device() != device or w.dim() != 3 or not w.is_contiguous() or w.shape[2] * 2 != x.cols:
         raise CsfError(f"expert_matmul: w must be a contiguous uint8 CUDA tensor [E, N, {x.cols // 2}]{_where(device)}")
     E, N = w.shape[0], w.shape[1]
@@ -330,7 +344,7 @@ def expert_matmul(x: Quantized, w: torch.Tensor, w_scales: torch.Tensor, expert_
     elif isinstance(out, int):
         out = empty_quantized(out, S, F, x.codes.device, out_tensor_scale)
     if isinstance(out, Quantized):
-        _check_quantized(out, "expert_matmul: out", device)
+        _check_quantized(out, "expert_matmul: out", device, (NVFP4, MXFP8))
         if out.rows != S or out.cols != F:
             raise CsfError("expert_matmul: out does not match the product")
         out.tensor_scale = _tensor_scale(out, out_tensor_scale, "expert_matmul", device)
@@ -353,4 +367,251 @@ def expert_matmul(x: Quantized, w: torch.Tensor, w_scales: torch.Tensor, expert_
     finally:
         if own_word:
             _error_lock.release()
+    return out
+
+
+# ---- tokens to slots and back, and the gradients (csf_layer.h) ----
+
+def _reporting(call, pack: struct.Struct, fields: tuple, error_word, device: int, what: str):
+    """The library call with an error word as its last field: the one given, or the device's own."""
+    if error_word is not None:
+        word = _vector(error_word, f"{what}: error_word", 1, torch.int32, device)
+        return _launch(call, pack.pack(*fields, word), device, "csf_" + what)
+    with _error_lock:
+        _launch(call, pack.pack(*fields, _error_word(device).data_ptr()), device, "csf_" + what)
+
+
+def _slots(slots, tokens: int, what: str, device: int):
+    if slots.get_device() != device or slots.dtype != torch.int32 or slots.dim() != 2 or slots.shape[0] != tokens or \
+            not slots.is_contiguous():
+        raise CsfError(f"{what}: slots must be a contiguous int32 CUDA tensor [{tokens}, k]{_where(device)}")
+    if not 1 <= slots.shape[1] <= 1024:
+        raise CsfError(f"{what}: k must be 1 to 1024")
+    return slots.data_ptr(), slots.shape[1]
+
+
+def _choice_vector(t, name: str, like: torch.Tensor, device: int):
+    """A float32 value per choice, contiguous, of the slots' or ids' shape."""
+    if t is not None and tuple(t.shape) != tuple(like.shape):
+        raise CsfError(f"{name} must be {list(like.shape)}")
+    return _vector(t, name, like.numel(), torch.float32, device)
+
+
+def _output(out, rows: int, cols: int, dtype, tensor_scale, what: str, x: torch.Tensor):
+    """An output that a call is given or names by dtype or kind: the result,
+    then the fields (pointer, stride, csf_dtype) of a plain one and those of
+    csf_rows, zeros for the one that it is not."""
+    device = x.get_device()
+    if out is None:
+        out = dtype
+    if isinstance(out, torch.dtype):
+        if out not in _DTYPES:
+            raise CsfError(f"{what}: out must be bfloat16, float16 or float32")
+        out = torch.empty((rows, cols), dtype=out, device=x.device)
+    elif isinstance(out, int):
+        out = empty_quantized(out, rows, cols, x.device, tensor_scale)
+    if isinstance(out, Quantized):
+        _check_quantized(out, f"{what}: out", device)
+        if out.rows != rows or out.cols != cols:
+            raise CsfError(f"{what}: out is {out.rows} rows of {out.cols}, not {rows} of {cols}")
+        out.tensor_scale = _tensor_scale(out, tensor_scale, what, device)
+        return out, (0, 0, 0), out.fields()
+    if tensor_scale is not None:
+        raise CsfError(f"{what}: only NVFP4 rows have a tensor scale")
+    return out, (*_matrix(out, f"{what}: out", rows, cols, device), _DTYPES[out.dtype]), _NO_ROWS
+
+
+def _plain(x: torch.Tensor, what: str):
+    if x.dim() != 2 or x.dtype not in _DTYPES:
+        raise CsfError(f"{what} must be [rows, cols] of bfloat16, float16 or float32")
+    if x.shape[1] < 1:
+        raise CsfError(f"{what} has at least one column")
+    return _matrix(x, what, x.shape[0], x.shape[1], x.get_device())
+
+
+def quantize(x: torch.Tensor, kind: int, tensor_scale: torch.Tensor | None = None, out: Quantized | None = None,
+             stream=None) -> Quantized:
+    """The rows of `x` [rows, cols] quantised (csf_dispatch without slots)."""
+    if stream is not None:
+        return _on(stream, quantize, x, kind, tensor_scale, out)
+    xp, xs = _plain(x, "quantize: x")
+    T, H = x.shape
+    if kind not in _KINDS:
+        raise CsfError("quantised rows are NVFP4 or MXFP8 or FP8")
+    if out is not None and (not isinstance(out, Quantized) or out.kind != kind):
+        raise CsfError("quantize: out does not match kind")
+    out, plain, rows = _output(kind if out is None else out, T, H, None, tensor_scale, "quantize", x)
+    _launch(lib.csf_dispatch, _DISPATCH.pack(xp, xs, _DTYPES[x.dtype], T, H, 0, 0, T, *plain, *rows, 0), x.get_device(), "csf_dispatch")
+    return out
+
+
+def dispatch(x: torch.Tensor, slots: torch.Tensor, out=None, tensor_scale: torch.Tensor | None = None,
+             error_word: torch.Tensor | None = None, stream=None):
+    """The rows of `x` [tokens, cols] to the slots of their choices (`slots`
+    [tokens, k] of a Routing): out[slots[t, j]] = x[t] (csf_dispatch).
+
+    `out` is a dtype (x's without one), a kind (a new Quantized, made in the
+    same pass), a tensor or a Quantized of any number of rows.  New ones have
+    tokens * k rows; rows that no slot names hold nothing, in one that is given
+    they stay as they were.  Slots of -1 fell away; others out of range reach
+    `error_word` or errors().  The gradient is dispatch_grad."""
+    if stream is not None:
+        return _on(stream, dispatch, x, slots, out, tensor_scale, error_word)
+    xp, xs = _plain(x, "dispatch: x")
+    T, H = x.shape
+    device = x.get_device()
+    sp, k = _slots(slots, T, "dispatch", device)
+    S = out.rows if isinstance(out, Quantized) else out.shape[0] if isinstance(out, torch.Tensor) and out.dim() else T * k
+    out, plain, rows = _output(out, S, H, x.dtype, tensor_scale, "dispatch", x)
+    _reporting(lib.csf_dispatch, _DISPATCH, (xp, xs, _DTYPES[x.dtype], T, H, k, sp, S, *plain, *rows), error_word, device, "dispatch")
+    return out
+
+
+def combine(y: torch.Tensor, slots: torch.Tensor, weights: torch.Tensor | None = None, residual: torch.Tensor | None = None,
+            out=None, error_word: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Each token's sum of its slots' rows of `y` [slots, cols], with the
+    router's `weights` (1 without), plus `residual` (csf_combine):
+    out[t] = sum_j weights[t, j] * y[slots[t, j]] + residual[t], in 32 bits.
+    `out` is a dtype (y's without one) or a tensor, `residual` itself too.
+    Slots of -1 add nothing.  The gradient is combine_grad."""
+    if stream is not None:
+        return _on(stream, combine, y, slots, weights, residual, out, error_word)
+    yp, ys = _plain(y, "combine: y")
+    if slots.dim() != 2:
+        raise CsfError("combine: slots must be [tokens, k]")
+    (S, H), T, device = y.shape, slots.shape[0], y.get_device()
+    sp, k = _slots(slots, T, "combine", device)
+    rp, rs = (0, 0) if residual is None else _matrix(residual, "combine: residual", T, H, device)
+    if not isinstance(out, (torch.Tensor, torch.dtype, type(None))):
+        raise CsfError("combine: out is a dtype or a tensor")
+    out, (op, os_, odt), _ = _output(out, T, H, y.dtype, None, "combine", y)
+    _reporting(lib.csf_combine, _COMBINE, (yp, ys, S, _DTYPES[y.dtype], T, H, k, sp, _choice_vector(weights, "combine: weights", slots, device),
+                                           rp, rs, 0 if residual is None else _DTYPES[residual.dtype], odt, op, os_),
+               error_word, device, "combine")
+    return out
+
+
+def dispatch_grad(g: torch.Tensor, slots: torch.Tensor, out=None, error_word: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """The gradient of dispatch for its x, from that of its result: each
+    token's rows of `g` [slots, cols] added up."""
+    return combine(g, slots, None, None, out, error_word, stream)
+
+
+def combine_grad(g: torch.Tensor, y: torch.Tensor | None, slots: torch.Tensor, weights: torch.Tensor | None = None, out=None,
+                 tensor_scale: torch.Tensor | None = None, error_word: torch.Tensor | None = None, stream=None):
+    """The gradients of combine, from that of its result, `g` [tokens, cols]
+    (csf_combine_grad): dy[slots[t, j]] = weights[t, j] * g[t], and the
+    weights' dweights[t, j] = sum(g[t] * y[slots[t, j]]), float32 [tokens, k]
+    (None without `y`).  The residual's is g itself.
+
+    `out` says what dy is, as dispatch's does (rows likewise: y's number of
+    them, or tokens * k); False: no dy is wanted, and None is returned."""
+    if stream is not None:
+        return _on(stream, combine_grad, g, y, slots, weights, out, tensor_scale, error_word)
+    gp, gs = _plain(g, "combine_grad: g")
+    T, H = g.shape
+    device = g.get_device()
+    sp, k = _slots(slots, T, "combine_grad", device)
+    if y is not None:
+        S = y.shape[0] if y.dim() else 0
+    else:
+        S = out.rows if isinstance(out, Quantized) else out.shape[0] if isinstance(out, torch.Tensor) and out.dim() else T * k
+    yp, ys = (0, 0) if y is None else _matrix(y, "combine_grad: y", S, H, device)
+    if out is False:
+        dy, (dp, ds, ddt), rows = None, (0, 0, 0), _NO_ROWS
+    else:
+        dy, (dp, ds, ddt), rows = _output(out, S, H, (g if y is None else y).dtype, tensor_scale, "combine_grad", g)
+    wp = _choice_vector(weights, "combine_grad: weights", slots, device)
+    dweights = None if y is None else torch.empty((T, k), dtype=torch.float32, device=g.device)
+    _reporting(lib.csf_combine_grad, _COMBINE_GRAD,
+               (gp, gs, yp, ys, S, _DTYPES[g.dtype], 0 if y is None else _DTYPES[y.dtype], T, H, k, ddt, sp, wp, dp, ds, *rows,
+                0 if y is None else dweights.data_ptr()), error_word, device, "combine_grad")
+    return dy, dweights
+
+
+def route_grad(logits: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, dweights: torch.Tensor, renormalize: bool = True,
+               out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """The gradient of route's weights for its logits, from theirs
+    (csf_route_grad): `ids` and `weights` are those of the Routing,
+    `renormalize` that of the call.  The choice of experts counts as fixed.
+    The result has the logits' type, in `out` (the logits themselves too) or a
+    new tensor."""
+    if stream is not None:
+        return _on(stream, route_grad, logits, ids, weights, dweights, renormalize, out)
+    lp, ls = _plain(logits, "route_grad: logits")
+    T, E = logits.shape
+    device = logits.get_device()
+    if ids.get_device() != device or ids.dtype != torch.int32 or ids.dim() != 2 or ids.shape[0] != T or not ids.is_contiguous():
+        raise CsfError(f"route_grad: ids must be a contiguous int32 CUDA tensor [{T}, k]{_where(device)}")
+    k = ids.shape[1]
+    if not 1 <= k <= min(32, E):
+        raise CsfError(f"route_grad: k must be 1 to {min(32, E)}")
+    if out is None:
+        out = torch.empty((T, E), dtype=logits.dtype, device=logits.device)
+    op, os_ = _matrix(out, "route_grad: out", T, E, device, logits.dtype)
+    if weights is None or dweights is None:
+        raise CsfError("route_grad: weights and dweights are needed")
+    a = _ROUTE_GRAD.pack(lp, ls, op, os_, _DTYPES[logits.dtype], T, E, k, ids.data_ptr(),
+                         _choice_vector(weights, "route_grad: weights", ids, device),
+                         _choice_vector(dweights, "route_grad: dweights", ids, device), renormalize)
+    _launch(lib.csf_route_grad, a, device, "csf_route_grad")
+    return out
+
+
+# ---- products with a scale for each block of 128 (csf_layer.h) ----
+
+def fp8_matmul(x: Quantized, w: torch.Tensor, w_scales: torch.Tensor, expert_start: torch.Tensor | None = None,
+               rows: torch.Tensor | None = None, bias: torch.Tensor | None = None, activation: str | None = None,
+               gated: bool = False, row_scale: torch.Tensor | None = None, residual: torch.Tensor | None = None,
+               transposed: bool = False, out=torch.bfloat16, error_word: torch.Tensor | None = None, stream=None):
+    """Product of FP8 rows with E4M3 weights that have a scale per 128 x 128
+    block (csf_fp8_matmul).
+
+    `w` is float8_e4m3fn (or its bytes) [E, N, K], `w_scales` float32
+    [E, ceil(N / 128), ceil(K / 128)].  Slots, `rows`, `bias`, `activation`,
+    `gated`, `row_scale` and `residual` are expert_matmul's.  `transposed`: x has N
+    columns and the result K, x . w in place of x . w^T; with x the quantised
+    gradient of a product's result it is that of the product's x.
+    `out` is a dtype, a tensor, FP8 (a new Quantized), or a Quantized.
+    Data errors reach `error_word` (int32 [1]) or, without one, errors()."""
+    if stream is not None:
+        return _on(stream, fp8_matmul, x, w, w_scales, expert_start, rows, bias, activation, gated, row_scale, residual,
+                   transposed, out, error_word)
+    device = x.codes.get_device()
+    _check_quantized(x, "fp8_matmul: x", device, (FP8,))
+    if w.dtype not in (torch.float8_e4m3fn, torch.uint8) or w.get_device() != device or w.dim() != 3 or not w.is_contiguous():
+        raise CsfError(f"fp8_matmul: w must be a contiguous float8_e4m3fn or uint8 CUDA tensor [E, N, K]{_where(device)}")
+    E, N, K = w.shape
+    if x.cols != (N if transposed else K):
+        raise CsfError(f"fp8_matmul: x has {x.cols} columns, w{' transposed' if transposed else ''} takes {N if transposed else K}")
+    if tuple(w_scales.shape) != (E, (N + 127) // 128, (K + 127) // 128):
+        raise CsfError(f"fp8_matmul: w_scales must be [{E}, {(N + 127) // 128}, {(K + 127) // 128}]")
+    wp = _vector(w_scales, "fp8_matmul: w_scales", w_scales.numel(), torch.float32, device)
+    if activation not in _ACTS:
+        raise CsfError(f"fp8_matmul: unknown activation {activation!r}")
+    if rows is not None and (rows.get_device() != device or rows.dtype != torch.int32 or not rows.is_contiguous() or rows.dim() != 1):
+        raise CsfError(f"fp8_matmul: rows must be a contiguous int32 CUDA vector{_where(device)}")
+    es, es64 = _es(expert_start)
+    if expert_start is not None:
+        if expert_start.get_device() != device:
+            raise CsfError(f"expert_start must be a CUDA tensor{_where(device)}")
+        if expert_start.numel() != E + 1:
+            raise CsfError("expert_start must have E+1 entries")
+    S = x.rows if rows is None else rows.shape[0]
+    O = K if transposed else N
+    F = O // 2 if gated else O
+    bias_dtype = 0
+    if bias is not None:
+        if bias.dtype not in _DTYPES:
+            raise CsfError("fp8_matmul: bias must be bfloat16, float16 or float32")
+        bias_dtype = _DTYPES[bias.dtype]
+    rp, rs = (0, 0) if residual is None else _matrix(residual, "fp8_matmul: residual", S, F, device)
+    if (isinstance(out, int) and out != FP8) or (isinstance(out, Quantized) and out.kind != FP8):
+        raise CsfError("fp8_matmul: out is a dtype, a tensor or FP8 rows")
+    out, (op, os_, odt), orows = _output(out, S, F, torch.bfloat16, None, "fp8_matmul", x.codes)
+    _reporting(lib.csf_fp8_matmul, _FP8_MATMUL, (
+        *x.fields(), 0 if rows is None else rows.data_ptr(), S, E, N, K, transposed, w.data_ptr(), wp, es or 0, es64, bias_dtype,
+        0 if bias is None else _vector(bias, "fp8_matmul: bias", E * O, bias.dtype, device), _ACTS[activation], gated,
+        _vector(row_scale, "fp8_matmul: row_scale", S, torch.float32, device), rp, rs,
+        0 if residual is None else _DTYPES[residual.dtype], odt, op, os_, *orows), error_word, device, "fp8_matmul")
     return out
