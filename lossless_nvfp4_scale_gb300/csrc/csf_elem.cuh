@@ -107,6 +107,30 @@ __device__ __forceinline__ void store(void *row, int c, int cols, const Raw &r, 
     }
 }
 
+// The same for kernels that are short of registers: what is not wide is a
+// function of its own.
+static __device__ __noinline__ Raw load_few(const void *row, int c, int cols, int dtype) { return load(row, c, cols, dtype, false); }
+static __device__ __noinline__ void store_few(void *row, int c, int cols, const Raw r, int dtype) { store(row, c, cols, r, dtype, false); }
+
+__device__ __forceinline__ Raw load_apart(const void *row, int c, int cols, int dtype, bool wide) {
+    if (!wide || c + 8 > cols) return load_few(row, c, cols, dtype);
+    Raw r;
+    const uint4 *at = reinterpret_cast<const uint4 *>(static_cast<const char *>(row) + (size_t)c * (dtype == CSF_F32 ? 4 : 2));
+    r.a = __ldg(at);
+    r.b = dtype == CSF_F32 ? __ldg(at + 1) : make_uint4(0, 0, 0, 0);
+    return r;
+}
+
+__device__ __forceinline__ void store_apart(void *row, int c, int cols, const Raw &r, int dtype, bool wide) {
+    if (!wide || c + 8 > cols) {
+        store_few(row, c, cols, r, dtype);
+        return;
+    }
+    uint4 *at = reinterpret_cast<uint4 *>(static_cast<char *>(row) + (size_t)c * (dtype == CSF_F32 ? 4 : 2));
+    at[0] = r.a;
+    if (dtype == CSF_F32) at[1] = r.b;
+}
+
 }  // namespace elem
 
 // Whether rows may be accessed 16 bytes at a time.

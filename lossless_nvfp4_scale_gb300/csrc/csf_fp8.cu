@@ -60,7 +60,8 @@ extern "C" csf_status csf_fp8_matmul(const csf_fp8_matmul_args *a, void *stream)
     p.es64 = a->expert_start_is_int64;
     const int32_t nb = (N + 127) / 128, kb = (K + 127) / 128;
     p.w_scales = a->w_scales;
-    p.ws_expert = (int64_t)nb * kb;
+    if ((int64_t)nb * kb * E > INT32_MAX) return CSF_ERR_UNSUPPORTED;      // scales count in 32 bits
+    p.ws_expert = nb * kb;
     p.ws_f = a->transposed ? 1 : kb;
     p.ws_b = a->transposed ? kb : 1;
     p.bias = a->bias;
@@ -134,7 +135,9 @@ extern "C" csf_status csf_fp8_matmul(const csf_fp8_matmul_args *a, void *stream)
     {
         const cuuint64_t dims[3] = {(cuuint64_t)K, (cuuint64_t)N, (cuuint64_t)E};
         const cuuint64_t strides[2] = {(cuuint64_t)K, (cuuint64_t)K * (cuuint64_t)N};
-        const cuuint32_t box[3] = {128, 128, 1};
+        // a pair's blocks hold 64 of a weight block's 128 output columns each
+        const cuuint32_t part = shape == kPair ? 64 : 128;
+        const cuuint32_t box[3] = {a->transposed ? part : 128, a->transposed ? 128 : part, 1};
         if (!byte_map(&wmap, a->w, 3, dims, strides, box)) return CSF_ERR_CUDA;
     }
     if (!a->rows) {
@@ -145,7 +148,8 @@ extern "C" csf_status csf_fp8_matmul(const csf_fp8_matmul_args *a, void *stream)
     } else {
         xmap = wmap;      // not read
     }
-    Kernel k = a->rows ? rows_by_index(shape, !a->out) : rows_in_order(shape, !a->out);
+    const int mode = !a->out ? kQuant : a->residual || a->out_dtype == CSF_F32 ? kPlain : kHalves;
+    Kernel k = a->rows ? rows_by_index(shape, mode) : rows_in_order(shape, mode);
     // the register split waits for what the block was launched with
     const int regs = shape == kOne || shape == kOneShared ? 0 : kLaunchRegs;
     if (!allow_smem(reinterpret_cast<const void *>(k), kSmemLimit, regs)) return CSF_ERR_CUDA;

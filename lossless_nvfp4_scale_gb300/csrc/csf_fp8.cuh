@@ -6,8 +6,7 @@
 // exactly scaled alike at a time, into tensor memory; eight warps then take
 // each such partial sum out, multiply it with its row's scale times the weight
 // block's and add it up in registers, in 32 bits: lane and register are row
-// and column, so the factor is one number a thread and block, and two columns
-// go through a multiply-add at once.  Meanwhile the next partial sums form in
+// and column, so the factor is one number a thread and block.  Meanwhile the next partial sums form in
 // other columns of tensor memory.
 //
 // Where slots are many, two neighbouring blocks pair up: 256 slots by 256
@@ -49,11 +48,10 @@ constexpr int kMaxSplit = 8;
 constexpr int kSplitSlots = 64;          // slots of a tile that a cluster shares
 constexpr uint32_t kTileBytes = 128 * 128;
 constexpr uint32_t kTmemCols = 512;
-constexpr int kTurnStride = 36;          // floats between rows of a warp's 32 x 32 piece
-constexpr uint32_t kTurnBytes = kSumWarps * 32 * kTurnStride * 4;
+constexpr uint32_t kTurnBytes = kSumWarps * 32 * 128;      // a piece of 32 rows of 128 bytes each
 // Registers of the warps that copy and of those that sum, where a thread holds
 // 128 sums: together what the block was launched with, 384 x 168.
-constexpr int kCopyRegs = 72, kSumRegs = 216, kLaunchRegs = 168;
+constexpr int kCopyRegs = 56, kSumRegs = 224, kLaunchRegs = 168;
 static_assert(128 * kCopyRegs + 256 * kSumRegs == kThreads * kLaunchRegs, "registers of a block");
 
 struct Params {
@@ -62,8 +60,7 @@ struct Params {
     const int32_t *rows;
     const void *start;
     const float *w_scales;
-    int64_t ws_expert;           // floats between experts' scales
-    int32_t ws_f, ws_b;          // floats between output blocks, and between summed blocks
+    int32_t ws_expert, ws_f, ws_b;   // floats between experts' scales, output blocks, summed blocks
     const void *bias;
     const float *row_scale;
     const void *residual;
@@ -93,12 +90,25 @@ struct Params {
 struct Shared {
     uint64_t full[kMaxStages], empty[kMaxStages], acc_full[4], acc_empty[4];
     uint32_t tmem, abort, warp_sum[kThreads / 32];
-    float amax[2][2][2][128];    // by tile, half, weight block and row
+    Tile tile[kSumWarps];        // the summing warps' next
+    float amax[2][2][128];       // by tile, half and row
 };
 
 __device__ __forceinline__ float activate(float v, int act) {
     if (act == CSF_ACT_SILU || act == CSF_ACT_GELU_TANH) return mm::smooth(v, act == CSF_ACT_GELU_TANH);
     return act == CSF_ACT_RELU && v < 0.f ? 0.f : v;
+}
+
+__device__ __forceinline__ void activate16(float (&y)[16], int act) {
+    if (act == CSF_ACT_NONE) return;
+    if (act == CSF_ACT_RELU) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) y[i] = y[i] < 0.f ? 0.f : y[i];
+    } else {
+        const bool gelu = act == CSF_ACT_GELU_TANH;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) y[i] = mm::smooth(y[i], gelu);
+    }
 }
 
 // One slot's columns f .. f+7 of y = act(p): row weight, residual, and out.
@@ -113,7 +123,7 @@ __device__ __forceinline__ void finish8(const Params &p, float (&y)[8], int64_t 
     if (p.residual && live) {
         float r[8];
         const char *row = static_cast<const char *>(p.residual) + slot * p.residual_stride * (p.residual_dtype == CSF_F32 ? 4 : 2);
-        elem::to_floats(r, elem::load(row, f, p.F, p.residual_dtype, p.residual_wide), p.residual_dtype);
+        elem::to_floats(r, elem::load_apart(row, f, p.F, p.residual_dtype, p.residual_wide), p.residual_dtype);
 #pragma unroll
         for (int i = 0; i < 8; ++i) y[i] += r[i];
     }
@@ -129,7 +139,7 @@ __device__ __forceinline__ void finish8(const Params &p, float (&y)[8], int64_t 
             for (int i = n; i < ((n + 15) & ~15); i += 4) *reinterpret_cast<float *>(scales + i) = 0.f;
         }
     } else {
-        if (live && f < p.F) elem::store(out, f, p.F, elem::from_floats(y, p.out_dtype), p.out_dtype, p.out_wide);
+        if (live && f < p.F) elem::store_apart(out, f, p.F, elem::from_floats(y, p.out_dtype), p.out_dtype, p.out_wide);
     }
 }
 
@@ -137,22 +147,27 @@ __device__ __forceinline__ void finish8(const Params &p, float (&y)[8], int64_t 
 __device__ __forceinline__ void add_bias8(const Params &p, float *y, int e, int c) {
     float b[8];
     const char *row = static_cast<const char *>(p.bias) + (int64_t)e * p.O * (p.bias_dtype == CSF_F32 ? 4 : 2);
-    elem::to_floats(b, elem::load(row, c, p.O, p.bias_dtype, p.bias_wide), p.bias_dtype);
+    elem::to_floats(b, elem::load_apart(row, c, p.O, p.bias_dtype, p.bias_wide), p.bias_dtype);
 #pragma unroll
     for (int i = 0; i < 8; ++i) y[i] += b[i];
 }
 
+// What comes out: 16-bit rows, any plain rows (float32, or with a residual),
+// FP8 rows.  Kernels of their own, since what one holds in registers another
+// would spill.
+enum Mode { kHalves = 0, kPlain = 1, kQuant = 2 };
+
 // CTAS: blocks of a pair.  AT: 128-column weight blocks per tile.  ROWS: slot
 // s reads row rows[s] of x, else row s.  SPLIT: clusters share a tile's depth.
-// QUANT: FP8 rows come out.
-template <int CTAS, int AT, bool ROWS, bool SPLIT, bool QUANT>
+// MODE: what comes out.
+template <int CTAS, int AT, bool ROWS, bool SPLIT, int MODE>
 __global__ void __launch_bounds__(kThreads, 1)
 fp8_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap, const __grid_constant__ Params p) {
     static_assert(CTAS == 1 || (AT == 2 && !SPLIT), "a pair has 256 columns and all of the depth");
     extern __shared__ __align__(1024) uint8_t dyn[];
     __shared__ Shared sh;
-    constexpr int kSets = (int)kTmemCols / (128 * AT);      // partial sums under way
-    constexpr int kWeights = CTAS == 2 ? 1 : AT;            // weight blocks of this block of threads
+    constexpr int kSets = (int)kTmemCols / 128;             // partial sums of 128 columns under way
+    constexpr uint32_t kPart = kTileBytes / CTAS;           // bytes of a weight block that this block of threads holds
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t ring0 = (tc::smem_u32(dyn) + 1023u) & ~1023u;
     uint8_t *after_ring = dyn + (ring0 - tc::smem_u32(dyn)) + (size_t)p.stages * p.stage_bytes;
@@ -167,12 +182,13 @@ fp8_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constan
 
     if (tid == 0) {
         for (int i = 0; i < p.stages; ++i) {
-            tc::bar_init(full0 + 8 * i, ROWS ? 1 + 2 * CTAS : 1);      // the weights; the copying warps
+            // the weights; the copying lanes; the copies of a pair's other block (which counts only its lanes)
+            tc::bar_init(full0 + 8 * i, !ROWS ? 1 : CTAS == 1 ? 65 : pair_rank == 0 ? 66 : 64);
             tc::bar_init(empty0 + 8 * i, 1);
         }
         for (int i = 0; i < kSets; ++i) {
             tc::bar_init(accf0 + 8 * i, 1);
-            tc::bar_init(acce0 + 8 * i, kSumWarps * CTAS);
+            tc::bar_init(acce0 + 8 * i, kSumWarps / AT * CTAS);
         }
         sh.abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -199,65 +215,91 @@ fp8_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constan
 
     // This block's slots of a tile.
     auto rows_of = [&](const Tile &t, int r) { return CTAS == 1 ? t.n : max(0, min(128, t.n - 128 * r)); };
-    auto stopped = [&]() { return __any_sync(0xFFFFFFFFu, *abort != 0); };
 
     if (warp < kFirstSumWarp) {
         if constexpr (AT == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kCopyRegs));
         if (warp == 0) {
             // ---- weights, and x rows in order ----
-            const bool one = tc::elect_one();
+            const uint32_t one = tc::elect_one(), first_one = CTAS == 1 || rank == 0 ? one : 0;
+            const uint32_t full_at = CTAS == 2 ? tc::in_block(full0, 0) : full0;
             Ring ring;
-            for (uint32_t tile = unit; tile < total && !stopped(); tile += units) {
+            bool ok = true;
+#pragma unroll 1
+            for (uint32_t tile = unit; ok && tile < total; tile += units) {
                 const Tile t = mm::find_tile(p, first, slot0, tile, lane);
-                if (one) {
-                    uint32_t bytes = CTAS * kWeights * kTileBytes;
-                    const int n = rows_of(t, pair_rank);
-                    if (!ROWS)
-                        for (int r = 0; r < CTAS; ++r) bytes += (uint32_t)((rows_of(t, r) + 31) >> 5) * 4096u;
-                    const int col = t.rt * p.tile_step + pair_rank * p.second, row = (int)t.slot + 128 * pair_rank;
-                    for (int k = k0; k < k1; ++k, ring.next(p.stages)) {
-                        if (!tc::bar_wait(empty0 + 8 * ring.s, ring.parity ^ 1u, abort)) break;
-                        const uint32_t base = ring0 + ring.s * p.stage_bytes;
-                        uint32_t bar = full0 + 8 * ring.s;
-                        if (CTAS == 1 || rank == 0) tc::bar_expect(bar, bytes);
-                        if (CTAS == 2) bar = tc::in_block(bar, 0);
+                uint32_t bytes = AT * kTileBytes;
+                const int n = rows_of(t, pair_rank);
+                if (!ROWS)
+                    for (int r = 0; r < CTAS; ++r) bytes += (uint32_t)((rows_of(t, r) + 31) >> 5) * 4096u;
+                const int col = t.rt * p.tile_step + pair_rank * 64, row = (int)t.slot + 128 * pair_rank;
+#pragma unroll 1
+                for (int k = k0; k < k1; ++k, ring.next(p.stages)) {
+                    ok = __all_sync(0xFFFFFFFFu, tc::bar_wait_ready(empty0 + 8 * ring.s, ring.parity ^ 1u, abort));
+                    if (!ok) break;
+                    const uint32_t base = ring0 + ring.s * p.stage_bytes, bar = full_at + 8 * ring.s;
+                    tc::bar_expect_if(first_one, full0 + 8 * ring.s, bytes);
 #pragma unroll
-                        for (int b = 0; b < kWeights; ++b) {
-                            const int c = col + b * p.second;
-                            tc::tma_load_3d_n<CTAS>(base + (1 + b) * kTileBytes, &wmap, p.transposed ? c : k * 128, p.transposed ? k * 128 : c, t.e, bar);
-                        }
-                        if (!ROWS)
-                            for (int c = 0; c < n; c += 32) tc::tma_load_2d_n<CTAS>(base + c * 128u, &xmap, k * 128, row + c, bar);
+                    for (int a = 0; a < AT; ++a) {
+                        const int c = col + a * p.second;
+                        tc::tma_load_3d_if<CTAS>(one, base + kTileBytes + a * kPart, &wmap, p.transposed ? c : k * 128, p.transposed ? k * 128 : c, t.e, bar);
+                    }
+                    if (!ROWS) {
+#pragma unroll
+                        for (int c = 0; c < 128; c += 32)
+                            if (c < n) tc::tma_load_2d_if<CTAS>(one, base + c * 128u, &xmap, k * 128, row + c, bar);
                     }
                 }
-                __syncwarp();
             }
         } else if (warp == 1) {
             // ---- matrix instructions ----
+            const uint32_t one = tc::elect_one();
             if (rank == 0 || CTAS == 1) {
-                if (tc::elect_one()) {
-                    // D in 32 bits, E4M3 operands, B's order, N / 8, M / 16
-                    const uint32_t idesc = (1u << 4) | (p.transposed ? 1u << 16 : 0) | ((uint32_t)(AT * 128 / 8) << 17) | ((uint32_t)(CTAS * 128 / 16) << 24);
-                    const uint32_t b_step = p.transposed ? 4096 >> 4 : 32 >> 4;
-                    Ring ring, sets;
-                    bool ok = true;
-                    for (uint32_t tile = unit; ok && tile < total; tile += units) {
-                        for (int k = k0; k < k1; ++k, ring.next(p.stages), sets.next(kSets)) {
-                            ok = tc::bar_wait<CTAS == 2>(acce0 + 8 * sets.s, sets.parity ^ 1u, abort) &&
-                                 tc::bar_wait<CTAS == 2>(full0 + 8 * ring.s, ring.parity, abort);
+                // D in 32 bits, E4M3 operands, B's order, N / 8, M / 16
+                const uint32_t idesc = (1u << 4) | (p.transposed ? 1u << 16 : 0) | ((128u / 8) << 17) | ((uint32_t)(CTAS * 128 / 16) << 24);
+                const uint32_t b_step = (p.transposed ? 4096 / CTAS : 32) >> 4;
+                const uint64_t a0 = tc::desc_sw128(ring0);
+                const uint64_t b0 = !p.transposed ? tc::desc_sw128(ring0 + kTileBytes) : CTAS == 1 ? tc::desc_across(ring0 + kTileBytes) : tc::desc_across64(ring0 + kTileBytes);
+                const uint32_t a_hi = (uint32_t)(a0 >> 32), b_hi = (uint32_t)(b0 >> 32), stage = p.stage_bytes >> 4;
+                Ring ring;
+                uint32_t count = 0;      // steps of the depth so far: AT sets each
+                bool ok = true;
+#pragma unroll 1
+                for (uint32_t tile = unit; ok && tile < total; tile += units) {
+#pragma unroll 1
+                    for (int k = k0; k < k1; ++k, ++count, ring.next(p.stages)) {
+                        const uint32_t set = AT == 2 ? (count & 1) * 2 : count & 3, parity = ~(count >> (AT == 2 ? 1 : 2)) & 1;
+                        const uint32_t acce = acce0 + 8 * set, accf = accf0 + 8 * set, full = full0 + 8 * ring.s;
+                        bool here = tc::bar_try(full, ring.parity);
+                        here &= tc::bar_try(acce, parity);
+                        if (AT == 2) here &= tc::bar_try(acce + 8, parity);
+                        if (!__all_sync(0xFFFFFFFFu, here)) {
+                            ok = __all_sync(0xFFFFFFFFu, tc::bar_wait_on(full, ring.parity, abort) && tc::bar_wait_on(acce, parity, abort) &&
+                                                             (AT == 1 || tc::bar_wait_on(acce + 8, parity, abort)));
                             if (!ok) break;
-                            tc::fence_after();
-                            const uint32_t base = ring0 + ring.s * p.stage_bytes, d = tmem + sets.s * (AT * 128);
-                            const uint64_t ad = tc::desc_sw128(base);
-                            const uint64_t bd = p.transposed ? tc::desc_across(base + kTileBytes) : tc::desc_sw128(base + kTileBytes);
-#pragma unroll
-                            for (uint32_t i = 0; i < 4; ++i) tc::mma_f8<CTAS>(d, ad + 2 * i, bd + b_step * i, idesc, i != 0);
-                            tc::commit_n<CTAS>(empty0 + 8 * ring.s);
-                            tc::commit_n<CTAS>(accf0 + 8 * sets.s);
                         }
+                        tc::fence_after();
+                        if (ROWS) tc::fence_async_proxy();       // x came by ordinary copies
+                        const uint32_t at = ring.s * stage, a_lo = (uint32_t)a0 + at, b_lo = (uint32_t)b0 + at, d = tmem + set * 128;
+                        tc::mma_f8_128<CTAS>(one, d, a_lo, a_hi, b_lo, b_hi, b_step, idesc, accf);
+                        if (AT == 2) tc::mma_f8_128<CTAS>(one, d + 128, a_lo, a_hi, b_lo + (kPart >> 4), b_hi, b_step, idesc, accf + 8);
+                        tc::commit_if<CTAS>(one, empty0 + 8 * ring.s);
                     }
                 }
-                __syncwarp();
+            } else if constexpr (ROWS) {
+                // the other block: x copies that have landed, handed on
+                const uint32_t to = tc::in_block(full0, 0);
+                Ring ring;
+                bool ok = true;
+#pragma unroll 1
+                for (uint32_t tile = unit; ok && tile < total; tile += units) {
+#pragma unroll 1
+                    for (int k = k0; k < k1; ++k, ring.next(p.stages)) {
+                        ok = __all_sync(0xFFFFFFFFu, tc::bar_wait_ready(full0 + 8 * ring.s, ring.parity, abort));
+                        if (!ok) break;
+                        tc::fence_async_proxy();
+                        tc::bar_arrive_if<true>(to + 8 * ring.s, one);
+                    }
+                }
             }
         } else if constexpr (ROWS) {
             // ---- x rows through the index ----
@@ -265,20 +307,9 @@ fp8_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constan
             const uint32_t row0 = (uint32_t)(4 * g + sub);
             // row r's 16-byte piece q lies at piece q ^ (r % 8) of its 128 bytes
             const uint32_t dst0 = row0 * 128u + (((uint32_t)piece ^ (row0 & 7)) << 4);
-            const int lag = p.stages >= 3 ? 2 : 1;       // copies of that many stages are under way
-            int pending = 0;
-            Ring ring, done;
-            auto signal = [&]() {
-                tc::fence_async_proxy();
-                __syncwarp();
-                if (lane == 0) {
-                    if (CTAS == 1) tc::bar_arrive(full0 + 8 * done.s);
-                    else tc::bar_arrive_cluster(tc::in_block(full0 + 8 * done.s, 0));
-                }
-                done.next(p.stages);
-                --pending;
-            };
+            Ring ring;
             bool ok = true;
+#pragma unroll 1
             for (uint32_t tile = unit; ok && tile < total; tile += units) {
                 const Tile t = mm::find_tile(p, first, slot0, tile, lane);
                 const int n = rows_of(t, pair_rank), copies = (n + 7) >> 3;
@@ -291,8 +322,9 @@ fp8_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constan
                         r[j] = v < 0 || v >= p.x_rows ? 0 : v;
                     }
                 }
+#pragma unroll 1
                 for (int k = k0; k < k1; ++k, ring.next(p.stages)) {
-                    ok = __all_sync(0xFFFFFFFFu, tc::bar_wait(empty0 + 8 * ring.s, ring.parity ^ 1u, abort));
+                    ok = __all_sync(0xFFFFFFFFu, tc::bar_wait_ready(empty0 + 8 * ring.s, ring.parity ^ 1u, abort));
                     if (!ok) break;
                     const uint32_t dst = ring0 + ring.s * p.stage_bytes + dst0;
                     const int at = k * 128 + 16 * piece;
@@ -301,300 +333,345 @@ fp8_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constan
 #pragma unroll
                     for (int j = 0; j < 16; ++j)
                         if (j < copies) tc::cp_async16(dst + j * 1024u, src + r[j] * p.x_code_stride, live);
-                    tc::cp_async_group();
-                    if (++pending > lag) {
-                        if (lag == 2) tc::cp_async_wait<2>();
-                        else tc::cp_async_wait<1>();
-                        signal();
-                    }
+                    tc::cp_async_arrive(full0 + 8 * ring.s);
                 }
             }
-            tc::cp_async_wait<0>();
-            while (pending > 0) signal();
         }
     } else {
         // ---- partial sums and the epilogue ----
         if constexpr (AT == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSumRegs));
-        const int w = warp & 3, half = (warp - kFirstSumWarp) >> 2;        // lanes 32 w .., columns 64 half .. of each weight block
-        float *buf = region + (warp - kFirstSumWarp) * 32 * kTurnStride;
-        const uint32_t mine = tmem + ((uint32_t)(32 * w) << 16) + 64 * half;
-        const int part = lane & 3, sub = lane >> 2;                         // after the turn: 8 columns of a row
+        // Two weight blocks: warps 4-7 sum the first one's columns and warps 8-11
+        // the second one's; one: 64 columns each.  Warps w and w + 4 have the
+        // same 32 rows.
+        const int w = warp & 3, half = (warp - kFirstSumWarp) >> 2;
+        constexpr int kCols = AT * 64;                                      // this warp's columns
+        const int col0 = kCols * half;
+        float *buf = region + (warp - kFirstSumWarp) * 32 * 32;
+        const uint32_t lanes = tmem + ((uint32_t)(32 * w) << 16);
         // What a tile's first sums need, fetched before the last tile's epilogue.
+        // (Little, and the tile itself in shared memory: sums and partial sums
+        // take 192 registers.)
         struct Head {
-            Tile t;
-            const float4 *xs;
-            const float *ws[AT];
-            float4 x0, x1;               // the row's scales of 4 blocks, and of the next 4
-            float w0[AT], w1[AT];        // a lane's block of 32, and of the next 32
+            int n;                       // this warp's rows, if any
+            int32_t row, ws;             // x's row, and where the weight block's scales begin
+            float2 x0, x1;               // the row's scales of 2 blocks, and of the next 2
+            float w0, w1;                // a lane's block of 32, and of the next 32
         };
+        const int groups = (p.blocks + 1) >> 1;
+        auto x_scales = [&](const Head &h, int g) {
+            return __ldg(reinterpret_cast<const float2 *>(p.x_scales + h.row * p.x_scale_stride) + min(g, groups - 1));
+        };
+        auto w_scales = [&](const Head &h, int k) { return __ldg(p.w_scales + h.ws + min(k + lane, p.blocks - 1) * p.ws_b); };
         bool bad_row = false;
         auto open = [&](Head &h, uint32_t tile) {
-            h.t.n = 0;
             if (tile >= total) return;
-            h.t = mm::find_tile(p, first, slot0, tile, lane);
+            const Tile t = mm::find_tile(p, first, slot0, tile, lane);
+            if (lane == 0) sh.tile[warp - kFirstSumWarp] = t;
             const int r = 128 * pair_rank + 32 * w + lane;
-            const int64_t slot = (int64_t)h.t.slot + min(r, h.t.n - 1);
-            int64_t row = slot;
+            const int64_t slot = (int64_t)t.slot + min(r, t.n - 1);
+            h.n = rows_of(t, pair_rank) - 32 * w;
+            h.row = (int32_t)slot;
             if constexpr (ROWS) {
-                row = __ldg(p.rows + slot);
-                const bool out = row < 0 || row >= p.x_rows;
+                h.row = __ldg(p.rows + slot);
+                const bool out = h.row < 0 || h.row >= p.x_rows;
                 bad_row |= out;
-                if (out) row = 0;
+                if (out) h.row = 0;
             }
-            h.xs = reinterpret_cast<const float4 *>(p.x_scales + row * p.x_scale_stride);
-            const int last = (p.blocks - 1) >> 2;
-            h.x0 = __ldg(h.xs + (k0 >> 2));
-            h.x1 = __ldg(h.xs + min((k0 >> 2) + 1, last));
-#pragma unroll
-            for (int a = 0; a < AT; ++a) {
-                const int f = min((h.t.rt * p.tile_step + a * p.second) >> 7, p.f_blocks - 1);
-                h.ws[a] = p.w_scales + h.t.e * p.ws_expert + (int64_t)f * p.ws_f;
-                h.w0[a] = __ldg(h.ws[a] + (int64_t)min(k0 + lane, p.blocks - 1) * p.ws_b);
-                h.w1[a] = k1 - k0 > 32 ? __ldg(h.ws[a] + (int64_t)min(k0 + 32 + lane, p.blocks - 1) * p.ws_b) : 0.f;
-            }
+            const int f = min((t.rt * p.tile_step + (AT == 2 ? half * p.second : 0)) >> 7, p.f_blocks - 1);
+            h.ws = t.e * p.ws_expert + f * p.ws_f;
+            h.x0 = x_scales(h, k0 >> 1);
+            h.x1 = x_scales(h, (k0 >> 1) + 1);
+            h.w0 = w_scales(h, k0);
+            h.w1 = w_scales(h, k0 + 32);
         };
-        Ring sets;
+        const uint32_t release0 = CTAS == 1 ? acce0 : tc::in_block(acce0, 0);
+        auto release = [&](uint32_t set) {
+            tc::fence_before();
+            __syncwarp();
+            tc::bar_arrive_if<CTAS == 2>(release0 + 8 * set, lane == 0);
+        };
+        uint32_t count = 0;              // partial sums so far
+        // where the partial sum with that number is: its set, and the parity of its round
+        auto set_of = [&](uint32_t i) { return AT == 2 ? (i & 1) * 2 + half : i & 3; };
         Head h;
         open(h, unit);
         bool ok = true;
+#pragma unroll 1
         for (uint32_t tile = unit, nth = 0; tile < total; tile += units, ++nth) {
-            const Tile t = h.t;
-            const int n = rows_of(t, pair_rank) - 32 * w;       // this warp's rows, if any
-            uint64_t sum[AT][32];
+            const int n = h.n;
+            float sum[kCols];
 #pragma unroll
-            for (int a = 0; a < AT; ++a)
-#pragma unroll
-                for (int i = 0; i < 32; ++i) sum[a][i] = 0;
-            const int groups = (p.blocks + 3) >> 2;
-            for (int k = k0; k < k1; ++k) {
-                ok = __all_sync(0xFFFFFFFFu, tc::bar_wait(accf0 + 8 * sets.s, sets.parity, abort));
+            for (int i = 0; i < kCols; ++i) sum[i] = 0.f;
+#pragma unroll 1
+            for (int k = k0; k < k1; ++k, ++count) {
+                const int i = (k - k0) & 31;
+                const uint32_t set = set_of(count);
+                const float factor = (k & 1 ? h.x0.y : h.x0.x) * __shfl_sync(0xFFFFFFFFu, h.w0, i);
+                ok = __all_sync(0xFFFFFFFFu, tc::bar_wait_here(accf0 + 8 * set, (count >> (AT == 2 ? 1 : 2)) & 1, abort));
                 if (!ok) break;
                 tc::fence_after();
+                const bool keep = k + 1 == k1 && !SPLIT;        // the whole sums go back there
                 if (n > 0) {
-                    const int q = k & 3, i = (k - k0) & 31;
-                    const float xs = q < 2 ? (q == 0 ? h.x0.x : h.x0.y) : (q == 2 ? h.x0.z : h.x0.w);
-                    uint64_t factor[AT];
+                    const uint32_t at = lanes + set * 128 + (AT == 2 ? 0 : col0);
 #pragma unroll
-                    for (int a = 0; a < AT; ++a) {
-                        const uint32_t f = __float_as_uint(xs * __shfl_sync(0xFFFFFFFFu, h.w0[a], i));
-                        factor[a] = tc::pack2(f, f);
-                    }
-                    if (q == 3) {
-                        h.x0 = h.x1;
-                        if ((k >> 2) + 2 < groups) h.x1 = __ldg(h.xs + (k >> 2) + 2);
-                    }
-                    if (i == 31) {
+                    for (int c = 0; c < kCols; c += 64) {
+                        uint32_t v[2][32];
+                        tc::tmem_load(at + c, v[0]);
+                        tc::tmem_load(at + c + 32, v[1]);
+                        tc::wait_ld();
+                        if (c + 64 == kCols && !keep) release(set);
 #pragma unroll
-                        for (int a = 0; a < AT; ++a) {
-                            h.w0[a] = h.w1[a];
-                            h.w1[a] = __ldg(h.ws[a] + (int64_t)min(k + 33 + lane, p.blocks - 1) * p.ws_b);
-                        }
+                        for (int j = 0; j < 64; ++j) tc::fma_after(sum[c + j], v[j >> 5][j & 31], factor);
                     }
-                    const uint32_t d = mine + sets.s * (AT * 128);
-                    uint32_t v[2][32];
-                    tc::tmem_load(d, v[0]);
-#pragma unroll
-                    for (int c = 0; c < 2 * AT; ++c) {
-                        tc::wait_ld(v[c & 1]);
-                        if (c + 1 < 2 * AT) tc::tmem_load(d + ((c + 1) >> 1) * 128 + ((c + 1) & 1) * 32, v[(c + 1) & 1]);
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) tc::fma2(sum[c >> 1][(c & 1) * 16 + j], tc::pack2(v[c & 1][2 * j], v[c & 1][2 * j + 1]), factor[c >> 1]);
-                    }
+                } else if (!keep) {
+                    release(set);
                 }
-                if (k + 1 < k1 || SPLIT) {
-                    tc::fence_before();
-                    __syncwarp();
-                    if (lane == 0) {
-                        if (CTAS == 1) tc::bar_arrive(acce0 + 8 * sets.s);
-                        else tc::bar_arrive_cluster(tc::in_block(acce0 + 8 * sets.s, 0));
-                    }
-                    sets.next(kSets);
+                if (k & 1) {
+                    h.x0 = h.x1;
+                    h.x1 = x_scales(h, (k >> 1) + 2);
+                }
+                if (i == 31) {
+                    h.w0 = h.w1;
+                    h.w1 = w_scales(h, k + 33);
                 }
             }
+            const Tile t = sh.tile[warp - kFirstSumWarp];
+            __syncwarp();                // read before the next one is written
             if (!ok) break;
             if constexpr (SPLIT) {
                 // a row's sums to the block that finishes it
                 const uint32_t share = ((uint32_t)t.n + split - 1) / split, r = (uint32_t)(32 * w + lane);
                 if (lane < n) {
                     const uint32_t to = r / share;
-                    const uint32_t at = tc::in_block(tc::smem_u32(region + ((rank * share + (r - to * share)) * AT) * 128 + 64 * half), to);
+                    const uint32_t at = tc::in_block(tc::smem_u32(region + (rank * share + (r - to * share)) * (AT * 128) + col0), to);
 #pragma unroll
-                    for (int a = 0; a < AT; ++a)
-#pragma unroll
-                        for (int j = 0; j < 32; j += 2) {
-                            uint32_t v[4];
-                            tc::unpack2(sum[a][j], v[0], v[1]);
-                            tc::unpack2(sum[a][j + 1], v[2], v[3]);
-                            tc::store_cluster4(at + a * 512u + j * 8u, v[0], v[1], v[2], v[3]);
-                        }
+                    for (int j = 0; j < kCols; j += 4) tc::store_cluster4(at + j * 4u, sum[j], sum[j + 1], sum[j + 2], sum[j + 3]);
                 }
                 break;
             }
             // The sums, back to where the last partial ones were.
-            const uint32_t d = mine + sets.s * (AT * 128);
+            const uint32_t set = set_of(count - 1), own = lanes + set * 128 + (AT == 2 ? 0 : col0);
             if (n > 0) {
 #pragma unroll
-                for (int a = 0; a < AT; ++a)
+                for (int c = 0; c < kCols / 16; ++c) {
+                    uint32_t v[16];
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        uint32_t v[16];
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) tc::unpack2(sum[a][c * 8 + j], v[2 * j], v[2 * j + 1]);
-                        tc::tmem_store(d + a * 128 + c * 16, v);
-                    }
+                    for (int j = 0; j < 16; ++j) v[j] = __float_as_uint(sum[c * 16 + j]);
+                    tc::tmem_store(own + c * 16, v);
+                }
                 tc::wait_st();
             }
             open(h, tile + units);
             if (n > 0) {
                 const int64_t slot = (int64_t)t.slot + 128 * pair_rank + 32 * w;
-                const int outs = p.gated ? 1 : AT, f_tile = t.rt * p.tile_step + 64 * half;
-                // 16 columns of y from f on, this lane's row: d's columns are c on
-                auto values = [&](float (&y)[16], int c, int f) {
+                const bool gated = AT == 2 && p.gated;
+                // this warp's columns of the output, and where their sums are (a gated product's: 64 of both blocks)
+                const int f0 = t.rt * p.tile_step + (gated ? 64 * half : col0), cols = gated ? 64 : kCols;
+                const uint32_t gate = gated ? lanes + (set & 2) * 128 + 64 * half : own, up = gate + 128;
+                if (gated) {
+                    tc::fence_before();
+                    tc::named_sync(1 + w, 64);
+                    tc::fence_after();
+                }
+                const bool live = lane < n;
+                const float rs = p.row_scale && live ? __ldg(p.row_scale + slot + lane) : 1.f;
+                // 16 columns of this lane's row from column c of f0 on: act(p) and the row's weight
+                auto values = [&](float (&y)[16], int c) {
                     uint32_t v[16];
-                    tc::tmem_load(d + c, v);
-                    if (AT == 2 && p.gated) {
+                    tc::tmem_load(gate + c, v);
+                    if (gated) {
                         uint32_t u[16];
-                        tc::tmem_load(d + 128 + c, u);
+                        tc::tmem_load(up + c, u);
                         tc::wait_ld(v);
                         tc::wait_ld(u);
-                        float up[16];
+                        float b[16];
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) y[i] = __uint_as_float(v[i]), up[i] = __uint_as_float(u[i]);
+                        for (int i = 0; i < 16; ++i) y[i] = __uint_as_float(v[i]), b[i] = __uint_as_float(u[i]);
                         if (p.bias) {
-                            add_bias8(p, y, t.e, f);
-                            add_bias8(p, y + 8, t.e, f + 8);
-                            add_bias8(p, up, t.e, p.F + f);
-                            add_bias8(p, up + 8, t.e, p.F + f + 8);
+                            add_bias8(p, y, t.e, f0 + c);
+                            add_bias8(p, y + 8, t.e, f0 + c + 8);
+                            add_bias8(p, b, t.e, p.F + f0 + c);
+                            add_bias8(p, b + 8, t.e, p.F + f0 + c + 8);
                         }
+                        activate16(y, p.act);
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) y[i] = activate(y[i], p.act) * up[i];
+                        for (int i = 0; i < 16; ++i) y[i] *= b[i];
                     } else {
                         tc::wait_ld(v);
 #pragma unroll
                         for (int i = 0; i < 16; ++i) y[i] = __uint_as_float(v[i]);
                         if (p.bias) {
-                            add_bias8(p, y, t.e, f);
-                            add_bias8(p, y + 8, t.e, f + 8);
+                            add_bias8(p, y, t.e, f0 + c);
+                            add_bias8(p, y + 8, t.e, f0 + c + 8);
                         }
-                        if (p.act != CSF_ACT_NONE) {
+                        activate16(y, p.act);
+                    }
+                    if (p.row_scale) {
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) y[i] = activate(y[i], p.act);
-                        }
+                        for (int i = 0; i < 16; ++i) y[i] *= rs;
                     }
                 };
-                if constexpr (!QUANT) {
+                // A warp's piece lies as 32 rows of 128 bytes, row r's 16-byte
+                // part q at q ^ (r % 8): written a row a lane and read 4 or 8
+                // rows at a time, both without bank conflicts.
+                auto piece_at = [&](int r, int q) { return buf + r * 32 + ((q ^ (r & 7)) << 2); };
+                if constexpr (MODE == kHalves) {
+                    // 64 columns at a time, rounded before the turn
 #pragma unroll 1
-                    for (int piece = 0; piece < 2 * outs; ++piece) {
-                        const int c = (piece >> 1) * 128 + (piece & 1) * 32, f = f_tile + c;
-                        if (f >= p.F) continue;
+                    for (int c0 = 0; c0 < cols && f0 + c0 < p.F; c0 += 64) {
 #pragma unroll 1
-                        for (int q = 0; q < 32; q += 16) {
+                        for (int q = 0; q < 4; ++q) {
                             float y[16];
-                            values(y, c + q, f + q);
+                            values(y, c0 + 16 * q);
+                            uint32_t o[8];
 #pragma unroll
-                            for (int i = 0; i < 16; i += 4)
-                                *reinterpret_cast<float4 *>(buf + lane * kTurnStride + q + i) = make_float4(y[i], y[i + 1], y[i + 2], y[i + 3]);
+                            for (int i = 0; i < 8; ++i) {
+                                if (p.out_dtype == CSF_BF16) {
+                                    const __nv_bfloat162 b = __floats2bfloat162_rn(y[2 * i], y[2 * i + 1]);
+                                    memcpy(&o[i], &b, 4);
+                                } else {
+                                    const __half2 b = __floats2half2_rn(y[2 * i], y[2 * i + 1]);
+                                    memcpy(&o[i], &b, 4);
+                                }
+                            }
+                            *reinterpret_cast<uint4 *>(piece_at(lane, 2 * q)) = make_uint4(o[0], o[1], o[2], o[3]);
+                            *reinterpret_cast<uint4 *>(piece_at(lane, 2 * q + 1)) = make_uint4(o[4], o[5], o[6], o[7]);
                         }
                         __syncwarp();
+                        const int q = lane & 7, f = f0 + c0 + 8 * q;
+                        char *out = p.out + (slot + (lane >> 3)) * p.out_stride;
+                        if (p.out_wide && f + 8 <= p.F) {
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                const int r = 4 * i + (lane >> 3);
+                                if (r < n) *reinterpret_cast<uint4 *>(out + 4 * i * p.out_stride + 2 * f) = *reinterpret_cast<const uint4 *>(piece_at(r, q));
+                            }
+                        } else {
+                            for (int r = lane >> 3; r < min(n, 32); r += 4) {
+                                elem::Raw o;
+                                o.a = *reinterpret_cast<const uint4 *>(piece_at(r, q));
+                                o.b = o.a;
+                                elem::store_few(p.out + (slot + r) * p.out_stride, f, p.F, o, p.out_dtype);
+                            }
+                        }
+                        __syncwarp();
+                    }
+                } else if constexpr (MODE == kPlain) {
+                    // 32 columns as floats; a residual's piece is fetched while the sums of the last are turned
+                    const int part = lane & 3, sub = lane >> 2;
+                    const int res_bytes = p.residual_dtype == CSF_F32 ? 4 : 2;
+                    const char *res = static_cast<const char *>(p.residual) + (slot + sub) * p.residual_stride * res_bytes;
+                    elem::Raw next[4] = {};       // (defined on every path: else it is held through the products, too)
+                    auto fetch = [&](int c0) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (8 * i + sub < n) next[i] = elem::load_apart(res + 8 * i * p.residual_stride * res_bytes, f0 + c0 + 8 * part, p.F, p.residual_dtype, p.residual_wide);
+                    };
+                    if (p.residual) fetch(0);
+#pragma unroll 1
+                    for (int c0 = 0; c0 < cols && f0 + c0 < p.F; c0 += 32) {
+                        elem::Raw now[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) now[i] = next[i];
+                        if (p.residual && c0 + 32 < cols) fetch(c0 + 32);
+#pragma unroll 1
+                        for (int q = 0; q < 2; ++q) {
+                            float y[16];
+                            values(y, c0 + 16 * q);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                *reinterpret_cast<float4 *>(piece_at(lane, 4 * q + i)) = make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
+                        }
+                        __syncwarp();
+                        const int f = f0 + c0 + 8 * part;
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             const int r = 8 * i + sub;
-                            const float4 *from = reinterpret_cast<const float4 *>(buf + r * kTurnStride + 8 * part);
-                            const float4 lo = from[0], hi = from[1];
+                            const float4 lo = *reinterpret_cast<const float4 *>(piece_at(r, 2 * part)), hi = *reinterpret_cast<const float4 *>(piece_at(r, 2 * part + 1));
                             float y[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-                            finish8<false>(p, y, slot + r, f + 8 * part, r < n);
+                            if (r >= n || f >= p.F) continue;
+                            if (p.residual) {
+                                float b[8];
+                                elem::to_floats(b, now[i], p.residual_dtype);
+#pragma unroll
+                                for (int j = 0; j < 8; ++j) y[j] += b[j];
+                            }
+                            elem::store_apart(p.out + (slot + r) * p.out_stride, f, p.F, elem::from_floats(y, p.out_dtype), p.out_dtype, p.out_wide);
                         }
                         __syncwarp();
                     }
                 } else {
-                    // The largest magnitude of a block of 128 columns comes from
-                    // both warps of these rows.
                     const int padded = (p.F + 31) & ~31;
-                    const bool live = lane < n;
-                    const float rs = p.row_scale && live ? __ldg(p.row_scale + slot + lane) : 1.f;
                     const char *res = p.residual ? static_cast<const char *>(p.residual) + (slot + (live ? lane : 0)) * p.residual_stride * (p.residual_dtype == CSF_F32 ? 4 : 2) : nullptr;
-                    float (&amax)[2][2][128] = sh.amax[nth & 1];
-                    for (int a = 0; a < outs; ++a) {
-                        uint32_t m = 0;
+                    uint32_t m = 0;
 #pragma unroll 1
-                        for (int q = 0; q < 64; q += 16) {
-                            const int c = a * 128 + q, f = f_tile + c;
-                            if (f >= padded) break;
-                            float y[16];
-                            values(y, c, f);
-                            uint32_t v[16];
-                            if (p.row_scale) {
+                    for (int c = 0; c < cols && f0 + c < padded; c += 16) {
+                        float y[16];
+                        values(y, c);
+                        if (res) {
+                            float b[8];
 #pragma unroll
-                                for (int i = 0; i < 16; ++i) y[i] *= rs;
+                            for (int g = 0; g < 16; g += 8) {
+                                elem::to_floats(b, elem::load_apart(res, f0 + c + g, p.F, p.residual_dtype, p.residual_wide), p.residual_dtype);
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) y[g + i] += b[i];
                             }
-                            if (res) {
-                                float b[8];
-#pragma unroll
-                                for (int g = 0; g < 16; g += 8) {
-                                    elem::to_floats(b, elem::load(res, f + g, p.F, p.residual_dtype, p.residual_wide), p.residual_dtype);
-#pragma unroll
-                                    for (int i = 0; i < 8; ++i) y[g + i] += b[i];
-                                }
-                            }
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) {
-                                v[i] = f + i < p.F ? __float_as_uint(y[i]) : 0;
-                                m = max(m, v[i] & 0x7FFFFFFFu);
-                            }
-                            tc::tmem_store(d + c, v);
                         }
-                        amax[half][a][32 * w + lane] = __uint_as_float(m);
+                        uint32_t v[16];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            v[i] = f0 + c + i < p.F ? __float_as_uint(y[i]) : 0;
+                            m = max(m, v[i] & 0x7FFFFFFFu);
+                        }
+                        tc::tmem_store(gate + c, v);
                     }
                     tc::wait_st();
-                    tc::named_sync(1 + w, 64);
-                    for (int a = 0; a < outs; ++a) {
-                        const int f = f_tile + a * 128;
-                        if (f >= padded) break;
-                        const uint32_t m = max(__float_as_uint(amax[0][a][32 * w + lane]), __float_as_uint(amax[1][a][32 * w + lane]));
-                        const float scale = quant::fp8_scale(m), up = quant::fp8_up(scale);
-                        const quant::Whole whole = quant::fp8_whole(scale * up);
+                    if (cols == 64) {
+                        // the largest magnitude of a block of 128 columns comes from both warps of these rows
+                        float (&amax)[2][128] = sh.amax[nth & 1];
+                        amax[half][32 * w + lane] = __uint_as_float(m);
+                        tc::named_sync(1 + w, 64);
+                        m = max(m, __float_as_uint(amax[half ^ 1][32 * w + lane]));
+                    }
+                    const float scale = quant::fp8_scale(m), scale_up = quant::fp8_up(scale);
+                    const quant::Whole whole = quant::fp8_whole(scale * scale_up);
+                    const int part = lane & 3, sub = lane >> 2;
 #pragma unroll 1
-                        for (int q = 0; q < 64; q += 16) {
-                            if (f + q >= padded) break;
+                    for (int c0 = 0; c0 < cols && f0 + c0 < padded; c0 += 64) {
+#pragma unroll 1
+                        for (int q = 0; q < 4 && f0 + c0 + 16 * q < padded; ++q) {
                             uint32_t v[16];
-                            tc::tmem_load(d + a * 128 + q, v);
+                            tc::tmem_load(gate + c0 + 16 * q, v);
                             tc::wait_ld(v);
                             uint32_t o[4];
 #pragma unroll
                             for (int i = 0; i < 4; ++i) {
                                 float y[4];
 #pragma unroll
-                                for (int j = 0; j < 4; ++j) y[j] = quant::over(__uint_as_float(v[4 * i + j]) * up, whole);
+                                for (int j = 0; j < 4; ++j) y[j] = quant::over(__uint_as_float(v[4 * i + j]) * scale_up, whole);
                                 o[i] = quant::e4m3x2(y[0], y[1]) | quant::e4m3x2(y[2], y[3]) << 16;
                             }
-                            *reinterpret_cast<uint4 *>(buf + lane * 20 + (q >> 2)) = make_uint4(o[0], o[1], o[2], o[3]);
+                            *reinterpret_cast<uint4 *>(piece_at(lane, q)) = make_uint4(o[0], o[1], o[2], o[3]);
                         }
                         __syncwarp();
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
-                            const int r = 8 * i + sub;
-                            if (r < n && f + 16 * part < padded)
-                                *reinterpret_cast<uint4 *>(p.out + (slot + r) * p.out_stride + f + 16 * part) =
-                                    *reinterpret_cast<const uint4 *>(buf + r * 20 + 4 * part);
+                            const int r = 8 * i + sub, f = f0 + c0 + 16 * part;
+                            if (r < n && f < padded) *reinterpret_cast<uint4 *>(p.out + (slot + r) * p.out_stride + f) = *reinterpret_cast<const uint4 *>(piece_at(r, part));
                         }
                         __syncwarp();
-                        if (half == 0 && live) {
-                            float *scales = reinterpret_cast<float *>(p.out_scales + (slot + lane) * p.out_scale_stride);
-                            const int b = f >> 7, n_blocks = (p.F + 127) >> 7;
-                            scales[b] = scale;
-                            if (b + 1 == n_blocks)       // clear the scale row's padding
-                                for (int i = n_blocks; i & 3; ++i) scales[i] = 0.f;
-                        }
+                    }
+                    if ((f0 & 127) == 0 && f0 < padded && live) {
+                        float *scales = reinterpret_cast<float *>(p.out_scales + (slot + lane) * p.out_scale_stride);
+                        const int b = f0 >> 7, n_blocks = (p.F + 127) >> 7;
+                        scales[b] = scale;
+                        if (b + 1 == n_blocks)       // clear the scale row's padding
+                            for (int i = n_blocks; i & 3; ++i) scales[i] = 0.f;
                     }
                 }
+                if (gated) tc::named_sync(1 + w, 64);      // the other warp has read this one's block, too
             }
-            tc::fence_before();
-            __syncwarp();
-            if (lane == 0) {
-                if (CTAS == 1) tc::bar_arrive(acce0 + 8 * sets.s);
-                else tc::bar_arrive_cluster(tc::in_block(acce0 + 8 * sets.s, 0));
-            }
-            sets.next(kSets);
+            release(set);
         }
         if (bad_row && p.err) atomicOr(p.err, CSF_DEV_ERR_CORRUPT);
     }
@@ -639,7 +716,7 @@ fp8_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constan
                     y[0][i] = activate(y[0][i], p.act);
                     if (AT == 2) y[0][i] *= y[AT - 1][i];       // gated
                 }
-                finish8<QUANT>(p, y[0], (int64_t)t.slot + (int64_t)rank * share + r, f, live);
+                finish8<MODE == kQuant>(p, y[0], (int64_t)t.slot + (int64_t)rank * share + r, f, live);
             }
         }
     }
@@ -651,21 +728,28 @@ using Kernel = void (*)(CUtensorMap, CUtensorMap, Params);
 // A pair, one block of 128 or 256 columns, or those with the depth shared.
 enum Shape { kPair = 0, kOne = 1, kTwo = 2, kOneShared = 3, kTwoShared = 4 };
 
-template <bool ROWS, bool QUANT>
+template <bool ROWS, int MODE>
 Kernel pick(int shape) {
+    // where the depth is shared, what comes out is asked at run time
+    constexpr int kAny = MODE == kHalves ? kPlain : MODE;
     switch (shape) {
-        case kPair: return fp8_matmul_kernel<2, 2, ROWS, false, QUANT>;
-        case kOne: return fp8_matmul_kernel<1, 1, ROWS, false, QUANT>;
-        case kTwo: return fp8_matmul_kernel<1, 2, ROWS, false, QUANT>;
-        case kOneShared: return fp8_matmul_kernel<1, 1, ROWS, true, QUANT>;
-        default: return fp8_matmul_kernel<1, 2, ROWS, true, QUANT>;
+        case kPair: return fp8_matmul_kernel<2, 2, ROWS, false, MODE>;
+        case kOne: return fp8_matmul_kernel<1, 1, ROWS, false, MODE>;
+        case kTwo: return fp8_matmul_kernel<1, 2, ROWS, false, MODE>;
+        case kOneShared: return fp8_matmul_kernel<1, 1, ROWS, true, kAny>;
+        default: return fp8_matmul_kernel<1, 2, ROWS, true, kAny>;
     }
+}
+
+template <bool ROWS>
+Kernel pick_kernel(int shape, int mode) {
+    return mode == kHalves ? pick<ROWS, kHalves>(shape) : mode == kPlain ? pick<ROWS, kPlain>(shape) : pick<ROWS, kQuant>(shape);
 }
 
 // The kernel of a shape, one translation unit each for x rows in order and
 // through an index.
-Kernel rows_in_order(int shape, bool quant);
-Kernel rows_by_index(int shape, bool quant);
+Kernel rows_in_order(int shape, int mode);
+Kernel rows_by_index(int shape, int mode);
 
 }  // namespace f8
 }  // namespace csfk

@@ -4,7 +4,7 @@
 namespace csfk {
 namespace f8 {
 
-Kernel rows_by_index(int shape, bool quant) { return quant ? pick<true, true>(shape) : pick<true, false>(shape); }
+Kernel rows_by_index(int shape, int mode) { return pick_kernel<true>(shape, mode); }
 
 }  // namespace f8
 }  // namespace csfk

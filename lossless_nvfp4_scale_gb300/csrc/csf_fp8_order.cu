@@ -4,7 +4,7 @@
 namespace csfk {
 namespace f8 {
 
-Kernel rows_in_order(int shape, bool quant) { return quant ? pick<false, true>(shape) : pick<false, false>(shape); }
+Kernel rows_in_order(int shape, int mode) { return pick_kernel<false>(shape, mode); }
 
 }  // namespace f8
 }  // namespace csfk

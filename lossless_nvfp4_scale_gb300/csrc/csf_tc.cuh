@@ -94,6 +94,37 @@ __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile
     return false;
 }
 
+// The same with nothing but the barrier's answer in the way of a phase that
+// is there already: the loop above took 180 cycles then, in a warp alone on
+// its scheduler, and this takes 57.
+static __device__ __noinline__ bool bar_wait_on(uint32_t bar, uint32_t parity, volatile uint32_t *abort) {
+    return bar_wait(bar, parity, abort);
+}
+
+__device__ __forceinline__ bool bar_wait_ready(uint32_t bar, uint32_t parity, volatile uint32_t *abort) {
+    if (__builtin_expect(bar_try(bar, parity), 1)) return true;
+    return bar_wait_on(bar, parity, abort);
+}
+
+// The same without a call, for warps whose registers are full of sums: they
+// would be saved around it.
+__device__ __forceinline__ bool bar_wait_here(uint32_t bar, uint32_t parity, volatile uint32_t *abort) {
+    if (__builtin_expect(bar_try(bar, parity), 1)) return true;
+    uint64_t t0 = 0;
+#pragma unroll 1
+    for (uint32_t i = 0; !bar_try(bar, parity); ++i) {
+        if ((i & 63) != 63) continue;
+        if (*abort) return false;
+        const uint64_t t = timer_ns();
+        if (t0 == 0) t0 = t;
+        if (t - t0 > kWaitLimitNs) {
+            *abort = 1;
+            return false;
+        }
+    }
+    return true;
+}
+
 // ---- clusters -----------------------------------------------------------------------------------------------------
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -126,6 +157,26 @@ __device__ __forceinline__ uint32_t load_cluster(uint32_t src) {
 
 __device__ __forceinline__ void bar_arrive_cluster(uint32_t bar) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// The same without waiting until the whole cluster sees this thread's writes:
+// for what only tells that tensor memory or a stage has been read, or that
+// copies which were waited for have been handed to the asynchronous proxy.
+// (The waiting took a thousand cycles an arrival.)
+__device__ __forceinline__ void bar_arrive_remote(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// One lane's arrival, of this block's barrier or (REMOTE) at a cluster
+// address, without a branch that the warp would have to come together after.
+template <bool REMOTE>
+__device__ __forceinline__ void bar_arrive_if(uint32_t bar, bool is) {
+    if constexpr (REMOTE)
+        asm volatile("{\n .reg .pred p;\n setp.ne.u32 p, %1, 0;\n @p mbarrier.arrive.shared::cluster.b64 _, [%0];\n}" ::"r"(bar), "r"((uint32_t)is)
+                     : "memory");
+    else
+        asm volatile("{\n .reg .pred p;\n setp.ne.u32 p, %1, 0;\n @p mbarrier.arrive.shared::cta.b64 _, [%0];\n}" ::"r"(bar), "r"((uint32_t)is)
+                     : "memory");
 }
 
 // ---- copies -------------------------------------------------------------------------------------------------------
@@ -244,63 +295,110 @@ __device__ __forceinline__ void tmem_free_n(uint32_t addr, uint32_t cols) {
     }
 }
 
+// What follows is issued by the lane whose `one` is set, in code that the whole
+// warp runs: addresses and descriptors then stay in uniform registers, where
+// the instructions want them.  (In a branch of one lane's own each operand had
+// to be moved there: 160 cycles a step of the loop alone, before any wait.)
+
 // Into this block's memory; what has landed is counted by bar, which may be
 // the other block's (a cluster address).
 template <int CTAS>
-__device__ __forceinline__ void tma_load_3d_n(uint32_t dst, const void *map, int x, int y, int z, uint32_t bar) {
-    if constexpr (CTAS == 1) {
-        tma_load_3d(dst, map, x, y, z, bar);
-    } else {
+__device__ __forceinline__ void tma_load_3d_if(uint32_t one, uint32_t dst, const void *map, int x, int y, int z, uint32_t bar) {
+    if constexpr (CTAS == 1)
         asm volatile(
-            "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, "
-            "%4}], [%5];" ::"r"(dst),
-            "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
+            "{\n .reg .pred p;\n setp.ne.u32 p, %6, 0;\n"
+            " @p cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];\n}" ::"r"(dst),
+            "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar), "r"(one)
             : "memory");
-    }
+    else
+        asm volatile(
+            "{\n .reg .pred p;\n setp.ne.u32 p, %6, 0;\n"
+            " @p cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, "
+            "%4}], [%5];\n}" ::"r"(dst),
+            "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar), "r"(one)
+            : "memory");
 }
 
 template <int CTAS>
-__device__ __forceinline__ void tma_load_2d_n(uint32_t dst, const void *map, int x, int y, uint32_t bar) {
-    if constexpr (CTAS == 1) {
-        tma_load_2d(dst, map, x, y, bar);
-    } else {
+__device__ __forceinline__ void tma_load_2d_if(uint32_t one, uint32_t dst, const void *map, int x, int y, uint32_t bar) {
+    if constexpr (CTAS == 1)
         asm volatile(
-            "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], "
-            "[%4];" ::"r"(dst),
-            "l"(map), "r"(x), "r"(y), "r"(bar)
+            "{\n .reg .pred p;\n setp.ne.u32 p, %5, 0;\n"
+            " @p cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];\n}" ::"r"(dst),
+            "l"(map), "r"(x), "r"(y), "r"(bar), "r"(one)
             : "memory");
-    }
+    else
+        asm volatile(
+            "{\n .reg .pred p;\n setp.ne.u32 p, %5, 0;\n"
+            " @p cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], "
+            "[%4];\n}" ::"r"(dst),
+            "l"(map), "r"(x), "r"(y), "r"(bar), "r"(one)
+            : "memory");
+}
+
+__device__ __forceinline__ void bar_expect_if(uint32_t one, uint32_t bar, uint32_t bytes) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.u32 p, %2, 0;\n @p mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n}" ::"r"(bar),
+        "r"(bytes), "r"(one)
+        : "memory");
 }
 
 // One arrival on bar (of each block of a pair) once every tcgen05 operation
 // this thread issued so far is done.
 template <int CTAS>
-__device__ __forceinline__ void commit_n(uint32_t bar) {
-    if constexpr (CTAS == 1) {
-        commit(bar);
-    } else {
-        asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
-                     "h"((uint16_t)3)
-                     : "memory");
-    }
-}
-
-// D[128 CTAS x N] (+)= A * B^T with E4M3 operands, K = 32.  A pair has 128
-// rows of A and N / 2 of B in each block's memory.
-template <int CTAS>
-__device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+__device__ __forceinline__ void commit_if(uint32_t one, uint32_t bar) {
     if constexpr (CTAS == 1)
         asm volatile(
-            "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
-            " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}" ::"r"(d),
-            "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+            "{\n .reg .pred p;\n setp.ne.u32 p, %1, 0;\n"
+            " @p tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}" ::"r"(bar),
+            "r"(one)
             : "memory");
     else
         asm volatile(
-            "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
-            " tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n}" ::"r"(d),
-            "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+            "{\n .reg .pred p;\n setp.ne.u32 p, %2, 0;\n"
+            " @p tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n}" ::"r"(bar),
+            "h"((uint16_t)3), "r"(one)
             : "memory");
+}
+
+// D[128 CTAS x N] = A * B^T with E4M3 operands, K = 128 in four steps, and an
+// arrival on bar when they are done.  A pair has 128 rows of A and N / 2 of B
+// in each block's memory.  Descriptors come as their halves, of which the low
+// ones advance; all in one piece, since each instruction that the loop around
+// it takes waits for its turn among the summing warps'.
+template <int CTAS>
+__device__ __forceinline__ void mma_f8_128(uint32_t one, uint32_t d, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo, uint32_t b_hi,
+                                           uint32_t b_step, uint32_t idesc, uint32_t bar) {
+    if constexpr (CTAS == 1)
+        asm volatile(
+                "{\n .reg .pred p, t, f;\n .reg .b32 x;\n .reg .b64 ad, bd;\n setp.ne.u32 p, %8, 0;\n setp.eq.u32 t, %8, %8;\n setp.ne.u32 f, %8, %8;\n"
+                " add.u32 x, %1, 0;\n mov.b64 ad, {x, %2};\n mad.lo.u32 x, %5, 0, %3;\n mov.b64 bd, {x, %4};\n"
+                " @p tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], ad, bd, %6, f;\n"
+                " add.u32 x, %1, 2;\n mov.b64 ad, {x, %2};\n mad.lo.u32 x, %5, 1, %3;\n mov.b64 bd, {x, %4};\n"
+                " @p tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], ad, bd, %6, t;\n"
+                " add.u32 x, %1, 4;\n mov.b64 ad, {x, %2};\n mad.lo.u32 x, %5, 2, %3;\n mov.b64 bd, {x, %4};\n"
+                " @p tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], ad, bd, %6, t;\n"
+                " add.u32 x, %1, 6;\n mov.b64 ad, {x, %2};\n mad.lo.u32 x, %5, 3, %3;\n mov.b64 bd, {x, %4};\n"
+                " @p tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], ad, bd, %6, t;\n"
+                " @p tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%7];\n"
+                "}" ::"r"(d),
+                "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(b_step), "r"(idesc), "r"(bar), "r"(one)
+                : "memory");
+    else
+        asm volatile(
+                "{\n .reg .pred p, t, f;\n .reg .b32 x;\n .reg .b64 ad, bd;\n setp.ne.u32 p, %8, 0;\n setp.eq.u32 t, %8, %8;\n setp.ne.u32 f, %8, %8;\n"
+                " add.u32 x, %1, 0;\n mov.b64 ad, {x, %2};\n mad.lo.u32 x, %5, 0, %3;\n mov.b64 bd, {x, %4};\n"
+                " @p tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], ad, bd, %6, f;\n"
+                " add.u32 x, %1, 2;\n mov.b64 ad, {x, %2};\n mad.lo.u32 x, %5, 1, %3;\n mov.b64 bd, {x, %4};\n"
+                " @p tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], ad, bd, %6, t;\n"
+                " add.u32 x, %1, 4;\n mov.b64 ad, {x, %2};\n mad.lo.u32 x, %5, 2, %3;\n mov.b64 bd, {x, %4};\n"
+                " @p tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], ad, bd, %6, t;\n"
+                " add.u32 x, %1, 6;\n mov.b64 ad, {x, %2};\n mad.lo.u32 x, %5, 3, %3;\n mov.b64 bd, {x, %4};\n"
+                " @p tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], ad, bd, %6, t;\n"
+                " @p tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%7], %9;\n"
+                "}" ::"r"(d),
+                "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(b_step), "r"(idesc), "r"(bar), "r"(one), "h"((uint16_t)3)
+                : "memory");
 }
 
 // Descriptor of 128 elements of 8 bits a row and rows along the summed index
@@ -311,16 +409,24 @@ __device__ __forceinline__ uint64_t desc_across(uint32_t addr) {
            (2ull << 61);
 }
 
-// 32 or 16 columns of this warp's lanes, as they are; wait_ld on them makes
-// what uses them come after.
+// The same with 64 elements a row (64-byte swizzle).
+__device__ __forceinline__ uint64_t desc_across64(uint32_t addr) {
+    return (uint64_t)((addr & 0x3FFFFu) >> 4) | ((uint64_t)(8192 >> 4) << 16) | ((uint64_t)(512 >> 4) << 32) | (1ull << 46) |
+           (4ull << 61);
+}
+
+// Columns of this warp's lanes, as they are; wait_ld on them makes what uses
+// them come after.
 __device__ __forceinline__ void tmem_load(uint32_t taddr, uint32_t (&r)[32]) {
     asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {"
+        "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, "
+        "%22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]),
-          "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]),
-          "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]),
+          "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]),
+          "=r"(r[30]), "=r"(r[31])
         : "r"(taddr));
 }
 
@@ -363,19 +469,10 @@ __device__ __forceinline__ void tmem_store(uint32_t taddr, const uint32_t (&r)[1
 
 __device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// Two floats a lane: d += a * b, each rounded once.
-__device__ __forceinline__ void fma2(uint64_t &d, uint64_t a, uint64_t b) {
-    asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(d) : "l"(a), "l"(b));
-}
-
-__device__ __forceinline__ uint64_t pack2(uint32_t lo, uint32_t hi) {
-    uint64_t v;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "r"(lo), "r"(hi));
-    return v;
-}
-
-__device__ __forceinline__ void unpack2(uint64_t v, uint32_t &lo, uint32_t &hi) {
-    asm("mov.b64 {%0, %1}, %2;" : "=r"(lo), "=r"(hi) : "l"(v));
+// d += a * b, rounded once.  (Volatile: what comes out of tensor memory is used
+// after the wait for it, in the order written here.)
+__device__ __forceinline__ void fma_after(float &d, uint32_t a, float b) {
+    asm volatile("fma.rn.f32 %0, %1, %2, %0;" : "+f"(d) : "f"(__uint_as_float(a)), "f"(b));
 }
 
 // A named barrier of `threads` threads.
@@ -390,8 +487,8 @@ __device__ __forceinline__ void cp_async_wait() {
 
 __device__ __forceinline__ void cp_async_group() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 
-__device__ __forceinline__ void store_cluster4(uint32_t dst, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-    asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+__device__ __forceinline__ void store_cluster4(uint32_t dst, float a, float b, float c, float d) {
+    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "f"(a), "f"(b), "f"(c), "f"(d) : "memory");
 }
 
 // 8 columns of this warp's 32 lanes.
