@@ -110,7 +110,7 @@ extern "C" csf_status csf_fp8_matmul(const csf_fp8_matmul_args *a, void *stream)
         p.nt = shape == kPair ? 256 : shape >= kOneShared ? kSplitSlots : 128;
         p.stage_bytes = kTileBytes * (shape == kTwo || shape == kTwoShared ? 3 : 2);
         const int64_t region = shape >= kOneShared ? (int64_t)kSplitSlots * 512 * (shape == kTwoShared ? 2 : 1) : kTurnBytes;
-        const int64_t fixed = 1024 + region + 8 * ((int64_t)E + 1) + 16, held = (int64_t)round_up(sizeof(Shared), 1024);
+        const int64_t fixed = 1024 + region + 8 * ((int64_t)E + 1) + 16, held = (int64_t)round_up(sizeof(Shared) + kFactorSteps * 512 * (wide ? 2 : 1), 1024);
         p.stages = (int32_t)std::min<int64_t>(kMaxStages, (kSmemLimit - held - fixed) / p.stage_bytes);
         return (int64_t)fixed + p.stages * (int64_t)p.stage_bytes;
     };
@@ -150,13 +150,12 @@ extern "C" csf_status csf_fp8_matmul(const csf_fp8_matmul_args *a, void *stream)
     }
     const int mode = !a->out ? kQuant : a->residual || a->out_dtype == CSF_F32 ? kPlain : kHalves;
     Kernel k = a->rows ? rows_by_index(shape, mode) : rows_in_order(shape, mode);
-    // the register split waits for what the block was launched with
-    const int regs = shape == kOne || shape == kOneShared ? 0 : kLaunchRegs;
-    if (!allow_smem(reinterpret_cast<const void *>(k), kSmemLimit, regs)) return CSF_ERR_CUDA;
+    // the register split waits for what the block was launched with (given out in eights)
+    if (!allow_smem(reinterpret_cast<const void *>(k), kSmemLimit, launch_regs(a->rows) - 7)) return CSF_ERR_CUDA;
     const unsigned per = shape == kPair ? 2 : (unsigned)p.split;
     cudaLaunchConfig_t config = {};
     config.gridDim = dim3((unsigned)(p.split > 1 ? most_tiles * p.split : per * std::min<int64_t>(sms / per, most_tiles)));
-    config.blockDim = dim3(f8::kThreads);
+    config.blockDim = dim3((unsigned)threads_of(a->rows));
     config.dynamicSmemBytes = (size_t)smem;
     config.stream = static_cast<cudaStream_t>(stream);
     cudaLaunchAttribute cluster;

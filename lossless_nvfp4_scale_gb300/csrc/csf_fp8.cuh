@@ -19,9 +19,10 @@
 //
 //   warp 0      weights, and x rows where slots are rows (TMA, 128-byte swizzle)
 //   warp 1      matrix instructions (the first block's of a pair)
-//   warps 2, 3  x rows through the index: 16-byte asynchronous copies,
-//               swizzled as TMA would
-//   warps 4-11  partial sums, then the epilogue: the sums go back to tensor
+//   warps 2, 3  the factors, a step's 128 rows at a time, into shared memory
+//   warps 4-7   x rows through an index, where there is one: 16-byte
+//               asynchronous copies, swizzled as TMA would
+//   the last 8  partial sums, then the epilogue: the sums go back to tensor
 //               memory, whose columns a rolled loop can take one by one
 #pragma once
 
@@ -39,8 +40,10 @@ namespace f8 {
 using mm::Ring;
 using mm::Tile;
 
-constexpr int kThreads = 384;
-constexpr int kSumWarps = 8, kFirstSumWarp = 4;
+constexpr int kSumWarps = 8;
+constexpr int kFactorWarps = 2, kFirstFactorWarp = 2;      // 64 rows each
+constexpr int kXWarps = 4, kFirstXWarp = 4;                // 32 rows each, where an index is followed
+__host__ __device__ constexpr int threads_of(bool rows) { return rows ? 512 : 384; }
 constexpr int kMaxStages = 8;
 constexpr int kSmemLimit = 227 * 1024;
 constexpr int kMaxExperts = 8192;
@@ -50,9 +53,17 @@ constexpr uint32_t kTileBytes = 128 * 128;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTurnBytes = kSumWarps * 32 * 128;      // a piece of 32 rows of 128 bytes each
 // Registers of the warps that copy and of those that sum, where a thread holds
-// 128 sums: together what the block was launched with, 384 x 168.
-constexpr int kCopyRegs = 56, kSumRegs = 224, kLaunchRegs = 168;
-static_assert(128 * kCopyRegs + 256 * kSumRegs == kThreads * kLaunchRegs, "registers of a block");
+// 128 sums and takes out 64 partial ones: together what the block was launched
+// with.
+__host__ __device__ constexpr int launch_regs(bool rows) { return rows ? 128 : 168; }
+template <bool ROWS> constexpr int kCopyRegs = ROWS ? 48 : 56;
+template <bool ROWS> constexpr int kSumRegs = ROWS ? 208 : 224;
+static_assert(256 * kCopyRegs<true> + 256 * kSumRegs<true> == 512 * launch_regs(true), "registers of a block");
+static_assert(128 * kCopyRegs<false> + 256 * kSumRegs<false> == 384 * launch_regs(false), "registers of a block");
+// Steps whose factors are held: those of the ring's stages, and of partial
+// sums that are formed (4 steps at most) or taken out.
+constexpr int kFactorSteps = 16;
+static_assert(kFactorSteps >= kMaxStages + 5, "factors are written when their stage is free");
 
 struct Params {
     const uint8_t *x_codes, *x_scales;
@@ -89,8 +100,7 @@ struct Params {
 
 struct Shared {
     uint64_t full[kMaxStages], empty[kMaxStages], acc_full[4], acc_empty[4];
-    uint32_t tmem, abort, warp_sum[kThreads / 32];
-    Tile tile[kSumWarps];        // the summing warps' next
+    uint32_t tmem, abort, warp_sum[16];
     float amax[2][2][128];       // by tile, half and row
 };
 
@@ -161,11 +171,13 @@ enum Mode { kHalves = 0, kPlain = 1, kQuant = 2 };
 // s reads row rows[s] of x, else row s.  SPLIT: clusters share a tile's depth.
 // MODE: what comes out.
 template <int CTAS, int AT, bool ROWS, bool SPLIT, int MODE>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(threads_of(ROWS), 1)
 fp8_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap, const __grid_constant__ Params p) {
     static_assert(CTAS == 1 || (AT == 2 && !SPLIT), "a pair has 256 columns and all of the depth");
     extern __shared__ __align__(1024) uint8_t dyn[];
     __shared__ Shared sh;
+    __shared__ float factors[kFactorSteps][AT][128];        // a row's scale times the weight block's
+    constexpr int kThreads = threads_of(ROWS), kFirstSumWarp = ROWS ? 8 : 4;
     constexpr int kSets = (int)kTmemCols / 128;             // partial sums of 128 columns under way
     constexpr uint32_t kPart = kTileBytes / CTAS;           // bytes of a weight block that this block of threads holds
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -182,8 +194,9 @@ fp8_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constan
 
     if (tid == 0) {
         for (int i = 0; i < p.stages; ++i) {
-            // the weights; the copying lanes; the copies of a pair's other block (which counts only its lanes)
-            tc::bar_init(full0 + 8 * i, !ROWS ? 1 : CTAS == 1 ? 65 : pair_rank == 0 ? 66 : 64);
+            // the weights; the factors of both blocks; the copying lanes and a pair's other block's copies (that
+            // block counts only its lanes)
+            tc::bar_init(full0 + 8 * i, pair_rank == 1 ? 32 * kXWarps : 1 + kFactorWarps * CTAS + (ROWS ? 32 * kXWarps + CTAS - 1 : 0));
             tc::bar_init(empty0 + 8 * i, 1);
         }
         for (int i = 0; i < kSets; ++i) {
@@ -217,7 +230,7 @@ fp8_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constan
     auto rows_of = [&](const Tile &t, int r) { return CTAS == 1 ? t.n : max(0, min(128, t.n - 128 * r)); };
 
     if (warp < kFirstSumWarp) {
-        if constexpr (AT == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kCopyRegs));
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kCopyRegs<ROWS>));
         if (warp == 0) {
             // ---- weights, and x rows in order ----
             const uint32_t one = tc::elect_one(), first_one = CTAS == 1 || rank == 0 ? one : 0;
@@ -301,9 +314,79 @@ fp8_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constan
                     }
                 }
             }
+        } else if (warp < kFirstXWarp) {
+            // ---- factors ----
+            // Two rows a lane; a row's scales of 4 blocks and of the next 4, and of each weight block a lane's block
+            // of 32 and of the next 32.
+            const int r0 = 64 * (warp - kFirstFactorWarp) + lane, groups = (p.blocks + 3) >> 2;
+            const uint32_t full_at = CTAS == 2 ? tc::in_block(full0, 0) : full0;
+            uint32_t count = 0;
+            bool ok = true, bad_row = false;
+            Ring ring;
+#pragma unroll 1
+            for (uint32_t tile = unit; ok && tile < total; tile += units) {
+                const Tile t = mm::find_tile(p, first, slot0, tile, lane);
+                const float4 *xs[2];
+                float4 x0[2], x1[2];
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const int64_t slot = (int64_t)t.slot + min(128 * pair_rank + r0 + 32 * j, t.n - 1);
+                    int64_t row = slot;
+                    if constexpr (ROWS) {
+                        row = __ldg(p.rows + slot);
+                        const bool out = row < 0 || row >= p.x_rows;
+                        bad_row |= out;
+                        if (out) row = 0;
+                    }
+                    xs[j] = reinterpret_cast<const float4 *>(p.x_scales + row * p.x_scale_stride);
+                    x0[j] = __ldg(xs[j] + (k0 >> 2));
+                    x1[j] = __ldg(xs[j] + min((k0 >> 2) + 1, groups - 1));
+                }
+                const float *ws[AT];
+                float w0[AT], w1[AT];
+#pragma unroll
+                for (int a = 0; a < AT; ++a) {
+                    const int f = min((t.rt * p.tile_step + a * p.second) >> 7, p.f_blocks - 1);
+                    ws[a] = p.w_scales + t.e * p.ws_expert + (int64_t)f * p.ws_f;
+                    w0[a] = __ldg(ws[a] + (int64_t)min(k0 + lane, p.blocks - 1) * p.ws_b);
+                    w1[a] = __ldg(ws[a] + (int64_t)min(k0 + 32 + lane, p.blocks - 1) * p.ws_b);
+                }
+#pragma unroll 1
+                for (int k = k0; k < k1; ++k, ++count, ring.next(p.stages)) {
+                    const int q = k & 3, i = (k - k0) & 31;
+                    float *at = &factors[count % kFactorSteps][0][r0];
+                    ok = __all_sync(0xFFFFFFFFu, tc::bar_wait_ready(empty0 + 8 * ring.s, ring.parity ^ 1u, abort));
+                    if (!ok) break;
+#pragma unroll
+                    for (int a = 0; a < AT; ++a) {
+                        const float w = __shfl_sync(0xFFFFFFFFu, w0[a], i);
+#pragma unroll
+                        for (int j = 0; j < 2; ++j)
+                            at[a * 128 + 32 * j] = w * (q < 2 ? (q == 0 ? x0[j].x : x0[j].y) : (q == 2 ? x0[j].z : x0[j].w));
+                    }
+                    __threadfence_block();
+                    __syncwarp();
+                    tc::bar_arrive_if<CTAS == 2>(full_at + 8 * ring.s, lane == 0);
+                    if (q == 3) {
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            x0[j] = x1[j];
+                            x1[j] = __ldg(xs[j] + min((k >> 2) + 2, groups - 1));
+                        }
+                    }
+                    if (i == 31) {
+#pragma unroll
+                        for (int a = 0; a < AT; ++a) {
+                            w0[a] = w1[a];
+                            w1[a] = __ldg(ws[a] + (int64_t)min(k + 33 + lane, p.blocks - 1) * p.ws_b);
+                        }
+                    }
+                }
+            }
+            if (bad_row && p.err) atomicOr(p.err, CSF_DEV_ERR_CORRUPT);
         } else if constexpr (ROWS) {
             // ---- x rows through the index ----
-            const int g = warp - 2, piece = lane & 7, sub = lane >> 3;      // 8 lanes a row, 4 rows a copy, every other 4 rows
+            const int g = warp - kFirstXWarp, piece = lane & 7, sub = lane >> 3;      // 8 lanes a row, 4 rows a copy, every fourth 4 rows
             const uint32_t row0 = (uint32_t)(4 * g + sub);
             // row r's 16-byte piece q lies at piece q ^ (r % 8) of its 128 bytes
             const uint32_t dst0 = row0 * 128u + (((uint32_t)piece ^ (row0 & 7)) << 4);
@@ -312,34 +395,36 @@ fp8_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constan
 #pragma unroll 1
             for (uint32_t tile = unit; ok && tile < total; tile += units) {
                 const Tile t = mm::find_tile(p, first, slot0, tile, lane);
-                const int n = rows_of(t, pair_rank), copies = (n + 7) >> 3;
-                int32_t r[16];
+                const int n = rows_of(t, pair_rank), copies = (n + 15) >> 4;
+                const uint8_t *src[8];
 #pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    r[j] = 0;
+                for (int j = 0; j < 8; ++j) {
+                    src[j] = p.x_codes;
                     if (j < copies) {
-                        const int32_t v = __ldg(p.rows + (int64_t)t.slot + 128 * pair_rank + min(8 * j + (int)row0, n - 1));
-                        r[j] = v < 0 || v >= p.x_rows ? 0 : v;
+                        const int32_t v = __ldg(p.rows + (int64_t)t.slot + 128 * pair_rank + min(16 * j + (int)row0, n - 1));
+                        src[j] += (v < 0 || v >= p.x_rows ? 0 : v) * p.x_code_stride;
                     }
+                    src[j] += k0 * 128 + 16 * piece;
                 }
+                int at = k0 * 128 + 16 * piece;
 #pragma unroll 1
-                for (int k = k0; k < k1; ++k, ring.next(p.stages)) {
+                for (int k = k0; k < k1; ++k, at += 128, ring.next(p.stages)) {
                     ok = __all_sync(0xFFFFFFFFu, tc::bar_wait_ready(empty0 + 8 * ring.s, ring.parity ^ 1u, abort));
                     if (!ok) break;
                     const uint32_t dst = ring0 + ring.s * p.stage_bytes + dst0;
-                    const int at = k * 128 + 16 * piece;
                     const bool live = at < p.depth;
-                    const uint8_t *src = p.x_codes + (live ? at : 0);
 #pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                        if (j < copies) tc::cp_async16(dst + j * 1024u, src + r[j] * p.x_code_stride, live);
+                    for (int j = 0; j < 8; ++j) {
+                        if (j < copies) tc::cp_async16(dst + j * 2048u, src[j], live);
+                        src[j] += 128;
+                    }
                     tc::cp_async_arrive(full0 + 8 * ring.s);
                 }
             }
         }
     } else {
         // ---- partial sums and the epilogue ----
-        if constexpr (AT == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSumRegs));
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSumRegs<ROWS>));
         // Two weight blocks: warps 4-7 sum the first one's columns and warps 8-11
         // the second one's; one: 64 columns each.  Warps w and w + 4 have the
         // same 32 rows.
@@ -348,42 +433,6 @@ fp8_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constan
         const int col0 = kCols * half;
         float *buf = region + (warp - kFirstSumWarp) * 32 * 32;
         const uint32_t lanes = tmem + ((uint32_t)(32 * w) << 16);
-        // What a tile's first sums need, fetched before the last tile's epilogue.
-        // (Little, and the tile itself in shared memory: sums and partial sums
-        // take 192 registers.)
-        struct Head {
-            int n;                       // this warp's rows, if any
-            int32_t row, ws;             // x's row, and where the weight block's scales begin
-            float2 x0, x1;               // the row's scales of 2 blocks, and of the next 2
-            float w0, w1;                // a lane's block of 32, and of the next 32
-        };
-        const int groups = (p.blocks + 1) >> 1;
-        auto x_scales = [&](const Head &h, int g) {
-            return __ldg(reinterpret_cast<const float2 *>(p.x_scales + h.row * p.x_scale_stride) + min(g, groups - 1));
-        };
-        auto w_scales = [&](const Head &h, int k) { return __ldg(p.w_scales + h.ws + min(k + lane, p.blocks - 1) * p.ws_b); };
-        bool bad_row = false;
-        auto open = [&](Head &h, uint32_t tile) {
-            if (tile >= total) return;
-            const Tile t = mm::find_tile(p, first, slot0, tile, lane);
-            if (lane == 0) sh.tile[warp - kFirstSumWarp] = t;
-            const int r = 128 * pair_rank + 32 * w + lane;
-            const int64_t slot = (int64_t)t.slot + min(r, t.n - 1);
-            h.n = rows_of(t, pair_rank) - 32 * w;
-            h.row = (int32_t)slot;
-            if constexpr (ROWS) {
-                h.row = __ldg(p.rows + slot);
-                const bool out = h.row < 0 || h.row >= p.x_rows;
-                bad_row |= out;
-                if (out) h.row = 0;
-            }
-            const int f = min((t.rt * p.tile_step + (AT == 2 ? half * p.second : 0)) >> 7, p.f_blocks - 1);
-            h.ws = t.e * p.ws_expert + f * p.ws_f;
-            h.x0 = x_scales(h, k0 >> 1);
-            h.x1 = x_scales(h, (k0 >> 1) + 1);
-            h.w0 = w_scales(h, k0);
-            h.w1 = w_scales(h, k0 + 32);
-        };
         const uint32_t release0 = CTAS == 1 ? acce0 : tc::in_block(acce0, 0);
         auto release = [&](uint32_t set) {
             tc::fence_before();
@@ -393,50 +442,45 @@ fp8_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constan
         uint32_t count = 0;              // partial sums so far
         // where the partial sum with that number is: its set, and the parity of its round
         auto set_of = [&](uint32_t i) { return AT == 2 ? (i & 1) * 2 + half : i & 3; };
-        Head h;
-        open(h, unit);
         bool ok = true;
 #pragma unroll 1
         for (uint32_t tile = unit, nth = 0; tile < total; tile += units, ++nth) {
-            const int n = h.n;
-            float sum[kCols];
+            const Tile t = mm::find_tile(p, first, slot0, tile, lane);
+            const int n = rows_of(t, pair_rank) - 32 * w;       // this warp's rows, if any
+            uint64_t sum[kCols / 2];     // two columns each
 #pragma unroll
-            for (int i = 0; i < kCols; ++i) sum[i] = 0.f;
+            for (int i = 0; i < kCols / 2; ++i) sum[i] = 0;
+            bool there = false;          // the next partial sums: asked for while these come out of tensor memory
 #pragma unroll 1
             for (int k = k0; k < k1; ++k, ++count) {
-                const int i = (k - k0) & 31;
-                const uint32_t set = set_of(count);
-                const float factor = (k & 1 ? h.x0.y : h.x0.x) * __shfl_sync(0xFFFFFFFFu, h.w0, i);
-                ok = __all_sync(0xFFFFFFFFu, tc::bar_wait_here(accf0 + 8 * set, (count >> (AT == 2 ? 1 : 2)) & 1, abort));
-                if (!ok) break;
+                const uint32_t set = set_of(count), next = set_of(count + 1);
+                constexpr int kRound = AT == 2 ? 1 : 2;
+                if (!__any_sync(0xFFFFFFFFu, there)) {
+                    ok = __all_sync(0xFFFFFFFFu, tc::bar_wait_here(accf0 + 8 * set, (count >> kRound) & 1, abort));
+                    if (!ok) break;
+                }
                 tc::fence_after();
-                const bool keep = k + 1 == k1 && !SPLIT;        // the whole sums go back there
+                const bool last = k + 1 == k1, keep = last && !SPLIT;        // the whole sums go back there
+                there = false;
                 if (n > 0) {
                     const uint32_t at = lanes + set * 128 + (AT == 2 ? 0 : col0);
+                    uint64_t factor = 0;
 #pragma unroll
                     for (int c = 0; c < kCols; c += 64) {
                         uint32_t v[2][32];
                         tc::tmem_load(at + c, v[0]);
                         tc::tmem_load(at + c + 32, v[1]);
+                        if (c == 0) factor = tc::twice(factors[count % kFactorSteps][AT == 2 ? half : 0][32 * w + lane]);
+                        if (c + 64 == kCols) there = tc::bar_try_if(accf0 + 8 * next, ((count + 1) >> kRound) & 1, lane == 0 && !last);
                         tc::wait_ld();
                         if (c + 64 == kCols && !keep) release(set);
 #pragma unroll
-                        for (int j = 0; j < 64; ++j) tc::fma_after(sum[c + j], v[j >> 5][j & 31], factor);
+                        for (int j = 0; j < 32; ++j) tc::fma2_after(sum[c / 2 + j], v[j >> 4][2 * (j & 15)], v[j >> 4][2 * (j & 15) + 1], factor);
                     }
                 } else if (!keep) {
                     release(set);
                 }
-                if (k & 1) {
-                    h.x0 = h.x1;
-                    h.x1 = x_scales(h, (k >> 1) + 2);
-                }
-                if (i == 31) {
-                    h.w0 = h.w1;
-                    h.w1 = w_scales(h, k + 33);
-                }
             }
-            const Tile t = sh.tile[warp - kFirstSumWarp];
-            __syncwarp();                // read before the next one is written
             if (!ok) break;
             if constexpr (SPLIT) {
                 // a row's sums to the block that finishes it
@@ -445,7 +489,12 @@ fp8_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constan
                     const uint32_t to = r / share;
                     const uint32_t at = tc::in_block(tc::smem_u32(region + (rank * share + (r - to * share)) * (AT * 128) + col0), to);
 #pragma unroll
-                    for (int j = 0; j < kCols; j += 4) tc::store_cluster4(at + j * 4u, sum[j], sum[j + 1], sum[j + 2], sum[j + 3]);
+                    for (int j = 0; j < kCols; j += 4) {
+                        float v[4];
+                        tc::halves(sum[j / 2], v[0], v[1]);
+                        tc::halves(sum[j / 2 + 1], v[2], v[3]);
+                        tc::store_cluster4(at + j * 4u, v[0], v[1], v[2], v[3]);
+                    }
                 }
                 break;
             }
@@ -456,12 +505,15 @@ fp8_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constan
                 for (int c = 0; c < kCols / 16; ++c) {
                     uint32_t v[16];
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) v[j] = __float_as_uint(sum[c * 16 + j]);
+                    for (int j = 0; j < 8; ++j) {
+                        float lo, hi;
+                        tc::halves(sum[c * 8 + j], lo, hi);
+                        v[2 * j] = __float_as_uint(lo), v[2 * j + 1] = __float_as_uint(hi);
+                    }
                     tc::tmem_store(own + c * 16, v);
                 }
                 tc::wait_st();
             }
-            open(h, tile + units);
             if (n > 0) {
                 const int64_t slot = (int64_t)t.slot + 128 * pair_rank + 32 * w;
                 const bool gated = AT == 2 && p.gated;
@@ -673,7 +725,6 @@ fp8_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constan
             }
             release(set);
         }
-        if (bad_row && p.err) atomicOr(p.err, CSF_DEV_ERR_CORRUPT);
     }
 
     tc::fence_before();      // the last tensor-memory reads, before they are freed

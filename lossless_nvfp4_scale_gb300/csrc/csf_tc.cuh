@@ -469,10 +469,32 @@ __device__ __forceinline__ void tmem_store(uint32_t taddr, const uint32_t (&r)[1
 
 __device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// d += a * b, rounded once.  (Volatile: what comes out of tensor memory is used
-// after the wait for it, in the order written here.)
-__device__ __forceinline__ void fma_after(float &d, uint32_t a, float b) {
-    asm volatile("fma.rn.f32 %0, %1, %2, %0;" : "+f"(d) : "f"(__uint_as_float(a)), "f"(b));
+// Two sums' d += a * b, each rounded once.  (Volatile: what comes out of tensor
+// memory is used after the wait for it, in the order written here.)
+__device__ __forceinline__ void fma2_after(uint64_t &d, uint32_t a_lo, uint32_t a_hi, uint64_t b) {
+    asm volatile("{\n .reg .b64 a;\n mov.b64 a, {%1, %2};\n fma.rn.f32x2 %0, a, %3, %0;\n}" : "+l"(d) : "r"(a_lo), "r"(a_hi), "l"(b));
+}
+
+__device__ __forceinline__ uint64_t twice(float v) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %1};" : "=l"(r) : "f"(v));
+    return r;
+}
+
+__device__ __forceinline__ void halves(uint64_t v, float &lo, float &hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v)); }
+
+// Whether a phase is there, asked by one lane alone: the barriers answer the
+// lanes one after the other.
+__device__ __forceinline__ bool bar_try_if(uint32_t bar, uint32_t parity, bool is) {
+    uint32_t done;
+    asm volatile(
+        "{\n .reg .pred p, q;\n setp.ne.u32 q, %3, 0;\n setp.ne.u32 p, %3, %3;\n"
+        " @q mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+        " selp.u32 %0, 1, 0, p;\n}"
+        : "=r"(done)
+        : "r"(bar), "r"(parity), "r"((uint32_t)is)
+        : "memory");
+    return done != 0;
 }
 
 // A named barrier of `threads` threads.
