@@ -109,15 +109,15 @@ __device__ __forceinline__ float activate(float v, int act) {
     return act == CSF_ACT_RELU && v < 0.f ? 0.f : v;
 }
 
-__device__ __forceinline__ void activate16(float (&y)[16], int act) {
+__device__ __forceinline__ void activate32(float (&y)[32], int act) {
     if (act == CSF_ACT_NONE) return;
     if (act == CSF_ACT_RELU) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) y[i] = y[i] < 0.f ? 0.f : y[i];
+        for (int i = 0; i < 32; ++i) y[i] = y[i] < 0.f ? 0.f : y[i];
     } else {
         const bool gelu = act == CSF_ACT_GELU_TANH;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) y[i] = mm::smooth(y[i], gelu);
+        for (int i = 0; i < 32; ++i) y[i] = mm::smooth(y[i], gelu);
     }
 }
 
@@ -284,17 +284,22 @@ fp8_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constan
                         const uint32_t acce = acce0 + 8 * set, accf = accf0 + 8 * set, full = full0 + 8 * ring.s;
                         bool here = tc::bar_try(full, ring.parity);
                         here &= tc::bar_try(acce, parity);
-                        if (AT == 2) here &= tc::bar_try(acce + 8, parity);
                         if (!__all_sync(0xFFFFFFFFu, here)) {
-                            ok = __all_sync(0xFFFFFFFFu, tc::bar_wait_on(full, ring.parity, abort) && tc::bar_wait_on(acce, parity, abort) &&
-                                                             (AT == 1 || tc::bar_wait_on(acce + 8, parity, abort)));
+                            ok = __all_sync(0xFFFFFFFFu, tc::bar_wait_on(full, ring.parity, abort) && tc::bar_wait_on(acce, parity, abort));
                             if (!ok) break;
                         }
                         tc::fence_after();
                         if (ROWS) tc::fence_async_proxy();       // x came by ordinary copies
                         const uint32_t at = ring.s * stage, a_lo = (uint32_t)a0 + at, b_lo = (uint32_t)b0 + at, d = tmem + set * 128;
                         tc::mma_f8_128<CTAS>(one, d, a_lo, a_hi, b_lo, b_hi, b_step, idesc, accf);
-                        if (AT == 2) tc::mma_f8_128<CTAS>(one, d + 128, a_lo, a_hi, b_lo + (kPart >> 4), b_hi, b_step, idesc, accf + 8);
+                        if constexpr (AT == 2) {
+                            if (!__all_sync(0xFFFFFFFFu, tc::bar_try(acce + 8, parity))) {
+                                ok = __all_sync(0xFFFFFFFFu, tc::bar_wait_on(acce + 8, parity, abort));
+                                if (!ok) break;
+                            }
+                            tc::fence_after();
+                            tc::mma_f8_128<CTAS>(one, d + 128, a_lo, a_hi, b_lo + (kPart >> 4), b_hi, b_step, idesc, accf + 8);
+                        }
                         tc::commit_if<CTAS>(one, empty0 + 8 * ring.s);
                     }
                 }
@@ -527,40 +532,40 @@ fp8_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constan
                 }
                 const bool live = lane < n;
                 const float rs = p.row_scale && live ? __ldg(p.row_scale + slot + lane) : 1.f;
-                // 16 columns of this lane's row from column c of f0 on: act(p) and the row's weight
-                auto values = [&](float (&y)[16], int c) {
-                    uint32_t v[16];
+                // 32 columns of this lane's row from column c of f0 on: act(p) and the row's weight
+                auto values = [&](float (&y)[32], int c) {
+                    uint32_t v[32];
                     tc::tmem_load(gate + c, v);
                     if (gated) {
-                        uint32_t u[16];
+                        uint32_t u[32];
                         tc::tmem_load(up + c, u);
                         tc::wait_ld(v);
                         tc::wait_ld(u);
-                        float b[16];
+                        float b[32];
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) y[i] = __uint_as_float(v[i]), b[i] = __uint_as_float(u[i]);
+                        for (int i = 0; i < 32; ++i) y[i] = __uint_as_float(v[i]), b[i] = __uint_as_float(u[i]);
                         if (p.bias) {
-                            add_bias8(p, y, t.e, f0 + c);
-                            add_bias8(p, y + 8, t.e, f0 + c + 8);
-                            add_bias8(p, b, t.e, p.F + f0 + c);
-                            add_bias8(p, b + 8, t.e, p.F + f0 + c + 8);
-                        }
-                        activate16(y, p.act);
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) y[i] *= b[i];
+                            for (int i = 0; i < 32; i += 8) add_bias8(p, y + i, t.e, f0 + c + i);
+#pragma unroll
+                            for (int i = 0; i < 32; i += 8) add_bias8(p, b + i, t.e, p.F + f0 + c + i);
+                        }
+                        activate32(y, p.act);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) y[i] *= b[i];
                     } else {
                         tc::wait_ld(v);
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) y[i] = __uint_as_float(v[i]);
+                        for (int i = 0; i < 32; ++i) y[i] = __uint_as_float(v[i]);
                         if (p.bias) {
-                            add_bias8(p, y, t.e, f0 + c);
-                            add_bias8(p, y + 8, t.e, f0 + c + 8);
+#pragma unroll
+                            for (int i = 0; i < 32; i += 8) add_bias8(p, y + i, t.e, f0 + c + i);
                         }
-                        activate16(y, p.act);
+                        activate32(y, p.act);
                     }
                     if (p.row_scale) {
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) y[i] *= rs;
+                        for (int i = 0; i < 32; ++i) y[i] *= rs;
                     }
                 };
                 // A warp's piece lies as 32 rows of 128 bytes, row r's 16-byte
@@ -572,12 +577,12 @@ fp8_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constan
 #pragma unroll 1
                     for (int c0 = 0; c0 < cols && f0 + c0 < p.F; c0 += 64) {
 #pragma unroll 1
-                        for (int q = 0; q < 4; ++q) {
-                            float y[16];
-                            values(y, c0 + 16 * q);
-                            uint32_t o[8];
+                        for (int q = 0; q < 8; q += 4) {
+                            float y[32];
+                            values(y, c0 + 8 * q);
+                            uint32_t o[16];
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) {
+                            for (int i = 0; i < 16; ++i) {
                                 if (p.out_dtype == CSF_BF16) {
                                     const __nv_bfloat162 b = __floats2bfloat162_rn(y[2 * i], y[2 * i + 1]);
                                     memcpy(&o[i], &b, 4);
@@ -586,8 +591,8 @@ fp8_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constan
                                     memcpy(&o[i], &b, 4);
                                 }
                             }
-                            *reinterpret_cast<uint4 *>(piece_at(lane, 2 * q)) = make_uint4(o[0], o[1], o[2], o[3]);
-                            *reinterpret_cast<uint4 *>(piece_at(lane, 2 * q + 1)) = make_uint4(o[4], o[5], o[6], o[7]);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4 *>(piece_at(lane, q + i)) = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
                         }
                         __syncwarp();
                         const int q = lane & 7, f = f0 + c0 + 8 * q;
@@ -626,13 +631,12 @@ fp8_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constan
 #pragma unroll
                         for (int i = 0; i < 4; ++i) now[i] = next[i];
                         if (p.residual && c0 + 32 < cols) fetch(c0 + 32);
-#pragma unroll 1
-                        for (int q = 0; q < 2; ++q) {
-                            float y[16];
-                            values(y, c0 + 16 * q);
+                        {
+                            float y[32];
+                            values(y, c0);
 #pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                *reinterpret_cast<float4 *>(piece_at(lane, 4 * q + i)) = make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
+                            for (int i = 0; i < 8; ++i)
+                                *reinterpret_cast<float4 *>(piece_at(lane, i)) = make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
                         }
                         __syncwarp();
                         const int f = f0 + c0 + 8 * part;
@@ -657,25 +661,28 @@ fp8_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constan
                     const char *res = p.residual ? static_cast<const char *>(p.residual) + (slot + (live ? lane : 0)) * p.residual_stride * (p.residual_dtype == CSF_F32 ? 4 : 2) : nullptr;
                     uint32_t m = 0;
 #pragma unroll 1
-                    for (int c = 0; c < cols && f0 + c < padded; c += 16) {
-                        float y[16];
+                    for (int c = 0; c < cols && f0 + c < padded; c += 32) {
+                        float y[32];
                         values(y, c);
                         if (res) {
                             float b[8];
 #pragma unroll
-                            for (int g = 0; g < 16; g += 8) {
+                            for (int g = 0; g < 32; g += 8) {
                                 elem::to_floats(b, elem::load_apart(res, f0 + c + g, p.F, p.residual_dtype, p.residual_wide), p.residual_dtype);
 #pragma unroll
                                 for (int i = 0; i < 8; ++i) y[g + i] += b[i];
                             }
                         }
-                        uint32_t v[16];
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            v[i] = f0 + c + i < p.F ? __float_as_uint(y[i]) : 0;
-                            m = max(m, v[i] & 0x7FFFFFFFu);
+                        for (int h = 0; h < 32; h += 16) {
+                            uint32_t v[16];
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) {
+                                v[i] = f0 + c + h + i < p.F ? __float_as_uint(y[h + i]) : 0;
+                                m = max(m, v[i] & 0x7FFFFFFFu);
+                            }
+                            tc::tmem_store(gate + c + h, v);
                         }
-                        tc::tmem_store(gate + c, v);
                     }
                     tc::wait_st();
                     if (cols == 64) {
@@ -691,19 +698,20 @@ fp8_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constan
 #pragma unroll 1
                     for (int c0 = 0; c0 < cols && f0 + c0 < padded; c0 += 64) {
 #pragma unroll 1
-                        for (int q = 0; q < 4 && f0 + c0 + 16 * q < padded; ++q) {
-                            uint32_t v[16];
+                        for (int q = 0; q < 4 && f0 + c0 + 16 * q < padded; q += 2) {
+                            uint32_t v[32];
                             tc::tmem_load(gate + c0 + 16 * q, v);
                             tc::wait_ld(v);
-                            uint32_t o[4];
+                            uint32_t o[8];
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) {
+                            for (int i = 0; i < 8; ++i) {
                                 float y[4];
 #pragma unroll
                                 for (int j = 0; j < 4; ++j) y[j] = quant::over(__uint_as_float(v[4 * i + j]) * scale_up, whole);
                                 o[i] = quant::e4m3x2(y[0], y[1]) | quant::e4m3x2(y[2], y[3]) << 16;
                             }
                             *reinterpret_cast<uint4 *>(piece_at(lane, q)) = make_uint4(o[0], o[1], o[2], o[3]);
+                            *reinterpret_cast<uint4 *>(piece_at(lane, q + 1)) = make_uint4(o[4], o[5], o[6], o[7]);
                         }
                         __syncwarp();
 #pragma unroll

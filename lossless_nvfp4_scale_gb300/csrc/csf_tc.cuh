@@ -172,7 +172,7 @@ __device__ __forceinline__ void bar_arrive_remote(uint32_t bar) {
 template <bool REMOTE>
 __device__ __forceinline__ void bar_arrive_if(uint32_t bar, bool is) {
     if constexpr (REMOTE)
-        asm volatile("{\n .reg .pred p;\n setp.ne.u32 p, %1, 0;\n @p mbarrier.arrive.shared::cluster.b64 _, [%0];\n}" ::"r"(bar), "r"((uint32_t)is)
+        asm volatile("{\n .reg .pred p;\n setp.ne.u32 p, %1, 0;\n @p mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];\n}" ::"r"(bar), "r"((uint32_t)is)
                      : "memory");
     else
         asm volatile("{\n .reg .pred p;\n setp.ne.u32 p, %1, 0;\n @p mbarrier.arrive.shared::cta.b64 _, [%0];\n}" ::"r"(bar), "r"((uint32_t)is)
