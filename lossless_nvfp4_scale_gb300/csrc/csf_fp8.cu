@@ -98,8 +98,20 @@ extern "C" csf_status csf_fp8_matmul(const csf_fp8_matmul_args *a, void *stream)
 
     const int sms = sm_count();
     const int64_t busy = std::min<int64_t>(E, a->slots);      // experts with slots, at most
-    const int64_t mean = a->slots / busy;
-    int shape = mean > 128 ? kPair : a->gated ? kTwo : kOne;
+    // A tile's shape by the rounds of tiles that it takes, each as long as
+    // measured with 5120 columns and depth (pair 1, two blocks 1.04, one 0.65).
+    // Experts' last slot tiles are half full on average.  512 / 8191 slots of a
+    // dense 5120 x 5120: one block 38 / 246 us, two 31 / 193, a pair 29 / 183;
+    // 128 experts of 256 slots, gated 4096 x 2048: two blocks 455, a pair 539.
+    auto tiles_of = [&](int nt, int step) {
+        const int64_t rows = E == 1 ? (a->slots + nt - 1) / nt : std::max(busy, busy / 2 + a->slots / nt);
+        return rows * ((p.F + step - 1) / step);
+    };
+    auto rounds = [&](int64_t t, int units) { return (double)((t + units - 1) / units); };
+    const int wide_step = a->gated ? 128 : 256, units = std::max(sms, 2);
+    const double pair = rounds(tiles_of(256, wide_step), units / 2), two = 1.04 * rounds(tiles_of(128, wide_step), units);
+    const double one = a->gated ? 2 * two : 0.65 * rounds(tiles_of(128, 128), units);
+    int shape = one <= two && one <= pair ? kOne : two <= pair ? kTwo : kPair;
     auto tiles = [&](int nt) { return (int64_t)p.row_tiles * (busy + a->slots / nt); };      // at most
     auto lay = [&]() {
         const bool wide = shape == kPair || shape == kTwo || shape == kTwoShared;
@@ -117,11 +129,15 @@ extern "C" csf_status csf_fp8_matmul(const csf_fp8_matmul_args *a, void *stream)
     p.split = 1;
     int64_t smem = lay();
     if (shape != kPair) {
-        // Few tiles: clusters share their depth.
-        const int64_t few = (int64_t)p.row_tiles * (busy + a->slots / kSplitSlots);
-        while (p.split < kMaxSplit && few * p.split * 2 <= sms && p.blocks >= 4 * p.split) p.split *= 2;
+        // Few tiles: clusters share their depth.  Clusters of half the SMs' blocks
+        // are placed at once, larger ones than pairs of more in turns: one slot of
+        // 2048 x 5120 takes 14.5 us in 16 clusters of 8 and 9.3 in 16 of 4, of
+        // 5120 x 5120 15.4 in 40 blocks and 12.3 in 40 pairs.
+        const int64_t slot_tiles = E == 1 ? (a->slots + kSplitSlots - 1) / kSplitSlots : busy + a->slots / kSplitSlots;
+        const int64_t few = (int64_t)((p.F + 127) / 128) * slot_tiles;
+        while (p.split < kMaxSplit && few * p.split * 2 <= (p.split == 1 ? sms : sms / 2) && p.blocks >= 4 * p.split) p.split *= 2;
         if (p.split > 1) {
-            shape = a->gated ? kTwoShared : kOneShared;
+            shape = a->gated ? kTwoShared : kOneShared;      // (fewer columns, so that more blocks have some)
             smem = lay();
         }
     }

@@ -452,6 +452,13 @@ fp8_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constan
         for (uint32_t tile = unit, nth = 0; tile < total; tile += units, ++nth) {
             const Tile t = mm::find_tile(p, first, slot0, tile, lane);
             const int n = rows_of(t, pair_rank) - 32 * w;       // this warp's rows, if any
+            if (MODE != kHalves && !SPLIT && p.residual && lane < n) {
+                // what the epilogue will add to this lane's row, into L2
+                const int bytes = p.residual_dtype == CSF_F32 ? 4 : 2, f = t.rt * p.tile_step + (p.gated ? 64 * half : col0);
+                const char *at = static_cast<const char *>(p.residual) + (((int64_t)t.slot + 128 * pair_rank + 32 * w + lane) * p.residual_stride + f) * bytes;
+                const int end = min(p.gated ? 64 : kCols, p.F - f) * bytes;
+                for (int b = 0; b < end; b += 32) tc::prefetch_l2(at + b);
+            }
             uint64_t sum[kCols / 2];     // two columns each
 #pragma unroll
             for (int i = 0; i < kCols / 2; ++i) sum[i] = 0;

@@ -104,6 +104,23 @@ __device__ __forceinline__ uint32_t block_amax(const float (&y)[8]) {
     return m;
 }
 
+// The same with 16 of this lane's columns: 8 lanes (FP8), 2 (MXFP8) or this
+// one (NVFP4).
+template <int KIND>
+__device__ __forceinline__ uint32_t block_amax16(const float (&y)[2][8]) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(y[h][i]) & 0x7FFFFFFFu);
+    if constexpr (KIND != CSF_ROWS_NVFP4) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+    if constexpr (KIND == CSF_ROWS_FP8) {
+        m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+        m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 4));
+    }
+    return m;
+}
+
 // 8 columns' codes (NVFP4: 4 bytes, in x) and their block's scale.
 struct Coded {
     uint2 codes;
@@ -158,6 +175,18 @@ __device__ __forceinline__ void put8(const Coded &q, uint8_t *codes, uint8_t *sc
     if (chunk % kLanes == 0) {
         if constexpr (KIND == CSF_ROWS_FP8) *reinterpret_cast<uint32_t *>(scales + (chunk >> 2)) = q.scale;
         else scales[chunk / kLanes] = (uint8_t)q.scale;
+    }
+}
+
+// Columns 16 * piece .. +15 of a row.
+template <int KIND>
+__device__ __forceinline__ void put16(const Coded (&q)[2], uint8_t *codes, uint8_t *scales, int piece) {
+    if constexpr (KIND == CSF_ROWS_NVFP4) *reinterpret_cast<uint2 *>(codes + piece * 8) = make_uint2(q[0].codes.x, q[1].codes.x);
+    else *reinterpret_cast<uint4 *>(codes + piece * 16) = make_uint4(q[0].codes.x, q[0].codes.y, q[1].codes.x, q[1].codes.y);
+    constexpr int kLanes = KIND == CSF_ROWS_FP8 ? 8 : KIND == CSF_ROWS_MXFP8 ? 2 : 1;
+    if (piece % kLanes == 0) {
+        if constexpr (KIND == CSF_ROWS_FP8) *reinterpret_cast<uint32_t *>(scales + (piece >> 1)) = q[0].scale;
+        else scales[piece / kLanes] = (uint8_t)q[0].scale;
     }
 }
 

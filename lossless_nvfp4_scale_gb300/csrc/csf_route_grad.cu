@@ -4,6 +4,8 @@
 // neighbouring experts, whose logits (for the softmax over all experts) stay
 // in registers.  The row is written once without the choices' own parts, and
 // then the choices' places once more: k of them, still in L2.  Bound by memory.
+#include <algorithm>
+
 #include "csf_elem.cuh"
 #include "csf_internal.cuh"
 #include "csf_layer.h"
@@ -12,6 +14,7 @@ namespace csfk {
 namespace {
 
 constexpr int kGradThreads = 256;
+constexpr int kGradBlocks = 8;       // blocks an SM, which take tokens in turn
 
 struct RouteGradParams {
     const char *logits;
@@ -29,93 +32,155 @@ __device__ __forceinline__ float at(const char *row, int e, int dtype) {
     return dtype == CSF_BF16 ? __uint_as_float((uint32_t)v << 16) : __half2float(__ushort_as_half(v));
 }
 
+// The largest of the lanes' values, by integers in the floats' order.  (A NaN
+// comes out somewhere; the sum shows it.)
+__device__ __forceinline__ float warp_max(float v) {
+    const int b = __float_as_int(v), m = __reduce_max_sync(0xFFFFFFFFu, b ^ (b >> 31 & 0x7FFFFFFF));
+    return __int_as_float(m ^ (m >> 31 & 0x7FFFFFFF));
+}
+
+// exp of a difference from the row's largest.  For 16-bit results, whose
+// rounding is 2^-12 at least, within |x| 2^-23 + 2^-22 of itself (and 0 below
+// 2^-126).
+template <int DTYPE>
+__device__ __forceinline__ float exp_below(float x) {
+    if constexpr (DTYPE == CSF_F32) return expf(x);
+    float e;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x * 1.4426950408889634f));
+    return e;
+}
+
 // CHUNKS: 256 experts each; 0: renormalised weights, whose gradient is 0 but
-// for the choices.
-template <int DTYPE, int CHUNKS>
+// for the choices.  WIDE: rows in whole 16-byte pieces, read and written.
+template <int DTYPE, int CHUNKS, bool WIDE>
 __global__ void __launch_bounds__(kGradThreads) route_grad_kernel(const __grid_constant__ RouteGradParams p) {
     const int lane = threadIdx.x & 31;
-    const int64_t t = (int64_t)blockIdx.x * (kGradThreads / 32) + (threadIdx.x >> 5);
-    if (t >= p.tokens) return;
     constexpr bool kAll = CHUNKS > 0;
-    const char *row = p.logits + t * p.logits_stride;
-    char *out = p.out + t * p.out_stride;
-    int id = -1;
-    float w = 0.f, d = 0.f;
-    if (lane < p.k) {
-        id = p.ids[t * p.k + lane];
-        if (id < 0 || id >= p.experts) id = -1;
-        if (id >= 0) w = p.weights[t * p.k + lane], d = p.dweights[t * p.k + lane];
-    }
-    float dot = w * d;
+    // A token's choices and logits are under way while the one before is done.
+    struct Token {
+        int id;
+        float w, d;
+        elem::Raw r[kAll ? CHUNKS : 1];
+    };
+    auto load = [&](Token &n, int64_t t) {
+        n.id = -1;
+        n.w = n.d = 0.f;
+        if (t >= p.tokens) return;
+        const char *row = p.logits + t * p.logits_stride;
+        if constexpr (kAll) {
 #pragma unroll
-    for (int s = 16; s > 0; s >>= 1) dot += __shfl_xor_sync(0xFFFFFFFFu, dot, s);
-    float own = kAll ? w * d : w * (d - dot);
-    // a choice made twice has both parts
-    float both = 0.f;
-    for (int j = 0; j < p.k; ++j) {
-        const float other = __shfl_sync(0xFFFFFFFFu, own, j);
-        if (__shfl_sync(0xFFFFFFFFu, id, j) == id) both += other;
-    }
-    own = both;
-    if constexpr (kAll) {
-        elem::Raw r[CHUNKS];
-#pragma unroll
-        for (int i = 0; i < CHUNKS; ++i) r[i] = elem::load(row, (lane + 32 * i) * 8, p.experts, DTYPE, p.wide_logits);
-        const float mine = id >= 0 ? at(row, id, DTYPE) : 0.f;
-        float most = __int_as_float(0xFF800000), sum = 0.f;
-        float v[CHUNKS][8];
-#pragma unroll
-        for (int i = 0; i < CHUNKS; ++i) {
-            elem::to_floats(v[i], r[i], DTYPE);
-#pragma unroll
-            for (int q = 0; q < 8; ++q) {
-                if ((lane + 32 * i) * 8 + q >= p.experts) v[i][q] = __int_as_float(0xFF800000);
-                most = fmaxf(most, v[i][q]);
+            for (int i = 0; i < CHUNKS; ++i) {
+                if constexpr (WIDE) {
+                    const uint4 *from = reinterpret_cast<const uint4 *>(row) + (lane + 32 * i) * (DTYPE == CSF_F32 ? 2 : 1);
+                    // past the row's end: -infinity
+                    constexpr uint32_t kOff = DTYPE == CSF_F32 ? 0xFF800000u : DTYPE == CSF_BF16 ? 0xFF80FF80u : 0xFC00FC00u;
+                    n.r[i].a = n.r[i].b = make_uint4(kOff, kOff, kOff, kOff);
+                    if ((lane + 32 * i) * 8 < p.experts) {
+                        n.r[i].a = __ldg(from);
+                        if (DTYPE == CSF_F32) n.r[i].b = __ldg(from + 1);
+                    }
+                } else {
+                    n.r[i] = elem::load(row, (lane + 32 * i) * 8, p.experts, DTYPE, p.wide_logits);
+                }
             }
         }
-#pragma unroll
-        for (int s = 16; s > 0; s >>= 1) most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, s));
-        const bool none = most == __int_as_float(0xFF800000);      // every expert is off: their exponentials are 0
-        const float zero = none ? 0.f : most;
-#pragma unroll
-        for (int i = 0; i < CHUNKS; ++i)
-#pragma unroll
-            for (int q = 0; q < 8; ++q) sum += v[i][q] = expf(v[i][q] - zero);
-#pragma unroll
-        for (int s = 16; s > 0; s >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, s);
-        const float rate = none ? 0.f : -dot / sum;
-        own += expf(mine - zero) * rate;
-        __syncwarp();      // every lane has read: the row may be written where it lay
-#pragma unroll
-        for (int i = 0; i < CHUNKS; ++i) {
-            const int c = (lane + 32 * i) * 8;
-            if (c >= p.experts) break;
-#pragma unroll
-            for (int q = 0; q < 8; ++q) v[i][q] *= rate;
-            elem::store(out, c, p.experts, elem::from_floats(v[i], DTYPE), DTYPE, p.wide_out);
+        if (lane < p.k) {
+            n.id = __ldg(p.ids + t * p.k + lane);
+            n.w = __ldg(p.weights + t * p.k + lane), n.d = __ldg(p.dweights + t * p.k + lane);
         }
-    } else {
-        const elem::Raw zeros = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
-        for (int c = lane * 8; c < p.experts; c += 256) elem::store(out, c, p.experts, zeros, DTYPE, p.wide_out);
+    };
+    const int64_t step = (int64_t)gridDim.x * (kGradThreads / 32);
+    int64_t t = (int64_t)blockIdx.x * (kGradThreads / 32) + (threadIdx.x >> 5);
+    Token next;
+    load(next, t);
+    for (; t < p.tokens; t += step) {
+        Token n = next;
+        load(next, t + step);
+        if (n.id < 0 || n.id >= p.experts) n.id = -1, n.w = 0.f, n.d = 0.f;
+        // (again, from a cache: where it lies in the registers is not known when this is compiled)
+        const float mine = kAll && n.id >= 0 ? at(p.logits + t * p.logits_stride, n.id, DTYPE) : 0.f;
+        char *out = p.out + t * p.out_stride;
+        float dot = n.w * n.d;
+#pragma unroll
+        for (int s = 16; s > 0; s >>= 1) dot += __shfl_xor_sync(0xFFFFFFFFu, dot, s);
+        float own = kAll ? n.w * n.d : n.w * (n.d - dot);
+        // a choice made twice has both parts
+        bool again = false;
+        if (p.k <= 8) {
+#pragma unroll
+            for (int j = 1; j < 8; ++j) again |= __shfl_down_sync(0xFFFFFFFFu, n.id, j, 8) == n.id && lane + j < 8;
+        } else {
+            for (int j = 0; j < p.k; ++j) again |= __shfl_sync(0xFFFFFFFFu, n.id, j) == n.id && j != lane;
+        }
+        if (__any_sync(0xFFFFFFFFu, again && n.id >= 0)) {
+            float both = 0.f;
+            for (int j = 0; j < p.k; ++j) {
+                const float other = __shfl_sync(0xFFFFFFFFu, own, j);
+                if (__shfl_sync(0xFFFFFFFFu, n.id, j) == n.id) both += other;
+            }
+            own = both;
+        }
+        if constexpr (kAll) {
+            float most = __int_as_float(0xFF800000), sum = 0.f;
+            float v[CHUNKS][8];
+#pragma unroll
+            for (int i = 0; i < CHUNKS; ++i) {
+                elem::to_floats(v[i], n.r[i], DTYPE);
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                    if (!WIDE && (lane + 32 * i) * 8 + q >= p.experts) v[i][q] = __int_as_float(0xFF800000);
+                    most = fmaxf(most, v[i][q]);
+                }
+            }
+            most = warp_max(most);
+            const bool none = most == __int_as_float(0xFF800000);      // every expert is off: their exponentials are 0
+            const float zero = none ? 0.f : most;
+#pragma unroll
+            for (int i = 0; i < CHUNKS; ++i)
+#pragma unroll
+                for (int q = 0; q < 8; ++q) sum += v[i][q] = exp_below<DTYPE>(v[i][q] - zero);
+#pragma unroll
+            for (int s = 16; s > 0; s >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, s);
+            const float rate = none ? 0.f : -dot / sum;
+            own += exp_below<DTYPE>(mine - zero) * rate;
+            __syncwarp();      // every lane has read: the row may be written where it lay
+#pragma unroll
+            for (int i = 0; i < CHUNKS; ++i) {
+                const int c = (lane + 32 * i) * 8;
+                if (c >= p.experts) break;
+#pragma unroll
+                for (int q = 0; q < 8; ++q) v[i][q] *= rate;
+                elem::store(out, c, p.experts, elem::from_floats(v[i], DTYPE), DTYPE, WIDE || p.wide_out);
+            }
+        } else {
+            const elem::Raw zeros = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+            for (int c = lane * 8; c < p.experts; c += 256) elem::store(out, c, p.experts, zeros, DTYPE, p.wide_out);
+        }
+        __syncwarp();      // the row is written: the choices' places once more
+        if (n.id >= 0) {
+            if (DTYPE == CSF_F32) reinterpret_cast<float *>(out)[n.id] = own;
+            else if (DTYPE == CSF_BF16) reinterpret_cast<__nv_bfloat16 *>(out)[n.id] = __float2bfloat16_rn(own);
+            else reinterpret_cast<__half *>(out)[n.id] = __float2half_rn(own);
+        }
     }
-    __syncwarp();
-    if (id >= 0) {
-        if (DTYPE == CSF_F32) reinterpret_cast<float *>(out)[id] = own;
-        else if (DTYPE == CSF_BF16) reinterpret_cast<__nv_bfloat16 *>(out)[id] = __float2bfloat16_rn(own);
-        else reinterpret_cast<__half *>(out)[id] = __float2half_rn(own);
-    }
+}
+
+template <int DTYPE, int CHUNKS>
+void launch_chunks(const RouteGradParams &p, cudaStream_t s) {
+    const int64_t blocks = ((int64_t)p.tokens + kGradThreads / 32 - 1) / (kGradThreads / 32);
+    const unsigned grid = (unsigned)std::min<int64_t>(blocks, kGradBlocks * (int64_t)std::max(sm_count(), 1));
+    if (CHUNKS > 0 && p.wide_logits && p.wide_out && p.experts % 8 == 0) route_grad_kernel<DTYPE, CHUNKS, true><<<grid, kGradThreads, 0, s>>>(p);
+    else route_grad_kernel<DTYPE, CHUNKS, false><<<grid, kGradThreads, 0, s>>>(p);
 }
 
 template <int DTYPE>
 void launch(const RouteGradParams &p, bool renormalize, cudaStream_t s) {
-    const unsigned grid = (unsigned)(((int64_t)p.tokens + kGradThreads / 32 - 1) / (kGradThreads / 32));
-    const int chunks = renormalize ? 0 : (p.experts + 255) / 256;
-    switch (chunks) {
-        case 0: route_grad_kernel<DTYPE, 0><<<grid, kGradThreads, 0, s>>>(p); break;
-        case 1: route_grad_kernel<DTYPE, 1><<<grid, kGradThreads, 0, s>>>(p); break;
-        case 2: route_grad_kernel<DTYPE, 2><<<grid, kGradThreads, 0, s>>>(p); break;
-        case 3: route_grad_kernel<DTYPE, 3><<<grid, kGradThreads, 0, s>>>(p); break;
-        default: route_grad_kernel<DTYPE, 4><<<grid, kGradThreads, 0, s>>>(p); break;
+    switch (renormalize ? 0 : (p.experts + 255) / 256) {
+        case 0: launch_chunks<DTYPE, 0>(p, s); break;
+        case 1: launch_chunks<DTYPE, 1>(p, s); break;
+        case 2: launch_chunks<DTYPE, 2>(p, s); break;
+        case 3: launch_chunks<DTYPE, 3>(p, s); break;
+        default: launch_chunks<DTYPE, 4>(p, s); break;
     }
 }
 

@@ -190,9 +190,10 @@ def _check_quantized(q: Quantized, what: str, device: int, kinds=_KINDS):
         raise CsfError(f"{what}: quantised rows are {' or '.join(('NVFP4', 'MXFP8', '', 'FP8')[k] for k in kinds)}")
     if c.dtype != torch.uint8 or s.dtype != torch.uint8 or device < 0 or c.get_device() != device or s.get_device() != device:
         raise CsfError(f"{what}: codes and scales must be uint8 CUDA tensors{_where(device)}")
-    if c.dim() != 2 or s.dim() != 2 or c.shape[0] != s.shape[0] or c.stride(1) != 1 or s.stride(1) != 1:
+    cs, ss = c.shape, s.shape
+    if len(cs) != 2 or len(ss) != 2 or cs[0] != ss[0] or c.stride(1) != 1 or s.stride(1) != 1:
         raise CsfError(f"{what}: codes and scales must be [rows, bytes] with contiguous rows")
-    if q.cols < 1 or c.shape[1] < _code_bytes(q.kind, q.cols) or s.shape[1] < _scale_bytes(q.kind, q.cols):
+    if q.cols < 1 or cs[1] < _code_bytes(q.kind, q.cols) or ss[1] < _scale_bytes(q.kind, q.cols):
         raise CsfError(f"{what}: codes or scales are too narrow for {q.cols} columns")
 
 
@@ -371,6 +372,15 @@ def expert_matmul(x: Quantized, w: torch.Tensor, w_scales: torch.Tensor, expert_
 
 
 # ---- tokens to slots and back, and the gradients (csf_layer.h) ----
+#
+# One token's call waits for these checks, so each looks at a tensor once and
+# leaves the finding of words for what is wrong to the checks above.
+
+def _error_pointer(device: int) -> int:
+    """The address of the device's own error word."""
+    word = _error_words.get(device)
+    return (_error_word(device) if word is None else word).data_ptr()
+
 
 def _reporting(call, pack: struct.Struct, fields: tuple, error_word, device: int, what: str):
     """The library call with an error word as its last field: the one given, or the device's own."""
@@ -378,55 +388,94 @@ def _reporting(call, pack: struct.Struct, fields: tuple, error_word, device: int
         word = _vector(error_word, f"{what}: error_word", 1, torch.int32, device)
         return _launch(call, pack.pack(*fields, word), device, "csf_" + what)
     with _error_lock:
-        _launch(call, pack.pack(*fields, _error_word(device).data_ptr()), device, "csf_" + what)
+        _launch(call, pack.pack(*fields, _error_pointer(device)), device, "csf_" + what)
+
+
+def _rows_of(t, name: str, rows: int, cols: int, device: int):
+    """Pointer, stride and csf_dtype of a plain matrix [rows, cols] (_matrix)."""
+    d = _DTYPES.get(t.dtype)
+    if d is not None and device >= 0 and t.get_device() == device and t.shape == (rows, cols):
+        s0, s1 = t.stride()
+        if s1 == 1 or cols <= 1:
+            return t.data_ptr(), s0 if rows > 1 else max(s0, cols), d
+    return (*_matrix(t, name, rows, cols, device), d)       # which finds what is wrong
+
+
+def _any_rows(t, name: str):
+    """Its rows, columns and device too, of a matrix that says what they are."""
+    if t.dim() != 2 or t.dtype not in _DTYPES:
+        raise CsfError(f"{name} must be [rows, cols] of bfloat16, float16 or float32")
+    rows, cols = t.shape
+    if cols < 1:
+        raise CsfError(f"{name} has at least one column")
+    device = t.get_device()
+    return (*_rows_of(t, name, rows, cols, device), rows, cols, device)
 
 
 def _slots(slots, tokens: int, what: str, device: int):
-    if slots.get_device() != device or slots.dtype != torch.int32 or slots.dim() != 2 or slots.shape[0] != tokens or \
-            not slots.is_contiguous():
+    shape = slots.shape
+    if slots.dtype != torch.int32 or len(shape) != 2 or shape[0] != tokens or slots.get_device() != device or not slots.is_contiguous():
         raise CsfError(f"{what}: slots must be a contiguous int32 CUDA tensor [{tokens}, k]{_where(device)}")
-    if not 1 <= slots.shape[1] <= 1024:
+    if not 1 <= shape[1] <= 1024:
         raise CsfError(f"{what}: k must be 1 to 1024")
-    return slots.data_ptr(), slots.shape[1]
+    return slots.data_ptr(), shape[1]
 
 
-def _choice_vector(t, name: str, like: torch.Tensor, device: int):
+def _choice_vector(t, name: str, shape, device: int):
     """A float32 value per choice, contiguous, of the slots' or ids' shape."""
-    if t is not None and tuple(t.shape) != tuple(like.shape):
-        raise CsfError(f"{name} must be {list(like.shape)}")
-    return _vector(t, name, like.numel(), torch.float32, device)
+    if t is None:
+        return 0
+    if t.shape != shape:
+        raise CsfError(f"{name} must be {list(shape)}")
+    if t.dtype != torch.float32 or t.get_device() != device or not t.is_contiguous():
+        raise CsfError(f"{name} must be a contiguous float32 CUDA tensor{_where(device)}")
+    return t.data_ptr()
 
 
-def _output(out, rows: int, cols: int, dtype, tensor_scale, what: str, x: torch.Tensor):
+_PLAIN_NONE = (0, 0, 0)
+
+
+def _output(out, rows: int, cols: int, dtype, tensor_scale, what: str, device: int):
     """An output that a call is given or names by dtype or kind: the result,
     then the fields (pointer, stride, csf_dtype) of a plain one and those of
     csf_rows, zeros for the one that it is not."""
-    device = x.get_device()
     if out is None:
         out = dtype
     if isinstance(out, torch.dtype):
-        if out not in _DTYPES:
+        d = _DTYPES.get(out)
+        if d is None:
             raise CsfError(f"{what}: out must be bfloat16, float16 or float32")
-        out = torch.empty((rows, cols), dtype=out, device=x.device)
+        if tensor_scale is None:
+            if device < 0:
+                raise CsfError(f"{what}: not CUDA tensors")
+            out = torch.empty((rows, cols), dtype=out, device=_devices[device])
+            return out, (out.data_ptr(), cols, d), _NO_ROWS
     elif isinstance(out, int):
-        out = empty_quantized(out, rows, cols, x.device, tensor_scale)
+        if device < 0:
+            raise CsfError(f"{what}: not CUDA tensors")
+        out = empty_quantized(out, rows, cols, _devices[device], tensor_scale)
+        if tensor_scale is not None:
+            _tensor_scale(out, tensor_scale, what, device)
+        return out, _PLAIN_NONE, out.fields()
     if isinstance(out, Quantized):
         _check_quantized(out, f"{what}: out", device)
         if out.rows != rows or out.cols != cols:
             raise CsfError(f"{what}: out is {out.rows} rows of {out.cols}, not {rows} of {cols}")
-        out.tensor_scale = _tensor_scale(out, tensor_scale, what, device)
-        return out, (0, 0, 0), out.fields()
+        if tensor_scale is not None or out.tensor_scale is not None:
+            out.tensor_scale = _tensor_scale(out, tensor_scale, what, device)
+        return out, _PLAIN_NONE, out.fields()
     if tensor_scale is not None:
         raise CsfError(f"{what}: only NVFP4 rows have a tensor scale")
-    return out, (*_matrix(out, f"{what}: out", rows, cols, device), _DTYPES[out.dtype]), _NO_ROWS
+    return out, _rows_of(out, f"{what}: out", rows, cols, device), _NO_ROWS
 
 
-def _plain(x: torch.Tensor, what: str):
-    if x.dim() != 2 or x.dtype not in _DTYPES:
-        raise CsfError(f"{what} must be [rows, cols] of bfloat16, float16 or float32")
-    if x.shape[1] < 1:
-        raise CsfError(f"{what} has at least one column")
-    return _matrix(x, what, x.shape[0], x.shape[1], x.get_device())
+class _Devices(dict):
+    def __missing__(self, index: int) -> torch.device:
+        device = self[index] = torch.device("cuda", index)
+        return device
+
+
+_devices = _Devices()
 
 
 def quantize(x: torch.Tensor, kind: int, tensor_scale: torch.Tensor | None = None, out: Quantized | None = None,
@@ -434,14 +483,13 @@ def quantize(x: torch.Tensor, kind: int, tensor_scale: torch.Tensor | None = Non
     """The rows of `x` [rows, cols] quantised (csf_dispatch without slots)."""
     if stream is not None:
         return _on(stream, quantize, x, kind, tensor_scale, out)
-    xp, xs = _plain(x, "quantize: x")
-    T, H = x.shape
     if kind not in _KINDS:
         raise CsfError("quantised rows are NVFP4 or MXFP8 or FP8")
+    xp, xs, xd, T, H, device = _any_rows(x, "quantize: x")
     if out is not None and (not isinstance(out, Quantized) or out.kind != kind):
         raise CsfError("quantize: out does not match kind")
-    out, plain, rows = _output(kind if out is None else out, T, H, None, tensor_scale, "quantize", x)
-    _launch(lib.csf_dispatch, _DISPATCH.pack(xp, xs, _DTYPES[x.dtype], T, H, 0, 0, T, *plain, *rows, 0), x.get_device(), "csf_dispatch")
+    out, plain, rows = _output(kind if out is None else out, T, H, None, tensor_scale, "quantize", device)
+    _launch(lib.csf_dispatch, _DISPATCH.pack(xp, xs, xd, T, H, 0, 0, T, *plain, *rows, 0), device, "csf_dispatch")
     return out
 
 
@@ -457,13 +505,11 @@ def dispatch(x: torch.Tensor, slots: torch.Tensor, out=None, tensor_scale: torch
     `error_word` or errors().  The gradient is dispatch_grad."""
     if stream is not None:
         return _on(stream, dispatch, x, slots, out, tensor_scale, error_word)
-    xp, xs = _plain(x, "dispatch: x")
-    T, H = x.shape
-    device = x.get_device()
+    xp, xs, xd, T, H, device = _any_rows(x, "dispatch: x")
     sp, k = _slots(slots, T, "dispatch", device)
     S = out.rows if isinstance(out, Quantized) else out.shape[0] if isinstance(out, torch.Tensor) and out.dim() else T * k
-    out, plain, rows = _output(out, S, H, x.dtype, tensor_scale, "dispatch", x)
-    _reporting(lib.csf_dispatch, _DISPATCH, (xp, xs, _DTYPES[x.dtype], T, H, k, sp, S, *plain, *rows), error_word, device, "dispatch")
+    out, plain, rows = _output(out, S, H, x.dtype, tensor_scale, "dispatch", device)
+    _reporting(lib.csf_dispatch, _DISPATCH, (xp, xs, xd, T, H, k, sp, S, *plain, *rows), error_word, device, "dispatch")
     return out
 
 
@@ -476,18 +522,18 @@ def combine(y: torch.Tensor, slots: torch.Tensor, weights: torch.Tensor | None =
     Slots of -1 add nothing.  The gradient is combine_grad."""
     if stream is not None:
         return _on(stream, combine, y, slots, weights, residual, out, error_word)
-    yp, ys = _plain(y, "combine: y")
-    if slots.dim() != 2:
+    yp, ys, yd, S, H, device = _any_rows(y, "combine: y")
+    shape = slots.shape
+    if len(shape) != 2:
         raise CsfError("combine: slots must be [tokens, k]")
-    (S, H), T, device = y.shape, slots.shape[0], y.get_device()
+    T = shape[0]
     sp, k = _slots(slots, T, "combine", device)
-    rp, rs = (0, 0) if residual is None else _matrix(residual, "combine: residual", T, H, device)
+    rp, rs, rd = _PLAIN_NONE if residual is None else _rows_of(residual, "combine: residual", T, H, device)
     if not isinstance(out, (torch.Tensor, torch.dtype, type(None))):
         raise CsfError("combine: out is a dtype or a tensor")
-    out, (op, os_, odt), _ = _output(out, T, H, y.dtype, None, "combine", y)
-    _reporting(lib.csf_combine, _COMBINE, (yp, ys, S, _DTYPES[y.dtype], T, H, k, sp, _choice_vector(weights, "combine: weights", slots, device),
-                                           rp, rs, 0 if residual is None else _DTYPES[residual.dtype], odt, op, os_),
-               error_word, device, "combine")
+    out, (op, os_, od), _ = _output(out, T, H, y.dtype, None, "combine", device)
+    _reporting(lib.csf_combine, _COMBINE, (yp, ys, S, yd, T, H, k, sp, _choice_vector(weights, "combine: weights", shape, device),
+                                           rp, rs, rd, od, op, os_), error_word, device, "combine")
     return out
 
 
@@ -508,24 +554,22 @@ def combine_grad(g: torch.Tensor, y: torch.Tensor | None, slots: torch.Tensor, w
     them, or tokens * k); False: no dy is wanted, and None is returned."""
     if stream is not None:
         return _on(stream, combine_grad, g, y, slots, weights, out, tensor_scale, error_word)
-    gp, gs = _plain(g, "combine_grad: g")
-    T, H = g.shape
-    device = g.get_device()
+    gp, gs, gd, T, H, device = _any_rows(g, "combine_grad: g")
     sp, k = _slots(slots, T, "combine_grad", device)
     if y is not None:
         S = y.shape[0] if y.dim() else 0
     else:
         S = out.rows if isinstance(out, Quantized) else out.shape[0] if isinstance(out, torch.Tensor) and out.dim() else T * k
-    yp, ys = (0, 0) if y is None else _matrix(y, "combine_grad: y", S, H, device)
+    yp, ys, yd = _PLAIN_NONE if y is None else _rows_of(y, "combine_grad: y", S, H, device)
     if out is False:
-        dy, (dp, ds, ddt), rows = None, (0, 0, 0), _NO_ROWS
+        dy, (dp, ds, dd), rows = None, _PLAIN_NONE, _NO_ROWS
     else:
-        dy, (dp, ds, ddt), rows = _output(out, S, H, (g if y is None else y).dtype, tensor_scale, "combine_grad", g)
-    wp = _choice_vector(weights, "combine_grad: weights", slots, device)
-    dweights = None if y is None else torch.empty((T, k), dtype=torch.float32, device=g.device)
+        dy, (dp, ds, dd), rows = _output(out, S, H, (g if y is None else y).dtype, tensor_scale, "combine_grad", device)
+    wp = _choice_vector(weights, "combine_grad: weights", slots.shape, device)
+    dweights = None if y is None else torch.empty((T, k), dtype=torch.float32, device=_devices[device])
     _reporting(lib.csf_combine_grad, _COMBINE_GRAD,
-               (gp, gs, yp, ys, S, _DTYPES[g.dtype], 0 if y is None else _DTYPES[y.dtype], T, H, k, ddt, sp, wp, dp, ds, *rows,
-                0 if y is None else dweights.data_ptr()), error_word, device, "combine_grad")
+               (gp, gs, yp, ys, S, gd, yd, T, H, k, dd, sp, wp, dp, ds, *rows, 0 if y is None else dweights.data_ptr()),
+               error_word, device, "combine_grad")
     return dy, dweights
 
 
@@ -538,23 +582,21 @@ def route_grad(logits: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, d
     new tensor."""
     if stream is not None:
         return _on(stream, route_grad, logits, ids, weights, dweights, renormalize, out)
-    lp, ls = _plain(logits, "route_grad: logits")
-    T, E = logits.shape
-    device = logits.get_device()
-    if ids.get_device() != device or ids.dtype != torch.int32 or ids.dim() != 2 or ids.shape[0] != T or not ids.is_contiguous():
+    lp, ls, ld, T, E, device = _any_rows(logits, "route_grad: logits")
+    shape = ids.shape
+    if ids.dtype != torch.int32 or len(shape) != 2 or shape[0] != T or ids.get_device() != device or not ids.is_contiguous():
         raise CsfError(f"route_grad: ids must be a contiguous int32 CUDA tensor [{T}, k]{_where(device)}")
-    k = ids.shape[1]
+    k = shape[1]
     if not 1 <= k <= min(32, E):
         raise CsfError(f"route_grad: k must be 1 to {min(32, E)}")
-    if out is None:
-        out = torch.empty((T, E), dtype=logits.dtype, device=logits.device)
-    op, os_ = _matrix(out, "route_grad: out", T, E, device, logits.dtype)
     if weights is None or dweights is None:
         raise CsfError("route_grad: weights and dweights are needed")
-    a = _ROUTE_GRAD.pack(lp, ls, op, os_, _DTYPES[logits.dtype], T, E, k, ids.data_ptr(),
-                         _choice_vector(weights, "route_grad: weights", ids, device),
-                         _choice_vector(dweights, "route_grad: dweights", ids, device), renormalize)
-    _launch(lib.csf_route_grad, a, device, "csf_route_grad")
+    wp, dp = _choice_vector(weights, "route_grad: weights", shape, device), _choice_vector(dweights, "route_grad: dweights", shape, device)
+    if out is None:
+        out, (op, os_, _), _ = _output(None, T, E, logits.dtype, None, "route_grad", device)
+    else:
+        op, os_ = _matrix(out, "route_grad: out", T, E, device, logits.dtype)
+    _launch(lib.csf_route_grad, _ROUTE_GRAD.pack(lp, ls, op, os_, ld, T, E, k, ids.data_ptr(), wp, dp, renormalize), device, "csf_route_grad")
     return out
 
 
@@ -579,39 +621,39 @@ def fp8_matmul(x: Quantized, w: torch.Tensor, w_scales: torch.Tensor, expert_sta
                    transposed, out, error_word)
     device = x.codes.get_device()
     _check_quantized(x, "fp8_matmul: x", device, (FP8,))
-    if w.dtype not in (torch.float8_e4m3fn, torch.uint8) or w.get_device() != device or w.dim() != 3 or not w.is_contiguous():
+    if (w.dtype != torch.float8_e4m3fn and w.dtype != torch.uint8) or w.get_device() != device or w.dim() != 3 or not w.is_contiguous():
         raise CsfError(f"fp8_matmul: w must be a contiguous float8_e4m3fn or uint8 CUDA tensor [E, N, K]{_where(device)}")
     E, N, K = w.shape
     if x.cols != (N if transposed else K):
         raise CsfError(f"fp8_matmul: x has {x.cols} columns, w{' transposed' if transposed else ''} takes {N if transposed else K}")
-    if tuple(w_scales.shape) != (E, (N + 127) // 128, (K + 127) // 128):
-        raise CsfError(f"fp8_matmul: w_scales must be [{E}, {(N + 127) // 128}, {(K + 127) // 128}]")
-    wp = _vector(w_scales, "fp8_matmul: w_scales", w_scales.numel(), torch.float32, device)
+    wp = _choice_vector(w_scales, "fp8_matmul: w_scales", (E, (N + 127) // 128, (K + 127) // 128), device)
     if activation not in _ACTS:
         raise CsfError(f"fp8_matmul: unknown activation {activation!r}")
-    if rows is not None and (rows.get_device() != device or rows.dtype != torch.int32 or not rows.is_contiguous() or rows.dim() != 1):
-        raise CsfError(f"fp8_matmul: rows must be a contiguous int32 CUDA vector{_where(device)}")
-    es, es64 = _es(expert_start)
+    rows_p, S = 0, x.codes.shape[0]
+    if rows is not None:
+        if rows.dtype != torch.int32 or rows.get_device() != device or rows.dim() != 1 or not rows.is_contiguous():
+            raise CsfError(f"fp8_matmul: rows must be a contiguous int32 CUDA vector{_where(device)}")
+        rows_p, S = rows.data_ptr(), rows.shape[0]
+    es = es64 = 0
     if expert_start is not None:
+        es, es64 = _es(expert_start)
         if expert_start.get_device() != device:
             raise CsfError(f"expert_start must be a CUDA tensor{_where(device)}")
         if expert_start.numel() != E + 1:
             raise CsfError("expert_start must have E+1 entries")
-    S = x.rows if rows is None else rows.shape[0]
     O = K if transposed else N
     F = O // 2 if gated else O
-    bias_dtype = 0
+    bp = bd = 0
     if bias is not None:
         if bias.dtype not in _DTYPES:
             raise CsfError("fp8_matmul: bias must be bfloat16, float16 or float32")
-        bias_dtype = _DTYPES[bias.dtype]
-    rp, rs = (0, 0) if residual is None else _matrix(residual, "fp8_matmul: residual", S, F, device)
+        bp, bd = _vector(bias, "fp8_matmul: bias", E * O, bias.dtype, device), _DTYPES[bias.dtype]
+    rp, rs, rd = _PLAIN_NONE if residual is None else _rows_of(residual, "fp8_matmul: residual", S, F, device)
     if (isinstance(out, int) and out != FP8) or (isinstance(out, Quantized) and out.kind != FP8):
         raise CsfError("fp8_matmul: out is a dtype, a tensor or FP8 rows")
-    out, (op, os_, odt), orows = _output(out, S, F, torch.bfloat16, None, "fp8_matmul", x.codes)
+    out, (op, os_, od), orows = _output(out, S, F, torch.bfloat16, None, "fp8_matmul", device)
     _reporting(lib.csf_fp8_matmul, _FP8_MATMUL, (
-        *x.fields(), 0 if rows is None else rows.data_ptr(), S, E, N, K, transposed, w.data_ptr(), wp, es or 0, es64, bias_dtype,
-        0 if bias is None else _vector(bias, "fp8_matmul: bias", E * O, bias.dtype, device), _ACTS[activation], gated,
-        _vector(row_scale, "fp8_matmul: row_scale", S, torch.float32, device), rp, rs,
-        0 if residual is None else _DTYPES[residual.dtype], odt, op, os_, *orows), error_word, device, "fp8_matmul")
+        *x.fields(), rows_p, S, E, N, K, transposed, w.data_ptr(), wp, es, es64, bd, bp, _ACTS[activation], gated,
+        0 if row_scale is None else _vector(row_scale, "fp8_matmul: row_scale", S, torch.float32, device), rp, rs, rd, od, op, os_, *orows),
+        error_word, device, "fp8_matmul")
     return out
