@@ -164,7 +164,8 @@ extern "C" csf_status csf_fp8_matmul(const csf_fp8_matmul_args *a, void *stream)
     } else {
         xmap = wmap;      // not read
     }
-    const int mode = !a->out ? kQuant : a->residual || a->out_dtype == CSF_F32 ? kPlain : kHalves;
+    const bool sums = a->residual && a->residual_dtype != CSF_F32 && p.residual_wide && p.out_wide && p.F % 8 == 0;
+    const int mode = !a->out ? kQuant : a->out_dtype == CSF_F32 ? kPlain : !a->residual ? kHalves : sums ? kHalvesSum : kPlain;
     Kernel k = a->rows ? rows_by_index(shape, mode) : rows_in_order(shape, mode);
     // the register split waits for what the block was launched with (given out in eights)
     if (!allow_smem(reinterpret_cast<const void *>(k), kSmemLimit, launch_regs(a->rows) - 7)) return CSF_ERR_CUDA;

@@ -114,10 +114,12 @@ __device__ __forceinline__ void activate32(float (&y)[32], int act) {
     if (act == CSF_ACT_RELU) {
 #pragma unroll
         for (int i = 0; i < 32; ++i) y[i] = y[i] < 0.f ? 0.f : y[i];
-    } else {
-        const bool gelu = act == CSF_ACT_GELU_TANH;
+    } else if (act == CSF_ACT_SILU) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) y[i] = mm::smooth(y[i], gelu);
+        for (int i = 0; i < 32; ++i) y[i] = mm::smooth(y[i], false);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) y[i] = mm::smooth(y[i], true);
     }
 }
 
@@ -162,10 +164,10 @@ __device__ __forceinline__ void add_bias8(const Params &p, float *y, int e, int 
     for (int i = 0; i < 8; ++i) y[i] += b[i];
 }
 
-// What comes out: 16-bit rows, any plain rows (float32, or with a residual),
-// FP8 rows.  Kernels of their own, since what one holds in registers another
+// What comes out: 16-bit rows, any plain rows, FP8 rows, 16-bit rows with a
+// 16-bit residual (both in whole 16-byte pieces).  Kernels of their own, since what one holds in registers another
 // would spill.
-enum Mode { kHalves = 0, kPlain = 1, kQuant = 2 };
+enum Mode { kHalves = 0, kPlain = 1, kQuant = 2, kHalvesSum = 3 };
 
 // CTAS: blocks of a pair.  AT: 128-column weight blocks per tile.  ROWS: slot
 // s reads row rows[s] of x, else row s.  SPLIT: clusters share a tile's depth.
@@ -452,7 +454,7 @@ fp8_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constan
         for (uint32_t tile = unit, nth = 0; tile < total; tile += units, ++nth) {
             const Tile t = mm::find_tile(p, first, slot0, tile, lane);
             const int n = rows_of(t, pair_rank) - 32 * w;       // this warp's rows, if any
-            if (MODE != kHalves && !SPLIT && p.residual && lane < n) {
+            if (MODE != kHalves && !SPLIT && (MODE == kHalvesSum || p.residual) && lane < n) {
                 // what the epilogue will add to this lane's row, into L2
                 const int bytes = p.residual_dtype == CSF_F32 ? 4 : 2, f = t.rt * p.tile_step + (p.gated ? 64 * half : col0);
                 const char *at = static_cast<const char *>(p.residual) + (((int64_t)t.slot + 128 * pair_rank + 32 * w + lane) * p.residual_stride + f) * bytes;
@@ -579,14 +581,44 @@ fp8_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constan
                 // part q at q ^ (r % 8): written a row a lane and read 4 or 8
                 // rows at a time, both without bank conflicts.
                 auto piece_at = [&](int r, int q) { return buf + r * 32 + ((q ^ (r & 7)) << 2); };
-                if constexpr (MODE == kHalves) {
-                    // 64 columns at a time, rounded before the turn
+                if constexpr (MODE == kHalves || MODE == kHalvesSum) {
+                    // 64 columns at a time, rounded before the turn.  A residual
+                    // comes the other way through the same piece, the next 64
+                    // columns' under way meanwhile.
+                    constexpr bool kSum = MODE == kHalvesSum;
+                    const int q8 = lane & 7, r8 = lane >> 3;
+                    uint4 next[8] = {};           // (defined on every path: else it is held through the products, too)
+                    auto fetch = [&](int c0) {
+                        const uint4 *at = reinterpret_cast<const uint4 *>(static_cast<const char *>(p.residual) + ((slot + r8) * p.residual_stride + f0 + c0) * 2) + q8;
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            if (4 * i + r8 < n && f0 + c0 + 8 * q8 < p.F) next[i] = __ldg(at + i * (p.residual_stride >> 1));
+                    };
+                    if (kSum) fetch(0);
 #pragma unroll 1
                     for (int c0 = 0; c0 < cols && f0 + c0 < p.F; c0 += 64) {
+                        if (kSum) {
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) *reinterpret_cast<uint4 *>(piece_at(4 * i + r8, q8)) = next[i];
+                            __syncwarp();
+                            if (c0 + 64 < cols) fetch(c0 + 64);
+                        }
 #pragma unroll 1
                         for (int q = 0; q < 8; q += 4) {
                             float y[32];
                             values(y, c0 + 8 * q);
+                            if (kSum) {
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) {
+                                    elem::Raw raw;
+                                    raw.a = *reinterpret_cast<const uint4 *>(piece_at(lane, q + i));
+                                    raw.b = raw.a;
+                                    float b[8];
+                                    elem::to_floats(b, raw, p.residual_dtype);
+#pragma unroll
+                                    for (int j = 0; j < 8; ++j) y[8 * i + j] += b[j];
+                                }
+                            }
                             uint32_t o[16];
 #pragma unroll
                             for (int i = 0; i < 16; ++i) {
@@ -797,7 +829,7 @@ enum Shape { kPair = 0, kOne = 1, kTwo = 2, kOneShared = 3, kTwoShared = 4 };
 template <bool ROWS, int MODE>
 Kernel pick(int shape) {
     // where the depth is shared, what comes out is asked at run time
-    constexpr int kAny = MODE == kHalves ? kPlain : MODE;
+    constexpr int kAny = MODE == kQuant ? kQuant : kPlain;
     switch (shape) {
         case kPair: return fp8_matmul_kernel<2, 2, ROWS, false, MODE>;
         case kOne: return fp8_matmul_kernel<1, 1, ROWS, false, MODE>;
@@ -809,7 +841,12 @@ Kernel pick(int shape) {
 
 template <bool ROWS>
 Kernel pick_kernel(int shape, int mode) {
-    return mode == kHalves ? pick<ROWS, kHalves>(shape) : mode == kPlain ? pick<ROWS, kPlain>(shape) : pick<ROWS, kQuant>(shape);
+    switch (mode) {
+        case kHalves: return pick<ROWS, kHalves>(shape);
+        case kHalvesSum: return pick<ROWS, kHalvesSum>(shape);
+        case kPlain: return pick<ROWS, kPlain>(shape);
+        default: return pick<ROWS, kQuant>(shape);
+    }
 }
 
 // The kernel of a shape, one translation unit each for x rows in order and
