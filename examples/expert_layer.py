@@ -4,9 +4,10 @@
 
 The layer keeps its weights as E2M1 codes and their scales as CSF stacks.  A
 call adds the residual stream and norms and quantises it in one launch, chooses
-each token's experts, decodes the scales of the chosen experts only, and runs
-the experts' gate/up and down products with the activation, the requantisation
-and the router's weights in their epilogues.  Nothing is read back by the host.
+each token's experts, decodes the scales of the chosen experts only, runs the
+experts' gate/up and down products with the activation and the requantisation
+in their epilogues, and adds up each token's experts with the router's weights.
+Nothing is read back by the host.
 """
 from __future__ import annotations
 
@@ -46,15 +47,10 @@ class ExpertLayer:
         act = ops.expert_matmul(q, self.gate_up, self.workspace[0], expert_start=r.expert_start, rows=r.rows,
                                 alpha=self.alpha[0], activation="silu", gated=True, out=ops.NVFP4,
                                 out_tensor_scale=self.act_scale)
-        # the router's weight of each slot; a choice that fell away has slot -1, the last of one slot more than there are
-        weight = r.weights.new_empty(r.weights.numel() + 1)
-        weight[r.slots.view(-1).long()] = r.weights.view(-1)
         y = ops.expert_matmul(act, self.down, self.workspace[1], expert_start=r.expert_start, alpha=self.alpha[1],
-                              row_scale=weight[:-1], out=torch.float32)
-        y = y[r.slots.long()]
-        if off is not None:          # rows of choices that fell away hold nothing
-            y = torch.where((r.slots >= 0).unsqueeze(-1), y, 0.0)
-        return y.sum(1).to(x.dtype), residual
+                              out=torch.float32)
+        # choices that fell away have slot -1 and add nothing
+        return ops.combine(y, r.slots, r.weights, out=x.dtype), residual
 
 
 def random_layer(experts: int, hidden: int, inner: int, seed: int = 0) -> ExpertLayer:

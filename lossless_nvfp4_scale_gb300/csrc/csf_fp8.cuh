@@ -437,6 +437,10 @@ fp8_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constan
         // same 32 rows.
         const int w = warp & 3, half = (warp - kFirstSumWarp) >> 2;
         constexpr int kCols = AT * 64;                                      // this warp's columns
+        // columns taken out of tensor memory at a time: as many as the registers
+        // hold beside the sums (128 experts of 256 slots, gated, through an index:
+        // 412 us with 32, 445 with 64; dense 8191 x 5120 x 5120: 197 and 183)
+        constexpr int kTaken = ROWS ? 32 : 64;
         const int col0 = kCols * half;
         float *buf = region + (warp - kFirstSumWarp) * 32 * 32;
         const uint32_t lanes = tmem + ((uint32_t)(32 * w) << 16);
@@ -480,16 +484,17 @@ fp8_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constan
                     const uint32_t at = lanes + set * 128 + (AT == 2 ? 0 : col0);
                     uint64_t factor = 0;
 #pragma unroll
-                    for (int c = 0; c < kCols; c += 64) {
-                        uint32_t v[2][32];
-                        tc::tmem_load(at + c, v[0]);
-                        tc::tmem_load(at + c + 32, v[1]);
-                        if (c == 0) factor = tc::twice(factors[count % kFactorSteps][AT == 2 ? half : 0][32 * w + lane]);
-                        if (c + 64 == kCols) there = tc::bar_try_if(accf0 + 8 * next, ((count + 1) >> kRound) & 1, lane == 0 && !last);
-                        tc::wait_ld();
-                        if (c + 64 == kCols && !keep) release(set);
+                    for (int c = 0; c < kCols; c += kTaken) {
+                        uint32_t v[kTaken / 16][16];
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) tc::fma2_after(sum[c / 2 + j], v[j >> 4][2 * (j & 15)], v[j >> 4][2 * (j & 15) + 1], factor);
+                        for (int i = 0; i < kTaken / 16; ++i) tc::tmem_load(at + c + 16 * i, v[i]);
+                        if (c == 0) factor = tc::twice(factors[count % kFactorSteps][AT == 2 ? half : 0][32 * w + lane]);
+                        if (c + kTaken >= kCols) there = tc::bar_try_if(accf0 + 8 * next, ((count + 1) >> kRound) & 1, lane == 0 && !last);
+                        tc::wait_ld();
+                        if (c + kTaken >= kCols && !keep) release(set);
+#pragma unroll
+                        for (int j = 0; j < kTaken / 2; ++j)
+                            if (c / 2 + j < kCols / 2) tc::fma2_after(sum[c / 2 + j], v[j >> 3][2 * (j & 7)], v[j >> 3][2 * (j & 7) + 1], factor);
                     }
                 } else if (!keep) {
                     release(set);

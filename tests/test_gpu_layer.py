@@ -633,3 +633,120 @@ def test_route_gradient_of_repeated_and_missing_ids(ops):
         want = torch.zeros(2, 9, dtype=torch.float64, device="cuda") if renormalize else -torch.softmax(logits.double(), 1) * dot
         want.scatter_add_(1, torch.where(on, ids, 0).long(), own)
         close(d, want, 2.0 ** -20 * torch.ones_like(want))
+
+
+# ---- together ------------------------------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("T,masked", [(1, False), (37, True), (300, False)])
+def test_a_layer_forwards_and_back(ops, T, masked):
+    """Norm, router, 8-bit gate/up and down products and the sum of each token's experts; then the gradients from the
+    sum's back to the layer's input and the router's logits.  Each step against 64 bits, from what the steps before
+    made."""
+    H, I, E, k = 640, 256, 12, 4
+    g = gen(T)
+    dev = dict(device="cuda", generator=g)
+    x = torch.randn(T, H, **dev).to(torch.bfloat16)
+    h = torch.randn(T, H, **dev).to(torch.bfloat16)
+    w1 = (torch.randn(E, 2 * I, H, **dev) * 100).clamp(-448, 448).to(torch.float8_e4m3fn)
+    w2 = (torch.randn(E, H, I, **dev) * 100).clamp(-448, 448).to(torch.float8_e4m3fn)
+    s1 = (0.5 + torch.rand(E, blocks(2 * I), blocks(H), **dev)) / (100 * H ** 0.5)
+    s2 = (0.5 + torch.rand(E, blocks(H), blocks(I), **dev)) / (100 * I ** 0.5)
+    q, h = ops.rms_norm(x, torch.ones(H, dtype=torch.bfloat16, device="cuda"), ops.FP8, residual=h)
+    logits = torch.randn(T, E, **dev)
+    if masked:
+        logits[torch.rand(T, E, **dev) < 0.6] = -math.inf
+        logits[5::6] = -math.inf
+    r = ops.route(logits, k)
+    a = ops.fp8_matmul(q, w1, s1, expert_start=r.expert_start, rows=r.rows.clamp(min=0), activation="silu", gated=True, out=ops.FP8)
+    y = ops.fp8_matmul(a, w2, s2, expert_start=r.expert_start)
+    out = ops.combine(y, r.slots, r.weights, residual=h)
+
+    used = int(r.expert_start[-1])
+    expert = torch.repeat_interleave(torch.arange(E, device="cuda"), r.expert_start.diff().long())
+    rows = r.rows[:used].long()
+    wide = lambda s: s.double().repeat_interleave(128, 1).repeat_interleave(128, 2)  # noqa: E731
+    v1, v2 = w1.double() * wide(s1), w2.double() * wide(s2)
+
+    def product(x64, w64, transposed=False):          # and its slack
+        w = w64[expert]
+        w = w if transposed else w.transpose(1, 2)
+        depth = w.shape[1]
+        return (x64[:, None] @ w)[:, 0], (x64.abs()[:, None] @ w.abs())[:, 0] * (depth / 32 + 4) * 2.0 ** -23
+
+    cut = lambda z: ops.Quantized(z.kind, z.codes[:used], z.scales[:used], z.cols)  # noqa: E731
+    p64, slack = product(values(q)[rows], v1)
+    gate, upper = p64[:, :I], p64[:, I:]
+    eg, eu = slack[:, :I], slack[:, I:]
+    act = act64(gate, "silu")
+    check_quantized(cut(a), act * upper, (1.1 * eg + act.abs() * 2.0 ** -20) * (upper.abs() + eu) + act.abs() * eu + (act * upper).abs() * 2.0 ** -23)
+    y64, slack = product(values(a)[:used], v2)
+    close(y[:used], y64, slack)
+    want = combine64(torch.where(torch.isfinite(y), y, 0).double(), r.slots, r.weights.double(), h.double())
+    size = combine64(torch.where(torch.isfinite(y), y, 0).double().abs(), r.slots, r.weights.double(), h.double().abs())
+    close(out, want, size * (k + 2) * 2.0 ** -24)
+
+    # back
+    go = torch.randn(T, H, **dev).to(torch.bfloat16)
+    dy, dw = ops.combine_grad(go, y, r.slots, r.weights, out=ops.FP8)
+    da = ops.fp8_matmul(dy, w2, s2, expert_start=r.expert_start, transposed=True, out=torch.float32)
+    p = ops.fp8_matmul(q, w1, s1, expert_start=r.expert_start, rows=r.rows.clamp(min=0), out=torch.float32)
+    sg = torch.sigmoid(p[:, :I])
+    dp = torch.cat([da * p[:, I:] * sg * (1 + p[:, :I] * (1 - sg)), da * p[:, :I] * sg], 1)
+    dp[used:] = 0
+    dxs = ops.fp8_matmul(ops.quantize(dp, ops.FP8), w1, s1, expert_start=r.expert_start, transposed=True, out=torch.float32)
+    dx = ops.dispatch_grad(dxs, r.slots)
+    dl = ops.route_grad(logits, r.ids, r.weights, dw)
+
+    weight = torch.zeros(T * k + 1, device="cuda")
+    weight[r.slots.view(-1).long()] = r.weights.view(-1)
+    check_quantized(cut(dy), (weight[:used, None] * go[rows].float()).double())
+    da64, slack = product(values(dy)[:used], v2, transposed=True)
+    close(da[:used], da64, slack)
+    # silu(u) v and its derivatives in 64 bits, from the 32-bit sums, against differences
+    u, v = p[:used, :I].double(), p[:used, I:].double()
+    step = 2.0 ** -12
+    slope = (act64(u + step, "silu") - act64(u - step, "silu")) / (2 * step)
+    want = torch.cat([da[:used].double() * v * slope, da[:used].double() * act64(u, "silu")], 1)
+    assert ((dp[:used].double() - want).abs() <= want.abs() * 2.0 ** -18 + (da[:used].double().abs() * v.abs()).repeat(1, 2) * 2.0 ** -18).all()
+    dx64, slack = product(values(ops.quantize(dp, ops.FP8))[:used], v1, transposed=True)
+    close(dxs[:used], dx64, slack)
+    sums, size = torch.zeros(T, H, dtype=torch.float64, device="cuda"), torch.zeros(T, H, dtype=torch.float64, device="cuda")
+    sums.index_add_(0, rows, dxs[:used].double())
+    size.index_add_(0, rows, dxs[:used].double().abs())
+    close(dx, sums, size * k * 2.0 ** -24)
+    w64, dw64 = r.weights.double(), dw.double()
+    own = w64 * (dw64 - (w64 * dw64).sum(1, keepdim=True))
+    want = torch.zeros(T, E, dtype=torch.float64, device="cuda").scatter_add_(1, r.ids.clamp(min=0).long(), torch.where(r.ids >= 0, own, 0))
+    bound = (w64 * (dw64.abs() + (w64 * dw64.abs()).sum(1, keepdim=True))).sum(1, keepdim=True)
+    close(dl, want, bound * 2.0 ** -20)
+
+
+def test_inputs_may_be_let_go_of_and_capture_beside_eager_calls(ops):
+    """Calls on another stream keep their inputs; a captured run of the operators replays beside eager ones."""
+    r, _ = routes(ops, 64, 4, 16, 1, False)
+    g = gen(2)
+    p = Problem(ops, [256], 256, 512, seed=3)
+    side = torch.cuda.Stream()
+    want = ops.combine(p.run(out=torch.float32), r.slots, r.weights)
+    torch.cuda.synchronize()
+    side.wait_stream(torch.cuda.current_stream())
+    y = p.run(out=torch.float32, stream=side)
+    out = ops.combine(y, r.slots, r.weights, stream=side)
+    del y
+    torch.randn(1 << 22, device="cuda", generator=g)   # memory that is taken again meanwhile
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
+    ops.errors()                                       # the device's word, before a capture
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = p.run(out=torch.float32)
+        out = ops.combine(y, r.slots, r.weights)
+        dy, dw = ops.combine_grad(out, y, r.slots, r.weights, out=ops.FP8)
+        back = ops.fp8_matmul(dy, p.w, p.ws, transposed=True)
+    eager = p.run(out=torch.float32)
+    graph.replay()
+    eager2 = p.run(out=torch.float32)
+    torch.cuda.synchronize()
+    assert torch.equal(eager, eager2) and torch.equal(out, want)
+    dy2, dw2 = ops.combine_grad(want, eager, r.slots, r.weights, out=ops.FP8)
+    assert torch.equal(dw, dw2) and torch.equal(dy.codes, dy2.codes) and torch.equal(back, ops.fp8_matmul(dy2, p.w, p.ws, transposed=True))
