@@ -1,9 +1,11 @@
 // The gradient of the router's weights for its logits (csf_route_grad).
 //
-// A token is a warp's: lane j < k has choice j, and each lane up to 4 times 8
-// neighbouring experts, whose logits (for the softmax over all experts) stay
-// in registers.  The row is written once without the choices' own parts, and
-// then the choices' places once more: k of them, still in L2.  Bound by memory.
+// A token is a warp's or half a warp's: lane j < k has choice j, and each lane
+// pieces of 8 neighbouring experts, whose logits (for the softmax over all
+// experts) stay in registers.  The row is written once without the choices'
+// own parts, and then the choices' places once more: k of them, still in L2.
+// 32768 bfloat16 tokens of 384 experts, k = 8: bound by instructions (a warp a
+// token took 322 of them and 19.8 us; memory alone 7.9).
 #include <algorithm>
 
 #include "csf_elem.cuh"
@@ -32,11 +34,19 @@ __device__ __forceinline__ float at(const char *row, int e, int dtype) {
     return dtype == CSF_BF16 ? __uint_as_float((uint32_t)v << 16) : __half2float(__ushort_as_half(v));
 }
 
-// The largest of the lanes' values, by integers in the floats' order.  (A NaN
-// comes out somewhere; the sum shows it.)
-__device__ __forceinline__ float warp_max(float v) {
-    const int b = __float_as_int(v), m = __reduce_max_sync(0xFFFFFFFFu, b ^ (b >> 31 & 0x7FFFFFFF));
-    return __int_as_float(m ^ (m >> 31 & 0x7FFFFFFF));
+// Over the lanes of a token.
+template <int LANES>
+__device__ __forceinline__ float lanes_sum(float v) {
+#pragma unroll
+    for (int s = LANES / 2; s > 0; s >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, s);
+    return v;
+}
+
+template <int LANES>
+__device__ __forceinline__ float lanes_max(float v) {
+#pragma unroll
+    for (int s = LANES / 2; s > 0; s >>= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, s));
+    return v;
 }
 
 // exp of a difference from the row's largest.  For 16-bit results, whose
@@ -50,11 +60,12 @@ __device__ __forceinline__ float exp_below(float x) {
     return e;
 }
 
-// CHUNKS: 256 experts each; 0: renormalised weights, whose gradient is 0 but
-// for the choices.  WIDE: rows in whole 16-byte pieces, read and written.
-template <int DTYPE, int CHUNKS, bool WIDE>
+// LANES of a token, 16 or 32.  CHUNKS: pieces of 8 experts a lane; 0:
+// renormalised weights, whose gradient is 0 but for the choices.  WIDE: rows
+// in whole 16-byte pieces, read and written.
+template <int DTYPE, int LANES, int CHUNKS, bool WIDE>
 __global__ void __launch_bounds__(kGradThreads) route_grad_kernel(const __grid_constant__ RouteGradParams p) {
-    const int lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & (LANES - 1);
     constexpr bool kAll = CHUNKS > 0;
     // A token's choices and logits are under way while the one before is done.
     struct Token {
@@ -65,22 +76,25 @@ __global__ void __launch_bounds__(kGradThreads) route_grad_kernel(const __grid_c
     auto load = [&](Token &n, int64_t t) {
         n.id = -1;
         n.w = n.d = 0.f;
+        if constexpr (kAll) {
+            // past the row's end: -infinity
+            constexpr uint32_t kOff = DTYPE == CSF_F32 ? 0xFF800000u : DTYPE == CSF_BF16 ? 0xFF80FF80u : 0xFC00FC00u;
+#pragma unroll
+            for (int i = 0; i < CHUNKS; ++i) n.r[i].a = n.r[i].b = make_uint4(kOff, kOff, kOff, kOff);
+        }
         if (t >= p.tokens) return;
         const char *row = p.logits + t * p.logits_stride;
         if constexpr (kAll) {
 #pragma unroll
             for (int i = 0; i < CHUNKS; ++i) {
                 if constexpr (WIDE) {
-                    const uint4 *from = reinterpret_cast<const uint4 *>(row) + (lane + 32 * i) * (DTYPE == CSF_F32 ? 2 : 1);
-                    // past the row's end: -infinity
-                    constexpr uint32_t kOff = DTYPE == CSF_F32 ? 0xFF800000u : DTYPE == CSF_BF16 ? 0xFF80FF80u : 0xFC00FC00u;
-                    n.r[i].a = n.r[i].b = make_uint4(kOff, kOff, kOff, kOff);
-                    if ((lane + 32 * i) * 8 < p.experts) {
+                    const uint4 *from = reinterpret_cast<const uint4 *>(row) + (lane + LANES * i) * (DTYPE == CSF_F32 ? 2 : 1);
+                    if ((lane + LANES * i) * 8 < p.experts) {
                         n.r[i].a = __ldg(from);
                         if (DTYPE == CSF_F32) n.r[i].b = __ldg(from + 1);
                     }
                 } else {
-                    n.r[i] = elem::load(row, (lane + 32 * i) * 8, p.experts, DTYPE, p.wide_logits);
+                    n.r[i] = elem::load(row, (lane + LANES * i) * 8, p.experts, DTYPE, p.wide_logits);
                 }
             }
         }
@@ -89,34 +103,35 @@ __global__ void __launch_bounds__(kGradThreads) route_grad_kernel(const __grid_c
             n.w = __ldg(p.weights + t * p.k + lane), n.d = __ldg(p.dweights + t * p.k + lane);
         }
     };
-    const int64_t step = (int64_t)gridDim.x * (kGradThreads / 32);
-    int64_t t = (int64_t)blockIdx.x * (kGradThreads / 32) + (threadIdx.x >> 5);
+    constexpr int kPerBlock = kGradThreads / LANES;
+    const int64_t step = (int64_t)gridDim.x * kPerBlock;
+    const int nth = threadIdx.x / LANES, first = (threadIdx.x >> 5) * (32 / LANES);      // of the block's, and of the warp's
     Token next;
-    load(next, t);
-    for (; t < p.tokens; t += step) {
+    load(next, (int64_t)blockIdx.x * kPerBlock + nth);
+    for (int64_t t0 = (int64_t)blockIdx.x * kPerBlock; t0 + first < p.tokens; t0 += step) {
+        const int64_t t = t0 + nth;
+        const bool live = t < p.tokens;
         Token n = next;
         load(next, t + step);
         if (n.id < 0 || n.id >= p.experts) n.id = -1, n.w = 0.f, n.d = 0.f;
         // (again, from a cache: where it lies in the registers is not known when this is compiled)
         const float mine = kAll && n.id >= 0 ? at(p.logits + t * p.logits_stride, n.id, DTYPE) : 0.f;
         char *out = p.out + t * p.out_stride;
-        float dot = n.w * n.d;
-#pragma unroll
-        for (int s = 16; s > 0; s >>= 1) dot += __shfl_xor_sync(0xFFFFFFFFu, dot, s);
+        const float dot = lanes_sum<LANES>(n.w * n.d);
         float own = kAll ? n.w * n.d : n.w * (n.d - dot);
         // a choice made twice has both parts
         bool again = false;
         if (p.k <= 8) {
 #pragma unroll
-            for (int j = 1; j < 8; ++j) again |= __shfl_down_sync(0xFFFFFFFFu, n.id, j, 8) == n.id && lane + j < 8;
+            for (int j = 1; j < 8; ++j) again |= __shfl_down_sync(0xFFFFFFFFu, n.id, j, 8) == n.id && (lane & 7) + j < 8;
         } else {
-            for (int j = 0; j < p.k; ++j) again |= __shfl_sync(0xFFFFFFFFu, n.id, j) == n.id && j != lane;
+            for (int j = 0; j < p.k; ++j) again |= __shfl_sync(0xFFFFFFFFu, n.id, j, LANES) == n.id && j != lane;
         }
         if (__any_sync(0xFFFFFFFFu, again && n.id >= 0)) {
             float both = 0.f;
             for (int j = 0; j < p.k; ++j) {
-                const float other = __shfl_sync(0xFFFFFFFFu, own, j);
-                if (__shfl_sync(0xFFFFFFFFu, n.id, j) == n.id) both += other;
+                const float other = __shfl_sync(0xFFFFFFFFu, own, j, LANES);
+                if (__shfl_sync(0xFFFFFFFFu, n.id, j, LANES) == n.id) both += other;
             }
             own = both;
         }
@@ -128,33 +143,32 @@ __global__ void __launch_bounds__(kGradThreads) route_grad_kernel(const __grid_c
                 elem::to_floats(v[i], n.r[i], DTYPE);
 #pragma unroll
                 for (int q = 0; q < 8; ++q) {
-                    if (!WIDE && (lane + 32 * i) * 8 + q >= p.experts) v[i][q] = __int_as_float(0xFF800000);
+                    if (!WIDE && (lane + LANES * i) * 8 + q >= p.experts) v[i][q] = __int_as_float(0xFF800000);
                     most = fmaxf(most, v[i][q]);
                 }
             }
-            most = warp_max(most);
+            most = lanes_max<LANES>(most);
             const bool none = most == __int_as_float(0xFF800000);      // every expert is off: their exponentials are 0
             const float zero = none ? 0.f : most;
 #pragma unroll
             for (int i = 0; i < CHUNKS; ++i)
 #pragma unroll
                 for (int q = 0; q < 8; ++q) sum += v[i][q] = exp_below<DTYPE>(v[i][q] - zero);
-#pragma unroll
-            for (int s = 16; s > 0; s >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, s);
+            sum = lanes_sum<LANES>(sum);
             const float rate = none ? 0.f : -dot / sum;
             own += exp_below<DTYPE>(mine - zero) * rate;
             __syncwarp();      // every lane has read: the row may be written where it lay
 #pragma unroll
             for (int i = 0; i < CHUNKS; ++i) {
-                const int c = (lane + 32 * i) * 8;
-                if (c >= p.experts) break;
+                const int c = (lane + LANES * i) * 8;
+                if (!live || c >= p.experts) break;
 #pragma unroll
                 for (int q = 0; q < 8; ++q) v[i][q] *= rate;
                 elem::store(out, c, p.experts, elem::from_floats(v[i], DTYPE), DTYPE, WIDE || p.wide_out);
             }
         } else {
             const elem::Raw zeros = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
-            for (int c = lane * 8; c < p.experts; c += 256) elem::store(out, c, p.experts, zeros, DTYPE, p.wide_out);
+            for (int c = lane * 8; live && c < p.experts; c += 8 * LANES) elem::store(out, c, p.experts, zeros, DTYPE, p.wide_out);
         }
         __syncwarp();      // the row is written: the choices' places once more
         if (n.id >= 0) {
@@ -165,22 +179,33 @@ __global__ void __launch_bounds__(kGradThreads) route_grad_kernel(const __grid_c
     }
 }
 
-template <int DTYPE, int CHUNKS>
+template <int DTYPE, int LANES, int CHUNKS>
 void launch_chunks(const RouteGradParams &p, cudaStream_t s) {
-    const int64_t blocks = ((int64_t)p.tokens + kGradThreads / 32 - 1) / (kGradThreads / 32);
+    constexpr int kPerBlock = kGradThreads / LANES;
+    const int64_t blocks = ((int64_t)p.tokens + kPerBlock - 1) / kPerBlock;
     const unsigned grid = (unsigned)std::min<int64_t>(blocks, kGradBlocks * (int64_t)std::max(sm_count(), 1));
-    if (CHUNKS > 0 && p.wide_logits && p.wide_out && p.experts % 8 == 0) route_grad_kernel<DTYPE, CHUNKS, true><<<grid, kGradThreads, 0, s>>>(p);
-    else route_grad_kernel<DTYPE, CHUNKS, false><<<grid, kGradThreads, 0, s>>>(p);
+    if (CHUNKS > 0 && p.wide_logits && p.wide_out && p.experts % 8 == 0)
+        route_grad_kernel<DTYPE, LANES, CHUNKS, true><<<grid, kGradThreads, 0, s>>>(p);
+    else route_grad_kernel<DTYPE, LANES, CHUNKS, false><<<grid, kGradThreads, 0, s>>>(p);
 }
 
 template <int DTYPE>
 void launch(const RouteGradParams &p, bool renormalize, cudaStream_t s) {
-    switch (renormalize ? 0 : (p.experts + 255) / 256) {
-        case 0: launch_chunks<DTYPE, 0>(p, s); break;
-        case 1: launch_chunks<DTYPE, 1>(p, s); break;
-        case 2: launch_chunks<DTYPE, 2>(p, s); break;
-        case 3: launch_chunks<DTYPE, 3>(p, s); break;
-        default: launch_chunks<DTYPE, 4>(p, s); break;
+    if (renormalize) return launch_chunks<DTYPE, 32, 0>(p, s);
+    // Two tokens a warp where a half's registers hold a row: what a warp does
+    // once a token it then does for two.
+    if (p.k <= 16 && p.experts <= 384) {
+        switch ((p.experts + 127) / 128) {
+            case 1: return launch_chunks<DTYPE, 16, 1>(p, s);
+            case 2: return launch_chunks<DTYPE, 16, 2>(p, s);
+            default: return launch_chunks<DTYPE, 16, 3>(p, s);
+        }
+    }
+    switch ((p.experts + 255) / 256) {
+        case 1: return launch_chunks<DTYPE, 32, 1>(p, s);
+        case 2: return launch_chunks<DTYPE, 32, 2>(p, s);
+        case 3: return launch_chunks<DTYPE, 32, 3>(p, s);
+        default: return launch_chunks<DTYPE, 32, 4>(p, s);
     }
 }
 

@@ -567,7 +567,7 @@ def test_rows_past_32_bit_offsets(ops):
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("renormalize", [True, False])
 @pytest.mark.parametrize("T,E,k,masked", [(1, 1, 1, False), (1, 512, 8, False), (33, 129, 6, True), (300, 40, 8, True), (50, 1024, 32, False), (9, 700, 3, True),
-                                          (5000, 256, 8, False)])
+                                          (5000, 256, 8, False), (71, 384, 12, True), (6, 100, 16, False), (3, 390, 5, False)])
 def test_route_gradient(ops, T, E, k, masked, renormalize, dtype):
     g = gen(T + E)
     logits = torch.randn(T, E, device="cuda", generator=g)
