@@ -736,7 +736,7 @@ fp8_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constan
                         tc::named_sync(1 + w, 64);
                         m = max(m, __float_as_uint(amax[half ^ 1][32 * w + lane]));
                     }
-                    const float scale = quant::fp8_scale(m), scale_up = quant::fp8_up(scale);
+                    const float scale = quant::fp8_scale(m), scale_up = scale < quant::kLeastWhole ? quant::kWholeUp : 1.f;
                     const quant::Whole whole = quant::fp8_whole(scale * scale_up);
                     const int part = lane & 3, sub = lane >> 2;
 #pragma unroll 1

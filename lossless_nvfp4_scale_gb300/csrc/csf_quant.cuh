@@ -69,17 +69,20 @@ __device__ __forceinline__ uint32_t e2m1x2(float lo, float hi) {
 }
 
 // FP8 scale of a block whose largest magnitude is amax: a normal number, or
-// NaN.
+// NaN.  The quotient by its corrected product, as in over(): 448 is 7 * 2^6, so
+// that the remainder is exact down to the least scale.
 __device__ __forceinline__ float fp8_scale(uint32_t amax_bits) {
     if ((amax_bits >> 23) == 255) return __int_as_float(0x7FFFFFFF);
-    return fmaxf(__fdiv_rn(__uint_as_float(amax_bits), 448.f), 0x1p-126f);
+    constexpr float kInverse = 1.f / 448.f;
+    const float m = __uint_as_float(amax_bits), q = m * kInverse;
+    return fmaxf(fmaf(fmaf(-q, 448.f, m), kInverse, q), 0x1p-126f);
 }
 
-// What FP8 values and their scale are multiplied by before over(), so that its
-// remainders stay normal numbers.
-__device__ __forceinline__ float fp8_up(float scale) { return scale < 0x1p-60f ? 0x1p60f : 1.f; }
+// FP8 values whose scale is smaller, and it, are taken that many times larger
+// before over(), so that its remainders stay normal numbers.
+constexpr float kLeastWhole = 0x1p-60f, kWholeUp = 0x1p60f;
 
-// A scale (times fp8_up) and its inverse, for over().
+// A scale and its inverse, for over().
 __device__ __forceinline__ Whole fp8_whole(float scale) {
     Whole w;
     w.value = scale;
@@ -132,11 +135,18 @@ template <int KIND>
 __device__ __forceinline__ Coded encode8(const float (&y)[8], uint32_t m, float tensor_scale) {
     Coded q;
     if constexpr (KIND == CSF_ROWS_FP8) {
-        const float scale = fp8_scale(m), up = fp8_up(scale);
-        const Whole w = fp8_whole(scale * up);
-        float v[8];
+        const float scale = fp8_scale(m);
+        float v[8], whole = scale;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = over(y[i] * up, w);
+        for (int i = 0; i < 8; ++i) v[i] = y[i];
+        if (scale < kLeastWhole) {
+            whole *= kWholeUp;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] *= kWholeUp;
+        }
+        const Whole w = fp8_whole(whole);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = over(v[i], w);
         q.codes.x = e4m3x2(v[0], v[1]) | e4m3x2(v[2], v[3]) << 16;
         q.codes.y = e4m3x2(v[4], v[5]) | e4m3x2(v[6], v[7]) << 16;
         q.scale = __float_as_uint(scale);

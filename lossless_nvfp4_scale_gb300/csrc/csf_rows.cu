@@ -35,13 +35,22 @@ Span span_of(int32_t tokens, int32_t cols, int least_lanes, int width = 8) {
     s.cols = cols;
     s.chunks = (int32_t)(round_up(cols, 32) / 8);
     const int pieces = s.chunks * 8 / width, rounds = (pieces + kRowThreads - 1) / kRowThreads;
-    int each = (pieces + rounds - 1) / rounds;
+    const int each = (pieces + rounds - 1) / rounds;
     s.lanes = (int32_t)round_up(each, each <= least_lanes ? least_lanes : 32);
     s.per_block = kRowThreads / s.lanes;
     return s;
 }
 
 unsigned blocks_of(const Span &s) { return (unsigned)(((int64_t)s.tokens + s.per_block - 1) / s.per_block); }
+
+// Blocks of a launch whose rows need nothing of one another's columns: where
+// the tokens alone make few, a row's rounds are blocks too (one token of 5120,
+// 8 choices: 5.1 us in one block).
+dim3 grid_of(const Span &s, int width) {
+    const int pieces = s.chunks * 8 / width, rounds = (pieces + s.lanes - 1) / s.lanes;
+    const unsigned blocks = blocks_of(s);
+    return dim3(blocks, (int)blocks < sm_count() ? (unsigned)std::min(rounds, 64) : 1u);
+}
 
 struct DispatchParams {
     Span span;
@@ -75,7 +84,7 @@ __global__ void __launch_bounds__(kRowThreads) dispatch_kernel(const __grid_cons
     const float g = KIND == CSF_ROWS_NVFP4 && p.tensor_scale ? *p.tensor_scale : 1.f;
     const int pieces = p.span.chunks >> 1;       // of 16 columns
     bool bad = false;
-    for (int c0 = 0; c0 < pieces; c0 += p.span.lanes) {
+    for (int c0 = blockIdx.y * p.span.lanes; c0 < pieces; c0 += gridDim.y * p.span.lanes) {
         const int c = c0 + tid;
         elem::Raw r[2];
         quant::Coded q[2];
@@ -161,7 +170,7 @@ __global__ void __launch_bounds__(kRowThreads) combine_kernel(const __grid_const
     bool bad = false;
     Choices ch;
     ch.load(p.slots, p.weights, t * p.k, p.k, p.y_rows, lane, bad);
-    for (int c0 = 0; c0 * 8 < p.span.cols; c0 += p.span.lanes) {
+    for (int c0 = blockIdx.y * p.span.lanes; c0 * 8 < p.span.cols; c0 += gridDim.y * p.span.lanes) {
         const int c = c0 + tid;
         const bool live = c * 8 < p.span.cols;
         elem::Raw res;
@@ -342,7 +351,8 @@ __global__ void __launch_bounds__(kRowThreads) combine_grad_kernel(const __grid_
 
 template <int DTYPE>
 void launch_dispatch(const DispatchParams &p, int kind, cudaStream_t s) {
-    const unsigned grid = blocks_of(p.span), threads = (unsigned)(p.span.lanes * p.span.per_block);
+    const dim3 grid = grid_of(p.span, 16);
+    const unsigned threads = (unsigned)(p.span.lanes * p.span.per_block);
     switch (kind) {
         case kPlain: dispatch_kernel<DTYPE, kPlain><<<grid, threads, 0, s>>>(p); break;
         case CSF_ROWS_NVFP4: dispatch_kernel<DTYPE, CSF_ROWS_NVFP4><<<grid, threads, 0, s>>>(p); break;
@@ -371,7 +381,8 @@ void launch_combine_grad(const CombineGradParams &p, int kind, cudaStream_t s) {
 
 template <int DTYPE>
 void launch_combine(const CombineParams &p, cudaStream_t s) {
-    const unsigned grid = blocks_of(p.span), threads = (unsigned)(p.span.lanes * p.span.per_block);
+    const dim3 grid = grid_of(p.span, 8);
+    const unsigned threads = (unsigned)(p.span.lanes * p.span.per_block);
     if (p.wide_y && p.span.cols % 8 == 0) combine_kernel<DTYPE, true><<<grid, threads, 0, s>>>(p);
     else combine_kernel<DTYPE, false><<<grid, threads, 0, s>>>(p);
 }
