@@ -2,20 +2,39 @@
 // block (csf_fp8_matmul): the kernel.
 //
 // The slots are the M side, 128 to a block of threads, and the weights' output
-// columns the N side.  The 5th-generation tensor cores sum 128 products
-// exactly scaled alike at a time, into tensor memory; eight warps then take
-// each such partial sum out, multiply it with its row's scale times the weight
-// block's and add it up in registers, in 32 bits: lane and register are row
-// and column, so the factor is one number a thread and block.  Meanwhile the next partial sums form in
-// other columns of tensor memory.
+// columns the N side.  The 5th-generation tensor cores form the partial sum of
+// a block of 128 of the depth, whose products are all scaled alike, in tensor
+// memory; eight warps then take it out, multiply it with its row's scale times
+// the weight block's and add it up in registers, in 32 bits.  Lane and
+// register are row and column, so the factor is one number a thread.  Tensor
+// memory holds four partial sums of 128 columns: two steps of the depth are
+// under way while one is taken out.
 //
-// Where slots are many, two neighbouring blocks pair up: 256 slots by 256
-// columns, each block holding its 128 slots and 128 of the columns, which
-// halves what shared memory has to take in per product.  A gated product's
-// tile has 128 gate and the 128 up columns of the same numbers, so that both
-// lie in one thread.  Where tiles are few, a cluster of 2 to 8 blocks shares
-// one: each sums its part of the depth, hands the rows' sums round, and
-// finishes its share of the rows.
+// A tile is 128 slots by 128 or 256 columns; a dense product of many slots
+// pairs two neighbouring blocks for 256 by 256, each holding its 128 slots and
+// half of the columns, which halves what shared memory has to take in and give
+// out per product.  A gated product's tile has 128 gate columns and the 128 up
+// columns of the same numbers.  Where tiles are few, a cluster of 2 to 8
+// blocks shares one: each sums its part of the depth, hands the rows' sums
+// round, and finishes its share of the rows.
+//
+// What bounds it: taking the partial sums out.  A step of 256 columns takes
+// the matrix instructions 0.26 us (0.32 with their copies), the eight warps
+// 0.34 alone, both together 0.42: a load of 64 columns from tensor memory is
+// 160 to 190 cycles under way, twice a step, and 128 sums leave registers for
+// no more in flight.  Measured (2070 MHz):
+//   8191 slots, 5120 x 5120, bfloat16 out           183 us, 2.35 PFLOP/s
+//     with a residual and row weights               205 us
+//   32768 slots on 128 experts, gated 4096 x 2048   412 us to bfloat16, 445 to
+//     FP8: 2.5 tiles of 128 slots an expert of 256, the SiLU
+//   4000 slots on 64 experts, 1600 x 2048 across    51 us, 4.6 TB/s
+//   64 slots on 8 of 128 experts, gated 1024 x 1600 14.5 us: latency
+//   one slot of 2048 x 5120                         10 us: latency
+// What that took: arrivals at another block's barrier without a cluster-wide
+// release (which waited a thousand cycles); waits whose ready path has no
+// taken branch (180 -> 57 cycles); issue code that the whole warp runs, with
+// one lane's predicate on the instructions; partial sums a weight block each;
+// packed multiply-adds; the factors by warps of their own, for the registers.
 //
 //   warp 0      weights, and x rows where slots are rows (TMA, 128-byte swizzle)
 //   warp 1      matrix instructions (the first block's of a pair)
@@ -53,8 +72,8 @@ constexpr uint32_t kTileBytes = 128 * 128;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTurnBytes = kSumWarps * 32 * 128;      // a piece of 32 rows of 128 bytes each
 // Registers of the warps that copy and of those that sum, where a thread holds
-// 128 sums and takes out 64 partial ones: together what the block was launched
-// with.
+// 128 sums and takes out 64 or 32 partial ones: together what the block was
+// launched with.
 __host__ __device__ constexpr int launch_regs(bool rows) { return rows ? 128 : 168; }
 template <bool ROWS> constexpr int kCopyRegs = ROWS ? 48 : 56;
 template <bool ROWS> constexpr int kSumRegs = ROWS ? 208 : 224;
@@ -165,8 +184,8 @@ __device__ __forceinline__ void add_bias8(const Params &p, float *y, int e, int 
 }
 
 // What comes out: 16-bit rows, any plain rows, FP8 rows, 16-bit rows with a
-// 16-bit residual (both in whole 16-byte pieces).  Kernels of their own, since what one holds in registers another
-// would spill.
+// 16-bit residual (both in whole 16-byte pieces).  Kernels of their own, since
+// what one holds in registers another would spill.
 enum Mode { kHalves = 0, kPlain = 1, kQuant = 2, kHalvesSum = 3 };
 
 // CTAS: blocks of a pair.  AT: 128-column weight blocks per tile.  ROWS: slot

@@ -159,16 +159,12 @@ __device__ __forceinline__ void bar_arrive_cluster(uint32_t bar) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
-// The same without waiting until the whole cluster sees this thread's writes:
-// for what only tells that tensor memory or a stage has been read, or that
-// copies which were waited for have been handed to the asynchronous proxy.
-// (The waiting took a thousand cycles an arrival.)
-__device__ __forceinline__ void bar_arrive_remote(uint32_t bar) {
-    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-
 // One lane's arrival, of this block's barrier or (REMOTE) at a cluster
 // address, without a branch that the warp would have to come together after.
+// The remote one does not wait until the whole cluster sees this thread's
+// writes, which took a thousand cycles: it tells that tensor memory has been
+// read, that copies which were waited for are the asynchronous proxy's, or
+// that factors are in this block's own memory.
 template <bool REMOTE>
 __device__ __forceinline__ void bar_arrive_if(uint32_t bar, bool is) {
     if constexpr (REMOTE)
@@ -501,13 +497,6 @@ __device__ __forceinline__ bool bar_try_if(uint32_t bar, uint32_t parity, bool i
 __device__ __forceinline__ void named_sync(uint32_t id, uint32_t threads) {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
-
-template <int LEFT>
-__device__ __forceinline__ void cp_async_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory");
-}
-
-__device__ __forceinline__ void cp_async_group() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 
 __device__ __forceinline__ void store_cluster4(uint32_t dst, float a, float b, float c, float d) {
     asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "f"(a), "f"(b), "f"(c), "f"(d) : "memory");
