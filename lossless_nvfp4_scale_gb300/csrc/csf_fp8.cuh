@@ -469,12 +469,14 @@ fp8_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constan
             __syncwarp();
             tc::bar_arrive_if<CTAS == 2>(release0 + 8 * set, lane == 0);
         };
+        auto meet = [&]() { tc::named_sync(1 + w, 64); };      // warps w and w + 4
         uint32_t count = 0;              // partial sums so far
         // where the partial sum with that number is: its set, and the parity of its round
         auto set_of = [&](uint32_t i) { return AT == 2 ? (i & 1) * 2 + half : i & 3; };
         bool ok = true;
+        uint32_t tile = unit;
 #pragma unroll 1
-        for (uint32_t tile = unit, nth = 0; tile < total; tile += units, ++nth) {
+        for (uint32_t nth = 0; tile < total; tile += units, ++nth) {
             const Tile t = mm::find_tile(p, first, slot0, tile, lane);
             const int n = rows_of(t, pair_rank) - 32 * w;       // this warp's rows, if any
             if (MODE != kHalves && !SPLIT && (MODE == kHalvesSum || p.residual) && lane < n) {
@@ -560,7 +562,7 @@ fp8_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constan
                 const uint32_t gate = gated ? lanes + (set & 2) * 128 + 64 * half : own, up = gate + 128;
                 if (gated) {
                     tc::fence_before();
-                    tc::named_sync(1 + w, 64);
+                    meet();
                     tc::fence_after();
                 }
                 const bool live = lane < n;
@@ -752,7 +754,7 @@ fp8_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constan
                         // the largest magnitude of a block of 128 columns comes from both warps of these rows
                         float (&amax)[2][128] = sh.amax[nth & 1];
                         amax[half][32 * w + lane] = __uint_as_float(m);
-                        tc::named_sync(1 + w, 64);
+                        meet();
                         m = max(m, __float_as_uint(amax[half ^ 1][32 * w + lane]));
                     }
                     const float scale = quant::fp8_scale(m), scale_up = scale < quant::kLeastWhole ? quant::kWholeUp : 1.f;
@@ -792,9 +794,17 @@ fp8_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constan
                             for (int i = n_blocks; i & 3; ++i) scales[i] = 0.f;
                     }
                 }
-                if (gated) tc::named_sync(1 + w, 64);      // the other warp has read this one's block, too
+                if (gated) meet();      // the other warp has read this one's block, too
             }
             release(set);
+        }
+        if (!SPLIT && !ok && ((AT == 2 && p.gated) || (MODE == kQuant && AT == 1))) {
+            // A wait gave up.  The other warp of these rows may not have: it is
+            // met as often as the tiles that are left have it do.
+            const int meetings = AT == 1 ? 1 : MODE == kQuant ? 3 : 2;
+            for (; tile < total; tile += units)
+                if (rows_of(mm::find_tile(p, first, slot0, tile, lane), pair_rank) > 32 * w)
+                    for (int i = 0; i < meetings; ++i) meet();
         }
     }
 
