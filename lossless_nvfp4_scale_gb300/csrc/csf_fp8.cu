@@ -137,8 +137,14 @@ extern "C" csf_status csf_fp8_matmul(const csf_fp8_matmul_args *a, void *stream)
         const int64_t few = (int64_t)((p.F + 127) / 128) * slot_tiles;
         while (p.split < kMaxSplit && few * p.split * 2 <= (p.split == 1 ? sms : sms / 2) && p.blocks >= 4 * p.split) p.split *= 2;
         if (p.split > 1) {
+            const int whole = shape;
             shape = a->gated ? kTwoShared : kOneShared;      // (fewer columns, so that more blocks have some)
             smem = lay();
+            if (p.stages < 2) {      // many experts' prefixes leave too little for the sums handed round
+                shape = whole;
+                p.split = 1;
+                smem = lay();
+            }
         }
     }
     if (p.stages < 2) return CSF_ERR_UNSUPPORTED;

@@ -323,6 +323,37 @@ def test_one_expert_of_8192(ops):
     p.check(ops.fp8_matmul(p.x, w, ws, expert_start=start, out=torch.float32))
 
 
+def test_gated_product_of_few_slots_on_8192_experts(ops):
+    """Prefixes of many experts leave no room for clusters that share the depth."""
+    E = 8192
+    p = Problem(ops, [2], 256, 1024, seed=10)
+    w, ws = p.w.view(torch.uint8).expand(E, -1, -1).contiguous(), p.ws.expand(E, -1, -1).contiguous()
+    start = torch.zeros(E + 1, dtype=torch.int32, device="cuda")
+    start[8192:] = 2
+    for out in (torch.float32, ops.FP8):
+        p.check(ops.fp8_matmul(p.x, w, ws, expert_start=start, out=out, gated=True, activation="silu"), act="silu", gated=True)
+
+
+def test_many_choices_a_token(ops):
+    T, k, H = 5, 70, 200
+    g = gen(6)
+    slots = torch.randperm(T * k, device="cuda", generator=g).int().view(T, k)
+    slots[1, 3:60], slots[4] = -1, -1
+    y, w = torch.randn(T * k, H, device="cuda", generator=g), torch.randn(T, k, device="cuda", generator=g)
+    go = torch.randn(T, H, device="cuda", generator=g)
+    want = combine64(y.double(), slots, w.double(), None)
+    close(ops.combine(y, slots, w), want, combine64(y.double().abs(), slots, w.double().abs(), None) * k * 2.0 ** -24)
+    dy, dw = ops.combine_grad(go, y, slots, w)
+    on = slots >= 0
+    rows = y.double()[slots.clamp(min=0).long()]
+    want = torch.where(on, (go.double()[:, None] * rows).sum(2), 0)
+    close(dw, want, (go.double().abs()[:, None] * rows.abs()).sum(2) * 24 * 2.0 ** -24)
+    want = (w.double()[..., None] * go.double()[:, None])[on]
+    close(dy[slots[on].long()], want, want.abs() * 2.0 ** -24)
+    out = ops.dispatch(go, slots)
+    assert torch.equal(out[slots[on].long()], go[:, None].expand(-1, k, -1)[on])
+
+
 def test_weights_past_32_bit_offsets(ops):
     E, N, K = 3, 40000, 20000                         # 2.4e9 bytes of weights
     x = ops.quantize(torch.randn(5, K, device="cuda"), ops.FP8)
