@@ -218,6 +218,7 @@ def test_ragged_quantized_outputs(ops, N, counts):
     ([700], 2560, 256, True, False),
     ([130] * 12, 2560, 256, False, False),           # 256 columns a block
     ([100] * 16, 640, 2560, False, True),
+    ([100] * 40, 256, 2048, False, True),
     ([128, 1, 129, 0] * 10, 1024, 256, True, False),
     ([140] * 3, 256, 384, False, False),             # 128 columns a block
 ])
