@@ -111,7 +111,9 @@ extern "C" csf_status csf_fp8_matmul(const csf_fp8_matmul_args *a, void *stream)
     const int wide_step = a->gated ? 128 : 256, units = std::max(sms, 2);
     const double pair = rounds(tiles_of(256, wide_step), units / 2), two = 1.04 * rounds(tiles_of(128, wide_step), units);
     const double one = a->gated ? 2 * two : 0.65 * rounds(tiles_of(128, 128), units);
-    int shape = one <= two && one <= pair ? kOne : two <= pair ? kTwo : kPair;
+    // Rows through an index take no pair: its second block's copies would be handed to the block that issues, a release
+    // to the cluster a step (8191 slots of 5120 x 5120: 315 us, two blocks 229).
+    int shape = one <= two && (one <= pair || a->rows) ? kOne : two <= pair || a->rows ? kTwo : kPair;
     auto tiles = [&](int nt) { return (int64_t)p.row_tiles * (busy + a->slots / nt); };      // at most
     auto lay = [&]() {
         const bool wide = shape == kPair || shape == kTwo || shape == kTwoShared;

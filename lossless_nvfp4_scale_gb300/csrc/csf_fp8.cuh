@@ -23,21 +23,24 @@
 // 0.34 alone, both together 0.42: a load of 64 columns from tensor memory is
 // 160 to 190 cycles under way, twice a step, and 128 sums leave registers for
 // no more in flight.  Measured (2070 MHz):
-//   8191 slots, 5120 x 5120, bfloat16 out           183 us, 2.35 PFLOP/s
-//     with a residual and row weights               205 us
+//   8191 slots, 5120 x 5120, bfloat16 out           191 us, 2.25 PFLOP/s
+//     with a residual and row weights               215 us
 //   32768 slots on 128 experts, gated 4096 x 2048   412 us to bfloat16, 445 to
 //     FP8: 2.5 tiles of 128 slots an expert of 256, the SiLU
 //   4000 slots on 64 experts, 1600 x 2048 across    51 us, 4.6 TB/s
 //   64 slots on 8 of 128 experts, gated 1024 x 1600 14.5 us: latency
 //   one slot of 2048 x 5120                         10 us: latency
-// What that took: arrivals at another block's barrier without a cluster-wide
-// release (which waited a thousand cycles); waits whose ready path has no
-// taken branch (180 -> 57 cycles); issue code that the whole warp runs, with
-// one lane's predicate on the instructions; partial sums a weight block each;
-// packed multiply-adds; the factors by warps of their own, for the registers.
+// What that took: arrivals at another block's barrier that order no memory (a
+// cluster-wide release waited a thousand cycles), so that what passes between
+// a pair's blocks is tensor memory alone, between tcgen05 fences; waits whose
+// ready path has no taken branch (180 -> 57 cycles); issue code that the whole
+// warp runs, with one lane's predicate on the instructions; partial sums a
+// weight block each; packed multiply-adds; the factors by warps of their own,
+// for the registers.
 //
 //   warp 0      weights, and x rows where slots are rows (TMA, 128-byte swizzle)
-//   warp 1      matrix instructions (the first block's of a pair)
+//   warp 1      matrix instructions; in a pair's second block, whose first one
+//               issues for both, the factors handed on
 //   warps 2, 3  the factors, a step's 128 rows at a time, into shared memory
 //   warps 4-7   x rows through an index, where there is one: 16-byte
 //               asynchronous copies, swizzled as TMA would
@@ -80,9 +83,12 @@ template <bool ROWS> constexpr int kSumRegs = ROWS ? 208 : 224;
 static_assert(256 * kCopyRegs<true> + 256 * kSumRegs<true> == 512 * launch_regs(true), "registers of a block");
 static_assert(128 * kCopyRegs<false> + 256 * kSumRegs<false> == 384 * launch_regs(false), "registers of a block");
 // Steps whose factors are held: those of the ring's stages, and of partial
-// sums that are formed (4 steps at most) or taken out.
-constexpr int kFactorSteps = 16;
+// sums that are formed (4 steps at most) or taken out.  In a pair's second
+// block the summing warps say of each group of steps that they have read it (a
+// word of every step cost 4% of a dense product).
+constexpr int kFactorSteps = 16, kFactorGroup = 8;
 static_assert(kFactorSteps >= kMaxStages + 5, "factors are written when their stage is free");
+static_assert(kFactorSteps % kFactorGroup == 0, "groups are whole");
 
 struct Params {
     const uint8_t *x_codes, *x_scales;
@@ -119,6 +125,7 @@ struct Params {
 
 struct Shared {
     uint64_t full[kMaxStages], empty[kMaxStages], acc_full[4], acc_empty[4];
+    uint64_t fac_full[kFactorSteps], fac_empty[kFactorSteps / kFactorGroup];      // of a pair's second block
     uint32_t tmem, abort, warp_sum[16];
     float amax[2][2][128];       // by tile, half and row
 };
@@ -194,13 +201,14 @@ enum Mode { kHalves = 0, kPlain = 1, kQuant = 2, kHalvesSum = 3 };
 template <int CTAS, int AT, bool ROWS, bool SPLIT, int MODE>
 __global__ void __launch_bounds__(threads_of(ROWS), 1)
 fp8_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap, const __grid_constant__ Params p) {
-    static_assert(CTAS == 1 || (AT == 2 && !SPLIT), "a pair has 256 columns and all of the depth");
+    static_assert(CTAS == 1 || (AT == 2 && !SPLIT && !ROWS), "a pair has 256 columns, all of the depth and rows in order");
     extern __shared__ __align__(1024) uint8_t dyn[];
     __shared__ Shared sh;
     __shared__ float factors[kFactorSteps][AT][128];        // a row's scale times the weight block's
     constexpr int kThreads = threads_of(ROWS), kFirstSumWarp = ROWS ? 8 : 4;
     constexpr int kSets = (int)kTmemCols / 128;             // partial sums of 128 columns under way
     constexpr uint32_t kPart = kTileBytes / CTAS;           // bytes of a weight block that this block of threads holds
+    constexpr bool kFar = CTAS == 2;                        // the other block's copies and warps arrive at full and acc_empty
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t ring0 = (tc::smem_u32(dyn) + 1023u) & ~1023u;
     uint8_t *after_ring = dyn + (ring0 - tc::smem_u32(dyn)) + (size_t)p.stages * p.stage_bytes;
@@ -212,18 +220,22 @@ fp8_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constan
     const int pair_rank = CTAS == 2 ? (int)rank : 0;
     const uint32_t full0 = tc::smem_u32(sh.full), empty0 = tc::smem_u32(sh.empty);
     const uint32_t accf0 = tc::smem_u32(sh.acc_full), acce0 = tc::smem_u32(sh.acc_empty);
+    const uint32_t facf0 = tc::smem_u32(sh.fac_full), face0 = tc::smem_u32(sh.fac_empty);
+    const bool second = CTAS == 2 && rank == 1;
 
     if (tid == 0) {
         for (int i = 0; i < p.stages; ++i) {
-            // the weights; the factors of both blocks; the copying lanes and a pair's other block's copies (that
-            // block counts only its lanes)
-            tc::bar_init(full0 + 8 * i, pair_rank == 1 ? 32 * kXWarps : 1 + kFactorWarps * CTAS + (ROWS ? 32 * kXWarps + CTAS - 1 : 0));
+            // the weights, the factors, the copying lanes
+            tc::bar_init(full0 + 8 * i, 1 + kFactorWarps + (ROWS ? 32 * kXWarps : 0));
             tc::bar_init(empty0 + 8 * i, 1);
         }
         for (int i = 0; i < kSets; ++i) {
-            tc::bar_init(accf0 + 8 * i, 1);
+            // (a pair's second block: its factors, too)
+            tc::bar_init(accf0 + 8 * i, second ? 2 : 1);
             tc::bar_init(acce0 + 8 * i, kSumWarps / AT * CTAS);
         }
+        for (int i = 0; second && i < kFactorSteps; ++i) tc::bar_init(facf0 + 8 * i, kFactorWarps);
+        for (int i = 0; second && i < kFactorSteps / kFactorGroup; ++i) tc::bar_init(face0 + 8 * i, kSumWarps);
         sh.abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -303,10 +315,10 @@ fp8_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constan
                     for (int k = k0; k < k1; ++k, ++count, ring.next(p.stages)) {
                         const uint32_t set = AT == 2 ? (count & 1) * 2 : count & 3, parity = ~(count >> (AT == 2 ? 1 : 2)) & 1;
                         const uint32_t acce = acce0 + 8 * set, accf = accf0 + 8 * set, full = full0 + 8 * ring.s;
-                        bool here = tc::bar_try(full, ring.parity);
-                        here &= tc::bar_try(acce, parity);
+                        bool here = tc::bar_try_of<kFar>(full, ring.parity);
+                        here &= tc::bar_try_of<kFar>(acce, parity);
                         if (!__all_sync(0xFFFFFFFFu, here)) {
-                            ok = __all_sync(0xFFFFFFFFu, tc::bar_wait_on(full, ring.parity, abort) && tc::bar_wait_on(acce, parity, abort));
+                            ok = __all_sync(0xFFFFFFFFu, tc::bar_wait_on<kFar>(full, ring.parity, abort) && tc::bar_wait_on<kFar>(acce, parity, abort));
                             if (!ok) break;
                         }
                         tc::fence_after();
@@ -314,8 +326,8 @@ fp8_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constan
                         const uint32_t at = ring.s * stage, a_lo = (uint32_t)a0 + at, b_lo = (uint32_t)b0 + at, d = tmem + set * 128;
                         tc::mma_f8_128<CTAS>(one, d, a_lo, a_hi, b_lo, b_hi, b_step, idesc, accf);
                         if constexpr (AT == 2) {
-                            if (!__all_sync(0xFFFFFFFFu, tc::bar_try(acce + 8, parity))) {
-                                ok = __all_sync(0xFFFFFFFFu, tc::bar_wait_on(acce + 8, parity, abort));
+                            if (!__all_sync(0xFFFFFFFFu, tc::bar_try_of<kFar>(acce + 8, parity))) {
+                                ok = __all_sync(0xFFFFFFFFu, tc::bar_wait_on<kFar>(acce + 8, parity, abort));
                                 if (!ok) break;
                             }
                             tc::fence_after();
@@ -324,19 +336,22 @@ fp8_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constan
                         tc::commit_if<CTAS>(one, empty0 + 8 * ring.s);
                     }
                 }
-            } else if constexpr (ROWS) {
-                // the other block: x copies that have landed, handed on
-                const uint32_t to = tc::in_block(full0, 0);
-                Ring ring;
+            } else {
+                // A pair's second block.  The first one issues for both and says nothing of this one's shared memory, so
+                // that factors go from warp to warp of this block, counted with the partial sums that they are for.
+                uint32_t count = 0;
                 bool ok = true;
 #pragma unroll 1
                 for (uint32_t tile = unit; ok && tile < total; tile += units) {
 #pragma unroll 1
-                    for (int k = k0; k < k1; ++k, ring.next(p.stages)) {
-                        ok = __all_sync(0xFFFFFFFFu, tc::bar_wait_ready(full0 + 8 * ring.s, ring.parity, abort));
+                    for (int k = k0; k < k1; ++k, ++count) {
+                        const uint32_t accf = accf0 + 8 * ((count & 1) * 2), parity = ~(count >> 1) & 1;
+                        // the factors, and that the set's partial sums before have been counted
+                        ok = __all_sync(0xFFFFFFFFu, tc::bar_wait_ready(facf0 + 8 * (count % kFactorSteps), count / kFactorSteps & 1, abort) &&
+                                                         tc::bar_wait_ready(accf, parity, abort) && tc::bar_wait_ready(accf + 8, parity, abort));
                         if (!ok) break;
-                        tc::fence_async_proxy();
-                        tc::bar_arrive_if<true>(to + 8 * ring.s, one);
+                        tc::bar_arrive_if<false>(accf, one);
+                        tc::bar_arrive_if<false>(accf + 8, one);
                     }
                 }
             }
@@ -345,7 +360,6 @@ fp8_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constan
             // Two rows a lane; a row's scales of 4 blocks and of the next 4, and of each weight block a lane's block
             // of 32 and of the next 32.
             const int r0 = 64 * (warp - kFirstFactorWarp) + lane, groups = (p.blocks + 3) >> 2;
-            const uint32_t full_at = CTAS == 2 ? tc::in_block(full0, 0) : full0;
             uint32_t count = 0;
             bool ok = true, bad_row = false;
             Ring ring;
@@ -380,8 +394,10 @@ fp8_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constan
 #pragma unroll 1
                 for (int k = k0; k < k1; ++k, ++count, ring.next(p.stages)) {
                     const int q = k & 3, i = (k - k0) & 31;
-                    float *at = &factors[count % kFactorSteps][0][r0];
-                    ok = __all_sync(0xFFFFFFFFu, tc::bar_wait_ready(empty0 + 8 * ring.s, ring.parity ^ 1u, abort));
+                    const uint32_t step = count % kFactorSteps;
+                    float *at = &factors[step][0][r0];
+                    ok = __all_sync(0xFFFFFFFFu, second ? tc::bar_wait_ready(face0 + 8 * (step / kFactorGroup), ~(count / kFactorSteps) & 1, abort)
+                                                        : tc::bar_wait_ready(empty0 + 8 * ring.s, ring.parity ^ 1u, abort));
                     if (!ok) break;
 #pragma unroll
                     for (int a = 0; a < AT; ++a) {
@@ -390,9 +406,8 @@ fp8_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constan
                         for (int j = 0; j < 2; ++j)
                             at[a * 128 + 32 * j] = w * (q < 2 ? (q == 0 ? x0[j].x : x0[j].y) : (q == 2 ? x0[j].z : x0[j].w));
                     }
-                    __threadfence_block();
                     __syncwarp();
-                    tc::bar_arrive_if<CTAS == 2>(full_at + 8 * ring.s, lane == 0);
+                    tc::bar_arrive_if<false>(second ? facf0 + 8 * step : full0 + 8 * ring.s, lane == 0);
                     if (q == 3) {
 #pragma unroll
                         for (int j = 0; j < 2; ++j) {
@@ -421,13 +436,13 @@ fp8_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constan
 #pragma unroll 1
             for (uint32_t tile = unit; ok && tile < total; tile += units) {
                 const Tile t = mm::find_tile(p, first, slot0, tile, lane);
-                const int n = rows_of(t, pair_rank), copies = (n + 15) >> 4;
+                const int n = t.n, copies = (n + 15) >> 4;
                 const uint8_t *src[8];
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     src[j] = p.x_codes;
                     if (j < copies) {
-                        const int32_t v = __ldg(p.rows + (int64_t)t.slot + 128 * pair_rank + min(16 * j + (int)row0, n - 1));
+                        const int32_t v = __ldg(p.rows + (int64_t)t.slot + min(16 * j + (int)row0, n - 1));
                         src[j] += (v < 0 || v >= p.x_rows ? 0 : v) * p.x_code_stride;
                     }
                     src[j] += k0 * 128 + 16 * piece;
@@ -490,37 +505,45 @@ fp8_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constan
 #pragma unroll
             for (int i = 0; i < kCols / 2; ++i) sum[i] = 0;
             bool there = false;          // the next partial sums: asked for while these come out of tensor memory
+            int k = k0;
+            do {
+                const int stop = CTAS == 1 ? k1 : min(k1, k + kFactorGroup - (int)(count % kFactorGroup));
 #pragma unroll 1
-            for (int k = k0; k < k1; ++k, ++count) {
-                const uint32_t set = set_of(count), next = set_of(count + 1);
-                constexpr int kRound = AT == 2 ? 1 : 2;
-                if (!__any_sync(0xFFFFFFFFu, there)) {
-                    ok = __all_sync(0xFFFFFFFFu, tc::bar_wait_here(accf0 + 8 * set, (count >> kRound) & 1, abort));
-                    if (!ok) break;
-                }
-                tc::fence_after();
-                const bool last = k + 1 == k1, keep = last && !SPLIT;        // the whole sums go back there
-                there = false;
-                if (n > 0) {
-                    const uint32_t at = lanes + set * 128 + (AT == 2 ? 0 : col0);
-                    uint64_t factor = 0;
-#pragma unroll
-                    for (int c = 0; c < kCols; c += kTaken) {
-                        uint32_t v[kTaken / 16][16];
-#pragma unroll
-                        for (int i = 0; i < kTaken / 16; ++i) tc::tmem_load(at + c + 16 * i, v[i]);
-                        if (c == 0) factor = tc::twice(factors[count % kFactorSteps][AT == 2 ? half : 0][32 * w + lane]);
-                        if (c + kTaken >= kCols) there = tc::bar_try_if(accf0 + 8 * next, ((count + 1) >> kRound) & 1, lane == 0 && !last);
-                        tc::wait_ld();
-                        if (c + kTaken >= kCols && !keep) release(set);
-#pragma unroll
-                        for (int j = 0; j < kTaken / 2; ++j)
-                            if (c / 2 + j < kCols / 2) tc::fma2_after(sum[c / 2 + j], v[j >> 3][2 * (j & 7)], v[j >> 3][2 * (j & 7) + 1], factor);
+                for (; k < stop; ++k, ++count) {
+                    const uint32_t set = set_of(count), next = set_of(count + 1);
+                    constexpr int kRound = AT == 2 ? 1 : 2;
+                    if (!__any_sync(0xFFFFFFFFu, there)) {
+                        ok = __all_sync(0xFFFFFFFFu, tc::bar_wait_here(accf0 + 8 * set, (count >> kRound) & 1, abort));
+                        if (!ok) break;
                     }
-                } else if (!keep) {
-                    release(set);
+                    tc::fence_after();
+                    const bool last = k + 1 == k1, keep = last && !SPLIT;        // the whole sums go back there
+                    there = false;
+                    if (n > 0) {
+                        const uint32_t at = lanes + set * 128 + (AT == 2 ? 0 : col0);
+                        uint64_t factor = 0;
+#pragma unroll
+                        for (int c = 0; c < kCols; c += kTaken) {
+                            uint32_t v[kTaken / 16][16];
+#pragma unroll
+                            for (int i = 0; i < kTaken / 16; ++i) tc::tmem_load(at + c + 16 * i, v[i]);
+                            if (c == 0) factor = tc::twice(factors[count % kFactorSteps][AT == 2 ? half : 0][32 * w + lane]);
+                            if (c + kTaken >= kCols) there = tc::bar_try_if(accf0 + 8 * next, ((count + 1) >> kRound) & 1, lane == 0 && !last);
+                            tc::wait_ld();
+                            if (c + kTaken >= kCols && !keep) release(set);
+#pragma unroll
+                            for (int j = 0; j < kTaken / 2; ++j)
+                                if (c / 2 + j < kCols / 2) tc::fma2_after(sum[c / 2 + j], v[j >> 3][2 * (j & 7)], v[j >> 3][2 * (j & 7) + 1], factor);
+                        }
+                    } else if (!keep) {
+                        release(set);
+                    }
                 }
-            }
+                if (CTAS == 2) {      // a group of factors has been read
+                    __syncwarp();
+                    tc::bar_arrive_if<false>(face0 + 8 * ((count / kFactorGroup - 1) % (kFactorSteps / kFactorGroup)), second && ok && lane == 0 && count % kFactorGroup == 0);
+                }
+            } while (CTAS == 2 && ok && k < k1);
             if (!ok) break;
             if constexpr (SPLIT) {
                 // a row's sums to the block that finishes it
@@ -865,7 +888,7 @@ Kernel pick(int shape) {
     // where the depth is shared, what comes out is asked at run time
     constexpr int kAny = MODE == kQuant ? kQuant : kPlain;
     switch (shape) {
-        case kPair: return fp8_matmul_kernel<2, 2, ROWS, false, MODE>;
+        case kPair: return ROWS ? nullptr : fp8_matmul_kernel<2, 2, false, false, MODE>;
         case kOne: return fp8_matmul_kernel<1, 1, ROWS, false, MODE>;
         case kTwo: return fp8_matmul_kernel<1, 2, ROWS, false, MODE>;
         case kOneShared: return fp8_matmul_kernel<1, 1, ROWS, true, kAny>;

@@ -97,8 +97,14 @@ __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile
 // The same with nothing but the barrier's answer in the way of a phase that
 // is there already: the loop above took 180 cycles then, in a warp alone on
 // its scheduler, and this takes 57.
+template <bool CLUSTER = false>
 static __device__ __noinline__ bool bar_wait_on(uint32_t bar, uint32_t parity, volatile uint32_t *abort) {
-    return bar_wait(bar, parity, abort);
+    return bar_wait<CLUSTER>(bar, parity, abort);
+}
+
+template <bool CLUSTER>
+__device__ __forceinline__ bool bar_try_of(uint32_t bar, uint32_t parity) {
+    return CLUSTER ? bar_try_cluster(bar, parity) : bar_try(bar, parity);
 }
 
 __device__ __forceinline__ bool bar_wait_ready(uint32_t bar, uint32_t parity, volatile uint32_t *abort) {
@@ -161,10 +167,9 @@ __device__ __forceinline__ void bar_arrive_cluster(uint32_t bar) {
 
 // One lane's arrival, of this block's barrier or (REMOTE) at a cluster
 // address, without a branch that the warp would have to come together after.
-// The remote one does not wait until the whole cluster sees this thread's
-// writes, which took a thousand cycles: it tells that tensor memory has been
-// read, that copies which were waited for are the asynchronous proxy's, or
-// that factors are in this block's own memory.
+// The remote one orders no memory (a release to the cluster took a thousand
+// cycles): it stands between tcgen05 fences, and tells that tensor memory has
+// been read.
 template <bool REMOTE>
 __device__ __forceinline__ void bar_arrive_if(uint32_t bar, bool is) {
     if constexpr (REMOTE)
