@@ -38,7 +38,7 @@ def _inputs():
               os.path.join(INCLUDE, "csf.h"), os.path.join(INCLUDE, "csf_tile.cuh"),
               os.path.join(CSRC, "csf_quant.cuh"), os.path.join(CSRC, "csf_tc.cuh"),
               os.path.join(CSRC, "csf_experts.cuh"), os.path.join(INCLUDE, "csf_ops.h"),
-              os.path.join(CSRC, "csf_elem.cuh"), os.path.join(CSRC, "csf_fp8.cuh"),
+              os.path.join(CSRC, "csf_elem.cuh"), os.path.join(CSRC, "csf_fp8.cuh"), os.path.join(CSRC, "csf_fp8_plan.h"),
               os.path.join(CSRC, "csf_grouped.cuh"), os.path.join(CSRC, "csf_host.cuh"), os.path.join(INCLUDE, "csf_layer.h")]
     return files
 

@@ -97,63 +97,18 @@ extern "C" csf_status csf_fp8_matmul(const csf_fp8_matmul_args *a, void *stream)
     }
 
     const int sms = sm_count();
-    const int64_t busy = std::min<int64_t>(E, a->slots);      // experts with slots, at most
-    // A tile's shape by the rounds of tiles that it takes, each as long as
-    // measured with 5120 columns and depth (pair 1, two blocks 1.04, one 0.65).
-    // Experts' last slot tiles are half full on average.  512 / 8191 slots of a
-    // dense 5120 x 5120: one block 38 / 246 us, two 31 / 193, a pair 29 / 183;
-    // 128 experts of 256 slots, gated 4096 x 2048: two blocks 455, a pair 539.
-    auto tiles_of = [&](int nt, int step) {
-        const int64_t rows = E == 1 ? (a->slots + nt - 1) / nt : std::max(busy, busy / 2 + a->slots / nt);
-        return rows * ((p.F + step - 1) / step);
-    };
-    auto rounds = [&](int64_t t, int units) { return (double)((t + units - 1) / units); };
-    const int wide_step = a->gated ? 128 : 256, units = std::max(sms, 2);
-    const double pair = rounds(tiles_of(256, wide_step), units / 2), two = 1.04 * rounds(tiles_of(128, wide_step), units);
-    const double one = a->gated ? 2 * two : 0.65 * rounds(tiles_of(128, 128), units);
-    // Rows through an index take no pair: its second block's copies would be handed to the block that issues, a release
-    // to the cluster a step (8191 slots of 5120 x 5120: 315 us, two blocks 229).
-    int shape = one <= two && (one <= pair || a->rows) ? kOne : two <= pair || a->rows ? kTwo : kPair;
-    auto tiles = [&](int nt) { return (int64_t)p.row_tiles * (busy + a->slots / nt); };      // at most
-    auto lay = [&]() {
-        const bool wide = shape == kPair || shape == kTwo || shape == kTwoShared;
-        p.tile_step = wide && !a->gated ? 256 : 128;
-        p.second = a->gated ? N / 2 : 128;
-        p.row_tiles = (p.F + p.tile_step - 1) / p.tile_step;
-        p.row_tiles_magic = (uint32_t)((1ull << 32) / (uint32_t)p.row_tiles + 1);
-        p.nt = shape == kPair ? 256 : shape >= kOneShared ? kSplitSlots : 128;
-        p.stage_bytes = kTileBytes * (shape == kTwo || shape == kTwoShared ? 3 : 2);
-        const int64_t region = shape >= kOneShared ? (int64_t)kSplitSlots * 512 * (shape == kTwoShared ? 2 : 1) : kTurnBytes;
-        const int64_t fixed = 1024 + region + 8 * ((int64_t)E + 1) + 16, held = (int64_t)round_up(sizeof(Shared) + kFactorSteps * 512 * (wide ? 2 : 1), 1024);
-        p.stages = (int32_t)std::min<int64_t>(kMaxStages, (kSmemLimit - held - fixed) / p.stage_bytes);
-        return (int64_t)fixed + p.stages * (int64_t)p.stage_bytes;
-    };
-    p.split = 1;
-    int64_t smem = lay();
-    if (shape != kPair) {
-        // Few tiles: clusters share their depth.  Clusters of half the SMs' blocks
-        // are placed at once, larger ones than pairs of more in turns: one slot of
-        // 2048 x 5120 takes 14.5 us in 16 clusters of 8 and 9.3 in 16 of 4, of
-        // 5120 x 5120 15.4 in 40 blocks and 12.3 in 40 pairs.
-        const int64_t slot_tiles = E == 1 ? (a->slots + kSplitSlots - 1) / kSplitSlots : busy + a->slots / kSplitSlots;
-        const int64_t few = (int64_t)((p.F + 127) / 128) * slot_tiles;
-        while (p.split < kMaxSplit && few * p.split * 2 <= (p.split == 1 ? sms : sms / 2) && p.blocks >= 4 * p.split) p.split *= 2;
-        if (p.split > 1) {
-            const int whole = shape;
-            shape = a->gated ? kTwoShared : kOneShared;      // (fewer columns, so that more blocks have some)
-            smem = lay();
-            if (p.stages < 2) {      // many experts' prefixes leave too little for the sums handed round
-                shape = whole;
-                p.split = 1;
-                smem = lay();
-            }
-        }
-    }
-    if (p.stages < 2) return CSF_ERR_UNSUPPORTED;
-    smem = std::max<int64_t>(smem, 120 * 1024);      // never two blocks on an SM: each holds the whole tensor memory
-    const int64_t most_tiles = tiles(p.nt);
-    if (most_tiles >= (1ll << 31)) return CSF_ERR_UNSUPPORTED;
+    const Plan plan = plan_of({sms, a->slots, E, p.F, p.blocks, a->gated != 0, a->rows != nullptr});
+    if (plan.stages < 2 || plan.most_tiles >= (1ll << 31)) return CSF_ERR_UNSUPPORTED;
     if (sms < 1) return CSF_ERR_CUDA;
+    const int shape = plan.shape;
+    p.tile_step = plan.tile_step;
+    p.second = a->gated ? N / 2 : 128;
+    p.row_tiles = plan.row_tiles;
+    p.row_tiles_magic = (uint32_t)((1ull << 32) / (uint32_t)p.row_tiles + 1);
+    p.nt = plan.nt;
+    p.stage_bytes = plan.stage_bytes;
+    p.stages = plan.stages;
+    p.split = plan.split;
 
     CUtensorMap wmap, xmap;
     {
@@ -179,9 +134,9 @@ extern "C" csf_status csf_fp8_matmul(const csf_fp8_matmul_args *a, void *stream)
     if (!allow_smem(reinterpret_cast<const void *>(k), kSmemLimit, launch_regs(a->rows) - 7)) return CSF_ERR_CUDA;
     const unsigned per = shape == kPair ? 2 : (unsigned)p.split;
     cudaLaunchConfig_t config = {};
-    config.gridDim = dim3((unsigned)(p.split > 1 ? most_tiles * p.split : per * std::min<int64_t>(sms / per, most_tiles)));
+    config.gridDim = dim3((unsigned)(p.split > 1 ? plan.most_tiles * p.split : per * std::min<int64_t>(sms / per, plan.most_tiles)));
     config.blockDim = dim3((unsigned)threads_of(a->rows));
-    config.dynamicSmemBytes = (size_t)smem;
+    config.dynamicSmemBytes = (size_t)plan.smem;
     config.stream = static_cast<cudaStream_t>(stream);
     cudaLaunchAttribute cluster;
     if (per > 1) {

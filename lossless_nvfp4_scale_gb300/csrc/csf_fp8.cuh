@@ -51,6 +51,7 @@
 #include <cuda.h>
 
 #include "csf_elem.cuh"
+#include "csf_fp8_plan.h"
 #include "csf_grouped.cuh"
 #include "csf_internal.cuh"
 #include "csf_layer.h"
@@ -62,18 +63,10 @@ namespace f8 {
 using mm::Ring;
 using mm::Tile;
 
-constexpr int kSumWarps = 8;
 constexpr int kFactorWarps = 2, kFirstFactorWarp = 2;      // 64 rows each
 constexpr int kXWarps = 4, kFirstXWarp = 4;                // 32 rows each, where an index is followed
 __host__ __device__ constexpr int threads_of(bool rows) { return rows ? 512 : 384; }
-constexpr int kMaxStages = 8;
-constexpr int kSmemLimit = 227 * 1024;
-constexpr int kMaxExperts = 8192;
-constexpr int kMaxSplit = 8;
-constexpr int kSplitSlots = 64;          // slots of a tile that a cluster shares
-constexpr uint32_t kTileBytes = 128 * 128;
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kTurnBytes = kSumWarps * 32 * 128;      // a piece of 32 rows of 128 bytes each
 // Registers of the warps that copy and of those that sum, where a thread holds
 // 128 sums and takes out 64 or 32 partial ones: together what the block was
 // launched with.
@@ -82,13 +75,6 @@ template <bool ROWS> constexpr int kCopyRegs = ROWS ? 48 : 56;
 template <bool ROWS> constexpr int kSumRegs = ROWS ? 208 : 224;
 static_assert(256 * kCopyRegs<true> + 256 * kSumRegs<true> == 512 * launch_regs(true), "registers of a block");
 static_assert(128 * kCopyRegs<false> + 256 * kSumRegs<false> == 384 * launch_regs(false), "registers of a block");
-// Steps whose factors are held: those of the ring's stages, and of partial
-// sums that are formed (4 steps at most) or taken out.  In a pair's second
-// block the summing warps say of each group of steps that they have read it (a
-// word of every step cost 4% of a dense product).
-constexpr int kFactorSteps = 16, kFactorGroup = 8;
-static_assert(kFactorSteps >= kMaxStages + 5, "factors are written when their stage is free");
-static_assert(kFactorSteps % kFactorGroup == 0, "groups are whole");
 
 struct Params {
     const uint8_t *x_codes, *x_scales;
@@ -121,13 +107,6 @@ struct Params {
     int32_t bias_dtype, residual_dtype, out_dtype;
     int32_t bias_wide, residual_wide, out_wide;
     int32_t split;               // blocks of a cluster that share a tile's depth
-};
-
-struct Shared {
-    uint64_t full[kMaxStages], empty[kMaxStages], acc_full[4], acc_empty[4];
-    uint64_t fac_full[kFactorSteps], fac_empty[kFactorSteps / kFactorGroup];      // of a pair's second block
-    uint32_t tmem, abort, warp_sum[16];
-    float amax[2][2][128];       // by tile, half and row
 };
 
 __device__ __forceinline__ float activate(float v, int act) {
@@ -879,9 +858,6 @@ fp8_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constan
 }
 
 using Kernel = void (*)(CUtensorMap, CUtensorMap, Params);
-
-// A pair, one block of 128 or 256 columns, or those with the depth shared.
-enum Shape { kPair = 0, kOne = 1, kTwo = 2, kOneShared = 3, kTwoShared = 4 };
 
 template <bool ROWS, int MODE>
 Kernel pick(int shape) {

@@ -1,0 +1,114 @@
+// Which kernel of csf_fp8.cuh a call of csf_fp8_matmul takes, and what it is
+// launched with: arithmetic on the call's sizes, for the host alone.  Internal
+// to the library.
+#pragma once
+
+#include <algorithm>
+#include <cstddef>
+#include <cstdint>
+
+namespace csfk {
+namespace f8 {
+
+constexpr int kMaxStages = 8;
+constexpr int kSmemLimit = 227 * 1024;
+constexpr int kMaxExperts = 8192;
+constexpr int kMaxSplit = 8;
+constexpr int kSplitSlots = 64;          // slots of a tile that a cluster shares
+constexpr uint32_t kTileBytes = 128 * 128;
+constexpr int kSumWarps = 8;
+constexpr uint32_t kTurnBytes = kSumWarps * 32 * 128;      // a piece of 32 rows of 128 bytes each
+// Steps whose factors are held: those of the ring's stages, and of partial
+// sums that are formed (4 steps at most) or taken out.  In a pair's second
+// block the summing warps say of each group of steps that they have read it (a
+// word of every step cost 4% of a dense product).
+constexpr int kFactorSteps = 16, kFactorGroup = 8;
+static_assert(kFactorSteps >= kMaxStages + 5, "factors are written when their stage is free");
+static_assert(kFactorSteps % kFactorGroup == 0, "groups are whole");
+
+struct Shared {
+    uint64_t full[kMaxStages], empty[kMaxStages], acc_full[4], acc_empty[4];
+    uint64_t fac_full[kFactorSteps], fac_empty[kFactorSteps / kFactorGroup];      // of a pair's second block
+    uint32_t tmem, abort, warp_sum[16];
+    float amax[2][2][128];       // by tile, half and row
+};
+
+// A pair, one block of 128 or 256 columns, or those with the depth shared.
+enum Shape { kPair = 0, kOne = 1, kTwo = 2, kOneShared = 3, kTwoShared = 4 };
+
+struct Call {
+    int sms;             // of the device
+    int64_t slots;
+    int32_t experts;
+    int32_t F, blocks;   // output columns, blocks of 128 of the depth
+    bool gated, rows;    // rows: x is read through an index
+};
+
+struct Plan {
+    int shape, split;            // split: blocks of a cluster that share a tile's depth
+    int32_t nt;                  // most slots per tile
+    int32_t tile_step, row_tiles;   // columns of the weights' outputs from a tile to the next, tiles of them
+    int32_t stages;              // fewer than 2: there is no room
+    uint32_t stage_bytes;
+    int64_t smem;                // dynamic shared memory
+    int64_t most_tiles;          // at most
+};
+
+inline void lay(Plan &p, const Call &c, int shape) {
+    const bool wide = shape == kPair || shape == kTwo || shape == kTwoShared;
+    const int64_t busy = std::min<int64_t>(c.experts, c.slots);
+    p.shape = shape;
+    p.tile_step = wide && !c.gated ? 256 : 128;
+    p.row_tiles = (c.F + p.tile_step - 1) / p.tile_step;
+    p.nt = shape == kPair ? 256 : shape >= kOneShared ? kSplitSlots : 128;
+    p.stage_bytes = kTileBytes * (shape == kTwo || shape == kTwoShared ? 3 : 2);
+    const int64_t region = shape >= kOneShared ? (int64_t)kSplitSlots * 512 * (shape == kTwoShared ? 2 : 1) : kTurnBytes;
+    const int64_t fixed = 1024 + region + 8 * ((int64_t)c.experts + 1) + 16;
+    const int64_t held = ((int64_t)sizeof(Shared) + kFactorSteps * 512 * (wide ? 2 : 1) + 1023) / 1024 * 1024;
+    p.stages = (int32_t)std::min<int64_t>(kMaxStages, (kSmemLimit - held - fixed) / p.stage_bytes);
+    p.smem = std::max<int64_t>(fixed + p.stages * (int64_t)p.stage_bytes, 120 * 1024);      // never two blocks on an SM: each holds the whole tensor memory
+    p.most_tiles = (int64_t)p.row_tiles * (busy + c.slots / p.nt);
+}
+
+inline Plan plan_of(const Call &c) {
+    const int64_t busy = std::min<int64_t>(c.experts, c.slots);      // experts with slots, at most
+    // A tile's shape by the rounds of tiles that it takes, each as long as
+    // measured with 5120 columns and depth (pair 1, two blocks 1.04, one 0.65).
+    // Experts' last slot tiles are half full on average.  512 / 8191 slots of a
+    // dense 5120 x 5120: one block 38 / 246 us, two 31 / 193, a pair 29 / 183;
+    // 128 experts of 256 slots, gated 4096 x 2048: two blocks 455, a pair 539.
+    auto tiles_of = [&](int nt, int step) {
+        const int64_t rows = c.experts == 1 ? (c.slots + nt - 1) / nt : std::max(busy, busy / 2 + c.slots / nt);
+        return rows * ((c.F + step - 1) / step);
+    };
+    auto rounds = [&](int64_t t, int units) { return (double)((t + units - 1) / units); };
+    const int wide_step = c.gated ? 128 : 256, units = std::max(c.sms, 2);
+    const double pair = rounds(tiles_of(256, wide_step), units / 2), two = 1.04 * rounds(tiles_of(128, wide_step), units);
+    const double one = c.gated ? 2 * two : 0.65 * rounds(tiles_of(128, 128), units);
+    // Rows through an index take no pair: its second block's copies would be handed to the block that issues, a release
+    // to the cluster a step (8191 slots of 5120 x 5120: 315 us, two blocks 229).
+    const int whole = one <= two && (one <= pair || c.rows) ? kOne : two <= pair || c.rows ? kTwo : kPair;
+    Plan p;
+    p.split = 1;
+    lay(p, c, whole);
+    if (whole != kPair) {
+        // Few tiles: clusters share their depth.  Clusters of half the SMs' blocks
+        // are placed at once, larger ones than pairs of more in turns: one slot of
+        // 2048 x 5120 takes 14.5 us in 16 clusters of 8 and 9.3 in 16 of 4, of
+        // 5120 x 5120 15.4 in 40 blocks and 12.3 in 40 pairs.
+        const int64_t slot_tiles = c.experts == 1 ? (c.slots + kSplitSlots - 1) / kSplitSlots : busy + c.slots / kSplitSlots;
+        const int64_t few = (int64_t)((c.F + 127) / 128) * slot_tiles;
+        while (p.split < kMaxSplit && few * p.split * 2 <= (p.split == 1 ? c.sms : c.sms / 2) && c.blocks >= 4 * p.split) p.split *= 2;
+        if (p.split > 1) {
+            lay(p, c, c.gated ? kTwoShared : kOneShared);      // (fewer columns, so that more blocks have some)
+            if (p.stages < 2) {      // many experts' prefixes leave too little for the sums handed round
+                p.split = 1;
+                lay(p, c, whole);
+            }
+        }
+    }
+    return p;
+}
+
+}  // namespace f8
+}  // namespace csfk
