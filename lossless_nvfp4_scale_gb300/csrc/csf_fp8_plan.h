@@ -91,20 +91,25 @@ inline Plan plan_of(const Call &c) {
     Plan p;
     p.split = 1;
     lay(p, c, whole);
-    if (whole != kPair) {
-        // Few tiles: clusters share their depth.  Clusters of half the SMs' blocks
-        // are placed at once, larger ones than pairs of more in turns: one slot of
-        // 2048 x 5120 takes 14.5 us in 16 clusters of 8 and 9.3 in 16 of 4, of
-        // 5120 x 5120 15.4 in 40 blocks and 12.3 in 40 pairs.
-        const int64_t slot_tiles = c.experts == 1 ? (c.slots + kSplitSlots - 1) / kSplitSlots : busy + c.slots / kSplitSlots;
-        const int64_t few = (int64_t)((c.F + 127) / 128) * slot_tiles;
-        while (p.split < kMaxSplit && few * p.split * 2 <= (p.split == 1 ? c.sms : c.sms / 2) && c.blocks >= 4 * p.split) p.split *= 2;
-        if (p.split > 1) {
-            lay(p, c, c.gated ? kTwoShared : kOneShared);      // (fewer columns, so that more blocks have some)
-            if (p.stages < 2) {      // many experts' prefixes leave too little for the sums handed round
-                p.split = 1;
-                lay(p, c, whole);
-            }
+    // Few tiles, whatever they would be: clusters share their depth.  Clusters of
+    // half the SMs' blocks are placed at once, larger ones than pairs of more in
+    // turns: one slot of 2048 x 5120 takes 14.5 us in 16 clusters of 8 and 9.3 in
+    // 16 of 4, of 5120 x 5120 15.4 in 40 blocks and 12.3 in 40 pairs.
+    const int64_t slot_tiles = c.experts == 1 ? (c.slots + kSplitSlots - 1) / kSplitSlots : busy + c.slots / kSplitSlots;
+    const int64_t few = (int64_t)((c.F + 127) / 128) * slot_tiles;
+    while (p.split < kMaxSplit && few * p.split * 2 <= (p.split == 1 ? c.sms : c.sms / 2) && c.blocks >= 4 * p.split) p.split *= 2;
+    // Gated, the sums handed round are twice as many: two blocks share where few
+    // rows or much depth pay for them.  1 / 32 / 64 slots of 8192 x 2048 take 12.6 /
+    // 13.9 / 16.4 us in twos and 13.9 / 14.3 / 14.9 whole, 256 of 4096 x 5120 23.9
+    // and 26.3; in fours and eights all gain (64 of 1024 x 1024 10.0 and 10.7, 1 of
+    // 4096 x 5120 14.9 and 22.7).
+    const int64_t tiles_with_slots = c.experts == 1 ? slot_tiles : busy;
+    if (c.gated && p.split == 2 && c.slots > 32 * tiles_with_slots && c.blocks < 32) p.split = 1;
+    if (p.split > 1) {
+        lay(p, c, c.gated ? kTwoShared : kOneShared);      // (fewer columns, so that more blocks have some)
+        if (p.stages < 2) {      // many experts' prefixes leave too little for the sums handed round
+            p.split = 1;
+            lay(p, c, whole);
         }
     }
     return p;

@@ -46,3 +46,43 @@ def test_every_plan_can_be_launched():
         assert p.split == 1 or p.most_tiles * p.split <= 2 * SMS, c
         assert not (p.shape == PAIR and c["rows"]) and not (p.shape in (ONE, ONE_SHARED) and c["gated"]), c
         assert p.most_tiles * p.nt * p.tile_step >= c["slots"] * c["F"], c
+
+
+@pytest.mark.parametrize("slots,experts,F,depth,rows,split", [
+    (1, 1, 2048, 5120, False, 4), (32, 1, 2048, 5120, False, 4), (128, 1, 2048, 5120, False, 2), (1, 1, 512, 2048, False, 8), (64, 1, 512, 1600, True, 4),
+    (8, 128, 512, 1600, True, 2), (2, 6000, 128, 1024, False, 4), (1, 1, 128, 512, False, 2),
+])
+def test_gated_products_of_few_slots_share_their_depth(slots, experts, F, depth, rows, split):
+    p = Plan(SMS, slots, experts, F, depth, True, rows)
+    assert (p.shape, p.split) == (TWO_SHARED, split)
+
+
+def test_prefixes_of_many_experts_leave_no_room_to_share_a_gated_products_depth():
+    # 8 bytes an expert beside 64 KB of sums and two stages of 48 KB
+    assert Plan(SMS, 2, 6000, 128, 1024, True).split == 4
+    for rows in (False, True):
+        p = Plan(SMS, 2, 8192, 128, 1024, True, rows)
+        assert p.split == 1 and p.shape == (TWO if rows else PAIR) and p.stages >= 2
+    assert Plan(SMS, 2, 8192, 128, 1024).split == 4          # half the sums: there is room
+
+
+def test_two_blocks_share_a_gated_product_where_it_pays():
+    # (the kernels' times are beside the rule)
+    for slots, experts, F, depth, split in ((64, 1, 4096, 2048, 1), (32, 1, 4096, 2048, 2), (1, 1, 8192, 2048, 2), (256, 1, 2048, 5120, 2), (256, 1, 2048, 1024, 1),
+                                            (64, 1, 512, 1024, 4), (128, 8, 512, 1600, 2), (1024, 8, 256, 1600, 1)):
+        assert Plan(SMS, slots, experts, F, depth, True).split == split, (slots, experts, F, depth)
+
+
+def test_few_tiles_share_their_depth_gated_or_not():
+    seen = set()
+    for c in sizes(20000):
+        p = Plan(SMS, **c)
+        seen.add((p.shape, c["rows"]))
+        slot_tiles = -(-c["slots"] // 64) if c["experts"] == 1 else min(c["experts"], c["slots"]) + c["slots"] // 64
+        few = -(-c["F"] // 128) * slot_tiles
+        if few * 2 <= SMS and c["depth"] > 3 * 128 and c["experts"] < 5000:
+            deep = few * 4 <= SMS // 2 and c["depth"] > 7 * 128
+            assert p.split > 1 or (c["gated"] and not deep), c
+            assert p.split >= 4 or not deep, c
+    # every kernel is some product's
+    assert seen == {(s, r) for s in (PAIR, ONE, TWO, ONE_SHARED, TWO_SHARED) for r in (False, True)} - {(PAIR, True)}
