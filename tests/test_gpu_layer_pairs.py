@@ -3,6 +3,7 @@
 import pytest
 import torch
 
+from fp8_plan import PAIR, TWO, Plan
 from test_gpu_layer import Problem, no_errors_left, ops  # noqa: F401  (fixtures)
 
 pytestmark = pytest.mark.gpu
@@ -10,11 +11,13 @@ pytestmark = pytest.mark.gpu
 
 @pytest.mark.parametrize("gather", [0, 700])
 @pytest.mark.parametrize("counts,N,K,gated,transposed", [
-    ([1000], 4000, 528, False, False), ([2000], 640, 2560, False, True), ([1500], 2560, 1040, True, False), ([700, 0, 900], 4096, 272, False, False),
+    ([1000], 4000, 528, False, False), ([2000], 640, 2048, False, True), ([1500], 2560, 1040, True, False), ([900, 0, 1000], 4096, 272, False, False),
     ([5000], 4000, 1040, False, False),               # several tiles of 9 steps a pair
 ])
 def test_pairs_repeat_themselves(ops, counts, N, K, gated, transposed, gather):  # noqa: F811
     p = Problem(ops, counts, N, K, seed=21, gather=gather, transposed=transposed)
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    assert Plan(sms, p.S, p.E, p.O // 2 if gated else p.O, p.depth, gated, gather > 0).shape == (TWO if gather else PAIR)
     act = "silu" if gated else None
     want = p.run(out=torch.float32, activation=act, gated=gated)
     p.check(want, act=act, gated=gated)

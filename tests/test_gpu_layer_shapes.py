@@ -3,7 +3,7 @@ own rule, so that each case is what it is named."""
 import pytest
 import torch
 
-from fp8_plan import TWO_SHARED, Plan
+from fp8_plan import ONE, ONE_SHARED, PAIR, TWO, TWO_SHARED, Plan
 from test_gpu_layer import Problem, no_errors_left, ops  # noqa: F401  (fixtures)
 
 pytestmark = pytest.mark.gpu
@@ -43,3 +43,47 @@ def test_gated_product_beside_the_prefix_of_many_experts(ops):  # noqa: F811
         start[E:] = 2
         for out in (torch.float32, ops.FP8):
             p.check(ops.fp8_matmul(p.x, w, ws, expert_start=start, out=out, gated=True, activation="silu"), act="silu", gated=True)
+
+
+# counts, N, K, gated, the shape in order and through an index
+SHAPES = [
+    ([300], 1000, 256, False, ONE, ONE),
+    ([100] * 100, 256, 256, False, TWO, TWO),
+    ([1000], 4000, 528, False, PAIR, TWO),
+    ([900, 0, 1000], 4096, 272, False, PAIR, TWO),
+    ([40], 1000, 1040, False, ONE_SHARED, ONE_SHARED),
+    ([1500], 2560, 272, True, PAIR, TWO),
+    ([128, 1, 129, 0] * 10, 1024, 256, True, TWO, TWO),
+]
+
+
+@pytest.mark.parametrize("gather", [0, 300])
+@pytest.mark.parametrize("out", [torch.bfloat16, torch.float16, torch.float32, "fp8"])
+@pytest.mark.parametrize("counts,N,K,gated,in_order,by_index", SHAPES)
+def test_epilogue_of_every_shape(ops, counts, N, K, gated, in_order, by_index, out, gather):  # noqa: F811
+    p = Problem(ops, counts, N, K, seed=41, gather=gather)
+    assert plan_of(p, gated).shape == (by_index if gather else in_order)
+    F = p.O // 2 if gated else p.O
+    out = ops.FP8 if out == "fp8" else out
+    row_scale = torch.rand(p.S, **p.dev)
+    for bias_dtype, dtype, act in ((torch.bfloat16, torch.float16, "silu"), (torch.float32, torch.bfloat16, None), (torch.float16, torch.float32, "gelu")):
+        kw = dict(bias=torch.randn(p.E, p.O, **p.dev).to(bias_dtype), row_scale=row_scale, residual=torch.randn(p.S, F, **p.dev).to(dtype))
+        p.check(p.run(activation=act, gated=gated, out=out, **kw), act=act, gated=gated, **kw)
+    for kw in (dict(residual=torch.randn(p.S, F + 9, **p.dev).to(torch.bfloat16)[:, 3:3 + F]),       # rows off 16 bytes
+               dict(residual=torch.randn(p.S, F, **p.dev).to(torch.bfloat16)), dict(row_scale=row_scale), dict(bias=torch.randn(p.E, p.O, **p.dev))):
+        p.check(p.run(activation="relu", gated=gated, out=out, **kw), act="relu", gated=gated, **kw)
+    if out != ops.FP8:                                # rows of the result off 16 bytes, the residual on them
+        wide = torch.full((p.S, F + 9), 5.0, dtype=out, device="cuda")
+        kw = dict(residual=torch.randn(p.S, F, **p.dev).to(torch.bfloat16))
+        p.run(gated=gated, out=wide[:, 1:1 + F], **kw)
+        p.check(wide[:, 1:1 + F], gated=gated, **kw)
+        assert (wide[:, 0] == 5).all() and (wide[:, 1 + F:] == 5).all()
+
+
+@pytest.mark.parametrize("out", [torch.bfloat16, torch.float32, "fp8"])
+@pytest.mark.parametrize("counts,N,K,shape", [([2000], 640, 2048, PAIR), ([300], 256, 992, ONE), ([100] * 100, 256, 256, TWO), ([40], 1040, 1008, ONE_SHARED)])
+def test_epilogue_of_transposed_products(ops, counts, N, K, shape, out):  # noqa: F811
+    p = Problem(ops, counts, N, K, seed=43, transposed=True)
+    assert plan_of(p).shape == shape
+    kw = dict(bias=torch.randn(p.E, K, **p.dev), row_scale=torch.rand(p.S, **p.dev), residual=torch.randn(p.S, K, **p.dev).to(torch.bfloat16))
+    p.check(p.run(activation="silu", out=ops.FP8 if out == "fp8" else out, **kw), act="silu", **kw)
