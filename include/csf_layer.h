@@ -81,8 +81,10 @@ csf_status csf_fp8_matmul(const csf_fp8_matmul_args *a, void *stream);
  * out[slots[t][j]] = x[t], rounded to the output's type or quantised as
  * csf_rows says.  Slots of -1 are choices that fell away; others outside
  * [0, out_count) are not written and set CSF_DEV_ERR_CORRUPT.  Output rows
- * that no slot names are left as they were.  A slot named twice gets rows of
- * one or the other, whichever is last.  Without slots out[t] = x[t].
+ * that no slot names are left as they were.  Each slot belongs to one choice,
+ * as csf_route numbers them: a row that two choices name, of one token or of
+ * two, may hold parts of both, and codes of one with scales of the other.
+ * Without slots out[t] = x[t].
  */
 typedef struct {
     const void *x;           /* [tokens][cols] of dtype, row stride x_stride elements */

@@ -501,7 +501,8 @@ def dispatch(x: torch.Tensor, slots: torch.Tensor, out=None, tensor_scale: torch
     `out` is a dtype (x's without one), a kind (a new Quantized, made in the
     same pass), a tensor or a Quantized of any number of rows.  New ones have
     tokens * k rows; rows that no slot names hold nothing, in one that is given
-    they stay as they were.  Slots of -1 fell away; others out of range reach
+    they stay as they were.  Each slot belongs to one choice: rows that two name
+    are undefined.  Slots of -1 fell away; others out of range reach
     `error_word` or errors().  The gradient is dispatch_grad."""
     if stream is not None:
         return _on(stream, dispatch, x, slots, out, tensor_scale, error_word)
