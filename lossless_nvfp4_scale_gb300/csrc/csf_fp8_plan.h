@@ -73,17 +73,18 @@ inline void lay(Plan &p, const Call &c, int shape) {
 inline Plan plan_of(const Call &c) {
     const int64_t busy = std::min<int64_t>(c.experts, c.slots);      // experts with slots, at most
     // A tile's shape by the rounds of tiles that it takes, each as long as
-    // measured with 5120 columns and depth (pair 1, two blocks 1.04, one 0.65).
-    // Experts' last slot tiles are half full on average.  512 / 8191 slots of a
-    // dense 5120 x 5120: one block 38 / 246 us, two 31 / 193, a pair 29 / 183;
-    // 128 experts of 256 slots, gated 4096 x 2048: two blocks 455, a pair 539.
+    // measured with 5120 columns and depth (256 columns a block 1, 128 0.65, a
+    // pair 0.95 and 0.2 once).  Experts' last slot tiles are half full on average.
+    // 512 / 2048 / 8191 slots of a dense 5120 x 5120: 128 columns 31 / 71 / 236 us,
+    // 256 24.3 / 64.2 / 194, a pair 26.0 / 66.0 / 189; 8191 slots of 8192 x 5120
+    // gated 303 and 298; 128 experts of 256 slots, gated 4096 x 2048, 455 and 539.
     auto tiles_of = [&](int nt, int step) {
         const int64_t rows = c.experts == 1 ? (c.slots + nt - 1) / nt : std::max(busy, busy / 2 + c.slots / nt);
         return rows * ((c.F + step - 1) / step);
     };
     auto rounds = [&](int64_t t, int units) { return (double)((t + units - 1) / units); };
     const int wide_step = c.gated ? 128 : 256, units = std::max(c.sms, 2);
-    const double pair = rounds(tiles_of(256, wide_step), units / 2), two = 1.04 * rounds(tiles_of(128, wide_step), units);
+    const double pair = 0.2 + 0.95 * rounds(tiles_of(256, wide_step), units / 2), two = rounds(tiles_of(128, wide_step), units);
     const double one = c.gated ? 2 * two : 0.65 * rounds(tiles_of(128, 128), units);
     // Rows through an index take no pair: its second block's copies would be handed to the block that issues, a release
     // to the cluster a step (8191 slots of 5120 x 5120: 315 us, two blocks 229).

@@ -18,7 +18,8 @@ SMS = 152
     (10000, 100, 256, 1024, False, False, TWO, 1),
     (8191, 1, 5120, 5120, False, False, PAIR, 1),
     (8191, 1, 5120, 5120, False, True, TWO, 1),             # rows through an index take no pair
-    (1000, 1, 4000, 528, False, False, PAIR, 1),
+    (1000, 1, 4000, 528, False, False, TWO, 1),             # a pair's start costs more than its rounds save
+    (5000, 1, 4000, 528, False, False, PAIR, 1),
     (32768, 128, 2048, 2048, True, True, TWO, 1),
     (8191, 1, 4096, 5120, True, False, PAIR, 1),
 ])
@@ -62,7 +63,7 @@ def test_prefixes_of_many_experts_leave_no_room_to_share_a_gated_products_depth(
     assert Plan(SMS, 2, 6000, 128, 1024, True).split == 4
     for rows in (False, True):
         p = Plan(SMS, 2, 8192, 128, 1024, True, rows)
-        assert p.split == 1 and p.shape == (TWO if rows else PAIR) and p.stages >= 2
+        assert p.split == 1 and p.shape == TWO and p.stages >= 2
     assert Plan(SMS, 2, 8192, 128, 1024).split == 4          # half the sums: there is room
 
 

@@ -11,8 +11,8 @@ pytestmark = pytest.mark.gpu
 
 @pytest.mark.parametrize("gather", [0, 700])
 @pytest.mark.parametrize("counts,N,K,gated,transposed", [
-    ([1000], 4000, 528, False, False), ([2000], 640, 2048, False, True), ([1500], 2560, 1040, True, False), ([900, 0, 1000], 4096, 272, False, False),
-    ([5000], 4000, 1040, False, False),               # several tiles of 9 steps a pair
+    ([5000], 4000, 528, False, False), ([5000], 640, 4096, False, True), ([5000], 8192, 1040, True, False), ([2500, 0, 2600], 4096, 272, False, False),
+    ([5000], 4000, 1040, False, False),
 ])
 def test_pairs_repeat_themselves(ops, counts, N, K, gated, transposed, gather):  # noqa: F811
     p = Problem(ops, counts, N, K, seed=21, gather=gather, transposed=transposed)

@@ -49,10 +49,11 @@ def test_gated_product_beside_the_prefix_of_many_experts(ops):  # noqa: F811
 SHAPES = [
     ([300], 1000, 256, False, ONE, ONE),
     ([100] * 100, 256, 256, False, TWO, TWO),
-    ([1000], 4000, 528, False, PAIR, TWO),
-    ([900, 0, 1000], 4096, 272, False, PAIR, TWO),
+    ([1000], 4000, 528, False, TWO, TWO),
+    ([5000], 4000, 528, False, PAIR, TWO),
+    ([2500, 0, 2600], 4096, 272, False, PAIR, TWO),
     ([40], 1000, 1040, False, ONE_SHARED, ONE_SHARED),
-    ([1500], 2560, 272, True, PAIR, TWO),
+    ([5000], 8192, 272, True, PAIR, TWO),
     ([128, 1, 129, 0] * 10, 1024, 256, True, TWO, TWO),
 ]
 
@@ -81,7 +82,7 @@ def test_epilogue_of_every_shape(ops, counts, N, K, gated, in_order, by_index, o
 
 
 @pytest.mark.parametrize("out", [torch.bfloat16, torch.float32, "fp8"])
-@pytest.mark.parametrize("counts,N,K,shape", [([2000], 640, 2048, PAIR), ([300], 256, 992, ONE), ([100] * 100, 256, 256, TWO), ([40], 1040, 1008, ONE_SHARED)])
+@pytest.mark.parametrize("counts,N,K,shape", [([5000], 640, 4096, PAIR), ([300], 256, 992, ONE), ([100] * 100, 256, 256, TWO), ([40], 1040, 1008, ONE_SHARED)])
 def test_epilogue_of_transposed_products(ops, counts, N, K, shape, out):  # noqa: F811
     p = Problem(ops, counts, N, K, seed=43, transposed=True)
     assert plan_of(p).shape == shape
