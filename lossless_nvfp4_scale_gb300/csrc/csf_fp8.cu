@@ -97,10 +97,9 @@ extern "C" csf_status csf_fp8_matmul(const csf_fp8_matmul_args *a, void *stream)
     }
 
     const int sms = sm_count();
-    const Plan plan = plan_of({sms, a->slots, E, p.F, p.blocks, a->gated != 0, a->rows != nullptr});
+    const Plan plan = plan_of({sms, a->slots, E, p.F, p.blocks, a->gated != 0});
     if (plan.stages < 2 || plan.most_tiles >= (1ll << 31)) return CSF_ERR_UNSUPPORTED;
     if (sms < 1) return CSF_ERR_CUDA;
-    const int shape = plan.shape;
     p.tile_step = plan.tile_step;
     p.second = a->gated ? N / 2 : 128;
     p.row_tiles = plan.row_tiles;
@@ -114,9 +113,7 @@ extern "C" csf_status csf_fp8_matmul(const csf_fp8_matmul_args *a, void *stream)
     {
         const cuuint64_t dims[3] = {(cuuint64_t)K, (cuuint64_t)N, (cuuint64_t)E};
         const cuuint64_t strides[2] = {(cuuint64_t)K, (cuuint64_t)K * (cuuint64_t)N};
-        // a pair's blocks hold 64 of a weight block's 128 output columns each
-        const cuuint32_t part = shape == kPair ? 64 : 128;
-        const cuuint32_t box[3] = {a->transposed ? part : 128, a->transposed ? 128 : part, 1};
+        const cuuint32_t box[3] = {128, 128, 1};
         if (!byte_map(&wmap, a->w, 3, dims, strides, box)) return CSF_ERR_CUDA;
     }
     if (!a->rows) {
@@ -129,12 +126,12 @@ extern "C" csf_status csf_fp8_matmul(const csf_fp8_matmul_args *a, void *stream)
     }
     const bool sums = a->residual && a->residual_dtype != CSF_F32 && p.residual_wide && p.out_wide && p.F % 8 == 0;
     const int mode = !a->out ? kQuant : a->out_dtype == CSF_F32 ? kPlain : !a->residual ? kHalves : sums ? kHalvesSum : kPlain;
-    Kernel k = a->rows ? rows_by_index(shape, mode) : rows_in_order(shape, mode);
+    Kernel k = a->rows ? rows_by_index(plan.shape, mode) : rows_in_order(plan.shape, mode);
     // the register split waits for what the block was launched with (given out in eights)
     if (!allow_smem(reinterpret_cast<const void *>(k), kSmemLimit, launch_regs(a->rows) - 7)) return CSF_ERR_CUDA;
-    const unsigned per = shape == kPair ? 2 : (unsigned)p.split;
+    const unsigned per = (unsigned)p.split;      // blocks of a cluster
     cudaLaunchConfig_t config = {};
-    config.gridDim = dim3((unsigned)(p.split > 1 ? plan.most_tiles * p.split : per * std::min<int64_t>(sms / per, plan.most_tiles)));
+    config.gridDim = dim3((unsigned)(per > 1 ? plan.most_tiles * per : std::min<int64_t>(sms, plan.most_tiles)));
     config.blockDim = dim3((unsigned)threads_of(a->rows));
     config.dynamicSmemBytes = (size_t)plan.smem;
     config.stream = static_cast<cudaStream_t>(stream);

@@ -10,37 +10,35 @@
 // memory holds four partial sums of 128 columns: two steps of the depth are
 // under way while one is taken out.
 //
-// A tile is 128 slots by 128 or 256 columns; a dense product of many slots
-// pairs two neighbouring blocks for 256 by 256, each holding its 128 slots and
-// half of the columns, which halves what shared memory has to take in and give
-// out per product.  A gated product's tile has 128 gate columns and the 128 up
-// columns of the same numbers.  Where tiles are few, a cluster of 2 to 8
-// blocks shares one: each sums its part of the depth, hands the rows' sums
-// round, and finishes its share of the rows.
+// A tile is 128 slots by 128 or 256 columns.  A gated product's tile has 128
+// gate columns and the 128 up columns of the same numbers.  Where tiles are
+// few, a cluster of 2 to 8 blocks shares one: each sums its part of the depth,
+// hands the rows' sums round, and finishes its share of the rows.
+//
+// (Tiles of 256 by 256 on two neighbouring blocks, whose instructions one block
+// issues, halve what shared memory has to take in per product, which is not
+// the bound.  With factors and arrivals that pass between the blocks in order,
+// they took 193 us for the first line below and 215 for the second.)
 //
 // What bounds it: taking the partial sums out.  A step of 256 columns takes
 // the matrix instructions 0.26 us (0.32 with their copies), the eight warps
-// 0.34 alone, both together 0.42: a load of 64 columns from tensor memory is
+// 0.34 alone, both together 0.44: a load of 64 columns from tensor memory is
 // 160 to 190 cycles under way, twice a step, and 128 sums leave registers for
 // no more in flight.  Measured (2070 MHz):
-//   8191 slots, 5120 x 5120, bfloat16 out           191 us, 2.25 PFLOP/s
+//   8191 slots, 5120 x 5120, bfloat16 out           193 us, 2.23 PFLOP/s
 //     with a residual and row weights               215 us
 //   32768 slots on 128 experts, gated 4096 x 2048   412 us to bfloat16, 445 to
 //     FP8: 2.5 tiles of 128 slots an expert of 256, the SiLU
 //   4000 slots on 64 experts, 1600 x 2048 across    51 us, 4.6 TB/s
-//   64 slots on 8 of 128 experts, gated 1024 x 1600 14.5 us: latency
-//   one slot of 2048 x 5120                         10 us: latency
-// What that took: arrivals at another block's barrier that order no memory (a
-// cluster-wide release waited a thousand cycles), so that what passes between
-// a pair's blocks is tensor memory alone, between tcgen05 fences; waits whose
-// ready path has no taken branch (180 -> 57 cycles); issue code that the whole
-// warp runs, with one lane's predicate on the instructions; partial sums a
-// weight block each; packed multiply-adds; the factors by warps of their own,
-// for the registers.
+//   64 slots on 8 of 128 experts, gated 1024 x 1600 14.8 us: latency
+//   one slot of 2048 x 5120, of 4096 x 5120 gated   9.7, 14.6 us: latency
+// What that took: waits whose ready path has no taken branch (180 -> 57
+// cycles); issue code that the whole warp runs, with one lane's predicate on
+// the instructions; partial sums a weight block each; packed multiply-adds; the
+// factors by warps of their own, for the registers.
 //
 //   warp 0      weights, and x rows where slots are rows (TMA, 128-byte swizzle)
-//   warp 1      matrix instructions; in a pair's second block, whose first one
-//               issues for both, the factors handed on
+//   warp 1      matrix instructions
 //   warps 2, 3  the factors, a step's 128 rows at a time, into shared memory
 //   warps 4-7   x rows through an index, where there is one: 16-byte
 //               asynchronous copies, swizzled as TMA would
@@ -174,20 +172,16 @@ __device__ __forceinline__ void add_bias8(const Params &p, float *y, int e, int 
 // what one holds in registers another would spill.
 enum Mode { kHalves = 0, kPlain = 1, kQuant = 2, kHalvesSum = 3 };
 
-// CTAS: blocks of a pair.  AT: 128-column weight blocks per tile.  ROWS: slot
-// s reads row rows[s] of x, else row s.  SPLIT: clusters share a tile's depth.
-// MODE: what comes out.
-template <int CTAS, int AT, bool ROWS, bool SPLIT, int MODE>
+// AT: 128-column weight blocks per tile.  ROWS: slot s reads row rows[s] of x,
+// else row s.  SPLIT: clusters share a tile's depth.  MODE: what comes out.
+template <int AT, bool ROWS, bool SPLIT, int MODE>
 __global__ void __launch_bounds__(threads_of(ROWS), 1)
 fp8_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap, const __grid_constant__ Params p) {
-    static_assert(CTAS == 1 || (AT == 2 && !SPLIT && !ROWS), "a pair has 256 columns, all of the depth and rows in order");
     extern __shared__ __align__(1024) uint8_t dyn[];
     __shared__ Shared sh;
     __shared__ float factors[kFactorSteps][AT][128];        // a row's scale times the weight block's
     constexpr int kThreads = threads_of(ROWS), kFirstSumWarp = ROWS ? 8 : 4;
     constexpr int kSets = (int)kTmemCols / 128;             // partial sums of 128 columns under way
-    constexpr uint32_t kPart = kTileBytes / CTAS;           // bytes of a weight block that this block of threads holds
-    constexpr bool kFar = CTAS == 2;                        // the other block's copies and warps arrive at full and acc_empty
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t ring0 = (tc::smem_u32(dyn) + 1023u) & ~1023u;
     uint8_t *after_ring = dyn + (ring0 - tc::smem_u32(dyn)) + (size_t)p.stages * p.stage_bytes;
@@ -195,12 +189,9 @@ fp8_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constan
     float *region = reinterpret_cast<float *>(after_ring);
     uint32_t *first = reinterpret_cast<uint32_t *>(after_ring + (SPLIT ? kSplitSlots * AT * 512u : kTurnBytes));
     uint32_t *slot0 = first + p.E + 1;
-    const uint32_t rank = CTAS == 2 || SPLIT ? tc::cluster_rank() : 0, split = SPLIT ? (uint32_t)p.split : 1;
-    const int pair_rank = CTAS == 2 ? (int)rank : 0;
+    const uint32_t rank = SPLIT ? tc::cluster_rank() : 0, split = SPLIT ? (uint32_t)p.split : 1;
     const uint32_t full0 = tc::smem_u32(sh.full), empty0 = tc::smem_u32(sh.empty);
     const uint32_t accf0 = tc::smem_u32(sh.acc_full), acce0 = tc::smem_u32(sh.acc_empty);
-    const uint32_t facf0 = tc::smem_u32(sh.fac_full), face0 = tc::smem_u32(sh.fac_empty);
-    const bool second = CTAS == 2 && rank == 1;
 
     if (tid == 0) {
         for (int i = 0; i < p.stages; ++i) {
@@ -209,16 +200,13 @@ fp8_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constan
             tc::bar_init(empty0 + 8 * i, 1);
         }
         for (int i = 0; i < kSets; ++i) {
-            // (a pair's second block: its factors, too)
-            tc::bar_init(accf0 + 8 * i, second ? 2 : 1);
-            tc::bar_init(acce0 + 8 * i, kSumWarps / AT * CTAS);
+            tc::bar_init(accf0 + 8 * i, 1);
+            tc::bar_init(acce0 + 8 * i, kSumWarps / AT);
         }
-        for (int i = 0; second && i < kFactorSteps; ++i) tc::bar_init(facf0 + 8 * i, kFactorWarps);
-        for (int i = 0; second && i < kFactorSteps / kFactorGroup; ++i) tc::bar_init(face0 + 8 * i, kSumWarps);
         sh.abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == 1) tc::tmem_alloc_n<CTAS>(tc::smem_u32(&sh.tmem), kTmemCols);
+    if (warp == 1) tc::tmem_alloc(tc::smem_u32(&sh.tmem), kTmemCols);
     bool bad = false;
     const uint32_t running = mm::number_tiles<kThreads>(p, first, slot0, sh.warp_sum, bad);
     if (tid == 0) first[p.E] = running, slot0[p.E] = (uint32_t)mm::start_at(p, p.E);
@@ -228,110 +216,81 @@ fp8_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constan
     if (bad && p.err && blockIdx.x == 0 && tid == 0) atomicOr(p.err, CSF_DEV_ERR_CORRUPT);
     // An expert_start out of order or range makes no tiles.
     uint32_t total = bad ? 0 : first[p.E] * (uint32_t)p.row_tiles;
-    constexpr bool kCluster = CTAS == 2 || SPLIT;
-    const uint32_t per = CTAS == 2 ? 2 : split;
-    const uint32_t unit = kCluster ? blockIdx.x / per : blockIdx.x, units = kCluster ? gridDim.x / per : gridDim.x;
+    const uint32_t unit = SPLIT ? blockIdx.x / split : blockIdx.x, units = SPLIT ? gridDim.x / split : gridDim.x;
     if constexpr (SPLIT) total = min(total, units);         // one tile a cluster
     const uint32_t tmem = sh.tmem;
     volatile uint32_t *abort = &sh.abort;
     const int k0 = SPLIT ? (int)(rank * (uint32_t)p.blocks / split) : 0;
     const int k1 = SPLIT ? (int)((rank + 1) * (uint32_t)p.blocks / split) : p.blocks;
-    if constexpr (kCluster) tc::cluster_sync();             // the other blocks' barriers are set up
-
-    // This block's slots of a tile.
-    auto rows_of = [&](const Tile &t, int r) { return CTAS == 1 ? t.n : max(0, min(128, t.n - 128 * r)); };
+    if constexpr (SPLIT) tc::cluster_sync();                // the other blocks have begun
 
     if (warp < kFirstSumWarp) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kCopyRegs<ROWS>));
         if (warp == 0) {
             // ---- weights, and x rows in order ----
-            const uint32_t one = tc::elect_one(), first_one = CTAS == 1 || rank == 0 ? one : 0;
-            const uint32_t full_at = CTAS == 2 ? tc::in_block(full0, 0) : full0;
+            const uint32_t one = tc::elect_one();
             Ring ring;
             bool ok = true;
 #pragma unroll 1
             for (uint32_t tile = unit; ok && tile < total; tile += units) {
                 const Tile t = mm::find_tile(p, first, slot0, tile, lane);
-                uint32_t bytes = AT * kTileBytes;
-                const int n = rows_of(t, pair_rank);
-                if (!ROWS)
-                    for (int r = 0; r < CTAS; ++r) bytes += (uint32_t)((rows_of(t, r) + 31) >> 5) * 4096u;
-                const int col = t.rt * p.tile_step + pair_rank * 64, row = (int)t.slot + 128 * pair_rank;
+                const uint32_t bytes = AT * kTileBytes + (ROWS ? 0 : (uint32_t)((t.n + 31) >> 5) * 4096u);
+                const int col = t.rt * p.tile_step, row = (int)t.slot;
 #pragma unroll 1
                 for (int k = k0; k < k1; ++k, ring.next(p.stages)) {
                     ok = __all_sync(0xFFFFFFFFu, tc::bar_wait_ready(empty0 + 8 * ring.s, ring.parity ^ 1u, abort));
                     if (!ok) break;
-                    const uint32_t base = ring0 + ring.s * p.stage_bytes, bar = full_at + 8 * ring.s;
-                    tc::bar_expect_if(first_one, full0 + 8 * ring.s, bytes);
+                    const uint32_t base = ring0 + ring.s * p.stage_bytes, bar = full0 + 8 * ring.s;
+                    tc::bar_expect_if(one, bar, bytes);
 #pragma unroll
                     for (int a = 0; a < AT; ++a) {
                         const int c = col + a * p.second;
-                        tc::tma_load_3d_if<CTAS>(one, base + kTileBytes + a * kPart, &wmap, p.transposed ? c : k * 128, p.transposed ? k * 128 : c, t.e, bar);
+                        tc::tma_load_3d_if(one, base + kTileBytes + a * kTileBytes, &wmap, p.transposed ? c : k * 128, p.transposed ? k * 128 : c, t.e, bar);
                     }
                     if (!ROWS) {
 #pragma unroll
                         for (int c = 0; c < 128; c += 32)
-                            if (c < n) tc::tma_load_2d_if<CTAS>(one, base + c * 128u, &xmap, k * 128, row + c, bar);
+                            if (c < t.n) tc::tma_load_2d_if(one, base + c * 128u, &xmap, k * 128, row + c, bar);
                     }
                 }
             }
         } else if (warp == 1) {
             // ---- matrix instructions ----
             const uint32_t one = tc::elect_one();
-            if (rank == 0 || CTAS == 1) {
-                // D in 32 bits, E4M3 operands, B's order, N / 8, M / 16
-                const uint32_t idesc = (1u << 4) | (p.transposed ? 1u << 16 : 0) | ((128u / 8) << 17) | ((uint32_t)(CTAS * 128 / 16) << 24);
-                const uint32_t b_step = (p.transposed ? 4096 / CTAS : 32) >> 4;
-                const uint64_t a0 = tc::desc_sw128(ring0);
-                const uint64_t b0 = !p.transposed ? tc::desc_sw128(ring0 + kTileBytes) : CTAS == 1 ? tc::desc_across(ring0 + kTileBytes) : tc::desc_across64(ring0 + kTileBytes);
-                const uint32_t a_hi = (uint32_t)(a0 >> 32), b_hi = (uint32_t)(b0 >> 32), stage = p.stage_bytes >> 4;
-                Ring ring;
-                uint32_t count = 0;      // steps of the depth so far: AT sets each
-                bool ok = true;
+            // D in 32 bits, E4M3 operands, B's order, N / 8, M / 16
+            const uint32_t idesc = (1u << 4) | (p.transposed ? 1u << 16 : 0) | ((128u / 8) << 17) | ((128u / 16) << 24);
+            const uint32_t b_step = (p.transposed ? 4096 : 32) >> 4;
+            const uint64_t a0 = tc::desc_sw128(ring0);
+            const uint64_t b0 = p.transposed ? tc::desc_across(ring0 + kTileBytes) : tc::desc_sw128(ring0 + kTileBytes);
+            const uint32_t a_hi = (uint32_t)(a0 >> 32), b_hi = (uint32_t)(b0 >> 32), stage = p.stage_bytes >> 4;
+            Ring ring;
+            uint32_t count = 0;      // steps of the depth so far: AT sets each
+            bool ok = true;
 #pragma unroll 1
-                for (uint32_t tile = unit; ok && tile < total; tile += units) {
+            for (uint32_t tile = unit; ok && tile < total; tile += units) {
 #pragma unroll 1
-                    for (int k = k0; k < k1; ++k, ++count, ring.next(p.stages)) {
-                        const uint32_t set = AT == 2 ? (count & 1) * 2 : count & 3, parity = ~(count >> (AT == 2 ? 1 : 2)) & 1;
-                        const uint32_t acce = acce0 + 8 * set, accf = accf0 + 8 * set, full = full0 + 8 * ring.s;
-                        bool here = tc::bar_try_of<kFar>(full, ring.parity);
-                        here &= tc::bar_try_of<kFar>(acce, parity);
-                        if (!__all_sync(0xFFFFFFFFu, here)) {
-                            ok = __all_sync(0xFFFFFFFFu, tc::bar_wait_on<kFar>(full, ring.parity, abort) && tc::bar_wait_on<kFar>(acce, parity, abort));
+                for (int k = k0; k < k1; ++k, ++count, ring.next(p.stages)) {
+                    const uint32_t set = AT == 2 ? (count & 1) * 2 : count & 3, parity = ~(count >> (AT == 2 ? 1 : 2)) & 1;
+                    const uint32_t acce = acce0 + 8 * set, accf = accf0 + 8 * set, full = full0 + 8 * ring.s;
+                    bool here = tc::bar_try(full, ring.parity);
+                    here &= tc::bar_try(acce, parity);
+                    if (!__all_sync(0xFFFFFFFFu, here)) {
+                        ok = __all_sync(0xFFFFFFFFu, tc::bar_wait_on(full, ring.parity, abort) && tc::bar_wait_on(acce, parity, abort));
+                        if (!ok) break;
+                    }
+                    tc::fence_after();
+                    if (ROWS) tc::fence_async_proxy();       // x came by ordinary copies
+                    const uint32_t at = ring.s * stage, a_lo = (uint32_t)a0 + at, b_lo = (uint32_t)b0 + at, d = tmem + set * 128;
+                    tc::mma_f8_128(one, d, a_lo, a_hi, b_lo, b_hi, b_step, idesc, accf);
+                    if constexpr (AT == 2) {
+                        if (!__all_sync(0xFFFFFFFFu, tc::bar_try(acce + 8, parity))) {
+                            ok = __all_sync(0xFFFFFFFFu, tc::bar_wait_on(acce + 8, parity, abort));
                             if (!ok) break;
                         }
                         tc::fence_after();
-                        if (ROWS) tc::fence_async_proxy();       // x came by ordinary copies
-                        const uint32_t at = ring.s * stage, a_lo = (uint32_t)a0 + at, b_lo = (uint32_t)b0 + at, d = tmem + set * 128;
-                        tc::mma_f8_128<CTAS>(one, d, a_lo, a_hi, b_lo, b_hi, b_step, idesc, accf);
-                        if constexpr (AT == 2) {
-                            if (!__all_sync(0xFFFFFFFFu, tc::bar_try_of<kFar>(acce + 8, parity))) {
-                                ok = __all_sync(0xFFFFFFFFu, tc::bar_wait_on<kFar>(acce + 8, parity, abort));
-                                if (!ok) break;
-                            }
-                            tc::fence_after();
-                            tc::mma_f8_128<CTAS>(one, d + 128, a_lo, a_hi, b_lo + (kPart >> 4), b_hi, b_step, idesc, accf + 8);
-                        }
-                        tc::commit_if<CTAS>(one, empty0 + 8 * ring.s);
+                        tc::mma_f8_128(one, d + 128, a_lo, a_hi, b_lo + (kTileBytes >> 4), b_hi, b_step, idesc, accf + 8);
                     }
-                }
-            } else {
-                // A pair's second block.  The first one issues for both and says nothing of this one's shared memory, so
-                // that factors go from warp to warp of this block, counted with the partial sums that they are for.
-                uint32_t count = 0;
-                bool ok = true;
-#pragma unroll 1
-                for (uint32_t tile = unit; ok && tile < total; tile += units) {
-#pragma unroll 1
-                    for (int k = k0; k < k1; ++k, ++count) {
-                        const uint32_t accf = accf0 + 8 * ((count & 1) * 2), parity = ~(count >> 1) & 1;
-                        // the factors, and that the set's partial sums before have been counted
-                        ok = __all_sync(0xFFFFFFFFu, tc::bar_wait_ready(facf0 + 8 * (count % kFactorSteps), count / kFactorSteps & 1, abort) &&
-                                                         tc::bar_wait_ready(accf, parity, abort) && tc::bar_wait_ready(accf + 8, parity, abort));
-                        if (!ok) break;
-                        tc::bar_arrive_if<false>(accf, one);
-                        tc::bar_arrive_if<false>(accf + 8, one);
-                    }
+                    tc::commit_if(one, empty0 + 8 * ring.s);
                 }
             }
         } else if (warp < kFirstXWarp) {
@@ -349,7 +308,7 @@ fp8_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constan
                 float4 x0[2], x1[2];
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    const int64_t slot = (int64_t)t.slot + min(128 * pair_rank + r0 + 32 * j, t.n - 1);
+                    const int64_t slot = (int64_t)t.slot + min(r0 + 32 * j, t.n - 1);
                     int64_t row = slot;
                     if constexpr (ROWS) {
                         row = __ldg(p.rows + slot);
@@ -373,10 +332,8 @@ fp8_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constan
 #pragma unroll 1
                 for (int k = k0; k < k1; ++k, ++count, ring.next(p.stages)) {
                     const int q = k & 3, i = (k - k0) & 31;
-                    const uint32_t step = count % kFactorSteps;
-                    float *at = &factors[step][0][r0];
-                    ok = __all_sync(0xFFFFFFFFu, second ? tc::bar_wait_ready(face0 + 8 * (step / kFactorGroup), ~(count / kFactorSteps) & 1, abort)
-                                                        : tc::bar_wait_ready(empty0 + 8 * ring.s, ring.parity ^ 1u, abort));
+                    float *at = &factors[count % kFactorSteps][0][r0];
+                    ok = __all_sync(0xFFFFFFFFu, tc::bar_wait_ready(empty0 + 8 * ring.s, ring.parity ^ 1u, abort));
                     if (!ok) break;
 #pragma unroll
                     for (int a = 0; a < AT; ++a) {
@@ -386,7 +343,7 @@ fp8_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constan
                             at[a * 128 + 32 * j] = w * (q < 2 ? (q == 0 ? x0[j].x : x0[j].y) : (q == 2 ? x0[j].z : x0[j].w));
                     }
                     __syncwarp();
-                    tc::bar_arrive_if<false>(second ? facf0 + 8 * step : full0 + 8 * ring.s, lane == 0);
+                    tc::bar_arrive_if(full0 + 8 * ring.s, lane == 0);
                     if (q == 3) {
 #pragma unroll
                         for (int j = 0; j < 2; ++j) {
@@ -457,11 +414,10 @@ fp8_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constan
         const int col0 = kCols * half;
         float *buf = region + (warp - kFirstSumWarp) * 32 * 32;
         const uint32_t lanes = tmem + ((uint32_t)(32 * w) << 16);
-        const uint32_t release0 = CTAS == 1 ? acce0 : tc::in_block(acce0, 0);
         auto release = [&](uint32_t set) {
             tc::fence_before();
             __syncwarp();
-            tc::bar_arrive_if<CTAS == 2>(release0 + 8 * set, lane == 0);
+            tc::bar_arrive_if(acce0 + 8 * set, lane == 0);
         };
         auto meet = [&]() { tc::named_sync(1 + w, 64); };      // warps w and w + 4
         uint32_t count = 0;              // partial sums so far
@@ -472,11 +428,11 @@ fp8_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constan
 #pragma unroll 1
         for (uint32_t nth = 0; tile < total; tile += units, ++nth) {
             const Tile t = mm::find_tile(p, first, slot0, tile, lane);
-            const int n = rows_of(t, pair_rank) - 32 * w;       // this warp's rows, if any
+            const int n = t.n - 32 * w;         // this warp's rows, if any
             if (MODE != kHalves && !SPLIT && (MODE == kHalvesSum || p.residual) && lane < n) {
                 // what the epilogue will add to this lane's row, into L2
                 const int bytes = p.residual_dtype == CSF_F32 ? 4 : 2, f = t.rt * p.tile_step + (p.gated ? 64 * half : col0);
-                const char *at = static_cast<const char *>(p.residual) + (((int64_t)t.slot + 128 * pair_rank + 32 * w + lane) * p.residual_stride + f) * bytes;
+                const char *at = static_cast<const char *>(p.residual) + (((int64_t)t.slot + 32 * w + lane) * p.residual_stride + f) * bytes;
                 const int end = min(p.gated ? 64 : kCols, p.F - f) * bytes;
                 for (int b = 0; b < end; b += 32) tc::prefetch_l2(at + b);
             }
@@ -484,45 +440,37 @@ fp8_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constan
 #pragma unroll
             for (int i = 0; i < kCols / 2; ++i) sum[i] = 0;
             bool there = false;          // the next partial sums: asked for while these come out of tensor memory
-            int k = k0;
-            do {
-                const int stop = CTAS == 1 ? k1 : min(k1, k + kFactorGroup - (int)(count % kFactorGroup));
 #pragma unroll 1
-                for (; k < stop; ++k, ++count) {
-                    const uint32_t set = set_of(count), next = set_of(count + 1);
-                    constexpr int kRound = AT == 2 ? 1 : 2;
-                    if (!__any_sync(0xFFFFFFFFu, there)) {
-                        ok = __all_sync(0xFFFFFFFFu, tc::bar_wait_here(accf0 + 8 * set, (count >> kRound) & 1, abort));
-                        if (!ok) break;
-                    }
-                    tc::fence_after();
-                    const bool last = k + 1 == k1, keep = last && !SPLIT;        // the whole sums go back there
-                    there = false;
-                    if (n > 0) {
-                        const uint32_t at = lanes + set * 128 + (AT == 2 ? 0 : col0);
-                        uint64_t factor = 0;
-#pragma unroll
-                        for (int c = 0; c < kCols; c += kTaken) {
-                            uint32_t v[kTaken / 16][16];
-#pragma unroll
-                            for (int i = 0; i < kTaken / 16; ++i) tc::tmem_load(at + c + 16 * i, v[i]);
-                            if (c == 0) factor = tc::twice(factors[count % kFactorSteps][AT == 2 ? half : 0][32 * w + lane]);
-                            if (c + kTaken >= kCols) there = tc::bar_try_if(accf0 + 8 * next, ((count + 1) >> kRound) & 1, lane == 0 && !last);
-                            tc::wait_ld();
-                            if (c + kTaken >= kCols && !keep) release(set);
-#pragma unroll
-                            for (int j = 0; j < kTaken / 2; ++j)
-                                if (c / 2 + j < kCols / 2) tc::fma2_after(sum[c / 2 + j], v[j >> 3][2 * (j & 7)], v[j >> 3][2 * (j & 7) + 1], factor);
-                        }
-                    } else if (!keep) {
-                        release(set);
-                    }
+            for (int k = k0; k < k1; ++k, ++count) {
+                const uint32_t set = set_of(count), next = set_of(count + 1);
+                constexpr int kRound = AT == 2 ? 1 : 2;
+                if (!__any_sync(0xFFFFFFFFu, there)) {
+                    ok = __all_sync(0xFFFFFFFFu, tc::bar_wait_here(accf0 + 8 * set, (count >> kRound) & 1, abort));
+                    if (!ok) break;
                 }
-                if (CTAS == 2) {      // a group of factors has been read
-                    __syncwarp();
-                    tc::bar_arrive_if<false>(face0 + 8 * ((count / kFactorGroup - 1) % (kFactorSteps / kFactorGroup)), second && ok && lane == 0 && count % kFactorGroup == 0);
+                tc::fence_after();
+                const bool last = k + 1 == k1, keep = last && !SPLIT;        // the whole sums go back there
+                there = false;
+                if (n > 0) {
+                    const uint32_t at = lanes + set * 128 + (AT == 2 ? 0 : col0);
+                    uint64_t factor = 0;
+#pragma unroll
+                    for (int c = 0; c < kCols; c += kTaken) {
+                        uint32_t v[kTaken / 16][16];
+#pragma unroll
+                        for (int i = 0; i < kTaken / 16; ++i) tc::tmem_load(at + c + 16 * i, v[i]);
+                        if (c == 0) factor = tc::twice(factors[count % kFactorSteps][AT == 2 ? half : 0][32 * w + lane]);
+                        if (c + kTaken >= kCols) there = tc::bar_try_if(accf0 + 8 * next, ((count + 1) >> kRound) & 1, lane == 0 && !last);
+                        tc::wait_ld();
+                        if (c + kTaken >= kCols && !keep) release(set);
+#pragma unroll
+                        for (int j = 0; j < kTaken / 2; ++j)
+                            if (c / 2 + j < kCols / 2) tc::fma2_after(sum[c / 2 + j], v[j >> 3][2 * (j & 7)], v[j >> 3][2 * (j & 7) + 1], factor);
+                    }
+                } else if (!keep) {
+                    release(set);
                 }
-            } while (CTAS == 2 && ok && k < k1);
+            }
             if (!ok) break;
             if constexpr (SPLIT) {
                 // a row's sums to the block that finishes it
@@ -557,7 +505,7 @@ fp8_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constan
                 tc::wait_st();
             }
             if (n > 0) {
-                const int64_t slot = (int64_t)t.slot + 128 * pair_rank + 32 * w;
+                const int64_t slot = (int64_t)t.slot + 32 * w;
                 const bool gated = AT == 2 && p.gated;
                 // this warp's columns of the output, and where their sums are (a gated product's: 64 of both blocks)
                 const int f0 = t.rt * p.tile_step + (gated ? 64 * half : col0), cols = gated ? 64 : kCols;
@@ -805,7 +753,7 @@ fp8_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constan
             // met as often as the tiles that are left have it do.
             const int meetings = AT == 1 ? 1 : MODE == kQuant ? 3 : 2;
             for (; tile < total; tile += units)
-                if (rows_of(mm::find_tile(p, first, slot0, tile, lane), pair_rank) > 32 * w)
+                if (mm::find_tile(p, first, slot0, tile, lane).n > 32 * w)
                     for (int i = 0; i < meetings; ++i) meet();
         }
     }
@@ -821,7 +769,7 @@ fp8_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constan
         while (tc::timer_ns() - t0 < 5000000ull) __nanosleep(1000);
         __syncthreads();
     }
-    if constexpr (kCluster) tc::cluster_sync();      // the sums have come; nothing is under way to a block that leaves
+    if constexpr (SPLIT) tc::cluster_sync();         // the sums have come; nothing is under way to a block that leaves
     if constexpr (SPLIT) {
         if (unit < total && !sh.abort) {
             const Tile t = mm::find_tile(p, first, slot0, unit, lane);
@@ -854,7 +802,7 @@ fp8_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constan
             }
         }
     }
-    if (warp == 1) tc::tmem_free_n<CTAS>(tmem, kTmemCols);
+    if (warp == 1) tc::tmem_free(tmem, kTmemCols);
 }
 
 using Kernel = void (*)(CUtensorMap, CUtensorMap, Params);
@@ -864,11 +812,10 @@ Kernel pick(int shape) {
     // where the depth is shared, what comes out is asked at run time
     constexpr int kAny = MODE == kQuant ? kQuant : kPlain;
     switch (shape) {
-        case kPair: return ROWS ? nullptr : fp8_matmul_kernel<2, 2, false, false, MODE>;
-        case kOne: return fp8_matmul_kernel<1, 1, ROWS, false, MODE>;
-        case kTwo: return fp8_matmul_kernel<1, 2, ROWS, false, MODE>;
-        case kOneShared: return fp8_matmul_kernel<1, 1, ROWS, true, kAny>;
-        default: return fp8_matmul_kernel<1, 2, ROWS, true, kAny>;
+        case kOne: return fp8_matmul_kernel<1, ROWS, false, MODE>;
+        case kTwo: return fp8_matmul_kernel<2, ROWS, false, MODE>;
+        case kOneShared: return fp8_matmul_kernel<1, ROWS, true, kAny>;
+        default: return fp8_matmul_kernel<2, ROWS, true, kAny>;
     }
 }
 

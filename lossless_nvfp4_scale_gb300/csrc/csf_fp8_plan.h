@@ -19,29 +19,25 @@ constexpr uint32_t kTileBytes = 128 * 128;
 constexpr int kSumWarps = 8;
 constexpr uint32_t kTurnBytes = kSumWarps * 32 * 128;      // a piece of 32 rows of 128 bytes each
 // Steps whose factors are held: those of the ring's stages, and of partial
-// sums that are formed (4 steps at most) or taken out.  In a pair's second
-// block the summing warps say of each group of steps that they have read it (a
-// word of every step cost 4% of a dense product).
-constexpr int kFactorSteps = 16, kFactorGroup = 8;
+// sums that are formed (4 steps at most) or taken out.
+constexpr int kFactorSteps = 16;
 static_assert(kFactorSteps >= kMaxStages + 5, "factors are written when their stage is free");
-static_assert(kFactorSteps % kFactorGroup == 0, "groups are whole");
 
 struct Shared {
     uint64_t full[kMaxStages], empty[kMaxStages], acc_full[4], acc_empty[4];
-    uint64_t fac_full[kFactorSteps], fac_empty[kFactorSteps / kFactorGroup];      // of a pair's second block
     uint32_t tmem, abort, warp_sum[16];
     float amax[2][2][128];       // by tile, half and row
 };
 
-// A pair, one block of 128 or 256 columns, or those with the depth shared.
-enum Shape { kPair = 0, kOne = 1, kTwo = 2, kOneShared = 3, kTwoShared = 4 };
+// Tiles of 128 or 256 columns, or those with the depth shared.
+enum Shape { kOne = 0, kTwo = 1, kOneShared = 2, kTwoShared = 3 };
 
 struct Call {
     int sms;             // of the device
     int64_t slots;
     int32_t experts;
     int32_t F, blocks;   // output columns, blocks of 128 of the depth
-    bool gated, rows;    // rows: x is read through an index
+    bool gated;
 };
 
 struct Plan {
@@ -55,13 +51,13 @@ struct Plan {
 };
 
 inline void lay(Plan &p, const Call &c, int shape) {
-    const bool wide = shape == kPair || shape == kTwo || shape == kTwoShared;
+    const bool wide = shape == kTwo || shape == kTwoShared;
     const int64_t busy = std::min<int64_t>(c.experts, c.slots);
     p.shape = shape;
     p.tile_step = wide && !c.gated ? 256 : 128;
     p.row_tiles = (c.F + p.tile_step - 1) / p.tile_step;
-    p.nt = shape == kPair ? 256 : shape >= kOneShared ? kSplitSlots : 128;
-    p.stage_bytes = kTileBytes * (shape == kTwo || shape == kTwoShared ? 3 : 2);
+    p.nt = shape >= kOneShared ? kSplitSlots : 128;
+    p.stage_bytes = kTileBytes * (wide ? 3 : 2);
     const int64_t region = shape >= kOneShared ? (int64_t)kSplitSlots * 512 * (shape == kTwoShared ? 2 : 1) : kTurnBytes;
     const int64_t fixed = 1024 + region + 8 * ((int64_t)c.experts + 1) + 16;
     const int64_t held = ((int64_t)sizeof(Shared) + kFactorSteps * 512 * (wide ? 2 : 1) + 1023) / 1024 * 1024;
@@ -72,23 +68,17 @@ inline void lay(Plan &p, const Call &c, int shape) {
 
 inline Plan plan_of(const Call &c) {
     const int64_t busy = std::min<int64_t>(c.experts, c.slots);      // experts with slots, at most
-    // A tile's shape by the rounds of tiles that it takes, each as long as
-    // measured with 5120 columns and depth (256 columns a block 1, 128 0.65, a
-    // pair 0.95 and 0.2 once).  Experts' last slot tiles are half full on average.
-    // 512 / 2048 / 8191 slots of a dense 5120 x 5120: 128 columns 31 / 71 / 236 us,
-    // 256 24.3 / 64.2 / 194, a pair 26.0 / 66.0 / 189; 8191 slots of 8192 x 5120
-    // gated 303 and 298; 128 experts of 256 slots, gated 4096 x 2048, 455 and 539.
-    auto tiles_of = [&](int nt, int step) {
-        const int64_t rows = c.experts == 1 ? (c.slots + nt - 1) / nt : std::max(busy, busy / 2 + c.slots / nt);
+    // A tile's width by the rounds of tiles that it takes, a round of 128 columns
+    // 0.65 of one of 256 as measured with 5120 columns and depth.  Experts' last
+    // slot tiles are half full on average.  512 / 2048 / 8191 slots of a dense 5120
+    // x 5120: 128 columns 31 / 71 / 236 us, 256 24.3 / 64.2 / 193.
+    auto tiles_of = [&](int step) {
+        const int64_t rows = c.experts == 1 ? (c.slots + 127) / 128 : std::max(busy, busy / 2 + c.slots / 128);
         return rows * ((c.F + step - 1) / step);
     };
-    auto rounds = [&](int64_t t, int units) { return (double)((t + units - 1) / units); };
-    const int wide_step = c.gated ? 128 : 256, units = std::max(c.sms, 2);
-    const double pair = 0.2 + 0.95 * rounds(tiles_of(256, wide_step), units / 2), two = rounds(tiles_of(128, wide_step), units);
-    const double one = c.gated ? 2 * two : 0.65 * rounds(tiles_of(128, 128), units);
-    // Rows through an index take no pair: its second block's copies would be handed to the block that issues, a release
-    // to the cluster a step (8191 slots of 5120 x 5120: 315 us, two blocks 229).
-    const int whole = one <= two && (one <= pair || c.rows) ? kOne : two <= pair || c.rows ? kTwo : kPair;
+    const int units = std::max(c.sms, 1);
+    auto rounds = [&](int64_t t) { return (double)((t + units - 1) / units); };
+    const int whole = !c.gated && 0.65 * rounds(tiles_of(128)) <= rounds(tiles_of(256)) ? kOne : kTwo;
     Plan p;
     p.split = 1;
     lay(p, c, whole);
@@ -102,8 +92,8 @@ inline Plan plan_of(const Call &c) {
     // Gated, the sums handed round are twice as many: two blocks share where few
     // rows or much depth pay for them.  1 / 32 / 64 slots of 8192 x 2048 take 12.6 /
     // 13.9 / 16.4 us in twos and 13.9 / 14.3 / 14.9 whole, 256 of 4096 x 5120 23.9
-    // and 26.3; in fours and eights all gain (64 of 1024 x 1024 10.0 and 10.7, 1 of
-    // 4096 x 5120 14.9 and 22.7).
+    // and 24.6; in fours and eights all gain (64 of 1024 x 2048 10.9 and 12.7, 1 of
+    // 4096 x 5120 14.9 and 23.3).
     const int64_t tiles_with_slots = c.experts == 1 ? slot_tiles : busy;
     if (c.gated && p.split == 2 && c.slots > 32 * tiles_with_slots && c.blocks < 32) p.split = 1;
     if (p.split > 1) {

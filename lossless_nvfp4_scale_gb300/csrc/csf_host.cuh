@@ -21,14 +21,13 @@ EncodeFn encode_fn();
 // fewer than `least_regs` registers a thread.
 bool allow_smem(const void *kernel, int limit, int least_regs = 0) noexcept;
 
-// The map of a tensor of bytes; boxes of 128 (or 64) bytes a row in the
-// swizzle of that width.
+// The map of a tensor of bytes; boxes of 128 bytes a row, 128-byte swizzle.
 inline bool byte_map(CUtensorMap *map, const void *base, cuuint32_t rank, const cuuint64_t *dims, const cuuint64_t *strides,
                      const cuuint32_t *box) {
     const cuuint32_t ones[3] = {1, 1, 1};
     EncodeFn encode = encode_fn();
     return encode && encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, rank, const_cast<void *>(base), dims, strides, box, ones,
-                            CU_TENSOR_MAP_INTERLEAVE_NONE, box[0] == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                             CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }

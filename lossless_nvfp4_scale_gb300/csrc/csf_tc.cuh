@@ -97,14 +97,8 @@ __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile
 // The same with nothing but the barrier's answer in the way of a phase that
 // is there already: the loop above took 180 cycles then, in a warp alone on
 // its scheduler, and this takes 57.
-template <bool CLUSTER = false>
 static __device__ __noinline__ bool bar_wait_on(uint32_t bar, uint32_t parity, volatile uint32_t *abort) {
-    return bar_wait<CLUSTER>(bar, parity, abort);
-}
-
-template <bool CLUSTER>
-__device__ __forceinline__ bool bar_try_of(uint32_t bar, uint32_t parity) {
-    return CLUSTER ? bar_try_cluster(bar, parity) : bar_try(bar, parity);
+    return bar_wait(bar, parity, abort);
 }
 
 __device__ __forceinline__ bool bar_wait_ready(uint32_t bar, uint32_t parity, volatile uint32_t *abort) {
@@ -165,19 +159,11 @@ __device__ __forceinline__ void bar_arrive_cluster(uint32_t bar) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
-// One lane's arrival, of this block's barrier or (REMOTE) at a cluster
-// address, without a branch that the warp would have to come together after.
-// The remote one orders no memory (a release to the cluster took a thousand
-// cycles): it stands between tcgen05 fences, and tells that tensor memory has
-// been read.
-template <bool REMOTE>
+// One lane's arrival, without a branch that the warp would have to come
+// together after.
 __device__ __forceinline__ void bar_arrive_if(uint32_t bar, bool is) {
-    if constexpr (REMOTE)
-        asm volatile("{\n .reg .pred p;\n setp.ne.u32 p, %1, 0;\n @p mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];\n}" ::"r"(bar), "r"((uint32_t)is)
-                     : "memory");
-    else
-        asm volatile("{\n .reg .pred p;\n setp.ne.u32 p, %1, 0;\n @p mbarrier.arrive.shared::cta.b64 _, [%0];\n}" ::"r"(bar), "r"((uint32_t)is)
-                     : "memory");
+    asm volatile("{\n .reg .pred p;\n setp.ne.u32 p, %1, 0;\n @p mbarrier.arrive.shared::cta.b64 _, [%0];\n}" ::"r"(bar), "r"((uint32_t)is)
+                 : "memory");
 }
 
 // ---- copies -------------------------------------------------------------------------------------------------------
@@ -278,63 +264,27 @@ __device__ __forceinline__ void mma_mxf8(uint32_t d, uint64_t a, uint64_t b, uin
         : "memory");
 }
 
-// ---- 8-bit products of one block or of a pair (CTAS = 2, the blocks of a cluster of two) ---------------------------------
-
-template <int CTAS>
-__device__ __forceinline__ void tmem_alloc_n(uint32_t result, uint32_t cols) {
-    if constexpr (CTAS == 1) tmem_alloc(result, cols);
-    else asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(result), "r"(cols) : "memory");
-}
-
-template <int CTAS>
-__device__ __forceinline__ void tmem_free_n(uint32_t addr, uint32_t cols) {
-    if constexpr (CTAS == 1) {
-        tmem_free(addr, cols);
-    } else {
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
-        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols));
-    }
-}
+// ---- 8-bit products -----------------------------------------------------------------------------------------------
 
 // What follows is issued by the lane whose `one` is set, in code that the whole
 // warp runs: addresses and descriptors then stay in uniform registers, where
 // the instructions want them.  (In a branch of one lane's own each operand had
 // to be moved there: 160 cycles a step of the loop alone, before any wait.)
 
-// Into this block's memory; what has landed is counted by bar, which may be
-// the other block's (a cluster address).
-template <int CTAS>
 __device__ __forceinline__ void tma_load_3d_if(uint32_t one, uint32_t dst, const void *map, int x, int y, int z, uint32_t bar) {
-    if constexpr (CTAS == 1)
-        asm volatile(
-            "{\n .reg .pred p;\n setp.ne.u32 p, %6, 0;\n"
-            " @p cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];\n}" ::"r"(dst),
-            "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar), "r"(one)
-            : "memory");
-    else
-        asm volatile(
-            "{\n .reg .pred p;\n setp.ne.u32 p, %6, 0;\n"
-            " @p cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, "
-            "%4}], [%5];\n}" ::"r"(dst),
-            "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar), "r"(one)
-            : "memory");
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.u32 p, %6, 0;\n"
+        " @p cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];\n}" ::"r"(dst),
+        "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar), "r"(one)
+        : "memory");
 }
 
-template <int CTAS>
 __device__ __forceinline__ void tma_load_2d_if(uint32_t one, uint32_t dst, const void *map, int x, int y, uint32_t bar) {
-    if constexpr (CTAS == 1)
-        asm volatile(
-            "{\n .reg .pred p;\n setp.ne.u32 p, %5, 0;\n"
-            " @p cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];\n}" ::"r"(dst),
-            "l"(map), "r"(x), "r"(y), "r"(bar), "r"(one)
-            : "memory");
-    else
-        asm volatile(
-            "{\n .reg .pred p;\n setp.ne.u32 p, %5, 0;\n"
-            " @p cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], "
-            "[%4];\n}" ::"r"(dst),
-            "l"(map), "r"(x), "r"(y), "r"(bar), "r"(one)
-            : "memory");
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.u32 p, %5, 0;\n"
+        " @p cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];\n}" ::"r"(dst),
+        "l"(map), "r"(x), "r"(y), "r"(bar), "r"(one)
+        : "memory");
 }
 
 __device__ __forceinline__ void bar_expect_if(uint32_t one, uint32_t bar, uint32_t bytes) {
@@ -344,62 +294,36 @@ __device__ __forceinline__ void bar_expect_if(uint32_t one, uint32_t bar, uint32
         : "memory");
 }
 
-// One arrival on bar (of each block of a pair) once every tcgen05 operation
-// this thread issued so far is done.
-template <int CTAS>
+// One arrival on bar once every tcgen05 operation this thread issued so far is
+// done.
 __device__ __forceinline__ void commit_if(uint32_t one, uint32_t bar) {
-    if constexpr (CTAS == 1)
-        asm volatile(
-            "{\n .reg .pred p;\n setp.ne.u32 p, %1, 0;\n"
-            " @p tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}" ::"r"(bar),
-            "r"(one)
-            : "memory");
-    else
-        asm volatile(
-            "{\n .reg .pred p;\n setp.ne.u32 p, %2, 0;\n"
-            " @p tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n}" ::"r"(bar),
-            "h"((uint16_t)3), "r"(one)
-            : "memory");
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.u32 p, %1, 0;\n"
+        " @p tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}" ::"r"(bar),
+        "r"(one)
+        : "memory");
 }
 
-// D[128 CTAS x N] = A * B^T with E4M3 operands, K = 128 in four steps, and an
-// arrival on bar when they are done.  A pair has 128 rows of A and N / 2 of B
-// in each block's memory.  Descriptors come as their halves, of which the low
-// ones advance; all in one piece, since each instruction that the loop around
-// it takes waits for its turn among the summing warps'.
-template <int CTAS>
+// D[128 x N] = A * B^T with E4M3 operands, K = 128 in four steps, and an
+// arrival on bar when they are done.  Descriptors come as their halves, of
+// which the low ones advance; all in one piece, since each instruction that the
+// loop around it takes waits for its turn among the summing warps'.
 __device__ __forceinline__ void mma_f8_128(uint32_t one, uint32_t d, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo, uint32_t b_hi,
                                            uint32_t b_step, uint32_t idesc, uint32_t bar) {
-    if constexpr (CTAS == 1)
-        asm volatile(
-                "{\n .reg .pred p, t, f;\n .reg .b32 x;\n .reg .b64 ad, bd;\n setp.ne.u32 p, %8, 0;\n setp.eq.u32 t, %8, %8;\n setp.ne.u32 f, %8, %8;\n"
-                " add.u32 x, %1, 0;\n mov.b64 ad, {x, %2};\n mad.lo.u32 x, %5, 0, %3;\n mov.b64 bd, {x, %4};\n"
-                " @p tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], ad, bd, %6, f;\n"
-                " add.u32 x, %1, 2;\n mov.b64 ad, {x, %2};\n mad.lo.u32 x, %5, 1, %3;\n mov.b64 bd, {x, %4};\n"
-                " @p tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], ad, bd, %6, t;\n"
-                " add.u32 x, %1, 4;\n mov.b64 ad, {x, %2};\n mad.lo.u32 x, %5, 2, %3;\n mov.b64 bd, {x, %4};\n"
-                " @p tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], ad, bd, %6, t;\n"
-                " add.u32 x, %1, 6;\n mov.b64 ad, {x, %2};\n mad.lo.u32 x, %5, 3, %3;\n mov.b64 bd, {x, %4};\n"
-                " @p tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], ad, bd, %6, t;\n"
-                " @p tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%7];\n"
-                "}" ::"r"(d),
-                "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(b_step), "r"(idesc), "r"(bar), "r"(one)
-                : "memory");
-    else
-        asm volatile(
-                "{\n .reg .pred p, t, f;\n .reg .b32 x;\n .reg .b64 ad, bd;\n setp.ne.u32 p, %8, 0;\n setp.eq.u32 t, %8, %8;\n setp.ne.u32 f, %8, %8;\n"
-                " add.u32 x, %1, 0;\n mov.b64 ad, {x, %2};\n mad.lo.u32 x, %5, 0, %3;\n mov.b64 bd, {x, %4};\n"
-                " @p tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], ad, bd, %6, f;\n"
-                " add.u32 x, %1, 2;\n mov.b64 ad, {x, %2};\n mad.lo.u32 x, %5, 1, %3;\n mov.b64 bd, {x, %4};\n"
-                " @p tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], ad, bd, %6, t;\n"
-                " add.u32 x, %1, 4;\n mov.b64 ad, {x, %2};\n mad.lo.u32 x, %5, 2, %3;\n mov.b64 bd, {x, %4};\n"
-                " @p tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], ad, bd, %6, t;\n"
-                " add.u32 x, %1, 6;\n mov.b64 ad, {x, %2};\n mad.lo.u32 x, %5, 3, %3;\n mov.b64 bd, {x, %4};\n"
-                " @p tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], ad, bd, %6, t;\n"
-                " @p tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%7], %9;\n"
-                "}" ::"r"(d),
-                "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(b_step), "r"(idesc), "r"(bar), "r"(one), "h"((uint16_t)3)
-                : "memory");
+    asm volatile(
+            "{\n .reg .pred p, t, f;\n .reg .b32 x;\n .reg .b64 ad, bd;\n setp.ne.u32 p, %8, 0;\n setp.eq.u32 t, %8, %8;\n setp.ne.u32 f, %8, %8;\n"
+            " add.u32 x, %1, 0;\n mov.b64 ad, {x, %2};\n mad.lo.u32 x, %5, 0, %3;\n mov.b64 bd, {x, %4};\n"
+            " @p tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], ad, bd, %6, f;\n"
+            " add.u32 x, %1, 2;\n mov.b64 ad, {x, %2};\n mad.lo.u32 x, %5, 1, %3;\n mov.b64 bd, {x, %4};\n"
+            " @p tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], ad, bd, %6, t;\n"
+            " add.u32 x, %1, 4;\n mov.b64 ad, {x, %2};\n mad.lo.u32 x, %5, 2, %3;\n mov.b64 bd, {x, %4};\n"
+            " @p tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], ad, bd, %6, t;\n"
+            " add.u32 x, %1, 6;\n mov.b64 ad, {x, %2};\n mad.lo.u32 x, %5, 3, %3;\n mov.b64 bd, {x, %4};\n"
+            " @p tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], ad, bd, %6, t;\n"
+            " @p tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%7];\n"
+            "}" ::"r"(d),
+            "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(b_step), "r"(idesc), "r"(bar), "r"(one)
+            : "memory");
 }
 
 // Descriptor of 128 elements of 8 bits a row and rows along the summed index
@@ -408,12 +332,6 @@ __device__ __forceinline__ void mma_f8_128(uint32_t one, uint32_t d, uint32_t a_
 __device__ __forceinline__ uint64_t desc_across(uint32_t addr) {
     return (uint64_t)((addr & 0x3FFFFu) >> 4) | ((uint64_t)(16384 >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) | (1ull << 46) |
            (2ull << 61);
-}
-
-// The same with 64 elements a row (64-byte swizzle).
-__device__ __forceinline__ uint64_t desc_across64(uint32_t addr) {
-    return (uint64_t)((addr & 0x3FFFFu) >> 4) | ((uint64_t)(8192 >> 4) << 16) | ((uint64_t)(512 >> 4) << 32) | (1ull << 46) |
-           (4ull << 61);
 }
 
 // Columns of this warp's lanes, as they are; wait_ld on them makes what uses

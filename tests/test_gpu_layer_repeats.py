@@ -1,23 +1,24 @@
-"""Products on pairs of blocks, and the same through an index on blocks by themselves: what one warp hands to another
-(rows, factors, partial sums) is there in every one of many calls, beside other work on the GPU and alone."""
+"""Products on every shape of tile: what one warp hands to another (rows, factors, partial sums), and one block of a
+cluster to the next, is there in every one of many calls, beside other work on the GPU and alone."""
 import pytest
 import torch
 
-from fp8_plan import PAIR, TWO, Plan
+from fp8_plan import ONE, ONE_SHARED, TWO, TWO_SHARED
 from test_gpu_layer import Problem, no_errors_left, ops  # noqa: F401  (fixtures)
+from test_gpu_layer_shapes import plan_of
 
 pytestmark = pytest.mark.gpu
 
 
 @pytest.mark.parametrize("gather", [0, 700])
-@pytest.mark.parametrize("counts,N,K,gated,transposed", [
-    ([5000], 4000, 528, False, False), ([5000], 640, 4096, False, True), ([5000], 8192, 1040, True, False), ([2500, 0, 2600], 4096, 272, False, False),
-    ([5000], 4000, 1040, False, False),
+@pytest.mark.parametrize("counts,N,K,gated,transposed,shape", [
+    ([5000], 4000, 528, False, False, TWO), ([5000], 640, 4096, False, True, TWO), ([5000], 8192, 1040, True, False, TWO),
+    ([300], 1000, 256, False, False, ONE), ([3000, 0, 2900], 300, 272, False, False, ONE),
+    ([64], 1000, 2048, False, False, ONE_SHARED), ([60], 1024, 2048, True, False, TWO_SHARED),
 ])
-def test_pairs_repeat_themselves(ops, counts, N, K, gated, transposed, gather):  # noqa: F811
+def test_products_repeat_themselves(ops, counts, N, K, gated, transposed, shape, gather):  # noqa: F811
     p = Problem(ops, counts, N, K, seed=21, gather=gather, transposed=transposed)
-    sms = torch.cuda.get_device_properties(0).multi_processor_count
-    assert Plan(sms, p.S, p.E, p.O // 2 if gated else p.O, p.depth, gated, gather > 0).shape == (TWO if gather else PAIR)
+    assert plan_of(p, gated).shape == shape
     act = "silu" if gated else None
     want = p.run(out=torch.float32, activation=act, gated=gated)
     p.check(want, act=act, gated=gated)

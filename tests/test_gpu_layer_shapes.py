@@ -3,7 +3,7 @@ own rule, so that each case is what it is named."""
 import pytest
 import torch
 
-from fp8_plan import ONE, ONE_SHARED, PAIR, TWO, TWO_SHARED, Plan
+from fp8_plan import ONE, ONE_SHARED, TWO, TWO_SHARED, Plan
 from test_gpu_layer import Problem, no_errors_left, ops  # noqa: F401  (fixtures)
 
 pytestmark = pytest.mark.gpu
@@ -11,7 +11,7 @@ pytestmark = pytest.mark.gpu
 
 def plan_of(p, gated=False):
     sms = torch.cuda.get_device_properties(0).multi_processor_count
-    return Plan(sms, p.S, p.E, p.O // 2 if gated else p.O, p.depth, gated, p.rows is not None)
+    return Plan(sms, p.S, p.E, p.O // 2 if gated else p.O, p.depth, gated)
 
 
 @pytest.mark.parametrize("gather", [0, 40])
@@ -45,25 +45,24 @@ def test_gated_product_beside_the_prefix_of_many_experts(ops):  # noqa: F811
             p.check(ops.fp8_matmul(p.x, w, ws, expert_start=start, out=out, gated=True, activation="silu"), act="silu", gated=True)
 
 
-# counts, N, K, gated, the shape in order and through an index
+# counts, N, K, gated, the shape
 SHAPES = [
-    ([300], 1000, 256, False, ONE, ONE),
-    ([100] * 100, 256, 256, False, TWO, TWO),
-    ([1000], 4000, 528, False, TWO, TWO),
-    ([5000], 4000, 528, False, PAIR, TWO),
-    ([2500, 0, 2600], 4096, 272, False, PAIR, TWO),
-    ([40], 1000, 1040, False, ONE_SHARED, ONE_SHARED),
-    ([5000], 8192, 272, True, PAIR, TWO),
-    ([128, 1, 129, 0] * 10, 1024, 256, True, TWO, TWO),
+    ([300], 1000, 256, False, ONE),
+    ([100] * 100, 256, 256, False, TWO),
+    ([1000], 4000, 528, False, TWO),
+    ([2500, 0, 2600], 4096, 272, False, TWO),
+    ([40], 1000, 1040, False, ONE_SHARED),
+    ([5000], 2560, 272, True, TWO),
+    ([128, 1, 129, 0] * 10, 1024, 256, True, TWO),
 ]
 
 
 @pytest.mark.parametrize("gather", [0, 300])
 @pytest.mark.parametrize("out", [torch.bfloat16, torch.float16, torch.float32, "fp8"])
-@pytest.mark.parametrize("counts,N,K,gated,in_order,by_index", SHAPES)
-def test_epilogue_of_every_shape(ops, counts, N, K, gated, in_order, by_index, out, gather):  # noqa: F811
+@pytest.mark.parametrize("counts,N,K,gated,shape", SHAPES)
+def test_epilogue_of_every_shape(ops, counts, N, K, gated, shape, out, gather):  # noqa: F811
     p = Problem(ops, counts, N, K, seed=41, gather=gather)
-    assert plan_of(p, gated).shape == (by_index if gather else in_order)
+    assert plan_of(p, gated).shape == shape
     F = p.O // 2 if gated else p.O
     out = ops.FP8 if out == "fp8" else out
     row_scale = torch.rand(p.S, **p.dev)
@@ -82,7 +81,7 @@ def test_epilogue_of_every_shape(ops, counts, N, K, gated, in_order, by_index, o
 
 
 @pytest.mark.parametrize("out", [torch.bfloat16, torch.float32, "fp8"])
-@pytest.mark.parametrize("counts,N,K,shape", [([5000], 640, 4096, PAIR), ([300], 256, 992, ONE), ([100] * 100, 256, 256, TWO), ([40], 1040, 1008, ONE_SHARED)])
+@pytest.mark.parametrize("counts,N,K,shape", [([5000], 640, 4096, TWO), ([300], 256, 992, ONE), ([100] * 100, 256, 256, TWO), ([40], 1040, 1008, ONE_SHARED)])
 def test_epilogue_of_transposed_products(ops, counts, N, K, shape, out):  # noqa: F811
     p = Problem(ops, counts, N, K, seed=43, transposed=True)
     assert plan_of(p).shape == shape
