@@ -41,7 +41,8 @@ extern "C" {
  *   plain:  y[f] = act(p[f])
  *   gated:  y[f] = act(p[f]) * p[N/2 + f], 0 <= f < N/2; not with transposed
  *   out[s][f] = y[f] * row_scale[s] + residual[s][f]
- * Sums in 32 bits, within (depth / 32 + 4) 2^-23 of sum |x w| of the values.
+ * Sums in 32 bits, within (depth / 32 + 4) 2^-23 of sum |x w| of the values
+ * where xs ws, which is formed first, is a normal float32 number or 0.
  * SiLU and GELU are as csf_expert_matmul's.  Slots at or past expert_start[E]
  * are not written; with an expert_start that is out of order or range, none
  * is.  A row index out of range stands for row 0.

@@ -53,7 +53,7 @@ typedef enum { CSF_BF16 = 0, CSF_F16 = 1, CSF_F32 = 2 } csf_dtype;
  *   FP8:   scale = m / 448 (2^-126 at least); code = v / scale rounded to E4M3
  *          (ties to even, saturating).
  * A block that holds an infinity or a NaN gets a NaN scale (0x7F, 255, a
- * float's NaN). */
+ * float's NaN); its codes, those past `cols` too, mean nothing then. */
 typedef enum { CSF_ROWS_NVFP4 = 0, CSF_ROWS_MXFP8 = 1, CSF_ROWS_FP8 = 3 } csf_rows_kind;
 
 typedef struct {

@@ -27,7 +27,7 @@
 // no more in flight.  Measured (2070 MHz):
 //   8191 slots, 5120 x 5120, bfloat16 out           193 us, 2.23 PFLOP/s
 //     with a residual and row weights               215 us
-//   32768 slots on 128 experts, gated 4096 x 2048   412 us to bfloat16, 445 to
+//   32768 slots on 128 experts, gated 4096 x 2048   403 us to bfloat16, 440 to
 //     FP8: 2.5 tiles of 128 slots an expert of 256, the SiLU
 //   4000 slots on 64 experts, 1600 x 2048 across    51 us, 4.6 TB/s
 //   64 slots on 8 of 128 experts, gated 1024 x 1600 14.8 us: latency
@@ -409,7 +409,7 @@ fp8_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constan
         constexpr int kCols = AT * 64;                                      // this warp's columns
         // columns taken out of tensor memory at a time: as many as the registers
         // hold beside the sums (128 experts of 256 slots, gated, through an index:
-        // 412 us with 32, 445 with 64; dense 8191 x 5120 x 5120: 197 and 183)
+        // 402 us with 32, 434 with 64; dense 8191 x 5120 x 5120: 200 and 194)
         constexpr int kTaken = ROWS ? 32 : 64;
         const int col0 = kCols * half;
         float *buf = region + (warp - kFirstSumWarp) * 32 * 32;

@@ -99,8 +99,8 @@ def _error_word(device: int) -> torch.Tensor:
 
 
 def errors(device: int | None = None) -> int:
-    """CSF_DEV_ERR_* bits of the expert_matmul calls on a device that were given
-    no error_word, and clears them.  Synchronises; calls of other threads wait
+    """CSF_DEV_ERR_* bits of the calls on a device that take an error_word and
+    were given none, and clears them.  Synchronises; calls of other threads wait
     meanwhile.  (Not so replays of captured calls: what one sets between the
     reading and the clearing is lost.)  Before a capture of such calls it makes
     the word that they report to."""
